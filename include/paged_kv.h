@@ -78,6 +78,7 @@ extern "C" {
 #define KV_DEVERR_CONTEXT_TOO_LONG 4      /* context_lens[s] > 16*max_blocks_per_seq, or < 0 */
 #define KV_DEVERR_PIPELINE_TIMEOUT 8      /* a bulk copy never arrived (a bug, never expected) */
 #define KV_DEVERR_BAD_PREFIX 16           /* a prefix chunk table entry is inconsistent */
+#define KV_DEVERR_BAD_TREE 32             /* a draft tree's table entry is inconsistent */
 
 /* ------------------------------------------------------------------ sizing */
 
@@ -147,6 +148,33 @@ int kv_seq_free(kv_alloc_t* a, int64_t seq_id);
 int kv_step(kv_alloc_t* a, const int64_t* seq_ids, int n, int64_t* slot_mapping,
             int32_t* block_tables, int max_blocks, int32_t* context_lens, int32_t* cow_src,
             int32_t* cow_dst, int cow_cap, int* n_cow);
+
+/* Plan one step that appends a tree (or chain) of drafted tokens to each of n
+ * sequences (kv_step for more than one token a sequence; an interface of this
+ * implementation).  Row i appends num_nodes[i] >= 0 tokens at positions
+ * len .. len + num_nodes[i] - 1 of sequence seq_ids[i]:
+ *   - a shared tail block that receives tokens is replaced by a fresh one and
+ *     reported in cow_src/cow_dst (as kv_step); every further block is fresh,
+ *     so the blocks the tokens go to are private to the sequence;
+ *   - node_starts[0] = 0, node_starts[i+1] = node_starts[i] + num_nodes[i]
+ *     (host int32 [n + 1]); slot_mapping[node_starts[i] + k] is the slot of
+ *     position len + k (host int64, sum of num_nodes entries);
+ *   - the length becomes len + num_nodes[i]; context_lens[i] and row i of
+ *     block_tables ([n][max_blocks], -1 padded) are the state after it.
+ * num_nodes[i] == 1 for every row gives what kv_step gives.  All-or-nothing,
+ * with kv_step's errors; KV_ERR_INVALID_ARG also for a negative count or a
+ * total of 2^31 or more.  After the tokens are verified, kv_seq_truncate
+ * drops the rejected ones. */
+int kv_tree_step(kv_alloc_t* a, const int64_t* seq_ids, const int32_t* num_nodes, int n,
+                 int64_t* slot_mapping, int32_t* block_tables, int max_blocks,
+                 int32_t* context_lens, int32_t* node_starts, int32_t* cow_src,
+                 int32_t* cow_dst, int cow_cap, int* n_cow);
+
+/* Cut sequences to new_lens[i] <= len tokens: blocks past ceil(new_lens[i]/16)
+ * lose one reference and return to the pool at zero (the tokens of a draft
+ * that were not accepted, after kv_tree_compact).  seq_ids distinct and live;
+ * on an error (KV_ERR_NOT_FOUND, KV_ERR_INVALID_ARG) nothing changes. */
+int kv_seq_truncate(kv_alloc_t* a, const int64_t* seq_ids, const int64_t* new_lens, int n);
 
 /* Reorder the KV state of a batch of live sequences (beam search selection
  * or batch-row reuse): after the call, sequence seq_ids[i] holds the length
@@ -499,6 +527,137 @@ int paged_decode_timed(void* out, int out_dtype, const void* q, const void* k_ne
                        const int32_t* seq_chunk, int num_chunks, unsigned flags,
                        void* workspace, size_t workspace_bytes, void* stream, void* ev_begin,
                        void* ev_split_end, void* ev_end);
+
+/* ------------------------------------------------------ trees of drafted tokens */
+
+/* Speculative decoding verifies several drafted tokens a sequence in one step
+ * ("KV Cache, Flash Attention and inference optimization", section
+ * "Speculative decoding": a draft proposes k tokens, the large model verifies
+ * them).  (The entry points are interfaces of this implementation; the pages
+ * describe the idea, not a kernel for it.)  One step of a sequence is
+ *     kv_tree_step (host) -> kv_append -> paged_tree_attention, per layer
+ *     -> kv_tree_verify -> kv_tree_compact -> kv_seq_truncate (host).
+ *
+ * A tree of sequence s is its nodes node_starts[s] .. node_starts[s+1] - 1
+ * (n_s = their number, at most max_nodes <= KV_TREE_MAX_NODES) with
+ * parents[node] = the index of the node's parent within the sequence's own
+ * tree, less than the node's own index, or
+ *     -1  the node is a root (it follows the committed tokens directly);
+ *     KV_TREE_PAD (-2)  the node is padding: it sees nothing and no node but
+ *         its own children, which take it for a root, refers to it.
+ * parents == NULL: every tree is a chain (node i's parent is i - 1).  Node 0
+ * is the token the previous step emitted, whose K/V is not in the cache yet;
+ * the others are drafted.  The nodes' K/V is appended at positions
+ * base .. base + n_s - 1, base = context_lens[s] - n_s.
+ *
+ * Table faults never lead to a fault on the device; each raises
+ * KV_DEVERR_BAD_TREE with the first bad value: node_starts out of
+ * [0, total_nodes], decreasing, or more than max_nodes apart (the sequence is
+ * taken to have no nodes), 0 < context_lens[s] < n_s (as many of the first
+ * nodes as there is room for count), a parent below -2 or not before its node
+ * (the node is taken for a root). */
+#define KV_TREE_MAX_NODES 128
+#define KV_TREE_PAD (-2)
+
+/* Workspace bytes of paged_tree_attention for at most num_seqs sequences of at
+ * most max_nodes nodes on the current device.  As paged_decode's: no
+ * initialisation, nothing carried over, one per call in flight. */
+int paged_tree_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int num_kv_heads,
+                               int head_dim, int kv_dtype, size_t* bytes);
+
+/* Attention of every node of every sequence's tree over the paged cache:
+ *   out, q:        [total_nodes][num_q_heads][head_dim], as paged_decode_attention
+ *                  (rows from node_starts[num_seqs] on are left as they were)
+ *   node_starts:   [num_seqs + 1] int32; parents: [total_nodes] int32 or NULL
+ *   context_lens:  [num_seqs] int32, cached tokens including the tree's nodes
+ * and the other arguments as paged_decode_attention.  For node i of sequence s
+ *     out[i][h] = sum_j softmax_j(scale * q[i][h] . K[s][h / G][j]) V[s][h / G][j]
+ * over the positions j < base and j = base + a for a = i and every ancestor a
+ * of i.  A node that sees no position (a padding node, context_lens[s] == 0)
+ * gets zeros; what is stored at positions a node does not see, infinities and
+ * NaN among it, does not reach its output.  One node per sequence, a root,
+ * gives paged_decode_attention's result up to summation order.
+ * Supported: head_dim 64 or 128, any num_q_heads that is a multiple of
+ * num_kv_heads with G = num_q_heads / num_kv_heads <= 128.  Deterministic as
+ * paged_decode_attention.  Errors as paged_decode_attention; KV_ERR_INVALID_ARG
+ * also for max_nodes < 1 or total_nodes < 0, KV_ERR_TOO_LARGE for max_nodes
+ * above KV_TREE_MAX_NODES. */
+int paged_tree_attention(void* out, int out_dtype, const void* q, const void* k_cache,
+                         const void* v_cache, int kv_dtype, float k_scale, float v_scale,
+                         int num_blocks, const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* node_starts,
+                         const int32_t* parents, int num_seqs, int total_nodes, int max_nodes,
+                         int num_q_heads, int num_kv_heads, int head_dim, float scale,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Flags of kv_tree_verify. */
+#define KV_VERIFY_GREEDY 1u   /* accept what the target would pick greedily */
+
+/* Verify each sequence's tree against the target's probabilities, from given
+ * uniform random numbers in [0, 1):
+ *   target_probs:  [total_nodes] rows of vocab probabilities, row stride
+ *                  target_stride elements, prob_dtype KV_DTYPE_F32 or
+ *                  KV_DTYPE_BF16: row i is the target's distribution of the
+ *                  token after node i
+ *   draft_probs:   likewise (draft_stride): row i is the distribution that node
+ *                  i's children were drawn from, independently; NULL: the
+ *                  children were chosen, not drawn (a drafted token has
+ *                  probability one)
+ *   tokens:        [total_nodes] int32, a node's token
+ *   accept_u:      [total_nodes] float32, the number node i is accepted by
+ *   sample_u:      [num_seqs] float32, the number the last token is drawn by
+ * The walk starts at node 0.  At node v, with p and q the two rows of v, let
+ * R = p, Z = 1, a = 0.  For each child c of v in index order, x = tokens[c]:
+ * it is accepted, and the walk goes on at c, if
+ *     accept_u[c] * q(x) * Z < R(x)       (draft_probs NULL: q(x) = 1);
+ * else a += Z, R = max(p - a q, 0), Z = sum R (draft_probs NULL: Z -= R(x),
+ * R(x) = 0): R / Z is the distribution that is left once the child is refused,
+ * so that the emitted tokens have the target's distribution.  Where no child
+ * is accepted, the last token is the first i with
+ *     sum_{j <= i} R(j) > sample_u[s] * sum_j R(j)
+ * (of p where R is zero everywhere; -1 where p is too).  Negative, infinite
+ * and NaN probabilities count as zero.  A child whose token is outside
+ * [0, vocab) is never accepted and changes nothing.  Sums run in twice the
+ * precision of float32 or more, so that the decisions are those of the
+ * formulas in double precision but for ties within its rounding.
+ * KV_VERIFY_GREEDY: target_probs may hold logits; a child is accepted if its
+ * token is the largest entry of v's row (NaN: never; the lowest index of equal
+ * ones), and the last token is that entry; draft_probs, accept_u and sample_u
+ * are not read and may be NULL.
+ * Outputs, for each sequence:
+ *   accept_lens:   [num_seqs] int32, the nodes on the accepted path, node 0
+ *                  among them (0 for a sequence without nodes)
+ *   accept_nodes:  [num_seqs][max_nodes] int32, their indices in the sequence's
+ *                  tree, in order, -1 after them
+ *   out_tokens:    [num_seqs][max_nodes] int32, the token after each of them:
+ *                  the accepted tokens, then the last token, -1 after it
+ * Padding nodes are never children.  One launch, no workspace, deterministic. */
+int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32_t* out_tokens,
+                   const void* target_probs, int64_t target_stride, const void* draft_probs,
+                   int64_t draft_stride, int prob_dtype, const int32_t* tokens,
+                   const int32_t* parents, const int32_t* node_starts, const float* accept_u,
+                   const float* sample_u, int num_seqs, int total_nodes, int max_nodes,
+                   int vocab, unsigned flags, void* stream);
+
+/* Move the K and V of the accepted nodes of each sequence's tree together, in
+ * every layer's cache: for i < accept_lens[s], the vectors at position
+ * base + accept_nodes[s][i] go to position base + i (all KV heads), in place.
+ *   k_caches, v_caches: host arrays of num_layers device pointers, the caches of
+ *                  the layers, all of the same shape, dtype and block tables
+ *   accept_nodes:  [num_seqs][max_nodes] int32, strictly increasing over its first
+ *                  accept_lens[s] entries, each less than n_s (as kv_tree_verify
+ *                  leaves it); accept_lens: [num_seqs] int32
+ * A path that breaks this raises KV_DEVERR_BAD_TREE and its sequence's moves
+ * are left out; a move from or to a block id outside [0, num_blocks) raises
+ * KV_DEVERR_BLOCK_OUT_OF_RANGE and is left out.  The blocks that hold the nodes
+ * must be private to their sequence (kv_tree_step's are).  Nothing else in the
+ * caches changes.  One launch for up to 128 layers. */
+int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers,
+                    const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* context_lens, const int32_t* node_starts,
+                    const int32_t* accept_nodes, const int32_t* accept_lens, int num_seqs,
+                    int max_nodes, int num_kv_heads, int head_dim, int num_blocks, int kv_dtype,
+                    void* stream);
 
 /* Read-only bandwidth ceiling (a measurement hook; the pages have no
  * counterpart): streams `bytes` of device memory at `buf` into shared memory

@@ -40,6 +40,10 @@ DEVERR_BLOCK_OUT_OF_RANGE = 2
 DEVERR_CONTEXT_TOO_LONG = 4
 DEVERR_PIPELINE_TIMEOUT = 8
 DEVERR_BAD_PREFIX = 16
+DEVERR_BAD_TREE = 32
+
+TREE_MAX_NODES = 128        # KV_TREE_MAX_NODES
+TREE_PAD = -2               # KV_TREE_PAD, the parent of a padding node
 
 # columns of a kv_alloc_trace row (KV_TRACE_*)
 TRACE_KEYS = ("seq_id", "slot", "len", "position", "blocks", "shared_blocks", "cache_bytes",
@@ -105,6 +109,14 @@ _SIGS = {
     "paged_decode_timed": (_i, [_p, _i, _p, _p, _p, _p, _p, _i, _f, _f, _i, _p, _i, _p, _i, _i,
                                 _i, _i, _f, _p, _p, _i, ctypes.c_uint, _p, ctypes.c_size_t, _p,
                                 _p, _p, _p]),
+    "kv_tree_step": (_i, [_p, _p, _p, _i, _p, _p, _i, _p, _p, _p, _p, _i, ctypes.POINTER(_i)]),
+    "kv_seq_truncate": (_i, [_p, _p, _p, _i]),
+    "paged_tree_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "paged_tree_attention": (_i, [_p, _i, _p, _p, _p, _i, _f, _f, _i, _p, _i, _p, _p, _p, _i, _i,
+                                  _i, _i, _i, _i, _f, _p, ctypes.c_size_t, _p]),
+    "kv_tree_verify": (_i, [_p, _p, _p, _p, _i64, _p, _i64, _i, _p, _p, _p, _p, _p, _i, _i, _i,
+                            _i, ctypes.c_uint, _p]),
+    "kv_tree_compact": (_i, [_p, _p, _i, _p, _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
     "kv_read_ceiling": (_i, [_p, ctypes.c_size_t, _p, _p]),
     "kv_test_pipeline_stall": (_i, [ctypes.c_longlong]),
     "kv_get_device_error": (_i, [ctypes.POINTER(_i), ctypes.POINTER(_i64)]),
@@ -132,6 +144,9 @@ _HOT_PAGED_DECODE = _hot("paged_decode")
 _HOT_PAGED_DECODE_STEP = _hot("paged_decode_step")
 _HOT_PAGED_DECODE_ATTENTION = _hot("paged_decode_attention")
 _HOT_KV_APPEND = _hot("kv_append")
+_HOT_TREE_ATTENTION = _hot("paged_tree_attention")
+_HOT_TREE_VERIFY = _hot("kv_tree_verify")
+_HOT_TREE_COMPACT = _hot("kv_tree_compact")
 
 
 def fast_path():
@@ -254,6 +269,39 @@ class BlockAllocator:
                             _np_ptr(lens), _np_ptr(src), _np_ptr(dst), cap, ctypes.byref(ncow)),
                "kv_step")
         return slots, bt, lens, (src[:ncow.value].copy(), dst[:ncow.value].copy())
+
+    def tree_step(self, seq_ids, num_nodes, max_blocks, cow_cap=None):
+        """Plan one step that appends num_nodes[i] drafted tokens to sequence
+        seq_ids[i] (kv_tree_step); returns (slot_mapping int64[sum],
+        block_tables int32[n, max_blocks], context_lens int32[n], node_starts
+        int32[n + 1], (cow_src, cow_dst))."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        counts = np.ascontiguousarray(num_nodes, dtype=np.int32)
+        n = ids.shape[0]
+        assert counts.shape == ids.shape
+        cap = n if cow_cap is None else cow_cap
+        slots = np.empty(max(int(np.maximum(counts, 0).sum(dtype=np.int64)), 1), dtype=np.int64)
+        bt = np.empty((n, max_blocks), dtype=np.int32)
+        lens = np.empty(n, dtype=np.int32)
+        starts = np.empty(n + 1, dtype=np.int32)
+        src = np.empty(max(cap, 1), dtype=np.int32)
+        dst = np.empty(max(cap, 1), dtype=np.int32)
+        ncow = _i(0)
+        _check(_lib.kv_tree_step(self._h, _np_ptr(ids), _np_ptr(counts), n, _np_ptr(slots),
+                                 _np_ptr(bt), max_blocks, _np_ptr(lens), _np_ptr(starts),
+                                 _np_ptr(src), _np_ptr(dst), cap, ctypes.byref(ncow)),
+               "kv_tree_step")
+        return (slots[:starts[n]], bt, lens, starts,
+                (src[:ncow.value].copy(), dst[:ncow.value].copy()))
+
+    def truncate(self, seq_ids, new_lens):
+        """Cut sequence seq_ids[i] to new_lens[i] tokens; blocks behind them
+        return to the pool (kv_seq_truncate)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        lens = np.ascontiguousarray(new_lens, dtype=np.int64)
+        assert ids.shape == lens.shape
+        _check(_lib.kv_seq_truncate(self._h, _np_ptr(ids), _np_ptr(lens), ids.shape[0]),
+               "kv_seq_truncate")
 
     def reorder(self, seq_ids, src_index):
         """Row i of seq_ids takes the KV state row src_index[i] had (beam
@@ -523,6 +571,167 @@ def paged_decode_timed(out, q, k_cache, v_cache, block_tables, context_lens, sca
         DECODE_EARLY_INPUTS if early_inputs else 0, _dptr(workspace),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream), ev[0], ev[1], ev[2]),
         "paged_decode_timed")
+
+
+# ------------------------------------------------------- trees of drafted tokens
+
+def _int32(name, t, *shape):
+    """The address of a contiguous int32 tensor of the given shape (None: any)."""
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or any(
+            want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, list(shape)))
+    return t.data_ptr()
+
+
+def _reachable(*tensors):
+    """A call launches on the current device: its tensors have to be there, or
+    in pinned host memory."""
+    import torch
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            if not t.is_pinned():
+                raise ValueError("tensors must be on the device or in pinned host memory")
+        elif t.device.index != torch.cuda.current_device():
+            raise ValueError("tensor on %s, current device is cuda:%d"
+                             % (t.device, torch.cuda.current_device()))
+
+
+def tree_workspace_bytes(num_seqs, max_nodes, num_q_heads, num_kv_heads, head_dim, kv_dtype=BF16):
+    n = ctypes.c_size_t(0)
+    _check(_lib.paged_tree_workspace_bytes(num_seqs, max_nodes, num_q_heads, num_kv_heads,
+                                           head_dim, kv_dtype, ctypes.byref(n)),
+           "paged_tree_workspace_bytes")
+    return n.value
+
+
+def alloc_tree_workspace(num_seqs, max_nodes, num_q_heads, num_kv_heads, head_dim, kv_dtype=BF16,
+                         device=None):
+    import torch
+    nbytes = tree_workspace_bytes(num_seqs, max_nodes, num_q_heads, num_kv_heads, head_dim,
+                                  kv_dtype)
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_tree_attention(out, q, k_cache, v_cache, block_tables, context_lens, node_starts,
+                         parents, max_nodes, scale, workspace, k_scale=1.0, v_scale=1.0,
+                         stream=None):
+    """out [T, Hq, D] (bfloat16 or float32) = attention of the T nodes' queries
+    q [T, Hq, D] (bfloat16) over the paged caches, each node seeing its
+    sequence's committed tokens, its ancestors in the drafted tree and itself
+    (paged_tree_attention): node_starts int32 [B + 1], parents int32 [T]
+    (None: chains), context_lens int32 [B] including the nodes, at most
+    max_nodes nodes a sequence; workspace from alloc_tree_workspace."""
+    import torch
+    T, Hq, D = q.shape
+    NB, Hkv, _, D2 = k_cache.shape
+    B, max_blocks = block_tables.shape
+    if (q.dtype != torch.bfloat16 or out.dtype not in (torch.bfloat16, torch.float32)
+            or out.shape != q.shape or D != D2 or k_cache.shape != v_cache.shape
+            or k_cache.dtype != v_cache.dtype):
+        raise ValueError("q must be bfloat16 [T, Hq, D], out bfloat16 or float32 of its shape, "
+                         "k_cache and v_cache alike")
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous()):
+        raise ValueError("q, out and the caches must be contiguous")
+    _reachable(q, out, k_cache, v_cache, block_tables, context_lens, node_starts, parents,
+                 workspace)
+    _check(_HOT_TREE_ATTENTION(
+        out.data_ptr(), F32 if out.dtype == torch.float32 else BF16, q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), _cache_dtype(k_cache), float(k_scale),
+        float(v_scale), NB, _int32("block_tables", block_tables, B, max_blocks), max_blocks,
+        _int32("context_lens", context_lens, B), _int32("node_starts", node_starts, B + 1),
+        _int32("parents", parents, T) if parents is not None else 0, B, T, int(max_nodes), Hq,
+        Hkv, D, float(scale), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_int(stream)),
+        "paged_tree_attention")
+
+
+VERIFY_GREEDY = 1           # KV_VERIFY_GREEDY
+
+
+def kv_tree_verify(accept_lens, accept_nodes, out_tokens, target_probs, tokens, parents,
+                   node_starts, accept_u=None, sample_u=None, draft_probs=None, greedy=False,
+                   stream=None):
+    """Verify drafted trees against the target's probabilities from given
+    uniform numbers (kv_tree_verify).  target_probs [T, V] (and draft_probs,
+    or None: the children were chosen, not drawn) float32 or bfloat16 with any
+    row stride; tokens, parents (None: chains) int32 [T], node_starts int32
+    [B + 1], accept_u float32 [T], sample_u float32 [B].  Writes accept_lens
+    int32 [B], accept_nodes and out_tokens int32 [B, max_nodes].  greedy:
+    target_probs may be logits; accept_u, sample_u and draft_probs are not
+    used."""
+    import torch
+    T, V = target_probs.shape
+    B, max_nodes = accept_nodes.shape
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("target_probs must be float32 or bfloat16")
+    draft = None if greedy else draft_probs
+    if draft is not None and (draft.dtype != target_probs.dtype
+                              or draft.shape != target_probs.shape):
+        raise ValueError("draft_probs must have target_probs' type and shape")
+    for p in (target_probs, draft):
+        if p is not None and V > 1 and p.stride(1) != 1:
+            raise ValueError("the rows of probabilities must be contiguous")
+    if not greedy:
+        for u, n in ((accept_u, T), (sample_u, B)):
+            if u is None or u.dtype != torch.float32 or u.shape != (n,) or not u.is_contiguous():
+                raise ValueError("accept_u and sample_u must be contiguous float32 [T] and [B]")
+    _reachable(target_probs, accept_lens, accept_nodes, out_tokens, tokens, parents,
+                 node_starts, draft, None if greedy else accept_u, None if greedy else sample_u)
+    _check(_HOT_TREE_VERIFY(
+        _int32("accept_lens", accept_lens, B), _int32("accept_nodes", accept_nodes, B, max_nodes),
+        _int32("out_tokens", out_tokens, B, max_nodes), target_probs.data_ptr(),
+        target_probs.stride(0) if T > 1 else V, draft.data_ptr() if draft is not None else 0,
+        (draft.stride(0) if T > 1 else V) if draft is not None else 0,
+        F32 if target_probs.dtype == torch.float32 else BF16, _int32("tokens", tokens, T),
+        _int32("parents", parents, T) if parents is not None else 0,
+        _int32("node_starts", node_starts, B + 1), 0 if greedy else accept_u.data_ptr(),
+        0 if greedy else sample_u.data_ptr(), B, T, max_nodes, V, VERIFY_GREEDY if greedy else 0,
+        _stream_int(stream)), "kv_tree_verify")
+
+
+class CacheLayers:
+    """The K and V caches of a model's layers, all of one shape, dtype and
+    device: what a program keeps to pass to kv_tree_compact."""
+
+    def __init__(self, k_caches, v_caches):
+        if not k_caches or len(k_caches) != len(v_caches):
+            raise ValueError("one K and one V cache per layer")
+        first = k_caches[0]
+        for t in list(k_caches) + list(v_caches):
+            if (t.shape != first.shape or t.dtype != first.dtype or t.device != first.device
+                    or not t.is_contiguous() or t.dim() != 4 or t.shape[2] != BLOCK_SIZE):
+                raise ValueError("caches must be contiguous [NB, Hkv, 16, D], all alike")
+        self.tensors = (list(k_caches), list(v_caches))     # keeps the memory alive
+        self.num_layers = len(k_caches)
+        self.num_blocks, self.num_kv_heads, _, self.head_dim = first.shape
+        self.kv_dtype = _cache_dtype(first)
+        self.first = first
+        self._k = (_p * self.num_layers)(*[t.data_ptr() for t in k_caches])
+        self._v = (_p * self.num_layers)(*[t.data_ptr() for t in v_caches])
+        self.k_ptrs = ctypes.addressof(self._k)
+        self.v_ptrs = ctypes.addressof(self._v)
+
+
+def kv_tree_compact(layers, block_tables, context_lens, node_starts, accept_nodes, accept_lens,
+                    stream=None):
+    """Move the accepted nodes' K and V together in the caches of all layers (a
+    CacheLayers), in place (kv_tree_compact): node accept_nodes[s, i] goes to
+    position base + i, base = context_lens[s] less the tree's nodes."""
+    B, max_nodes = accept_nodes.shape
+    max_blocks = block_tables.shape[1]
+    _reachable(layers.first, block_tables, context_lens, node_starts, accept_nodes, accept_lens)
+    _check(_HOT_TREE_COMPACT(
+        layers.k_ptrs, layers.v_ptrs, layers.num_layers,
+        _int32("block_tables", block_tables, B, max_blocks), max_blocks,
+        _int32("context_lens", context_lens, B), _int32("node_starts", node_starts, B + 1),
+        _int32("accept_nodes", accept_nodes, B, max_nodes),
+        _int32("accept_lens", accept_lens, B), B, max_nodes, layers.num_kv_heads,
+        layers.head_dim, layers.num_blocks, layers.kv_dtype, _stream_int(stream)),
+        "kv_tree_compact")
 
 
 def read_ceiling(buf, sink, stream=None):

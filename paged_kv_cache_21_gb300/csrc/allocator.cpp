@@ -201,6 +201,113 @@ int kv_step(kv_alloc_t* a, const int64_t* seq_ids, int n, int64_t* slot_mapping,
     return KV_OK;
 }
 
+int kv_tree_step(kv_alloc_t* a, const int64_t* seq_ids, const int32_t* num_nodes, int n,
+                 int64_t* slot_mapping, int32_t* block_tables, int max_blocks,
+                 int32_t* context_lens, int32_t* node_starts, int32_t* cow_src,
+                 int32_t* cow_dst, int cow_cap, int* n_cow)
+try {
+    if (!a || n < 0 || max_blocks <= 0 || cow_cap < 0 || !node_starts) return KV_ERR_INVALID_ARG;
+    if (n > 0 && (!seq_ids || !num_nodes || !block_tables || !context_lens))
+        return KV_ERR_INVALID_ARG;
+    if (cow_cap > 0 && (!cow_src || !cow_dst)) return KV_ERR_INVALID_ARG;
+    if (n_cow) *n_cow = 0;
+
+    // Pass 1: check and count, with the reference counts as kv_step has them
+    // (of sequences that share a tail block, all but the last copy it).
+    std::unordered_set<int64_t> seen;
+    std::unordered_map<int32_t, int> ref_delta;
+    std::vector<Seq*> rows(n);
+    int64_t need_new = 0, need_cow = 0, total = 0;
+    for (int i = 0; i < n; ++i) {
+        auto it = a->seqs.find(seq_ids[i]);
+        if (it == a->seqs.end()) return KV_ERR_NOT_FOUND;
+        if (!seen.insert(seq_ids[i]).second || num_nodes[i] < 0) return KV_ERR_INVALID_ARG;
+        Seq& s = it->second;
+        rows[i] = &s;
+        const int64_t blocks = ceil_blocks(s.len + num_nodes[i]);
+        if (blocks > max_blocks || s.len + num_nodes[i] > INT32_MAX) return KV_ERR_INVALID_ARG;
+        total += num_nodes[i];
+        if (num_nodes[i] == 0) continue;
+        need_new += blocks - ceil_blocks(s.len);
+        if (s.len % KV_BLOCK_SIZE != 0) {
+            const int32_t tail = s.blocks[s.len / KV_BLOCK_SIZE];
+            if (a->refcount[tail] + ref_delta[tail] > 1) {
+                need_new += 1;
+                need_cow += 1;
+                ref_delta[tail] -= 1;
+            }
+        }
+    }
+    if (total > INT32_MAX || (total > 0 && !slot_mapping)) return KV_ERR_INVALID_ARG;
+    if (need_new > (int64_t)a->free_list.size()) return KV_ERR_OUT_OF_BLOCKS;
+    if (need_cow > cow_cap) return KV_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)     // what could throw does so before anything changes
+        rows[i]->blocks.reserve(ceil_blocks(rows[i]->len + num_nodes[i]));
+
+    // Pass 2: apply.
+    int ncow = 0;
+    node_starts[0] = 0;
+    for (int i = 0; i < n; ++i) {
+        Seq& s = *rows[i];
+        const int64_t pos = s.len, end = pos + num_nodes[i];
+        if (end > pos && pos % KV_BLOCK_SIZE != 0) {
+            const int32_t tail = s.blocks[pos / KV_BLOCK_SIZE];
+            if (a->refcount[tail] > 1) {
+                const int32_t fresh = a->take();
+                cow_src[ncow] = tail;
+                cow_dst[ncow] = fresh;
+                ++ncow;
+                a->release(tail);
+                s.blocks[pos / KV_BLOCK_SIZE] = fresh;
+            }
+        }
+        while ((int64_t)s.blocks.size() < ceil_blocks(end)) s.blocks.push_back(a->take());
+        for (int64_t p = pos; p < end; ++p)
+            slot_mapping[node_starts[i] + (p - pos)] =
+                (int64_t)s.blocks[p / KV_BLOCK_SIZE] * KV_BLOCK_SIZE + p % KV_BLOCK_SIZE;
+        node_starts[i + 1] = node_starts[i] + num_nodes[i];
+        s.len = end;
+        s.slot = i;
+        context_lens[i] = (int32_t)end;
+        int32_t* row = block_tables + (int64_t)i * max_blocks;
+        const int nb = (int)s.blocks.size();
+        std::copy(s.blocks.begin(), s.blocks.end(), row);
+        for (int j = nb; j < max_blocks; ++j) row[j] = -1;
+    }
+    if (n_cow) *n_cow = ncow;
+    return KV_OK;
+} catch (...) {      // out of host memory, before anything changed
+    return KV_ERR_INVALID_ARG;
+}
+
+int kv_seq_truncate(kv_alloc_t* a, const int64_t* seq_ids, const int64_t* new_lens, int n)
+try {
+    if (!a || n < 0 || (n > 0 && (!seq_ids || !new_lens))) return KV_ERR_INVALID_ARG;
+    std::unordered_set<int64_t> seen;
+    std::vector<Seq*> rows(n);
+    int64_t dropped = 0;
+    for (int i = 0; i < n; ++i) {
+        auto it = a->seqs.find(seq_ids[i]);
+        if (it == a->seqs.end()) return KV_ERR_NOT_FOUND;
+        if (!seen.insert(seq_ids[i]).second || new_lens[i] < 0 || new_lens[i] > it->second.len)
+            return KV_ERR_INVALID_ARG;
+        rows[i] = &it->second;
+        dropped += (int64_t)it->second.blocks.size() - ceil_blocks(new_lens[i]);
+    }
+    a->free_list.reserve(a->free_list.size() + dropped);
+    for (int i = 0; i < n; ++i) {
+        Seq& s = *rows[i];
+        s.len = new_lens[i];
+        while ((int64_t)s.blocks.size() > ceil_blocks(s.len)) {
+            a->release(s.blocks.back());
+            s.blocks.pop_back();
+        }
+    }
+    return KV_OK;
+} catch (...) {
+    return KV_ERR_INVALID_ARG;
+}
+
 int kv_seq_reorder(kv_alloc_t* a, const int64_t* seq_ids, const int32_t* src_index, int n)
 {
     if (!a || n < 0) return KV_ERR_INVALID_ARG;

@@ -11,6 +11,9 @@ int num_sms_current();
 // Read and clear the sticky device error word of one translation unit.
 int append_read_error(unsigned* flags, long long* detail);
 int decode_read_error(unsigned* flags, long long* detail);
+int tree_read_error(unsigned* flags, long long* detail);
+int verify_read_error(unsigned* flags, long long* detail);
+int compact_read_error(unsigned* flags, long long* detail);
 
 // The decision of kv_prefix_plan for a given number of resident warps of the
 // split-KV kernel (host only; allocator.cpp).

@@ -2215,13 +2215,20 @@ extern "C" int paged_decode_step(void* out, int out_dtype, const void* q, const 
 
 extern "C" int kv_get_device_error(int* flags, int64_t* detail)
 {
-    unsigned f1 = 0, f2 = 0, f3 = 0;
-    long long d1 = -1, d2 = -1, d3 = -1;
-    if (int rc = append_read_error(&f1, &d1)) return rc;
-    if (int rc = decode_read_error(&f2, &d2)) return rc;
-    if (int rc = wide_read_error(&f3, &d3)) return rc;
-    if (flags) *flags = (int)(f1 | f2 | f3);
-    if (detail) *detail = f1 ? d1 : (f2 ? d2 : d3);
+    int (*const words[])(unsigned*, long long*) = {append_read_error, decode_read_error,
+                                                   wide_read_error, tree_read_error,
+                                                   verify_read_error, compact_read_error};
+    unsigned all = 0;
+    long long first = -1;
+    for (auto read : words) {
+        unsigned f = 0;
+        long long d = -1;
+        if (int rc = read(&f, &d)) return rc;
+        if (f && !all) first = d;
+        all |= f;
+    }
+    if (flags) *flags = (int)all;
+    if (detail) *detail = first;
     return KV_OK;
 }
 
