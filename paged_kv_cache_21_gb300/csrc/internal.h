@@ -8,6 +8,9 @@ namespace pkv {
 // Number of SMs of the current device (cached per device), or 1 on error.
 int num_sms_current();
 
+// The clocks of kv_test_pipeline_stall (0: off).
+long long test_stall_cycles();
+
 // Read and clear the sticky device error word of one translation unit.
 int append_read_error(unsigned* flags, long long* detail);
 int decode_read_error(unsigned* flags, long long* detail);

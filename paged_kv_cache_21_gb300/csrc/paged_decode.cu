@@ -67,6 +67,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache_map.h"
 #include "device_common.cuh"
 #include "internal.h"
 #include "paged_kv.h"
@@ -2017,6 +2018,13 @@ int decode_launch(void* out, int out_dtype, const void* q, const void* k_cache,
 }
 
 }  // namespace
+
+int cache_tensor_map(CUtensorMap* map, const void* base, int D, bool fp8, int num_blocks, int Hkv)
+{
+    return make_cache_map(map, base, D, fp8, num_blocks, Hkv);
+}
+
+long long test_stall_cycles() { return g_test_stall.load(std::memory_order_relaxed); }
 
 int num_sms_current()
 {

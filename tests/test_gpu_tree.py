@@ -302,6 +302,52 @@ def test_repeated_calls_are_bit_identical_and_physical_places_do_not_matter(pk):
     assert torch.equal(first, b.run(pk))
 
 
+@pytest.mark.parametrize("heads,n,fp8", [((32, 8), 8, False), ((32, 8), 30, False),
+                                         ((32, 8), 64, False), ((16, 8), 20, True),
+                                         ((32, 8), 48, True)])
+def test_a_full_gpu_of_long_contexts(pk, heads, n, fp8):
+    """Enough bytes that every copy takes its time: the 64-bit formula on the GPU
+    for all rows, and the same bits from every call."""
+    Hq, Hkv, D, B, L = heads[0], heads[1], 128, 24, 3000 + n
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    nb = -(-L // BS)
+    NB = B * nb
+    bt = torch.randperm(NB, generator=gen, device="cuda").to(torch.int32).view(B, nb)
+    x = [torch.randn((NB, Hkv, BS, D), generator=gen, device="cuda") for _ in range(2)]
+    ks = vs = 1.0
+    if fp8:
+        ks, vs = 0.02, 0.03
+        k, v = ((t / s).clamp(-448, 448).to(torch.float8_e4m3fn) for t, s in zip(x, (ks, vs)))
+    else:
+        k, v = (t.to(torch.bfloat16) for t in x)
+    q = torch.randn((B * n, Hq, D), generator=gen, device="cuda").to(torch.bfloat16)
+    rng = np.random.default_rng(n)
+    par = np.concatenate([R.random_tree(rng, n, 3) for _ in range(B)]).astype(np.int32)
+    starts = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    ws = pk.alloc_tree_workspace(B, n, Hq, Hkv, D, pk.FP8_E4M3 if fp8 else pk.BF16)
+    dpar = torch.from_numpy(par).cuda()
+    outs = []
+    for _ in range(8):
+        outs.append(torch.empty((B * n, Hq, D), dtype=torch.float32, device="cuda"))
+        pk.paged_tree_attention(outs[-1], q, k, v, bt, lens, starts, dpar, n, D ** -0.5, ws, ks, vs)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    G = Hq // Hkv
+    for s in range(B):
+        K, V = (t[bt[s].long()].double().transpose(0, 1).reshape(Hkv, -1, D)[:, :L] * z
+                for t, z in ((k, ks), (v, vs)))
+        Q = q[s * n:(s + 1) * n].double().view(n, Hkv, G, D).transpose(0, 1).reshape(Hkv, n * G, D)
+        mask = torch.zeros((n, L), dtype=torch.float64)
+        mask[:, L - n:] = -np.inf
+        for i, seen in enumerate(R.ancestors(par[s * n:(s + 1) * n])):
+            mask[i, [L - n + j for j in seen]] = 0
+        w = torch.softmax(Q @ K.transpose(1, 2) * D ** -0.5
+                          + mask.cuda().repeat_interleave(G, 0)[None], -1)
+        ref = (w @ V).view(Hkv, n, G, D).transpose(0, 1).reshape(n, Hq, D)
+        tol = 2 * float(V.abs().max()) * (2.0 ** -10 if fp8 else 2.0 ** -12)
+        assert float((outs[0][s * n:(s + 1) * n].double() - ref).abs().max()) <= tol
+
+
 def test_two_streams_and_two_captured_graphs(pk):
     cases = [Case([2500, 400], [20, 5], 16, 4, 128, seed=14),
              Case([90, 4000], [3, 64], 32, 8, 128, True, seed=15)]
