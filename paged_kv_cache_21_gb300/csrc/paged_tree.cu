@@ -56,6 +56,7 @@
 #include <climits>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "cache_map.h"
 #include "device_common.cuh"
@@ -81,6 +82,18 @@ constexpr float kMaxLag = 8.f;                  // the reference maximum may lag
 // rounds to zero is below 2^-31 of the largest weight
 constexpr float kBiasF16 = 7.f;
 
+// Columns of O joined at a time, and the floats between two rows of them.
+constexpr int kStageCols = 16, kStageRow = 17;
+
+// Few rows leave most of a tile's 128 lanes empty.  They are then repeated: R
+// copies of up to 128 / R rows, copy i (a quarter or a half of the lanes, the
+// warps that own them) with the weights of the i-th share of each chunk's keys
+// and zeros for the rest, so that the exponentials are spread over all warps.
+__host__ __device__ constexpr int row_copies(int rows)
+{
+    return rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+}
+
 // A stream's chunks: every second one, or all.
 constexpr int chunk_step(int tiles) { return tiles == 1 ? 2 : 1; }
 
@@ -100,7 +113,7 @@ struct Geo {
     // ring of codes in front of them
     static constexpr int kSlots = FP8 ? (D == 128 ? 3 : 6)
                                       : (TILES == 1 ? 5 : 4) * (D == 128 ? 1 : 2);
-    static constexpr int kRawSlots = !FP8 ? 0 : (TILES == 1 ? 5 : 3) * (D == 128 ? 1 : 2);
+    static constexpr int kRawSlots = !FP8 ? 0 : (TILES == 1 ? 4 : 3) * (D == 128 ? 1 : 2);
     static constexpr int kLoadSlots = FP8 ? kRawSlots : kSlots;
     static constexpr int kQOff = 0;
     static constexpr int kSlotOff = kQOff + TILES * kQTile;
@@ -119,8 +132,9 @@ struct Geo {
     static constexpr int B_PVDONE = B_PFULL + 2;             // + stream
     static constexpr int B_OFULL = B_PVDONE + 2;             // both accumulators are complete
     static constexpr int B_OFREE = B_OFULL + 1;              // + segment & 1: they have been read
-    static constexpr int B_ML = B_OFREE + 2;                 // the streams' (max, sum) are written
-    static constexpr int B_END = B_ML + 1;                   // + stream: all its MMAs are done
+    static constexpr int B_ML = B_OFREE + 2;                 // partial (max, sum)s are written
+    static constexpr int B_STAGE = B_ML + 1;                 // staged partials are written / read
+    static constexpr int B_END = B_STAGE + 1;                // + stream: all its MMAs are done
     static constexpr int B_STALL = B_END + 2;                // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
@@ -128,8 +142,12 @@ struct Geo {
     static constexpr int kPtrOff = kAncOff + 2 * kN * 16;    // [kN] bytes used by pointer jumping
     static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
     static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
-    static constexpr int kMlOff = kBadOff + 2 * kPrepWarps * 16;  // [2][kTile] float2 (TILES == 1)
-    static constexpr int kQfacOff = kMlOff + (TILES == 1 ? 2 * kTile * 8 : 0);
+    // the warps whose partial results of a row are joined in the CTA: those of
+    // both streams (TILES == 1) or of one
+    static constexpr int kJoinWarps = TILES == 1 ? 8 : 4;
+    static constexpr int kMlOff = kBadOff + 2 * kPrepWarps * 16;  // [kJoinWarps][32] float2
+    static constexpr int kStageOff = kMlOff + kJoinWarps * 32 * 8;  // [kJoinWarps][32][kStageRow]
+    static constexpr int kQfacOff = kStageOff + kJoinWarps * 32 * kStageRow * 4;
     static constexpr int kEnd = kQfacOff + (FP8 ? 2 * TILES * kTile * 4 : 0);
     static constexpr int kSmem = kEnd + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -391,7 +409,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             mbar_init(bar(G::B_END + w), 1);
         }
         mbar_init(bar(G::B_OFULL), 2);
-        mbar_init(bar(G::B_ML), 8);
+        mbar_init(bar(G::B_ML), G::kJoinWarps);
+        mbar_init(bar(G::B_STAGE), G::kJoinWarps);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
         misc[M_ISSUED] = 0;
@@ -643,6 +662,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             // ---- the query rows of the team's tiles
             const int r0 = team * TILES * kTile;
             const int rows = min(n * p.G - r0, TILES * kTile);
+            const int copies = row_copies(n * p.G - r0), stride = kTile / copies;
             constexpr int C = D / 8;             // 16-byte chunks (8 elements) of a row
             constexpr int RI = 32 / C;           // rows of a warp's instruction
             const int c = lane % C;
@@ -654,8 +674,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     p.q + ((size_t)(w.q.t0 + node) * p.Hq + (size_t)w.h * p.G + g) * D + 8 * c;
                 const uint32_t dst = sb + (uint32_t)(G::kQOff + (rc >> 7) * G::kQTile + (c >> 3) * kTile * 128) +
                                      region_off(rc & 127, c & 7);
+                // (a copy's rows are a multiple of 8 on: the same place in the swizzle)
                 if (!FP8) {
-                    if (r < rows) cp_async16(dst, src);
+                    if (r < rows)
+                        for (int k = 0; k < copies; ++k) cp_async16(dst + (uint32_t)(k * stride * 128), src);
                 } else {
                     // f16 overflows above 65504: a row whose largest |element| is 2^15
                     // or more is divided by a power of two that brings it below (exact
@@ -677,7 +699,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     for (int k = 0; k < 4; ++k)
                         h4[k] = pack_f16x2(bf16_lo(q4[k]) * down, bf16_hi(q4[k]) * down);
                     if (r < rows) {
-                        sts128(dst, make_uint4(h4[0], h4[1], h4[2], h4[3]));
+                        for (int k = 0; k < copies; ++k)
+                            sts128(dst + (uint32_t)(k * stride * 128), make_uint4(h4[0], h4[1], h4[2], h4[3]));
                         if (c == 0)
                             reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * TILES * kTile + r] = up;
                     }
@@ -789,34 +812,48 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (pw == 0 && lane == 0) misc[M_ISSUED] = hx + 1;
                         const uint32_t raw = sb + (uint32_t)(G::kRawOff + rs * G::kRawSlot);
                         const uint32_t dst = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
-                        for (int rb = 0; rb < keys; rb += RS) {
-                            const int r = rb + t / CR;
-                            uint32_t v[4] = {0u, 0u, 0u, 0u};
-                            if (r < keys) {
-                                // the copy's swizzle: 16-byte pieces XOR bits 7 and up
-                                const uint32_t a = (uint32_t)(r * D + cc * 16);
-                                lds128(v, raw + (a ^ (((a >> 7) & (D == 128 ? 7u : 3u)) << 4)));
+                        // the copy's swizzle: 16-byte pieces XOR bits 7 and up
+                        auto load = [&](int r, uint32_t (&v)[4]) {
+                            const uint32_t a = (uint32_t)(r * D + cc * 16);
+                            lds128(v, raw + (a ^ (((a >> 7) & (D == 128 ? 7u : 3u)) << 4)));
+                        };
+                        // (the pieces of the second column group go in the other order:
+                        // the eight lanes of a row then write to all banks at once)
+                        auto store = [&](int r, const uint32_t (&v)[4]) {
+                            const uint32_t d0 = dst + (uint32_t)((cc >> 2) * G::kRegion);
+                            uint4 o[2];
+                            o[0] = make_uint4(e4m3x2_to_f16x2(v[0]), e4m3x2_to_f16x2(v[0] >> 16),
+                                              e4m3x2_to_f16x2(v[1]), e4m3x2_to_f16x2(v[1] >> 16));
+                            o[1] = make_uint4(e4m3x2_to_f16x2(v[2]), e4m3x2_to_f16x2(v[2] >> 16),
+                                              e4m3x2_to_f16x2(v[3]), e4m3x2_to_f16x2(v[3] >> 16));
+                            const int second = (cc >> 2) & 1;
+                            sts128(d0 + region_off(r, (2 * cc + second) & 7), second ? o[1] : o[0]);
+                            sts128(d0 + region_off(r, (2 * cc + 1 - second) & 7), second ? o[0] : o[1]);
+                        };
+                        if (keys == kKeys && !(kv == 1 && drafted)) {
+                            constexpr int kStep = 4;         // loads in flight
+#pragma unroll
+                            for (int rb = 0; rb < kKeys; rb += kStep * RS) {
+                                uint32_t v[kStep][4];
+#pragma unroll
+                                for (int k = 0; k < kStep; ++k) load(rb + k * RS + t / CR, v[k]);
+#pragma unroll
+                                for (int k = 0; k < kStep; ++k) store(rb + k * RS + t / CR, v[k]);
                             }
-                            if (kv == 1 && drafted) {
-                                const int pos = p0 + r;
-                                if (pos >= w.q.L) {
+                        } else {
+                            for (int rb = 0; rb < keys; rb += RS) {
+                                const int r = rb + t / CR, pos = p0 + r;
+                                if (r >= keys) continue;
+                                uint32_t v[4];
+                                load(r, v);
+                                if (kv == 1 && pos >= w.q.L) {
                                     v[0] = v[1] = v[2] = v[3] = 0u;
-                                } else if (r < keys && pos >= w.q.base && drop_non_finite<true>(v)) {
+                                } else if (kv == 1 && pos >= w.q.base && drop_non_finite<true>(v)) {
                                     const int an = pos - w.q.base;
                                     atomicOr(const_cast<uint32_t*>(&badw[(buf * G::kPrepWarps + pw) * 4 + (an >> 5)]),
                                              1u << (an & 31));
                                 }
-                            }
-                            if (r < keys) {
-                                const uint32_t d0 = dst + (uint32_t)((cc >> 2) * G::kRegion);
-                                uint32_t o[8];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    o[2 * k] = e4m3x2_to_f16x2(v[k]);
-                                    o[2 * k + 1] = e4m3x2_to_f16x2(v[k] >> 16);
-                                }
-                                sts128(d0 + region_off(r, (2 * cc) & 7), make_uint4(o[0], o[1], o[2], o[3]));
-                                sts128(d0 + region_off(r, (2 * cc + 1) & 7), make_uint4(o[4], o[5], o[6], o[7]));
+                                store(r, v);
                             }
                         }
                         fence_proxy_async_smem();
@@ -851,18 +888,21 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
         }
         if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-        int pc = 0, flat = misc[M_B0];
+        int pc = 0, flat = misc[M_B0], joins = 0, stages = 0;
         bool ok = true;
         for (Walk<TILES> w(p, misc, team); ok && w.more(); w.next(p, team)) {
             const int seg = w.seg, buf = seg & 1, nc = w.chunks();
             const int r0 = team * TILES * kTile;
             const int rows = w.q.n * p.G - r0;   // rows of this team and those behind it
-            const int rt = r + (TILES == 2 ? st * kTile : 0);
+            const int copies = row_copies(rows);
             const bool idle = TILES == 2 && st == 1 && rows <= kTile;
+            const int rt = (r & (kTile / copies - 1)) + (TILES == 2 ? st * kTile : 0);
             const bool warp_live = (rt & ~31) < rows;
             const bool in = rt < rows;
             const int node = in ? row_node(p, r0 + rt) : 0;
             const uint32_t* am = anc + (buf * kN + node) * 4;
+            // the groups of 32 keys of a chunk that this warp's copy weighs
+            const int gshare = 4 / copies, g_lo = (warp & 3) * copies / 4 * gshare, g_hi = g_lo + gshare;
             float m_ref = -INFINITY, l = 0.f;
             float sl2 = p.sl2;
             bool first = true;
@@ -877,6 +917,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const int p0 = (w.j + c * kPages) * kBlock;
                     const bool masked = np < kPages || w.drafted(c);
                     const int ng = (np + 1) / 2;         // groups of 32 keys
+                    const int g_end = min(g_hi, ng);
                     // the keys of group g this row sees, as bits
                     auto visible = [&](int g) -> uint32_t {
                         const int a0 = p0 + 32 * g - w.q.base;   // tree index of the first key
@@ -894,61 +935,89 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (lim < 32) v &= lim <= 0 ? 0u : (1u << lim) - 1u;
                         return v;
                     };
-                    // ---- the largest scaled score
-                    float mx = -INFINITY;
-                    for (int g = 0; g < ng; ++g) {
-                        uint32_t sr[32];
-                        umma::tmem_ld32(tS + (uint32_t)(32 * g), sr);
-                        umma::tmem_wait_ld();
-                        float a = -INFINITY, b = -INFINITY;
+                    // the largest scaled score of a group
+                    auto group_max = [&](const uint32_t (&sr)[32], uint32_t vis) -> float {
+                        float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                         if (!masked && sl2 >= 0.f) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                a = fmaxf(a, __uint_as_float(sr[k]));
-                                b = fmaxf(b, __uint_as_float(sr[k + 1]));
-                            }
-                            mx = fmaxf(mx, fmaxf(a, b) * sl2);
-                        } else {
-                            const uint32_t vis = masked ? visible(g) : ~0u;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                a = fmaxf(a, (vis >> k) & 1u ? __uint_as_float(sr[k]) * sl2 : -INFINITY);
-                            mx = fmaxf(mx, a);
+                            for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], __uint_as_float(sr[k]));
+                            return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * sl2;
                         }
-                    }
-                    // ---- the reference moves only when it lags by more than 2^8; what
-                    // has been accumulated is then scaled down in place
-                    bool move = false;
-                    float alpha = 1.f;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            a[k & 3] = fmaxf(a[k & 3], (vis >> k) & 1u ? __uint_as_float(sr[k]) * sl2 : -INFINITY);
+                        return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                    };
                     if (first) {
-                        m_ref = mx;
-                    } else if (in && mx > m_ref + kMaxLag) {
-                        alpha = ex2(m_ref - mx);         // 0 while nothing was seen
-                        m_ref = mx;
-                        l *= alpha;
-                        move = true;
-                    }
-                    if (__any_sync(kFull, move)) {
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            umma::tmem_ld32(tO0 + (uint32_t)(128 * st + c0), o);
+                        // the first chunk sets the reference maximum
+                        float mx = -INFINITY;
+                        for (int g = g_lo; g < g_end; ++g) {
+                            uint32_t sr[32];
+                            umma::tmem_ld32(tS + (uint32_t)(32 * g), sr);
                             umma::tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                            umma::tmem_st32(tO0 + (uint32_t)(128 * st + c0), o);
+                            mx = fmaxf(mx, group_max(sr, masked ? visible(g) : ~0u));
                         }
+                        m_ref = mx;
                     }
-                    // ---- weights, in place of the scores
-                    const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + (FP8 ? kBiasF16 : 0.f);
                     float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                    for (int g = 0; g < ng; ++g) {
-                        uint32_t sr[32];
-                        umma::tmem_ld32(tS + (uint32_t)(32 * g), sr);
-                        umma::tmem_wait_ld();
-                        uint32_t hi[16], lo[16];
+                    // one group: its weights, in place of its scores
+                    auto weigh = [&](const uint32_t (&sr)[32], int g) {
                         const uint32_t vis = masked ? visible(g) : ~0u;
+                        const float gm = group_max(sr, vis);
+                        // the reference moves only when it lags by more than 2^8; what
+                        // was made with the old one is then scaled down in place
+                        const bool move = in && gm > m_ref + kMaxLag;
+                        if (__any_sync(kFull, move)) {
+                            float alpha = 1.f;
+                            if (move) {
+                                alpha = ex2(m_ref - gm);     // 0 while nothing was seen
+                                m_ref = gm;
+                                l *= alpha;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) ls[k] *= alpha;
+                            }
+                            if (!first) {
+#pragma unroll 1
+                                for (int c0 = 0; c0 < D; c0 += 16) {
+                                    uint32_t o[16];
+                                    umma::tmem_ld16(tO0 + (uint32_t)(128 * st + c0), o);
+                                    umma::tmem_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                                    umma::tmem_st16(tO0 + (uint32_t)(128 * st + c0), o);
+                                }
+                            }
+#pragma unroll 1
+                            for (int gg = g_lo; gg < g; ++gg) {
+                                uint32_t h[16];
+                                umma::tmem_ld16(tS + (uint32_t)(32 * gg), h);
+                                umma::tmem_wait_ld();
+                                if (FP8) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const __half2 x = *reinterpret_cast<const __half2*>(&h[e]);
+                                        h[e] = pack_f16x2(__low2float(x) * alpha, __high2float(x) * alpha);
+                                    }
+                                } else {
+                                    // the sum of the parts, scaled and split again
+                                    uint32_t lw[16];
+                                    umma::tmem_ld16(tS + (uint32_t)(32 * gg + 16), lw);
+                                    umma::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const float w0 = (bf16_lo(h[e]) + bf16_lo(lw[e])) * alpha;
+                                        const float w1 = (bf16_hi(h[e]) + bf16_hi(lw[e])) * alpha;
+                                        h[e] = pack_bf16x2(w0, w1);
+                                        lw[e] = pack_bf16x2(w0 - bf16_lo(h[e]), w1 - bf16_hi(h[e]));
+                                    }
+                                    umma::tmem_st16(tS + (uint32_t)(32 * gg + 16), lw);
+                                }
+                                umma::tmem_st16(tS + (uint32_t)(32 * gg), h);
+                            }
+                        }
+                        const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + (FP8 ? kBiasF16 : 0.f);
+                        uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float w0 = ex2(fmaf(__uint_as_float(sr[2 * e]), sl2, nm));
@@ -967,6 +1036,29 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                         umma::tmem_st16(tS + (uint32_t)(32 * g), hi);
                         if (!FP8) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), lo);
+                    };
+                    if (copies > 1) {
+                        // the keys of the other copies weigh nothing here
+                        uint32_t zero[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) zero[k] = 0u;
+                        for (int g = 0; g < ng; ++g)
+                            if (g < g_lo || g >= g_hi) {
+                                umma::tmem_st16(tS + (uint32_t)(32 * g), zero);
+                                if (!FP8) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), zero);
+                            }
+                    }
+                    // a group's scores are loaded while the one before is weighed
+                    uint32_t next[32];
+                    if (g_lo < g_end) umma::tmem_ld32(tS + (uint32_t)(32 * g_lo), next);
+#pragma unroll 1
+                    for (int g = g_lo; g < g_end; ++g) {
+                        umma::tmem_wait_ld();
+                        uint32_t sr[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) sr[k] = next[k];
+                        if (g + 1 < g_end) umma::tmem_ld32(tS + (uint32_t)(32 * (g + 1)), next);
+                        weigh(sr, g);
                     }
                     l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     first = false;
@@ -988,116 +1080,159 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                 m_ref = -INFINITY;
                 l = 0.f;
             }
-            float a0 = 1.f, a1 = 0.f;            // weights of the two accumulators (TILES == 1)
-            if (TILES == 1) {
-                volatile float* ml = reinterpret_cast<volatile float*>(gb + G::kMlOff);
-                ml[(st * kTile + r) * 2] = m_ref;
-                ml[(st * kTile + r) * 2 + 1] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(G::B_ML));
-                ok = wait_warp(bar(G::B_ML), (uint32_t)(seg & 1), misc);
-                if (!ok) break;
-                const float m0 = ml[r * 2], l0 = ml[r * 2 + 1];
-                const float m1 = ml[(kTile + r) * 2], l1 = ml[(kTile + r) * 2 + 1];
-                const float mm = fmaxf(m0, m1);
-                a0 = m0 == -INFINITY ? 0.f : ex2(m0 - mm);
-                a1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
-                m_ref = mm;
-                l = l0 * a0 + l1 * a1;
-            }
-            if (warp_live && !idle) {
-                const bool whole = w.j == 0 && w.np == w.q.nb;
-                const int g = r0 + rt - node * p.G;
-                const size_t orow = ((size_t)(w.q.t0 + node) * p.Hq + (size_t)w.h * p.G + (in ? g : 0)) * D;
-                const size_t prow = (((size_t)blockIdx.x * 2 + (w.j == 0 ? 1 : 0)) * (TILES * kTile) + rt);
-                const float inv = l == 0.f ? 0.f : v_scale / l;
-                // drafted V rows that were zeroed for their infinities or NaN
-                uint32_t back[4] = {0u, 0u, 0u, 0u};
-                bool any_back = false;
-                if (w.drafted(nc - 1)) {
+            const bool whole = w.j == 0 && w.np == w.q.nb;
+            // drafted V elements that were zeroed as infinities or NaN: added back for
+            // the rows that see them
+            auto add_back = [&](float* v, int cols, int c0, int of_node) {
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    uint32_t b = 0u;
+                    for (int q = 0; q < G::kPrepWarps; ++q) b |= badw[(buf * G::kPrepWarps + q) * 4 + k4];
+                    for (b &= anc[(buf * kN + of_node) * 4 + k4]; b != 0u; b &= b - 1u) {
+                        const int pos = w.q.base + 32 * k4 + __ffs(b) - 1;
+                        const int blk = __ldg(p.bt + (size_t)w.s * p.max_blocks + pos / kBlock);
+                        if (blk < 0 || blk >= p.num_blocks) continue;
+                        const size_t at = (((size_t)blk * p.Hkv + w.h) * kBlock + pos % kBlock) * D + c0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b = 0u;
-                        for (int q = 0; q < G::kPrepWarps; ++q) b |= badw[(buf * G::kPrepWarps + q) * 4 + k];
-                        back[k] = in && !pad ? b & am[k] : 0u;
-                        any_back = any_back || back[k] != 0u;
-                    }
-                }
-                const int c_lo = TILES == 1 ? st * (D / 2) : 0, c_hi = TILES == 1 ? c_lo + D / 2 : D;
-#pragma unroll 1
-                for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-                    uint32_t o[32];
-                    umma::tmem_ld32(tO0 + (uint32_t)((TILES == 2 ? 128 * st : 0) + c0), o);
-                    umma::tmem_wait_ld();
-                    float v[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
-                    if (TILES == 1) {
-                        if (nc > 1) {            // the second accumulator holds something
-                            umma::tmem_ld32(tO0 + (uint32_t)(128 + c0), o);
-                            umma::tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = v[k] * a0 + __uint_as_float(o[k]) * a1;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] *= a0;
-                        }
-                    }
-                    if (l == 0.f) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
-                    }
-                    if (any_back) {
-#pragma unroll 1
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            for (uint32_t b = k4 == 0 ? back[0] : k4 == 1 ? back[1] : k4 == 2 ? back[2] : back[3];
-                                 b != 0u; b &= b - 1u) {
-                                const int pos = w.q.base + 32 * k4 + __ffs(b) - 1;
-                                const int blk = __ldg(p.bt + (size_t)w.s * p.max_blocks + pos / kBlock);
-                                if (blk < 0 || blk >= p.num_blocks) continue;
-                                const size_t at = (((size_t)blk * p.Hkv + w.h) * kBlock + pos % kBlock) * D + c0;
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    if (FP8) {
-                                        if ((p.v_cache[at + k] & 0x7fu) == 0x7fu) v[k] = __uint_as_float(0x7fffffffu);
-                                    } else {
-                                        const float z = __uint_as_float(
-                                            (uint32_t) reinterpret_cast<const uint16_t*>(p.v_cache)[at + k] << 16);
-                                        if (!(fabsf(z) < INFINITY)) v[k] += z;
-                                    }
-                                }
+                        for (int k = 0; k < kStageCols; ++k) {
+                            if (k >= cols) break;
+                            if (FP8) {
+                                if ((p.v_cache[at + k] & 0x7fu) == 0x7fu) v[k] = __uint_as_float(0x7fffffffu);
+                            } else {
+                                const float z = __uint_as_float(
+                                    (uint32_t) reinterpret_cast<const uint16_t*>(p.v_cache)[at + k] << 16);
+                                if (!(fabsf(z) < INFINITY)) v[k] += z;
                             }
                         }
                     }
-                    if (!in) continue;
-                    if (whole) {
-                        if (p.out_f32) {
-                            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + c0);
+                }
+            };
+            bool back = false;                   // is there any such element?
+            if (w.drafted(nc - 1))
+                for (int q = 0; q < G::kPrepWarps * 4; ++q) back = back || badw[buf * G::kPrepWarps * 4 + q] != 0u;
+            const size_t slot = (size_t)blockIdx.x * 2 + (w.j == 0 ? 1 : 0);
+            // `cols` columns of one row, to the output or to the partials
+            auto put = [&](float* v, auto cols, int c0, int row, float sum) {
+                constexpr int N = decltype(cols)::value;
+                const int nd = row_node(p, r0 + row);
+                if (sum == 0.f) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                dst[k / 4] = make_float4(v[k] * inv, v[k + 1] * inv, v[k + 2] * inv, v[k + 3] * inv);
-                        } else {
-                            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + c0);
+                    for (int k = 0; k < N; ++k) v[k] = 0.f;
+                }
+                if (back && !((padw[buf * 4 + (nd >> 5)] >> (nd & 31)) & 1u)) add_back(v, N, c0, nd);
+                if (!whole) {
+                    float* dst = p.part_o + (slot * (TILES * kTile) + row) * D + c0;
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8)
-                                dst[k / 8] = make_uint4(pack_bf16x2(v[k] * inv, v[k + 1] * inv),
-                                                        pack_bf16x2(v[k + 2] * inv, v[k + 3] * inv),
-                                                        pack_bf16x2(v[k + 4] * inv, v[k + 5] * inv),
-                                                        pack_bf16x2(v[k + 6] * inv, v[k + 7] * inv));
-                        }
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c0);
+                    for (int k = 0; k < N; k += 2) *reinterpret_cast<float2*>(dst + k) = make_float2(v[k], v[k + 1]);
+                    return;
+                }
+                const float inv = sum == 0.f ? 0.f : v_scale / sum;
+                const size_t at = ((size_t)(w.q.t0 + nd) * p.Hq + (size_t)w.h * p.G + (r0 + row - nd * p.G)) * D + c0;
+                if (p.out_f32) {
+                    float* dst = static_cast<float*>(p.out) + at;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    for (int k = 0; k < N; k += 2)
+                        *reinterpret_cast<float2*>(dst + k) = make_float2(v[k] * inv, v[k + 1] * inv);
+                } else {
+                    uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+                    for (int k = 0; k < N; k += 2)
+                        *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2(v[k] * inv, v[k + 1] * inv);
+                }
+            };
+            if (TILES == 1 || (copies > 1 && st == 0)) {
+                // ---- join the partial results of a row: both streams' (TILES == 1),
+                // all copies'
+                float2* ml = reinterpret_cast<float2*>(gb + G::kMlOff);
+                float* stage = reinterpret_cast<float*>(gb + G::kStageOff);
+                ml[tid] = make_float2(m_ref, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(G::B_ML));
+                ok = wait_warp(bar(G::B_ML), (uint32_t)(joins & 1), misc);
+                if (!ok) break;
+                ++joins;
+                constexpr int streams = TILES == 1 ? 2 : 1;
+                const int stride = kTile / copies;
+                // largest maximum and joined sum of row `row`
+                auto joined = [&](int row, float& M) -> float {
+                    M = -INFINITY;
+                    for (int i = 0; i < streams * copies; ++i)
+                        M = fmaxf(M, ml[(i / copies) * kTile + (i % copies) * stride + row].x);
+                    float sum = 0.f;
+                    for (int i = 0; i < streams * copies; ++i) {
+                        const float2 x = ml[(i / copies) * kTile + (i % copies) * stride + row];
+                        sum += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
                     }
+                    return sum;
+                };
+                float M;
+                const float sum = joined(rt, M);
+                const bool mine = nc > 1 || st == 0;     // did this stream have a chunk?
+                const float a = m_ref == -INFINITY || !mine ? 0.f : ex2(m_ref - M);
+                if (in && r == rt && st == 0 && !whole)
+                    p.part_ml[slot * (TILES * kTile) + rt] = make_float2(M, sum);
+                // kStageCols columns at a time through shared memory
+                constexpr int T = G::kJoinWarps * 32;
+                const int per = kStageCols * stride / T;         // columns of a thread: 2 .. 16
+                const int row = tid * per / kStageCols, col = tid * per % kStageCols;
+                float M2;
+                const float sum2 = row < rows ? joined(row, M2) : 0.f;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += kStageCols) {
+                    if (warp_live) {
+                        uint32_t o[16];
+                        umma::tmem_ld16(tO0 + (uint32_t)(128 * st + c0), o);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            stage[tid * kStageRow + k] = a == 0.f ? 0.f : __uint_as_float(o[k]) * a;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(G::B_STAGE));
+                    ok = wait_warp(bar(G::B_STAGE), (uint32_t)(stages & 1), misc);
+                    if (!ok) break;
+                    ++stages;
+                    if (row < rows) {
+                        float v[kStageCols];
+                        auto add = [&](auto cols) {
+                            constexpr int N = decltype(cols)::value;
+#pragma unroll
+                            for (int k = 0; k < N; ++k) v[k] = 0.f;
+                            for (int i = 0; i < streams * copies; ++i) {
+                                const float* src = stage + ((i / copies) * kTile + (i % copies) * stride + row) * kStageRow + col;
+#pragma unroll
+                                for (int k = 0; k < N; ++k) v[k] += src[k];
+                            }
+                            put(v, cols, c0 + col, row, sum2);
+                        };
+                        if (per == 2) add(std::integral_constant<int, 2>());
+                        else if (per == 4) add(std::integral_constant<int, 4>());
+                        else add(std::integral_constant<int, 8>());
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(G::B_STAGE));
+                    ok = wait_warp(bar(G::B_STAGE), (uint32_t)(stages & 1), misc);
+                    if (!ok) break;
+                    ++stages;
                 }
-                if (in && !whole && (TILES == 2 || st == 0)) p.part_ml[prow] = make_float2(m_ref, l);
-                if (tid == 0 && w.j == 0 && !whole) {
-                    // the CTA with the first pages says where the partials are
-                    const int last = (int)(((long long)flat + w.q.nb - 1) / misc[M_Q]);
-                    p.meta[blockIdx.x] = make_int4(w.s, w.h, last - cta + 1, min(rows, TILES * kTile));
+                if (!ok) break;
+            } else if (warp_live && !idle) {
+                // ---- a row per thread, its whole result in one accumulator
+                if (in && !whole) p.part_ml[slot * (TILES * kTile) + rt] = make_float2(m_ref, l);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                    uint32_t o[16];
+                    umma::tmem_ld16(tO0 + (uint32_t)(128 * st + c0), o);
+                    umma::tmem_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]);
+                    if (in) put(v, std::integral_constant<int, 16>(), c0, rt, l);
                 }
+            }
+            if (tid == 0 && w.j == 0 && !whole) {
+                // the CTA with the first pages says where the partials are
+                const int last = (int)(((long long)flat + w.q.nb - 1) / misc[M_Q]);
+                p.meta[blockIdx.x] = make_int4(w.s, w.h, last - cta + 1, min(rows, TILES * kTile));
             }
             flat += w.np;
             umma::fence_before_sync();
