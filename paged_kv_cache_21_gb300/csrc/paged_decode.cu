@@ -71,6 +71,7 @@
 #include "device_common.cuh"
 #include "internal.h"
 #include "paged_kv.h"
+#include "tree_launch.h"
 #include "wide.h"
 
 namespace pkv {
@@ -2225,7 +2226,8 @@ extern "C" int kv_get_device_error(int* flags, int64_t* detail)
 {
     int (*const words[])(unsigned*, long long*) = {append_read_error, decode_read_error,
                                                    wide_read_error, tree_read_error,
-                                                   verify_read_error, compact_read_error};
+                                                   tree_small_read_error, verify_read_error,
+                                                   compact_read_error};
     unsigned all = 0;
     long long first = -1;
     for (auto read : words) {

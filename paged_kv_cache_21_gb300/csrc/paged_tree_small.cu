@@ -1,0 +1,724 @@
+// paged_tree_attention for sequences of at most 64 query rows per KV head (nodes
+// times heads per KV head): small trees, and single tokens.
+//
+// The mathematics is paged_tree.cu's; the products are the other way round.  A
+// tcgen05.mma of M = 128 takes ~64 clocks whatever its N up to 128 (measured),
+// so with the queries as M, 32 rows would cost what 128 do.  Here the 128 keys of
+// a chunk, and then the head's dimensions, are M, and the rows are N:
+//     S^T = K Q^T   (128 keys x N rows, K as it lies in the ring),
+//     O^T += V^T P^T   (head_dim x N, V as it lies in the ring, P through shared
+//                       memory; its high and low parts are N columns each of ONE
+//                       product, added at the end: the low part costs nothing).
+// 16 products, ~1030 clocks, for 128 keys, whose bf16 K and V take ~2450 clocks
+// to arrive at 6.8 TB/s over 152 SMs (E4M3: ~1220): HBM is the bound.
+//
+// How (the rest as in paged_tree.cu):
+//  * One thread per key of a chunk weighs that key for every row, so the
+//    exponentials of few rows use all lanes.  Two groups of four warps take the
+//    chunks in turn, each with its own accumulator O^T (columns 4 N + w PW of
+//    tensor memory) and references; the score products run up to three chunks
+//    ahead (four S^T buffers).
+//  * The reference maximum of a row moves only when a score is more than 2^8
+//    above it (the four warps agree on that once per chunk, through an mbarrier);
+//    the first chunk of a segment sets it.  Then, seldom, the columns of O^T and
+//    the sums are scaled.
+//  * D < 128: the lower lanes of O^T hold the result, the upper ones products of
+//    whatever follows V in shared memory, never read.
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "cache_map.h"
+#include "internal.h"
+#include "tree_kernel.cuh"
+
+namespace pkv {
+
+namespace {
+
+template <int D, bool FP8, int N>
+struct SmallGeo {
+    static constexpr int kD = D;
+    static constexpr bool kFp8 = FP8;
+    static constexpr int kPrepWarp = 10;                     // first of the prep / widening warps
+    static constexpr int kPrepWarps = FP8 ? 4 : 1;
+    static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kSlot = kBoxes * kRegion;           // K or V of a chunk, 2 bytes each
+    static constexpr int kPageBytes = kBlock * D * (FP8 ? 1 : 2);
+    static constexpr int kRawSlot = kPages * kBlock * D;     // E4M3 codes of K or V of a chunk
+    // columns of P and of an accumulator: the high parts of the rows' weights,
+    // then the low parts.  64 rows of an E4M3 cache go without: f16's 11 bits
+    // against the cache's 4, and the room goes to the rings.
+    static constexpr bool kLow = !(FP8 && N == 64);
+    static constexpr int kPW = kLow ? 2 * N : N;
+    static constexpr int kPBuf = kPW / 64 * kRegion;         // [column group of 64][128 keys][128 B]
+    static constexpr int kQBytes = kBoxes * N * 128;
+    static constexpr int kSlots = (FP8 ? 3 : N == 32 ? 5 : 4) * (128 / D);
+    static constexpr int kRawSlots = !FP8 ? 0 : 4 * (128 / D);
+    static constexpr int kLoadSlots = FP8 ? kRawSlots : kSlots;
+    static constexpr int kQOff = 0;
+    static constexpr int kSlotOff = (kQOff + kQBytes + 1023) / 1024 * 1024;
+    static constexpr int kPOff = kSlotOff + kSlots * kSlot;  // two buffers (behind the ring: see D < 128)
+    static constexpr int kRawOff = kPOff + 2 * kPBuf;
+    static constexpr int kBarOff = kRawOff + kRawSlots * kRawSlot;
+    // barriers
+    static constexpr int B_FULL = 0;                         // + load slot: the copies have landed
+    static constexpr int B_EMPTY = B_FULL + kLoadSlots;      // + load slot: it may be refilled
+    static constexpr int B_WIDE = B_EMPTY + kLoadSlots;      // + slot: widened (FP8)
+    static constexpr int B_WFREE = B_WIDE + (FP8 ? kSlots : 0);  // + slot: the MMAs have read it
+    static constexpr int B_FIX = B_WFREE + (FP8 ? kSlots : 0);   // + slot: V rows fixed (bf16)
+    static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kSlots);   // Q and the tree of a segment
+    static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
+    static constexpr int B_SFULL = B_QFREE + 1;              // + buffer (4): scores
+    static constexpr int B_PFULL = B_SFULL + 4;              // + group: weights written
+    static constexpr int B_PVDONE = B_PFULL + 2;             // + group: their products are done
+    static constexpr int B_VOTE = B_PVDONE + 2;              // + group: its four warps agree
+    static constexpr int B_OFULL = B_VOTE + 2;               // both accumulators are complete
+    static constexpr int B_OFREE = B_OFULL + 1;              // + segment & 1: they have been read
+    static constexpr int B_JOIN = B_OFREE + 2;               // the eight warps meet
+    static constexpr int B_END = B_JOIN + 1;                 // all MMAs are done
+    static constexpr int B_STALL = B_END + 1;                // nothing arrives (the test hook)
+    static constexpr int kNumBars = B_STALL + 1;
+    static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kAncOff = kMiscOff + 64;            // [2][kN][4] words
+    static constexpr int kPtrOff = kAncOff + 2 * kN * 16;    // [kN] words
+    static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
+    static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
+    static constexpr int kQfacOff = kBadOff + 2 * kPrepWarps * 16;   // [2][N] floats (FP8)
+    static constexpr int kSnOff = kQfacOff + 2 * N * 4;      // [group][N] float2: (scale, -reference)
+    static constexpr int kRefOff = kSnOff + 2 * N * 8;       // [group][N] floats: the reference
+    static constexpr int kAlphaOff = kRefOff + 2 * N * 4;    // [group][N] floats
+    static constexpr int kWmaxOff = kAlphaOff + 2 * N * 4;   // [group][4][N] floats: maxima, later sums
+    static constexpr int kFacOff = kWmaxOff + 8 * N * 4;     // [N] float4
+    static constexpr int kVoteOff = kFacOff + N * 16;        // [group][4] words, then [group][2]
+    static constexpr int kEnd = kVoteOff + 64;
+    static constexpr int kSmem = kEnd + 1024;
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+    // tensor memory: S^T buffers, then the accumulators
+    static constexpr uint32_t kColO = 4 * N;
+    static constexpr uint32_t kTmemCols = 4 * N + 2 * kPW <= 256 ? 256 : 512;
+};
+
+// Order-preserving map of floats to ints (NaN aside).
+__device__ __forceinline__ int ordered(float x)
+{
+    const int b = __float_as_int(x);
+    return b >= 0 ? b : b ^ 0x7fffffff;
+}
+
+__device__ __forceinline__ float unordered(int b)
+{
+    return __int_as_float(b >= 0 ? b : b ^ 0x7fffffff);
+}
+
+// Sums over the warp of 32 values a lane: lane l gets the sum of v[l].
+__device__ __forceinline__ float column_sums(float (&v)[32], int lane)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < o; ++k) {
+            const float keep = up ? v[k + o] : v[k], send = up ? v[k] : v[k + o];
+            v[k] = keep + __shfl_xor_sync(kFull, send, o);
+        }
+    }
+    return v[0];
+}
+
+template <int D, bool FP8, int N>
+__global__ void __launch_bounds__(SmallGeo<D, FP8, N>::kThreads, 1)
+paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const TreeParams p)
+{
+    using G = SmallGeo<D, FP8, N>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t sraw = smem_u32(smem_raw);
+    const uint32_t sb = (sraw + 1023u) & ~1023u;
+    uint8_t* gb = smem_raw + (sb - sraw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    volatile int* misc = reinterpret_cast<volatile int*>(gb + G::kMiscOff);
+    auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
+
+    if (tid == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        for (int i = 0; i < G::kLoadSlots; ++i) {
+            mbar_init(bar(G::B_FULL + i), 1);
+            mbar_init(bar(G::B_EMPTY + i), FP8 ? G::kPrepWarps : 1);
+        }
+        for (int i = 0; i < G::kSlots; ++i) {
+            if (FP8) {
+                mbar_init(bar(G::B_WIDE + i), G::kPrepWarps);
+                mbar_init(bar(G::B_WFREE + i), 1);
+            } else {
+                mbar_init(bar(G::B_FIX + i), 1);
+            }
+        }
+        mbar_init(bar(G::B_QFULL), G::kPrepWarps);
+        mbar_init(bar(G::B_QFREE), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(G::B_SFULL + i), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(bar(G::B_PFULL + w), 4);
+            mbar_init(bar(G::B_PVDONE + w), 1);
+            mbar_init(bar(G::B_VOTE + w), 4);
+            mbar_init(bar(G::B_OFREE + w), 8);
+        }
+        mbar_init(bar(G::B_OFULL), 1);
+        mbar_init(bar(G::B_JOIN), 8);
+        mbar_init(bar(G::B_END), 1);
+        mbar_init(bar(G::B_STALL), 1);
+        misc[M_ABORT] = 0;
+        misc[M_ISSUED] = 0;
+        fence_mbar_init();
+    }
+    if (tid < 16) reinterpret_cast<volatile int*>(gb + G::kVoteOff)[tid] = 0;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == 9) {
+        umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, G::kTmemCols);
+        umma::tmem_relinquish();
+    }
+    if (warp == 8) cut_work(p, misc, 0, cta, p.tidy && cta == 0, lane);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = (uint32_t)misc[M_TMEM];
+
+    if (warp == 8) {
+        copy_role<G>(p, tm_k, tm_v, sb, misc, 0, lane);
+    } else if (warp == 9) {
+        // --------------------------------------------------------------- MMAs
+        if (lane == 0) {
+            const uint64_t qdesc = umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
+            const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kSlotOff, 16, 1024);
+            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kSlotOff, kRegion, 1024);
+            const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, kRegion, 1024);
+            constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, N, false, false)
+                                             : umma::idesc_bf16_f32(128, N, false, false);
+            constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(128, G::kPW, true, true)
+                                              : umma::idesc_bf16_f32(128, G::kPW, true, true);
+            constexpr int full0 = FP8 ? G::B_WIDE : G::B_FULL, free0 = FP8 ? G::B_WFREE : G::B_EMPTY;
+            uint32_t fix_parity = 0;             // bit slot: parity of its next fix
+            int g0 = 0;                          // first chunk of the segment
+            bool ok = true;
+            if (p.test_stall > 0 && misc[M_CNT] > 0 &&
+                !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
+                misc[M_ABORT] = 1;
+                raise_flag(&g_tree_err, KV_DEVERR_PIPELINE_TIMEOUT, blockIdx.x);
+                ok = false;
+            }
+            for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
+                const int nc = w.chunks(), seg = w.seg;
+                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc);
+                if (!ok) break;
+                int sc = 0;                      // next chunk to issue S^T of
+                // S^T of the chunks up to c, and of up to three more whose keys are
+                // there: buffer g & 3 was read for chunk g - 4, whose weights have
+                // been waited for when chunk c >= g - 3 comes
+                auto scores_up_to = [&](int c) -> bool {
+                    for (; sc <= c + 3 && sc < nc; ++sc) {
+                        const int g = g0 + sc, x = 2 * g, ks = x % G::kSlots;
+                        const uint32_t parity = (uint32_t)((x / G::kSlots) & 1);
+                        if (sc > c) {
+                            if (misc[M_ISSUED] <= x || !mbar_test(bar(full0 + ks), parity)) break;
+                        } else if (!(wait_issued(x, misc) && wait_bar(bar(full0 + ks), parity, misc))) {
+                            return false;
+                        }
+                        umma::fence_after_sync();
+                        const uint64_t kd = kdesc + (uint64_t)((ks * G::kSlot) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma::mma_bf16_ss(tmem + (uint32_t)(N * (g & 3)),
+                                              kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4),
+                                              qdesc + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
+                                              idesc_s, kk > 0);
+                        umma::commit(bar(G::B_SFULL + (g & 3)));
+                        umma::commit(bar(free0 + ks));
+                        if (sc + 1 == nc) umma::commit(bar(G::B_QFREE));
+                    }
+                    return true;
+                };
+                for (int c = 0; ok && c < nc; ++c) {
+                    const int g = g0 + c, x = 2 * g + 1, vs = x % G::kSlots, grp = g & 1;
+                    ok = scores_up_to(c) && wait_bar(bar(G::B_PFULL + grp), (uint32_t)((g >> 1) & 1), misc) &&
+                         wait_issued(x, misc) &&
+                         wait_bar(bar(full0 + vs), (uint32_t)((x / G::kSlots) & 1), misc);
+                    if (ok && !FP8 && w.drafted(c)) {
+                        ok = wait_bar(bar(G::B_FIX + vs), (fix_parity >> vs) & 1u, misc);
+                        fix_parity ^= 1u << vs;
+                    }
+                    // the accumulators of the segment before have been read
+                    if (ok && c < 2 && seg > 0)
+                        ok = wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
+                    const uint64_t pd = pdesc + (uint64_t)((grp * G::kPBuf) >> 4);
+                    const int np = w.chunk_pages(c);
+                    for (int kk = 0; kk < np; ++kk)
+                        umma::mma_bf16_ss(tmem + G::kColO + (uint32_t)(grp * G::kPW),
+                                          vd + (uint64_t)((kk * kBlock * 128) >> 4),
+                                          pd + (uint64_t)((kk * kBlock * 128) >> 4), idesc_pv, !(c < 2 && kk == 0));
+                    umma::commit(bar(free0 + vs));
+                    umma::commit(bar(G::B_PVDONE + grp));
+                    if (c + 1 == nc) umma::commit(bar(G::B_OFULL));
+                }
+                g0 += nc;
+            }
+            // every MMA issued by this thread is complete before the CTA ends
+            umma::commit(bar(G::B_END));
+            mbar_wait_bounded(bar(G::B_END), 0u, kWaitLimit);
+        }
+        __syncwarp();
+    } else if (warp >= G::kPrepWarp) {
+        // ------------------------- queries, trees, V rows, and widening (E4M3)
+        const int pw = warp - G::kPrepWarp;
+        int x0 = 0;
+        bool ok = true;
+        for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
+            const int seg = w.seg, buf = seg & 1;
+            // the segment's entry of the tree tables was last read two segments ago
+            if (seg >= 2) ok = wait_warp(bar(G::B_OFREE + buf), (uint32_t)(((seg - 2) >> 1) & 1), misc);
+            if (ok && seg >= 1) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((seg - 1) & 1), misc);
+            if (!ok) break;
+            volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(gb + G::kBadOff);
+            if (lane < 4) badw[(buf * G::kPrepWarps + pw) * 4 + lane] = 0u;
+            const int rows = w.q.n * p.G;        // <= N
+            constexpr int C = D / 8, RI = 32 / C;    // 16-byte chunks of a row, rows of an instruction
+            const int c = lane % C;
+            for (int rb = pw * RI; rb < rows; rb += G::kPrepWarps * RI) {
+                const int r = rb + lane / C, rc = min(r, rows - 1);
+                const int node = row_node(p, rc), gq = rc - node * p.G;
+                const uint16_t* src =
+                    p.q + ((size_t)(w.q.t0 + node) * p.Hq + (size_t)w.h * p.G + gq) * D + 8 * c;
+                const uint32_t dst = sb + (uint32_t)(G::kQOff + (c >> 3) * N * 128) + region_off(rc, c & 7);
+                if (!FP8) {
+                    if (r < rows) cp_async16(dst, src);
+                } else {
+                    float up;
+                    const uint4 h = query_f16<D>(__ldg(reinterpret_cast<const uint4*>(src)), up);
+                    if (r < rows) {
+                        sts128(dst, h);
+                        if (c == 0) reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + r] = up;
+                    }
+                }
+            }
+            if (pw == 0) tree_masks<G>(p, w, gb, lane);
+            if (!FP8) cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(G::B_QFULL));
+            if constexpr (FP8)
+                ok = widen<G>(p, w, sb, gb, misc, x0, pw, lane);
+            else
+                ok = fix_values<G>(p, w, sb, gb, misc, x0, lane);
+            x0 += 2 * w.chunks();
+        }
+        if (!FP8) cp_async_wait_all();
+    } else {
+        // ------------------------------------------------- weights and output
+        const int grp = warp >> 2, key = tid & 127, wq = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t tO = lanes + G::kColO + (uint32_t)(grp * G::kPW);
+        float2* sn = reinterpret_cast<float2*>(gb + G::kSnOff) + grp * N;
+        float* ref = reinterpret_cast<float*>(gb + G::kRefOff) + grp * N;
+        float* alphas = reinterpret_cast<float*>(gb + G::kAlphaOff) + grp * N;
+        float* wmax = reinterpret_cast<float*>(gb + G::kWmaxOff) + grp * 4 * N;
+        volatile int* vote = reinterpret_cast<volatile int*>(gb + G::kVoteOff) + grp * 4;
+        volatile int* unset = reinterpret_cast<volatile int*>(gb + G::kVoteOff) + 8 + grp * 2;
+        const uint32_t pb = sb + (uint32_t)(G::kPOff + grp * G::kPBuf + key * 128);
+        if (p.tidy) zero_empty(p, D, cta, p.nctas, tid, 256);
+        if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
+        int votes = 0, joins = 0, g0 = 0, flat = misc[M_B0];
+        bool ok = true;
+        // the group's four warps meet
+        auto meet = [&]() -> bool {
+            // (the word of the vote after next: its last readers have all met since)
+            if (wq == 0 && lane == 0) vote[(votes + 2) & 3] = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(G::B_VOTE + grp));
+            const bool r = wait_warp(bar(G::B_VOTE + grp), (uint32_t)(votes & 1), misc);
+            ++votes;
+            return r;
+        };
+        auto join = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(G::B_JOIN));
+            const bool r = wait_warp(bar(G::B_JOIN), (uint32_t)(joins & 1), misc);
+            ++joins;
+            return r;
+        };
+        for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
+            const int seg = w.seg, buf = seg & 1, nc = w.chunks();
+            const int rows = w.q.n * p.G;
+            const uint32_t* anc = reinterpret_cast<const uint32_t*>(gb + G::kAncOff) + buf * kN * 4;
+            const volatile uint32_t* padw = reinterpret_cast<const volatile uint32_t*>(gb + G::kPadOff) + buf * 4;
+            // sums: of up to 32 rows in a register each, of 64 rows in lanes (column_sums)
+            constexpr int kSums = N == 32 ? 32 : 2;
+            float l[kSums];
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) l[k] = 0.f;
+            bool first = true;
+            for (int c = (g0 ^ grp) & 1; c < nc; c += 2) {
+                const int g = g0 + c;
+                ok = wait_warp(bar(G::B_SFULL + (g & 3)), (uint32_t)((g >> 2) & 1), misc);
+                if (!ok) break;
+                if (first) {
+                    // the rows' scale and reference: none yet for rows that see
+                    // something, and never a weight for the others
+                    if (key < N) {
+                        const int nd = key < rows ? row_node(p, key) : 0;
+                        const bool live = key < rows && !((padw[nd >> 5] >> (nd & 31)) & 1u);
+                        const float f = FP8 && live ? reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + key] : 1.f;
+                        sn[key] = live ? make_float2(p.sl2 * f, 0.f) : make_float2(0.f, -INFINITY);
+                        ref[key] = -INFINITY;
+                        const bool any = __any_sync(kFull, live);
+                        if (lane == 0) unset[wq] = any;
+                    }
+                    if (N == 32 && key == 32) unset[1] = 0;
+                    ok = meet();
+                    if (!ok) break;
+                }
+                umma::fence_after_sync();
+                const uint32_t tS = lanes + (uint32_t)(N * (g & 3));
+                const int np = w.chunk_pages(c), pos = (w.j + c * kPages) * kBlock + key;
+                // the rows that see this key, as bits
+                uint32_t vis[N / 32];
+#pragma unroll
+                for (int q = 0; q < N / 32; ++q) vis[q] = key < np * kBlock && pos < w.q.L ? ~0u : 0u;
+                if (w.drafted(c) && pos >= w.q.base && vis[0]) {
+                    const int a = pos - w.q.base;
+#pragma unroll
+                    for (int q = 0; q < N / 32; ++q) {
+                        uint32_t v = 0u;
+                        for (int r = 32 * q; r < min(rows, 32 * q + 32); ++r)
+                            v |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - 32 * q);
+                        vis[q] = v;
+                    }
+                }
+                const bool masked = w.drafted(c) || np < kPages;     // (for the whole chunk)
+                float t[N];
+                // the scores relative to the references, in log2 units
+                auto load = [&](bool again) -> float {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int q = 0; q < N / 32; ++q)
+                        umma::tmem_ld32(tS + (uint32_t)(32 * q), *reinterpret_cast<uint32_t(*)[32]>(&t[32 * q]));
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < N; k += 2) {
+                        const float4 f = *reinterpret_cast<const float4*>(sn + k);   // two rows
+                        t[k] = fmaf(t[k], f.x, f.y);
+                        t[k + 1] = fmaf(t[k + 1], f.z, f.w);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < N; ++k) t[k] = (vis[k / 32] >> (k & 31)) & 1u ? t[k] : -INFINITY;
+                    }
+                    if (!again) {
+#pragma unroll
+                        for (int k = 0; k < N; ++k) mx[k & 3] = fmaxf(mx[k & 3], t[k]);
+                    }
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                };
+                const float mx = load(false);
+                // does any row's reference lag too far behind?
+                {
+                    const int slot = votes & 3;
+                    const bool any = __any_sync(kFull, mx > kMaxLag + (FP8 ? kBiasF16 : 0.f));
+                    if (any && lane == 0) vote[slot] = 1;
+                    ok = meet();
+                    if (!ok) break;
+                    const bool need = vote[slot] != 0 || unset[0] != 0 || unset[1] != 0;
+                    if (need) {
+                        // ---- new references: the largest score of each row in the chunk
+#pragma unroll
+                        for (int q = 0; q < N / 32; ++q) {
+                            int best = INT32_MIN;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int r = 32 * q + k;
+                                // (relative to the old reference, or to none)
+                                const int m = __reduce_max_sync(kFull, ordered(t[r]));
+                                if (lane == k) best = m;
+                            }
+                            wmax[wq * N + 32 * q + lane] = unordered(best);
+                        }
+                        ok = meet();
+                        if (!ok) break;
+                        if (key < N) {
+                            const float rel = fmaxf(fmaxf(wmax[key], wmax[N + key]), fmaxf(wmax[2 * N + key], wmax[3 * N + key]));
+                            const float2 f = sn[key];
+                            const float old = ref[key];
+                            const bool live = f.y != -INFINITY;
+                            // rel = score * scale + f.y, with f.y = bias - reference, or 0 for none
+                            const float best = old == -INFINITY ? rel : rel - f.y;
+                            float a = 1.f;
+                            if (live && (old == -INFINITY ? best > -INFINITY : best > old + kMaxLag)) {
+                                a = old == -INFINITY ? 0.f : ex2(old - best);
+                                ref[key] = best;
+                                sn[key].y = (FP8 ? kBiasF16 : 0.f) - best;
+                            }
+                            alphas[key] = a;
+                            const bool left = __any_sync(kFull, live && ref[key] == -INFINITY);
+                            if (lane == 0) unset[wq] = left;
+                        }
+                        ok = meet();
+                        if (!ok) break;
+                        if (!first) {
+                            // what has been accumulated follows, once the products of the
+                            // group's chunk before are done
+#pragma unroll
+                            for (int k = 0; k < kSums; ++k) l[k] *= alphas[N == 32 ? k : 32 * k + lane];
+                            ok = wait_warp(bar(G::B_PVDONE + grp), (uint32_t)(((g >> 1) - 1) & 1), misc);
+                            if (!ok) break;
+                            umma::fence_after_sync();
+#pragma unroll 1
+                            for (int c0 = 0; c0 < G::kPW; c0 += 16) {
+                                uint32_t o[16];
+                                umma::tmem_ld16(tO + (uint32_t)c0, o);
+                                umma::tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * alphas[(c0 + k) % N]);
+                                umma::tmem_st16(tO + (uint32_t)c0, o);
+                            }
+                            umma::tmem_wait_st();
+                        }
+                        load(true);
+                    }
+                }
+                // ---- the weights
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    t[k] = ex2(t[k]);
+                    if (N == 32) l[k] += t[k];
+                }
+                if (g >= 2) {
+                    // the group's buffer: the products of its chunk before are done
+                    ok = wait_warp(bar(G::B_PVDONE + grp), (uint32_t)(((g >> 1) - 1) & 1), misc);
+                    if (!ok) break;
+                }
+                first = false;
+                if (key < np * kBlock) {
+#pragma unroll
+                    for (int k = 0; k < N; k += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = t[k + 2 * e], b = t[k + 2 * e + 1];
+                            if (FP8) {
+                                hi[e] = pack_f16x2(a, b);
+                                const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
+                                lo[e] = pack_f16x2(a - __low2float(h), b - __high2float(h));
+                            } else {
+                                hi[e] = pack_bf16x2(a, b);
+                                lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
+                            }
+                        }
+                        // 16 bytes: rows k .. k + 7; the low parts N columns on
+                        const int ch = k / 8, cl = (k + N) / 8;
+                        sts128(pb + (uint32_t)((ch >> 3) * kRegion + ((ch ^ key) & 7) * 16),
+                               make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        if (G::kLow)
+                            sts128(pb + (uint32_t)((cl >> 3) * kRegion + ((cl ^ key) & 7) * 16),
+                                   make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    }
+                }
+                fence_proxy_async_smem();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(G::B_PFULL + grp));
+                if constexpr (N == 64) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = t[32 * q + k];
+                        l[q] += column_sums(v, lane);
+                    }
+                }
+            }
+            if (!ok) break;
+            // ---- the segment's result: join the two groups' sums and accumulators
+            ok = wait_warp(bar(G::B_OFULL), (uint32_t)(seg & 1), misc);
+            if (!ok) break;
+            umma::fence_after_sync();
+            if constexpr (N == 32) {
+                wmax[wq * N + lane] = column_sums(*reinterpret_cast<float(*)[32]>(&l[0]), lane);
+            } else {
+                wmax[wq * N + lane] = l[0];
+                wmax[wq * N + 32 + lane] = l[1];
+            }
+            if (first && key < N) ref[key] = -INFINITY;      // no chunk of this group
+            ok = join();
+            if (!ok) break;
+            const bool whole = w.whole();
+            const size_t slot = (size_t)cta * 2 + (w.j == 0 ? 1 : 0);
+            float4* fac = reinterpret_cast<float4*>(gb + G::kFacOff);
+            if (tid < N) {
+                const float* base = reinterpret_cast<const float*>(gb + G::kWmaxOff);
+                const float* refs = reinterpret_cast<const float*>(gb + G::kRefOff);
+                float s[2], m[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float* b = base + q * 4 * N + tid;
+                    s[q] = (b[0] + b[N]) + (b[2 * N] + b[3 * N]);
+                    m[q] = refs[q * N + tid];
+                    if (m[q] == -INFINITY) s[q] = 0.f;
+                }
+                const float M = fmaxf(m[0], m[1]);
+                const float a0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - M);
+                const float a1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - M);
+                const float L = s[0] * a0 + s[1] * a1;
+                fac[tid] = make_float4(a0, a1, L == 0.f ? 0.f : p.v_scale / L, L);
+                if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
+            }
+            ok = join();
+            if (!ok) break;
+            // drafted V elements that were zeroed as infinities or NaN
+            const volatile uint32_t* badw = reinterpret_cast<const volatile uint32_t*>(gb + G::kBadOff) + buf * G::kPrepWarps * 4;
+            bool back = false;
+            if (w.drafted(nc - 1))
+                for (int q = 0; q < G::kPrepWarps * 4; ++q) back = back || badw[q] != 0u;
+            // a thread per dimension (the lower D lanes), half of the rows a group
+            if (wq * 32 < D) {
+                const int d = key;
+#pragma unroll 1
+                for (int r0 = grp * (N / 2); r0 < min((grp + 1) * (N / 2), rows); r0 += 16) {
+                    float v[16];
+                    uint32_t o[16];
+                    const uint32_t t0 = lanes + G::kColO + (uint32_t)r0;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int part = 0; part < (G::kLow ? 2 : 1); ++part) {
+                            umma::tmem_ld16(t0 + (uint32_t)(q * G::kPW + part * N), o);
+                            umma::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float a = q == 0 ? fac[r0 + k].x : fac[r0 + k].y;
+                                if (a != 0.f) v[k] += __uint_as_float(o[k]) * a;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int r = r0 + k;
+                        if (r >= rows) continue;
+                        const int nd = row_node(p, r);
+                        const float4 f = fac[r];
+                        float x = f.w == 0.f ? 0.f : v[k];
+                        if (back && !((padw[nd >> 5] >> (nd & 31)) & 1u)) {
+                            for (int k4 = 0; k4 < 4; ++k4) {
+                                uint32_t b = 0u;
+                                for (int q = 0; q < G::kPrepWarps; ++q) b |= badw[q * 4 + k4];
+                                for (b &= anc[nd * 4 + k4]; b != 0u; b &= b - 1u) {
+                                    const int pos = w.q.base + 32 * k4 + __ffs(b) - 1;
+                                    const int blk = __ldg(p.bt + (size_t)w.s * p.max_blocks + pos / kBlock);
+                                    if (blk < 0 || blk >= p.num_blocks) continue;
+                                    const size_t at = (((size_t)blk * p.Hkv + w.h) * kBlock + pos % kBlock) * D + d;
+                                    if (FP8) {
+                                        if ((p.v_cache[at] & 0x7fu) == 0x7fu) x = __uint_as_float(0x7fffffffu);
+                                    } else {
+                                        const float z = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.v_cache)[at] << 16);
+                                        if (!(fabsf(z) < INFINITY)) x += z;
+                                    }
+                                }
+                            }
+                        }
+                        if (!whole) {
+                            p.part_o[(slot * N + r) * D + d] = x;
+                            continue;
+                        }
+                        const size_t at = ((size_t)(w.q.t0 + nd) * p.Hq + (size_t)w.h * p.G + (r - nd * p.G)) * D + d;
+                        x *= f.z;
+                        if (p.out_f32) static_cast<float*>(p.out)[at] = x;
+                        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+                    }
+                }
+            }
+            if (tid == 0 && w.j == 0 && !whole) {
+                // the CTA with the first pages says where the partials are
+                const int last = (int)(((long long)flat + w.q.nb - 1) / misc[M_Q]);
+                p.meta[cta] = make_int4(w.s, w.h, last - cta + 1, rows);
+            }
+            flat += w.np;
+            g0 += nc;
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(G::B_OFREE + buf));
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc(tmem, G::kTmemCols);
+    }
+}
+
+std::mutex g_small_mu;
+
+template <int D, bool FP8, int N>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t st)
+{
+    using G = SmallGeo<D, FP8, N>;
+    static bool ready[64] = {};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(g_small_mu);
+        if (!ready[dev]) {
+            if (cudaError_t e = cudaFuncSetAttribute(paged_tree_small_kernel<D, FP8, N>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem))
+                return e;
+            ready[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.nctas);
+    cfg.blockDim = dim3(G::kThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_tree_small_kernel<D, FP8, N>, mk, mv, p);
+}
+
+}  // namespace
+
+int tree_small_rows(int rows) { return rows <= 32 ? 32 : 64; }
+
+cudaError_t tree_small_launch(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, int D,
+                              bool fp8, int rows, cudaStream_t st)
+{
+    const bool n32 = tree_small_rows(rows) == 32;
+    if (D == 128) {
+        if (fp8) return n32 ? launch<128, true, 32>(mk, mv, p, st) : launch<128, true, 64>(mk, mv, p, st);
+        return n32 ? launch<128, false, 32>(mk, mv, p, st) : launch<128, false, 64>(mk, mv, p, st);
+    }
+    if (fp8) return n32 ? launch<64, true, 32>(mk, mv, p, st) : launch<64, true, 64>(mk, mv, p, st);
+    return n32 ? launch<64, false, 32>(mk, mv, p, st) : launch<64, false, 64>(mk, mv, p, st);
+}
+
+int tree_small_read_error(unsigned* flags, long long* detail)
+{
+    DevErr e;
+    if (cudaMemcpyFromSymbol(&e, g_tree_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
+    DevErr z = {0u, -1LL};
+    if (cudaMemcpyToSymbol(g_tree_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
+    *flags = e.flags;
+    *detail = e.flags ? e.detail : -1;
+    return KV_OK;
+}
+
+}  // namespace pkv

@@ -1,0 +1,591 @@
+// What the kernels of paged_tree_attention share (paged_tree.cu, for trees of
+// many query rows, and paged_tree_small.cu, for few): parameters, the cut of the
+// work over CTAs, and the roles that bring queries, trees, keys and values into
+// shared memory.
+//
+// A kernel's geometry G names its shared memory (offsets k..Off from a
+// 1024-byte aligned base) and its barriers (B_..); both kernels consume K and V
+// in chunks of up to 8 pages, in "halves": half 2 c is the K, half 2 c + 1 the V
+// of the CTA's chunk c, in slot x % slots of a ring.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "paged_kv.h"
+#include "tree_common.cuh"
+#include "tree_launch.h"
+#include "umma.cuh"
+
+namespace pkv {
+
+static __device__ DevErr g_tree_err;            // one per translation unit
+
+namespace {
+
+constexpr int kPages = 8;                       // pages of a chunk
+constexpr int kKeys = kPages * kBlock;
+constexpr int kN = KV_TREE_MAX_NODES;
+constexpr int kRegion = kKeys * 128;            // one 128-byte column group of a chunk
+constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
+constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
+// f16 weights carry a factor of 2^7: at most 2^15 with the lag, and what f16
+// rounds to zero is below 2^-31 of the largest weight
+constexpr float kBiasF16 = 7.f;
+
+// misc words: tensor-memory base; abort; the range: first unit, units, units per
+// CTA, first sequence, KV head and page; halves handed to the ring the MMAs read
+enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_ISSUED };
+
+__device__ __forceinline__ void pdl_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void pdl_launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Has the phase with the given parity completed?  Never waits.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait that also gives up when another role of the CTA has given up.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* misc)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (misc[M_ABORT]) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            misc[M_ABORT] = 1;
+            raise_flag(&g_tree_err, KV_DEVERR_PIPELINE_TIMEOUT, blockIdx.x);
+            return false;
+        }
+    }
+}
+
+// Wait until half x is on its way into its slot.  A role that does not follow
+// every half of a ring (a stream that takes every second chunk, the warp that
+// fixes V rows) does this before it waits for the half's barrier: the slot's
+// previous phase is then known to be over, and the phase's parity to be that of
+// half x.
+__device__ __forceinline__ bool wait_issued(int x, volatile int* misc)
+{
+    if (misc[M_ISSUED] > x) return true;
+    const long long t0 = clock64();
+    while (misc[M_ISSUED] <= x) {
+        if (misc[M_ABORT]) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            misc[M_ABORT] = 1;
+            raise_flag(&g_tree_err, KV_DEVERR_PIPELINE_TIMEOUT, blockIdx.x);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for a whole warp.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* misc)
+{
+    return __all_sync(kFull, wait_bar(bar, parity, misc));
+}
+
+__device__ __forceinline__ long long warp_sum_ll(long long v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// One sequence as a team of CTAs sees it.
+struct SeqInfo {
+    int t0, n, L, base, nb;     // nb: pages, 0 when the team has no rows here
+};
+
+// `first_row`: the team's first row of a KV head's n * G rows.
+__device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int s, int first_row, bool flag)
+{
+    SeqInfo q;
+    int bad = 0;
+    if (!tree_span(p.starts, s, p.total, p.max_nodes, q.t0, q.n, bad) && flag)
+        raise_flag(&g_tree_err, KV_DEVERR_BAD_TREE, bad);
+    int L = __ldg(p.ctx + s);
+    const int cap = p.max_blocks * kBlock;
+    if (L < 0 || L > cap) {
+        if (flag) raise_flag(&g_tree_err, KV_DEVERR_CONTEXT_TOO_LONG, L);
+        L = L < 0 ? 0 : cap;
+    }
+    if (flag && L > 0 && L < q.n) raise_flag(&g_tree_err, KV_DEVERR_BAD_TREE, L);
+    const int rows = q.n * p.G;
+    q.L = L;
+    q.base = L > q.n ? L - q.n : 0;
+    q.nb = rows > first_row && rows > p.rows_above && rows <= p.rows_to ? (L + kBlock - 1) / kBlock : 0;
+    return q;
+}
+
+// Node (within the sequence) of row r of a KV head's rows.
+__device__ __forceinline__ int row_node(const TreeParams& p, int r)
+{
+    return p.g_magic ? (int)__umulhi((uint32_t)r, p.g_magic) : r;
+}
+
+// The segments of a CTA's range: the pages [j, j + np) of one (sequence, KV
+// head) each.  Every role walks the same list.
+struct Walk {
+    int s, h, j, rem, seg, np;
+    SeqInfo q;
+    __device__ __forceinline__ Walk(const TreeParams& p, const volatile int* misc, int first_row)
+    {
+        s = misc[M_S0];
+        h = misc[M_H0];
+        j = misc[M_J0];
+        rem = misc[M_CNT];
+        seg = 0;
+        np = 0;
+        if (rem > 0) {
+            q = seq_info(p, s, first_row, false);
+            np = min(q.nb - j, rem);
+        }
+    }
+    __device__ __forceinline__ bool more() const { return rem > 0; }
+    __device__ __forceinline__ int chunks() const { return (np + kPages - 1) / kPages; }
+    __device__ __forceinline__ int chunk_pages(int c) const { return min(kPages, np - c * kPages); }
+    // does chunk c reach the drafted positions?
+    __device__ __forceinline__ bool drafted(int c) const
+    {
+        return (j + c * kPages + chunk_pages(c)) * kBlock > q.base;
+    }
+    __device__ __forceinline__ bool whole() const { return j == 0 && np == q.nb; }
+    __device__ __forceinline__ void next(const TreeParams& p, int first_row)
+    {
+        rem -= np;
+        ++seg;
+        if (rem <= 0) return;
+        j = 0;
+        if (++h == p.Hkv) {
+            h = 0;
+            do {
+                if (++s >= p.B) {
+                    rem = 0;
+                    return;
+                }
+                q = seq_info(p, s, first_row, false);
+            } while (q.nb == 0);
+        }
+        np = min(q.nb, rem);
+    }
+};
+
+// This CTA's range of its team's flat (sequence, KV head, page) list: equal
+// shares of at least p.min_q pages.  One warp.
+__device__ __forceinline__ void cut_work(const TreeParams& p, volatile int* misc, int first_row, int cta,
+                                         bool flag, int lane)
+{
+    long long total = 0;
+    for (int b = 0; b < p.B; b += 32) {
+        int nb = 0;
+        if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, flag).nb;
+        total += warp_sum_ll(nb);
+    }
+    total *= p.Hkv;
+    long long q = (total + p.nctas - 1) / p.nctas;
+    if (q < p.min_q) q = p.min_q;
+    const long long b0 = (long long)cta * q;
+    long long cnt = total - b0;
+    if (cnt > q) cnt = q;
+    if (cnt < 0) cnt = 0;
+    int s0 = 0, h0 = 0, j0 = 0;
+    if (cnt > 0) {
+        long long excl = 0;
+        bool found = false;
+        for (int b = 0; b < p.B && !found; b += 32) {
+            int nb = 0;
+            if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, false).nb;
+            const long long v = (long long)nb * p.Hkv;
+            long long inc = v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(kFull, inc, o);
+                if (lane >= o) inc += t;
+            }
+            inc += excl;
+            const unsigned m = __ballot_sync(kFull, inc > b0);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                const long long ex = __shfl_sync(kFull, inc - v, src);
+                const int nbs = __shfl_sync(kFull, nb, src);
+                s0 = b + src;
+                const long long off = b0 - ex;
+                h0 = (int)(off / nbs);
+                j0 = (int)(off - (long long)h0 * nbs);
+                found = true;
+            }
+            excl = __shfl_sync(kFull, inc, 31);
+        }
+        if (!found) cnt = 0;
+    }
+    if (lane == 0) {
+        misc[M_B0] = (int)b0;
+        misc[M_CNT] = (int)cnt;
+        misc[M_Q] = (int)q;
+        misc[M_S0] = s0;
+        misc[M_H0] = h0;
+        misc[M_J0] = j0;
+    }
+}
+
+// Byte offset of 16-byte chunk c of row r in a [128 rows x 128 B] region
+// (128-byte swizzle).
+__device__ __forceinline__ uint32_t region_off(int r, int c)
+{
+    return (uint32_t)(r * 128) + (uint32_t)(((c ^ (r & 7)) & 7) * 16);
+}
+
+// Two E4M3 codes (the low half of x) as two f16: exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+        : "=r"(r)
+        : "r"(x));
+    return r;
+}
+
+// Zero the infinities and NaN (bf16), or NaN (E4M3), of four elements' words;
+// true if there were any.
+template <bool FP8>
+__device__ __forceinline__ bool drop_non_finite(uint32_t (&x)[4])
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t m = FP8 ? __vcmpeq4(x[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                               : __vcmpeq2(x[k] & 0x7f807f80u, 0x7f807f80u);
+        x[k] &= ~m;
+        any |= m;
+    }
+    return any != 0;
+}
+
+// Role of one warp: K and V of every chunk through the ring of load slots by TMA.
+template <class G>
+__device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                          uint32_t sb, volatile int* misc, int first_row, int lane)
+{
+    constexpr bool FP8 = G::kFp8;
+    auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
+    const uint64_t pol = l2_evict_first_policy();
+    int x = 0;                               // halves (K or V of a chunk) issued
+    bool ok = true;
+    for (Walk w(p, misc, first_row); ok && w.more(); w.next(p, first_row)) {
+        const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
+        int ids = lane < w.np ? __ldg(row + lane) : -1;       // pages 0..31 of the segment
+        int ahead = 32 + lane < w.np ? __ldg(row + 32 + lane) : -1;
+        const int nc = w.chunks();
+        for (int c = 0; ok && c < nc; ++c) {
+            if (c > 0 && (c & 3) == 0) {
+                ids = ahead;
+                const int at = (c + 4) * kPages + lane;
+                ahead = at < w.np ? __ldg(row + at) : -1;
+            }
+            const int np = w.chunk_pages(c);
+            const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + lane / G::kBoxes % kPages);
+            const int box = FP8 ? 0 : lane % G::kBoxes;
+            const int page = FP8 ? lane : lane / G::kBoxes;
+            const int my = FP8 ? __shfl_sync(kFull, ids, (c & 3) * kPages + (lane & 7)) : id;
+            const bool mine = page < np;
+            const bool valid = mine && my >= 0 && my < p.num_blocks;
+            if (mine && !valid && box == 0) raise_flag(&g_tree_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, my);
+            const int nvalid = __popc(__ballot_sync(kFull, valid && box == 0));
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++x) {
+                const int slot = x % G::kLoadSlots, round = x / G::kLoadSlots;
+                if (round > 0) ok = wait_warp(bar(G::B_EMPTY + slot), (uint32_t)((round - 1) & 1), misc);
+                if (!ok) break;
+                const uint32_t fb = bar(G::B_FULL + slot);
+                if (lane == 0) {
+                    if (nvalid > 0) mbar_arrive_expect_tx(fb, (uint32_t)(nvalid * G::kPageBytes));
+                    else mbar_arrive(fb);
+                }
+                __syncwarp();
+                if (valid) {
+                    const uint32_t dst =
+                        FP8 ? sb + (uint32_t)(G::kRawOff + slot * G::kRawSlot + page * G::kPageBytes)
+                            : sb + (uint32_t)(G::kSlotOff + slot * G::kSlot + box * kRegion +
+                                              page * kBlock * 128);
+                    const void* tm = kv == 0 ? &tm_k : &tm_v;
+                    const int z = my * p.Hkv + w.h;
+                    if (p.teams == 1)        // read once: first out of L2
+                        tma_load_3d_hint(dst, tm, box * 64, 0, z, fb, pol);
+                    else
+                        tma_load_3d(dst, tm, box * 64, 0, z, fb);
+                }
+                if (!FP8 && lane == 0) misc[M_ISSUED] = x + 1;
+            }
+        }
+    }
+    // every issued copy lands before the CTA can end
+    if (lane == 0)
+        for (int i = x > G::kLoadSlots ? x - G::kLoadSlots : 0; i < x; ++i)
+            mbar_wait_bounded(bar(G::B_FULL + i % G::kLoadSlots),
+                              (uint32_t)((i / G::kLoadSlots) & 1), kWaitLimit);
+    __syncwarp();
+}
+
+// The nodes each node of the segment's tree sees, as bits, by doubling along the
+// parents; and which nodes are padding.  One warp.
+template <class G>
+__device__ __forceinline__ void tree_masks(const TreeParams& p, const Walk& w, uint8_t* gb, int lane)
+{
+    const int buf = w.seg & 1, n = w.q.n;
+    uint32_t* anc = reinterpret_cast<uint32_t*>(gb + G::kAncOff);
+    volatile uint32_t* padw = reinterpret_cast<volatile uint32_t*>(gb + G::kPadOff);
+    volatile int* ptr = reinterpret_cast<volatile int*>(gb + G::kPtrOff);
+    volatile uint32_t* am = anc + buf * kN * 4;
+    int up[kN / 32];
+    uint32_t m[kN / 32][4];
+#pragma unroll
+    for (int k = 0; k < kN / 32; ++k) {
+        const int i = 32 * k + lane;
+        int par = -1;
+        if (i < n)
+            par = tree_parent(p.parents, w.q.t0, i,
+                              w.h == 0 && w.j == 0 ? &g_tree_err : nullptr);
+        const bool pad = i < n && par == KV_TREE_PAD;
+        const unsigned pads = __ballot_sync(kFull, pad);
+        if (lane == 0) padw[buf * 4 + k] = pads;
+        up[k] = i < n && !pad ? par : -1;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            m[k][v] = v == k && i < n && !pad ? 1u << lane : 0u;
+    }
+    for (int reach = 1; reach < n; reach *= 2) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kN / 32; ++k) {
+            const int i = 32 * k + lane;
+            ptr[i] = up[k];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) am[4 * i + v] = m[k][v];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kN / 32; ++k) {
+            if (up[k] >= 0) {
+                const int a = up[k];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) m[k][v] |= am[4 * a + v];
+                up[k] = ptr[a];
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kN / 32; ++k)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) am[4 * (32 * k + lane) + v] = m[k][v];
+}
+
+// Zero the V rows behind the context, and the infinities and NaN of the drafted
+// rows, of the segment's chunks that reach the drafted positions (bf16).  One
+// warp.  False: given up.
+template <class G>
+__device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, uint32_t sb, uint8_t* gb,
+                                           volatile int* misc, int x0, int lane)
+{
+    auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
+    volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(gb + G::kBadOff);
+    constexpr int D = G::kD, C = D / 8, RI = 32 / C, pw = 0;
+    const int buf = w.seg & 1, nc = w.chunks(), c = lane % C;
+    bool ok = true;
+    // ---- V rows of the chunks that reach the drafted positions
+    for (int ch = 0; ok && ch < nc; ++ch) {
+        if (!w.drafted(ch)) continue;
+        const int vx = x0 + 2 * ch + 1, slot = vx % G::kSlots;
+        ok = __all_sync(kFull, wait_issued(vx, misc)) &&
+             wait_warp(bar(G::B_FULL + slot), (uint32_t)((vx / G::kSlots) & 1), misc);
+        if (!ok) break;
+        const uint32_t vb = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
+        const int p0 = (w.j + ch * kPages) * kBlock;
+        const int lo = max(0, w.q.base - p0), hi = w.chunk_pages(ch) * kBlock;
+        for (int rb = lo; rb < hi; rb += RI) {
+            const int r = rb + lane / C;
+            const uint32_t at = vb + (uint32_t)((c >> 3) * kRegion) + region_off(r & 127, c & 7);
+            const bool in = r < hi, tail = p0 + r >= w.q.L;
+            if (!in) continue;
+            uint32_t v[4] = {0u, 0u, 0u, 0u};
+            bool bad = false;
+            if (!tail) {
+                lds128(v, at);
+                bad = drop_non_finite<false>(v);
+            }
+            if (tail || bad) sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
+            if (bad) {
+                const int a = p0 + r - w.q.base;
+                atomicOr(const_cast<uint32_t*>(&badw[(buf * G::kPrepWarps + pw) * 4 + (a >> 5)]),
+                         1u << (a & 31));
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(G::B_FIX + slot));
+    }
+    return ok;
+}
+
+// Widen the E4M3 codes of K and V of the segment's chunks to f16, with what
+// fix_values does on the way.  One of four warps (pw).  False: given up.
+template <class G>
+__device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32_t sb, uint8_t* gb,
+                                      volatile int* misc, int x0, int pw, int lane)
+{
+    auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
+    volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(gb + G::kBadOff);
+    constexpr int D = G::kD;
+    const int buf = w.seg & 1, nc = w.chunks();
+    bool ok = true;
+    // ---- widen K and V of every chunk: 16 codes a thread and step
+    constexpr int CR = D / 16;           // 16-code pieces of a row
+    constexpr int RS = 128 / CR;         // rows of the four warps' step
+    const int t = pw * 32 + lane;
+    const int cc = t % CR;
+    for (int ch = 0; ok && ch < nc; ++ch) {
+        const int keys = w.chunk_pages(ch) * kBlock;
+        const int p0 = (w.j + ch * kPages) * kBlock;
+        const bool drafted = w.drafted(ch);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+            const int hx = x0 + 2 * ch + kv;
+            const int rs = hx % G::kRawSlots, slot = hx % G::kSlots;
+            ok = wait_warp(bar(G::B_FULL + rs), (uint32_t)((hx / G::kRawSlots) & 1), misc);
+            if (ok && hx >= G::kSlots)
+                ok = wait_warp(bar(G::B_WFREE + slot), (uint32_t)((hx / G::kSlots - 1) & 1), misc);
+            if (!ok) break;
+            if (pw == 0 && lane == 0) misc[M_ISSUED] = hx + 1;
+            const uint32_t raw = sb + (uint32_t)(G::kRawOff + rs * G::kRawSlot);
+            const uint32_t dst = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
+            // the copy's swizzle: 16-byte pieces XOR bits 7 and up
+            auto load = [&](int r, uint32_t (&v)[4]) {
+                const uint32_t a = (uint32_t)(r * D + cc * 16);
+                lds128(v, raw + (a ^ (((a >> 7) & (D == 128 ? 7u : 3u)) << 4)));
+            };
+            // (the pieces of the second column group go in the other order:
+            // the eight lanes of a row then write to all banks at once)
+            auto store = [&](int r, const uint32_t (&v)[4]) {
+                const uint32_t d0 = dst + (uint32_t)((cc >> 2) * kRegion);
+                uint4 o[2];
+                o[0] = make_uint4(e4m3x2_to_f16x2(v[0]), e4m3x2_to_f16x2(v[0] >> 16),
+                                  e4m3x2_to_f16x2(v[1]), e4m3x2_to_f16x2(v[1] >> 16));
+                o[1] = make_uint4(e4m3x2_to_f16x2(v[2]), e4m3x2_to_f16x2(v[2] >> 16),
+                                  e4m3x2_to_f16x2(v[3]), e4m3x2_to_f16x2(v[3] >> 16));
+                const int second = (cc >> 2) & 1;
+                sts128(d0 + region_off(r, (2 * cc + second) & 7), second ? o[1] : o[0]);
+                sts128(d0 + region_off(r, (2 * cc + 1 - second) & 7), second ? o[0] : o[1]);
+            };
+            if (keys == kKeys && !(kv == 1 && drafted)) {
+                constexpr int kStep = 4;         // loads in flight
+#pragma unroll
+                for (int rb = 0; rb < kKeys; rb += kStep * RS) {
+                    uint32_t v[kStep][4];
+#pragma unroll
+                    for (int k = 0; k < kStep; ++k) load(rb + k * RS + t / CR, v[k]);
+#pragma unroll
+                    for (int k = 0; k < kStep; ++k) store(rb + k * RS + t / CR, v[k]);
+                }
+            } else {
+                for (int rb = 0; rb < keys; rb += RS) {
+                    const int r = rb + t / CR, pos = p0 + r;
+                    if (r >= keys) continue;
+                    uint32_t v[4];
+                    load(r, v);
+                    if (kv == 1 && pos >= w.q.L) {
+                        v[0] = v[1] = v[2] = v[3] = 0u;
+                    } else if (kv == 1 && pos >= w.q.base && drop_non_finite<true>(v)) {
+                        const int an = pos - w.q.base;
+                        atomicOr(const_cast<uint32_t*>(&badw[(buf * G::kPrepWarps + pw) * 4 + (an >> 5)]),
+                                 1u << (an & 31));
+                    }
+                    store(r, v);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(G::B_EMPTY + rs));
+                mbar_arrive(bar(G::B_WIDE + slot));
+            }
+        }
+    }
+    return ok;
+}
+
+// A query row's 16 bytes as f16, for E4M3 keys.  f16 overflows above 65504: a row
+// whose largest |element| is 2^15 or more is divided by a power of two that
+// brings it below (exact but for elements below 2^-39 of the largest), which the
+// scores are multiplied by again: `up`.  The row's D / 8 lanes call together.
+template <int D>
+__device__ __forceinline__ uint4 query_f16(uint4 v, float& up)
+{
+    const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+    uint32_t big = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) big = max(big, max(q4[k] & 0x7fffu, (q4[k] >> 16) & 0x7fffu));
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
+    const int e = min(max((int)(big >> 7) - (127 + 14), 0), 126);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    up = __uint_as_float((uint32_t)(127 + e) << 23);
+    return make_uint4(pack_f16x2(bf16_lo(q4[0]) * down, bf16_hi(q4[0]) * down),
+                      pack_f16x2(bf16_lo(q4[1]) * down, bf16_hi(q4[1]) * down),
+                      pack_f16x2(bf16_lo(q4[2]) * down, bf16_hi(q4[2]) * down),
+                      pack_f16x2(bf16_lo(q4[3]) * down, bf16_hi(q4[3]) * down));
+}
+
+// Sequences without a context get zeros for their nodes (threads 0 .. nthreads - 1
+// of the CTAs of the kernel that does it).
+__device__ __forceinline__ void zero_empty(const TreeParams& p, int D, int cta, int ctas, int tid, int nthreads)
+{
+    for (int s = cta; s < p.B; s += ctas) {
+        const SeqInfo q = seq_info(p, s, 0, false);
+        if (q.L > 0 || q.n == 0) continue;
+        const size_t e0 = (size_t)q.t0 * p.Hq * D, cnt = (size_t)q.n * p.Hq * D;
+        const int es = p.out_f32 ? 4 : 2;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + e0 * es);
+        for (size_t i = tid; i < cnt * es / 16; i += nthreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+}  // namespace
+}  // namespace pkv

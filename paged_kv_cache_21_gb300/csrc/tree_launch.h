@@ -1,0 +1,47 @@
+// paged_tree_attention: parameters and host entry points shared by its CUDA
+// translation units.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace pkv {
+
+struct TreeParams {
+    const uint16_t* q;          // bf16 [total][Hq][D]
+    void* out;
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const int32_t* bt;
+    const int32_t* ctx;
+    const int32_t* starts;
+    const int32_t* parents;
+    float* part_o;              // [CTAs][2][rows of a CTA][D]
+    float2* part_ml;            // [CTAs][2][rows of a CTA]: (max in log2 units, sum)
+    int4* meta;                 // [CTAs]: (sequence, KV head, partials, rows)
+    int B, total, max_nodes, Hq, Hkv, G, max_blocks, num_blocks;
+    uint32_t g_magic;           // ceil(2^32 / G), 0 for G == 1
+    int nctas;                  // CTAs of a team
+    int teams;
+    int min_q;                  // least pages of a CTA's range
+    int rows_above, rows_to;    // the sequences served: rows_above < n * G <= rows_to
+    int tidy;                   // this kernel raises the table flags and zeroes empty sequences
+    float sl2, v_scale;
+    int out_f32;
+    long long test_stall;
+};
+
+// Query rows per KV head up to which a sequence is served by the kernel for few rows.
+constexpr int kSmallRows = 64;
+
+// The kernel for few rows: rows (32 or 64) of its instantiation for the most
+// rows a sequence may have there, and its launch (grid p.nctas).
+int tree_small_rows(int rows);
+cudaError_t tree_small_launch(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, int D,
+                              bool fp8, int rows, cudaStream_t st);
+int tree_small_read_error(unsigned* flags, long long* detail);
+
+}  // namespace pkv
