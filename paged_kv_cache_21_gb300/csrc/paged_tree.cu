@@ -220,7 +220,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                   w.q.n * p.G - first_row <= kTile;
                 bool first = true;
                 for (int c = 0; ok && c < nc; ++c) {
-                    const int kx = x0 + 2 * c, vx = kx + 1;
+                    const int kx = k_half(x0, c), vx = v_half(x0, c, nc);
                     const int ks = kx % G::kSlots, vs = vx % G::kSlots;
                     const uint32_t kp = (uint32_t)((kx / G::kSlots) & 1);
                     const uint32_t vp = (uint32_t)((vx / G::kSlots) & 1);
@@ -870,7 +870,8 @@ extern "C" int paged_tree_attention(void* out, int out_dtype, const void* q, con
     // flat work indices and tensor-map rows must fit in int32
     if ((long long)num_seqs * max_blocks_per_seq * num_kv_heads >= INT_MAX ||
         (long long)num_blocks * num_kv_heads >= INT_MAX ||
-        (long long)max_blocks_per_seq * kBlock >= INT_MAX)
+        (long long)max_blocks_per_seq * kBlock >= INT_MAX ||
+        (long long)total_nodes * num_q_heads >= INT_MAX)
         return KV_ERR_UNSUPPORTED;
     const TreePlan t = tree_plan(max_nodes, num_q_heads / num_kv_heads, head_dim);
     if (workspace_bytes < t.total) return KV_ERR_INVALID_ARG;

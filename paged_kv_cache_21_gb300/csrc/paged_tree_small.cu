@@ -91,7 +91,8 @@ struct SmallGeo {
     static constexpr int kAlphaOff = kRefOff + 2 * N * 4;    // [group][N] floats
     static constexpr int kWmaxOff = kAlphaOff + 2 * N * 4;   // [group][4][N] floats: maxima, later sums
     static constexpr int kFacOff = kWmaxOff + 8 * N * 4;     // [N] float4
-    static constexpr int kVoteOff = kFacOff + N * 16;        // [group][4] words, then [group][2]
+    static constexpr int kRowOff = kFacOff + N * 16;         // [N] words: (node, head) of a row
+    static constexpr int kVoteOff = kRowOff + N * 4;         // [group][4] words, then [group][2]
     static constexpr int kEnd = kVoteOff + 64;
     static constexpr int kSmem = kEnd + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -219,7 +220,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // been waited for when chunk c >= g - 3 comes
                 auto scores_up_to = [&](int c) -> bool {
                     for (; sc <= c + 3 && sc < nc; ++sc) {
-                        const int g = g0 + sc, x = 2 * g, ks = x % G::kSlots;
+                        const int g = g0 + sc, x = k_half(2 * g0, sc), ks = x % G::kSlots;
                         const uint32_t parity = (uint32_t)((x / G::kSlots) & 1);
                         if (sc > c) {
                             if (misc[M_ISSUED] <= x || !mbar_test(bar(full0 + ks), parity)) break;
@@ -241,7 +242,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     return true;
                 };
                 for (int c = 0; ok && c < nc; ++c) {
-                    const int g = g0 + c, x = 2 * g + 1, vs = x % G::kSlots, grp = g & 1;
+                    const int g = g0 + c, x = v_half(2 * g0, c, nc), vs = x % G::kSlots, grp = g & 1;
                     ok = scores_up_to(c) && wait_bar(bar(G::B_PFULL + grp), (uint32_t)((g >> 1) & 1), misc) &&
                          wait_issued(x, misc) &&
                          wait_bar(bar(full0 + vs), (uint32_t)((x / G::kSlots) & 1), misc);
@@ -399,31 +400,32 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                 }
                 const bool masked = w.drafted(c) || np < kPages;     // (for the whole chunk)
-                float t[N];
-                // the scores relative to the references, in log2 units
-                auto load = [&](bool again) -> float {
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int q = 0; q < N / 32; ++q)
-                        umma::tmem_ld32(tS + (uint32_t)(32 * q), *reinterpret_cast<uint32_t(*)[32]>(&t[32 * q]));
+                // the scores of 32 rows relative to the references, in log2 units.  (64
+                // rows are loaded twice, 32 at a time: half the registers)
+                float t[32];
+                auto load = [&](int q) {
+                    umma::tmem_ld32(tS + (uint32_t)(32 * q), *reinterpret_cast<uint32_t(*)[32]>(&t[0]));
                     umma::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < N; k += 2) {
-                        const float4 f = *reinterpret_cast<const float4*>(sn + k);   // two rows
+                    for (int k = 0; k < 32; k += 2) {
+                        const float4 f = *reinterpret_cast<const float4*>(sn + 32 * q + k);   // two rows
                         t[k] = fmaf(t[k], f.x, f.y);
                         t[k + 1] = fmaf(t[k + 1], f.z, f.w);
                     }
                     if (masked) {
 #pragma unroll
-                        for (int k = 0; k < N; ++k) t[k] = (vis[k / 32] >> (k & 31)) & 1u ? t[k] : -INFINITY;
+                        for (int k = 0; k < 32; ++k) t[k] = (vis[q] >> k) & 1u ? t[k] : -INFINITY;
                     }
-                    if (!again) {
-#pragma unroll
-                        for (int k = 0; k < N; ++k) mx[k & 3] = fmaxf(mx[k & 3], t[k]);
-                    }
-                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
-                const float mx = load(false);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < N / 32; ++q) {
+                    load(q);
+                    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], t[k]);
+                    mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
+                }
                 // does any row's reference lag too far behind?
                 {
                     const int slot = votes & 3;
@@ -437,11 +439,11 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                         for (int q = 0; q < N / 32; ++q) {
                             int best = INT32_MIN;
+                            if (N > 32) load(q);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
-                                const int r = 32 * q + k;
                                 // (relative to the old reference, or to none)
-                                const int m = __reduce_max_sync(kFull, ordered(t[r]));
+                                const int m = __reduce_max_sync(kFull, ordered(t[k]));
                                 if (lane == k) best = m;
                             }
                             wmax[wq * N + 32 * q + lane] = unordered(best);
@@ -487,14 +489,8 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                             }
                             umma::tmem_wait_st();
                         }
-                        load(true);
+                        if (N == 32) load(0);
                     }
-                }
-                // ---- the weights
-#pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    t[k] = ex2(t[k]);
-                    if (N == 32) l[k] += t[k];
                 }
                 if (g >= 2) {
                     // the group's buffer: the products of its chunk before are done
@@ -502,44 +498,47 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if (!ok) break;
                 }
                 first = false;
-                if (key < np * kBlock) {
+                // ---- the weights
+                const bool store = key < np * kBlock;
 #pragma unroll
-                    for (int k = 0; k < N; k += 8) {
-                        uint32_t hi[4], lo[4];
+                for (int q = 0; q < N / 32; ++q) {
+                    if (N > 32) load(q);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = t[k + 2 * e], b = t[k + 2 * e + 1];
-                            if (FP8) {
-                                hi[e] = pack_f16x2(a, b);
-                                const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
-                                lo[e] = pack_f16x2(a - __low2float(h), b - __high2float(h));
-                            } else {
-                                hi[e] = pack_bf16x2(a, b);
-                                lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
-                            }
-                        }
-                        // 16 bytes: rows k .. k + 7; the low parts N columns on
-                        const int ch = k / 8, cl = (k + N) / 8;
-                        sts128(pb + (uint32_t)((ch >> 3) * kRegion + ((ch ^ key) & 7) * 16),
-                               make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        if (G::kLow)
-                            sts128(pb + (uint32_t)((cl >> 3) * kRegion + ((cl ^ key) & 7) * 16),
-                                   make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    for (int k = 0; k < 32; ++k) {
+                        t[k] = ex2(t[k]);
+                        if (N == 32) l[k] += t[k];
                     }
+                    if (store) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float a = t[k + 2 * e], b = t[k + 2 * e + 1];
+                                if (FP8) {
+                                    hi[e] = pack_f16x2(a, b);
+                                    const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
+                                    lo[e] = pack_f16x2(a - __low2float(h), b - __high2float(h));
+                                } else {
+                                    hi[e] = pack_bf16x2(a, b);
+                                    lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
+                                }
+                            }
+                            // 16 bytes: eight rows; the low parts N columns on
+                            const int ch = 4 * q + k / 8, cl = ch + N / 8;
+                            sts128(pb + (uint32_t)((ch >> 3) * kRegion + ((ch ^ key) & 7) * 16),
+                                   make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                            if (G::kLow)
+                                sts128(pb + (uint32_t)((cl >> 3) * kRegion + ((cl ^ key) & 7) * 16),
+                                       make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                        }
+                    }
+                    if (N > 32) l[q] += column_sums(t, lane);
                 }
                 fence_proxy_async_smem();
                 umma::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(G::B_PFULL + grp));
-                if constexpr (N == 64) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float v[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = t[32 * q + k];
-                        l[q] += column_sums(v, lane);
-                    }
-                }
             }
             if (!ok) break;
             // ---- the segment's result: join the two groups' sums and accumulators
@@ -557,7 +556,9 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (!ok) break;
             const bool whole = w.whole();
             const size_t slot = (size_t)cta * 2 + (w.j == 0 ? 1 : 0);
+            // a row's factors (of the groups' accumulators, of the result) and its place
             float4* fac = reinterpret_cast<float4*>(gb + G::kFacOff);
+            int* rowat = reinterpret_cast<int*>(gb + G::kRowOff);
             if (tid < N) {
                 const float* base = reinterpret_cast<const float*>(gb + G::kWmaxOff);
                 const float* refs = reinterpret_cast<const float*>(gb + G::kRefOff);
@@ -573,7 +574,9 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float a0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - M);
                 const float a1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - M);
                 const float L = s[0] * a0 + s[1] * a1;
-                fac[tid] = make_float4(a0, a1, L == 0.f ? 0.f : p.v_scale / L, L);
+                fac[tid] = make_float4(a0, a1, whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
+                const int nd = row_node(p, tid);
+                rowat[tid] = whole ? (w.q.t0 + nd) * p.Hq + w.h * p.G + tid - nd * p.G : (int)(slot * N) + tid;
                 if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
             }
             ok = join();
@@ -595,25 +598,22 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     for (int k = 0; k < 16; ++k) v[k] = 0.f;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
+                        uint32_t low[16];
+                        umma::tmem_ld16(t0 + (uint32_t)(q * G::kPW), o);
+                        if (G::kLow) umma::tmem_ld16(t0 + (uint32_t)(q * G::kPW + N), low);
+                        umma::tmem_wait_ld();
 #pragma unroll
-                        for (int part = 0; part < (G::kLow ? 2 : 1); ++part) {
-                            umma::tmem_ld16(t0 + (uint32_t)(q * G::kPW + part * N), o);
-                            umma::tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float a = q == 0 ? fac[r0 + k].x : fac[r0 + k].y;
-                                if (a != 0.f) v[k] += __uint_as_float(o[k]) * a;
-                            }
+                        for (int k = 0; k < 16; ++k) {
+                            const float a = q == 0 ? fac[r0 + k].x : fac[r0 + k].y;
+                            const float sum = __uint_as_float(o[k]) + (G::kLow ? __uint_as_float(low[k]) : 0.f);
+                            if (a != 0.f) v[k] += sum * a;
                         }
                     }
+                    if (back) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int r = r0 + k;
-                        if (r >= rows) continue;
-                        const int nd = row_node(p, r);
-                        const float4 f = fac[r];
-                        float x = f.w == 0.f ? 0.f : v[k];
-                        if (back && !((padw[nd >> 5] >> (nd & 31)) & 1u)) {
+                        for (int k = 0; k < 16; ++k) {
+                            const int nd = row_node(p, r0 + k);
+                            if (r0 + k >= rows || ((padw[nd >> 5] >> (nd & 31)) & 1u)) continue;
                             for (int k4 = 0; k4 < 4; ++k4) {
                                 uint32_t b = 0u;
                                 for (int q = 0; q < G::kPrepWarps; ++q) b |= badw[q * 4 + k4];
@@ -623,21 +623,22 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                                     if (blk < 0 || blk >= p.num_blocks) continue;
                                     const size_t at = (((size_t)blk * p.Hkv + w.h) * kBlock + pos % kBlock) * D + d;
                                     if (FP8) {
-                                        if ((p.v_cache[at] & 0x7fu) == 0x7fu) x = __uint_as_float(0x7fffffffu);
+                                        if ((p.v_cache[at] & 0x7fu) == 0x7fu) v[k] = __uint_as_float(0x7fffffffu);
                                     } else {
                                         const float z = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.v_cache)[at] << 16);
-                                        if (!(fabsf(z) < INFINITY)) x += z;
+                                        if (!(fabsf(z) < INFINITY)) v[k] += z;
                                     }
                                 }
                             }
                         }
-                        if (!whole) {
-                            p.part_o[(slot * N + r) * D + d] = x;
-                            continue;
-                        }
-                        const size_t at = ((size_t)(w.q.t0 + nd) * p.Hq + (size_t)w.h * p.G + (r - nd * p.G)) * D + d;
-                        x *= f.z;
-                        if (p.out_f32) static_cast<float*>(p.out)[at] = x;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        if (r0 + k >= rows) break;
+                        const float x = v[k] * fac[r0 + k].z;
+                        const size_t at = (size_t)rowat[r0 + k] * D + d;
+                        if (!whole) p.part_o[at] = x;
+                        else if (p.out_f32) static_cast<float*>(p.out)[at] = x;
                         else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
                     }
                 }

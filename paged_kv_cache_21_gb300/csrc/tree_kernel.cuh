@@ -5,8 +5,10 @@
 //
 // A kernel's geometry G names its shared memory (offsets k..Off from a
 // 1024-byte aligned base) and its barriers (B_..); both kernels consume K and V
-// in chunks of up to 8 pages, in "halves": half 2 c is the K, half 2 c + 1 the V
-// of the CTA's chunk c, in slot x % slots of a ring.
+// in chunks of up to 8 pages.  The K or V of a chunk is a "half"; half x of a CTA
+// lies in slot x % slots of a ring.  V is needed a softmax later than K, so the
+// halves of a segment come in the order K0 K1 V0 K2 V1 ... : no slot is held by a
+// V whose weights are not there yet while K could be loaded.
 #pragma once
 
 #include <cuda.h>
@@ -35,6 +37,10 @@ constexpr float kMaxLag = 8.f;                  // the reference maximum may lag
 // f16 weights carry a factor of 2^7: at most 2^15 with the lag, and what f16
 // rounds to zero is below 2^-31 of the largest weight
 constexpr float kBiasF16 = 7.f;
+
+// The halves of chunk c of a segment of nc chunks whose first half is x0.
+__device__ __forceinline__ int k_half(int x0, int c) { return c == 0 ? x0 : x0 + 2 * c - 1; }
+__device__ __forceinline__ int v_half(int x0, int c, int nc) { return c == nc - 1 ? x0 + 2 * nc - 1 : x0 + 2 * c + 2; }
 
 // misc words: tensor-memory base; abort; the range: first unit, units, units per
 // CTA, first sequence, KV head and page; halves handed to the ring the MMAs read
@@ -273,14 +279,13 @@ __device__ __forceinline__ uint32_t region_off(int r, int c)
     return (uint32_t)(r * 128) + (uint32_t)(((c ^ (r & 7)) & 7) * 16);
 }
 
-// Two E4M3 codes (the low half of x) as two f16: exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
+// Four E4M3 codes as four f16: exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi)
 {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(r)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
         : "r"(x));
-    return r;
 }
 
 // Zero the infinities and NaN (bf16), or NaN (E4M3), of four elements' words;
@@ -314,45 +319,58 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
         int ids = lane < w.np ? __ldg(row + lane) : -1;       // pages 0..31 of the segment
         int ahead = 32 + lane < w.np ? __ldg(row + 32 + lane) : -1;
         const int nc = w.chunks();
-        for (int c = 0; ok && c < nc; ++c) {
-            if (c > 0 && (c & 3) == 0) {
-                ids = ahead;
-                const int at = (c + 4) * kPages + lane;
-                ahead = at < w.np ? __ldg(row + at) : -1;
+        const int box = FP8 ? 0 : lane % G::kBoxes, page = FP8 ? lane : lane / G::kBoxes;
+        int my = -1, nvalid = 0;                 // this lane's page of the chunk; pages to copy
+        bool valid = false;
+        auto issue = [&](const CUtensorMap& tm) -> bool {
+            const int slot = x % G::kLoadSlots, round = x / G::kLoadSlots;
+            if (round > 0 && !wait_warp(bar(G::B_EMPTY + slot), (uint32_t)((round - 1) & 1), misc)) return false;
+            const uint32_t fb = bar(G::B_FULL + slot);
+            if (lane == 0) {
+                if (nvalid > 0) mbar_arrive_expect_tx(fb, (uint32_t)(nvalid * G::kPageBytes));
+                else mbar_arrive(fb);
             }
-            const int np = w.chunk_pages(c);
-            const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + lane / G::kBoxes % kPages);
-            const int box = FP8 ? 0 : lane % G::kBoxes;
-            const int page = FP8 ? lane : lane / G::kBoxes;
-            const int my = FP8 ? __shfl_sync(kFull, ids, (c & 3) * kPages + (lane & 7)) : id;
-            const bool mine = page < np;
-            const bool valid = mine && my >= 0 && my < p.num_blocks;
-            if (mine && !valid && box == 0) raise_flag(&g_tree_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, my);
-            const int nvalid = __popc(__ballot_sync(kFull, valid && box == 0));
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++x) {
-                const int slot = x % G::kLoadSlots, round = x / G::kLoadSlots;
-                if (round > 0) ok = wait_warp(bar(G::B_EMPTY + slot), (uint32_t)((round - 1) & 1), misc);
-                if (!ok) break;
-                const uint32_t fb = bar(G::B_FULL + slot);
-                if (lane == 0) {
-                    if (nvalid > 0) mbar_arrive_expect_tx(fb, (uint32_t)(nvalid * G::kPageBytes));
-                    else mbar_arrive(fb);
+            __syncwarp();
+            if (valid) {
+                const uint32_t dst =
+                    FP8 ? sb + (uint32_t)(G::kRawOff + slot * G::kRawSlot + page * G::kPageBytes)
+                        : sb + (uint32_t)(G::kSlotOff + slot * G::kSlot + box * kRegion + page * kBlock * 128);
+                const int z = my * p.Hkv + w.h;
+                if (p.teams == 1)                // read once: first out of L2
+                    tma_load_3d_hint(dst, &tm, box * 64, 0, z, fb, pol);
+                else
+                    tma_load_3d(dst, &tm, box * 64, 0, z, fb);
+            }
+            ++x;
+            if (!FP8 && lane == 0) misc[M_ISSUED] = x;
+            return true;
+        };
+        for (int c = 0; ok && c <= nc; ++c) {
+            const int v_my = my, v_nvalid = nvalid;      // the chunk before, whose V follows
+            const bool v_valid = valid;
+            if (c < nc) {
+                if (c > 0 && (c & 3) == 0) {
+                    ids = ahead;
+                    const int at = (c + 4) * kPages + lane;
+                    ahead = at < w.np ? __ldg(row + at) : -1;
                 }
-                __syncwarp();
-                if (valid) {
-                    const uint32_t dst =
-                        FP8 ? sb + (uint32_t)(G::kRawOff + slot * G::kRawSlot + page * G::kPageBytes)
-                            : sb + (uint32_t)(G::kSlotOff + slot * G::kSlot + box * kRegion +
-                                              page * kBlock * 128);
-                    const void* tm = kv == 0 ? &tm_k : &tm_v;
-                    const int z = my * p.Hkv + w.h;
-                    if (p.teams == 1)        // read once: first out of L2
-                        tma_load_3d_hint(dst, tm, box * 64, 0, z, fb, pol);
-                    else
-                        tma_load_3d(dst, tm, box * 64, 0, z, fb);
-                }
-                if (!FP8 && lane == 0) misc[M_ISSUED] = x + 1;
+                my = __shfl_sync(kFull, ids, (c & 3) * kPages + page % kPages);
+                const bool mine = page < w.chunk_pages(c);
+                valid = mine && my >= 0 && my < p.num_blocks;
+                if (mine && !valid && box == 0) raise_flag(&g_tree_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, my);
+                nvalid = __popc(__ballot_sync(kFull, valid && box == 0));
+                ok = issue(tm_k);
+            }
+            if (ok && c > 0) {
+                const int k_my = my, k_nvalid = nvalid;
+                const bool k_valid = valid;
+                my = v_my;
+                nvalid = v_nvalid;
+                valid = v_valid;
+                ok = issue(tm_v);
+                my = k_my;
+                nvalid = k_nvalid;
+                valid = k_valid;
             }
         }
     }
@@ -433,7 +451,7 @@ __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, u
     // ---- V rows of the chunks that reach the drafted positions
     for (int ch = 0; ok && ch < nc; ++ch) {
         if (!w.drafted(ch)) continue;
-        const int vx = x0 + 2 * ch + 1, slot = vx % G::kSlots;
+        const int vx = v_half(x0, ch, nc), slot = vx % G::kSlots;
         ok = __all_sync(kFull, wait_issued(vx, misc)) &&
              wait_warp(bar(G::B_FULL + slot), (uint32_t)((vx / G::kSlots) & 1), misc);
         if (!ok) break;
@@ -476,76 +494,71 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
     constexpr int D = G::kD;
     const int buf = w.seg & 1, nc = w.chunks();
     bool ok = true;
-    // ---- widen K and V of every chunk: 16 codes a thread and step
-    constexpr int CR = D / 16;           // 16-code pieces of a row
-    constexpr int RS = 128 / CR;         // rows of the four warps' step
+    // 16 codes a thread and step: piece cc of row r.  Eight lanes that go to
+    // shared memory together have eight rows, so their pieces lie, swizzled, in
+    // different banks on both sides; a step is RS rows, a multiple of the swizzle's
+    // period, so that offsets between steps are constants.
+    constexpr int CR = D / 16;               // 16-code pieces of a row
+    constexpr int RS = 128 / CR;             // rows of the four warps' step
+    constexpr int kSteps = kKeys / RS;
     const int t = pw * 32 + lane;
-    const int cc = t % CR;
-    for (int ch = 0; ok && ch < nc; ++ch) {
+    const int r0 = t % RS, cc = t / RS;
+    // the copy's swizzle: 16-byte pieces XOR bits 7 and up of the address
+    const uint32_t flat = (uint32_t)(r0 * D + cc * 16);
+    const uint32_t src0 = flat ^ (((flat >> 7) & (D == 128 ? 7u : 3u)) << 4);
+    const uint32_t dst0 = (uint32_t)((cc >> 2) * kRegion) + region_off(r0, (2 * cc) & 7);
+    const uint32_t dst1 = (uint32_t)((cc >> 2) * kRegion) + region_off(r0, (2 * cc + 1) & 7);
+    for (int half = 0; ok && half < 2 * nc; ++half) {
+        const int hx = x0 + half;
+        const bool is_k = half == 0 || ((half & 1) && half < 2 * nc - 1);
+        const int ch = is_k ? (half + 1) / 2 : half == 2 * nc - 1 ? nc - 1 : half / 2 - 1;
+        const int rs = hx % G::kRawSlots, slot = hx % G::kSlots;
+        ok = wait_warp(bar(G::B_FULL + rs), (uint32_t)((hx / G::kRawSlots) & 1), misc);
+        if (ok && hx >= G::kSlots)
+            ok = wait_warp(bar(G::B_WFREE + slot), (uint32_t)((hx / G::kSlots - 1) & 1), misc);
+        if (!ok) break;
+        if (pw == 0 && lane == 0) misc[M_ISSUED] = hx + 1;
+        const uint32_t raw = sb + (uint32_t)(G::kRawOff + rs * G::kRawSlot) + src0;
+        const uint32_t dst = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
+        auto store = [&](int step, const uint32_t (&v)[4]) {
+            uint4 a, b;
+            e4m3x4_to_f16x4(v[0], a.x, a.y);
+            e4m3x4_to_f16x4(v[1], a.z, a.w);
+            e4m3x4_to_f16x4(v[2], b.x, b.y);
+            e4m3x4_to_f16x4(v[3], b.z, b.w);
+            sts128(dst + dst0 + (uint32_t)(step * RS * 128), a);
+            sts128(dst + dst1 + (uint32_t)(step * RS * 128), b);
+        };
         const int keys = w.chunk_pages(ch) * kBlock;
-        const int p0 = (w.j + ch * kPages) * kBlock;
-        const bool drafted = w.drafted(ch);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-            const int hx = x0 + 2 * ch + kv;
-            const int rs = hx % G::kRawSlots, slot = hx % G::kSlots;
-            ok = wait_warp(bar(G::B_FULL + rs), (uint32_t)((hx / G::kRawSlots) & 1), misc);
-            if (ok && hx >= G::kSlots)
-                ok = wait_warp(bar(G::B_WFREE + slot), (uint32_t)((hx / G::kSlots - 1) & 1), misc);
-            if (!ok) break;
-            if (pw == 0 && lane == 0) misc[M_ISSUED] = hx + 1;
-            const uint32_t raw = sb + (uint32_t)(G::kRawOff + rs * G::kRawSlot);
-            const uint32_t dst = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
-            // the copy's swizzle: 16-byte pieces XOR bits 7 and up
-            auto load = [&](int r, uint32_t (&v)[4]) {
-                const uint32_t a = (uint32_t)(r * D + cc * 16);
-                lds128(v, raw + (a ^ (((a >> 7) & (D == 128 ? 7u : 3u)) << 4)));
-            };
-            // (the pieces of the second column group go in the other order:
-            // the eight lanes of a row then write to all banks at once)
-            auto store = [&](int r, const uint32_t (&v)[4]) {
-                const uint32_t d0 = dst + (uint32_t)((cc >> 2) * kRegion);
-                uint4 o[2];
-                o[0] = make_uint4(e4m3x2_to_f16x2(v[0]), e4m3x2_to_f16x2(v[0] >> 16),
-                                  e4m3x2_to_f16x2(v[1]), e4m3x2_to_f16x2(v[1] >> 16));
-                o[1] = make_uint4(e4m3x2_to_f16x2(v[2]), e4m3x2_to_f16x2(v[2] >> 16),
-                                  e4m3x2_to_f16x2(v[3]), e4m3x2_to_f16x2(v[3] >> 16));
-                const int second = (cc >> 2) & 1;
-                sts128(d0 + region_off(r, (2 * cc + second) & 7), second ? o[1] : o[0]);
-                sts128(d0 + region_off(r, (2 * cc + 1 - second) & 7), second ? o[0] : o[1]);
-            };
-            if (keys == kKeys && !(kv == 1 && drafted)) {
-                constexpr int kStep = 4;         // loads in flight
+        if (keys == kKeys && (is_k || !w.drafted(ch))) {
 #pragma unroll
-                for (int rb = 0; rb < kKeys; rb += kStep * RS) {
-                    uint32_t v[kStep][4];
+            for (int s0 = 0; s0 < kSteps; s0 += 4) {     // four loads in flight
+                uint32_t v[4][4];
 #pragma unroll
-                    for (int k = 0; k < kStep; ++k) load(rb + k * RS + t / CR, v[k]);
+                for (int k = 0; k < 4; ++k) lds128(v[k], raw + (uint32_t)((s0 + k) * RS * D));
 #pragma unroll
-                    for (int k = 0; k < kStep; ++k) store(rb + k * RS + t / CR, v[k]);
-                }
-            } else {
-                for (int rb = 0; rb < keys; rb += RS) {
-                    const int r = rb + t / CR, pos = p0 + r;
-                    if (r >= keys) continue;
-                    uint32_t v[4];
-                    load(r, v);
-                    if (kv == 1 && pos >= w.q.L) {
-                        v[0] = v[1] = v[2] = v[3] = 0u;
-                    } else if (kv == 1 && pos >= w.q.base && drop_non_finite<true>(v)) {
-                        const int an = pos - w.q.base;
-                        atomicOr(const_cast<uint32_t*>(&badw[(buf * G::kPrepWarps + pw) * 4 + (an >> 5)]),
-                                 1u << (an & 31));
-                    }
-                    store(r, v);
-                }
+                for (int k = 0; k < 4; ++k) store(s0 + k, v[k]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(G::B_EMPTY + rs));
-                mbar_arrive(bar(G::B_WIDE + slot));
+        } else {
+            for (int step = 0; step * RS + r0 < keys; ++step) {
+                const int pos = (w.j + ch * kPages) * kBlock + step * RS + r0;
+                uint32_t v[4];
+                lds128(v, raw + (uint32_t)(step * RS * D));
+                if (!is_k && pos >= w.q.L) {
+                    v[0] = v[1] = v[2] = v[3] = 0u;
+                } else if (!is_k && pos >= w.q.base && drop_non_finite<true>(v)) {
+                    const int an = pos - w.q.base;
+                    atomicOr(const_cast<uint32_t*>(&badw[(buf * G::kPrepWarps + pw) * 4 + (an >> 5)]),
+                             1u << (an & 31));
+                }
+                store(step, v);
             }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar(G::B_EMPTY + rs));
+            mbar_arrive(bar(G::B_WIDE + slot));
         }
     }
     return ok;
