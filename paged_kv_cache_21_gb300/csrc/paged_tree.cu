@@ -87,23 +87,33 @@ struct Geo {
     static constexpr int kQTile = kBoxes * kTile * 128;
     static constexpr int kPageBytes = kBlock * D * (FP8 ? 1 : 2);
     static constexpr int kRawSlot = kPages * kBlock * D;     // E4M3 codes of K or V of a chunk
-    // slots the MMAs read (filled by TMA, or by the widening warps), and the
-    // ring of codes in front of them
-    static constexpr int kSlots = FP8 ? (D == 128 ? 3 : 6)
-                                      : (TILES == 1 ? 5 : 4) * (D == 128 ? 1 : 2);
-    static constexpr int kRawSlots = !FP8 ? 0 : (TILES == 1 ? 5 : 3) * (D == 128 ? 1 : 2);
-    static constexpr int kLoadSlots = FP8 ? kRawSlots : kSlots;
+    static constexpr int kScale = 128 / D;
+    static constexpr int kKSlots = (FP8 ? 1 : 2) * kScale, kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
+    static constexpr int kRawK = !FP8 ? 0 : 2 * kScale, kRawV = !FP8 ? 0 : (TILES == 1 ? 2 : 1) * kScale;
     static constexpr int kQOff = 0;
-    static constexpr int kSlotOff = kQOff + TILES * kQTile;
-    static constexpr int kRawOff = kSlotOff + kSlots * kSlot;
-    static constexpr int kBarOff = kRawOff + kRawSlots * kRawSlot;
+    static constexpr int kKOff = kQOff + TILES * kQTile;
+    static constexpr int kVOff = kKOff + kKSlots * kSlot;
+    static constexpr int kRawOff = kVOff + kVSlots * kSlot;
+    static constexpr int kBarOff = kRawOff + (kRawK + kRawV) * kRawSlot;
+    static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
+    static constexpr int kKLoadOff = FP8 ? kRawOff : kKOff;
+    static constexpr int kVLoadOff = FP8 ? kRawOff + kRawK * kRawSlot : kVOff;
     // barriers
-    static constexpr int B_FULL = 0;                         // + load slot: the copies have landed
-    static constexpr int B_EMPTY = B_FULL + kLoadSlots;      // + load slot: it may be refilled
-    static constexpr int B_WIDE = B_EMPTY + kLoadSlots;      // + slot: widened (FP8)
-    static constexpr int B_WFREE = B_WIDE + (FP8 ? kSlots : 0);  // + slot: the MMAs have read it
-    static constexpr int B_FIX = B_WFREE + (FP8 ? kSlots : 0);   // + slot: V rows fixed (bf16)
-    static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kSlots);   // Q and the tree of a segment
+    static constexpr int kKL = FP8 ? kRawK : kKSlots, kVL = FP8 ? kRawV : kVSlots;
+    static constexpr int B_KFULL = 0;                        // + slot: K has landed
+    static constexpr int B_KEMPTY = B_KFULL + kKL;           // + slot: it may be refilled
+    static constexpr int B_VFULL = B_KEMPTY + kKL;
+    static constexpr int B_VEMPTY = B_VFULL + kVL;
+    static constexpr int B_KWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
+    static constexpr int B_KWFREE = B_KWIDE + (FP8 ? kKSlots : 0);
+    static constexpr int B_VWIDE = B_KWFREE + (FP8 ? kKSlots : 0);
+    static constexpr int B_VWFREE = B_VWIDE + (FP8 ? kVSlots : 0);
+    static constexpr int B_FIX = B_VWFREE + (FP8 ? kVSlots : 0);     // (bf16) + slot: V rows fixed
+    using KLoad = Ring<kKL, B_KFULL, B_KEMPTY>;              // the rings that TMA fills,
+    using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;
+    using KRing = Ring<kKSlots, FP8 ? B_KWIDE : B_KFULL, FP8 ? B_KWFREE : B_KEMPTY>;   // and the MMAs read
+    using VRing = Ring<kVSlots, FP8 ? B_VWIDE : B_VFULL, FP8 ? B_VWFREE : B_VEMPTY>;
+    static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kVSlots);  // Q and the tree of a segment
     static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
     static constexpr int B_SFULL = B_QFREE + 1;              // + stream
     static constexpr int B_PFULL = B_SFULL + 2;              // + stream
@@ -149,17 +159,26 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         constexpr int kReaders = TILES;          // MMA warps that read every slot
-        for (int i = 0; i < G::kLoadSlots; ++i) {
-            mbar_init(bar(G::B_FULL + i), 1);
-            mbar_init(bar(G::B_EMPTY + i), FP8 ? G::kPrepWarps : kReaders);
+        for (int i = 0; i < G::kKL; ++i) {
+            mbar_init(bar(G::B_KFULL + i), 1);
+            mbar_init(bar(G::B_KEMPTY + i), FP8 ? 2 : kReaders);
         }
-        if (FP8)
-            for (int i = 0; i < G::kSlots; ++i) {
-                mbar_init(bar(G::B_WIDE + i), G::kPrepWarps);
-                mbar_init(bar(G::B_WFREE + i), kReaders);
+        for (int i = 0; i < G::kVL; ++i) {
+            mbar_init(bar(G::B_VFULL + i), 1);
+            mbar_init(bar(G::B_VEMPTY + i), FP8 ? 2 : kReaders);
+        }
+        if (FP8) {
+            for (int i = 0; i < G::kKSlots; ++i) {
+                mbar_init(bar(G::B_KWIDE + i), 2);
+                mbar_init(bar(G::B_KWFREE + i), kReaders);
             }
-        else
-            for (int i = 0; i < G::kSlots; ++i) mbar_init(bar(G::B_FIX + i), 1);
+            for (int i = 0; i < G::kVSlots; ++i) {
+                mbar_init(bar(G::B_VWIDE + i), 2);
+                mbar_init(bar(G::B_VWFREE + i), kReaders);
+            }
+        } else {
+            for (int i = 0; i < G::kVSlots; ++i) mbar_init(bar(G::B_FIX + i), 1);
+        }
         mbar_init(bar(G::B_QFULL), G::kPrepWarps);
         mbar_init(bar(G::B_QFREE), 2);
         for (int w = 0; w < 2; ++w) {
@@ -173,7 +192,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         mbar_init(bar(G::B_ML), 8);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
-        misc[M_ISSUED] = 0;
+        misc[M_KISSUED] = 0;
+        misc[M_VISSUED] = 0;
         fence_mbar_init();
     }
     pdl_launch_dependents();
@@ -189,7 +209,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
     if (warp == 8) {
-        copy_role<G>(p, tm_k, tm_v, sb, misc, first_row, lane);
+        copy_role<G, 2>(p, tm_k, tm_v, sb, misc, first_row, lane);
     } else if (warp == 9 || warp == 10) {
         // --------------------------------------------------------------- MMAs
         if (lane == 0) {
@@ -197,13 +217,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             const uint32_t tS = tmem + (uint32_t)(128 * st), tO = tmem + 256u + (uint32_t)(128 * st);
             const uint64_t qdesc =
                 umma::smem_desc_sw128(sb + G::kQOff + (TILES == 2 ? st * G::kQTile : 0), 16, 1024);
-            const uint64_t sdesc = umma::smem_desc_sw128(sb + G::kSlotOff, 16, 1024);
-            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kSlotOff, kRegion, 1024);
+            const uint64_t sdesc = umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
+            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
             constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(kTile, D, false, true)
                                               : umma::idesc_bf16_f32(kTile, D, false, true);
-            const int full0 = FP8 ? G::B_WIDE : G::B_FULL, free0 = FP8 ? G::B_WFREE : G::B_EMPTY;
+            using KR = typename G::KRing;
+            using VR = typename G::VRing;
             uint32_t fix_parity = 0;             // bit slot: parity of its next fix
-            int x0 = 0, pc = 0;                  // first half of the segment; chunks of the stream
+            int g0 = 0, pc = 0;                  // first chunk of the segment; chunks of the stream
             bool ok = true;
             if (p.test_stall > 0 && misc[M_CNT] > 0 &&
                 !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
@@ -220,20 +241,17 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                   w.q.n * p.G - first_row <= kTile;
                 bool first = true;
                 for (int c = 0; ok && c < nc; ++c) {
-                    const int kx = k_half(x0, c), vx = v_half(x0, c, nc);
-                    const int ks = kx % G::kSlots, vs = vx % G::kSlots;
-                    const uint32_t kp = (uint32_t)((kx / G::kSlots) & 1);
-                    const uint32_t vp = (uint32_t)((vx / G::kSlots) & 1);
+                    const int g = g0 + c, ks = KR::slot(g), vs = VR::slot(g);
                     const bool fix = !FP8 && w.drafted(c);
                     const uint32_t fixp = (fix_parity >> vs) & 1u;
                     if (fix) fix_parity ^= 1u << vs;
                     if (TILES == 1 && (c & 1) != st) continue;
-                    ok = wait_issued(kx, misc) && wait_bar(bar(full0 + ks), kp, misc);
+                    ok = wait_issued(M_KISSUED, g, misc) && wait_bar(bar(KR::full(g)), KR::parity(g), misc);
                     if (!ok) break;
                     if (idle) {
-                        mbar_arrive(bar(free0 + ks));
-                        ok = wait_issued(vx, misc) && wait_bar(bar(full0 + vs), vp, misc);
-                        if (ok) mbar_arrive(bar(free0 + vs));
+                        mbar_arrive(bar(KR::free(g)));
+                        ok = wait_issued(M_VISSUED, g, misc) && wait_bar(bar(VR::full(g)), VR::parity(g), misc);
+                        if (ok) mbar_arrive(bar(VR::free(g)));
                         continue;
                     }
                     const int np = w.chunk_pages(c);
@@ -253,11 +271,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                     umma::commit(bar(G::B_SFULL + st));
-                    umma::commit(bar(free0 + ks));
+                    umma::commit(bar(KR::free(g)));
                     if (c + chunk_step(TILES) >= nc) umma::commit(bar(G::B_QFREE));
                     ok = wait_bar(bar(G::B_PFULL + st), (uint32_t)(pc & 1), misc);
                     if (!ok) break;
-                    ok = wait_issued(vx, misc) && wait_bar(bar(full0 + vs), vp, misc);
+                    ok = wait_issued(M_VISSUED, g, misc) && wait_bar(bar(VR::full(g)), VR::parity(g), misc);
                     if (ok && fix) ok = wait_bar(bar(G::B_FIX + vs), fixp, misc);
                     if (ok && first && seg > 0)
                         ok = wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc);
@@ -274,14 +292,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                             if (LOW) umma::mma_bf16_ts(tO, a + 16u, b, idesc_pv, true);
                         }
                     }
-                    umma::commit(bar(free0 + vs));
+                    umma::commit(bar(VR::free(g)));
                     umma::commit(bar(G::B_PVDONE + st));
                     first = false;
                     ok = wait_bar(bar(G::B_PVDONE + st), (uint32_t)(pc & 1), misc);
                     ++pc;
                 }
                 if (!ok) break;
-                x0 += 2 * nc;
+                g0 += nc;
                 // a stream without a chunk arrives for both; not before the other
                 // stream has for the segment before
                 if (first) {
@@ -301,7 +319,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
     } else if (warp >= G::kPrepWarp) {
         // ------------------------- queries, trees, V rows, and widening (E4M3)
         const int pw = warp - G::kPrepWarp;
-        int x0 = 0;
+        int g0 = 0;
         bool ok = true;
         for (Walk w(p, misc, first_row); ok && w.more(); w.next(p, first_row)) {
             const int seg = w.seg, buf = seg & 1, nc = w.chunks(), n = w.q.n;
@@ -339,10 +357,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(G::B_QFULL));
             if constexpr (FP8)
-                ok = widen<G>(p, w, sb, gb, misc, x0, pw, lane);
+                ok = widen<G>(p, w, sb, gb, misc, g0, pw, lane);
             else
-                ok = fix_values<G>(p, w, sb, gb, misc, x0, lane);
-            x0 += 2 * nc;
+                ok = fix_values<G>(p, w, sb, gb, misc, g0, lane);
+            g0 += nc;
         }
         if (!FP8) cp_async_wait_all();
     } else {

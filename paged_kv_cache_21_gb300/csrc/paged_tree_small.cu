@@ -13,15 +13,16 @@
 // to arrive at 6.8 TB/s over 152 SMs (E4M3: ~1220): HBM is the bound.
 //
 // How (the rest as in paged_tree.cu):
-//  * One thread per key of a chunk weighs that key for every row, so the
-//    exponentials of few rows use all lanes.  Two groups of four warps take the
-//    chunks in turn, each with its own accumulator O^T (columns 4 N + w PW of
-//    tensor memory) and references; the score products run up to three chunks
-//    ahead (four S^T buffers).
+//  * One thread per key of a chunk weighs that key for 32 rows, so the
+//    exponentials of few rows use all lanes, and a row's sum stays in a register
+//    of each lane until the end.  Two groups of four warps: up to 32 rows (N = 32)
+//    they take the chunks in turn, each with its own accumulator O^T and
+//    references; above (N = 64) each takes 32 rows of every chunk.  The score
+//    products run up to three chunks ahead (four S^T buffers).
 //  * The reference maximum of a row moves only when a score is more than 2^8
-//    above it (the four warps agree on that once per chunk, through an mbarrier);
-//    the first chunk of a segment sets it.  Then, seldom, the columns of O^T and
-//    the sums are scaled.
+//    above it (the four warps of a group agree on that once per chunk); the first
+//    chunk of a segment sets it.  Then, seldom, the columns of O^T and the sums
+//    are scaled.
 //  * D < 128: the lower lanes of O^T hold the result, the upper ones products of
 //    whatever follows V in shared memory, never read.
 #include <cuda_runtime.h>
@@ -40,7 +41,7 @@ template <int D, bool FP8, int N>
 struct SmallGeo {
     static constexpr int kD = D;
     static constexpr bool kFp8 = FP8;
-    static constexpr int kPrepWarp = 10;                     // first of the prep / widening warps
+    static constexpr int kPrepWarp = 11;                     // first of the prep / widening warps
     static constexpr int kPrepWarps = FP8 ? 4 : 1;
     static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
     static constexpr int kBoxes = D / 64;
@@ -51,30 +52,44 @@ struct SmallGeo {
     // then the low parts.  64 rows of an E4M3 cache go without: f16's 11 bits
     // against the cache's 4, and the room goes to the rings.
     static constexpr bool kLow = !(FP8 && N == 64);
+    static constexpr bool kSplit = N == 64;                  // the groups split the rows, not the chunks
+    static constexpr int kAccs = kSplit ? 1 : 2;             // accumulators
     static constexpr int kPW = kLow ? 2 * N : N;
     static constexpr int kPBuf = kPW / 64 * kRegion;         // [column group of 64][128 keys][128 B]
     static constexpr int kQBytes = kBoxes * N * 128;
-    static constexpr int kSlots = (FP8 ? 3 : N == 32 ? 5 : 4) * (128 / D);
-    static constexpr int kRawSlots = !FP8 ? 0 : 4 * (128 / D);
-    static constexpr int kLoadSlots = FP8 ? kRawSlots : kSlots;
+    static constexpr int kScale = 128 / D;
+    static constexpr int kKSlots = (FP8 ? 1 : 2) * kScale, kVSlots = (FP8 || N == 64 ? 2 : 3) * kScale;
+    static constexpr int kRawSlots = !FP8 ? 0 : 2 * kScale;  // of K and of V
     static constexpr int kQOff = 0;
-    static constexpr int kSlotOff = (kQOff + kQBytes + 1023) / 1024 * 1024;
-    static constexpr int kPOff = kSlotOff + kSlots * kSlot;  // two buffers (behind the ring: see D < 128)
+    static constexpr int kKOff = (kQOff + kQBytes + 1023) / 1024 * 1024;
+    static constexpr int kVOff = kKOff + kKSlots * kSlot;
+    static constexpr int kPOff = kVOff + kVSlots * kSlot;    // two buffers (behind the ring: see D < 128)
     static constexpr int kRawOff = kPOff + 2 * kPBuf;
-    static constexpr int kBarOff = kRawOff + kRawSlots * kRawSlot;
+    static constexpr int kBarOff = kRawOff + 2 * kRawSlots * kRawSlot;
+    static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
+    static constexpr int kKLoadOff = FP8 ? kRawOff : kKOff;
+    static constexpr int kVLoadOff = FP8 ? kRawOff + kRawSlots * kRawSlot : kVOff;
     // barriers
-    static constexpr int B_FULL = 0;                         // + load slot: the copies have landed
-    static constexpr int B_EMPTY = B_FULL + kLoadSlots;      // + load slot: it may be refilled
-    static constexpr int B_WIDE = B_EMPTY + kLoadSlots;      // + slot: widened (FP8)
-    static constexpr int B_WFREE = B_WIDE + (FP8 ? kSlots : 0);  // + slot: the MMAs have read it
-    static constexpr int B_FIX = B_WFREE + (FP8 ? kSlots : 0);   // + slot: V rows fixed (bf16)
-    static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kSlots);   // Q and the tree of a segment
+    static constexpr int kKL = FP8 ? kRawSlots : kKSlots, kVL = FP8 ? kRawSlots : kVSlots;
+    static constexpr int B_KFULL = 0;                        // + slot: K has landed
+    static constexpr int B_KEMPTY = B_KFULL + kKL;           // + slot: it may be refilled
+    static constexpr int B_VFULL = B_KEMPTY + kKL;
+    static constexpr int B_VEMPTY = B_VFULL + kVL;
+    static constexpr int B_KWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
+    static constexpr int B_KWFREE = B_KWIDE + (FP8 ? kKSlots : 0);
+    static constexpr int B_VWIDE = B_KWFREE + (FP8 ? kKSlots : 0);
+    static constexpr int B_VWFREE = B_VWIDE + (FP8 ? kVSlots : 0);
+    static constexpr int B_FIX = B_VWFREE + (FP8 ? kVSlots : 0);     // (bf16) + slot: V rows fixed
+    using KLoad = Ring<kKL, B_KFULL, B_KEMPTY>;              // the rings that TMA fills,
+    using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;
+    using KRing = Ring<kKSlots, FP8 ? B_KWIDE : B_KFULL, FP8 ? B_KWFREE : B_KEMPTY>;   // and the MMAs read
+    using VRing = Ring<kVSlots, FP8 ? B_VWIDE : B_VFULL, FP8 ? B_VWFREE : B_VEMPTY>;
+    static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kVSlots);  // Q and the tree of a segment
     static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
     static constexpr int B_SFULL = B_QFREE + 1;              // + buffer (4): scores
-    static constexpr int B_PFULL = B_SFULL + 4;              // + group: weights written
-    static constexpr int B_PVDONE = B_PFULL + 2;             // + group: their products are done
-    static constexpr int B_VOTE = B_PVDONE + 2;              // + group: its four warps agree
-    static constexpr int B_OFULL = B_VOTE + 2;               // both accumulators are complete
+    static constexpr int B_PFULL = B_SFULL + 4;              // + buffer of P: weights written
+    static constexpr int B_PVDONE = B_PFULL + 2;             // + buffer of P: their products are done
+    static constexpr int B_OFULL = B_PVDONE + 2;             // the accumulators are complete
     static constexpr int B_OFREE = B_OFULL + 1;              // + segment & 1: they have been read
     static constexpr int B_JOIN = B_OFREE + 2;               // the eight warps meet
     static constexpr int B_END = B_JOIN + 1;                 // all MMAs are done
@@ -86,19 +101,19 @@ struct SmallGeo {
     static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
     static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
     static constexpr int kQfacOff = kBadOff + 2 * kPrepWarps * 16;   // [2][N] floats (FP8)
-    static constexpr int kSnOff = kQfacOff + 2 * N * 4;      // [group][N] float2: (scale, -reference)
-    static constexpr int kRefOff = kSnOff + 2 * N * 8;       // [group][N] floats: the reference
-    static constexpr int kAlphaOff = kRefOff + 2 * N * 4;    // [group][N] floats
-    static constexpr int kWmaxOff = kAlphaOff + 2 * N * 4;   // [group][4][N] floats: maxima, later sums
-    static constexpr int kFacOff = kWmaxOff + 8 * N * 4;     // [N] float4
-    static constexpr int kRowOff = kFacOff + N * 16;         // [N] words: (node, head) of a row
-    static constexpr int kVoteOff = kRowOff + N * 4;         // [group][4] words, then [group][2]
-    static constexpr int kEnd = kVoteOff + 64;
+    static constexpr int kSnOff = kQfacOff + 2 * N * 4;      // [group][32] float2: (scale, -reference)
+    static constexpr int kRefOff = kSnOff + 64 * 8;          // [group][32] floats: the reference
+    static constexpr int kAlphaOff = kRefOff + 64 * 4;       // [group][32] floats
+    static constexpr int kWmaxOff = kAlphaOff + 64 * 4;      // [group][4][32] floats: maxima, later sums
+    static constexpr int kFacOff = kWmaxOff + 256 * 4;       // [N] float4
+    static constexpr int kRowOff = kFacOff + N * 16;         // [N] words: place of a row's result
+    static constexpr int kUnsetOff = kRowOff + N * 4;        // [group] words
+    static constexpr int kEnd = kUnsetOff + 16;
     static constexpr int kSmem = kEnd + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
     // tensor memory: S^T buffers, then the accumulators
     static constexpr uint32_t kColO = 4 * N;
-    static constexpr uint32_t kTmemCols = 4 * N + 2 * kPW <= 256 ? 256 : 512;
+    static constexpr uint32_t kTmemCols = 4 * N + kAccs * kPW <= 256 ? 256 : 512;
 };
 
 // Order-preserving map of floats to ints (NaN aside).
@@ -145,25 +160,33 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (tid == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        for (int i = 0; i < G::kLoadSlots; ++i) {
-            mbar_init(bar(G::B_FULL + i), 1);
-            mbar_init(bar(G::B_EMPTY + i), FP8 ? G::kPrepWarps : 1);
+        // (a slot of codes is freed by its two widening warps, which also fill)
+        for (int i = 0; i < G::kKL; ++i) {
+            mbar_init(bar(G::B_KFULL + i), 1);
+            mbar_init(bar(G::B_KEMPTY + i), FP8 ? 2 : 1);
         }
-        for (int i = 0; i < G::kSlots; ++i) {
-            if (FP8) {
-                mbar_init(bar(G::B_WIDE + i), G::kPrepWarps);
-                mbar_init(bar(G::B_WFREE + i), 1);
-            } else {
-                mbar_init(bar(G::B_FIX + i), 1);
+        for (int i = 0; i < G::kVL; ++i) {
+            mbar_init(bar(G::B_VFULL + i), 1);
+            mbar_init(bar(G::B_VEMPTY + i), FP8 ? 2 : 1);
+        }
+        if (FP8) {
+            for (int i = 0; i < G::kKSlots; ++i) {
+                mbar_init(bar(G::B_KWIDE + i), 2);
+                mbar_init(bar(G::B_KWFREE + i), 1);
             }
+            for (int i = 0; i < G::kVSlots; ++i) {
+                mbar_init(bar(G::B_VWIDE + i), 2);
+                mbar_init(bar(G::B_VWFREE + i), 1);
+            }
+        } else {
+            for (int i = 0; i < G::kVSlots; ++i) mbar_init(bar(G::B_FIX + i), 1);
         }
         mbar_init(bar(G::B_QFULL), G::kPrepWarps);
         mbar_init(bar(G::B_QFREE), 1);
         for (int i = 0; i < 4; ++i) mbar_init(bar(G::B_SFULL + i), 1);
         for (int w = 0; w < 2; ++w) {
-            mbar_init(bar(G::B_PFULL + w), 4);
+            mbar_init(bar(G::B_PFULL + w), G::kSplit ? 8 : 4);
             mbar_init(bar(G::B_PVDONE + w), 1);
-            mbar_init(bar(G::B_VOTE + w), 4);
             mbar_init(bar(G::B_OFREE + w), 8);
         }
         mbar_init(bar(G::B_OFULL), 1);
@@ -171,13 +194,13 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         mbar_init(bar(G::B_END), 1);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
-        misc[M_ISSUED] = 0;
+        misc[M_KISSUED] = 0;
+        misc[M_VISSUED] = 0;
         fence_mbar_init();
     }
-    if (tid < 16) reinterpret_cast<volatile int*>(gb + G::kVoteOff)[tid] = 0;
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == 9) {
+    if (warp == 10) {
         umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, G::kTmemCols);
         umma::tmem_relinquish();
     }
@@ -188,19 +211,22 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
     if (warp == 8) {
-        copy_role<G>(p, tm_k, tm_v, sb, misc, 0, lane);
+        copy_role<G, 0>(p, tm_k, tm_v, sb, misc, 0, lane);
     } else if (warp == 9) {
+        copy_role<G, 1>(p, tm_k, tm_v, sb, misc, 0, lane);
+    } else if (warp == 10) {
         // --------------------------------------------------------------- MMAs
         if (lane == 0) {
             const uint64_t qdesc = umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
-            const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kSlotOff, 16, 1024);
-            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kSlotOff, kRegion, 1024);
+            const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
+            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
             const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, kRegion, 1024);
             constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, N, false, false)
                                              : umma::idesc_bf16_f32(128, N, false, false);
             constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(128, G::kPW, true, true)
                                               : umma::idesc_bf16_f32(128, G::kPW, true, true);
-            constexpr int full0 = FP8 ? G::B_WIDE : G::B_FULL, free0 = FP8 ? G::B_WFREE : G::B_EMPTY;
+            using KR = typename G::KRing;
+            using VR = typename G::VRing;
             uint32_t fix_parity = 0;             // bit slot: parity of its next fix
             int g0 = 0;                          // first chunk of the segment
             bool ok = true;
@@ -220,15 +246,14 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // been waited for when chunk c >= g - 3 comes
                 auto scores_up_to = [&](int c) -> bool {
                     for (; sc <= c + 3 && sc < nc; ++sc) {
-                        const int g = g0 + sc, x = k_half(2 * g0, sc), ks = x % G::kSlots;
-                        const uint32_t parity = (uint32_t)((x / G::kSlots) & 1);
+                        const int g = g0 + sc;
                         if (sc > c) {
-                            if (misc[M_ISSUED] <= x || !mbar_test(bar(full0 + ks), parity)) break;
-                        } else if (!(wait_issued(x, misc) && wait_bar(bar(full0 + ks), parity, misc))) {
+                            if (misc[M_KISSUED] <= g || !mbar_test(bar(KR::full(g)), KR::parity(g))) break;
+                        } else if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) {
                             return false;
                         }
                         umma::fence_after_sync();
-                        const uint64_t kd = kdesc + (uint64_t)((ks * G::kSlot) >> 4);
+                        const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kSlot) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             umma::mma_bf16_ss(tmem + (uint32_t)(N * (g & 3)),
@@ -236,34 +261,34 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                                               qdesc + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
                                               idesc_s, kk > 0);
                         umma::commit(bar(G::B_SFULL + (g & 3)));
-                        umma::commit(bar(free0 + ks));
+                        umma::commit(bar(KR::free(g)));
                         if (sc + 1 == nc) umma::commit(bar(G::B_QFREE));
                     }
                     return true;
                 };
                 for (int c = 0; ok && c < nc; ++c) {
-                    const int g = g0 + c, x = v_half(2 * g0, c, nc), vs = x % G::kSlots, grp = g & 1;
-                    ok = scores_up_to(c) && wait_bar(bar(G::B_PFULL + grp), (uint32_t)((g >> 1) & 1), misc) &&
-                         wait_issued(x, misc) &&
-                         wait_bar(bar(full0 + vs), (uint32_t)((x / G::kSlots) & 1), misc);
+                    const int g = g0 + c, vs = VR::slot(g), pbuf = g & 1;
+                    ok = scores_up_to(c) && wait_bar(bar(G::B_PFULL + pbuf), (uint32_t)((g >> 1) & 1), misc) &&
+                         wait_bar(bar(VR::full(g)), VR::parity(g), misc);
                     if (ok && !FP8 && w.drafted(c)) {
                         ok = wait_bar(bar(G::B_FIX + vs), (fix_parity >> vs) & 1u, misc);
                         fix_parity ^= 1u << vs;
                     }
                     // the accumulators of the segment before have been read
-                    if (ok && c < 2 && seg > 0)
+                    if (ok && c < G::kAccs && seg > 0)
                         ok = wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc);
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
-                    const uint64_t pd = pdesc + (uint64_t)((grp * G::kPBuf) >> 4);
+                    const uint64_t pd = pdesc + (uint64_t)((pbuf * G::kPBuf) >> 4);
                     const int np = w.chunk_pages(c);
                     for (int kk = 0; kk < np; ++kk)
-                        umma::mma_bf16_ss(tmem + G::kColO + (uint32_t)(grp * G::kPW),
+                        umma::mma_bf16_ss(tmem + G::kColO + (uint32_t)(G::kSplit ? 0 : pbuf * G::kPW),
                                           vd + (uint64_t)((kk * kBlock * 128) >> 4),
-                                          pd + (uint64_t)((kk * kBlock * 128) >> 4), idesc_pv, !(c < 2 && kk == 0));
-                    umma::commit(bar(free0 + vs));
-                    umma::commit(bar(G::B_PVDONE + grp));
+                                          pd + (uint64_t)((kk * kBlock * 128) >> 4), idesc_pv,
+                                          !(c < G::kAccs && kk == 0));
+                    umma::commit(bar(VR::free(g)));
+                    umma::commit(bar(G::B_PVDONE + pbuf));
                     if (c + 1 == nc) umma::commit(bar(G::B_OFULL));
                 }
                 g0 += nc;
@@ -276,7 +301,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     } else if (warp >= G::kPrepWarp) {
         // ------------------------- queries, trees, V rows, and widening (E4M3)
         const int pw = warp - G::kPrepWarp;
-        int x0 = 0;
+        int g0 = 0;
         bool ok = true;
         for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
             const int seg = w.seg, buf = seg & 1;
@@ -312,37 +337,39 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(G::B_QFULL));
             if constexpr (FP8)
-                ok = widen<G>(p, w, sb, gb, misc, x0, pw, lane);
+                ok = widen<G>(p, w, sb, gb, misc, g0, pw, lane);
             else
-                ok = fix_values<G>(p, w, sb, gb, misc, x0, lane);
-            x0 += 2 * w.chunks();
+                ok = fix_values<G>(p, w, sb, gb, misc, g0, lane);
+            g0 += w.chunks();
         }
         if (!FP8) cp_async_wait_all();
     } else {
         // ------------------------------------------------- weights and output
         const int grp = warp >> 2, key = tid & 127, wq = warp & 3;
+        const int row0 = G::kSplit ? 32 * grp : 0;       // the group's first row
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-        const uint32_t tO = lanes + G::kColO + (uint32_t)(grp * G::kPW);
-        float2* sn = reinterpret_cast<float2*>(gb + G::kSnOff) + grp * N;
-        float* ref = reinterpret_cast<float*>(gb + G::kRefOff) + grp * N;
-        float* alphas = reinterpret_cast<float*>(gb + G::kAlphaOff) + grp * N;
-        float* wmax = reinterpret_cast<float*>(gb + G::kWmaxOff) + grp * 4 * N;
-        volatile int* vote = reinterpret_cast<volatile int*>(gb + G::kVoteOff) + grp * 4;
-        volatile int* unset = reinterpret_cast<volatile int*>(gb + G::kVoteOff) + 8 + grp * 2;
-        const uint32_t pb = sb + (uint32_t)(G::kPOff + grp * G::kPBuf + key * 128);
+        // the group's columns of its accumulator; the low parts are N further on
+        const uint32_t tO = lanes + G::kColO + (uint32_t)(G::kSplit ? row0 : grp * G::kPW);
+        float2* sn = reinterpret_cast<float2*>(gb + G::kSnOff) + grp * 32;
+        float* ref = reinterpret_cast<float*>(gb + G::kRefOff) + grp * 32;
+        float* alphas = reinterpret_cast<float*>(gb + G::kAlphaOff) + grp * 32;
+        float* wmax = reinterpret_cast<float*>(gb + G::kWmaxOff) + grp * 128;
+        volatile int* unset = reinterpret_cast<volatile int*>(gb + G::kUnsetOff) + grp;
         if (p.tidy) zero_empty(p, D, cta, p.nctas, tid, 256);
         if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
-        int votes = 0, joins = 0, g0 = 0, flat = misc[M_B0];
+        int joins = 0, g0 = 0, flat = misc[M_B0];
         bool ok = true;
-        // the group's four warps meet
-        auto meet = [&]() -> bool {
-            // (the word of the vote after next: its last readers have all met since)
-            if (wq == 0 && lane == 0) vote[(votes + 2) & 3] = 0;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(G::B_VOTE + grp));
-            const bool r = wait_warp(bar(G::B_VOTE + grp), (uint32_t)(votes & 1), misc);
-            ++votes;
-            return r;
+        // The group's four warps meet: is `x` true anywhere?  Every warp comes to every
+        // meeting, also one whose waits have run out, which the others learn there.
+        auto meet = [&](bool x) -> bool {
+            int r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+                "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"(1 + grp), "r"(x ? 1 : 0)
+                : "memory");
+            return r != 0;
         };
         auto join = [&]() -> bool {
             __syncwarp();
@@ -356,203 +383,175 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int rows = w.q.n * p.G;
             const uint32_t* anc = reinterpret_cast<const uint32_t*>(gb + G::kAncOff) + buf * kN * 4;
             const volatile uint32_t* padw = reinterpret_cast<const volatile uint32_t*>(gb + G::kPadOff) + buf * 4;
-            // sums: of up to 32 rows in a register each, of 64 rows in lanes (column_sums)
-            constexpr int kSums = N == 32 ? 32 : 2;
-            float l[kSums];
+            float l[32];                         // each row's sum over this thread's keys
 #pragma unroll
-            for (int k = 0; k < kSums; ++k) l[k] = 0.f;
+            for (int k = 0; k < 32; ++k) l[k] = 0.f;
             bool first = true;
-            for (int c = (g0 ^ grp) & 1; c < nc; c += 2) {
+            for (int c = G::kSplit ? 0 : (g0 ^ grp) & 1; c < nc; c += G::kSplit ? 1 : 2) {
                 const int g = g0 + c;
-                ok = wait_warp(bar(G::B_SFULL + (g & 3)), (uint32_t)((g >> 2) & 1), misc);
-                if (!ok) break;
+                ok = ok && wait_warp(bar(G::B_SFULL + (g & 3)), (uint32_t)((g >> 2) & 1), misc);
                 if (first) {
                     // the rows' scale and reference: none yet for rows that see
                     // something, and never a weight for the others
-                    if (key < N) {
-                        const int nd = key < rows ? row_node(p, key) : 0;
-                        const bool live = key < rows && !((padw[nd >> 5] >> (nd & 31)) & 1u);
-                        const float f = FP8 && live ? reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + key] : 1.f;
-                        sn[key] = live ? make_float2(p.sl2 * f, 0.f) : make_float2(0.f, -INFINITY);
-                        ref[key] = -INFINITY;
+                    if (wq == 0) {
+                        const int r = row0 + lane, nd = r < rows ? row_node(p, r) : 0;
+                        const bool live = r < rows && !((padw[nd >> 5] >> (nd & 31)) & 1u);
+                        const float f = FP8 && live ? reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + r] : 1.f;
+                        sn[lane] = live ? make_float2(p.sl2 * f, 0.f) : make_float2(0.f, -INFINITY);
+                        ref[lane] = -INFINITY;
                         const bool any = __any_sync(kFull, live);
-                        if (lane == 0) unset[wq] = any;
+                        if (lane == 0) *unset = any;
                     }
-                    if (N == 32 && key == 32) unset[1] = 0;
-                    ok = meet();
-                    if (!ok) break;
+                    if (meet(!ok)) ok = false;
                 }
                 umma::fence_after_sync();
-                const uint32_t tS = lanes + (uint32_t)(N * (g & 3));
+                const uint32_t tS = lanes + (uint32_t)(N * (g & 3) + row0);
                 const int np = w.chunk_pages(c), pos = (w.j + c * kPages) * kBlock + key;
                 // the rows that see this key, as bits
-                uint32_t vis[N / 32];
-#pragma unroll
-                for (int q = 0; q < N / 32; ++q) vis[q] = key < np * kBlock && pos < w.q.L ? ~0u : 0u;
-                if (w.drafted(c) && pos >= w.q.base && vis[0]) {
+                uint32_t vis = key < np * kBlock && pos < w.q.L ? ~0u : 0u;
+                if (w.drafted(c) && pos >= w.q.base && vis) {
                     const int a = pos - w.q.base;
-#pragma unroll
-                    for (int q = 0; q < N / 32; ++q) {
-                        uint32_t v = 0u;
-                        for (int r = 32 * q; r < min(rows, 32 * q + 32); ++r)
-                            v |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - 32 * q);
-                        vis[q] = v;
-                    }
+                    vis = 0u;
+                    for (int r = row0; r < min(rows, row0 + 32); ++r)
+                        vis |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - row0);
                 }
                 const bool masked = w.drafted(c) || np < kPages;     // (for the whole chunk)
-                // the scores of 32 rows relative to the references, in log2 units.  (64
-                // rows are loaded twice, 32 at a time: half the registers)
+                // the scores relative to the references, in log2 units
                 float t[32];
-                auto load = [&](int q) {
-                    umma::tmem_ld32(tS + (uint32_t)(32 * q), *reinterpret_cast<uint32_t(*)[32]>(&t[0]));
+                auto load = [&]() {
+                    umma::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&t[0]));
                     umma::tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        const float4 f = *reinterpret_cast<const float4*>(sn + 32 * q + k);   // two rows
+                        const float4 f = *reinterpret_cast<const float4*>(sn + k);   // two rows
                         t[k] = fmaf(t[k], f.x, f.y);
                         t[k + 1] = fmaf(t[k + 1], f.z, f.w);
                     }
                     if (masked) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) t[k] = (vis[q] >> k) & 1u ? t[k] : -INFINITY;
+                        for (int k = 0; k < 32; ++k) t[k] = (vis >> k) & 1u ? t[k] : -INFINITY;
                     }
                 };
-                float mx = -INFINITY;
+                load();
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int q = 0; q < N / 32; ++q) {
-                    load(q);
-                    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], t[k]);
-                    mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
-                }
-                // does any row's reference lag too far behind?
-                {
-                    const int slot = votes & 3;
-                    const bool any = __any_sync(kFull, mx > kMaxLag + (FP8 ? kBiasF16 : 0.f));
-                    if (any && lane == 0) vote[slot] = 1;
-                    ok = meet();
-                    if (!ok) break;
-                    const bool need = vote[slot] != 0 || unset[0] != 0 || unset[1] != 0;
-                    if (need) {
-                        // ---- new references: the largest score of each row in the chunk
-#pragma unroll
-                        for (int q = 0; q < N / 32; ++q) {
-                            int best = INT32_MIN;
-                            if (N > 32) load(q);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                // (relative to the old reference, or to none)
-                                const int m = __reduce_max_sync(kFull, ordered(t[k]));
-                                if (lane == k) best = m;
-                            }
-                            wmax[wq * N + 32 * q + lane] = unordered(best);
-                        }
-                        ok = meet();
-                        if (!ok) break;
-                        if (key < N) {
-                            const float rel = fmaxf(fmaxf(wmax[key], wmax[N + key]), fmaxf(wmax[2 * N + key], wmax[3 * N + key]));
-                            const float2 f = sn[key];
-                            const float old = ref[key];
-                            const bool live = f.y != -INFINITY;
-                            // rel = score * scale + f.y, with f.y = bias - reference, or 0 for none
-                            const float best = old == -INFINITY ? rel : rel - f.y;
-                            float a = 1.f;
-                            if (live && (old == -INFINITY ? best > -INFINITY : best > old + kMaxLag)) {
-                                a = old == -INFINITY ? 0.f : ex2(old - best);
-                                ref[key] = best;
-                                sn[key].y = (FP8 ? kBiasF16 : 0.f) - best;
-                            }
-                            alphas[key] = a;
-                            const bool left = __any_sync(kFull, live && ref[key] == -INFINITY);
-                            if (lane == 0) unset[wq] = left;
-                        }
-                        ok = meet();
-                        if (!ok) break;
-                        if (!first) {
-                            // what has been accumulated follows, once the products of the
-                            // group's chunk before are done
-#pragma unroll
-                            for (int k = 0; k < kSums; ++k) l[k] *= alphas[N == 32 ? k : 32 * k + lane];
-                            ok = wait_warp(bar(G::B_PVDONE + grp), (uint32_t)(((g >> 1) - 1) & 1), misc);
-                            if (!ok) break;
-                            umma::fence_after_sync();
-#pragma unroll 1
-                            for (int c0 = 0; c0 < G::kPW; c0 += 16) {
-                                uint32_t o[16];
-                                umma::tmem_ld16(tO + (uint32_t)c0, o);
-                                umma::tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * alphas[(c0 + k) % N]);
-                                umma::tmem_st16(tO + (uint32_t)c0, o);
-                            }
-                            umma::tmem_wait_st();
-                        }
-                        if (N == 32) load(0);
+                for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], t[k]);
+                const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // does any row's reference lag too far behind, or has a wait run out?
+                if (meet(!ok || most > kMaxLag + (FP8 ? kBiasF16 : 0.f) || *unset != 0)) {
+                    if (meet(!ok)) {
+                        ok = false;
+                        break;
                     }
-                }
-                if (g >= 2) {
-                    // the group's buffer: the products of its chunk before are done
-                    ok = wait_warp(bar(G::B_PVDONE + grp), (uint32_t)(((g >> 1) - 1) & 1), misc);
-                    if (!ok) break;
-                }
-                first = false;
-                // ---- the weights
-                const bool store = key < np * kBlock;
-#pragma unroll
-                for (int q = 0; q < N / 32; ++q) {
-                    if (N > 32) load(q);
+                    // ---- new references: the largest score of each row in the chunk
+                    int best = INT32_MIN;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        t[k] = ex2(t[k]);
-                        if (N == 32) l[k] += t[k];
+                        // (relative to the old reference, or to none)
+                        const int m = __reduce_max_sync(kFull, ordered(t[k]));
+                        if (lane == k) best = m;
                     }
-                    if (store) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float a = t[k + 2 * e], b = t[k + 2 * e + 1];
-                                if (FP8) {
-                                    hi[e] = pack_f16x2(a, b);
-                                    const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
-                                    lo[e] = pack_f16x2(a - __low2float(h), b - __high2float(h));
-                                } else {
-                                    hi[e] = pack_bf16x2(a, b);
-                                    lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
-                                }
-                            }
-                            // 16 bytes: eight rows; the low parts N columns on
-                            const int ch = 4 * q + k / 8, cl = ch + N / 8;
-                            sts128(pb + (uint32_t)((ch >> 3) * kRegion + ((ch ^ key) & 7) * 16),
-                                   make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                            if (G::kLow)
-                                sts128(pb + (uint32_t)((cl >> 3) * kRegion + ((cl ^ key) & 7) * 16),
-                                       make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    wmax[wq * 32 + lane] = unordered(best);
+                    meet(false);
+                    if (wq == 0) {
+                        const float rel = fmaxf(fmaxf(wmax[lane], wmax[32 + lane]), fmaxf(wmax[64 + lane], wmax[96 + lane]));
+                        const float2 f = sn[lane];
+                        const float old = ref[lane];
+                        const bool live = f.y != -INFINITY;
+                        // rel = score * scale + f.y, with f.y = bias - reference, or 0 for none
+                        const float top = old == -INFINITY ? rel : rel - f.y;
+                        float a = 1.f;
+                        if (live && (old == -INFINITY ? top > -INFINITY : top > old + kMaxLag)) {
+                            a = old == -INFINITY ? 0.f : ex2(old - top);
+                            ref[lane] = top;
+                            sn[lane].y = (FP8 ? kBiasF16 : 0.f) - top;
                         }
+                        alphas[lane] = a;
+                        const bool left = __any_sync(kFull, live && ref[lane] == -INFINITY);
+                        if (lane == 0) *unset = left;
                     }
-                    if (N > 32) l[q] += column_sums(t, lane);
+                    if (!first) {
+                        // what has been accumulated follows, once the products under way
+                        // are done: those of the group's chunk before
+                        const int gb4 = G::kSplit ? g - 1 : g - 2;
+                        ok = wait_warp(bar(G::B_PVDONE + (gb4 & 1)), (uint32_t)((gb4 >> 1) & 1), misc);
+                    }
+                    if (meet(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!first) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) l[k] *= alphas[k];
+                        umma::fence_after_sync();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < (G::kLow ? 64 : 32); c0 += 16) {
+                            const uint32_t at = tO + (uint32_t)(c0 < 32 ? c0 : c0 - 32 + N);
+                            uint32_t o[16];
+                            umma::tmem_ld16(at, o);
+                            umma::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * alphas[(c0 & 16) + k]);
+                            umma::tmem_st16(at, o);
+                        }
+                        umma::tmem_wait_st();
+                    }
+                    load();
+                }
+                // ---- the weights
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    t[k] = ex2(t[k]);
+                    l[k] += t[k];
+                }
+                // the buffer: the products of the chunk before last are done.  (A wait
+                // that runs out is told at the next meeting; nothing is written then.)
+                if (g >= 2) ok = ok && wait_warp(bar(G::B_PVDONE + (g & 1)), (uint32_t)(((g >> 1) - 1) & 1), misc);
+                first = false;
+                if (ok && key < np * kBlock) {
+                    const uint32_t pb = sb + (uint32_t)(G::kPOff + (g & 1) * G::kPBuf + key * 128);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = t[k + 2 * e], b = t[k + 2 * e + 1];
+                            if (FP8) {
+                                hi[e] = pack_f16x2(a, b);
+                                const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
+                                lo[e] = pack_f16x2(a - __low2float(h), b - __high2float(h));
+                            } else {
+                                hi[e] = pack_bf16x2(a, b);
+                                lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
+                            }
+                        }
+                        // 16 bytes: eight rows; the low parts N columns on
+                        const int ch = (row0 + k) / 8, cl = ch + N / 8;
+                        sts128(pb + (uint32_t)((ch >> 3) * kRegion + ((ch ^ key) & 7) * 16),
+                               make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        if (G::kLow)
+                            sts128(pb + (uint32_t)((cl >> 3) * kRegion + ((cl ^ key) & 7) * 16),
+                                   make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    }
                 }
                 fence_proxy_async_smem();
                 umma::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(G::B_PFULL + grp));
+                if (ok && lane == 0) mbar_arrive(bar(G::B_PFULL + (g & 1)));
             }
+            // the group's warps go on together, or not at all
+            if (meet(!ok)) ok = false;
             if (!ok) break;
-            // ---- the segment's result: join the two groups' sums and accumulators
+            // ---- the segment's result: the sums, and both groups' accumulators
             ok = wait_warp(bar(G::B_OFULL), (uint32_t)(seg & 1), misc);
-            if (!ok) break;
             umma::fence_after_sync();
-            if constexpr (N == 32) {
-                wmax[wq * N + lane] = column_sums(*reinterpret_cast<float(*)[32]>(&l[0]), lane);
-            } else {
-                wmax[wq * N + lane] = l[0];
-                wmax[wq * N + 32 + lane] = l[1];
-            }
-            if (first && key < N) ref[key] = -INFINITY;      // no chunk of this group
+            wmax[wq * 32 + lane] = column_sums(l, lane);
+            if (first && wq == 0) ref[lane] = -INFINITY;     // no chunk of this group
+            if (meet(!ok)) ok = false;
+            if (!ok) break;
             ok = join();
+            if (meet(!ok)) ok = false;
             if (!ok) break;
             const bool whole = w.whole();
             const size_t slot = (size_t)cta * 2 + (w.j == 0 ? 1 : 0);
@@ -562,24 +561,27 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (tid < N) {
                 const float* base = reinterpret_cast<const float*>(gb + G::kWmaxOff);
                 const float* refs = reinterpret_cast<const float*>(gb + G::kRefOff);
-                float s[2], m[2];
+                float s[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float* b = base + q * 4 * N + tid;
-                    s[q] = (b[0] + b[N]) + (b[2 * N] + b[3 * N]);
-                    m[q] = refs[q * N + tid];
-                    if (m[q] == -INFINITY) s[q] = 0.f;
+                    if (G::kSplit && q != tid >> 5) continue;
+                    const float* b = base + q * 128 + (tid & 31);
+                    m[q] = refs[q * 32 + (tid & 31)];
+                    s[q] = m[q] == -INFINITY ? 0.f : (b[0] + b[32]) + (b[64] + b[96]);
                 }
                 const float M = fmaxf(m[0], m[1]);
                 const float a0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - M);
                 const float a1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - M);
                 const float L = s[0] * a0 + s[1] * a1;
-                fac[tid] = make_float4(a0, a1, whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
+                // (split rows: one accumulator, whose factor is in either place)
+                fac[tid] = make_float4(G::kSplit ? a0 + a1 : a0, a1,
+                                       whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
                 const int nd = row_node(p, tid);
                 rowat[tid] = whole ? (w.q.t0 + nd) * p.Hq + w.h * p.G + tid - nd * p.G : (int)(slot * N) + tid;
                 if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
             }
             ok = join();
+            if (meet(!ok)) ok = false;
             if (!ok) break;
             // drafted V elements that were zeroed as infinities or NaN
             const volatile uint32_t* badw = reinterpret_cast<const volatile uint32_t*>(gb + G::kBadOff) + buf * G::kPrepWarps * 4;
@@ -597,7 +599,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < G::kAccs; ++q) {
                         uint32_t low[16];
                         umma::tmem_ld16(t0 + (uint32_t)(q * G::kPW), o);
                         if (G::kLow) umma::tmem_ld16(t0 + (uint32_t)(q * G::kPW + N), low);
@@ -657,7 +659,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     umma::fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 10) {
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, G::kTmemCols);
     }

@@ -5,10 +5,8 @@
 //
 // A kernel's geometry G names its shared memory (offsets k..Off from a
 // 1024-byte aligned base) and its barriers (B_..); both kernels consume K and V
-// in chunks of up to 8 pages.  The K or V of a chunk is a "half"; half x of a CTA
-// lies in slot x % slots of a ring.  V is needed a softmax later than K, so the
-// halves of a segment come in the order K0 K1 V0 K2 V1 ... : no slot is held by a
-// V whose weights are not there yet while K could be loaded.
+// in chunks of up to 8 pages, chunk g of a CTA from slot g % slots of a ring of K
+// and of one of V (E4M3: rings of codes in front of rings of f16).
 #pragma once
 
 #include <cuda.h>
@@ -38,13 +36,10 @@ constexpr float kMaxLag = 8.f;                  // the reference maximum may lag
 // rounds to zero is below 2^-31 of the largest weight
 constexpr float kBiasF16 = 7.f;
 
-// The halves of chunk c of a segment of nc chunks whose first half is x0.
-__device__ __forceinline__ int k_half(int x0, int c) { return c == 0 ? x0 : x0 + 2 * c - 1; }
-__device__ __forceinline__ int v_half(int x0, int c, int nc) { return c == nc - 1 ? x0 + 2 * nc - 1 : x0 + 2 * c + 2; }
-
 // misc words: tensor-memory base; abort; the range: first unit, units, units per
-// CTA, first sequence, KV head and page; halves handed to the ring the MMAs read
-enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_ISSUED };
+// CTA, first sequence, KV head and page; chunks whose K, and whose V,
+// are on their way into the rings that the MMAs read
+enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_KISSUED, M_VISSUED };
 
 __device__ __forceinline__ void pdl_wait()
 {
@@ -103,16 +98,16 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-// Wait until half x is on its way into its slot.  A role that does not follow
-// every half of a ring (a stream that takes every second chunk, the warp that
-// fixes V rows) does this before it waits for the half's barrier: the slot's
-// previous phase is then known to be over, and the phase's parity to be that of
-// half x.
-__device__ __forceinline__ bool wait_issued(int x, volatile int* misc)
+// Wait until the K or V (`which`) of chunk g is on its way into its slot.  A role
+// that does not follow every chunk of a ring (a stream that takes every second
+// one, the warp that fixes V rows) does this before it waits for the chunk's
+// barrier: the slot's previous phase is then known to be over, and the phase's
+// parity to be that of chunk g.
+__device__ __forceinline__ bool wait_issued(int which, int g, volatile int* misc)
 {
-    if (misc[M_ISSUED] > x) return true;
+    if (misc[which] > g) return true;
     const long long t0 = clock64();
-    while (misc[M_ISSUED] <= x) {
+    while (misc[which] <= g) {
         if (misc[M_ABORT]) return false;
         if (clock64() - t0 > kWaitLimit) {
             misc[M_ABORT] = 1;
@@ -167,6 +162,16 @@ __device__ __forceinline__ int row_node(const TreeParams& p, int r)
 {
     return p.g_magic ? (int)__umulhi((uint32_t)r, p.g_magic) : r;
 }
+
+// One ring that the MMAs read: chunk g's slot, its barriers and their parity.
+template <int SLOTS, int FULL, int FREE>
+struct Ring {
+    static constexpr int kSlots = SLOTS;
+    static __device__ __forceinline__ int slot(int g) { return g % SLOTS; }
+    static __device__ __forceinline__ uint32_t parity(int g) { return (uint32_t)((g / SLOTS) & 1); }
+    static __device__ __forceinline__ int full(int g) { return FULL + g % SLOTS; }
+    static __device__ __forceinline__ int free(int g) { return FREE + g % SLOTS; }
+};
 
 // The segments of a CTA's range: the pages [j, j + np) of one (sequence, KV
 // head) each.  Every role walks the same list.
@@ -304,81 +309,86 @@ __device__ __forceinline__ bool drop_non_finite(uint32_t (&x)[4])
     return any != 0;
 }
 
-// Role of one warp: K and V of every chunk through the ring of load slots by TMA.
-template <class G>
+// Role of a warp: K (WHICH 0), V (1) or both (2) of every chunk by TMA.  A warp
+// issues one copy in ~80 clocks (measured: 26 bytes a clock in 2 KB boxes, twice
+// that from two warps), less than an SM's share of HBM at its usual clock, so
+// where K and V come fast each has a warp of its own.
+template <class G, int WHICH>
 __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                           uint32_t sb, volatile int* misc, int first_row, int lane)
 {
     constexpr bool FP8 = G::kFp8;
+    constexpr int kPage = FP8 ? G::kPageBytes : kBlock * 128;    // bytes of a box
     auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
     const uint64_t pol = l2_evict_first_policy();
-    int x = 0;                               // halves (K or V of a chunk) issued
-    bool ok = true;
+    const int box = FP8 ? 0 : lane % G::kBoxes, page = FP8 ? lane : lane / G::kBoxes;
+    int gk = 0, gv = 0;                          // chunks issued
+    // this lane's page of a chunk, its KV head; the pages to copy
+    struct Pages {
+        int z, n;
+        bool mine;
+    };
+    auto issue = [&](auto ring, int off, int slot_bytes, int which, const CUtensorMap& tm, int& g, const Pages& c) -> bool {
+        using R = decltype(ring);
+        if (g >= R::kSlots && !wait_warp(bar(R::free(g)), R::parity(g) ^ 1u, misc)) return false;
+        const uint32_t fb = bar(R::full(g));
+        if (lane == 0) {
+            if (c.n > 0) mbar_arrive_expect_tx(fb, (uint32_t)(c.n * G::kPageBytes));
+            else mbar_arrive(fb);
+        }
+        __syncwarp();
+        if (c.mine) {
+            const uint32_t dst = sb + (uint32_t)(off + R::slot(g) * slot_bytes + box * kRegion + page * kPage);
+            if (p.teams == 1)                    // read once: first out of L2
+                tma_load_3d_hint(dst, &tm, box * 64, 0, c.z, fb, pol);
+            else
+                tma_load_3d(dst, &tm, box * 64, 0, c.z, fb);
+        }
+        ++g;
+        if (!FP8 && lane == 0) misc[which] = g;
+        return true;
+    };
+    auto issue_k = [&](const Pages& c) {
+        return issue(typename G::KLoad(), G::kKLoadOff, G::kLoadBytes, M_KISSUED, tm_k, gk, c);
+    };
+    auto issue_v = [&](const Pages& c) {
+        return issue(typename G::VLoad(), G::kVLoadOff, G::kLoadBytes, M_VISSUED, tm_v, gv, c);
+    };
+    bool ok = true, held = false;                // (a warp for both: V comes a chunk after K)
+    Pages before = {0, 0, false};
     for (Walk w(p, misc, first_row); ok && w.more(); w.next(p, first_row)) {
         const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
         int ids = lane < w.np ? __ldg(row + lane) : -1;       // pages 0..31 of the segment
         int ahead = 32 + lane < w.np ? __ldg(row + 32 + lane) : -1;
         const int nc = w.chunks();
-        const int box = FP8 ? 0 : lane % G::kBoxes, page = FP8 ? lane : lane / G::kBoxes;
-        int my = -1, nvalid = 0;                 // this lane's page of the chunk; pages to copy
-        bool valid = false;
-        auto issue = [&](const CUtensorMap& tm) -> bool {
-            const int slot = x % G::kLoadSlots, round = x / G::kLoadSlots;
-            if (round > 0 && !wait_warp(bar(G::B_EMPTY + slot), (uint32_t)((round - 1) & 1), misc)) return false;
-            const uint32_t fb = bar(G::B_FULL + slot);
-            if (lane == 0) {
-                if (nvalid > 0) mbar_arrive_expect_tx(fb, (uint32_t)(nvalid * G::kPageBytes));
-                else mbar_arrive(fb);
+        for (int c = 0; ok && c < nc; ++c) {
+            if (c > 0 && (c & 3) == 0) {
+                ids = ahead;
+                const int at = (c + 4) * kPages + lane;
+                ahead = at < w.np ? __ldg(row + at) : -1;
             }
-            __syncwarp();
-            if (valid) {
-                const uint32_t dst =
-                    FP8 ? sb + (uint32_t)(G::kRawOff + slot * G::kRawSlot + page * G::kPageBytes)
-                        : sb + (uint32_t)(G::kSlotOff + slot * G::kSlot + box * kRegion + page * kBlock * 128);
-                const int z = my * p.Hkv + w.h;
-                if (p.teams == 1)                // read once: first out of L2
-                    tma_load_3d_hint(dst, &tm, box * 64, 0, z, fb, pol);
-                else
-                    tma_load_3d(dst, &tm, box * 64, 0, z, fb);
-            }
-            ++x;
-            if (!FP8 && lane == 0) misc[M_ISSUED] = x;
-            return true;
-        };
-        for (int c = 0; ok && c <= nc; ++c) {
-            const int v_my = my, v_nvalid = nvalid;      // the chunk before, whose V follows
-            const bool v_valid = valid;
-            if (c < nc) {
-                if (c > 0 && (c & 3) == 0) {
-                    ids = ahead;
-                    const int at = (c + 4) * kPages + lane;
-                    ahead = at < w.np ? __ldg(row + at) : -1;
-                }
-                my = __shfl_sync(kFull, ids, (c & 3) * kPages + page % kPages);
-                const bool mine = page < w.chunk_pages(c);
-                valid = mine && my >= 0 && my < p.num_blocks;
-                if (mine && !valid && box == 0) raise_flag(&g_tree_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, my);
-                nvalid = __popc(__ballot_sync(kFull, valid && box == 0));
-                ok = issue(tm_k);
-            }
-            if (ok && c > 0) {
-                const int k_my = my, k_nvalid = nvalid;
-                const bool k_valid = valid;
-                my = v_my;
-                nvalid = v_nvalid;
-                valid = v_valid;
-                ok = issue(tm_v);
-                my = k_my;
-                nvalid = k_nvalid;
-                valid = k_valid;
-            }
+            const int my = __shfl_sync(kFull, ids, (c & 3) * kPages + page % kPages);
+            const bool in = page < w.chunk_pages(c);
+            Pages now;
+            now.mine = in && my >= 0 && my < p.num_blocks;
+            now.z = my * p.Hkv + w.h;
+            if (WHICH != 1 && in && !now.mine && box == 0) raise_flag(&g_tree_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, my);
+            now.n = __popc(__ballot_sync(kFull, now.mine && box == 0));
+            if (WHICH != 1) ok = issue_k(now);
+            if (ok && WHICH == 1) ok = issue_v(now);
+            if (ok && WHICH == 2 && held) ok = issue_v(before);
+            before = now;
+            held = true;
         }
     }
+    if (ok && WHICH == 2 && held) issue_v(before);
     // every issued copy lands before the CTA can end
-    if (lane == 0)
-        for (int i = x > G::kLoadSlots ? x - G::kLoadSlots : 0; i < x; ++i)
-            mbar_wait_bounded(bar(G::B_FULL + i % G::kLoadSlots),
-                              (uint32_t)((i / G::kLoadSlots) & 1), kWaitLimit);
+    if (lane == 0) {
+        for (int i = gk > G::KLoad::kSlots ? gk - G::KLoad::kSlots : 0; i < gk; ++i)
+            mbar_wait_bounded(bar(G::KLoad::full(i)), G::KLoad::parity(i), kWaitLimit);
+        for (int i = gv > G::VLoad::kSlots ? gv - G::VLoad::kSlots : 0; i < gv; ++i)
+            mbar_wait_bounded(bar(G::VLoad::full(i)), G::VLoad::parity(i), kWaitLimit);
+    }
     __syncwarp();
 }
 
@@ -441,7 +451,7 @@ __device__ __forceinline__ void tree_masks(const TreeParams& p, const Walk& w, u
 // warp.  False: given up.
 template <class G>
 __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, uint32_t sb, uint8_t* gb,
-                                           volatile int* misc, int x0, int lane)
+                                           volatile int* misc, int g0, int lane)
 {
     auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
     volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(gb + G::kBadOff);
@@ -451,11 +461,11 @@ __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, u
     // ---- V rows of the chunks that reach the drafted positions
     for (int ch = 0; ok && ch < nc; ++ch) {
         if (!w.drafted(ch)) continue;
-        const int vx = v_half(x0, ch, nc), slot = vx % G::kSlots;
-        ok = __all_sync(kFull, wait_issued(vx, misc)) &&
-             wait_warp(bar(G::B_FULL + slot), (uint32_t)((vx / G::kSlots) & 1), misc);
+        const int gv = g0 + ch;
+        ok = __all_sync(kFull, wait_issued(M_VISSUED, gv, misc)) &&
+             wait_warp(bar(G::VRing::full(gv)), G::VRing::parity(gv), misc);
         if (!ok) break;
-        const uint32_t vb = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
+        const uint32_t vb = sb + (uint32_t)(G::kVOff + G::VRing::slot(gv) * G::kSlot);
         const int p0 = (w.j + ch * kPages) * kBlock;
         const int lo = max(0, w.q.base - p0), hi = w.chunk_pages(ch) * kBlock;
         for (int rb = lo; rb < hi; rb += RI) {
@@ -478,48 +488,47 @@ __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, u
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(G::B_FIX + slot));
+        if (lane == 0) mbar_arrive(bar(G::B_FIX + G::VRing::slot(gv)));
     }
     return ok;
 }
 
-// Widen the E4M3 codes of K and V of the segment's chunks to f16, with what
-// fix_values does on the way.  One of four warps (pw).  False: given up.
+// Widen the E4M3 codes of the segment's K (warps 0 and 1 of four) or V (2 and 3,
+// with what fix_values does on the way) to f16.  False: given up.
 template <class G>
 __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32_t sb, uint8_t* gb,
-                                      volatile int* misc, int x0, int pw, int lane)
+                                      volatile int* misc, int g0, int pw, int lane)
 {
     auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
     volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(gb + G::kBadOff);
     constexpr int D = G::kD;
     const int buf = w.seg & 1, nc = w.chunks();
-    bool ok = true;
+    const bool is_k = pw < 2;
     // 16 codes a thread and step: piece cc of row r.  Eight lanes that go to
     // shared memory together have eight rows, so their pieces lie, swizzled, in
     // different banks on both sides; a step is RS rows, a multiple of the swizzle's
     // period, so that offsets between steps are constants.
     constexpr int CR = D / 16;               // 16-code pieces of a row
-    constexpr int RS = 128 / CR;             // rows of the four warps' step
+    constexpr int RS = 64 / CR;              // rows of the two warps' step
     constexpr int kSteps = kKeys / RS;
-    const int t = pw * 32 + lane;
+    const int t = (pw & 1) * 32 + lane;
     const int r0 = t % RS, cc = t / RS;
     // the copy's swizzle: 16-byte pieces XOR bits 7 and up of the address
     const uint32_t flat = (uint32_t)(r0 * D + cc * 16);
     const uint32_t src0 = flat ^ (((flat >> 7) & (D == 128 ? 7u : 3u)) << 4);
     const uint32_t dst0 = (uint32_t)((cc >> 2) * kRegion) + region_off(r0, (2 * cc) & 7);
     const uint32_t dst1 = (uint32_t)((cc >> 2) * kRegion) + region_off(r0, (2 * cc + 1) & 7);
-    for (int half = 0; ok && half < 2 * nc; ++half) {
-        const int hx = x0 + half;
-        const bool is_k = half == 0 || ((half & 1) && half < 2 * nc - 1);
-        const int ch = is_k ? (half + 1) / 2 : half == 2 * nc - 1 ? nc - 1 : half / 2 - 1;
-        const int rs = hx % G::kRawSlots, slot = hx % G::kSlots;
-        ok = wait_warp(bar(G::B_FULL + rs), (uint32_t)((hx / G::kRawSlots) & 1), misc);
-        if (ok && hx >= G::kSlots)
-            ok = wait_warp(bar(G::B_WFREE + slot), (uint32_t)((hx / G::kSlots - 1) & 1), misc);
-        if (!ok) break;
-        if (pw == 0 && lane == 0) misc[M_ISSUED] = hx + 1;
-        const uint32_t raw = sb + (uint32_t)(G::kRawOff + rs * G::kRawSlot) + src0;
-        const uint32_t dst = sb + (uint32_t)(G::kSlotOff + slot * G::kSlot);
+    bool ok = true;
+    auto one = [&](auto load_ring, auto ring, int load_off, int off, int which, int ch) -> bool {
+        using L = decltype(load_ring);
+        using R = decltype(ring);
+        const int g = g0 + ch;
+        bool fine = wait_warp(bar(L::full(g)), L::parity(g), misc);
+        if (fine && g >= R::kSlots) fine = wait_warp(bar(R::free(g)), R::parity(g) ^ 1u, misc);
+        if (!fine) return false;
+        if ((pw & 1) == 0 && lane == 0) misc[which] = g + 1;
+        const uint32_t raw = sb + (uint32_t)(load_off + L::slot(g) * G::kLoadBytes) + src0;
+        const uint32_t dst = sb + (uint32_t)(off + R::slot(g) * G::kSlot);
         auto store = [&](int step, const uint32_t (&v)[4]) {
             uint4 a, b;
             e4m3x4_to_f16x4(v[0], a.x, a.y);
@@ -557,10 +566,14 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(bar(G::B_EMPTY + rs));
-            mbar_arrive(bar(G::B_WIDE + slot));
+            mbar_arrive(bar(L::free(g)));
+            mbar_arrive(bar(R::full(g)));
         }
-    }
+        return true;
+    };
+    for (int ch = 0; ok && ch < nc; ++ch)
+        ok = is_k ? one(typename G::KLoad(), typename G::KRing(), G::kKLoadOff, G::kKOff, M_KISSUED, ch)
+                  : one(typename G::VLoad(), typename G::VRing(), G::kVLoadOff, G::kVOff, M_VISSUED, ch);
     return ok;
 }
 
