@@ -36,8 +36,8 @@
 //    their two results are joined at the end of the range.  So one stream's
 //    matrix products run under the other's exponentials.
 //  * S = Q K^T with K as it lies in the ring; O += P V with P from tensor memory.
-//    P is f16 for an E4M3 cache (whose tiles warps 11-14 widen to f16, which
-//    holds every code exactly); for a bf16 cache it is bf16, in high and low
+//    P is f16 for an E4M3 cache (whose V warps 11-14 widen to f16, which holds
+//    every code exactly); for a bf16 cache it is bf16, in high and low
 //    parts (16 bits, two products) for a float32 output (LOW).  For a bf16 output
 //    the high part alone: its rounding, 2^-9 of each weight and averaged over
 //    the keys, stays below the output's own, and the second product would be a
@@ -88,30 +88,26 @@ struct Geo {
     static constexpr int kPageBytes = kBlock * D * (FP8 ? 1 : 2);
     static constexpr int kRawSlot = kPages * kBlock * D;     // E4M3 codes of K or V of a chunk
     static constexpr int kScale = 128 / D;
-    static constexpr int kKSlots = (FP8 ? 1 : 2) * kScale, kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
-    static constexpr int kRawK = !FP8 ? 0 : 2 * kScale, kRawV = !FP8 ? 0 : (TILES == 1 ? 2 : 1) * kScale;
+    static constexpr int kKSlots = (FP8 ? 3 : 2) * kScale, kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
+    static constexpr int kRawV = !FP8 ? 0 : 2 * kScale;
+    static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
     static constexpr int kQOff = 0;
     static constexpr int kKOff = kQOff + TILES * kQTile;
-    static constexpr int kVOff = kKOff + kKSlots * kSlot;
+    static constexpr int kVOff = kKOff + kKSlots * kLoadBytes;
     static constexpr int kRawOff = kVOff + kVSlots * kSlot;
-    static constexpr int kBarOff = kRawOff + (kRawK + kRawV) * kRawSlot;
-    static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
-    static constexpr int kKLoadOff = FP8 ? kRawOff : kKOff;
-    static constexpr int kVLoadOff = FP8 ? kRawOff + kRawK * kRawSlot : kVOff;
+    static constexpr int kBarOff = kRawOff + kRawV * kRawSlot;
+    static constexpr int kVLoadOff = FP8 ? kRawOff : kVOff;
     // barriers
-    static constexpr int kKL = FP8 ? kRawK : kKSlots, kVL = FP8 ? kRawV : kVSlots;
+    static constexpr int kVL = FP8 ? kRawV : kVSlots;
     static constexpr int B_KFULL = 0;                        // + slot: K has landed
-    static constexpr int B_KEMPTY = B_KFULL + kKL;           // + slot: it may be refilled
-    static constexpr int B_VFULL = B_KEMPTY + kKL;
+    static constexpr int B_KEMPTY = B_KFULL + kKSlots;       // + slot: it may be refilled
+    static constexpr int B_VFULL = B_KEMPTY + kKSlots;       // V, or its codes
     static constexpr int B_VEMPTY = B_VFULL + kVL;
-    static constexpr int B_KWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
-    static constexpr int B_KWFREE = B_KWIDE + (FP8 ? kKSlots : 0);
-    static constexpr int B_VWIDE = B_KWFREE + (FP8 ? kKSlots : 0);
+    static constexpr int B_VWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
     static constexpr int B_VWFREE = B_VWIDE + (FP8 ? kVSlots : 0);
     static constexpr int B_FIX = B_VWFREE + (FP8 ? kVSlots : 0);     // (bf16) + slot: V rows fixed
-    using KLoad = Ring<kKL, B_KFULL, B_KEMPTY>;              // the rings that TMA fills,
-    using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;
-    using KRing = Ring<kKSlots, FP8 ? B_KWIDE : B_KFULL, FP8 ? B_KWFREE : B_KEMPTY>;   // and the MMAs read
+    using KRing = Ring<kKSlots, B_KFULL, B_KEMPTY>;
+    using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;              // what TMA fills, and what the MMAs read
     using VRing = Ring<kVSlots, FP8 ? B_VWIDE : B_VFULL, FP8 ? B_VWFREE : B_VEMPTY>;
     static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kVSlots);  // Q and the tree of a segment
     static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
@@ -159,25 +155,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         constexpr int kReaders = TILES;          // MMA warps that read every slot
-        for (int i = 0; i < G::kKL; ++i) {
+        for (int i = 0; i < G::kKSlots; ++i) {
             mbar_init(bar(G::B_KFULL + i), 1);
-            mbar_init(bar(G::B_KEMPTY + i), FP8 ? 2 : kReaders);
+            mbar_init(bar(G::B_KEMPTY + i), kReaders);
         }
+        // (a slot of codes is freed by the widening warps, which also fill)
         for (int i = 0; i < G::kVL; ++i) {
             mbar_init(bar(G::B_VFULL + i), 1);
-            mbar_init(bar(G::B_VEMPTY + i), FP8 ? 2 : kReaders);
+            mbar_init(bar(G::B_VEMPTY + i), FP8 ? G::kPrepWarps : kReaders);
         }
-        if (FP8) {
-            for (int i = 0; i < G::kKSlots; ++i) {
-                mbar_init(bar(G::B_KWIDE + i), 2);
-                mbar_init(bar(G::B_KWFREE + i), kReaders);
-            }
-            for (int i = 0; i < G::kVSlots; ++i) {
-                mbar_init(bar(G::B_VWIDE + i), 2);
+        for (int i = 0; i < G::kVSlots; ++i) {
+            if (FP8) {
+                mbar_init(bar(G::B_VWIDE + i), G::kPrepWarps);
                 mbar_init(bar(G::B_VWFREE + i), kReaders);
+            } else {
+                mbar_init(bar(G::B_FIX + i), 1);
             }
-        } else {
-            for (int i = 0; i < G::kVSlots; ++i) mbar_init(bar(G::B_FIX + i), 1);
         }
         mbar_init(bar(G::B_QFULL), G::kPrepWarps);
         mbar_init(bar(G::B_QFREE), 2);
@@ -215,9 +208,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (lane == 0) {
             const int st = warp - 9;
             const uint32_t tS = tmem + (uint32_t)(128 * st), tO = tmem + 256u + (uint32_t)(128 * st);
-            const uint64_t qdesc =
-                umma::smem_desc_sw128(sb + G::kQOff + (TILES == 2 ? st * G::kQTile : 0), 16, 1024);
-            const uint64_t sdesc = umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
+            const uint32_t qt = sb + (uint32_t)(G::kQOff + (TILES == 2 ? st * G::kQTile : 0));
+            const uint64_t qdesc = FP8 ? code_desc<D>(qt) : umma::smem_desc_sw128(qt, 16, 1024);
+            const uint64_t sdesc = FP8 ? code_desc<D>(sb + G::kKOff) : umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
             const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
             constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(kTile, D, false, true)
                                               : umma::idesc_bf16_f32(kTile, D, false, true);
@@ -259,15 +252,23 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     // overwrites, are done (PVDONE below)
                     umma::fence_after_sync();
                     {
-                        const uint64_t kd = sdesc + (uint64_t)((ks * G::kSlot) >> 4);
+                        const uint64_t kd = sdesc + (uint64_t)((ks * G::kLoadBytes) >> 4);
                         const uint32_t idesc =
                             FP8 ? umma::idesc_f16_f32(kTile, kBlock * np, false, false)
                                 : umma::idesc_bf16_f32(kTile, kBlock * np, false, false);
+                        if constexpr (FP8) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t a = qdesc + (uint64_t)(((kk >> 2) * kTile * 128 + (kk & 3) * 32) >> 4);
-                            const uint64_t b = kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                            umma::mma_bf16_ss(tS, a, b, idesc, kk > 0);
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int kk = 0; kk < D / 32; ++kk)
+                                    umma::mma_e4m3_ss(tS, qdesc + (uint64_t)((part * kTile * D + kk * 32) >> 4),
+                                                      kd + (uint64_t)((kk * 32) >> 4), idesc, part + kk > 0);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma::mma_bf16_ss(tS, qdesc + (uint64_t)(((kk >> 2) * kTile * 128 + (kk & 3) * 32) >> 4),
+                                                  kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4), idesc,
+                                                  kk > 0);
                         }
                     }
                     umma::commit(bar(G::B_SFULL + st));
@@ -337,15 +338,18 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const int node = row_node(p, first_row + rc), g = first_row + rc - node * p.G;
                 const uint16_t* src =
                     p.q + ((size_t)(w.q.t0 + node) * p.Hq + (size_t)w.h * p.G + g) * D + 8 * c;
-                const uint32_t dst = sb + (uint32_t)(G::kQOff + (rc >> 7) * G::kQTile + (c >> 3) * kTile * 128) +
-                                     region_off(rc & 127, c & 7);
                 if (!FP8) {
+                    const uint32_t dst = sb + (uint32_t)(G::kQOff + (rc >> 7) * G::kQTile + (c >> 3) * kTile * 128) +
+                                         region_off(rc & 127, c & 7);
                     if (r < rows) cp_async16(dst, src);
                 } else {
                     float up;
-                    const uint4 q16 = query_f16<D>(__ldg(reinterpret_cast<const uint4*>(src)), up);
+                    uint2 first, second;
+                    query_e4m3<D>(__ldg(reinterpret_cast<const uint4*>(src)), first, second, up);
                     if (r < rows) {
-                        sts128(dst, q16);
+                        const uint32_t at = sb + (uint32_t)(G::kQOff + (rc >> 7) * G::kQTile) + code_off<D>(rc & 127, c);
+                        sts64(at, first);
+                        sts64(at + (uint32_t)(kTile * D), second);
                         if (c == 0)
                             reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * TILES * kTile + r] = up;
                     }

@@ -56,33 +56,29 @@ struct SmallGeo {
     static constexpr int kAccs = kSplit ? 1 : 2;             // accumulators
     static constexpr int kPW = kLow ? 2 * N : N;
     static constexpr int kPBuf = kPW / 64 * kRegion;         // [column group of 64][128 keys][128 B]
-    static constexpr int kQBytes = kBoxes * N * 128;
+    static constexpr int kQBytes = FP8 ? 2 * N * D : kBoxes * N * 128;   // (FP8: two parts)
     static constexpr int kScale = 128 / D;
-    static constexpr int kKSlots = (FP8 ? 1 : 2) * kScale, kVSlots = (FP8 || N == 64 ? 2 : 3) * kScale;
-    static constexpr int kRawSlots = !FP8 ? 0 : 2 * kScale;  // of K and of V
+    static constexpr int kKSlots = (FP8 ? 4 : 2) * kScale, kVSlots = (FP8 || N == 64 ? 2 : 3) * kScale;
+    static constexpr int kRawV = !FP8 ? 0 : (N == 32 ? 3 : 2) * kScale;
+    static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
     static constexpr int kQOff = 0;
     static constexpr int kKOff = (kQOff + kQBytes + 1023) / 1024 * 1024;
-    static constexpr int kVOff = kKOff + kKSlots * kSlot;
+    static constexpr int kVOff = kKOff + kKSlots * kLoadBytes;
     static constexpr int kPOff = kVOff + kVSlots * kSlot;    // two buffers (behind the ring: see D < 128)
     static constexpr int kRawOff = kPOff + 2 * kPBuf;
-    static constexpr int kBarOff = kRawOff + 2 * kRawSlots * kRawSlot;
-    static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
-    static constexpr int kKLoadOff = FP8 ? kRawOff : kKOff;
-    static constexpr int kVLoadOff = FP8 ? kRawOff + kRawSlots * kRawSlot : kVOff;
+    static constexpr int kBarOff = kRawOff + kRawV * kRawSlot;
+    static constexpr int kVLoadOff = FP8 ? kRawOff : kVOff;
     // barriers
-    static constexpr int kKL = FP8 ? kRawSlots : kKSlots, kVL = FP8 ? kRawSlots : kVSlots;
+    static constexpr int kVL = FP8 ? kRawV : kVSlots;
     static constexpr int B_KFULL = 0;                        // + slot: K has landed
-    static constexpr int B_KEMPTY = B_KFULL + kKL;           // + slot: it may be refilled
-    static constexpr int B_VFULL = B_KEMPTY + kKL;
+    static constexpr int B_KEMPTY = B_KFULL + kKSlots;       // + slot: it may be refilled
+    static constexpr int B_VFULL = B_KEMPTY + kKSlots;       // V, or its codes
     static constexpr int B_VEMPTY = B_VFULL + kVL;
-    static constexpr int B_KWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
-    static constexpr int B_KWFREE = B_KWIDE + (FP8 ? kKSlots : 0);
-    static constexpr int B_VWIDE = B_KWFREE + (FP8 ? kKSlots : 0);
+    static constexpr int B_VWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
     static constexpr int B_VWFREE = B_VWIDE + (FP8 ? kVSlots : 0);
     static constexpr int B_FIX = B_VWFREE + (FP8 ? kVSlots : 0);     // (bf16) + slot: V rows fixed
-    using KLoad = Ring<kKL, B_KFULL, B_KEMPTY>;              // the rings that TMA fills,
-    using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;
-    using KRing = Ring<kKSlots, FP8 ? B_KWIDE : B_KFULL, FP8 ? B_KWFREE : B_KEMPTY>;   // and the MMAs read
+    using KRing = Ring<kKSlots, B_KFULL, B_KEMPTY>;
+    using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;              // what TMA fills, and what the MMAs read
     using VRing = Ring<kVSlots, FP8 ? B_VWIDE : B_VFULL, FP8 ? B_VWFREE : B_VEMPTY>;
     static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kVSlots);  // Q and the tree of a segment
     static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
@@ -160,26 +156,22 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (tid == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        // (a slot of codes is freed by its two widening warps, which also fill)
-        for (int i = 0; i < G::kKL; ++i) {
+        for (int i = 0; i < G::kKSlots; ++i) {
             mbar_init(bar(G::B_KFULL + i), 1);
-            mbar_init(bar(G::B_KEMPTY + i), FP8 ? 2 : 1);
+            mbar_init(bar(G::B_KEMPTY + i), 1);
         }
+        // (a slot of codes is freed by the widening warps, which also fill)
         for (int i = 0; i < G::kVL; ++i) {
             mbar_init(bar(G::B_VFULL + i), 1);
-            mbar_init(bar(G::B_VEMPTY + i), FP8 ? 2 : 1);
+            mbar_init(bar(G::B_VEMPTY + i), FP8 ? G::kPrepWarps : 1);
         }
-        if (FP8) {
-            for (int i = 0; i < G::kKSlots; ++i) {
-                mbar_init(bar(G::B_KWIDE + i), 2);
-                mbar_init(bar(G::B_KWFREE + i), 1);
-            }
-            for (int i = 0; i < G::kVSlots; ++i) {
-                mbar_init(bar(G::B_VWIDE + i), 2);
+        for (int i = 0; i < G::kVSlots; ++i) {
+            if (FP8) {
+                mbar_init(bar(G::B_VWIDE + i), G::kPrepWarps);
                 mbar_init(bar(G::B_VWFREE + i), 1);
+            } else {
+                mbar_init(bar(G::B_FIX + i), 1);
             }
-        } else {
-            for (int i = 0; i < G::kVSlots; ++i) mbar_init(bar(G::B_FIX + i), 1);
         }
         mbar_init(bar(G::B_QFULL), G::kPrepWarps);
         mbar_init(bar(G::B_QFREE), 1);
@@ -217,8 +209,8 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     } else if (warp == 10) {
         // --------------------------------------------------------------- MMAs
         if (lane == 0) {
-            const uint64_t qdesc = umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
-            const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
+            const uint64_t qdesc = FP8 ? code_desc<D>(sb + G::kQOff) : umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
+            const uint64_t kdesc = FP8 ? code_desc<D>(sb + G::kKOff) : umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
             const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
             const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, kRegion, 1024);
             constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, N, false, false)
@@ -253,13 +245,23 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                             return false;
                         }
                         umma::fence_after_sync();
-                        const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kSlot) >> 4);
+                        const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
+                        const uint32_t d = tmem + (uint32_t)(N * (g & 3));
+                        if constexpr (FP8) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            umma::mma_bf16_ss(tmem + (uint32_t)(N * (g & 3)),
-                                              kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4),
-                                              qdesc + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
-                                              idesc_s, kk > 0);
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int kk = 0; kk < D / 32; ++kk)
+                                    umma::mma_e4m3_ss(d, kd + (uint64_t)((kk * 32) >> 4),
+                                                      qdesc + (uint64_t)((part * N * D + kk * 32) >> 4), idesc_s,
+                                                      part + kk > 0);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma::mma_bf16_ss(d, kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4),
+                                                  qdesc + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
+                                                  idesc_s, kk > 0);
+                        }
                         umma::commit(bar(G::B_SFULL + (g & 3)));
                         umma::commit(bar(KR::free(g)));
                         if (sc + 1 == nc) umma::commit(bar(G::B_QFREE));
@@ -319,14 +321,17 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const int node = row_node(p, rc), gq = rc - node * p.G;
                 const uint16_t* src =
                     p.q + ((size_t)(w.q.t0 + node) * p.Hq + (size_t)w.h * p.G + gq) * D + 8 * c;
-                const uint32_t dst = sb + (uint32_t)(G::kQOff + (c >> 3) * N * 128) + region_off(rc, c & 7);
                 if (!FP8) {
+                    const uint32_t dst = sb + (uint32_t)(G::kQOff + (c >> 3) * N * 128) + region_off(rc, c & 7);
                     if (r < rows) cp_async16(dst, src);
                 } else {
                     float up;
-                    const uint4 h = query_f16<D>(__ldg(reinterpret_cast<const uint4*>(src)), up);
+                    uint2 first, second;
+                    query_e4m3<D>(__ldg(reinterpret_cast<const uint4*>(src)), first, second, up);
                     if (r < rows) {
-                        sts128(dst, h);
+                        const uint32_t at = sb + (uint32_t)G::kQOff + code_off<D>(rc, c);
+                        sts64(at, first);
+                        sts64(at + (uint32_t)(N * D), second);
                         if (c == 0) reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + r] = up;
                     }
                 }

@@ -6,7 +6,8 @@
 // A kernel's geometry G names its shared memory (offsets k..Off from a
 // 1024-byte aligned base) and its barriers (B_..); both kernels consume K and V
 // in chunks of up to 8 pages, chunk g of a CTA from slot g % slots of a ring of K
-// and of one of V (E4M3: rings of codes in front of rings of f16).
+// and of one of V.  E4M3: the codes of K are multiplied as they are, with the
+// query in two E4M3 parts; V is widened from a ring of codes to one of f16.
 #pragma once
 
 #include <cuda.h>
@@ -345,11 +346,11 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
                 tma_load_3d(dst, &tm, box * 64, 0, c.z, fb);
         }
         ++g;
-        if (!FP8 && lane == 0) misc[which] = g;
+        if ((!FP8 || which == M_KISSUED) && lane == 0) misc[which] = g;
         return true;
     };
     auto issue_k = [&](const Pages& c) {
-        return issue(typename G::KLoad(), G::kKLoadOff, G::kLoadBytes, M_KISSUED, tm_k, gk, c);
+        return issue(typename G::KRing(), G::kKOff, G::kLoadBytes, M_KISSUED, tm_k, gk, c);
     };
     auto issue_v = [&](const Pages& c) {
         return issue(typename G::VLoad(), G::kVLoadOff, G::kLoadBytes, M_VISSUED, tm_v, gv, c);
@@ -384,8 +385,8 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
     if (ok && WHICH == 2 && held) issue_v(before);
     // every issued copy lands before the CTA can end
     if (lane == 0) {
-        for (int i = gk > G::KLoad::kSlots ? gk - G::KLoad::kSlots : 0; i < gk; ++i)
-            mbar_wait_bounded(bar(G::KLoad::full(i)), G::KLoad::parity(i), kWaitLimit);
+        for (int i = gk > G::KRing::kSlots ? gk - G::KRing::kSlots : 0; i < gk; ++i)
+            mbar_wait_bounded(bar(G::KRing::full(i)), G::KRing::parity(i), kWaitLimit);
         for (int i = gv > G::VLoad::kSlots ? gv - G::VLoad::kSlots : 0; i < gv; ++i)
             mbar_wait_bounded(bar(G::VLoad::full(i)), G::VLoad::parity(i), kWaitLimit);
     }
@@ -493,42 +494,39 @@ __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, u
     return ok;
 }
 
-// Widen the E4M3 codes of the segment's K (warps 0 and 1 of four) or V (2 and 3,
-// with what fix_values does on the way) to f16.  False: given up.
+// Widen the E4M3 codes of the segment's V to f16, with what fix_values does on the
+// way.  One of four warps (pw).  False: given up.
 template <class G>
 __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32_t sb, uint8_t* gb,
                                       volatile int* misc, int g0, int pw, int lane)
 {
+    using L = typename G::VLoad;
+    using R = typename G::VRing;
     auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
     volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(gb + G::kBadOff);
     constexpr int D = G::kD;
     const int buf = w.seg & 1, nc = w.chunks();
-    const bool is_k = pw < 2;
     // 16 codes a thread and step: piece cc of row r.  Eight lanes that go to
     // shared memory together have eight rows, so their pieces lie, swizzled, in
     // different banks on both sides; a step is RS rows, a multiple of the swizzle's
     // period, so that offsets between steps are constants.
     constexpr int CR = D / 16;               // 16-code pieces of a row
-    constexpr int RS = 64 / CR;              // rows of the two warps' step
+    constexpr int RS = 128 / CR;             // rows of the four warps' step
     constexpr int kSteps = kKeys / RS;
-    const int t = (pw & 1) * 32 + lane;
+    const int t = pw * 32 + lane;
     const int r0 = t % RS, cc = t / RS;
     // the copy's swizzle: 16-byte pieces XOR bits 7 and up of the address
     const uint32_t flat = (uint32_t)(r0 * D + cc * 16);
     const uint32_t src0 = flat ^ (((flat >> 7) & (D == 128 ? 7u : 3u)) << 4);
     const uint32_t dst0 = (uint32_t)((cc >> 2) * kRegion) + region_off(r0, (2 * cc) & 7);
     const uint32_t dst1 = (uint32_t)((cc >> 2) * kRegion) + region_off(r0, (2 * cc + 1) & 7);
-    bool ok = true;
-    auto one = [&](auto load_ring, auto ring, int load_off, int off, int which, int ch) -> bool {
-        using L = decltype(load_ring);
-        using R = decltype(ring);
+    for (int ch = 0; ch < nc; ++ch) {
         const int g = g0 + ch;
-        bool fine = wait_warp(bar(L::full(g)), L::parity(g), misc);
-        if (fine && g >= R::kSlots) fine = wait_warp(bar(R::free(g)), R::parity(g) ^ 1u, misc);
-        if (!fine) return false;
-        if ((pw & 1) == 0 && lane == 0) misc[which] = g + 1;
-        const uint32_t raw = sb + (uint32_t)(load_off + L::slot(g) * G::kLoadBytes) + src0;
-        const uint32_t dst = sb + (uint32_t)(off + R::slot(g) * G::kSlot);
+        if (!wait_warp(bar(L::full(g)), L::parity(g), misc)) return false;
+        if (g >= R::kSlots && !wait_warp(bar(R::free(g)), R::parity(g) ^ 1u, misc)) return false;
+        if (pw == 0 && lane == 0) misc[M_VISSUED] = g + 1;
+        const uint32_t raw = sb + (uint32_t)(G::kVLoadOff + L::slot(g) * G::kLoadBytes) + src0;
+        const uint32_t dst = sb + (uint32_t)(G::kVOff + R::slot(g) * G::kSlot);
         auto store = [&](int step, const uint32_t (&v)[4]) {
             uint4 a, b;
             e4m3x4_to_f16x4(v[0], a.x, a.y);
@@ -539,7 +537,7 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
             sts128(dst + dst1 + (uint32_t)(step * RS * 128), b);
         };
         const int keys = w.chunk_pages(ch) * kBlock;
-        if (keys == kKeys && (is_k || !w.drafted(ch))) {
+        if (keys == kKeys && !w.drafted(ch)) {
 #pragma unroll
             for (int s0 = 0; s0 < kSteps; s0 += 4) {     // four loads in flight
                 uint32_t v[4][4];
@@ -553,9 +551,9 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
                 const int pos = (w.j + ch * kPages) * kBlock + step * RS + r0;
                 uint32_t v[4];
                 lds128(v, raw + (uint32_t)(step * RS * D));
-                if (!is_k && pos >= w.q.L) {
+                if (pos >= w.q.L) {
                     v[0] = v[1] = v[2] = v[3] = 0u;
-                } else if (!is_k && pos >= w.q.base && drop_non_finite<true>(v)) {
+                } else if (pos >= w.q.base && drop_non_finite<true>(v)) {
                     const int an = pos - w.q.base;
                     atomicOr(const_cast<uint32_t*>(&badw[(buf * G::kPrepWarps + pw) * 4 + (an >> 5)]),
                              1u << (an & 31));
@@ -569,20 +567,18 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
             mbar_arrive(bar(L::free(g)));
             mbar_arrive(bar(R::full(g)));
         }
-        return true;
-    };
-    for (int ch = 0; ok && ch < nc; ++ch)
-        ok = is_k ? one(typename G::KLoad(), typename G::KRing(), G::kKLoadOff, G::kKOff, M_KISSUED, ch)
-                  : one(typename G::VLoad(), typename G::VRing(), G::kVLoadOff, G::kVOff, M_VISSUED, ch);
-    return ok;
+    }
+    return true;
 }
 
-// A query row's 16 bytes as f16, for E4M3 keys.  f16 overflows above 65504: a row
-// whose largest |element| is 2^15 or more is divided by a power of two that
-// brings it below (exact but for elements below 2^-39 of the largest), which the
-// scores are multiplied by again: `up`.  The row's D / 8 lanes call together.
+// A query row's 8 elements (16 bytes of bf16) as two E4M3 parts, for E4M3 keys:
+// the row is scaled by a power of two that brings its largest |element| into
+// [2^7, 2^8); the first part holds an element's leading four bits, the second what
+// is left, which bf16's eight bits leave exact down to 2^-14 of the largest, and
+// within 2^-17 of it below.  The scores are multiplied by `up` again.  A row with
+// infinities or NaN has up = NaN.  The row's D / 8 lanes call together.
 template <int D>
-__device__ __forceinline__ uint4 query_f16(uint4 v, float& up)
+__device__ __forceinline__ void query_e4m3(uint4 v, uint2& first, uint2& second, float& up)
 {
     const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
     uint32_t big = 0;
@@ -590,13 +586,51 @@ __device__ __forceinline__ uint4 query_f16(uint4 v, float& up)
     for (int k = 0; k < 4; ++k) big = max(big, max(q4[k] & 0x7fffu, (q4[k] >> 16) & 0x7fffu));
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
-    const int e = min(max((int)(big >> 7) - (127 + 14), 0), 126);
+    // (rows below 2^-93 keep their smaller elements)
+    const int e = big == 0 ? 0 : max((int)(big >> 7) - (127 + 7), -100);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    up = __uint_as_float((uint32_t)(127 + e) << 23);
-    return make_uint4(pack_f16x2(bf16_lo(q4[0]) * down, bf16_hi(q4[0]) * down),
-                      pack_f16x2(bf16_lo(q4[1]) * down, bf16_hi(q4[1]) * down),
-                      pack_f16x2(bf16_lo(q4[2]) * down, bf16_hi(q4[2]) * down),
-                      pack_f16x2(bf16_lo(q4[3]) * down, bf16_hi(q4[3]) * down));
+    up = big >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 + e) << 23);
+    uint32_t a[2], b[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float x[4];
+        uint32_t codes = 0, rest = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            x[2 * k] = bf16_lo(q4[2 * h + k]) * down;
+            x[2 * k + 1] = bf16_hi(q4[2 * h + k]) * down;
+            codes |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * k], x[2 * k + 1]), __NV_SATFINITE, __NV_E4M3)
+                     << (16 * k);
+        }
+        uint32_t lo, hi;
+        e4m3x4_to_f16x4(codes, lo, hi);
+        const __half2 h0 = *reinterpret_cast<const __half2*>(&lo), h1 = *reinterpret_cast<const __half2*>(&hi);
+        rest = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0] - __low2float(h0), x[1] - __high2float(h0)),
+                                                  __NV_SATFINITE, __NV_E4M3);
+        rest |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2] - __low2float(h1), x[3] - __high2float(h1)),
+                                                   __NV_SATFINITE, __NV_E4M3)
+                << 16;
+        a[h] = codes;
+        b[h] = rest;
+    }
+    first = make_uint2(a[0], a[1]);
+    second = make_uint2(b[0], b[1]);
+}
+
+// Byte offset of byte 8 c of row r of a tile of D-byte rows, with the swizzle that
+// the copies give the codes (128 bytes at D = 128, 64 at 64).
+template <int D>
+__device__ __forceinline__ uint32_t code_off(int r, int c)
+{
+    const uint32_t a = (uint32_t)(r * D + 8 * c);
+    return a ^ (((a >> 7) & (D == 128 ? 7u : 3u)) << 4);
+}
+
+// Descriptor of a K-major tile of E4M3 rows as the copies leave it.
+template <int D>
+__device__ __forceinline__ uint64_t code_desc(uint32_t saddr)
+{
+    return D == 128 ? umma::smem_desc_sw128(saddr, 16, 1024) : umma::smem_desc_sw64(saddr, 16, 512);
 }
 
 // Sequences without a context get zeros for their nodes (threads 0 .. nthreads - 1
