@@ -575,28 +575,42 @@ def paged_decode_timed(out, q, k_cache, v_cache, block_tables, context_lens, sca
 
 # ------------------------------------------------------- trees of drafted tokens
 
-def _int32(name, t, *shape):
-    """The address of a contiguous int32 tensor of the given shape (None: any)."""
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or any(
-            want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, list(shape)))
-    return t.data_ptr()
+_torch = None               # torch, once one of the functions below has been called
 
 
-def _reachable(*tensors):
-    """A call launches on the current device: its tensors have to be there, or
-    in pinned host memory."""
+def _load_torch():
+    global _torch
     import torch
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            if not t.is_pinned():
-                raise ValueError("tensors must be on the device or in pinned host memory")
-        elif t.device.index != torch.cuda.current_device():
-            raise ValueError("tensor on %s, current device is cuda:%d"
-                             % (t.device, torch.cuda.current_device()))
+    _torch = torch
+    return torch
+
+
+def _place(t):
+    """The device index the tensors of a call have to be on: that of `t`, which
+    has to be the current device (a call launches there).  Host memory the device
+    can address (pinned) will do for any of them."""
+    i = t.get_device()
+    if i < 0:
+        if not t.is_pinned():
+            raise ValueError("tensors must be on the device or in pinned host memory")
+        return _torch.cuda.current_device()
+    if i != _torch.cuda.current_device():
+        raise ValueError("tensor on cuda:%d, current device is cuda:%d"
+                         % (i, _torch.cuda.current_device()))
+    return i
+
+
+def _ptr(name, t, dtype, n, dev):
+    """The address of a contiguous tensor of n elements of `dtype` on device `dev`."""
+    if (t.dtype is dtype and t.numel() == n and t.is_contiguous()
+            and (t.get_device() == dev or (t.get_device() < 0 and t.is_pinned()))):
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s tensor of %d elements on cuda:%d or in pinned "
+                     "host memory" % (name, dtype, n, dev))
+
+
+def _raw_stream(stream, dev):
+    return stream.cuda_stream if stream is not None else _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def tree_workspace_bytes(num_seqs, max_nodes, num_q_heads, num_kv_heads, head_dim, kv_dtype=BF16):
@@ -624,28 +638,32 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_tables, context_lens, n
     (paged_tree_attention): node_starts int32 [B + 1], parents int32 [T]
     (None: chains), context_lens int32 [B] including the nodes, at most
     max_nodes nodes a sequence; workspace from alloc_tree_workspace."""
-    import torch
+    torch = _torch or _load_torch()
     T, Hq, D = q.shape
-    NB, Hkv, _, D2 = k_cache.shape
+    cache = k_cache.shape
+    NB, Hkv, _, D2 = cache
     B, max_blocks = block_tables.shape
-    if (q.dtype != torch.bfloat16 or out.dtype not in (torch.bfloat16, torch.float32)
-            or out.shape != q.shape or D != D2 or k_cache.shape != v_cache.shape
-            or k_cache.dtype != v_cache.dtype):
+    f32 = out.dtype is torch.float32
+    if (q.dtype is not torch.bfloat16 or not (f32 or out.dtype is torch.bfloat16)
+            or out.shape != q.shape or D != D2 or v_cache.shape != cache
+            or k_cache.dtype is not v_cache.dtype):
         raise ValueError("q must be bfloat16 [T, Hq, D], out bfloat16 or float32 of its shape, "
                          "k_cache and v_cache alike")
-    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
-            and v_cache.is_contiguous()):
-        raise ValueError("q, out and the caches must be contiguous")
-    _reachable(q, out, k_cache, v_cache, block_tables, context_lens, node_starts, parents,
-                 workspace)
+    dev = _place(k_cache)
+    i32, n = torch.int32, q.numel()
     _check(_HOT_TREE_ATTENTION(
-        out.data_ptr(), F32 if out.dtype == torch.float32 else BF16, q.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), _cache_dtype(k_cache), float(k_scale),
-        float(v_scale), NB, _int32("block_tables", block_tables, B, max_blocks), max_blocks,
-        _int32("context_lens", context_lens, B), _int32("node_starts", node_starts, B + 1),
-        _int32("parents", parents, T) if parents is not None else 0, B, T, int(max_nodes), Hq,
-        Hkv, D, float(scale), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_int(stream)),
+        _ptr("out", out, out.dtype, n, dev), F32 if f32 else BF16,
+        _ptr("q", q, torch.bfloat16, n, dev),
+        _ptr("k_cache", k_cache, k_cache.dtype, k_cache.numel(), dev),
+        _ptr("v_cache", v_cache, k_cache.dtype, v_cache.numel(), dev),
+        BF16 if k_cache.dtype is torch.bfloat16 else _cache_dtype(k_cache),
+        float(k_scale), float(v_scale), NB,
+        _ptr("block_tables", block_tables, i32, B * max_blocks, dev), max_blocks,
+        _ptr("context_lens", context_lens, i32, B, dev),
+        _ptr("node_starts", node_starts, i32, B + 1, dev),
+        _ptr("parents", parents, i32, T, dev) if parents is not None else 0, B, T,
+        int(max_nodes), Hq, Hkv, D, float(scale), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
         "paged_tree_attention")
 
 
@@ -663,34 +681,38 @@ def kv_tree_verify(accept_lens, accept_nodes, out_tokens, target_probs, tokens, 
     int32 [B], accept_nodes and out_tokens int32 [B, max_nodes].  greedy:
     target_probs may be logits; accept_u, sample_u and draft_probs are not
     used."""
-    import torch
+    torch = _torch or _load_torch()
     T, V = target_probs.shape
     B, max_nodes = accept_nodes.shape
-    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+    dtype, i32, f32 = target_probs.dtype, torch.int32, torch.float32
+    if dtype is not f32 and dtype is not torch.bfloat16:
         raise ValueError("target_probs must be float32 or bfloat16")
     draft = None if greedy else draft_probs
-    if draft is not None and (draft.dtype != target_probs.dtype
-                              or draft.shape != target_probs.shape):
+    if draft is not None and (draft.dtype is not dtype or draft.shape != target_probs.shape):
         raise ValueError("draft_probs must have target_probs' type and shape")
-    for p in (target_probs, draft):
-        if p is not None and V > 1 and p.stride(1) != 1:
-            raise ValueError("the rows of probabilities must be contiguous")
-    if not greedy:
-        for u, n in ((accept_u, T), (sample_u, B)):
-            if u is None or u.dtype != torch.float32 or u.shape != (n,) or not u.is_contiguous():
-                raise ValueError("accept_u and sample_u must be contiguous float32 [T] and [B]")
-    _reachable(target_probs, accept_lens, accept_nodes, out_tokens, tokens, parents,
-                 node_starts, draft, None if greedy else accept_u, None if greedy else sample_u)
+    if not greedy and (accept_u is None or sample_u is None):
+        raise ValueError("accept_u and sample_u are needed")
+    # the rows may be apart, their entries not
+    t_stride, t_step = target_probs.stride()
+    d_stride, d_step = draft.stride() if draft is not None else (0, 1)
+    if V > 1 and (t_step != 1 or d_step != 1):
+        raise ValueError("the rows of probabilities must be contiguous")
+    if T <= 1:
+        t_stride, d_stride = max(t_stride, V), max(d_stride, V)
+    dev = _place(target_probs)
+    if draft is not None and draft.get_device() != target_probs.get_device():
+        raise ValueError("draft_probs must be where target_probs is")
     _check(_HOT_TREE_VERIFY(
-        _int32("accept_lens", accept_lens, B), _int32("accept_nodes", accept_nodes, B, max_nodes),
-        _int32("out_tokens", out_tokens, B, max_nodes), target_probs.data_ptr(),
-        target_probs.stride(0) if T > 1 else V, draft.data_ptr() if draft is not None else 0,
-        (draft.stride(0) if T > 1 else V) if draft is not None else 0,
-        F32 if target_probs.dtype == torch.float32 else BF16, _int32("tokens", tokens, T),
-        _int32("parents", parents, T) if parents is not None else 0,
-        _int32("node_starts", node_starts, B + 1), 0 if greedy else accept_u.data_ptr(),
-        0 if greedy else sample_u.data_ptr(), B, T, max_nodes, V, VERIFY_GREEDY if greedy else 0,
-        _stream_int(stream)), "kv_tree_verify")
+        _ptr("accept_lens", accept_lens, i32, B, dev),
+        _ptr("accept_nodes", accept_nodes, i32, B * max_nodes, dev),
+        _ptr("out_tokens", out_tokens, i32, B * max_nodes, dev), target_probs.data_ptr(), t_stride,
+        draft.data_ptr() if draft is not None else 0, d_stride, F32 if dtype is f32 else BF16,
+        _ptr("tokens", tokens, i32, T, dev),
+        _ptr("parents", parents, i32, T, dev) if parents is not None else 0,
+        _ptr("node_starts", node_starts, i32, B + 1, dev),
+        0 if greedy else _ptr("accept_u", accept_u, f32, T, dev),
+        0 if greedy else _ptr("sample_u", sample_u, f32, B, dev), B, T, max_nodes, V,
+        VERIFY_GREEDY if greedy else 0, _raw_stream(stream, dev)), "kv_tree_verify")
 
 
 class CacheLayers:
@@ -721,16 +743,18 @@ def kv_tree_compact(layers, block_tables, context_lens, node_starts, accept_node
     """Move the accepted nodes' K and V together in the caches of all layers (a
     CacheLayers), in place (kv_tree_compact): node accept_nodes[s, i] goes to
     position base + i, base = context_lens[s] less the tree's nodes."""
+    torch = _torch or _load_torch()
     B, max_nodes = accept_nodes.shape
     max_blocks = block_tables.shape[1]
-    _reachable(layers.first, block_tables, context_lens, node_starts, accept_nodes, accept_lens)
+    dev, i32 = _place(layers.first), torch.int32
     _check(_HOT_TREE_COMPACT(
         layers.k_ptrs, layers.v_ptrs, layers.num_layers,
-        _int32("block_tables", block_tables, B, max_blocks), max_blocks,
-        _int32("context_lens", context_lens, B), _int32("node_starts", node_starts, B + 1),
-        _int32("accept_nodes", accept_nodes, B, max_nodes),
-        _int32("accept_lens", accept_lens, B), B, max_nodes, layers.num_kv_heads,
-        layers.head_dim, layers.num_blocks, layers.kv_dtype, _stream_int(stream)),
+        _ptr("block_tables", block_tables, i32, B * max_blocks, dev), max_blocks,
+        _ptr("context_lens", context_lens, i32, B, dev),
+        _ptr("node_starts", node_starts, i32, B + 1, dev),
+        _ptr("accept_nodes", accept_nodes, i32, B * max_nodes, dev),
+        _ptr("accept_lens", accept_lens, i32, B, dev), B, max_nodes, layers.num_kv_heads,
+        layers.head_dim, layers.num_blocks, layers.kv_dtype, _raw_stream(stream, dev)),
         "kv_tree_compact")
 
 
