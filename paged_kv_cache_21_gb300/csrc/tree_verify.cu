@@ -11,17 +11,18 @@
 //
 // What decides the result is a comparison with a cumulative sum over up to
 // hundreds of thousands of entries, so the sums must be far finer than the
-// entries' spacing in them: float32 would move one sampled token in a few
-// dozen.  Each thread sums in pairs of floats (two-sum, 2^-48), which costs a
-// tenth of the time of this GPU's double precision units; the few sums over
-// threads run in double.
+// entries' spacing in them: float32 would move one sampled token in a few dozen.
+// Each thread sums in pairs of floats (a sum and its rounding error: 2^-46), and
+// so do the joins over threads and CTAs: this GPU's double precision units would
+// take ten times as long.  Two entries go through one packed instruction.
 //
 // One cluster of CTAs serves a sequence: each CTA takes a contiguous slice of
 // the row, its warps contiguous sub-slices, and the CTAs exchange their sums
 // through distributed shared memory.  All CTAs walk the tree in step, from
 // copies of the tree and of the single probabilities at the drafted tokens
 // (gathered at once, for all nodes) in shared memory.  The CTA, warp and lane
-// that hold the cut then find the token; the row comes from L2 by then.
+// that hold the cut then find the token; the row comes from L2 by then.  The
+// cluster is as large as lets all sequences run at once, two CTAs an SM.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -42,6 +43,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCtasPerSm = 2;
 constexpr int kMaxCluster = 8;           // the portable cluster size
 constexpr int kN = KV_TREE_MAX_NODES;
 
@@ -60,17 +62,107 @@ struct VerifyParams {
     int total, max_nodes, vocab, greedy;
 };
 
-// A float32 sum carried with its rounding error.
-struct Sum2 {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float x, float xe)
-    {
-        const float s = hi + x, b = s - hi;
-        lo += ((hi - (s - b)) + (x - b)) + xe;
-        hi = s;
-    }
+// ------------------------------------------------- pairs of floats, packed pairs
+using u64 = unsigned long long;          // two floats, the first in the low half
+
+__device__ __forceinline__ u64 pack2(float a, float b)
+{
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(u64 x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b)
+{
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 sub2(u64 a, u64 b)
+{
+    u64 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b)
+{
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c)
+{
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A sum and its rounding error.
+struct Pair {
+    float hi, lo;
     __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
+
+__device__ __forceinline__ Pair add(Pair a, Pair b)
+{
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+
+__device__ __forceinline__ Pair shfl(Pair v, int src)
+{
+    return {__shfl_sync(kFull, v.hi, src), __shfl_sync(kFull, v.lo, src)};
+}
+
+__device__ __forceinline__ Pair warp_sum(Pair v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = add(v, Pair{__shfl_xor_sync(kFull, v.hi, o), __shfl_xor_sync(kFull, v.lo, o)});
+    return v;
+}
+
+// Sums up to and with each lane.
+__device__ __forceinline__ Pair warp_scan(Pair v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair up = {__shfl_up_sync(kFull, v.hi, o), __shfl_up_sync(kFull, v.lo, o)};
+        if (lane >= o) v = add(up, v);
+    }
+    return v;
+}
+
+// Two running sums side by side: x plus its error xe, for two entries.
+struct Sum2 {
+    u64 hi = 0ull, lo = 0ull;
+    __device__ __forceinline__ void add(u64 x, u64 xe)
+    {
+        const u64 s = add2(hi, x), b = sub2(s, hi);
+        lo = add2(lo, add2(add2(sub2(hi, sub2(s, b)), sub2(x, b)), xe));
+        hi = s;
+    }
+    __device__ __forceinline__ void add(u64 x)
+    {
+        const u64 s = add2(hi, x), b = sub2(s, hi);
+        lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(x, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ Pair value() const
+    {
+        float h0, h1, l0, l1;
+        unpack2(hi, h0, h1);
+        unpack2(lo, l0, l1);
+        return pkv::add(Pair{h0, l0}, Pair{h1, l1});
+    }
+};
+
+// ------------------------------------------------------------------- weights
 
 // What counts as zero: negative, infinite and NaN entries.
 __device__ __forceinline__ float clean(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
@@ -102,89 +194,65 @@ __device__ __forceinline__ void loadv(const void* row, long long i, float (&x)[V
     }
 }
 
-// The remaining weight of an entry as a float and its error: max(p - a q, 0)
-// with a = ah + al, the product and the difference exact but for 2^-48.
-struct Residual {
-    float ah = 0.f, al = 0.f;            // refusals so far; 0: the target itself
-    __device__ __forceinline__ float2 operator()(float p, float q) const
+// The remaining weights of a node: R_j = max(p_j - a q_j, 0) with a = ah + al, the
+// product and the difference exact but for 2^-46; or p_j without the refused tokens.
+struct Weights {
+    const void* p;
+    const void* q;                       // null: no refusal with a draft
+    float ah, al;
+    const int* gone;                     // refused tokens (no draft)
+    int ngone;
+
+    // one entry, by scalars
+    __device__ __forceinline__ Pair one(int i, float x, float y) const
     {
-        const float ph = __fmul_rn(ah, q);   // not to be contracted into the difference
-        const float pe = fmaf(ah, q, -ph) + al * q;
-        const float s = p - ph, b = s - p;
-        const float e = ((p - (s - b)) + (-ph - b)) - pe;
-        return s + e > 0.f ? make_float2(s, e) : make_float2(0.f, 0.f);
+        x = clean(x);
+        for (int g = 0; g < ngone; ++g)
+            if (gone[g] == i) x = 0.f;
+        if (!q) return {x, 0.f};
+        y = clean(y);
+        const float ph = __fmul_rn(ah, y);       // not to be contracted into the difference
+        const float pe = fmaf(ah, y, -ph) + al * y;
+        const float s = x - ph, b = s - x;
+        const float e = ((x - (s - b)) + (-ph - b)) - pe;
+        return s + e > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
+    }
+    // two entries into a sum, for entries that are not infinite
+    __device__ __forceinline__ void two(u64 x, u64 y, Sum2& sum) const
+    {
+        const u64 nph = mul2(pack2(-ah, -ah), y);
+        const u64 pe = fma2(pack2(al, al), y, fma2(pack2(ah, ah), y, nph));
+        const u64 s = add2(x, nph), b = sub2(s, x);
+        const u64 e = sub2(add2(sub2(x, sub2(s, b)), sub2(nph, b)), pe);
+        float s0, s1, e0, e1;
+        unpack2(s, s0, s1);
+        unpack2(e, e0, e1);
+        const bool k0 = s0 + e0 > 0.f, k1 = s1 + e1 > 0.f;
+        sum.add(pack2(k0 ? s0 : 0.f, k1 ? s1 : 0.f), pack2(k0 ? e0 : 0.f, k1 ? e1 : 0.f));
     }
 };
 
-__device__ __forceinline__ double warp_sum(double v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
-
 // Shared state of a CTA.  Every CTA of a cluster holds the same tree and walk.
 struct Shared {
-    int tok[kN], child[kN], sibling[kN];     // first child and next sibling, -1: none
-    float pv[kN], qv[kN], u[kN];             // p and q of the node's token at its parent
-    int gone[kN];                            // refused tokens of the node (no draft)
+    int par[kN], tok[kN], child[kN], sibling[kN];    // first child and next sibling, -1: none
+    float pv[kN], qv[kN], u[kN];         // p and q of the node's token at its parent
+    bool takes[kN];                      // accepted as its parent's first child
+    int gone[kN];                        // refused tokens of the node (no draft)
     int path[kN];
-    double warp_sums[kWarps];
-    double rank_sums[2][kMaxCluster];
-    float best[2][kMaxCluster];              // greedy: largest entry and where it is
+    Pair warp_sums[kWarps];
+    Pair rank_sums[2][kMaxCluster];
+    float best[2][kMaxCluster];          // greedy: largest entry and where it is
     int best_at[2][kMaxCluster];
     float wbest[kWarps];
     int wbest_at[kWarps];
     double a, Z;
-    int v, next_child, ngone, depth, state, n, t0;
+    int v, next_child, ngone, depth, state, n, t0, token;
 };
 
 enum State { kWalk, kNeedSum, kDone };
 
-// The rows of one node, cut into aligned vectors: entry 0 is element `shift`
-// of its first vector.
-template <bool BF16, int VEC>
-struct Rows {
-    const void* p;
-    const void* q;
-    int vocab;
-    int lead;                                // entries before the first whole vector
-
-    template <typename F>
-    __device__ __forceinline__ void for_each(int lo, int hi, int lane, F&& f) const
-    {
-        // entries lo .. hi of the row; lo is lead + a multiple of 32 * VEC, or 0
-        int i = lo;
-        if (VEC > 1 && lo == 0 && lead > 0) {
-            if (lane < lead && lane < hi) {
-                float x[1] = {load1<BF16>(p, lane)}, y[1] = {q ? load1<BF16>(q, lane) : 0.f};
-                f(lane, 1, x, y);
-            }
-            i = lead;
-        }
-#pragma unroll 4
-        for (int at = i + lane * VEC; at + VEC <= hi; at += 32 * VEC) {
-            float x[VEC], y[VEC];
-            loadv<BF16, VEC>(p, at, x);
-            if (q) {
-                loadv<BF16, VEC>(q, at, y);
-            } else {
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) y[k] = 0.f;
-            }
-            f(at, VEC, x, y);
-        }
-        if (VEC > 1 && hi > i) {
-            const int tail = (hi - i) % VEC, at = hi - tail + lane;
-            if (lane < tail) {
-                float x[1] = {load1<BF16>(p, at)}, y[1] = {q ? load1<BF16>(q, at) : 0.f};
-                f(at, 1, x, y);
-            }
-        }
-    }
-};
-
-// The slice [lo, hi) of warp `w` of `nw` over the whole cluster.
+// The slice [lo, hi) of warp w of nw: `lead` entries before the first whole vector
+// (the first warp's), then steps of 32 vectors, spread evenly.
 __device__ __forceinline__ void warp_slice(int vocab, int lead, int vec, int w, int nw, int& lo,
                                            int& hi)
 {
@@ -197,8 +265,89 @@ __device__ __forceinline__ void warp_slice(int vocab, int lead, int vec, int w, 
     if (lo > hi) lo = hi;
 }
 
+// Every entry of [lo, hi), lanes side by side: whole vectors to `vec(i, x, y)`, the
+// entries before and after them to `one(i, x, y)`.
+template <bool BF16, int VEC, typename FV, typename F1>
+__device__ __forceinline__ void for_slice(const void* p, const void* q, int lead, int lo, int hi,
+                                          int lane, FV&& vec, F1&& one)
+{
+    int i = lo;
+    if (VEC > 1 && lo == 0 && lead > 0) {
+        if (lane < lead && lane < hi) one(lane, load1<BF16>(p, lane), q ? load1<BF16>(q, lane) : 0.f);
+        i = lead;
+    }
+    if (q) {
+#pragma unroll 4
+        for (int at = i + lane * VEC; at + VEC <= hi; at += 32 * VEC) {
+            float x[VEC], y[VEC];
+            loadv<BF16, VEC>(p, at, x);
+            loadv<BF16, VEC>(q, at, y);
+            vec(at, x, y);
+        }
+    } else {
+#pragma unroll 4
+        for (int at = i + lane * VEC; at + VEC <= hi; at += 32 * VEC) {
+            float x[VEC];
+            loadv<BF16, VEC>(p, at, x);
+            vec(at, x, x);
+        }
+    }
+    if (VEC > 1 && hi > i) {
+        const int tail = (hi - i) % VEC, at = hi - tail + lane;
+        if (lane < tail) one(at, load1<BF16>(p, at), q ? load1<BF16>(q, at) : 0.f);
+    }
+}
+
+// Sum of the weights of this thread's entries of [lo, hi).
 template <bool BF16, int VEC>
-__global__ void __launch_bounds__(kThreads) kv_tree_verify_kernel(const VerifyParams prm)
+__device__ __forceinline__ Pair thread_sum(const Weights& w, int lead, int lo, int hi, int lane)
+{
+    Sum2 sum;
+    Pair rest = {0.f, 0.f};
+    auto careful = [&](int i, float x, float y) { rest = add(rest, w.one(i, x, y)); };
+    if (VEC == 1 || w.ngone > 0) {
+        for_slice<BF16, VEC>(
+            w.p, w.q, lead, lo, hi, lane,
+            [&](int i, const float (&x)[VEC], const float (&y)[VEC]) {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) careful(i + k, x[k], y[k]);
+            },
+            careful);
+        return rest;
+    }
+    // negative entries and NaN become zero on the way; the largest bit pattern tells
+    // whether there was an infinite one, for which the thread goes over its entries again
+    int top = 0;
+    for_slice<BF16, VEC>(
+        w.p, w.q, lead, lo, hi, lane,
+        [&](int, const float (&x)[VEC], const float (&y)[VEC]) {
+#pragma unroll
+            for (int k = 0; k + 1 < VEC; k += 2) {
+                top = max(top, max(__float_as_int(x[k]), __float_as_int(x[k + 1])));
+                const u64 xx = pack2(fmaxf(x[k], 0.f), fmaxf(x[k + 1], 0.f));
+                if (w.q) {
+                    top = max(top, max(__float_as_int(y[k]), __float_as_int(y[k + 1])));
+                    w.two(xx, pack2(fmaxf(y[k], 0.f), fmaxf(y[k + 1], 0.f)), sum);
+                } else {
+                    sum.add(xx);
+                }
+            }
+        },
+        careful);
+    if (top < 0x7f800000) return add(sum.value(), rest);
+    rest = {0.f, 0.f};
+    for_slice<BF16, VEC>(
+        w.p, w.q, lead, lo, hi, lane,
+        [&](int i, const float (&x)[VEC], const float (&y)[VEC]) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) careful(i + k, x[k], y[k]);
+        },
+        careful);
+    return rest;
+}
+
+template <bool BF16, int VEC>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(const VerifyParams prm)
 {
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -235,27 +384,33 @@ __global__ void __launch_bounds__(kThreads) kv_tree_verify_kernel(const VerifyPa
     }
     // no CTA writes to another's shared memory before that one has started
     cg::cluster_group::arrival_token started = cluster.barrier_arrive();
-    __shared__ int par[kN];
     if (tid < n) {
         const int p = tree_parent(prm.parents, t0, tid, rank == 0 ? &g_verify_err : nullptr);
-        par[tid] = p;
         const int x = __ldg(prm.tokens + t0 + tid);
+        sh.par[tid] = p;
         sh.tok[tid] = x;
-        sh.pv[tid] = 0.f;
+        bool takes = false;
         if (!prm.greedy && p >= 0 && x >= 0 && x < prm.vocab) {
             const long long prow = t0 + p;
-            sh.pv[tid] = clean(load1<BF16>(prm.target, prow * prm.target_stride + x));
-            sh.qv[tid] = prm.draft ? clean(load1<BF16>(prm.draft, prow * prm.draft_stride + x)) : 1.f;
-            sh.u[tid] = __ldg(prm.accept_u + t0 + tid);
+            const float pv = clean(load1<BF16>(prm.target, prow * prm.target_stride + x));
+            const float qv = prm.draft ? clean(load1<BF16>(prm.draft, prow * prm.draft_stride + x)) : 1.f;
+            const float u = __ldg(prm.accept_u + t0 + tid);
+            sh.pv[tid] = pv;
+            sh.qv[tid] = qv;
+            sh.u[tid] = u;
+            takes = (double)u * (double)qv < (double)pv;
         }
+        sh.takes[tid] = takes;
     }
     __syncthreads();
     if (tid < n) {
         int child = -1, sib = -1;
+        const int mine = sh.par[tid];
+#pragma unroll 4
         for (int j = n - 1; j > tid; --j) {
-            const int p = par[j];
+            const int p = sh.par[j];
             if (p == tid) child = j;
-            if (p >= 0 && p == par[tid]) sib = j;
+            if (p >= 0 && p == mine) sib = j;
         }
         sh.child[tid] = child;
         sh.sibling[tid] = sib;
@@ -281,15 +436,19 @@ __global__ void __launch_bounds__(kThreads) kv_tree_verify_kernel(const VerifyPa
                     sh.next_child = sh.sibling[c];
                     continue;
                 }
-                const double p = sh.pv[c], q = sh.qv[c];
-                double r = p - sh.a * q;
-                if (!prm.draft) {
-                    r = p;
+                bool takes = sh.takes[c];        // (as a first child)
+                double r = 0.0;
+                if (prm.draft ? sh.a > 0.0 : true) {
+                    r = sh.pv[c];
+                    if (prm.draft) {
+                        r -= sh.a * (double)sh.qv[c];
+                        if (r < 0.0) r = 0.0;
+                    }
                     for (int g = 0; g < sh.ngone; ++g)
                         if (sh.gone[g] == x) r = 0.0;
+                    if (sh.a > 0.0 || sh.ngone > 0) takes = (double)sh.u[c] * (double)sh.qv[c] * sh.Z < r;
                 }
-                if (r < 0.0) r = 0.0;
-                if ((double)sh.u[c] * q * sh.Z < r) {
+                if (takes) {
                     sh.v = c;
                     sh.path[sh.depth++] = c;
                     sh.next_child = sh.child[c];
@@ -311,30 +470,25 @@ __global__ void __launch_bounds__(kThreads) kv_tree_verify_kernel(const VerifyPa
             sh.state = state;
         }
         __syncthreads();
-        const int state = sh.state;
-        const int v = sh.v;
+        const int state = sh.state, v = sh.v;
         // ---- one pass over the node's rows
-        Rows<BF16, VEC> rows;
-        rows.p = (const uint8_t*)prm.target + (long long)(t0 + v) * prm.target_stride * ES;
-        Residual res;
-        const double a = sh.a;
-        res.ah = (float)a;
-        res.al = (float)(a - (double)res.ah);
-        rows.q = prm.draft && a > 0.0
-                     ? (const uint8_t*)prm.draft + (long long)(t0 + v) * prm.draft_stride * ES
-                     : nullptr;
-        rows.vocab = prm.vocab;
-        rows.lead = VEC > 1 ? (int)(((16 - ((uintptr_t)rows.p & 15)) & 15) / ES) : 0;
+        const void* p = (const uint8_t*)prm.target + (long long)(t0 + v) * prm.target_stride * ES;
+        const int lead = VEC > 1 ? (int)(((16 - ((uintptr_t)p & 15)) & 15) / ES) : 0;
         int lo, hi;
-        warp_slice(prm.vocab, rows.lead, VEC, rank * kWarps + warp, ranks * kWarps, lo, hi);
+        warp_slice(prm.vocab, lead, VEC, rank * kWarps + warp, ranks * kWarps, lo, hi);
 
         if (prm.greedy) {
             float m = -INFINITY;
             int at = INT32_MAX;
-            rows.for_each(lo, hi, lane, [&](int i, int cnt, const float* x, const float*) {
-                for (int k = 0; k < cnt; ++k)
-                    if (x[k] > m) { m = x[k]; at = i + k; }
-            });
+            auto one = [&](int i, float x, float) {
+                if (x > m) { m = x; at = i; }
+            };
+            for_slice<BF16, VEC>(p, nullptr, lead, lo, hi, lane,
+                                 [&](int i, const float (&x)[VEC], const float (&)[VEC]) {
+#pragma unroll
+                                     for (int k = 0; k < VEC; ++k) one(i + k, x[k], 0.f);
+                                 },
+                                 one);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const float om = __shfl_xor_sync(kFull, m, o);
@@ -343,195 +497,180 @@ __global__ void __launch_bounds__(kThreads) kv_tree_verify_kernel(const VerifyPa
             }
             if (lane == 0) { sh.wbest[warp] = m; sh.wbest_at[warp] = at; }
             __syncthreads();
-            if (tid == 0) {
-                for (int w = 1; w < kWarps; ++w)
-                    if (sh.wbest[w] > m || (sh.wbest[w] == m && sh.wbest_at[w] < at)) {
-                        m = sh.wbest[w];
-                        at = sh.wbest_at[w];
-                    }
-                for (int r = 0; r < ranks; ++r) {
-                    Shared* other = cluster.map_shared_rank(&sh, r);
+            auto join = [&](int width) {     // over the first `width` lanes of a warp
+                for (int o = width / 2; o > 0; o >>= 1) {
+                    const float om = __shfl_xor_sync(kFull, m, o);
+                    const int oa = __shfl_xor_sync(kFull, at, o);
+                    if (om > m || (om == m && oa < at)) { m = om; at = oa; }
+                }
+            };
+            if (warp == 0) {
+                m = sh.wbest[lane & (kWarps - 1)];
+                at = sh.wbest_at[lane & (kWarps - 1)];
+                join(kWarps);
+                if (lane < ranks) {
+                    Shared* other = cluster.map_shared_rank(&sh, lane);
                     other->best[phase][rank] = m;
                     other->best_at[phase][rank] = at;
                 }
             }
             cluster.sync();
-            m = -INFINITY;
-            at = INT32_MAX;
-            for (int r = 0; r < ranks; ++r)
-                if (sh.best[phase][r] > m || (sh.best[phase][r] == m && sh.best_at[phase][r] < at)) {
-                    m = sh.best[phase][r];
-                    at = sh.best_at[phase][r];
+            if (warp == 0) {
+                m = -INFINITY;
+                at = INT32_MAX;
+                if (lane < ranks) {
+                    m = sh.best[phase][lane];
+                    at = sh.best_at[phase][lane];
                 }
-            if (at == INT32_MAX) at = 0;         // nothing but -inf and NaN
+                join(kMaxCluster);
+                if (lane == 0) {
+                    if (at == INT32_MAX) at = 0;         // nothing but -inf and NaN
+                    int c = sh.next_child;
+                    while (c >= 0 && sh.tok[c] != at) c = sh.sibling[c];
+                    if (c >= 0) {
+                        sh.v = c;
+                        sh.path[sh.depth++] = c;
+                        sh.next_child = sh.child[c];
+                    }
+                    sh.state = c >= 0 ? kWalk : kDone;
+                    sh.token = at;
+                }
+            }
             phase ^= 1;
-            if (tid == 0) {
-                int c = sh.next_child;
-                while (c >= 0 && sh.tok[c] != at) c = sh.sibling[c];
-                if (c >= 0) {
-                    sh.v = c;
-                    sh.path[sh.depth++] = c;
-                    sh.next_child = sh.child[c];
-                }
-                sh.state = c >= 0 ? kWalk : kDone;
-            }
             __syncthreads();
-            if (sh.state == kDone) {
-                if (tid == 0 && rank == 0) sh.gone[0] = at;
-                __syncthreads();
-                break;
-            }
+            if (sh.state == kDone) break;
             continue;
         }
 
-        const int ngone = prm.draft ? 0 : sh.ngone;
-        auto weight = [&](int i, float x, float y) -> float2 {
-            float w = clean(x);
-            for (int g = 0; g < ngone; ++g)
-                if (sh.gone[g] == i) w = 0.f;
-            return res(w, clean(y));
-        };
-        Sum2 acc;
-        rows.for_each(lo, hi, lane, [&](int i, int cnt, const float* x, const float* y) {
-            for (int k = 0; k < cnt; ++k) {
-                const float2 w = weight(i + k, x[k], y[k]);
-                acc.add(w.x, w.y);
-            }
-        });
-        const double wsum = warp_sum(acc.value());
-        if (lane == 0) sh.warp_sums[warp] = wsum;
+        Weights w;
+        const double a = sh.a;
+        w.p = p;
+        w.q = prm.draft && a > 0.0
+                  ? (const uint8_t*)prm.draft + (long long)(t0 + v) * prm.draft_stride * ES
+                  : nullptr;
+        w.ah = (float)a;
+        w.al = (float)(a - (double)w.ah);
+        w.gone = sh.gone;
+        w.ngone = prm.draft ? 0 : sh.ngone;
+        const Pair ws = warp_sum(thread_sum<BF16, VEC>(w, lead, lo, hi, lane));
+        if (lane == 0) sh.warp_sums[warp] = ws;
         __syncthreads();
-        if (tid == 0) {
-            double t = 0.0;
-            for (int w = 0; w < kWarps; ++w) t += sh.warp_sums[w];
-            for (int r = 0; r < ranks; ++r)
-                cluster.map_shared_rank(&sh, r)->rank_sums[phase][rank] = t;
+        if (warp == 0) {
+            Pair t = lane < kWarps ? sh.warp_sums[lane] : Pair{0.f, 0.f};
+            t = warp_sum(t);
+            if (lane < ranks) cluster.map_shared_rank(&sh, lane)->rank_sums[phase][rank] = t;
         }
         cluster.sync();
-        double total = 0.0;
-        for (int r = 0; r < ranks; ++r) total += sh.rank_sums[phase][r];
+        // (every warp) the sums up to each CTA
+        const Pair mine = lane < ranks ? sh.rank_sums[phase][lane] : Pair{0.f, 0.f};
+        const Pair upto = warp_scan(mine, lane);
+        const double total = shfl(upto, ranks - 1).value();
+        phase ^= 1;
         if (state == kNeedSum) {
             if (tid == 0) sh.Z = total;
-            phase ^= 1;
             continue;
         }
-        if (total <= 0.0 && (a > 0.0 || ngone > 0)) {
+        if (!(total > 0.0) && (a > 0.0 || w.ngone > 0)) {
             // nothing is left of the target once the refused children are out:
             // the token comes from the target itself
             if (tid == 0) {
                 sh.a = 0.0;
                 sh.ngone = 0;
             }
-            phase ^= 1;
             continue;
         }
-        // ---- the first entry whose cumulative sum is above u * total
+        // ---- the first entry whose cumulative sum is above u * total: the CTA, the
+        // warp, the 32 vectors, the lane, the entry
         const double t = (double)__ldg(prm.sample_u + s) * total;
-        double before = 0.0;
-        int owner = -1, last = -1;
-        double owner_before = 0.0, last_before = 0.0;
-        for (int r = 0; r < ranks; ++r) {
-            const double x = sh.rank_sums[phase][r];
-            if (x > 0.0) {
-                last = r;
-                last_before = before;
-            }
-            if (owner < 0 && before + x > t) {
-                owner = r;
-                owner_before = before;
-            }
-            before += x;
-        }
-        if (owner < 0) {                 // u >= 1 or rounding: the last entry there is
-            owner = last;
-            owner_before = last_before;
-        }
-        if (owner < 0) {                 // no weight at all
-            if (tid == 0) sh.gone[0] = -1;
+        const unsigned over = __ballot_sync(kFull, lane < ranks && upto.value() > t);
+        const unsigned some = __ballot_sync(kFull, lane < ranks && mine.hi > 0.f);
+        if (some == 0) {                 // no weight at all
             if (rank != 0) return;
+            if (tid == 0) sh.token = -1;
             __syncthreads();
             break;
         }
+        // (u >= 1, or rounding: the last CTA with any weight)
+        const int owner = over ? __ffs(over) - 1 : 31 - __clz(some);
         if (rank != owner) return;
-        // the warp, then the 32 * VEC entries, then the entry
-        int ow = -1, lw = -1;
-        double b = owner_before, ow_before = 0.0, lw_before = 0.0;
-        for (int w = 0; w < kWarps; ++w) {
-            const double x = sh.warp_sums[w];
-            if (x > 0.0) {
-                lw = w;
-                lw_before = b;
-            }
-            if (ow < 0 && b + x > t) {
-                ow = w;
-                ow_before = b;
-            }
-            b += x;
+        Pair before = {0.f, 0.f};
+        {
+            const Pair b = shfl(upto, owner > 0 ? owner - 1 : 0);
+            if (owner > 0) before = b;
         }
-        if (ow < 0) {
-            ow = lw;
-            ow_before = lw_before;
-        }
+        const Pair wmine = lane < kWarps ? sh.warp_sums[lane] : Pair{0.f, 0.f};
+        const Pair wupto = add(before, warp_scan(wmine, lane));
+        const unsigned wover = __ballot_sync(kFull, lane < kWarps && wupto.value() > t);
+        const unsigned wsome = __ballot_sync(kFull, lane < kWarps && wmine.hi > 0.f);
+        const int ow = wover ? __ffs(wover) - 1 : 31 - __clz(wsome);
+        const Pair wb = shfl(wupto, ow > 0 ? ow - 1 : 0);
         if (warp == ow) {
-            double run = ow_before;
-            int found = -1, last_pos = -1;
+            Pair run = ow > 0 ? wb : before;
+            int found = -1, last = -1;
+            // four groups of 32 vectors at a time: sums of each, then the cut in one
             for (int g0 = lo; g0 < hi && found < 0;) {
-                // a group of entries in row order: the lead, whole vectors, or the tail
-                const int first = VEC > 1 && g0 == 0 && rows.lead > 0 ? min(rows.lead, hi)
-                                                                      : min(g0 + 32 * VEC, hi);
-                const int cnt = first - g0;
-                const int per = (cnt + 31) / 32;         // entries of a lane, in order
-                double mine = 0.0;
-                int lastk = -1;
-                for (int k = 0; k < per; ++k) {
-                    const int i = g0 + lane * per + k;
-                    if (i < first) {
-                        const float2 w = weight(i, load1<BF16>(rows.p, i),
-                                                rows.q ? load1<BF16>(rows.q, i) : 0.f);
-                        mine += (double)w.x + (double)w.y;
-                        if (w.x > 0.f) lastk = i;
-                    }
-                }
-                double incl = mine;
+                const bool head = VEC > 1 && g0 == 0 && lead > 0;
+                const int span = head ? min(lead, hi) : 32 * VEC;
+                const int groups = head ? 1 : min(4, (hi - g0 + span - 1) / span);
+                Pair sums[4];
+                int lasts[4];
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double up = __shfl_up_sync(kFull, incl, o);
-                    if (lane >= o) incl += up;
-                }
-                const unsigned hit = __ballot_sync(kFull, run + incl > t);
-                if (hit) {
-                    const int src = __ffs(hit) - 1;
-                    if (lane == src) {
-                        double c = run + (incl - mine);
-                        for (int k = 0; k < per; ++k) {
-                            const int i = g0 + lane * per + k;
-                            if (i >= first) break;
-                            const float2 w = weight(i, load1<BF16>(rows.p, i),
-                                                    rows.q ? load1<BF16>(rows.q, i) : 0.f);
-                            c += (double)w.x + (double)w.y;
-                            if (c > t) {
-                                found = i;
-                                break;
-                            }
+                for (int q = 0; q < 4; ++q) {
+                    sums[q] = {0.f, 0.f};
+                    lasts[q] = -1;
+                    if (q >= groups) continue;
+                    // entries of a lane, in order
+                    const int first = g0 + q * span, end = min(first + span, hi);
+                    const int per = (end - first + 31) / 32;
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        const int i = first + lane * per + k;
+                        if (k < per && i < end) {
+                            const Pair x = w.one(i, load1<BF16>(w.p, i), w.q ? load1<BF16>(w.q, i) : 0.f);
+                            sums[q] = add(sums[q], x);
+                            if (x.hi > 0.f) lasts[q] = i;
                         }
-                        if (found < 0) found = lastk;    // rounding: the lane's last entry
                     }
-                    found = __shfl_sync(kFull, found, src);
                 }
-                const int lp = __reduce_max_sync(kFull, lastk);
-                if (lp >= 0) last_pos = lp;
-                run += __shfl_sync(kFull, incl, 31);
-                g0 = first;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q >= groups || found >= 0) continue;
+                    const Pair incl = add(run, warp_scan(sums[q], lane));
+                    const unsigned hit = __ballot_sync(kFull, incl.value() > t);
+                    if (hit) {
+                        const int src = __ffs(hit) - 1;
+                        const Pair b = shfl(incl, src > 0 ? src - 1 : 0);
+                        if (lane == src) {
+                            const int first = g0 + q * span, end = min(first + span, hi);
+                            const int per = (end - first + 31) / 32;
+                            Pair c = src > 0 ? b : run;
+                            for (int k = 0; k < per; ++k) {
+                                const int i = first + lane * per + k;
+                                if (i >= end) break;
+                                c = add(c, w.one(i, load1<BF16>(w.p, i), w.q ? load1<BF16>(w.q, i) : 0.f));
+                                if (c.value() > t) {
+                                    found = i;
+                                    break;
+                                }
+                            }
+                            if (found < 0) found = lasts[q];     // rounding: the lane's last entry
+                        }
+                        found = __shfl_sync(kFull, found, src);
+                    }
+                    last = max(last, __reduce_max_sync(kFull, lasts[q]));
+                    run = shfl(incl, 31);
+                }
+                g0 += head ? span : groups * span;
             }
-            if (found < 0) found = last_pos;
-            if (lane == 0) sh.gone[0] = found;
+            if (found < 0) found = last;
+            if (lane == 0) sh.token = found;
         }
         __syncthreads();
         break;
     }
     // ---- results, from the one CTA that is left (greedy: the first)
     if (prm.greedy && rank != 0) return;
-    const int depth = sh.depth, token = sh.gone[0];
+    const int depth = sh.depth, token = sh.token;
     if (tid == 0) prm.lens[s] = depth;
     for (int i = tid; i < prm.max_nodes; i += kThreads) {
         const size_t at = (size_t)s * prm.max_nodes + i;
@@ -617,9 +756,10 @@ extern "C" int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32
     const bool vec = !draft_probs ||
                      (((uintptr_t)target_probs - (uintptr_t)draft_probs) % 16 == 0 &&
                       (target_stride - draft_stride) * (int64_t)es % 16 == 0);
+    // all sequences at once, where they fit: a second wave would wait for the first
+    // one's walks (64 trees, 128000 entries: 139 us with clusters of 8)
     int cluster = kMaxCluster;
-    while (cluster > 1 && (long long)num_seqs * cluster > INT32_MAX) cluster /= 2;
-    if ((long long)num_seqs * cluster > INT32_MAX) return KV_ERR_TOO_LARGE;
+    while (cluster > 1 && (long long)num_seqs * cluster > kCtasPerSm * num_sms_current()) cluster /= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t err =
         bf16 ? (vec ? launch_verify<true, 8>(p, num_seqs, cluster, st)
