@@ -103,7 +103,6 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c)
 // A sum and its rounding error.
 struct Pair {
     float hi, lo;
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
 
 __device__ __forceinline__ Pair add(Pair a, Pair b)
@@ -112,6 +111,20 @@ __device__ __forceinline__ Pair add(Pair a, Pair b)
     const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
     const float h = s + e;
     return {h, e - (h - s)};
+}
+
+__device__ __forceinline__ bool above(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.f; }
+
+__device__ __forceinline__ Pair mul(Pair a, float b)
+{
+    const float h = __fmul_rn(a.hi, b), e = fmaf(a.hi, b, -h) + a.lo * b, r = h + e;
+    return {r, e - (r - h)};
+}
+
+__device__ __forceinline__ Pair mul(Pair a, Pair b)
+{
+    const float h = __fmul_rn(a.hi, b.hi), e = fmaf(a.hi, b.hi, -h) + (a.hi * b.lo + a.lo * b.hi), r = h + e;
+    return {r, e - (r - h)};
 }
 
 __device__ __forceinline__ Pair shfl(Pair v, int src)
@@ -217,7 +230,8 @@ struct Weights {
         const float e = ((x - (s - b)) + (-ph - b)) - pe;
         return s + e > 0.f ? Pair{s, e} : Pair{0.f, 0.f};
     }
-    // two entries into a sum, for entries that are not infinite
+    // two entries into a sum, for entries of q that are finite and not negative (a
+    // negative or NaN entry of p adds nothing; an infinite one makes the sum so)
     __device__ __forceinline__ void two(u64 x, u64 y, Sum2& sum) const
     {
         const u64 nph = mul2(pack2(-ah, -ah), y);
@@ -227,8 +241,7 @@ struct Weights {
         float s0, s1, e0, e1;
         unpack2(s, s0, s1);
         unpack2(e, e0, e1);
-        const bool k0 = s0 + e0 > 0.f, k1 = s1 + e1 > 0.f;
-        sum.add(pack2(k0 ? s0 : 0.f, k1 ? s1 : 0.f), pack2(k0 ? e0 : 0.f, k1 ? e1 : 0.f));
+        sum.add(pack2(fmaxf(s0, 0.f), fmaxf(s1, 0.f)), pack2(s0 > 0.f ? e0 : 0.f, s1 > 0.f ? e1 : 0.f));
     }
 };
 
@@ -239,13 +252,12 @@ struct Shared {
     bool takes[kN];                      // accepted as its parent's first child
     int gone[kN];                        // refused tokens of the node (no draft)
     int path[kN];
-    Pair warp_sums[kWarps];
-    Pair rank_sums[2][kMaxCluster];
+    Pair sums[2][kMaxCluster * kWarps];  // of every warp of the cluster
     float best[2][kMaxCluster];          // greedy: largest entry and where it is
     int best_at[2][kMaxCluster];
     float wbest[kWarps];
     int wbest_at[kWarps];
-    double a, Z;
+    Pair a, Z;
     int v, next_child, ngone, depth, state, n, t0, token;
 };
 
@@ -315,26 +327,25 @@ __device__ __forceinline__ Pair thread_sum(const Weights& w, int lead, int lo, i
             careful);
         return rest;
     }
-    // negative entries and NaN become zero on the way; the largest bit pattern tells
-    // whether there was an infinite one, for which the thread goes over its entries again
-    int top = 0;
+    // negative entries and NaN become zero on the way; for an infinite one, which
+    // shows in the sum or in q's largest, the thread goes over its entries again
+    float top = 0.f;
     for_slice<BF16, VEC>(
         w.p, w.q, lead, lo, hi, lane,
         [&](int, const float (&x)[VEC], const float (&y)[VEC]) {
 #pragma unroll
             for (int k = 0; k + 1 < VEC; k += 2) {
-                top = max(top, max(__float_as_int(x[k]), __float_as_int(x[k + 1])));
-                const u64 xx = pack2(fmaxf(x[k], 0.f), fmaxf(x[k + 1], 0.f));
                 if (w.q) {
-                    top = max(top, max(__float_as_int(y[k]), __float_as_int(y[k + 1])));
-                    w.two(xx, pack2(fmaxf(y[k], 0.f), fmaxf(y[k + 1], 0.f)), sum);
+                    top = fmaxf(top, fmaxf(y[k], y[k + 1]));
+                    w.two(pack2(x[k], x[k + 1]), pack2(fmaxf(y[k], 0.f), fmaxf(y[k + 1], 0.f)), sum);
                 } else {
-                    sum.add(xx);
+                    sum.add(pack2(fmaxf(x[k], 0.f), fmaxf(x[k + 1], 0.f)));
                 }
             }
         },
         careful);
-    if (top < 0x7f800000) return add(sum.value(), rest);
+    const Pair fast = sum.value();
+    if (top < INFINITY && fast.hi < INFINITY) return add(fast, rest);
     rest = {0.f, 0.f};
     for_slice<BF16, VEC>(
         w.p, w.q, lead, lo, hi, lane,
@@ -366,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(co
         sh.v = 0;
         sh.depth = 1;
         sh.ngone = 0;
-        sh.a = 0.0;
-        sh.Z = 1.0;
+        sh.a = {0.f, 0.f};
+        sh.Z = {1.f, 0.f};
         sh.path[0] = 0;
     }
     __syncthreads();
@@ -398,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(co
             sh.pv[tid] = pv;
             sh.qv[tid] = qv;
             sh.u[tid] = u;
-            takes = (double)u * (double)qv < (double)pv;
+            takes = above(Pair{pv, 0.f}, mul(Pair{u, 0.f}, qv));
         }
         sh.takes[tid] = takes;
     }
@@ -437,32 +448,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(co
                     continue;
                 }
                 bool takes = sh.takes[c];        // (as a first child)
-                double r = 0.0;
-                if (prm.draft ? sh.a > 0.0 : true) {
-                    r = sh.pv[c];
+                const bool refused = prm.draft ? sh.a.hi > 0.f : sh.ngone > 0;
+                Pair r = {sh.pv[c], 0.f};
+                if (refused) {
                     if (prm.draft) {
-                        r -= sh.a * (double)sh.qv[c];
-                        if (r < 0.0) r = 0.0;
+                        const Pair aq = mul(sh.a, sh.qv[c]);
+                        r = add(r, Pair{-aq.hi, -aq.lo});
                     }
                     for (int g = 0; g < sh.ngone; ++g)
-                        if (sh.gone[g] == x) r = 0.0;
-                    if (sh.a > 0.0 || sh.ngone > 0) takes = (double)sh.u[c] * (double)sh.qv[c] * sh.Z < r;
+                        if (sh.gone[g] == x) r = {0.f, 0.f};
+                    takes = r.hi > 0.f && above(r, mul(mul(Pair{sh.u[c], 0.f}, sh.qv[c]), sh.Z));
                 }
                 if (takes) {
                     sh.v = c;
                     sh.path[sh.depth++] = c;
                     sh.next_child = sh.child[c];
-                    sh.a = 0.0;
-                    sh.Z = 1.0;
+                    sh.a = {0.f, 0.f};
+                    sh.Z = {1.f, 0.f};
                     sh.ngone = 0;
                 } else {
                     sh.next_child = sh.sibling[c];
                     if (prm.draft) {
-                        sh.a += sh.Z;
+                        sh.a = add(sh.a, sh.Z);
                         // the last child's refusal is summed by the final pass
                         if (sh.next_child >= 0) state = kNeedSum;
                     } else {
-                        sh.Z -= r;
+                        sh.Z = add(sh.Z, Pair{-r.hi, -r.lo});
                         sh.gone[sh.ngone++] = x;
                     }
                 }
@@ -543,127 +554,130 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(co
         }
 
         Weights w;
-        const double a = sh.a;
+        const Pair a = sh.a;
         w.p = p;
-        w.q = prm.draft && a > 0.0
+        w.q = prm.draft && a.hi > 0.f
                   ? (const uint8_t*)prm.draft + (long long)(t0 + v) * prm.draft_stride * ES
                   : nullptr;
-        w.ah = (float)a;
-        w.al = (float)(a - (double)w.ah);
+        w.ah = a.hi;
+        w.al = a.lo;
         w.gone = sh.gone;
         w.ngone = prm.draft ? 0 : sh.ngone;
+        // every warp's sum goes to every CTA
         const Pair ws = warp_sum(thread_sum<BF16, VEC>(w, lead, lo, hi, lane));
-        if (lane == 0) sh.warp_sums[warp] = ws;
-        __syncthreads();
-        if (warp == 0) {
-            Pair t = lane < kWarps ? sh.warp_sums[lane] : Pair{0.f, 0.f};
-            t = warp_sum(t);
-            if (lane < ranks) cluster.map_shared_rank(&sh, lane)->rank_sums[phase][rank] = t;
-        }
+        if (lane < ranks) cluster.map_shared_rank(&sh, lane)->sums[phase][rank * kWarps + warp] = ws;
         cluster.sync();
-        // (every warp) the sums up to each CTA
-        const Pair mine = lane < ranks ? sh.rank_sums[phase][lane] : Pair{0.f, 0.f};
-        const Pair upto = warp_scan(mine, lane);
-        const double total = shfl(upto, ranks - 1).value();
+        // the sums up to each warp: four consecutive warps a lane
+        constexpr int kPer = kMaxCluster * kWarps / 32;
+        Pair part[kPer], upto = {0.f, 0.f};
+        const Pair* sums = sh.sums[phase];
         phase ^= 1;
+        if (state == kNeedSum && warp != 0) continue;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = lane * kPer + k;
+            part[k] = i < ranks * kWarps ? sums[i] : Pair{0.f, 0.f};
+            upto = add(upto, part[k]);
+        }
+        const bool any = upto.hi > 0.f;
+        upto = warp_scan(upto, lane);
+        const Pair total = shfl(upto, 31);
         if (state == kNeedSum) {
             if (tid == 0) sh.Z = total;
             continue;
         }
-        if (!(total > 0.0) && (a > 0.0 || w.ngone > 0)) {
+        if (!(total.hi > 0.f) && (a.hi > 0.f || w.ngone > 0)) {
             // nothing is left of the target once the refused children are out:
             // the token comes from the target itself
             if (tid == 0) {
-                sh.a = 0.0;
+                sh.a = {0.f, 0.f};
                 sh.ngone = 0;
             }
             continue;
         }
-        // ---- the first entry whose cumulative sum is above u * total: the CTA, the
-        // warp, the 32 vectors, the lane, the entry
-        const double t = (double)__ldg(prm.sample_u + s) * total;
-        const unsigned over = __ballot_sync(kFull, lane < ranks && upto.value() > t);
-        const unsigned some = __ballot_sync(kFull, lane < ranks && mine.hi > 0.f);
+        // ---- the first entry whose cumulative sum is above t = u * total: the warp of
+        // the cluster whose slice holds it; then that CTA's warps, in equal shares of
+        // the slice, look for it, and the lanes of the one that has it
+        const Pair t = mul(total, fmaxf(__ldg(prm.sample_u + s), 0.f));
+        const unsigned some = __ballot_sync(kFull, any);
         if (some == 0) {                 // no weight at all
             if (rank != 0) return;
             if (tid == 0) sh.token = -1;
             __syncthreads();
             break;
         }
-        // (u >= 1, or rounding: the last CTA with any weight)
-        const int owner = over ? __ffs(over) - 1 : 31 - __clz(some);
-        if (rank != owner) return;
-        Pair before = {0.f, 0.f};
+        const unsigned over = __ballot_sync(kFull, above(upto, t));
+        // (u >= 1, or rounding: the last warp with any weight)
+        const int src = over ? __ffs(over) - 1 : 31 - __clz(some);
+        Pair run = shfl(upto, src > 0 ? src - 1 : 0);
+        if (src == 0) run = {0.f, 0.f};
+        int ow = -1;
         {
-            const Pair b = shfl(upto, owner > 0 ? owner - 1 : 0);
-            if (owner > 0) before = b;
-        }
-        const Pair wmine = lane < kWarps ? sh.warp_sums[lane] : Pair{0.f, 0.f};
-        const Pair wupto = add(before, warp_scan(wmine, lane));
-        const unsigned wover = __ballot_sync(kFull, lane < kWarps && wupto.value() > t);
-        const unsigned wsome = __ballot_sync(kFull, lane < kWarps && wmine.hi > 0.f);
-        const int ow = wover ? __ffs(wover) - 1 : 31 - __clz(wsome);
-        const Pair wb = shfl(wupto, ow > 0 ? ow - 1 : 0);
-        if (warp == ow) {
-            Pair run = ow > 0 ? wb : before;
-            int found = -1, last = -1;
-            // four groups of 32 vectors at a time: sums of each, then the cut in one
-            for (int g0 = lo; g0 < hi && found < 0;) {
-                const bool head = VEC > 1 && g0 == 0 && lead > 0;
-                const int span = head ? min(lead, hi) : 32 * VEC;
-                const int groups = head ? 1 : min(4, (hi - g0 + span - 1) / span);
-                Pair sums[4];
-                int lasts[4];
+            int pick = -1, last = 0;
+            Pair c = run, b = run, lb = run;
+            if (lane == src) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    sums[q] = {0.f, 0.f};
-                    lasts[q] = -1;
-                    if (q >= groups) continue;
-                    // entries of a lane, in order
-                    const int first = g0 + q * span, end = min(first + span, hi);
-                    const int per = (end - first + 31) / 32;
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const int i = first + lane * per + k;
-                        if (k < per && i < end) {
-                            const Pair x = w.one(i, load1<BF16>(w.p, i), w.q ? load1<BF16>(w.q, i) : 0.f);
-                            sums[q] = add(sums[q], x);
-                            if (x.hi > 0.f) lasts[q] = i;
-                        }
+                for (int k = 0; k < kPer; ++k) {
+                    const Pair up = add(c, part[k]);
+                    if (part[k].hi > 0.f) {
+                        last = k;
+                        lb = c;
                     }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q >= groups || found >= 0) continue;
-                    const Pair incl = add(run, warp_scan(sums[q], lane));
-                    const unsigned hit = __ballot_sync(kFull, incl.value() > t);
-                    if (hit) {
-                        const int src = __ffs(hit) - 1;
-                        const Pair b = shfl(incl, src > 0 ? src - 1 : 0);
-                        if (lane == src) {
-                            const int first = g0 + q * span, end = min(first + span, hi);
-                            const int per = (end - first + 31) / 32;
-                            Pair c = src > 0 ? b : run;
-                            for (int k = 0; k < per; ++k) {
-                                const int i = first + lane * per + k;
-                                if (i >= end) break;
-                                c = add(c, w.one(i, load1<BF16>(w.p, i), w.q ? load1<BF16>(w.q, i) : 0.f));
-                                if (c.value() > t) {
-                                    found = i;
-                                    break;
-                                }
-                            }
-                            if (found < 0) found = lasts[q];     // rounding: the lane's last entry
-                        }
-                        found = __shfl_sync(kFull, found, src);
+                    if (pick < 0 && above(up, t)) {
+                        pick = k;
+                        b = c;
                     }
-                    last = max(last, __reduce_max_sync(kFull, lasts[q]));
-                    run = shfl(incl, 31);
+                    c = up;
                 }
-                g0 += head ? span : groups * span;
+                if (pick < 0) {
+                    pick = last;
+                    b = lb;
+                }
             }
-            if (found < 0) found = last;
-            if (lane == 0) sh.token = found;
+            ow = src * kPer + __shfl_sync(kFull, pick, src);
+            run = shfl(b, src);
+        }
+        if (rank != ow / kWarps) return;
+        warp_slice(prm.vocab, lead, VEC, ow, ranks * kWarps, lo, hi);
+        // a share's sum, lanes side by side
+        const int per = (hi - lo + kWarps - 1) / kWarps;
+        int from = lo + warp * per, end = min(from + per, hi);
+        Pair sum = {0.f, 0.f};
+#pragma unroll 4
+        for (int i = from + lane; i < end; i += 32)
+            sum = add(sum, w.one(i, load1<BF16>(w.p, i), w.q ? load1<BF16>(w.q, i) : 0.f));
+        sum = warp_sum(sum);
+        Pair* shares = sh.sums[phase];           // (the exchange after next is not to come)
+        if (lane == 0) shares[warp] = sum;
+        __syncthreads();
+        // `of` things with a sum each, one a lane: the one that holds the cut, and `run`
+        // up to it.  (Rounding may leave none above t: the last with any weight.)
+        auto cut = [&](Pair mine, Pair& upto_it) -> int {
+            const Pair incl = add(upto_it, warp_scan(mine, lane));
+            const unsigned hit = __ballot_sync(kFull, above(incl, t));
+            const unsigned pos = __ballot_sync(kFull, mine.hi > 0.f);
+            const int l = hit ? __ffs(hit) - 1 : pos ? 31 - __clz(pos) : 0;
+            const Pair before = shfl(incl, l > 0 ? l - 1 : 0);
+            if (l > 0) upto_it = before;
+            return l;
+        };
+        const int share = cut(lane < kWarps ? shares[lane] : Pair{0.f, 0.f}, run);
+        if (warp == min(share, kWarps - 1)) {
+            // the warp's entries in equal consecutive shares of the lanes, until a share
+            // is one entry
+            int cnt = end - from;
+            while (true) {
+                const int each = (cnt + 31) / 32, i0 = from + lane * each, i1 = min(i0 + each, from + cnt);
+                Pair x = {0.f, 0.f};
+#pragma unroll 4
+                for (int i = i0; i < i1; ++i)
+                    x = add(x, w.one(i, load1<BF16>(w.p, i), w.q ? load1<BF16>(w.q, i) : 0.f));
+                const int l = cut(x, run);
+                from += l * each;
+                cnt = min(each, cnt - l * each);
+                if (each <= 1) break;
+            }
+            if (lane == 0) sh.token = min(from, prm.vocab - 1);
         }
         __syncthreads();
         break;
