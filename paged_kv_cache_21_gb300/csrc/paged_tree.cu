@@ -70,17 +70,18 @@ namespace {
 
 constexpr int kTile = 128;                      // rows of a tile: M of every MMA
 constexpr uint32_t kTmemCols = 512;             // S0, S1, O0, O1: 128 columns each
-
-// A stream's chunks: every second one, or all.
-constexpr int chunk_step(int tiles) { return tiles == 1 ? 2 : 1; }
+constexpr int kSoftWarps = 16;                  // softmax: 2 streams x 2 halves of the keys x 4
 
 template <int D, bool FP8, int TILES>
 struct Geo {
     static constexpr int kD = D;
     static constexpr bool kFp8 = FP8;
-    static constexpr int kPrepWarp = 11;                     // first of the prep / widening warps
-    static constexpr int kPrepWarps = FP8 ? 4 : 1;
-    static constexpr int kWarps = kPrepWarp + kPrepWarps;
+    static constexpr int kCopyWarp = kSoftWarps;
+    static constexpr int kMmaWarp = kCopyWarp + 1;
+    static constexpr int kPrepWarp = kMmaWarp + 1;           // first of the prep / widening warps
+    static constexpr int kPrepWarps = FP8 ? 2 : 1;
+    static constexpr int kCopyV = kPrepWarp + 1;             // (bf16) the copies of V
+    static constexpr int kWarps = kPrepWarp + 2;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kBoxes = D / 64;                    // 128-byte column groups of a row
     static constexpr int kSlot = kBoxes * kRegion;           // K or V of a chunk, 2 bytes each
@@ -88,6 +89,8 @@ struct Geo {
     static constexpr int kPageBytes = kBlock * D * (FP8 ? 1 : 2);
     static constexpr int kRawSlot = kPages * kBlock * D;     // E4M3 codes of K or V of a chunk
     static constexpr int kScale = 128 / D;
+    // the two streams take the chunks in turn, or both take each
+    static constexpr int kChunkStep = TILES == 1 ? 2 : 1;
     static constexpr int kKSlots = (FP8 ? 3 : 2) * kScale, kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
     static constexpr int kRawV = !FP8 ? 0 : 2 * kScale;
     static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
@@ -117,16 +120,18 @@ struct Geo {
     static constexpr int B_OFULL = B_PVDONE + 2;             // both accumulators are complete
     static constexpr int B_OFREE = B_OFULL + 1;              // + segment & 1: they have been read
     static constexpr int B_ML = B_OFREE + 2;                 // the streams' (max, sum) are written
-    static constexpr int B_END = B_ML + 1;                   // + stream: all its MMAs are done
-    static constexpr int B_STALL = B_END + 2;                // nothing arrives (the test hook)
+    static constexpr int B_MAX = B_ML + 1;                   // + stream * 4 + warp's rows: both maxima are written
+    static constexpr int B_END = B_MAX + 8;                  // all MMAs are done
+    static constexpr int B_STALL = B_END + 1;                // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kAncOff = kMiscOff + 64;            // [2][kN][4] words
     static constexpr int kPtrOff = kAncOff + 2 * kN * 16;    // [kN] bytes used by pointer jumping
     static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
     static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
-    static constexpr int kMlOff = kBadOff + 2 * kPrepWarps * 16;  // [2][kTile] float2 (TILES == 1)
-    static constexpr int kQfacOff = kMlOff + (TILES == 1 ? 2 * kTile * 8 : 0);
+    static constexpr int kMaxOff = kBadOff + 2 * kPrepWarps * 16;    // [2 streams][2 halves][kTile] floats
+    static constexpr int kMlOff = kMaxOff + 4 * kTile * 4;   // [2 streams][2 halves][kTile] float2
+    static constexpr int kQfacOff = kMlOff + 4 * kTile * 8;
     static constexpr int kEnd = kQfacOff + (FP8 ? 2 * TILES * kTile * 4 : 0);
     static constexpr int kSmem = kEnd + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -154,35 +159,35 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (tid == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        constexpr int kReaders = TILES;          // MMA warps that read every slot
         for (int i = 0; i < G::kKSlots; ++i) {
             mbar_init(bar(G::B_KFULL + i), 1);
-            mbar_init(bar(G::B_KEMPTY + i), kReaders);
+            mbar_init(bar(G::B_KEMPTY + i), 1);
         }
         // (a slot of codes is freed by the widening warps, which also fill)
         for (int i = 0; i < G::kVL; ++i) {
             mbar_init(bar(G::B_VFULL + i), 1);
-            mbar_init(bar(G::B_VEMPTY + i), FP8 ? G::kPrepWarps : kReaders);
+            mbar_init(bar(G::B_VEMPTY + i), FP8 ? G::kPrepWarps : 1);
         }
         for (int i = 0; i < G::kVSlots; ++i) {
             if (FP8) {
                 mbar_init(bar(G::B_VWIDE + i), G::kPrepWarps);
-                mbar_init(bar(G::B_VWFREE + i), kReaders);
+                mbar_init(bar(G::B_VWFREE + i), 1);
             } else {
                 mbar_init(bar(G::B_FIX + i), 1);
             }
         }
         mbar_init(bar(G::B_QFULL), G::kPrepWarps);
-        mbar_init(bar(G::B_QFREE), 2);
+        mbar_init(bar(G::B_QFREE), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(G::B_SFULL + w), 1);
-            mbar_init(bar(G::B_PFULL + w), 4);
+            mbar_init(bar(G::B_PFULL + w), 8);
             mbar_init(bar(G::B_PVDONE + w), 1);
-            mbar_init(bar(G::B_OFREE + w), 8);
-            mbar_init(bar(G::B_END + w), 1);
+            mbar_init(bar(G::B_OFREE + w), kSoftWarps);
         }
-        mbar_init(bar(G::B_OFULL), 2);
-        mbar_init(bar(G::B_ML), 8);
+        mbar_init(bar(G::B_OFULL), 1);
+        mbar_init(bar(G::B_END), 1);
+        mbar_init(bar(G::B_ML), kSoftWarps);
+        for (int i = 0; i < 8; ++i) mbar_init(bar(G::B_MAX + i), 2);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
         misc[M_KISSUED] = 0;
@@ -191,24 +196,24 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == 9) {
+    if (warp == G::kMmaWarp) {
         umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, kTmemCols);
         umma::tmem_relinquish();
     }
-    if (warp == 8) cut_work(p, misc, first_row, cta, p.tidy && blockIdx.x == 0, lane);
+    if (warp == G::kCopyWarp) cut_work(p, misc, first_row, cta, p.tidy && blockIdx.x == 0, lane);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
-    if (warp == 8) {
-        copy_role<G, 2>(p, tm_k, tm_v, sb, misc, first_row, lane);
-    } else if (warp == 9 || warp == 10) {
+    if (warp == G::kCopyWarp) {
+        copy_role<G, FP8 ? 2 : 0>(p, tm_k, tm_v, sb, misc, first_row, lane);
+    } else if (!FP8 && warp == G::kCopyV) {
+        copy_role<G, 1>(p, tm_k, tm_v, sb, misc, first_row, lane);
+    } else if (warp == G::kMmaWarp) {
         // --------------------------------------------------------------- MMAs
         if (lane == 0) {
-            const int st = warp - 9;
-            const uint32_t tS = tmem + (uint32_t)(128 * st), tO = tmem + 256u + (uint32_t)(128 * st);
-            const uint32_t qt = sb + (uint32_t)(G::kQOff + (TILES == 2 ? st * G::kQTile : 0));
+            const uint32_t qt = sb + (uint32_t)G::kQOff;
             const uint64_t qdesc = FP8 ? code_desc<D>(qt) : umma::smem_desc_sw128(qt, 16, 1024);
             const uint64_t sdesc = FP8 ? code_desc<D>(sb + G::kKOff) : umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
             const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
@@ -217,7 +222,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             using KR = typename G::KRing;
             using VR = typename G::VRing;
             uint32_t fix_parity = 0;             // bit slot: parity of its next fix
-            int g0 = 0, pc = 0;                  // first chunk of the segment; chunks of the stream
+            uint32_t turn = 0, used = 0;         // bit stream: parity of its next weights; it had some
+            int g0 = 0;                          // first chunk of the segment
             bool ok = true;
             if (p.test_stall > 0 && misc[M_CNT] > 0 &&
                 !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
@@ -227,94 +233,91 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             for (Walk w(p, misc, first_row); ok && w.more(); w.next(p, first_row)) {
                 const int nc = w.chunks(), seg = w.seg;
-                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc);
-                if (!ok) break;
-                // a second row tile without rows takes no part, but frees the slots
-                const bool idle = TILES == 2 && st == 1 &&
-                                  w.q.n * p.G - first_row <= kTile;
-                bool first = true;
-                for (int c = 0; ok && c < nc; ++c) {
-                    const int g = g0 + c, ks = KR::slot(g), vs = VR::slot(g);
-                    const bool fix = !FP8 && w.drafted(c);
-                    const uint32_t fixp = (fix_parity >> vs) & 1u;
-                    if (fix) fix_parity ^= 1u << vs;
-                    if (TILES == 1 && (c & 1) != st) continue;
-                    ok = wait_issued(M_KISSUED, g, misc) && wait_bar(bar(KR::full(g)), KR::parity(g), misc);
-                    if (!ok) break;
-                    if (idle) {
-                        mbar_arrive(bar(KR::free(g)));
-                        ok = wait_issued(M_VISSUED, g, misc) && wait_bar(bar(VR::full(g)), VR::parity(g), misc);
-                        if (ok) mbar_arrive(bar(VR::free(g)));
-                        continue;
+                // the streams that take part, and the segment's items: item i is chunk
+                // i / 2 for stream i % 2 (TILES == 2), or chunk i for stream i % 2
+                const int streams = TILES == 2 && w.q.n * p.G - first_row <= kTile ? 1 : 2;
+                const int items = TILES == 2 ? nc * streams : nc;
+                auto chunk = [&](int i) { return TILES == 2 ? (streams == 2 ? i >> 1 : i) : i; };
+                auto stream = [&](int i) { return streams == 2 ? i & 1 : 0; };
+                // is it the last, or the first, to read its chunk's slots?
+                auto closes = [&](int i) { return TILES == 1 || stream(i) == streams - 1; };
+                auto opens = [&](int i) { return TILES == 1 || stream(i) == 0; };
+                // S = Q K^T of item i
+                auto scores = [&](int i) -> bool {
+                    const int c = chunk(i), st = stream(i), g = g0 + c, ks = KR::slot(g);
+                    if (opens(i)) {
+                        if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) return false;
                     }
-                    const int np = w.chunk_pages(c);
-                    // S = Q K^T; the stream's previous P.V products, which read what S
-                    // overwrites, are done (PVDONE below)
+                    // the stream's products of the weights that S overwrites are done
+                    if (((used >> st) & 1u) && !wait_bar(bar(G::B_PVDONE + st), ((turn >> st) & 1u) ^ 1u, misc))
+                        return false;
                     umma::fence_after_sync();
-                    {
-                        const uint64_t kd = sdesc + (uint64_t)((ks * G::kLoadBytes) >> 4);
-                        const uint32_t idesc =
-                            FP8 ? umma::idesc_f16_f32(kTile, kBlock * np, false, false)
-                                : umma::idesc_bf16_f32(kTile, kBlock * np, false, false);
-                        if constexpr (FP8) {
+                    const uint32_t tS = tmem + (uint32_t)(128 * st);
+                    const uint64_t qd = qdesc + (uint64_t)((TILES == 2 ? st * G::kQTile : 0) >> 4);
+                    const uint64_t kd = sdesc + (uint64_t)((ks * G::kLoadBytes) >> 4);
+                    const uint32_t idesc = FP8 ? umma::idesc_f16_f32(kTile, kBlock * w.chunk_pages(c), false, false)
+                                               : umma::idesc_bf16_f32(kTile, kBlock * w.chunk_pages(c), false, false);
+                    if constexpr (FP8) {
 #pragma unroll
-                            for (int part = 0; part < 2; ++part)
+                        for (int part = 0; part < 2; ++part)
 #pragma unroll
-                                for (int kk = 0; kk < D / 32; ++kk)
-                                    umma::mma_e4m3_ss(tS, qdesc + (uint64_t)((part * kTile * D + kk * 32) >> 4),
-                                                      kd + (uint64_t)((kk * 32) >> 4), idesc, part + kk > 0);
-                        } else {
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                umma::mma_e4m3_ss(tS, qd + (uint64_t)((part * kTile * D + kk * 32) >> 4),
+                                                  kd + (uint64_t)((kk * 32) >> 4), idesc, part + kk > 0);
+                    } else {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                umma::mma_bf16_ss(tS, qdesc + (uint64_t)(((kk >> 2) * kTile * 128 + (kk & 3) * 32) >> 4),
-                                                  kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4), idesc,
-                                                  kk > 0);
-                        }
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma::mma_bf16_ss(tS, qd + (uint64_t)(((kk >> 2) * kTile * 128 + (kk & 3) * 32) >> 4),
+                                              kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4), idesc, kk > 0);
                     }
                     umma::commit(bar(G::B_SFULL + st));
-                    umma::commit(bar(KR::free(g)));
-                    if (c + chunk_step(TILES) >= nc) umma::commit(bar(G::B_QFREE));
-                    ok = wait_bar(bar(G::B_PFULL + st), (uint32_t)(pc & 1), misc);
-                    if (!ok) break;
-                    ok = wait_issued(M_VISSUED, g, misc) && wait_bar(bar(VR::full(g)), VR::parity(g), misc);
-                    if (ok && fix) ok = wait_bar(bar(G::B_FIX + vs), fixp, misc);
-                    if (ok && first && seg > 0)
-                        ok = wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc);
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    {
-                        const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
-                        for (int kk = 0; kk < np; ++kk) {
-                            // the weights of keys 16 kk .. 16 kk + 15: 8 columns of the
-                            // 32 that held the scores of 32 keys; their low parts 16 on
-                            const uint32_t a = tS + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1));
-                            const uint64_t b = vd + (uint64_t)((kk * kBlock * 128) >> 4);
-                            umma::mma_bf16_ts(tO, a, b, idesc_pv, !(first && kk == 0));
-                            if (LOW) umma::mma_bf16_ts(tO, a + 16u, b, idesc_pv, true);
+                    if (closes(i)) umma::commit(bar(KR::free(g)));
+                    if (i + 1 == items) umma::commit(bar(G::B_QFREE));
+                    return true;
+                };
+                // O += P V of item i
+                auto products = [&](int i) -> bool {
+                    const int c = chunk(i), st = stream(i), g = g0 + c, vs = VR::slot(g);
+                    if (opens(i)) {
+                        if (!wait_bar(bar(VR::full(g)), VR::parity(g), misc)) return false;
+                        if (!FP8 && w.drafted(c)) {
+                            if (!wait_bar(bar(G::B_FIX + vs), (fix_parity >> vs) & 1u, misc)) return false;
+                            fix_parity ^= 1u << vs;
                         }
                     }
-                    umma::commit(bar(VR::free(g)));
+                    if (i == 0 && seg > 0 &&
+                        !wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc))
+                        return false;
+                    if (!wait_bar(bar(G::B_PFULL + st), (turn >> st) & 1u, misc)) return false;
+                    umma::fence_after_sync();
+                    const uint32_t tS = tmem + (uint32_t)(128 * st), tO = tmem + 256u + (uint32_t)(128 * st);
+                    const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
+                    const bool first = i < streams;
+                    for (int kk = 0; kk < w.chunk_pages(c); ++kk) {
+                        // the weights of keys 16 kk .. 16 kk + 15: 8 columns of the
+                        // 32 that held the scores of 32 keys; their low parts 16 on
+                        const uint32_t a = tS + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1));
+                        const uint64_t b = vd + (uint64_t)((kk * kBlock * 128) >> 4);
+                        umma::mma_bf16_ts(tO, a, b, idesc_pv, !(first && kk == 0));
+                        if (LOW) umma::mma_bf16_ts(tO, a + 16u, b, idesc_pv, true);
+                    }
                     umma::commit(bar(G::B_PVDONE + st));
-                    first = false;
-                    ok = wait_bar(bar(G::B_PVDONE + st), (uint32_t)(pc & 1), misc);
-                    ++pc;
-                }
+                    if (closes(i)) umma::commit(bar(VR::free(g)));
+                    turn ^= 1u << st;
+                    used |= 1u << st;
+                    return true;
+                };
+                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc);
+                for (int i = 0; ok && i < min(streams, items); ++i) ok = scores(i);
+                for (int i = 0; ok && i < items; ++i)
+                    ok = products(i) && (i + streams >= items || scores(i + streams));
                 if (!ok) break;
+                umma::commit(bar(G::B_OFULL));
                 g0 += nc;
-                // a stream without a chunk arrives for both; not before the other
-                // stream has for the segment before
-                if (first) {
-                    mbar_arrive(bar(G::B_QFREE));
-                    if (seg > 0) ok = wait_bar(bar(G::B_OFULL), (uint32_t)((seg - 1) & 1), misc);
-                    if (!ok) break;
-                }
-                umma::fence_after_sync();
-                umma::fence_before_sync();
-                mbar_arrive(bar(G::B_OFULL));
             }
             // every MMA issued by this thread is complete before the CTA ends
-            umma::commit(bar(G::B_END + st));
-            mbar_wait_bounded(bar(G::B_END + st), 0u, kWaitLimit);
+            umma::commit(bar(G::B_END));
+            mbar_wait_bounded(bar(G::B_END), 0u, kWaitLimit);
         }
         __syncwarp();
     } else if (warp >= G::kPrepWarp) {
@@ -369,15 +372,19 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (!FP8) cp_async_wait_all();
     } else {
         // ------------------------------------------------- softmax and output
-        const int st = warp >> 2;                // stream
+        const int st = (warp >> 2) & 1;          // stream
+        const int half = warp >> 3;              // half of a chunk's keys, and of the output's columns
         const int r = tid & 127;                 // row of the stream's tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lanes + (uint32_t)(128 * st);
+        const uint32_t tS = tmem + lanes + (uint32_t)(128 * st + 64 * half);
+        volatile float* maxima = reinterpret_cast<volatile float*>(gb + G::kMaxOff) + st * 2 * kTile + r;
+        const uint32_t max_bar = bar(G::B_MAX + (warp & 7));
         const uint32_t tO0 = tmem + lanes + 256u;
         const float v_scale = p.v_scale;
-        if (p.tidy && team == 0) zero_empty(p, D, cta, p.nctas, tid, 256);
+        if (p.tidy && team == 0) zero_empty(p, D, cta, p.nctas, tid, kSoftWarps * 32);
         if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
         int pc = 0, flat = misc[M_B0];
+        uint32_t met = 0;                        // parity of the next exchange of maxima
         bool ok = true;
         for (Walk w(p, misc, first_row); ok && w.more(); w.next(p, first_row)) {
             const int seg = w.seg, buf = seg & 1, nc = w.chunks();
@@ -392,7 +399,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             float m_ref = -INFINITY, l = 0.f;
             float sl2 = p.sl2;
             bool first = true;
-            for (int c = TILES == 1 ? st : 0; c < nc && !idle; c += chunk_step(TILES)) {
+            for (int c = TILES == 1 ? st : 0; c < nc && !idle; c += G::kChunkStep) {
                 ok = wait_warp(bar(G::B_SFULL + st), (uint32_t)(pc & 1), misc);
                 if (!ok) break;
                 if (warp_live) {
@@ -402,8 +409,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const int np = w.chunk_pages(c);
                     const int p0 = (w.j + c * kPages) * kBlock;
                     const bool masked = np < kPages || w.drafted(c);
-                    const int ng = (np + 1) / 2;         // groups of 32 keys
-                    // the keys of group g this row sees, as bits
+                    // the keys of group g (32 keys) this row sees, as bits
                     auto visible = [&](int g) -> uint32_t {
                         const int a0 = p0 + 32 * g - w.q.base;   // tree index of the first key
                         uint32_t v;
@@ -420,28 +426,39 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (lim < 32) v &= lim <= 0 ? 0u : (1u << lim) - 1u;
                         return v;
                     };
-                    // ---- the largest scaled score
+                    // ---- the largest scaled score of this half, then of both
                     float mx = -INFINITY;
-                    for (int g = 0; g < ng; g += 2) {
-                        uint32_t sr[64];
-                        umma::tmem_ld32(tS + (uint32_t)(32 * g), *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                        umma::tmem_ld32(tS + (uint32_t)(32 * g + 32), *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-                        umma::tmem_wait_ld();
+                    uint32_t vis[2] = {~0u, ~0u};
+                    uint32_t sr[2][32];
+                    if (masked) {
+                        vis[0] = visible(2 * half);
+                        vis[1] = visible(2 * half + 1);
+                    }
+                    // (a half without keys has scores of an earlier chunk, and sees none)
+                    umma::tmem_ld32(tS, sr[0]);
+                    umma::tmem_ld32(tS + 32u, sr[1]);
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
                         float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                         if (!masked && sl2 >= 0.f) {
 #pragma unroll
-                            for (int k = 0; k < 64; ++k) a[k & 3] = fmaxf(a[k & 3], __uint_as_float(sr[k]));
+                            for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], __uint_as_float(sr[g][k]));
                             mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * sl2);
                         } else {
-                            const uint32_t v0 = masked ? visible(g) : ~0u, v1 = masked ? visible(g + 1) : ~0u;
 #pragma unroll
-                            for (int k = 0; k < 64; ++k) {
-                                const bool see = ((k < 32 ? v0 : v1) >> (k & 31)) & 1u;
-                                a[k & 3] = fmaxf(a[k & 3], see ? __uint_as_float(sr[k]) * sl2 : -INFINITY);
-                            }
+                            for (int k = 0; k < 32; ++k)
+                                a[k & 3] = fmaxf(a[k & 3], (vis[g] >> k) & 1u ? __uint_as_float(sr[g][k]) * sl2 : -INFINITY);
                             mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
                         }
                     }
+                    maxima[half * kTile] = mx;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(max_bar);
+                    ok = wait_warp(max_bar, met, misc);
+                    if (!ok) break;
+                    met ^= 1u;
+                    mx = fmaxf(mx, maxima[(1 - half) * kTile]);
                     // ---- the reference moves only when it lags by more than 2^8; what
                     // has been accumulated is then scaled down in place
                     bool move = false;
@@ -456,55 +473,48 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     if (__any_sync(kFull, move)) {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            umma::tmem_ld32(tO0 + (uint32_t)(128 * st + c0), o);
+                        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
+                            uint32_t o[16];
+                            umma::tmem_ld16(tO0 + (uint32_t)(128 * st + c0), o);
                             umma::tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
+                            for (int k = 0; k < 16; ++k)
                                 o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                            umma::tmem_st32(tO0 + (uint32_t)(128 * st + c0), o);
+                            umma::tmem_st16(tO0 + (uint32_t)(128 * st + c0), o);
                         }
                     }
                     // ---- weights, in place of the scores
                     const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + (FP8 ? kBiasF16 : 0.f);
-                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                    // (a group's scores are loaded while the one before is weighed)
-                    uint32_t next[32];
-                    umma::tmem_ld32(tS, next);
-                    for (int g = 0; g < ng; ++g) {
-                        umma::tmem_wait_ld();
-                        uint32_t sr[32];
+                    const u64 sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
+                    u64 ls[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) sr[k] = next[k];
-                        if (g + 1 < ng) umma::tmem_ld32(tS + (uint32_t)(32 * (g + 1)), next);
+                    for (int g = 0; g < 2; ++g) {
                         uint32_t hi[16], lo[16];
-                        const uint32_t vis = masked ? visible(g) : ~0u;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float w0 = ex2(fmaf(__uint_as_float(sr[2 * e]), sl2, nm));
-                            float w1 = ex2(fmaf(__uint_as_float(sr[2 * e + 1]), sl2, nm));
+                            float w0, w1;
+                            unpack2(fma2(pack2(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])), sl22, nm2),
+                                    w0, w1);
+                            w0 = ex2(w0);
+                            w1 = ex2(w1);
                             if (masked) {
-                                w0 = (vis >> (2 * e)) & 1u ? w0 : 0.f;
-                                w1 = (vis >> (2 * e + 1)) & 1u ? w1 : 0.f;
+                                w0 = (vis[g] >> (2 * e)) & 1u ? w0 : 0.f;
+                                w1 = (vis[g] >> (2 * e + 1)) & 1u ? w1 : 0.f;
                             }
-                            if (FP8) {
-                                hi[e] = pack_f16x2(w0, w1);
-                                ls[e & 3] += w0 + w1;
-                            } else {
-                                hi[e] = pack_bf16x2(w0, w1);
-                                if (LOW) {
-                                    lo[e] = pack_bf16x2(w0 - bf16_lo(hi[e]), w1 - bf16_hi(hi[e]));
-                                    ls[e & 3] += w0 + w1;
-                                } else {
-                                    ls[e & 3] += bf16_lo(hi[e]) + bf16_hi(hi[e]);
-                                }
+                            hi[e] = FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
+                            if (LOW) lo[e] = pack_bf16x2(w0 - bf16_lo(hi[e]), w1 - bf16_hi(hi[e]));
+                            if (!FP8 && !LOW) {
+                                w0 = bf16_lo(hi[e]);
+                                w1 = bf16_hi(hi[e]);
                             }
+                            ls[e & 1] = add2(ls[e & 1], pack2(w0, w1));
                         }
                         umma::tmem_st16(tS + (uint32_t)(32 * g), hi);
                         if (LOW) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), lo);
                     }
-                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    float l0, l1;
+                    unpack2(add2(ls[0], ls[1]), l0, l1);
+                    l += l0 + l1;
                     first = false;
                     umma::tmem_wait_st();
                     umma::fence_before_sync();
@@ -524,17 +534,20 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                 m_ref = -INFINITY;
                 l = 0.f;
             }
-            float a0 = 1.f, a1 = 0.f;            // weights of the two accumulators (TILES == 1)
-            if (TILES == 1) {
-                volatile float* ml = reinterpret_cast<volatile float*>(gb + G::kMlOff);
-                ml[(st * kTile + r) * 2] = m_ref;
-                ml[(st * kTile + r) * 2 + 1] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(G::B_ML));
-                ok = wait_warp(bar(G::B_ML), (uint32_t)(seg & 1), misc);
-                if (!ok) break;
-                const float m0 = ml[r * 2], l0 = ml[r * 2 + 1];
-                const float m1 = ml[(kTile + r) * 2], l1 = ml[(kTile + r) * 2 + 1];
+            // the halves' sums, and (TILES == 1) the streams' accumulators with their weights
+            float a0 = 1.f, a1 = 0.f;
+            volatile float* ml = reinterpret_cast<volatile float*>(gb + G::kMlOff) + 2 * r;
+            ml[(st * 2 + half) * 2 * kTile] = m_ref;
+            ml[(st * 2 + half) * 2 * kTile + 1] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(G::B_ML));
+            ok = wait_warp(bar(G::B_ML), (uint32_t)(seg & 1), misc);
+            if (!ok) break;
+            if (TILES == 2) {
+                l = ml[st * 4 * kTile + 1] + ml[(st * 2 + 1) * 2 * kTile + 1];
+            } else {
+                const float m0 = ml[0], l0 = ml[1] + ml[2 * kTile + 1];
+                const float m1 = ml[4 * kTile], l1 = ml[4 * kTile + 1] + ml[6 * kTile + 1];
                 const float mm = fmaxf(m0, m1);
                 a0 = m0 == -INFINITY ? 0.f : ex2(m0 - mm);
                 a1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
@@ -559,29 +572,31 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         any_back = any_back || back[k] != 0u;
                     }
                 }
-                const int c_lo = TILES == 1 ? st * (D / 2) : 0, c_hi = TILES == 1 ? c_lo + D / 2 : D;
+                // this warp's share of the output's columns, 16 at a time
+                constexpr int kShare = D / (TILES == 1 ? 4 : 2);
+                const int c_lo = (TILES == 1 ? st * 2 + half : half) * kShare;
 #pragma unroll 1
-                for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-                    uint32_t o[32];
-                    umma::tmem_ld32(tO0 + (uint32_t)((TILES == 2 ? 128 * st : 0) + c0), o);
+                for (int c0 = c_lo; c0 < c_lo + kShare; c0 += 16) {
+                    uint32_t o[16];
+                    umma::tmem_ld16(tO0 + (uint32_t)((TILES == 2 ? 128 * st : 0) + c0), o);
                     umma::tmem_wait_ld();
-                    float v[32];
+                    float v[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]);
                     if (TILES == 1) {
                         if (nc > 1) {            // the second accumulator holds something
-                            umma::tmem_ld32(tO0 + (uint32_t)(128 + c0), o);
+                            umma::tmem_ld16(tO0 + (uint32_t)(128 + c0), o);
                             umma::tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = v[k] * a0 + __uint_as_float(o[k]) * a1;
+                            for (int k = 0; k < 16; ++k) v[k] = v[k] * a0 + __uint_as_float(o[k]) * a1;
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] *= a0;
+                            for (int k = 0; k < 16; ++k) v[k] *= a0;
                         }
                     }
                     if (l == 0.f) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                        for (int k = 0; k < 16; ++k) v[k] = 0.f;
                     }
                     if (any_back) {
 #pragma unroll 1
@@ -593,7 +608,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 if (blk < 0 || blk >= p.num_blocks) continue;
                                 const size_t at = (((size_t)blk * p.Hkv + w.h) * kBlock + pos % kBlock) * D + c0;
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) {
+                                for (int k = 0; k < 16; ++k) {
                                     if (FP8) {
                                         if ((p.v_cache[at + k] & 0x7fu) == 0x7fu) v[k] = __uint_as_float(0x7fffffffu);
                                     } else {
@@ -610,12 +625,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (p.out_f32) {
                             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + c0);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)
+                            for (int k = 0; k < 16; k += 4)
                                 dst[k / 4] = make_float4(v[k] * inv, v[k + 1] * inv, v[k + 2] * inv, v[k + 3] * inv);
                         } else {
                             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + c0);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8)
+                            for (int k = 0; k < 16; k += 8)
                                 dst[k / 8] = make_uint4(pack_bf16x2(v[k] * inv, v[k + 1] * inv),
                                                         pack_bf16x2(v[k + 2] * inv, v[k + 3] * inv),
                                                         pack_bf16x2(v[k + 4] * inv, v[k + 5] * inv),
@@ -624,11 +639,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     } else {
                         float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c0);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
+                        for (int k = 0; k < 16; k += 4)
                             dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
                 }
-                if (in && !whole && (TILES == 2 || st == 0)) p.part_ml[prow] = make_float2(m_ref, l);
+                if (in && !whole && half == 0 && (TILES == 2 || st == 0)) p.part_ml[prow] = make_float2(m_ref, l);
                 if (tid == 0 && w.j == 0 && !whole) {
                     // the CTA with the first pages says where the partials are
                     const int last = (int)(((long long)flat + w.q.nb - 1) / misc[M_Q]);
@@ -643,7 +658,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     umma::fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == G::kMmaWarp) {
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, kTmemCols);
     }

@@ -1,5 +1,5 @@
 // Draft-tree tables shared by the kernels that read them (paged_tree.cu,
-// tree_verify.cu, kv_compact.cu).
+// tree_verify.cu, kv_compact.cu), and arithmetic on two floats at a time.
 #pragma once
 
 #include "device_common.cuh"
@@ -32,6 +32,43 @@ __device__ __forceinline__ int tree_parent(const int32_t* __restrict__ parents, 
     if (p >= KV_TREE_PAD && p < i) return p;
     if (e) raise_flag(e, KV_DEVERR_BAD_TREE, p);
     return -1;
+}
+
+using u64 = unsigned long long;          // two floats, the first in the low half
+
+__device__ __forceinline__ u64 pack2(float a, float b)
+{
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(u64 x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b)
+{
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 sub2(u64 a, u64 b)
+{
+    u64 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b)
+{
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c)
+{
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 }  // namespace pkv

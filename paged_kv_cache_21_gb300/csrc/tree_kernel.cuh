@@ -495,7 +495,7 @@ __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, u
 }
 
 // Widen the E4M3 codes of the segment's V to f16, with what fix_values does on the
-// way.  One of four warps (pw).  False: given up.
+// way.  One of the prep warps (pw).  False: given up.
 template <class G>
 __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32_t sb, uint8_t* gb,
                                       volatile int* misc, int g0, int pw, int lane)
@@ -511,7 +511,7 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
     // different banks on both sides; a step is RS rows, a multiple of the swizzle's
     // period, so that offsets between steps are constants.
     constexpr int CR = D / 16;               // 16-code pieces of a row
-    constexpr int RS = 128 / CR;             // rows of the four warps' step
+    constexpr int RS = G::kPrepWarps * 32 / CR;      // rows of the warps' step
     constexpr int kSteps = kKeys / RS;
     const int t = pw * 32 + lane;
     const int r0 = t % RS, cc = t / RS;
