@@ -59,6 +59,7 @@
 #include <climits>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "cache_map.h"
 #include "internal.h"
@@ -438,19 +439,18 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     umma::tmem_ld32(tS, sr[0]);
                     umma::tmem_ld32(tS + 32u, sr[1]);
                     umma::tmem_wait_ld();
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
+                    if (!masked && sl2 >= 0.f) {
                         float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        if (!masked && sl2 >= 0.f) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], __uint_as_float(sr[g][k]));
-                            mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * sl2);
-                        } else {
+                        for (int k = 0; k < 32; ++k)
+                            a[k & 3] = max3(a[k & 3], __uint_as_float(sr[0][k]), __uint_as_float(sr[1][k]));
+                        mx = fmaxf(max3(a[0], a[1], a[2]), a[3]) * sl2;
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                a[k & 3] = fmaxf(a[k & 3], (vis[g] >> k) & 1u ? __uint_as_float(sr[g][k]) * sl2 : -INFINITY);
-                            mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
-                        }
+                                mx = fmaxf(mx, (vis[g] >> k) & 1u ? __uint_as_float(sr[g][k]) * sl2 : -INFINITY);
                     }
                     maxima[half * kTile] = mx;
                     __syncwarp();
@@ -487,31 +487,36 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + (FP8 ? kBiasF16 : 0.f);
                     const u64 sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
                     u64 ls[2] = {0ull, 0ull};
+                    auto weigh = [&](auto all) {         // all: no key is masked
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t hi[16], lo[16];
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float w0, w1;
-                            unpack2(fma2(pack2(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])), sl22, nm2),
-                                    w0, w1);
-                            w0 = ex2(w0);
-                            w1 = ex2(w1);
-                            if (masked) {
-                                w0 = (vis[g] >> (2 * e)) & 1u ? w0 : 0.f;
-                                w1 = (vis[g] >> (2 * e + 1)) & 1u ? w1 : 0.f;
+                            for (int e = 0; e < 16; ++e) {
+                                float w0, w1;
+                                unpack2(fma2(pack2(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])),
+                                             sl22, nm2),
+                                        w0, w1);
+                                w0 = ex2(w0);
+                                w1 = ex2(w1);
+                                if (!decltype(all)::value) {
+                                    w0 = (vis[g] >> (2 * e)) & 1u ? w0 : 0.f;
+                                    w1 = (vis[g] >> (2 * e + 1)) & 1u ? w1 : 0.f;
+                                }
+                                hi[e] = FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
+                                if (LOW) lo[e] = pack_bf16x2(w0 - bf16_lo(hi[e]), w1 - bf16_hi(hi[e]));
+                                if (!FP8 && !LOW) {
+                                    w0 = bf16_lo(hi[e]);
+                                    w1 = bf16_hi(hi[e]);
+                                }
+                                ls[e & 1] = add2(ls[e & 1], pack2(w0, w1));
                             }
-                            hi[e] = FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
-                            if (LOW) lo[e] = pack_bf16x2(w0 - bf16_lo(hi[e]), w1 - bf16_hi(hi[e]));
-                            if (!FP8 && !LOW) {
-                                w0 = bf16_lo(hi[e]);
-                                w1 = bf16_hi(hi[e]);
-                            }
-                            ls[e & 1] = add2(ls[e & 1], pack2(w0, w1));
+                            umma::tmem_st16(tS + (uint32_t)(32 * g), hi);
+                            if (LOW) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), lo);
                         }
-                        umma::tmem_st16(tS + (uint32_t)(32 * g), hi);
-                        if (LOW) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), lo);
-                    }
+                    };
+                    if (masked) weigh(std::false_type());
+                    else weigh(std::true_type());
                     float l0, l1;
                     unpack2(add2(ls[0], ls[1]), l0, l1);
                     l += l0 + l1;
