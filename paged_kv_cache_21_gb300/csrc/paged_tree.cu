@@ -223,7 +223,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             using KR = typename G::KRing;
             using VR = typename G::VRing;
             uint32_t fix_parity = 0;             // bit slot: parity of its next fix
-            uint32_t turn = 0, used = 0;         // bit stream: parity of its next weights; it had some
+            uint32_t turn[2] = {0u, 0u};         // of a stream: parity of its next weights
+            bool used[2] = {false, false};       // it has had some
             int g0 = 0;                          // first chunk of the segment
             bool ok = true;
             if (p.test_stall > 0 && misc[M_CNT] > 0 &&
@@ -234,30 +235,33 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             for (Walk w(p, misc, first_row); ok && w.more(); w.next(p, first_row)) {
                 const int nc = w.chunks(), seg = w.seg;
-                // the streams that take part, and the segment's items: item i is chunk
-                // i / 2 for stream i % 2 (TILES == 2), or chunk i for stream i % 2
-                const int streams = TILES == 2 && w.q.n * p.G - first_row <= kTile ? 1 : 2;
-                const int items = TILES == 2 ? nc * streams : nc;
-                auto chunk = [&](int i) { return TILES == 2 ? (streams == 2 ? i >> 1 : i) : i; };
-                auto stream = [&](int i) { return streams == 2 ? i & 1 : 0; };
-                // is it the last, or the first, to read its chunk's slots?
-                auto closes = [&](int i) { return TILES == 1 || stream(i) == streams - 1; };
-                auto opens = [&](int i) { return TILES == 1 || stream(i) == 0; };
-                // S = Q K^T of item i
-                auto scores = [&](int i) -> bool {
-                    const int c = chunk(i), st = stream(i), g = g0 + c, ks = KR::slot(g);
-                    if (opens(i)) {
-                        if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) return false;
-                    }
+                // With TILES == 2 both streams take every chunk (the first alone, if the
+                // second tile has no rows), with TILES == 1 they take the chunks in turn.
+                // A stream's products are followed by its next scores at once, so that
+                // its softmax runs while the other stream has the tensor cores.
+                constexpr int kStep = G::kChunkStep;
+                const bool two = TILES == 1 || w.q.n * p.G - first_row > kTile;
+                auto keys = [&](int c) -> bool {
+                    return c >= nc || wait_bar(bar(KR::full(g0 + c)), KR::parity(g0 + c), misc);
+                };
+                // S = Q K^T of chunk c
+                auto scores = [&](auto stream, int c) -> bool {
+                    constexpr int st = decltype(stream)::value;
+                    const bool closes = TILES == 1 || st == 1 || !two;   // last to read the chunk
+                    const int g = g0 + c;
                     // the stream's products of the weights that S overwrites are done
-                    if (((used >> st) & 1u) && !wait_bar(bar(G::B_PVDONE + st), ((turn >> st) & 1u) ^ 1u, misc))
-                        return false;
+                    if (used[st] && !wait_bar(bar(G::B_PVDONE + st), turn[st] ^ 1u, misc)) return false;
+                    // and with them all that was issued before: slots are released by
+                    // plain arrivals, which cost less than a commit
+                    if (c >= kStep && closes) mbar_arrive(bar(VR::free(g - kStep)));
+                    if (c > kStep && (TILES == 1 || st == 0)) mbar_arrive(bar(KR::free(g - 1)));
                     umma::fence_after_sync();
                     const uint32_t tS = tmem + (uint32_t)(128 * st);
                     const uint64_t qd = qdesc + (uint64_t)((TILES == 2 ? st * G::kQTile : 0) >> 4);
-                    const uint64_t kd = sdesc + (uint64_t)((ks * G::kLoadBytes) >> 4);
-                    const uint32_t idesc = FP8 ? umma::idesc_f16_f32(kTile, kBlock * w.chunk_pages(c), false, false)
-                                               : umma::idesc_bf16_f32(kTile, kBlock * w.chunk_pages(c), false, false);
+                    const uint64_t kd = sdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
+                    const uint32_t keys16 = (uint32_t)(kBlock * w.chunk_pages(c));
+                    const uint32_t idesc = FP8 ? umma::idesc_f16_f32(kTile, keys16, false, false)
+                                               : umma::idesc_bf16_f32(kTile, keys16, false, false);
                     if constexpr (FP8) {
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
@@ -272,46 +276,70 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                               kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4), idesc, kk > 0);
                     }
                     umma::commit(bar(G::B_SFULL + st));
-                    if (closes(i)) umma::commit(bar(KR::free(g)));
-                    if (i + 1 == items) umma::commit(bar(G::B_QFREE));
+                    // (the first chunks' slots may be needed before any products are waited for)
+                    if (closes && (c < kStep || c + 1 == nc)) umma::commit(bar(KR::free(g)));
+                    if (closes && c + 1 == nc) umma::commit(bar(G::B_QFREE));
                     return true;
                 };
-                // O += P V of item i
-                auto products = [&](int i) -> bool {
-                    const int c = chunk(i), st = stream(i), g = g0 + c, vs = VR::slot(g);
-                    if (opens(i)) {
+                // O += P V of chunk c
+                auto products = [&](auto stream, int c) -> bool {
+                    constexpr int st = decltype(stream)::value;
+                    const bool closes = TILES == 1 || st == 1 || !two;
+                    const int g = g0 + c, vs = VR::slot(g), np = w.chunk_pages(c);
+                    // what is usually there comes first, the weights last
+                    if (TILES == 1 || st == 0) {
+                        if (!keys(c + kStep)) return false;
                         if (!wait_bar(bar(VR::full(g)), VR::parity(g), misc)) return false;
                         if (!FP8 && w.drafted(c)) {
                             if (!wait_bar(bar(G::B_FIX + vs), (fix_parity >> vs) & 1u, misc)) return false;
                             fix_parity ^= 1u << vs;
                         }
                     }
-                    if (i == 0 && seg > 0 &&
+                    if (st == 0 && c == 0 && seg > 0 &&
                         !wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc))
                         return false;
-                    if (!wait_bar(bar(G::B_PFULL + st), (turn >> st) & 1u, misc)) return false;
+                    if (!wait_bar(bar(G::B_PFULL + st), turn[st], misc)) return false;
                     umma::fence_after_sync();
                     const uint32_t tS = tmem + (uint32_t)(128 * st), tO = tmem + 256u + (uint32_t)(128 * st);
                     const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
-                    const bool first = i < streams;
-                    for (int kk = 0; kk < w.chunk_pages(c); ++kk) {
+                    const bool first = c < kStep;
+                    auto page = [&](int kk) {
                         // the weights of keys 16 kk .. 16 kk + 15: 8 columns of the
                         // 32 that held the scores of 32 keys; their low parts 16 on
                         const uint32_t a = tS + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1));
                         const uint64_t b = vd + (uint64_t)((kk * kBlock * 128) >> 4);
                         umma::mma_bf16_ts(tO, a, b, idesc_pv, !(first && kk == 0));
                         if (LOW) umma::mma_bf16_ts(tO, a + 16u, b, idesc_pv, true);
+                    };
+                    if (np == kPages) {
+#pragma unroll
+                        for (int kk = 0; kk < kPages; ++kk) page(kk);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < np; ++kk) page(kk);
                     }
                     umma::commit(bar(G::B_PVDONE + st));
-                    if (closes(i)) umma::commit(bar(VR::free(g)));
-                    turn ^= 1u << st;
-                    used |= 1u << st;
+                    if (closes && c + kStep >= nc) umma::commit(bar(VR::free(g)));
+                    turn[st] ^= 1u;
+                    used[st] = true;
                     return true;
                 };
-                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc);
-                for (int i = 0; ok && i < min(streams, items); ++i) ok = scores(i);
-                for (int i = 0; ok && i < items; ++i)
-                    ok = products(i) && (i + streams >= items || scores(i + streams));
+                constexpr std::integral_constant<int, 0> s0{};
+                constexpr std::integral_constant<int, 1> s1{};
+                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc) && keys(0) && scores(s0, 0);
+                if (TILES == 1) {
+                    if (ok && nc > 1) ok = keys(1) && scores(s1, 1);
+                    for (int c = 0; ok && c < nc; c += 2) {
+                        ok = products(s0, c) && (c + 2 >= nc || scores(s0, c + 2));
+                        if (ok && c + 1 < nc) ok = products(s1, c + 1) && (c + 3 >= nc || scores(s1, c + 3));
+                    }
+                } else {
+                    if (ok && two) ok = scores(s1, 0);
+                    for (int c = 0; ok && c < nc; ++c) {
+                        ok = products(s0, c) && (c + 1 >= nc || scores(s0, c + 1));
+                        if (ok && two) ok = products(s1, c) && (c + 1 >= nc || scores(s1, c + 1));
+                    }
+                }
                 if (!ok) break;
                 umma::commit(bar(G::B_OFULL));
                 g0 += nc;
@@ -401,15 +429,15 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
             float sl2 = p.sl2;
             bool first = true;
             for (int c = TILES == 1 ? st : 0; c < nc && !idle; c += G::kChunkStep) {
+                const int np = w.chunk_pages(c);
+                const int p0 = (w.j + c * kPages) * kBlock;
+                const bool masked = np < kPages || w.drafted(c);
                 ok = wait_warp(bar(G::B_SFULL + st), (uint32_t)(pc & 1), misc);
                 if (!ok) break;
                 if (warp_live) {
                     umma::fence_after_sync();
                     if (FP8 && first)
                         sl2 = p.sl2 * reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * TILES * kTile + (in ? rt : 0)];
-                    const int np = w.chunk_pages(c);
-                    const int p0 = (w.j + c * kPages) * kBlock;
-                    const bool masked = np < kPages || w.drafted(c);
                     // the keys of group g (32 keys) this row sees, as bits
                     auto visible = [&](int g) -> uint32_t {
                         const int a0 = p0 + 32 * g - w.q.base;   // tree index of the first key
