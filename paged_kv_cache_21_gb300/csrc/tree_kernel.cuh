@@ -37,8 +37,8 @@ constexpr float kMaxLag = 8.f;                  // the reference maximum may lag
 // rounds to zero is below 2^-31 of the largest weight
 constexpr float kBiasF16 = 7.f;
 
-// misc words: tensor-memory base; abort; the range: first unit, units, units per
-// CTA, first sequence, KV head and page; chunks whose K, and whose V,
+// misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
+// per CTA, first sequence, KV head and page; chunks whose K, and whose V,
 // are on their way into the rings that the MMAs read
 enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_KISSUED, M_VISSUED };
 
@@ -228,60 +228,70 @@ struct Walk {
     }
 };
 
-// This CTA's range of its team's flat (sequence, KV head, page) list: equal
-// shares of at least p.min_q pages.  One warp.
+// This CTA's range of its team's list of pages, by sequence and KV head: equal
+// shares of at least p.min_q units, where a page is a unit and each (sequence, KV
+// head) costs `extra` more before its first page (its queries, tree and results), so
+// that CTAs with many short sequences get fewer pages.  One warp.
 __device__ __forceinline__ void cut_work(const TreeParams& p, volatile int* misc, int first_row, int cta,
-                                         bool flag, int lane)
+                                         bool flag, int extra, int lane)
 {
     long long total = 0;
     for (int b = 0; b < p.B; b += 32) {
         int nb = 0;
         if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, flag).nb;
-        total += warp_sum_ll(nb);
+        total += warp_sum_ll(nb > 0 ? nb + extra : 0);
     }
     total *= p.Hkv;
     long long q = (total + p.nctas - 1) / p.nctas;
     if (q < p.min_q) q = p.min_q;
-    const long long b0 = (long long)cta * q;
-    long long cnt = total - b0;
-    if (cnt > q) cnt = q;
-    if (cnt < 0) cnt = 0;
-    int s0 = 0, h0 = 0, j0 = 0;
-    if (cnt > 0) {
-        long long excl = 0;
-        bool found = false;
-        for (int b = 0; b < p.B && !found; b += 32) {
-            int nb = 0;
-            if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, false).nb;
-            const long long v = (long long)nb * p.Hkv;
-            long long inc = v;
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(kFull, inc, o);
-                if (lane >= o) inc += t;
+    // the first page at or behind unit x: its sequence, head and index, its unit, and
+    // how many pages are before it
+    struct At {
+        int s, h, j;
+        long long unit, pages;
+    };
+    const long long lo = min((long long)cta * q, total), hi = min(lo + q, total);
+    At at[2] = {{0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}};
+    bool found[2] = {false, false};
+    long long units = 0, pages = 0;              // up to the 32 sequences at hand
+    for (int b = 0; b < p.B && !(found[0] && found[1]); b += 32) {
+        int nb = 0;
+        if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, false).nb;
+        const long long u = nb > 0 ? (long long)(nb + extra) * p.Hkv : 0, n = (long long)nb * p.Hkv;
+        long long iu = u, in = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
+            if (lane >= o) {
+                iu += tu;
+                in += tn;
             }
-            inc += excl;
-            const unsigned m = __ballot_sync(kFull, inc > b0);
-            if (m) {
-                const int src = __ffs(m) - 1;
-                const long long ex = __shfl_sync(kFull, inc - v, src);
-                const int nbs = __shfl_sync(kFull, nb, src);
-                s0 = b + src;
-                const long long off = b0 - ex;
-                h0 = (int)(off / nbs);
-                j0 = (int)(off - (long long)h0 * nbs);
-                found = true;
-            }
-            excl = __shfl_sync(kFull, inc, 31);
         }
-        if (!found) cnt = 0;
+        iu += units;
+        in += pages;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long x = e == 0 ? lo : hi;
+            const unsigned m = __ballot_sync(kFull, iu > x);
+            if (found[e] || !m) continue;
+            found[e] = true;
+            const int src = __ffs(m) - 1;
+            const int nbs = __shfl_sync(kFull, nb, src), v = nbs + extra;
+            const long long before = __shfl_sync(kFull, iu - u, src);
+            const int off = (int)(x - before), h = off / v, j = max(0, off - h * v - extra);
+            at[e] = {b + src, h, j, before + (long long)h * v + extra + j,
+                     __shfl_sync(kFull, in - n, src) + (long long)h * nbs + j};
+        }
+        units = __shfl_sync(kFull, iu, 31);
+        pages = __shfl_sync(kFull, in, 31);
     }
+    if (!found[1]) at[1].pages = pages;          // (hi is the end of the list)
     if (lane == 0) {
-        misc[M_B0] = (int)b0;
-        misc[M_CNT] = (int)cnt;
+        misc[M_B0] = (int)at[0].unit;
+        misc[M_CNT] = found[0] ? (int)(at[1].pages - at[0].pages) : 0;
         misc[M_Q] = (int)q;
-        misc[M_S0] = s0;
-        misc[M_H0] = h0;
-        misc[M_J0] = j0;
+        misc[M_S0] = at[0].s;
+        misc[M_H0] = at[0].h;
+        misc[M_J0] = at[0].j;
     }
 }
 
