@@ -41,7 +41,11 @@ template <int D, bool FP8, int N>
 struct SmallGeo {
     static constexpr int kD = D;
     static constexpr bool kFp8 = FP8;
-    static constexpr int kPrepWarp = 11;                     // first of the prep / widening warps
+    static constexpr bool kSplit = N == 64;                  // the groups split the rows, not the chunks
+    static constexpr int kWeighWarps = 8;                    // two groups of four
+    static constexpr int kCopyWarp = kWeighWarps;            // K; the next V
+    static constexpr int kMmaWarp = kCopyWarp + 2;
+    static constexpr int kPrepWarp = kMmaWarp + 1;           // first of the prep / widening warps
     static constexpr int kPrepWarps = FP8 ? 4 : 1;
     static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
     static constexpr int kBoxes = D / 64;
@@ -52,7 +56,6 @@ struct SmallGeo {
     // then the low parts.  64 rows of an E4M3 cache go without: f16's 11 bits
     // against the cache's 4, and the room goes to the rings.
     static constexpr bool kLow = !(FP8 && N == 64);
-    static constexpr bool kSplit = N == 64;                  // the groups split the rows, not the chunks
     static constexpr int kAccs = kSplit ? 1 : 2;             // accumulators
     static constexpr int kPW = kLow ? 2 * N : N;
     static constexpr int kPBuf = kPW / 64 * kRegion;         // [column group of 64][128 keys][128 B]
@@ -71,23 +74,24 @@ struct SmallGeo {
     // barriers
     static constexpr int kVL = FP8 ? kRawV : kVSlots;
     static constexpr int B_KFULL = 0;                        // + slot: K has landed
-    static constexpr int B_KEMPTY = B_KFULL + kKSlots;       // + slot: it may be refilled
-    static constexpr int B_VFULL = B_KEMPTY + kKSlots;       // V, or its codes
+    // + chunk % kScoreBars: its scores are there (and its K slot may be refilled)
+    static constexpr int kScoreBars = kKSlots > 4 ? kKSlots : 4;
+    static constexpr int B_SFULL = B_KFULL + kKSlots;
+    static constexpr int B_VFULL = B_SFULL + kScoreBars;     // V, or its codes
+    // + slot: it may be refilled (of what the MMAs read: a chunk's products are done)
     static constexpr int B_VEMPTY = B_VFULL + kVL;
     static constexpr int B_VWIDE = B_VEMPTY + kVL;           // (FP8) + slot: widened
     static constexpr int B_VWFREE = B_VWIDE + (FP8 ? kVSlots : 0);
     static constexpr int B_FIX = B_VWFREE + (FP8 ? kVSlots : 0);     // (bf16) + slot: V rows fixed
-    using KRing = Ring<kKSlots, B_KFULL, B_KEMPTY>;
+    using KRing = Ring<kKSlots, B_KFULL, B_SFULL, kScoreBars>;
     using VLoad = Ring<kVL, B_VFULL, B_VEMPTY>;              // what TMA fills, and what the MMAs read
     using VRing = Ring<kVSlots, FP8 ? B_VWIDE : B_VFULL, FP8 ? B_VWFREE : B_VEMPTY>;
     static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kVSlots);  // Q and the tree of a segment
     static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
-    static constexpr int B_SFULL = B_QFREE + 1;              // + buffer (4): scores
-    static constexpr int B_PFULL = B_SFULL + 4;              // + buffer of P: weights written
-    static constexpr int B_PVDONE = B_PFULL + 2;             // + buffer of P: their products are done
-    static constexpr int B_OFULL = B_PVDONE + 2;             // the accumulators are complete
+    static constexpr int B_PFULL = B_QFREE + 1;              // + buffer of P: weights written
+    static constexpr int B_OFULL = B_PFULL + 2;              // the accumulators are complete
     static constexpr int B_OFREE = B_OFULL + 1;              // + segment & 1: they have been read
-    static constexpr int B_JOIN = B_OFREE + 2;               // the eight warps meet
+    static constexpr int B_JOIN = B_OFREE + 2;               // the groups meet
     static constexpr int B_END = B_JOIN + 1;                 // all MMAs are done
     static constexpr int B_STALL = B_END + 1;                // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
@@ -97,10 +101,10 @@ struct SmallGeo {
     static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
     static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
     static constexpr int kQfacOff = kBadOff + 2 * kPrepWarps * 16;   // [2][N] floats (FP8)
-    static constexpr int kSnOff = kQfacOff + 2 * N * 4;      // [group][32] float2: (scale, -reference)
-    static constexpr int kRefOff = kSnOff + 64 * 8;          // [group][32] floats: the reference
-    static constexpr int kAlphaOff = kRefOff + 64 * 4;       // [group][32] floats
-    static constexpr int kWmaxOff = kAlphaOff + 64 * 4;      // [group][4][32] floats: maxima, later sums
+    static constexpr int kSnOff = kQfacOff + 2 * N * 4;      // [group][row] float2: (scale, -reference)
+    static constexpr int kRefOff = kSnOff + 64 * 8;          // [group][row] floats: the reference
+    static constexpr int kAlphaOff = kRefOff + 64 * 4;       // [group][row] floats
+    static constexpr int kWmaxOff = kAlphaOff + 64 * 4;      // [group][4][row] floats: maxima, later sums
     static constexpr int kFacOff = kWmaxOff + 256 * 4;       // [N] float4
     static constexpr int kRowOff = kFacOff + N * 16;         // [N] words: place of a row's result
     static constexpr int kUnsetOff = kRowOff + N * 4;        // [group] words
@@ -156,10 +160,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (tid == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        for (int i = 0; i < G::kKSlots; ++i) {
-            mbar_init(bar(G::B_KFULL + i), 1);
-            mbar_init(bar(G::B_KEMPTY + i), 1);
-        }
+        for (int i = 0; i < G::kKSlots; ++i) mbar_init(bar(G::B_KFULL + i), 1);
         // (a slot of codes is freed by the widening warps, which also fill)
         for (int i = 0; i < G::kVL; ++i) {
             mbar_init(bar(G::B_VFULL + i), 1);
@@ -175,14 +176,13 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         mbar_init(bar(G::B_QFULL), G::kPrepWarps);
         mbar_init(bar(G::B_QFREE), 1);
-        for (int i = 0; i < 4; ++i) mbar_init(bar(G::B_SFULL + i), 1);
+        for (int i = 0; i < G::kScoreBars; ++i) mbar_init(bar(G::B_SFULL + i), 1);
         for (int w = 0; w < 2; ++w) {
-            mbar_init(bar(G::B_PFULL + w), G::kSplit ? 8 : 4);
-            mbar_init(bar(G::B_PVDONE + w), 1);
-            mbar_init(bar(G::B_OFREE + w), 8);
+            mbar_init(bar(G::B_PFULL + w), G::kSplit ? G::kWeighWarps : 4);
+            mbar_init(bar(G::B_OFREE + w), G::kWeighWarps);
         }
         mbar_init(bar(G::B_OFULL), 1);
-        mbar_init(bar(G::B_JOIN), 8);
+        mbar_init(bar(G::B_JOIN), G::kWeighWarps);
         mbar_init(bar(G::B_END), 1);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
@@ -192,21 +192,21 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == 10) {
+    if (warp == G::kMmaWarp) {
         umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, G::kTmemCols);
         umma::tmem_relinquish();
     }
-    if (warp == 8) cut_work(p, misc, 0, cta, p.tidy && cta == 0, kExtraFew, lane);
+    if (warp == G::kCopyWarp) cut_work(p, misc, 0, cta, p.tidy && cta == 0, kExtraFew, lane);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
-    if (warp == 8) {
+    if (warp == G::kCopyWarp) {
         copy_role<G, 0>(p, tm_k, tm_v, sb, misc, 0, lane);
-    } else if (warp == 9) {
+    } else if (warp == G::kCopyWarp + 1) {
         copy_role<G, 1>(p, tm_k, tm_v, sb, misc, 0, lane);
-    } else if (warp == 10) {
+    } else if (warp == G::kMmaWarp) {
         // --------------------------------------------------------------- MMAs
         if (lane == 0) {
             const uint64_t qdesc = FP8 ? code_desc<D>(sb + G::kQOff) : umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
@@ -233,38 +233,51 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc);
                 if (!ok) break;
                 int sc = 0;                      // next chunk to issue S^T of
-                // S^T of the chunks up to c, and of up to three more whose keys are
-                // there: buffer g & 3 was read for chunk g - 4, whose weights have
-                // been waited for when chunk c >= g - 3 comes
+                auto scores = [&](int g) {
+                    umma::fence_after_sync();
+                    const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
+                    const uint32_t d = tmem + (uint32_t)(N * (g & 3));
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                umma::mma_e4m3_ss(d, kd + (uint64_t)((kk * 32) >> 4),
+                                                  qdesc + (uint64_t)((part * N * D + kk * 32) >> 4), idesc_s,
+                                                  part + kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma::mma_bf16_ss(d, kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4),
+                                              qdesc + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
+                                              idesc_s, kk > 0);
+                    }
+                    // (one commit for the scores and the slot of K: each takes this
+                    // thread ~100 clocks)
+                    umma::commit(bar(KR::free(g)));
+                    if (++sc == nc) umma::commit(bar(G::B_QFREE));
+                };
+                // S^T of the chunks up to c, and of some more: buffer g & 3 was read for
+                // chunk g - 4, whose weights have been waited for when chunk g - 3 comes.
+                // A ring of four slots or more holds two chunks ahead; with two slots, as
+                // many as happen to be there.
                 auto scores_up_to = [&](int c) -> bool {
-                    for (; sc <= c + 3 && sc < nc; ++sc) {
+                    if (G::kKSlots >= 4) {
+                        for (const int to = min(c + 3, nc); sc < to;) {
+                            const int g = g0 + sc;
+                            if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) return false;
+                            scores(g);
+                        }
+                        return true;
+                    }
+                    while (sc <= c + 3 && sc < nc) {
                         const int g = g0 + sc;
                         if (sc > c) {
                             if (misc[M_KISSUED] <= g || !mbar_test(bar(KR::full(g)), KR::parity(g))) break;
                         } else if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) {
                             return false;
                         }
-                        umma::fence_after_sync();
-                        const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
-                        const uint32_t d = tmem + (uint32_t)(N * (g & 3));
-                        if constexpr (FP8) {
-#pragma unroll
-                            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                                for (int kk = 0; kk < D / 32; ++kk)
-                                    umma::mma_e4m3_ss(d, kd + (uint64_t)((kk * 32) >> 4),
-                                                      qdesc + (uint64_t)((part * N * D + kk * 32) >> 4), idesc_s,
-                                                      part + kk > 0);
-                        } else {
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                umma::mma_bf16_ss(d, kd + (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4),
-                                                  qdesc + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
-                                                  idesc_s, kk > 0);
-                        }
-                        umma::commit(bar(G::B_SFULL + (g & 3)));
-                        umma::commit(bar(KR::free(g)));
-                        if (sc + 1 == nc) umma::commit(bar(G::B_QFREE));
+                        scores(g);
                     }
                     return true;
                 };
@@ -284,13 +297,20 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
                     const uint64_t pd = pdesc + (uint64_t)((pbuf * G::kPBuf) >> 4);
                     const int np = w.chunk_pages(c);
-                    for (int kk = 0; kk < np; ++kk)
+                    auto page = [&](int kk) {
                         umma::mma_bf16_ss(tmem + G::kColO + (uint32_t)(G::kSplit ? 0 : pbuf * G::kPW),
                                           vd + (uint64_t)((kk * kBlock * 128) >> 4),
                                           pd + (uint64_t)((kk * kBlock * 128) >> 4), idesc_pv,
                                           !(c < G::kAccs && kk == 0));
-                    umma::commit(bar(VR::free(g)));
-                    umma::commit(bar(G::B_PVDONE + pbuf));
+                    };
+                    if (np == kPages) {
+#pragma unroll
+                        for (int kk = 0; kk < kPages; ++kk) page(kk);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < np; ++kk) page(kk);
+                    }
+                    umma::commit(bar(VR::free(g)));      // and the buffer of P
                     if (c + 1 == nc) umma::commit(bar(G::B_OFULL));
                 }
                 g0 += nc;
@@ -351,16 +371,17 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     } else {
         // ------------------------------------------------- weights and output
         const int grp = warp >> 2, key = tid & 127, wq = warp & 3;
-        const int row0 = G::kSplit ? 32 * grp : 0;       // the group's first row
+        constexpr int R = 32;                    // rows that a group weighs
+        const int row0 = G::kSplit ? R * grp : 0;        // the group's first row
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         // the group's columns of its accumulator; the low parts are N further on
         const uint32_t tO = lanes + G::kColO + (uint32_t)(G::kSplit ? row0 : grp * G::kPW);
-        float2* sn = reinterpret_cast<float2*>(gb + G::kSnOff) + grp * 32;
-        float* ref = reinterpret_cast<float*>(gb + G::kRefOff) + grp * 32;
-        float* alphas = reinterpret_cast<float*>(gb + G::kAlphaOff) + grp * 32;
-        float* wmax = reinterpret_cast<float*>(gb + G::kWmaxOff) + grp * 128;
+        float2* sn = reinterpret_cast<float2*>(gb + G::kSnOff) + grp * R;
+        float* ref = reinterpret_cast<float*>(gb + G::kRefOff) + grp * R;
+        float* alphas = reinterpret_cast<float*>(gb + G::kAlphaOff) + grp * R;
+        float* wmax = reinterpret_cast<float*>(gb + G::kWmaxOff) + grp * 4 * R;
         volatile int* unset = reinterpret_cast<volatile int*>(gb + G::kUnsetOff) + grp;
-        if (p.tidy) zero_empty(p, D, cta, p.nctas, tid, 256);
+        if (p.tidy) zero_empty(p, D, cta, p.nctas, tid, G::kWeighWarps * 32);
         if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
         int joins = 0, g0 = 0, flat = misc[M_B0];
         bool ok = true;
@@ -388,13 +409,14 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int rows = w.q.n * p.G;
             const uint32_t* anc = reinterpret_cast<const uint32_t*>(gb + G::kAncOff) + buf * kN * 4;
             const volatile uint32_t* padw = reinterpret_cast<const volatile uint32_t*>(gb + G::kPadOff) + buf * 4;
-            float l[32];                         // each row's sum over this thread's keys
+            const int plain = w.plain_chunks();
+            float l[R];                          // each row's sum over this thread's keys
 #pragma unroll
-            for (int k = 0; k < 32; ++k) l[k] = 0.f;
+            for (int k = 0; k < R; ++k) l[k] = 0.f;
             bool first = true;
             for (int c = G::kSplit ? 0 : (g0 ^ grp) & 1; c < nc; c += G::kSplit ? 1 : 2) {
                 const int g = g0 + c;
-                ok = ok && wait_warp(bar(G::B_SFULL + (g & 3)), (uint32_t)((g >> 2) & 1), misc);
+                ok = ok && wait_warp(bar(G::KRing::free(g)), G::KRing::free_parity(g), misc);
                 if (first) {
                     // the rows' scale and reference: none yet for rows that see
                     // something, and never a weight for the others
@@ -411,36 +433,41 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 umma::fence_after_sync();
                 const uint32_t tS = lanes + (uint32_t)(N * (g & 3) + row0);
-                const int np = w.chunk_pages(c), pos = (w.j + c * kPages) * kBlock + key;
+                const bool masked = c >= plain;          // (for the whole chunk)
                 // the rows that see this key, as bits
-                uint32_t vis = key < np * kBlock && pos < w.q.L ? ~0u : 0u;
-                if (w.drafted(c) && pos >= w.q.base && vis) {
-                    const int a = pos - w.q.base;
-                    vis = 0u;
-                    for (int r = row0; r < min(rows, row0 + 32); ++r)
-                        vis |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - row0);
+                uint32_t vis = ~0u;
+                bool there = true;                       // is the key in one of the chunk's pages?
+                if (masked) {
+                    const int pos = (w.j + c * kPages) * kBlock + key;
+                    there = key < w.chunk_pages(c) * kBlock;
+                    vis = there && pos < w.q.L ? ~0u : 0u;
+                    if (pos >= w.q.base && vis) {
+                        const int a = pos - w.q.base;
+                        vis = 0u;
+                        for (int r = row0; r < min(rows, row0 + R); ++r)
+                            vis |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - row0);
+                    }
                 }
-                const bool masked = w.drafted(c) || np < kPages;     // (for the whole chunk)
                 // the scores relative to the references, in log2 units
-                float t[32];
+                float t[R];
                 auto load = [&]() {
-                    umma::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&t[0]));
+                    umma::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[R]>(&t[0]));
                     umma::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
+                    for (int k = 0; k < R; k += 2) {
                         const float4 f = *reinterpret_cast<const float4*>(sn + k);   // two rows
                         t[k] = fmaf(t[k], f.x, f.y);
                         t[k + 1] = fmaf(t[k + 1], f.z, f.w);
                     }
                     if (masked) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) t[k] = (vis >> k) & 1u ? t[k] : -INFINITY;
+                        for (int k = 0; k < R; ++k) t[k] = (vis >> k) & 1u ? t[k] : -INFINITY;
                     }
                 };
                 load();
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], t[k]);
+                for (int k = 0; k < R; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], t[k], t[k + 1]);
                 const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // does any row's reference lag too far behind, or has a wait run out?
                 if (meet(!ok || most > kMaxLag + (FP8 ? kBiasF16 : 0.f) || *unset != 0)) {
@@ -451,15 +478,15 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     // ---- new references: the largest score of each row in the chunk
                     int best = INT32_MIN;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < R; ++k) {
                         // (relative to the old reference, or to none)
                         const int m = __reduce_max_sync(kFull, ordered(t[k]));
                         if (lane == k) best = m;
                     }
-                    wmax[wq * 32 + lane] = unordered(best);
+                    wmax[wq * R + lane] = unordered(best);
                     meet(false);
                     if (wq == 0) {
-                        const float rel = fmaxf(fmaxf(wmax[lane], wmax[32 + lane]), fmaxf(wmax[64 + lane], wmax[96 + lane]));
+                        const float rel = fmaxf(fmaxf(wmax[lane], wmax[R + lane]), fmaxf(wmax[2 * R + lane], wmax[3 * R + lane]));
                         const float2 f = sn[lane];
                         const float old = ref[lane];
                         const bool live = f.y != -INFINITY;
@@ -479,7 +506,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         // what has been accumulated follows, once the products under way
                         // are done: those of the group's chunk before
                         const int gb4 = G::kSplit ? g - 1 : g - 2;
-                        ok = wait_warp(bar(G::B_PVDONE + (gb4 & 1)), (uint32_t)((gb4 >> 1) & 1), misc);
+                        ok = wait_warp(bar(G::VRing::free(gb4)), G::VRing::free_parity(gb4), misc);
                     }
                     if (meet(!ok)) {
                         ok = false;
@@ -487,11 +514,11 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     if (!first) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) l[k] *= alphas[k];
+                        for (int k = 0; k < R; ++k) l[k] *= alphas[k];
                         umma::fence_after_sync();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < (G::kLow ? 64 : 32); c0 += 16) {
-                            const uint32_t at = tO + (uint32_t)(c0 < 32 ? c0 : c0 - 32 + N);
+                        for (int c0 = 0; c0 < (G::kLow ? 2 * R : R); c0 += 16) {
+                            const uint32_t at = tO + (uint32_t)(c0 < R ? c0 : c0 - R + N);
                             uint32_t o[16];
                             umma::tmem_ld16(at, o);
                             umma::tmem_wait_ld();
@@ -506,18 +533,18 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 // ---- the weights
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
+                for (int k = 0; k < R; ++k) {
                     t[k] = ex2(t[k]);
                     l[k] += t[k];
                 }
                 // the buffer: the products of the chunk before last are done.  (A wait
                 // that runs out is told at the next meeting; nothing is written then.)
-                if (g >= 2) ok = ok && wait_warp(bar(G::B_PVDONE + (g & 1)), (uint32_t)(((g >> 1) - 1) & 1), misc);
+                if (g >= 2) ok = ok && wait_warp(bar(G::VRing::free(g - 2)), G::VRing::free_parity(g - 2), misc);
                 first = false;
-                if (ok && key < np * kBlock) {
+                if (ok && there) {
                     const uint32_t pb = sb + (uint32_t)(G::kPOff + (g & 1) * G::kPBuf + key * 128);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
+                    for (int k = 0; k < R; k += 8) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -551,7 +578,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             // ---- the segment's result: the sums, and both groups' accumulators
             ok = wait_warp(bar(G::B_OFULL), (uint32_t)(seg & 1), misc);
             umma::fence_after_sync();
-            wmax[wq * 32 + lane] = column_sums(l, lane);
+            wmax[wq * R + lane] = column_sums(l, lane);
             if (first && wq == 0) ref[lane] = -INFINITY;     // no chunk of this group
             if (meet(!ok)) ok = false;
             if (!ok) break;
@@ -568,19 +595,17 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float* refs = reinterpret_cast<const float*>(gb + G::kRefOff);
                 float s[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (G::kSplit && q != tid >> 5) continue;
-                    const float* b = base + q * 128 + (tid & 31);
-                    m[q] = refs[q * 32 + (tid & 31)];
-                    s[q] = m[q] == -INFINITY ? 0.f : (b[0] + b[32]) + (b[64] + b[96]);
+                for (int q = 0; q < G::kAccs; ++q) {
+                    const int g = G::kSplit ? tid / R : q, r = tid % R;
+                    const float* b = base + g * 4 * R + r;
+                    m[q] = refs[g * R + r];
+                    s[q] = m[q] == -INFINITY ? 0.f : (b[0] + b[R]) + (b[2 * R] + b[3 * R]);
                 }
                 const float M = fmaxf(m[0], m[1]);
                 const float a0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - M);
                 const float a1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - M);
                 const float L = s[0] * a0 + s[1] * a1;
-                // (split rows: one accumulator, whose factor is in either place)
-                fac[tid] = make_float4(G::kSplit ? a0 + a1 : a0, a1,
-                                       whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
+                fac[tid] = make_float4(a0, a1, whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
                 const int nd = row_node(p, tid);
                 rowat[tid] = whole ? (w.q.t0 + nd) * p.Hq + w.h * p.G + tid - nd * p.G : (int)(slot * N) + tid;
                 if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
@@ -664,7 +689,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     umma::fence_before_sync();
     __syncthreads();
-    if (warp == 10) {
+    if (warp == G::kMmaWarp) {
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, G::kTmemCols);
     }

@@ -171,14 +171,17 @@ __device__ __forceinline__ int row_node(const TreeParams& p, int r)
     return p.g_magic ? (int)__umulhi((uint32_t)r, p.g_magic) : r;
 }
 
-// One ring that the MMAs read: chunk g's slot, its barriers and their parity.
-template <int SLOTS, int FULL, int FREE>
+// One ring that the MMAs read: chunk g's slot, its barriers and their parity.  The
+// barriers that say a chunk's slot may be refilled may be more than the slots.
+template <int SLOTS, int FULL, int FREE, int FREES = SLOTS>
 struct Ring {
     static constexpr int kSlots = SLOTS;
-    static __device__ __forceinline__ int slot(int g) { return g % SLOTS; }
-    static __device__ __forceinline__ uint32_t parity(int g) { return (uint32_t)((g / SLOTS) & 1); }
-    static __device__ __forceinline__ int full(int g) { return FULL + g % SLOTS; }
-    static __device__ __forceinline__ int free(int g) { return FREE + g % SLOTS; }
+    static_assert(FREES >= SLOTS, "a slot's release is seen before the barrier's next phase");
+    static __device__ __forceinline__ int slot(int g) { return (int)((uint32_t)g % SLOTS); }
+    static __device__ __forceinline__ uint32_t parity(int g) { return (uint32_t)g / SLOTS & 1u; }
+    static __device__ __forceinline__ int full(int g) { return FULL + slot(g); }
+    static __device__ __forceinline__ int free(int g) { return FREE + (int)((uint32_t)g % FREES); }
+    static __device__ __forceinline__ uint32_t free_parity(int g) { return (uint32_t)g / FREES & 1u; }
 };
 
 // The segments of a CTA's range: the pages [j, j + np) of one (sequence, KV
@@ -206,6 +209,11 @@ struct Walk {
     __device__ __forceinline__ bool drafted(int c) const
     {
         return (j + c * kPages + chunk_pages(c)) * kBlock > q.base;
+    }
+    // the chunks before the first that is not whole or reaches them
+    __device__ __forceinline__ int plain_chunks() const
+    {
+        return max(0, min(np, q.base / kBlock - j) / kPages);
     }
     __device__ __forceinline__ bool whole() const { return j == 0 && np == q.nb; }
     __device__ __forceinline__ void next(const TreeParams& p, int first_row)
@@ -348,7 +356,8 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
     };
     auto issue = [&](auto ring, int off, int slot_bytes, int which, const CUtensorMap& tm, int& g, const Pages& c) -> bool {
         using R = decltype(ring);
-        if (g >= R::kSlots && !wait_warp(bar(R::free(g)), R::parity(g) ^ 1u, misc)) return false;
+        if (g >= R::kSlots && !wait_warp(bar(R::free(g - R::kSlots)), R::free_parity(g - R::kSlots), misc))
+            return false;
         const uint32_t fb = bar(R::full(g));
         if (lane == 0) {
             if (c.n > 0) mbar_arrive_expect_tx(fb, (uint32_t)(c.n * G::kPageBytes));
@@ -540,7 +549,8 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
     for (int ch = 0; ch < nc; ++ch) {
         const int g = g0 + ch;
         if (!wait_warp(bar(L::full(g)), L::parity(g), misc)) return false;
-        if (g >= R::kSlots && !wait_warp(bar(R::free(g)), R::parity(g) ^ 1u, misc)) return false;
+        if (g >= R::kSlots && !wait_warp(bar(R::free(g - R::kSlots)), R::free_parity(g - R::kSlots), misc))
+            return false;
         if (pw == 0 && lane == 0) misc[M_VISSUED] = g + 1;
         const uint32_t raw = sb + (uint32_t)(G::kVLoadOff + L::slot(g) * G::kLoadBytes) + src0;
         const uint32_t dst = sb + (uint32_t)(G::kVOff + R::slot(g) * G::kSlot);
