@@ -515,6 +515,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + (FP8 ? kBiasF16 : 0.f);
                     const u64 sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
                     u64 ls[2] = {0ull, 0ull};
+                    float lr[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
                     auto weigh = [&](auto all) {         // all: no key is masked
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
@@ -533,11 +534,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 }
                                 hi[e] = FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
                                 if (LOW) lo[e] = pack_bf16x2(w0 - bf16_lo(hi[e]), w1 - bf16_hi(hi[e]));
-                                if (!FP8 && !LOW) {
-                                    w0 = bf16_lo(hi[e]);
-                                    w1 = bf16_hi(hi[e]);
-                                }
-                                ls[e & 1] = add2(ls[e & 1], pack2(w0, w1));
+                                if (!FP8 && !LOW) add_bf16x2(lr[e & 1][0], lr[e & 1][1], hi[e]);
+                                else ls[e & 1] = add2(ls[e & 1], pack2(w0, w1));
                             }
                             umma::tmem_st16(tS + (uint32_t)(32 * g), hi);
                             if (LOW) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), lo);
@@ -547,7 +545,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     else weigh(std::true_type());
                     float l0, l1;
                     unpack2(add2(ls[0], ls[1]), l0, l1);
-                    l += l0 + l1;
+                    l += (l0 + l1) + ((lr[0][0] + lr[0][1]) + (lr[1][0] + lr[1][1]));
                     first = false;
                     umma::tmem_wait_st();
                     umma::fence_before_sync();

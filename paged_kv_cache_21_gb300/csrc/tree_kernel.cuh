@@ -59,6 +59,15 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// a += the lower, b += the upper of two bf16.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x));
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float y;
