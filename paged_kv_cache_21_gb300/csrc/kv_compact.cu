@@ -182,7 +182,9 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
             p.cache[1][l] = static_cast<uint4*>(v_caches[l0 + l]);
         }
         p.columns = (int)(per_layer * nl);
-        const dim3 grid((unsigned)((p.columns + kThreads - 1) / kThreads), (unsigned)num_seqs);
+        // no more CTAs than run at once, so that the tables are looked up in one wave
+        const int want = (p.columns + kThreads - 1) / kThreads, room = 8 * num_sms_current() / num_seqs;
+        const dim3 grid((unsigned)(room < 1 ? 1 : want < room ? want : room), (unsigned)num_seqs);
         kv_tree_compact_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
         if (cudaGetLastError() != cudaSuccess) return KV_ERR_CUDA;
     }
