@@ -579,9 +579,14 @@ int paged_tree_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int
  * gives paged_decode_attention's result up to summation order.
  * Supported: head_dim 64 or 128, any num_q_heads that is a multiple of
  * num_kv_heads with G = num_q_heads / num_kv_heads <= 128.  Deterministic as
- * paged_decode_attention.  Errors as paged_decode_attention; KV_ERR_INVALID_ARG
- * also for max_nodes < 1 or total_nodes < 0, KV_ERR_TOO_LARGE for max_nodes
- * above KV_TREE_MAX_NODES. */
+ * paged_decode_attention.  Scores and the softmax's (max, sum) are float32;
+ * weights are multiplied as two bf16 parts (16 bits; E4M3 caches: f16), but as
+ * one bf16 (8 bits, the sum being that of the rounded weights) for a bf16
+ * output of a tree with more than 64 rows (n_s * G) over a bf16 cache.
+ * Errors as paged_decode_attention; KV_ERR_INVALID_ARG also for max_nodes < 1 or
+ * total_nodes < 0, KV_ERR_TOO_LARGE for max_nodes above KV_TREE_MAX_NODES,
+ * KV_ERR_UNSUPPORTED for total_nodes * num_q_heads, or num_seqs * num_kv_heads *
+ * (max_blocks_per_seq + 48), of 2^31 - 1 or more. */
 int paged_tree_attention(void* out, int out_dtype, const void* q, const void* k_cache,
                          const void* v_cache, int kv_dtype, float k_scale, float v_scale,
                          int num_blocks, const int32_t* block_tables, int max_blocks_per_seq,
@@ -643,7 +648,8 @@ int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32_t* out_tok
  * every layer's cache: for i < accept_lens[s], the vectors at position
  * base + accept_nodes[s][i] go to position base + i (all KV heads), in place.
  *   k_caches, v_caches: host arrays of num_layers device pointers, the caches of
- *                  the layers, all of the same shape, dtype and block tables
+ *                  the layers, all of the same shape, dtype and block tables, no
+ *                  two of them overlapping (else KV_ERR_INVALID_ARG)
  *   accept_nodes:  [num_seqs][max_nodes] int32, strictly increasing over its first
  *                  accept_lens[s] entries, each less than n_s (as kv_tree_verify
  *                  leaves it); accept_lens: [num_seqs] int32
@@ -680,7 +686,8 @@ int kv_read_ceiling(const void* buf, size_t bytes, unsigned* sink, void* stream)
  * that call's output is undefined.  In the wide-group kernel (groups of more
  * than 32 rows, bf16 cache, head_dim 128) the score-MMA warp of every CTA does so on its first wait, and every
  * role of the CTA then stops (copies and MMAs in flight are waited for and
- * tensor memory is freed before the CTA ends).  It lets a test see the flag without a
+ * tensor memory is freed before the CTA ends); so does the MMA warp of
+ * paged_tree_attention's kernels.  It lets a test see the flag without a
  * copy that really never arrives.  0 (the default) turns it off; a value
  * outside [0, 2^31] returns KV_ERR_INVALID_ARG.  Process-wide. */
 int kv_test_pipeline_stall(long long cycles);

@@ -124,6 +124,19 @@ __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
 
 }  // namespace
 
+// Do any two of the caches (n of K, then n of V, of `bytes` each) overlap?
+static bool overlap(void* const* k, void* const* v, int n, uintptr_t bytes)
+{
+    auto at = [&](int i) { return (uintptr_t)(i < n ? k[i] : v[i - n]); };
+    for (int i = 1; i < 2 * n; ++i) {
+        const uintptr_t a = at(i);
+        bool hit = false;
+        for (int j = 0; j < i; ++j) hit |= (a > at(j) ? a - at(j) : at(j) - a) < bytes;
+        if (hit) return true;
+    }
+    return false;
+}
+
 int compact_read_error(unsigned* flags, long long* detail)
 {
     DevErr e;
@@ -161,6 +174,9 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
         if (!k_caches[l] || !v_caches[l] ||
             (((uintptr_t)k_caches[l] | (uintptr_t)v_caches[l]) & 15) != 0)
             return KV_ERR_INVALID_ARG;
+    // (a move done twice could read what the first one has written)
+    if (overlap(k_caches, v_caches, num_layers, (uintptr_t)num_blocks * num_kv_heads * kBlock * row_bytes))
+        return KV_ERR_INVALID_ARG;
     if (num_seqs > 65535) return KV_ERR_TOO_LARGE;      // one grid row per sequence
     const long long per_layer = 2LL * num_kv_heads * (row_bytes / 16);
     if (per_layer * kLayersPerLaunch > INT32_MAX / 2) return KV_ERR_UNSUPPORTED;

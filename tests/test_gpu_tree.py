@@ -166,13 +166,12 @@ def test_tree_sizes(pk, n, D, fp8):
 @pytest.mark.parametrize("heads", [(32, 8), (8, 8), (64, 4)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_ragged_batch_with_empty_rows_sequences_and_padding(pk, heads, fp8):
-    rng = np.random.default_rng(3)
     counts = np.array([5, 0, 1, 64, 9, 33, 2, 0, 12, 20])
     ctx = np.array([700, 0, 0, 130, 3, 2500, 16, 40, 95, 0])
     lens = ctx + counts
     lens[8] = 0                                   # nodes of a sequence without a context
     c = Case(lens, counts, *heads, 128, fp8, pads=0.3, seed=4, extra_rows=5)
-    assert (c.parents == R.np.int32(-2)).any() and rng is not None
+    assert (c.parents == -2).any()
     c.check(c.run(pk))
     c.check(c.run(pk, torch.float32))
 
@@ -306,6 +305,37 @@ def test_repeated_calls_are_bit_identical_and_physical_places_do_not_matter(pk):
     b.bt = np.where(a.bt >= 0, perm[np.maximum(a.bt, 0)], -1).astype(np.int32)
     b.q, b.parents = a.q, a.parents
     assert torch.equal(first, b.run(pk))
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (32, 2)])
+@pytest.mark.parametrize("B", [3, 90, 700])
+def test_many_short_contexts_beside_long_ones(pk, heads, B):
+    """Cuts of the work at every place: within a sequence, at its first page, and
+    CTAs with many (sequence, KV head) pairs or none."""
+    rng = np.random.default_rng(B)
+    counts = rng.integers(0, 9, size=B)
+    counts[B // 2] = 20
+    ctx = np.where(rng.random(B) < 0.02, 3000, rng.integers(0, 40, size=B))
+    ctx[0], ctx[-1] = 2100, 1500
+    c = Case(ctx + counts, counts, *heads, 64, seed=B)
+    ref = c.reference()
+    for dtype in (torch.bfloat16, torch.float32):
+        c.check(c.run(pk, dtype), ref)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_wait_that_runs_out_is_flagged_and_the_next_call_is_right(pk, fp8):
+    """The hook's wait in the kernels for few and for many rows."""
+    for counts in ([4, 3], [40, 33]):
+        c = Case([900, 50], counts, 8, 2, 128, fp8, seed=21)
+        pk.set_pipeline_stall(20000)               # ~10 us of SM clocks
+        try:
+            c.run(pk)
+            torch.cuda.synchronize()
+        finally:
+            pk.set_pipeline_stall(0)
+        assert pk.get_device_error()[0] == pk.DEVERR_PIPELINE_TIMEOUT
+        c.check(c.run(pk, torch.float32))
 
 
 @pytest.mark.parametrize("heads,n,fp8", [((32, 8), 8, False), ((32, 8), 30, False),
@@ -699,6 +729,27 @@ def test_compaction_moves_the_accepted_nodes_and_nothing_else(pk, B, n_hi, layer
     for l in range(layers):
         k, v = R.compact(caches[0, l], caches[1, l], bt, lens, starts, nodes, accept)
         assert np.array_equal(got[0, l], k) and np.array_equal(got[1, l], v)
+
+
+def test_compaction_of_more_sequences_than_run_at_once_and_replayed(pk):
+    rng = np.random.default_rng(8)
+    counts, lens, bt, starts, nodes, accept, caches = _compact_case(rng, 1300, 6, 1, 2, 64, np.int16)
+    dev = torch.from_numpy(caches).cuda()
+    typed = dev.view(torch.bfloat16)
+    layers = pk.CacheLayers(list(typed[0]), list(typed[1]))
+    t = [torch.from_numpy(np.ascontiguousarray(a).astype(np.int32)).cuda()
+         for a in (bt, lens, starts, nodes, accept)]
+    zero = torch.zeros_like(t[4])
+    pk.kv_tree_compact(layers, *t[:4], zero)       # nothing accepted, nothing moves
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pk.kv_tree_compact(layers, *t)
+    assert np.array_equal(dev.cpu().numpy(), caches)
+    g.replay()
+    torch.cuda.synchronize()
+    got = dev.cpu().numpy()
+    k, v = R.compact(caches[0, 0], caches[1, 0], bt, lens, starts, nodes, accept)
+    assert np.array_equal(got[0, 0], k) and np.array_equal(got[1, 0], v)
 
 
 def test_compaction_leaves_out_paths_and_blocks_that_break_the_rules(pk):

@@ -161,6 +161,10 @@ def test_entry_points_refuse_bad_arguments_before_any_launch(pk):
                      (dict(bt=None), E), (dict(cl=None), E), (dict(st=None), E),
                      (dict(an=None), E), (dict(al=None), E), (dict(B=0), 0), (dict(nl=0), 0)]:
         assert compact(**kw) == code, kw
+    # caches that overlap: 8 blocks x 2 heads x 16 x 128 bytes = 32 KB each
+    size = 8 * 2 * 16 * 128
+    for v in ([1 << 20, (1 << 20) + 2 * size], [(1 << 20) + size - 16, 1 << 22], [4096, 4096]):
+        assert compact(k=(ctypes.c_void_p * 2)(1 << 20, 1 << 21), v=(ctypes.c_void_p * 2)(*v)) == E
 
 
 def test_the_binding_refuses_tensors_of_the_wrong_type_or_place(pk):
