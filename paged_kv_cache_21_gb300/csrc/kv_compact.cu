@@ -125,16 +125,19 @@ __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
 }  // namespace
 
 // Do any two of the caches (n of K, then n of V, of `bytes` each) overlap?
-static bool overlap(void* const* k, void* const* v, int n, uintptr_t bytes)
+// (All pairs: 2016 for 32 layers, in loops without branches.)
+static bool overlap(void* const* k, void* const* v, int n, uint64_t bytes)
 {
-    auto at = [&](int i) { return (uintptr_t)(i < n ? k[i] : v[i - n]); };
-    for (int i = 1; i < 2 * n; ++i) {
-        const uintptr_t a = at(i);
-        bool hit = false;
-        for (int j = 0; j < i; ++j) hit |= (a > at(j) ? a - at(j) : at(j) - a) < bytes;
-        if (hit) return true;
+    uint64_t hit = 0;
+    auto among = [&](uint64_t a, void* const* b, int m) {
+        for (int j = 0; j < m; ++j) hit |= (uint64_t)(a - (uint64_t)b[j] + (bytes - 1) < 2 * bytes - 1);
+    };
+    for (int i = 0; i < n; ++i) {
+        among((uint64_t)k[i], k, i);
+        among((uint64_t)v[i], v, i);
+        among((uint64_t)v[i], k, n);
     }
-    return false;
+    return hit != 0;
 }
 
 int compact_read_error(unsigned* flags, long long* detail)
@@ -175,7 +178,7 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
             (((uintptr_t)k_caches[l] | (uintptr_t)v_caches[l]) & 15) != 0)
             return KV_ERR_INVALID_ARG;
     // (a move done twice could read what the first one has written)
-    if (overlap(k_caches, v_caches, num_layers, (uintptr_t)num_blocks * num_kv_heads * kBlock * row_bytes))
+    if (overlap(k_caches, v_caches, num_layers, (uint64_t)num_blocks * num_kv_heads * kBlock * row_bytes))
         return KV_ERR_INVALID_ARG;
     if (num_seqs > 65535) return KV_ERR_TOO_LARGE;      // one grid row per sequence
     const long long per_layer = 2LL * num_kv_heads * (row_bytes / 16);
