@@ -436,6 +436,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (!ok) break;
                 if (warp_live) {
                     umma::fence_after_sync();
+                    // (a half without keys has scores of an earlier chunk, and sees none)
+                    uint32_t sr[2][32];
+                    umma::tmem_ld32(tS, sr[0]);
+                    umma::tmem_ld32(tS + 32u, sr[1]);
+                    umma::tmem_wait_ld();
                     if (FP8 && first)
                         sl2 = p.sl2 * reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * TILES * kTile + (in ? rt : 0)];
                     // the keys of group g (32 keys) this row sees, as bits
@@ -458,15 +463,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     // ---- the largest scaled score of this half, then of both
                     float mx = -INFINITY;
                     uint32_t vis[2] = {~0u, ~0u};
-                    uint32_t sr[2][32];
                     if (masked) {
                         vis[0] = visible(2 * half);
                         vis[1] = visible(2 * half + 1);
                     }
-                    // (a half without keys has scores of an earlier chunk, and sees none)
-                    umma::tmem_ld32(tS, sr[0]);
-                    umma::tmem_ld32(tS + 32u, sr[1]);
-                    umma::tmem_wait_ld();
                     if (!masked && sl2 >= 0.f) {
                         float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -489,19 +489,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     mx = fmaxf(mx, maxima[(1 - half) * kTile]);
                     // ---- the reference moves only when it lags by more than 2^8; what
                     // has been accumulated is then scaled down in place
-                    bool move = false;
-                    float alpha = 1.f;
-                    if (first) {
-                        m_ref = mx;
-                    } else if (in && mx > m_ref + kMaxLag) {
-                        alpha = ex2(m_ref - mx);         // 0 while nothing was seen
-                        m_ref = mx;
-                        l *= alpha;
-                        move = true;
-                    }
+                    const bool move = in && mx > m_ref + kMaxLag;      // (m_ref is -inf at first)
                     if (__any_sync(kFull, move)) {
+                        const float alpha = move ? ex2(m_ref - mx) : 1.f;    // 0 while nothing was seen
+                        if (move) m_ref = mx;
+                        l *= alpha;
 #pragma unroll 1
-                        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
+                        for (int c0 = first ? D : half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
                             uint32_t o[16];
                             umma::tmem_ld16(tO0 + (uint32_t)(128 * st + c0), o);
                             umma::tmem_wait_ld();

@@ -200,8 +200,8 @@ struct Weights {
     {
         const u64 nph = mul2(pack2(-ah, -ah), y);
         const u64 pe = fma2(pack2(al, al), y, fma2(pack2(ah, ah), y, nph));
-        const u64 s = add2(x, nph), b = sub2(s, x);
-        const u64 e = sub2(add2(sub2(x, sub2(s, b)), sub2(nph, b)), pe);
+        // (the sum's rounding error this way needs x >= a y: so it is where s > 0)
+        const u64 s = add2(x, nph), e = sub2(sub2(nph, sub2(s, x)), pe);
         float s0, s1, e0, e1;
         unpack2(s, s0, s1);
         unpack2(e, e0, e1);
