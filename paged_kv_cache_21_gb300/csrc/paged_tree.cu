@@ -25,24 +25,42 @@
 //    served by as many teams of CTAs, which cut the same keys the same way, so
 //    that the repeated reads of a tile of keys come at about the same time and
 //    hit L2.
-//  * One persistent CTA per SM takes an equal contiguous range of the flat
-//    (sequence, KV head, page) list and consumes it in chunks of up to 8 pages
-//    (128 keys).  Warp 8 streams K and V of a chunk through a ring with TMA.
-//  * Two streams work side by side, each with its own MMA warp (9, 10), four
-//    softmax warps (0-3, 4-7; one row a thread) and half of tensor memory: the
+//  * One persistent CTA per SM takes a contiguous range of the flat (sequence,
+//    KV head, page) list (cut_work) and consumes it in chunks of up to 8 pages
+//    (128 keys).  A warp each streams K and V into rings with TMA (E4M3: one warp
+//    both, and two warps widen V).
+//  * Two streams work side by side, each with its half of tensor memory: the
 //    scores S (128 columns), overwritten in place by the weights P, and the
 //    accumulator O.  With TILES == 2 a stream has its own row tile and both
 //    consume every chunk; with TILES == 1 they take the chunks in turn and
-//    their two results are joined at the end of the range.  So one stream's
-//    matrix products run under the other's exponentials.
+//    their two results are joined at the end of the range.
+//  * A row has two threads, in two of the stream's eight softmax warps: half of
+//    the chunk's keys each, 64 scores that stay in registers from the maximum (the
+//    two meet in shared memory) to the weights.
+//  * One thread issues all MMAs.  A stream's products are followed by its own next
+//    scores at once, so that one stream's softmax runs while the other has the
+//    tensor cores: with an MMA thread a stream they ran S S PV PV, and both softmax
+//    phases contended for the same units (458 us against 361, at 64 nodes x 4 heads
+//    of 32 x 8192 tokens).  A commit costs this thread ~100 clocks and a test of a
+//    barrier as much, so slots are released by plain arrivals behind a wait that is
+//    due anyway, and what is usually ready is waited for ahead (361 -> 331 us).
 //  * S = Q K^T with K as it lies in the ring; O += P V with P from tensor memory.
-//    P is f16 for an E4M3 cache (whose V warps 11-14 widen to f16, which holds
-//    every code exactly); for a bf16 cache it is bf16, in high and low
-//    parts (16 bits, two products) for a float32 output (LOW).  For a bf16 output
-//    the high part alone: its rounding, 2^-9 of each weight and averaged over
-//    the keys, stays below the output's own, and the second product would be a
-//    third of the tensor cores' time.  The sum is that of the rounded weights.
-//  * Only the chunks that reach the drafted positions need masks; there warp 11
+//    P is f16 for an E4M3 cache (whose V is widened to f16, which holds every code
+//    exactly); for a bf16 cache it is bf16, in high and low parts (16 bits, two
+//    products) for a float32 output (LOW).  For a bf16 output the high part
+//    alone: its rounding, 2^-8 of each weight at most and averaged over the keys,
+//    stays below the output's own, and the second product costs a fifth (397 us
+//    against 321).  The sum is that of the rounded weights.
+//  * Measured at 64 nodes x 4 heads of 32 x 8192 tokens: 321 us; the bytes take 164,
+//    the products 149 at the tensor cores' rate, 117 the exponentials.  A 128-key
+//    chunk takes ~4900 clocks; a stream's chain is 590 to issue S, 230 until it is
+//    seen, ~2400 of softmax (200 until the scores are read, 360 maximum, 200 for
+//    the halves to meet, 900 weights; four warps share a scheduler), 650 to issue
+//    P V, 450 until its end is seen.  P in tensor memory of its own with S two
+//    chunks ahead removes the chain but has both softmax phases contend again (332),
+//    and takes two waits a chunk for a float32 output (846 against 397); 64-key
+//    pieces of S cost as many MMA clocks as 128 (530 against 499 then).
+//  * Only the chunks that reach the drafted positions need masks; there a prep warp
 //    (or the widening warps) first zeroes the V rows behind the context and the
 //    infinities and NaN of drafted rows, which 0 * V would spread to nodes that
 //    do not see them; nodes that do see them get them added back at the end.

@@ -23,6 +23,14 @@
 // (gathered at once, for all nodes) in shared memory.  The CTA, warp and lane
 // that hold the cut then find the token; the row comes from L2 by then.  The
 // cluster is as large as lets all sequences run at once, two CTAs an SM.
+//
+// Measured: 64 trees of 26 nodes, 128000 float32 entries: 55 us, where the rows of
+// the last nodes take 9.6 at HBM's rate.  The sequence with the most refusals sums
+// five times in turn, ~9.5K clocks each: 256 KB a CTA and pass through its SM's
+// share of L2 bandwidth (two CTAs, 53 of ~64 bytes a clock), ~17 packed operations
+// for two entries beside it.  Clusters of 8 do not run all at once (61 us), more
+// but smaller CTAs are slower too (63); one chain of 5, 32000 entries: 10.2 us, of
+// launch, tree and one pass.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
