@@ -115,9 +115,15 @@ struct SmallGeo {
     static constexpr int kEnd = kUnsetOff + 16;
     static constexpr int kSmem = kEnd + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
-    // tensor memory: S^T buffers, then the accumulators
-    static constexpr uint32_t kColO = 4 * N;
-    static constexpr uint32_t kTmemCols = 4 * N + kAccs * kPW <= 256 ? 256 : 512;
+    // E4M3: the query's two parts are 2 N columns of one product, added by the groups
+    // (8 nodes x 4 heads of 32 x 8192 tokens: 134 -> 126 us), or, where the groups have
+    // no time left (64 rows: 151 -> 159 us), two products into the same columns.
+    static constexpr bool kSideBySide = FP8 && !kSplit;
+    // tensor memory: four S^T buffers, then the accumulators
+    static constexpr int kScoreCols = kSideBySide ? 2 * N : N;
+    static constexpr uint32_t kColO = 4 * kScoreCols;
+    static constexpr uint32_t kTmemCols = kColO + kAccs * kPW <= 256 ? 256 : 512;
+    static_assert(kColO + kAccs * kPW <= 512, "tensor memory");
 };
 
 // Order-preserving map of floats to ints (NaN aside).
@@ -217,7 +223,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             const uint64_t kdesc = FP8 ? code_desc<D>(sb + G::kKOff) : umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
             const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
             const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, kRegion, 1024);
-            constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, N, false, false)
+            constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, G::kScoreCols, false, false)
                                              : umma::idesc_bf16_f32(128, N, false, false);
             constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(128, G::kPW, true, true)
                                               : umma::idesc_bf16_f32(128, G::kPW, true, true);
@@ -240,10 +246,10 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 auto scores = [&](int g) {
                     umma::fence_after_sync();
                     const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
-                    const uint32_t d = tmem + (uint32_t)(N * (g & 3));
+                    const uint32_t d = tmem + (uint32_t)(G::kScoreCols * (g & 3));
                     if constexpr (FP8) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                        for (int part = 0; part < (G::kSideBySide ? 1 : 2); ++part)
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
                                 umma::mma_e4m3_ss(d, kd + (uint64_t)((kk * 32) >> 4),
@@ -266,17 +272,10 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // A ring of four slots or more holds two chunks ahead; with two slots, as
                 // many as happen to be there.
                 auto scores_up_to = [&](int c) -> bool {
-                    if (G::kKSlots >= 4) {
-                        for (const int to = min(c + 3, nc); sc < to;) {
-                            const int g = g0 + sc;
-                            if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) return false;
-                            scores(g);
-                        }
-                        return true;
-                    }
-                    while (sc <= c + 3 && sc < nc) {
+                    constexpr bool poll = G::kKSlots < 4;
+                    for (const int to = min(c + (poll ? 4 : 3), nc); sc < to;) {
                         const int g = g0 + sc;
-                        if (sc > c) {
+                        if (poll && sc > c) {
                             if (misc[M_KISSUED] <= g || !mbar_test(bar(KR::full(g)), KR::parity(g))) break;
                         } else if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) {
                             return false;
@@ -436,7 +435,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if (meet(!ok)) ok = false;
                 }
                 umma::fence_after_sync();
-                const uint32_t tS = lanes + (uint32_t)(N * (g & 3) + row0);
+                const uint32_t tS = lanes + (uint32_t)(G::kScoreCols * (g & 3) + row0);
                 const bool masked = c >= plain;          // (for the whole chunk)
                 // the rows that see this key, as bits
                 uint32_t vis = ~0u;
@@ -456,7 +455,15 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 float t[R];
                 auto load = [&]() {
                     umma::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[R]>(&t[0]));
-                    umma::tmem_wait_ld();
+                    if (G::kSideBySide) {
+                        float rest[R];
+                        umma::tmem_ld32(tS + (uint32_t)N, *reinterpret_cast<uint32_t(*)[R]>(&rest[0]));
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < R; ++k) t[k] += rest[k];
+                    } else {
+                        umma::tmem_wait_ld();
+                    }
 #pragma unroll
                     for (int k = 0; k < R; k += 2) {
                         const float4 f = *reinterpret_cast<const float4*>(sn + k);   // two rows
