@@ -662,7 +662,8 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_tables, context_lens, n
         _ptr("context_lens", context_lens, i32, B, dev),
         _ptr("node_starts", node_starts, i32, B + 1, dev),
         _ptr("parents", parents, i32, T, dev) if parents is not None else 0, B, T,
-        int(max_nodes), Hq, Hkv, D, float(scale), workspace.data_ptr(),
+        int(max_nodes), Hq, Hkv, D, float(scale),
+        _ptr("workspace", workspace, workspace.dtype, workspace.numel(), dev),
         workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
         "paged_tree_attention")
 
@@ -700,7 +701,8 @@ def kv_tree_verify(accept_lens, accept_nodes, out_tokens, target_probs, tokens, 
     if T <= 1:
         t_stride, d_stride = max(t_stride, V), max(d_stride, V)
     dev = _place(target_probs)
-    if draft is not None and draft.get_device() != target_probs.get_device():
+    if draft is not None and (draft.get_device() != target_probs.get_device()
+                              or (draft.get_device() < 0 and not draft.is_pinned())):
         raise ValueError("draft_probs must be where target_probs is")
     _check(_HOT_TREE_VERIFY(
         _ptr("accept_lens", accept_lens, i32, B, dev),
@@ -747,6 +749,8 @@ def kv_tree_compact(layers, block_tables, context_lens, node_starts, accept_node
     B, max_nodes = accept_nodes.shape
     max_blocks = block_tables.shape[1]
     dev, i32 = _place(layers.first), torch.int32
+    if layers.first.get_device() < 0 and not all(t.is_pinned() for x in layers.tensors for t in x):
+        raise ValueError("caches in host memory must be pinned")
     _check(_HOT_TREE_COMPACT(
         layers.k_ptrs, layers.v_ptrs, layers.num_layers,
         _ptr("block_tables", block_tables, i32, B * max_blocks, dev), max_blocks,

@@ -177,6 +177,16 @@ def test_a_ragged_batch_with_empty_rows_sequences_and_padding(pk, heads, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_most_rows_and_a_limit_above_the_trees(pk, D, fp8):
+    c = Case([128, 300, 17], [128, 100, 1], 128, 1, D, fp8, seed=5)     # 16384 rows a KV head
+    c.check(c.run(pk))
+    c = Case([500, 40, 17], [3, 5, 1], 8, 2, D, fp8, seed=6)
+    c.max_nodes = 128
+    c.check(c.run(pk, torch.float32))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_chains_need_no_parents(pk, fp8):
     c = Case([40, 500, 129], [8, 40, 1], 8, 2, 128, fp8, chain=True)
     c.check(c.run(pk, torch.float32))
