@@ -586,7 +586,7 @@ int paged_tree_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int
  * Errors as paged_decode_attention; KV_ERR_INVALID_ARG also for max_nodes < 1 or
  * total_nodes < 0, KV_ERR_TOO_LARGE for max_nodes above KV_TREE_MAX_NODES,
  * KV_ERR_UNSUPPORTED for total_nodes * num_q_heads, or num_seqs * num_kv_heads *
- * (max_blocks_per_seq + 48), of 2^31 - 1 or more. */
+ * (max_blocks_per_seq + 32), of 2^31 - 1 or more. */
 int paged_tree_attention(void* out, int out_dtype, const void* q, const void* k_cache,
                          const void* v_cache, int kv_dtype, float k_scale, float v_scale,
                          int num_blocks, const int32_t* block_tables, int max_blocks_per_seq,

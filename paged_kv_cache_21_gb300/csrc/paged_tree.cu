@@ -219,7 +219,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, kTmemCols);
         umma::tmem_relinquish();
     }
-    if (warp == G::kCopyWarp) cut_work(p, misc, first_row, cta, p.tidy && blockIdx.x == 0, kExtraMany, lane);
+    if (warp == G::kCopyWarp) cut_work(p, misc, first_row, cta, p.tidy && blockIdx.x == 0, lane);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -693,7 +693,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     p.meta[blockIdx.x] = make_int4(w.s, w.h, last - cta + 1, min(rows, TILES * kTile));
                 }
             }
-            flat += w.np + kExtraMany;
+            flat += w.np + kExtraPages;
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(G::B_OFREE + buf));
@@ -785,8 +785,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(cons
 }
 
 // -------------------------------------------------------------------- host
-
-constexpr int kMinPages = 4;
 
 int check_tree_shape(int num_seqs, int max_nodes, int Hq, int Hkv, int D, int kv_dtype)
 {
@@ -948,7 +946,7 @@ extern "C" int paged_tree_attention(void* out, int out_dtype, const void* q, con
     if (fp8 && !(k_scale > 0.f && v_scale > 0.f && std::isfinite(k_scale) && std::isfinite(v_scale)))
         return KV_ERR_INVALID_ARG;
     // flat work indices and tensor-map rows must fit in int32
-    if (((long long)max_blocks_per_seq + kExtraMany) * num_seqs * num_kv_heads >= INT_MAX ||
+    if (((long long)max_blocks_per_seq + kExtraPages) * num_seqs * num_kv_heads >= INT_MAX ||
         (long long)num_blocks * num_kv_heads >= INT_MAX ||
         (long long)max_blocks_per_seq * kBlock >= INT_MAX ||
         (long long)total_nodes * num_q_heads >= INT_MAX)

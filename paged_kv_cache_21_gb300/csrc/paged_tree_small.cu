@@ -206,7 +206,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, G::kTmemCols);
         umma::tmem_relinquish();
     }
-    if (warp == G::kCopyWarp) cut_work(p, misc, 0, cta, p.tidy && cta == 0, kExtraFew, lane);
+    if (warp == G::kCopyWarp) cut_work(p, misc, 0, cta, p.tidy && cta == 0, lane);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -691,7 +691,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const int last = (int)(((long long)flat + w.q.nb - 1) / misc[M_Q]);
                 p.meta[cta] = make_int4(w.s, w.h, last - cta + 1, rows);
             }
-            flat += w.np + kExtraFew;
+            flat += w.np + kExtraPages;
             g0 += nc;
             umma::fence_before_sync();
             __syncwarp();

@@ -247,16 +247,16 @@ struct Walk {
 
 // This CTA's range of its team's list of pages, by sequence and KV head: equal
 // shares of at least p.min_q units, where a page is a unit and each (sequence, KV
-// head) costs `extra` more before its first page (its queries, tree and results), so
+// head) costs kExtraPages more before its first page (its queries, tree and results), so
 // that CTAs with many short sequences get fewer pages.  One warp.
 __device__ __forceinline__ void cut_work(const TreeParams& p, volatile int* misc, int first_row, int cta,
-                                         bool flag, int extra, int lane)
+                                         bool flag, int lane)
 {
     long long total = 0;
     for (int b = 0; b < p.B; b += 32) {
         int nb = 0;
         if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, flag).nb;
-        total += warp_sum_ll(nb > 0 ? nb + extra : 0);
+        total += warp_sum_ll(nb > 0 ? nb + kExtraPages : 0);
     }
     total *= p.Hkv;
     long long q = (total + p.nctas - 1) / p.nctas;
@@ -274,7 +274,7 @@ __device__ __forceinline__ void cut_work(const TreeParams& p, volatile int* misc
     for (int b = 0; b < p.B && !(found[0] && found[1]); b += 32) {
         int nb = 0;
         if (b + lane < p.B) nb = seq_info(p, b + lane, first_row, false).nb;
-        const long long u = nb > 0 ? (long long)(nb + extra) * p.Hkv : 0, n = (long long)nb * p.Hkv;
+        const long long u = nb > 0 ? (long long)(nb + kExtraPages) * p.Hkv : 0, n = (long long)nb * p.Hkv;
         long long iu = u, in = n;
         for (int o = 1; o < 32; o <<= 1) {
             const long long tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
@@ -292,10 +292,10 @@ __device__ __forceinline__ void cut_work(const TreeParams& p, volatile int* misc
             if (found[e] || !m) continue;
             found[e] = true;
             const int src = __ffs(m) - 1;
-            const int nbs = __shfl_sync(kFull, nb, src), v = nbs + extra;
+            const int nbs = __shfl_sync(kFull, nb, src), v = nbs + kExtraPages;
             const long long before = __shfl_sync(kFull, iu - u, src);
-            const int off = (int)(x - before), h = off / v, j = max(0, off - h * v - extra);
-            at[e] = {b + src, h, j, before + (long long)h * v + extra + j,
+            const int off = (int)(x - before), h = off / v, j = max(0, off - h * v - kExtraPages);
+            at[e] = {b + src, h, j, before + (long long)h * v + kExtraPages + j,
                      __shfl_sync(kFull, in - n, src) + (long long)h * nbs + j};
         }
         units = __shfl_sync(kFull, iu, 31);

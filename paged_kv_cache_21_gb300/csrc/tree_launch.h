@@ -10,11 +10,16 @@
 
 namespace pkv {
 
+// The least range of a CTA, in pages: two chunks, so that a short context needs no
+// second kernel's work on its parts (1 x 1024 tokens, 8 KV heads: 16.1 us with 4 pages,
+// 14.6 with 8, 13.4 with 16, 15.7 with 32).
+constexpr int kMinPages = 16;
+
 // What a (sequence, KV head) costs a CTA beside its pages, in pages: a multiple of
 // the least range, so that short contexts are cut at their pages.  (64 contexts of 16
-// to 16384 tokens: 331 us without it, 233 with 8 and 16, 193 with 16 and 32, 186 with
-// 24 and 48, 185 with 32 and 64.)
-constexpr int kExtraFew = 24, kExtraMany = 48;
+// to 16384 tokens, by kernel for few, many rows: 219 us with 0, 48; 195 with 16, 48; 177
+// with 32, 48; 172 with 32, 32; 172 with 48, 32; 331 for none and both least ranges 4.)
+constexpr int kExtraPages = 32;
 
 struct TreeParams {
     const uint16_t* q;          // bf16 [total][Hq][D]
