@@ -10,9 +10,9 @@
 // What bounds it: nothing but the moved bytes, read and written once, and for
 // one sequence the chain launch -> tables -> data.  One launch covers every
 // layer (the pointers travel as kernel parameters): a launch a layer would cost
-// more than the moves.  Measured: 64 sequences x 32 layers, 38.8 MB: 12.4 us (5.7 at
+// more than the moves.  Measured: 64 sequences x 32 layers, 38.8 MB: 10.6 us (5.7 at
 // HBM's rate, the rest launch and tables: launch, lengths, paths, block ids and
-// the first loads wait for each other); one sequence: 6.5 us.
+// the first loads wait for each other); one sequence: 6.5 us, host time (1.5 on the device).
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
@@ -50,6 +50,9 @@ __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
     __shared__ long long s_src[KV_TREE_MAX_NODES], s_dst[KV_TREE_MAX_NODES];
     __shared__ int s_moves;
     const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    // (starts while the kernel before drains; lets the next one start at its end only,
+    // since that may read the caches early)
+    pdl_wait();
     if (tid < 32) {
         int t0, n, bad = s;
         const bool span_ok = tree_span(p.starts, s, INT32_MAX, p.max_nodes, t0, n, bad);
@@ -206,8 +209,16 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
         // no more CTAs than run at once, so that the tables are looked up in one wave
         const int want = (p.columns + kThreads - 1) / kThreads, room = 8 * num_sms_current() / num_seqs;
         const dim3 grid((unsigned)(room < 1 ? 1 : want < room ? want : room), (unsigned)num_seqs);
-        kv_tree_compact_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return KV_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, kv_tree_compact_kernel, p) != cudaSuccess) return KV_ERR_CUDA;
     }
     return KV_OK;
 }

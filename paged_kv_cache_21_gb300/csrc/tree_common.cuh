@@ -1,11 +1,24 @@
 // Draft-tree tables shared by the kernels that read them (paged_tree.cu,
-// tree_verify.cu, kv_compact.cu), and arithmetic on two floats at a time.
+// tree_verify.cu, kv_compact.cu), dependent launches, and arithmetic on two floats at
+// a time.
 #pragma once
 
 #include "device_common.cuh"
 #include "paged_kv.h"
 
 namespace pkv {
+
+// A kernel of a chain of dependent launches: wait until the kernels before it have
+// completed; let the next one start.
+__device__ __forceinline__ void pdl_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void pdl_launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // First node and number of nodes of sequence s.  False, with no nodes and the
 // bad value, for a pair of starts that breaks the rules.

@@ -42,16 +42,6 @@ constexpr float kBiasF16 = 7.f;
 // are on their way into the rings that the MMAs read
 enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_KISSUED, M_VISSUED };
 
-__device__ __forceinline__ void pdl_wait()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void pdl_launch_dependents()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

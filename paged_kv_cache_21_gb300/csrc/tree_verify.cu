@@ -24,12 +24,12 @@
 // that hold the cut then find the token; the row comes from L2 by then.  The
 // cluster is as large as lets all sequences run at once, two CTAs an SM.
 //
-// Measured: 64 trees of 26 nodes, 128000 float32 entries: 55 us, where the rows of
+// Measured: 64 trees of 26 nodes, 128000 float32 entries: 54 us, where the rows of
 // the last nodes take 9.6 at HBM's rate.  The sequence with the most refusals sums
 // five times in turn, ~9.5K clocks each: 256 KB a CTA and pass through its SM's
 // share of L2 bandwidth (two CTAs, 53 of ~64 bytes a clock), ~17 packed operations
 // for two entries beside it.  Clusters of 8 do not run all at once (61 us), more
-// but smaller CTAs are slower too (63); one chain of 5, 32000 entries: 10.2 us, of
+// but smaller CTAs are slower too (63); one chain of 5, 32000 entries: 8.2 us, of
 // launch, tree and one pass.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -338,6 +338,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(co
     const int s = blockIdx.x / ranks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int ES = BF16 ? 2 : 4;
+    // (the next kernel may start now, not before: all that was launched earlier is done)
+    pdl_wait();
+    pdl_launch_dependents();
 
     // ---- the tree, and the single probabilities at its tokens
     if (tid == 0) {
@@ -672,13 +675,15 @@ cudaError_t launch_verify(const VerifyParams& p, int num_seqs, int cluster, cuda
     cfg.gridDim = dim3((unsigned)(num_seqs * cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kv_tree_verify_kernel<BF16, VEC>, p);
 }
 
