@@ -59,7 +59,8 @@
 //    P V, 450 until its end is seen.  P in tensor memory of its own with S two
 //    chunks ahead removes the chain but has both softmax phases contend again (332),
 //    and takes two waits a chunk for a float32 output (846 against 397); 64-key
-//    pieces of S cost as many MMA clocks as 128 (530 against 499 then).
+//    pieces of S cost as many MMA clocks as 128 (530 against 499 then); products of
+//    half the keys while the others are weighed cost what they gain (327).
 //  * Only the chunks that reach the drafted positions need masks; there a prep warp
 //    (or the widening warps) first zeroes the V rows behind the context and the
 //    infinities and NaN of drafted rows, which 0 * V would spread to nodes that

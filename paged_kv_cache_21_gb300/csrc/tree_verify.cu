@@ -625,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_tree_verify_kernel(co
         Pair* shares = sh.sums[phase];           // (the exchange after next is not to come)
         if (lane == 0) shares[warp] = sum;
         __syncthreads();
-        // `of` things with a sum each, one a lane: the one that holds the cut, and `run`
-        // up to it.  (Rounding may leave none above t: the last with any weight.)
+        // Of consecutive shares, one a lane with its sum: the one that holds the cut, and
+        // the sum up to it.  (Rounding may leave none above t: the last with any weight.)
         auto cut = [&](Pair mine, Pair& upto_it) -> int {
             const Pair incl = add(upto_it, warp_scan(mine, lane));
             const unsigned hit = __ballot_sync(kFull, above(incl, t));
