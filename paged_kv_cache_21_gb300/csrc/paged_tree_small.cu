@@ -11,8 +11,8 @@
 //                       product, added at the end: the low part costs nothing).
 // 16 products, ~1030 clocks, for 128 keys, whose bf16 K and V take ~2450 clocks
 // to arrive at 6.8 TB/s over 152 SMs (E4M3: ~1220): HBM is the bound.  Measured:
-// 32 x 8192 tokens, 8 nodes x 4 heads, bf16: 171 us (bytes: 159); 4 x 131072: 318
-// (316); E4M3, 16 nodes x 4 heads: 151 us (80), where shared memory carries ~190 KB
+// 32 x 8192 tokens, 8 nodes x 4 heads, bf16: 172 us (bytes: 159); 4 x 131072: 318
+// (316); E4M3, 16 nodes x 4 heads: 150 us (80), where shared memory carries ~190 KB
 // a chunk (~1500 clocks: codes, widened V, weights, the MMAs' operands), a chunk
 // keeps the MMA thread ~2400 clocks busy and a group's weights take as long.
 //
