@@ -50,8 +50,8 @@
 //    products) for a float32 output (LOW).  For a bf16 output the high part
 //    alone: its rounding, 2^-8 of each weight at most and averaged over the keys,
 //    stays below the output's own, and the second product costs a fifth (397 us
-//    against 324).  The sum is that of the rounded weights.
-//  * Measured at 64 nodes x 4 heads of 32 x 8192 tokens: 324 us; the bytes take 164,
+//    against 323).  The sum is that of the rounded weights.
+//  * Measured at 64 nodes x 4 heads of 32 x 8192 tokens: 323 us; the bytes take 164,
 //    the products 149 at the tensor cores' rate, 117 the exponentials.  A 128-key
 //    chunk takes ~4900 clocks; a stream's chain is 590 to issue S, 230 until it is
 //    seen, ~2400 of softmax (200 until the scores are read, 360 maximum, 200 for
@@ -210,7 +210,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < 8; ++i) mbar_init(bar(G::B_MAX + i), 2);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
-        misc[M_KISSUED] = 0;
         misc[M_VISSUED] = 0;
         fence_mbar_init();
     }

@@ -11,18 +11,22 @@
 //                       product, added at the end: the low part costs nothing).
 // 16 products, ~1030 clocks, for 128 keys, whose bf16 K and V take ~2450 clocks
 // to arrive at 6.8 TB/s over 152 SMs (E4M3: ~1220): HBM is the bound.  Measured:
-// 32 x 8192 tokens, 8 nodes x 4 heads, bf16: 172 us (bytes: 159); 4 x 131072: 318
-// (316); E4M3, 16 nodes x 4 heads: 150 us (80), where shared memory carries ~190 KB
-// a chunk (~1500 clocks: codes, widened V, weights, the MMAs' operands), a chunk
-// keeps the MMA thread ~2400 clocks busy and a group's weights take as long.
+// 32 x 8192 tokens, 8 nodes x 4 heads, bf16: 168 us (bytes: 159); 4 x 131072: 313
+// (316); E4M3, 8 nodes: 110 us, 16 nodes x 4 heads: 152 us (80), where shared memory
+// carries ~190 KB a chunk (~1500 clocks: codes, widened V, weights, the MMAs'
+// operands) and a group's weights take ~2300 clocks.
+//
+// Scores and products have an MMA thread each: one for both was busy ~2400 clocks a
+// chunk, of which the tensor cores 1024, with commits and waits of ~100 clocks (172
+// us for 8 nodes, E4M3 124; 16 nodes E4M3 150).
 //
 // How (the rest as in paged_tree.cu):
 //  * One thread per key of a chunk weighs that key for 32 rows, so the
 //    exponentials of few rows use all lanes, and a row's sum stays in a register
 //    of each lane until the end.  Two groups of four warps: up to 32 rows (N = 32)
 //    they take the chunks in turn, each with its own accumulator O^T and
-//    references; above (N = 64) each takes 32 rows of every chunk.  The score
-//    products run up to three chunks ahead (four S^T buffers).
+//    references; above (N = 64) each takes 32 rows of every chunk.  The scores run up
+//    to four chunks ahead (four S^T buffers).
 //  * The reference maximum of a row moves only when a score is more than 2^8
 //    above it (the four warps of a group agree on that once per chunk); the first
 //    chunk of a segment sets it.  Then, seldom, the columns of O^T and the sums
@@ -48,8 +52,8 @@ struct SmallGeo {
     static constexpr bool kSplit = N == 64;                  // the groups split the rows, not the chunks
     static constexpr int kWeighWarps = 8;                    // two groups of four
     static constexpr int kCopyWarp = kWeighWarps;            // K; the next V
-    static constexpr int kMmaWarp = kCopyWarp + 2;
-    static constexpr int kPrepWarp = kMmaWarp + 1;           // first of the prep / widening warps
+    static constexpr int kMmaWarp = kCopyWarp + 2;           // scores; the next products
+    static constexpr int kPrepWarp = kMmaWarp + 2;           // first of the prep / widening warps
     static constexpr int kPrepWarps = FP8 ? 4 : 1;
     static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
     static constexpr int kBoxes = D / 64;
@@ -92,12 +96,13 @@ struct SmallGeo {
     using VRing = Ring<kVSlots, FP8 ? B_VWIDE : B_VFULL, FP8 ? B_VWFREE : B_VEMPTY>;
     static constexpr int B_QFULL = B_FIX + (FP8 ? 0 : kVSlots);  // Q and the tree of a segment
     static constexpr int B_QFREE = B_QFULL + 1;              // its last scores are computed
-    static constexpr int B_PFULL = B_QFREE + 1;              // + buffer of P: weights written
+    static constexpr int B_SFREE = B_QFREE + 1;              // + buffer (4): the scores have been read
+    static constexpr int B_PFULL = B_SFREE + 4;              // + buffer of P: weights written
     static constexpr int B_OFULL = B_PFULL + 2;              // the accumulators are complete
     static constexpr int B_OFREE = B_OFULL + 1;              // + segment & 1: they have been read
     static constexpr int B_JOIN = B_OFREE + 2;               // the groups meet
-    static constexpr int B_END = B_JOIN + 1;                 // all MMAs are done
-    static constexpr int B_STALL = B_END + 1;                // nothing arrives (the test hook)
+    static constexpr int B_END = B_JOIN + 1;                 // + MMA warp: all its MMAs are done
+    static constexpr int B_STALL = B_END + 2;                // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kAncOff = kMiscOff + 64;            // [2][kN][4] words
@@ -193,10 +198,10 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         mbar_init(bar(G::B_OFULL), 1);
         mbar_init(bar(G::B_JOIN), G::kWeighWarps);
-        mbar_init(bar(G::B_END), 1);
+        for (int w = 0; w < 2; ++w) mbar_init(bar(G::B_END + w), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(G::B_SFREE + i), G::kSplit ? G::kWeighWarps : 4);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
-        misc[M_KISSUED] = 0;
         misc[M_VISSUED] = 0;
         fence_mbar_init();
     }
@@ -217,20 +222,14 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
     } else if (warp == G::kCopyWarp + 1) {
         copy_role<G, 1>(p, tm_k, tm_v, sb, misc, 0, lane);
     } else if (warp == G::kMmaWarp) {
-        // --------------------------------------------------------------- MMAs
+        // ------------------------------------------------------------- scores
         if (lane == 0) {
             const uint64_t qdesc = FP8 ? code_desc<D>(sb + G::kQOff) : umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
             const uint64_t kdesc = FP8 ? code_desc<D>(sb + G::kKOff) : umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
-            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
-            const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, kRegion, 1024);
             constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, G::kScoreCols, false, false)
                                              : umma::idesc_bf16_f32(128, N, false, false);
-            constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(128, G::kPW, true, true)
-                                              : umma::idesc_bf16_f32(128, G::kPW, true, true);
             using KR = typename G::KRing;
-            using VR = typename G::VRing;
-            uint32_t fix_parity = 0;             // bit slot: parity of its next fix
-            int g0 = 0;                          // first chunk of the segment
+            int g = 0;                           // chunk of the CTA
             bool ok = true;
             if (p.test_stall > 0 && misc[M_CNT] > 0 &&
                 !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
@@ -239,11 +238,13 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ok = false;
             }
             for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
-                const int nc = w.chunks(), seg = w.seg;
-                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(seg & 1), misc);
-                if (!ok) break;
-                int sc = 0;                      // next chunk to issue S^T of
-                auto scores = [&](int g) {
+                const int nc = w.chunks();
+                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(w.seg & 1), misc);
+                for (int c = 0; ok && c < nc; ++c, ++g) {
+                    // the buffer was read for chunk g - 4
+                    if (g >= 4) ok = wait_bar(bar(G::B_SFREE + (g & 3)), (uint32_t)((g >> 2) - 1) & 1u, misc);
+                    ok = ok && wait_bar(bar(KR::full(g)), KR::parity(g), misc);
+                    if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t kd = kdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
                     const uint32_t d = tmem + (uint32_t)(G::kScoreCols * (g & 3));
@@ -265,29 +266,31 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     // (one commit for the scores and the slot of K: each takes this
                     // thread ~100 clocks)
                     umma::commit(bar(KR::free(g)));
-                    if (++sc == nc) umma::commit(bar(G::B_QFREE));
-                };
-                // S^T of the chunks up to c, and of some more: buffer g & 3 was read for
-                // chunk g - 4, whose weights have been waited for when chunk g - 3 comes.
-                // A ring of four slots or more holds two chunks ahead; with two slots, as
-                // many as happen to be there.
-                auto scores_up_to = [&](int c) -> bool {
-                    constexpr bool poll = G::kKSlots < 4;
-                    for (const int to = min(c + (poll ? 4 : 3), nc); sc < to;) {
-                        const int g = g0 + sc;
-                        if (poll && sc > c) {
-                            if (misc[M_KISSUED] <= g || !mbar_test(bar(KR::full(g)), KR::parity(g))) break;
-                        } else if (!wait_bar(bar(KR::full(g)), KR::parity(g), misc)) {
-                            return false;
-                        }
-                        scores(g);
-                    }
-                    return true;
-                };
-                for (int c = 0; ok && c < nc; ++c) {
-                    const int g = g0 + c, vs = VR::slot(g), pbuf = g & 1;
-                    ok = scores_up_to(c) && wait_bar(bar(G::B_PFULL + pbuf), (uint32_t)((g >> 1) & 1), misc) &&
-                         wait_bar(bar(VR::full(g)), VR::parity(g), misc);
+                    if (c + 1 == nc) umma::commit(bar(G::B_QFREE));
+                }
+            }
+            // every MMA issued by this thread is complete before the CTA ends
+            umma::commit(bar(G::B_END));
+            mbar_wait_bounded(bar(G::B_END), 0u, kWaitLimit);
+        }
+        __syncwarp();
+    } else if (warp == G::kMmaWarp + 1) {
+        // ----------------------------------------------------------- products
+        if (lane == 0) {
+            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, kRegion, 1024);
+            const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, kRegion, 1024);
+            constexpr uint32_t idesc_pv = FP8 ? umma::idesc_f16_f32(128, G::kPW, true, true)
+                                              : umma::idesc_bf16_f32(128, G::kPW, true, true);
+            using VR = typename G::VRing;
+            uint32_t fix_parity = 0;             // bit slot: parity of its next fix
+            int g = 0;                           // chunk of the CTA
+            bool ok = true;
+            for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
+                const int nc = w.chunks(), seg = w.seg;
+                for (int c = 0; ok && c < nc; ++c, ++g) {
+                    const int vs = VR::slot(g), pbuf = g & 1;
+                    // what is usually there comes first, the weights last
+                    ok = wait_bar(bar(VR::full(g)), VR::parity(g), misc);
                     if (ok && !FP8 && w.drafted(c)) {
                         ok = wait_bar(bar(G::B_FIX + vs), (fix_parity >> vs) & 1u, misc);
                         fix_parity ^= 1u << vs;
@@ -295,6 +298,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     // the accumulators of the segment before have been read
                     if (ok && c < G::kAccs && seg > 0)
                         ok = wait_bar(bar(G::B_OFREE + ((seg - 1) & 1)), (uint32_t)(((seg - 1) >> 1) & 1), misc);
+                    ok = ok && wait_bar(bar(G::B_PFULL + pbuf), (uint32_t)((g >> 1) & 1), misc);
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t vd = vdesc + (uint64_t)((vs * G::kSlot) >> 4);
@@ -316,11 +320,9 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     umma::commit(bar(VR::free(g)));      // and the buffer of P
                     if (c + 1 == nc) umma::commit(bar(G::B_OFULL));
                 }
-                g0 += nc;
             }
-            // every MMA issued by this thread is complete before the CTA ends
-            umma::commit(bar(G::B_END));
-            mbar_wait_bounded(bar(G::B_END), 0u, kWaitLimit);
+            umma::commit(bar(G::B_END + 1));
+            mbar_wait_bounded(bar(G::B_END + 1), 0u, kWaitLimit);
         }
         __syncwarp();
     } else if (warp >= G::kPrepWarp) {
@@ -416,10 +418,18 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
             float l[R];                          // each row's sum over this thread's keys
 #pragma unroll
             for (int k = 0; k < R; ++k) l[k] = 0.f;
-            bool first = true;
+            bool first = true, pending = false;  // pending: a row has no reference yet
             for (int c = G::kSplit ? 0 : (g0 ^ grp) & 1; c < nc; c += G::kSplit ? 1 : 2) {
                 const int g = g0 + c;
-                ok = ok && wait_warp(bar(G::KRing::free(g)), G::KRing::free_parity(g), misc);
+                // the scores; and the buffer of P: the products of the chunk before last
+                // are done, which groups that take every chunk wait for here, others,
+                // whose own last chunk that was, when they need it.  (A wait that runs out
+                // is told at the next meeting; nothing is written then.)
+                auto buffer_free = [&]() -> bool {
+                    return g < 2 || wait_bar(bar(G::VRing::free(g - 2)), G::VRing::free_parity(g - 2), misc);
+                };
+                ok = __all_sync(kFull, ok && wait_bar(bar(G::KRing::free(g)), G::KRing::free_parity(g), misc) &&
+                                           (!G::kSplit || buffer_free()));
                 if (first) {
                     // the rows' scale and reference: none yet for rows that see
                     // something, and never a weight for the others
@@ -433,6 +443,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (lane == 0) *unset = any;
                     }
                     if (meet(!ok)) ok = false;
+                    pending = *unset != 0;
                 }
                 umma::fence_after_sync();
                 const uint32_t tS = lanes + (uint32_t)(G::kScoreCols * (g & 3) + row0);
@@ -481,7 +492,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 for (int k = 0; k < R; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], t[k], t[k + 1]);
                 const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // does any row's reference lag too far behind, or has a wait run out?
-                if (meet(!ok || most > kMaxLag + (FP8 ? kBiasF16 : 0.f) || *unset != 0)) {
+                if (meet(!ok || most > kMaxLag + (FP8 ? kBiasF16 : 0.f) || pending)) {
                     if (meet(!ok)) {
                         ok = false;
                         break;
@@ -523,6 +534,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         ok = false;
                         break;
                     }
+                    pending = *unset != 0;
                     if (!first) {
 #pragma unroll
                         for (int k = 0; k < R; ++k) l[k] *= alphas[k];
@@ -548,9 +560,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     t[k] = ex2(t[k]);
                     l[k] += t[k];
                 }
-                // the buffer: the products of the chunk before last are done.  (A wait
-                // that runs out is told at the next meeting; nothing is written then.)
-                if (g >= 2) ok = ok && wait_warp(bar(G::VRing::free(g - 2)), G::VRing::free_parity(g - 2), misc);
+                if (!G::kSplit) ok = __all_sync(kFull, ok && buffer_free());
                 first = false;
                 if (ok && there) {
                     const uint32_t pb = sb + (uint32_t)(G::kPOff + (g & 1) * G::kPBuf + key * 128);
@@ -581,7 +591,10 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 fence_proxy_async_smem();
                 umma::fence_before_sync();
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(bar(G::B_PFULL + (g & 1)));
+                if (ok && lane == 0) {
+                    mbar_arrive(bar(G::B_PFULL + (g & 1)));
+                    mbar_arrive(bar(G::B_SFREE + (g & 3)));
+                }
             }
             // the group's warps go on together, or not at all
             if (meet(!ok)) ok = false;

@@ -38,9 +38,8 @@ constexpr float kMaxLag = 8.f;                  // the reference maximum may lag
 constexpr float kBiasF16 = 7.f;
 
 // misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
-// per CTA, first sequence, KV head and page; chunks whose K, and whose V,
-// are on their way into the rings that the MMAs read
-enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_KISSUED, M_VISSUED };
+// per CTA, first sequence, KV head and page; chunks whose V is on its way (bf16)
+enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_H0, M_J0, M_VISSUED };
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -75,20 +74,6 @@ __device__ __forceinline__ void cp_async_wait_all()
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Has the phase with the given parity completed?  Never waits.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Bounded wait that also gives up when another role of the CTA has given up.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* misc)
 {
@@ -105,16 +90,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-// Wait until the K or V (`which`) of chunk g is on its way into its slot.  A role
-// that does not follow every chunk of a ring (a stream that takes every second
-// one, the warp that fixes V rows) does this before it waits for the chunk's
-// barrier: the slot's previous phase is then known to be over, and the phase's
-// parity to be that of chunk g.
-__device__ __forceinline__ bool wait_issued(int which, int g, volatile int* misc)
+// Wait until the V of chunk g is on its way into its slot.  The warp that fixes V
+// rows, which does not follow every chunk of the ring, does this before it waits for
+// the chunk's barrier: the slot's previous phase is then known to be over, and the
+// phase's parity to be that of chunk g.
+__device__ __forceinline__ bool wait_issued(int g, volatile int* misc)
 {
-    if (misc[which] > g) return true;
+    if (misc[M_VISSUED] > g) return true;
     const long long t0 = clock64();
-    while (misc[which] <= g) {
+    while (misc[M_VISSUED] <= g) {
         if (misc[M_ABORT]) return false;
         if (clock64() - t0 > kWaitLimit) {
             misc[M_ABORT] = 1;
@@ -125,7 +109,7 @@ __device__ __forceinline__ bool wait_issued(int which, int g, volatile int* misc
     return true;
 }
 
-// The same for a whole warp.
+// wait_bar for a whole warp.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* misc)
 {
     return __all_sync(kFull, wait_bar(bar, parity, misc));
@@ -353,7 +337,7 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
         int z, n;
         bool mine;
     };
-    auto issue = [&](auto ring, int off, int slot_bytes, int which, const CUtensorMap& tm, int& g, const Pages& c) -> bool {
+    auto issue = [&](auto ring, int off, int slot_bytes, const CUtensorMap& tm, int& g, const Pages& c) -> bool {
         using R = decltype(ring);
         if (g >= R::kSlots && !wait_warp(bar(R::free(g - R::kSlots)), R::free_parity(g - R::kSlots), misc))
             return false;
@@ -371,14 +355,15 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
                 tma_load_3d(dst, &tm, box * 64, 0, c.z, fb);
         }
         ++g;
-        if ((!FP8 || which == M_KISSUED) && lane == 0) misc[which] = g;
         return true;
     };
     auto issue_k = [&](const Pages& c) {
-        return issue(typename G::KRing(), G::kKOff, G::kLoadBytes, M_KISSUED, tm_k, gk, c);
+        return issue(typename G::KRing(), G::kKOff, G::kLoadBytes, tm_k, gk, c);
     };
     auto issue_v = [&](const Pages& c) {
-        return issue(typename G::VLoad(), G::kVLoadOff, G::kLoadBytes, M_VISSUED, tm_v, gv, c);
+        if (!issue(typename G::VLoad(), G::kVLoadOff, G::kLoadBytes, tm_v, gv, c)) return false;
+        if (!FP8 && lane == 0) misc[M_VISSUED] = gv;
+        return true;
     };
     bool ok = true, held = false;                // (a warp for both: V comes a chunk after K)
     Pages before = {0, 0, false};
@@ -488,7 +473,7 @@ __device__ __forceinline__ bool fix_values(const TreeParams& p, const Walk& w, u
     for (int ch = 0; ok && ch < nc; ++ch) {
         if (!w.drafted(ch)) continue;
         const int gv = g0 + ch;
-        ok = __all_sync(kFull, wait_issued(M_VISSUED, gv, misc)) &&
+        ok = __all_sync(kFull, wait_issued(gv, misc)) &&
              wait_warp(bar(G::VRing::full(gv)), G::VRing::parity(gv), misc);
         if (!ok) break;
         const uint32_t vb = sb + (uint32_t)(G::kVOff + G::VRing::slot(gv) * G::kSlot);
@@ -550,7 +535,6 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
         if (!wait_warp(bar(L::full(g)), L::parity(g), misc)) return false;
         if (g >= R::kSlots && !wait_warp(bar(R::free(g - R::kSlots)), R::free_parity(g - R::kSlots), misc))
             return false;
-        if (pw == 0 && lane == 0) misc[M_VISSUED] = g + 1;
         const uint32_t raw = sb + (uint32_t)(G::kVLoadOff + L::slot(g) * G::kLoadBytes) + src0;
         const uint32_t dst = sb + (uint32_t)(G::kVOff + R::slot(g) * G::kSlot);
         auto store = [&](int step, const uint32_t (&v)[4]) {
