@@ -131,7 +131,8 @@ struct SmallGeo {
     static_assert(kColO + kAccs * kPW <= 512, "tensor memory");
 };
 
-// Order-preserving map of floats to ints (NaN aside).
+// Order-preserving map of floats to ints, NaN above infinity (the one that arithmetic
+// gives, whose sign bit is clear).
 __device__ __forceinline__ int ordered(float x)
 {
     const int b = __float_as_int(x);
@@ -141,6 +142,14 @@ __device__ __forceinline__ int ordered(float x)
 __device__ __forceinline__ float unordered(int b)
 {
     return __int_as_float(b >= 0 ? b : b ^ 0x7fffffff);
+}
+
+// The larger of two; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 
 // Sums over the warp of 32 values a lane: lane l gets the sum of v[l].
@@ -508,12 +517,15 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     wmax[wq * R + lane] = unordered(best);
                     meet(false);
                     if (wq == 0) {
-                        const float rel = fmaxf(fmaxf(wmax[lane], wmax[R + lane]), fmaxf(wmax[2 * R + lane], wmax[3 * R + lane]));
+                        const float rel = max_nan(max_nan(wmax[lane], wmax[R + lane]),
+                                                  max_nan(wmax[2 * R + lane], wmax[3 * R + lane]));
                         const float2 f = sn[lane];
                         const float old = ref[lane];
                         const bool live = f.y != -INFINITY;
-                        // rel = score * scale + f.y, with f.y = bias - reference, or 0 for none
-                        const float top = old == -INFINITY ? rel : rel - f.y;
+                        // rel = score * scale + f.y, with f.y = bias - reference, or 0 for none;
+                        // a row whose first scores hold NaN is NaN whatever its reference: 0
+                        float top = old == -INFINITY ? rel : rel - f.y;
+                        if (old == -INFINITY && top != top) top = 0.f;
                         float a = 1.f;
                         if (live && (old == -INFINITY ? top > -INFINITY : top > old + kMaxLag)) {
                             a = old == -INFINITY ? 0.f : ex2(old - top);
@@ -618,19 +630,22 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float* base = reinterpret_cast<const float*>(gb + G::kWmaxOff);
                 const float* refs = reinterpret_cast<const float*>(gb + G::kRefOff);
                 float s[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
+                const int nd = row_node(p, tid);
+                // (rows behind the last, and padding nodes, hold what their lanes computed)
+                const bool live = tid < rows && !((padw[nd >> 5] >> (nd & 31)) & 1u);
 #pragma unroll
                 for (int q = 0; q < G::kAccs; ++q) {
                     const int g = G::kSplit ? tid / R : q, r = tid % R;
                     const float* b = base + g * 4 * R + r;
                     m[q] = refs[g * R + r];
-                    s[q] = m[q] == -INFINITY ? 0.f : (b[0] + b[R]) + (b[2 * R] + b[3 * R]);
+                    // (0 for a group without a chunk; NaN among the scores makes it NaN)
+                    s[q] = live ? (b[0] + b[R]) + (b[2 * R] + b[3 * R]) : 0.f;
                 }
                 const float M = fmaxf(m[0], m[1]);
                 const float a0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - M);
                 const float a1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - M);
                 const float L = s[0] * a0 + s[1] * a1;
                 fac[tid] = make_float4(a0, a1, whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
-                const int nd = row_node(p, tid);
                 rowat[tid] = whole ? (w.q.t0 + nd) * p.Hq + w.h * p.G + tid - nd * p.G : (int)(slot * N) + tid;
                 if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
             }
