@@ -638,8 +638,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                     if (l == 0.f) {
+                        const bool lost = whole && in && !pad && sees_any(w.q, am);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = 0.f;
+                        for (int k = 0; k < 16; ++k) v[k] = lost ? __uint_as_float(0x7fffffffu) : 0.f;
                     }
                     if (any_back) {
 #pragma unroll 1
@@ -769,8 +770,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(cons
     int t0, n, bad;
     tree_span(p.starts, meta.x, p.total, p.max_nodes, t0, n, bad);
     const size_t at = ((size_t)(t0 + node) * p.Hq + (size_t)meta.y * p.G + g) * D + lane * V;
+    float none = 0.f;                            // the result of a row without weight
+    if (l == 0.f) {
+        const SeqInfo q = seq_info(p, meta.x, 0, false);
+        bool any = q.base > 0 && tree_parent(p.parents, t0, node, nullptr) != KV_TREE_PAD;
+        if (q.base == 0)
+            for (int a = node; a >= 0 && !any;) {
+                const int up = tree_parent(p.parents, t0, a, nullptr);
+                any = up != KV_TREE_PAD && a < q.L;
+                a = up;
+            }
+        if (any) none = __uint_as_float(0x7fffffffu);
+    }
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = l == 0.f ? 0.f : acc[k] * inv;
+    for (int k = 0; k < V; ++k) acc[k] = l == 0.f ? none : acc[k] * inv;
     if (p.out_f32) {
         float* dst = static_cast<float*>(p.out) + at;
         if constexpr (V == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);

@@ -645,7 +645,10 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float a0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - M);
                 const float a1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - M);
                 const float L = s[0] * a0 + s[1] * a1;
-                fac[tid] = make_float4(a0, a1, whole ? (L == 0.f ? 0.f : p.v_scale / L) : 1.f, L);
+                float z = 1.f;
+                if (whole && L != 0.f) z = p.v_scale / L;
+                else if (whole) z = live && sees_any(w.q, anc + nd * 4) ? __uint_as_float(0x7fffffffu) : 0.f;
+                fac[tid] = make_float4(a0, a1, z, L);
                 rowat[tid] = whole ? (w.q.t0 + nd) * p.Hq + w.h * p.G + tid - nd * p.G : (int)(slot * N) + tid;
                 if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
             }

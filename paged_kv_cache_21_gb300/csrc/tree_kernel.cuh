@@ -148,6 +148,19 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int s, int firs
     return q;
 }
 
+// Does a node that is not padding see any position?  `am`: the nodes it sees, as bits.
+// (A row that does, and whose weights sum to nothing, had scores of -inf alone: its
+// softmax is NaN.)
+__device__ __forceinline__ bool sees_any(const SeqInfo& q, const uint32_t* am)
+{
+    bool any = q.base > 0;
+    for (int k = 0; k < kN / 32; ++k) {
+        const int lim = q.L - 32 * k;            // (nodes there is no room for are not cached)
+        if (lim > 0) any = any || (lim < 32 ? am[k] & ((1u << lim) - 1u) : am[k]) != 0u;
+    }
+    return any;
+}
+
 // Node (within the sequence) of row r of a KV head's rows.
 __device__ __forceinline__ int row_node(const TreeParams& p, int r)
 {

@@ -85,3 +85,38 @@ def test_a_nan_key_gives_nan_to_the_nodes_that_see_it(pk, ctx, counts, heads, D,
         half = heads[0] // heads[1]
         assert np.isnan(ref[2, :half]).all() and np.isfinite(ref[:, half:]).all()
         same(c, c.run(pk, torch.float32), ref)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,heads", ROWS)
+@pytest.mark.parametrize("ctx", [0, 9, 400, 5000])
+def test_infinite_queries_follow_the_formula(pk, ctx, counts, heads, D, fp8):
+    """Scores of infinities of one sign or both; where a node sees only scores of -inf, the
+    softmax is NaN."""
+    c = Case([ctx + counts[0], 30 + counts[1]], counts, *heads, D, fp8, seed=ctx + counts[0])
+    c.parents[counts[0] - 1] = -2
+    # element 3 of every key of KV head 0 is negative, element 4 of both signs
+    if fp8:
+        c.k[:, 0, :, 3] |= 0x80
+        c.k[:, 0, :, 3][c.k[:, 0, :, 3] == 0x80] = 0x90
+    else:
+        c.k[:, 0, :, 3] = -c.k[:, 0, :, 3].abs()
+    c.q[1, 0, 3] = float("inf")
+    c.q[2, 1, 3] = float("-inf")
+    c.q[3, 0, 4] = float("inf")
+    c.q[counts[0] - 1, 0, 4] = float("inf")
+    ref = reference(c)
+    assert np.isnan(ref[1:3].diagonal()).all() and (ref[counts[0] - 1] == 0).all()
+    same(c, c.run(pk, torch.float32), ref)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,heads", ROWS)
+@pytest.mark.parametrize("ctx", [0, 9, 400, 5000])
+def test_infinite_keys_follow_the_formula(pk, ctx, counts, heads, D):
+    c = Case([ctx + counts[0], 30 + counts[1]], counts, *heads, D, seed=ctx + counts[0])
+    for pos in {ctx // 3, ctx + 1}:
+        c.k[c.bt[0, pos // BS], 0, pos % BS, 7] = float("inf")
+    ref = reference(c)
+    same(c, c.run(pk, torch.float32), ref)
