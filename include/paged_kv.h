@@ -560,7 +560,8 @@ int paged_decode_timed(void* out, int out_dtype, const void* q, const void* k_ne
 #define KV_TREE_PAD (-2)
 
 /* Workspace bytes of paged_tree_attention for at most num_seqs sequences of at
- * most max_nodes nodes on the current device.  As paged_decode's: no
+ * most max_nodes nodes on the current device: never less for a larger max_nodes,
+ * so that one sized for the largest tree serves every step.  As paged_decode's: no
  * initialisation, nothing carried over, one per call in flight. */
 int paged_tree_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int num_kv_heads,
                                int head_dim, int kv_dtype, size_t* bytes);

@@ -842,10 +842,13 @@ TreePlan tree_plan(int max_nodes, int G, int D)
     t.tiles = rows > kTile ? 2 : 1;
     t.teams = (rows + t.tiles * kTile - 1) / (t.tiles * kTile);
     t.nctas = t.many ? std::max(1, sms / t.teams) : 0;
-    const size_t many_slots = (size_t)t.teams * t.nctas * 2 * t.tiles * kTile;
+    // (room for a CTA per SM, also where the teams leave some SMs out: what serves
+    // max_nodes nodes then serves fewer too)
+    const size_t many_ctas = t.many ? (size_t)std::max(sms, t.teams) : 0;
+    const size_t many_slots = many_ctas * 2 * t.tiles * kTile;
     t.many_o = take(many_slots * D * sizeof(float));
     t.many_ml = take(many_slots * sizeof(float2));
-    t.many_meta = take((size_t)t.teams * t.nctas * sizeof(int4));
+    t.many_meta = take(many_ctas * sizeof(int4));
     t.total = at;
     return t;
 }

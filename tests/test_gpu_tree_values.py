@@ -120,3 +120,17 @@ def test_infinite_keys_follow_the_formula(pk, ctx, counts, heads, D):
         c.k[c.bt[0, pos // BS], 0, pos % BS, 7] = float("inf")
     ref = reference(c)
     same(c, c.run(pk, torch.float32), ref)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_limits_workspace_serves_every_smaller_call(pk, fp8):
+    dt = pk.FP8_E4M3 if fp8 else pk.BF16
+    for D in (64, 128):
+        for G in (1, 2, 3, 4, 5, 7, 8, 16, 24, 33, 64, 65, 128):
+            sizes = [pk.tree_workspace_bytes(4, n, G, 1, D, dt) for n in range(1, 129)]
+            assert sizes == sorted(sizes), (D, G)
+    ws = pk.alloc_tree_workspace(2, 96, 16, 2, 128, dt)
+    for counts in ([64, 5], [40, 33], [8, 4]):
+        c = Case([300 + counts[0], 2000 + counts[1]], counts, 16, 2, 128, fp8, seed=counts[0])
+        ws.fill_(255)
+        c.check(c.run(pk, torch.float32, ws=ws))
