@@ -528,16 +528,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const u64 sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
                     u64 ls[2] = {0ull, 0ull};
                     float lr[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-                    auto weigh = [&](auto all) {         // all: no key is masked
+                    // all: no key is masked; fused: see kFusedTo
+                    auto weigh = [&](auto all, auto fused) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 float w0, w1;
-                                unpack2(fma2(pack2(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])),
-                                             sl22, nm2),
-                                        w0, w1);
+                                if (decltype(fused)::value) {
+                                    unpack2(fma2(pack2(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])),
+                                                 sl22, nm2),
+                                            w0, w1);
+                                } else {
+                                    w0 = __fadd_rn(__fmul_rn(__uint_as_float(sr[g][2 * e]), sl2), nm);
+                                    w1 = __fadd_rn(__fmul_rn(__uint_as_float(sr[g][2 * e + 1]), sl2), nm);
+                                }
                                 w0 = ex2(w0);
                                 w1 = ex2(w1);
                                 if (!decltype(all)::value) {
@@ -553,8 +559,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                             if (LOW) umma::tmem_st16(tS + (uint32_t)(32 * g + 16), lo);
                         }
                     };
-                    if (masked) weigh(std::false_type());
-                    else weigh(std::true_type());
+                    if (__any_sync(kFull, fabsf(nm) > kFusedTo)) weigh(std::false_type(), std::false_type());
+                    else if (masked) weigh(std::false_type(), std::true_type());
+                    else weigh(std::true_type(), std::true_type());
                     float l0, l1;
                     unpack2(add2(ls[0], ls[1]), l0, l1);
                     l += (l0 + l1) + ((lr[0][0] + lr[0][1]) + (lr[1][0] + lr[1][1]));

@@ -110,8 +110,9 @@ struct SmallGeo {
     static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
     static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
     static constexpr int kQfacOff = kBadOff + 2 * kPrepWarps * 16;   // [2][N] floats (FP8)
-    static constexpr int kSnOff = kQfacOff + 2 * N * 4;      // [group][row] float2: (scale, -reference)
-    static constexpr int kRefOff = kSnOff + 64 * 8;          // [group][row] floats: the reference
+    static constexpr int kScOff = kQfacOff + 2 * N * 4;      // [group][row] floats: the scale
+    static constexpr int kNrOff = kScOff + 64 * 4;           // [group][row] floats: what is added, -reference
+    static constexpr int kRefOff = kNrOff + 64 * 4;          // [group][row] floats: the reference
     static constexpr int kAlphaOff = kRefOff + 64 * 4;       // [group][row] floats
     static constexpr int kWmaxOff = kAlphaOff + 64 * 4;      // [group][4][row] floats: maxima, later sums
     static constexpr int kFacOff = kWmaxOff + 256 * 4;       // [N] float4
@@ -390,7 +391,8 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         // the group's columns of its accumulator; the low parts are N further on
         const uint32_t tO = lanes + G::kColO + (uint32_t)(G::kSplit ? row0 : grp * G::kPW);
-        float2* sn = reinterpret_cast<float2*>(gb + G::kSnOff) + grp * R;
+        float* sc = reinterpret_cast<float*>(gb + G::kScOff) + grp * R;
+        float* nr = reinterpret_cast<float*>(gb + G::kNrOff) + grp * R;
         float* ref = reinterpret_cast<float*>(gb + G::kRefOff) + grp * R;
         float* alphas = reinterpret_cast<float*>(gb + G::kAlphaOff) + grp * R;
         float* wmax = reinterpret_cast<float*>(gb + G::kWmaxOff) + grp * 4 * R;
@@ -428,6 +430,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int k = 0; k < R; ++k) l[k] = 0.f;
             bool first = true, pending = false;  // pending: a row has no reference yet
+            bool wide = false;                   // a row's is above kFusedTo
             for (int c = G::kSplit ? 0 : (g0 ^ grp) & 1; c < nc; c += G::kSplit ? 1 : 2) {
                 const int g = g0 + c;
                 // the scores; and the buffer of P: the products of the chunk before last
@@ -446,7 +449,8 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const int r = row0 + lane, nd = r < rows ? row_node(p, r) : 0;
                         const bool live = r < rows && !((padw[nd >> 5] >> (nd & 31)) & 1u);
                         const float f = FP8 && live ? reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + r] : 1.f;
-                        sn[lane] = live ? make_float2(p.sl2 * f, 0.f) : make_float2(0.f, -INFINITY);
+                        sc[lane] = live ? p.sl2 * f : 0.f;
+                        nr[lane] = live ? 0.f : -INFINITY;
                         ref[lane] = -INFINITY;
                         const bool any = __any_sync(kFull, live);
                         if (lane == 0) *unset = any;
@@ -471,24 +475,48 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                             vis |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - row0);
                     }
                 }
-                // the scores relative to the references, in log2 units
-                float t[R];
-                auto load = [&]() {
-                    umma::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[R]>(&t[0]));
+                // 16 rows' scores as the products left them
+                auto load16 = [&](int k0, float* x) {
+                    uint32_t(&a)[16] = *reinterpret_cast<uint32_t(*)[16]>(x);
+                    umma::tmem_ld16(tS + (uint32_t)k0, a);
                     if (G::kSideBySide) {
-                        float rest[R];
-                        umma::tmem_ld32(tS + (uint32_t)N, *reinterpret_cast<uint32_t(*)[R]>(&rest[0]));
+                        uint32_t b[16];
+                        umma::tmem_ld16(tS + (uint32_t)(N + k0), b);
                         umma::tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < R; ++k) t[k] += rest[k];
+                        for (int k = 0; k < 16; ++k) x[k] += __uint_as_float(b[k]);
                     } else {
                         umma::tmem_wait_ld();
                     }
+                };
+                // the scores relative to the references, in log2 units
+                float t[R];
+                auto load = [&]() {
+                    if (G::kSideBySide) {
+                        load16(0, t);
+                        load16(16, t + 16);
+                    } else {
+                        umma::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[R]>(&t[0]));
+                        umma::tmem_wait_ld();
+                    }
+                    if (!wide) {
 #pragma unroll
-                    for (int k = 0; k < R; k += 2) {
-                        const float4 f = *reinterpret_cast<const float4*>(sn + k);   // two rows
-                        t[k] = fmaf(t[k], f.x, f.y);
-                        t[k + 1] = fmaf(t[k + 1], f.z, f.w);
+                        for (int k = 0; k < R; k += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(sc + k);
+                            const float4 n = *reinterpret_cast<const float4*>(nr + k);
+                            unpack2(fma2(pack2(t[k], t[k + 1]), pack2(f.x, f.y), pack2(n.x, n.y)), t[k], t[k + 1]);
+                            unpack2(fma2(pack2(t[k + 2], t[k + 3]), pack2(f.z, f.w), pack2(n.z, n.w)), t[k + 2], t[k + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < R; k += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(sc + k);
+                            const float4 n = *reinterpret_cast<const float4*>(nr + k);
+                            t[k] = __fadd_rn(__fmul_rn(t[k], f.x), n.x);
+                            t[k + 1] = __fadd_rn(__fmul_rn(t[k + 1], f.y), n.y);
+                            t[k + 2] = __fadd_rn(__fmul_rn(t[k + 2], f.z), n.z);
+                            t[k + 3] = __fadd_rn(__fmul_rn(t[k + 3], f.w), n.w);
+                        }
                     }
                     if (masked) {
 #pragma unroll
@@ -508,33 +536,36 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     // ---- new references: the largest score of each row in the chunk
                     int best = INT32_MIN;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < R; k0 += 16) {
+                        float x[16];
+                        load16(k0, x);
 #pragma unroll
-                    for (int k = 0; k < R; ++k) {
-                        // (relative to the old reference, or to none)
-                        const int m = __reduce_max_sync(kFull, ordered(t[k]));
-                        if (lane == k) best = m;
+                        for (int k = 0; k < 16; ++k) {
+                            x[k] = (vis >> (k0 + k)) & 1u ? __fmul_rn(x[k], sc[k0 + k]) : -INFINITY;
+                            const int m = __reduce_max_sync(kFull, ordered(x[k]));
+                            if (lane == k0 + k) best = m;
+                        }
                     }
                     wmax[wq * R + lane] = unordered(best);
                     meet(false);
                     if (wq == 0) {
-                        const float rel = max_nan(max_nan(wmax[lane], wmax[R + lane]),
-                                                  max_nan(wmax[2 * R + lane], wmax[3 * R + lane]));
-                        const float2 f = sn[lane];
+                        float top = max_nan(max_nan(wmax[lane], wmax[R + lane]),
+                                            max_nan(wmax[2 * R + lane], wmax[3 * R + lane]));
                         const float old = ref[lane];
-                        const bool live = f.y != -INFINITY;
-                        // rel = score * scale + f.y, with f.y = bias - reference, or 0 for none;
+                        const bool live = nr[lane] != -INFINITY;
                         // a row whose first scores hold NaN is NaN whatever its reference: 0
-                        float top = old == -INFINITY ? rel : rel - f.y;
                         if (old == -INFINITY && top != top) top = 0.f;
                         float a = 1.f;
                         if (live && (old == -INFINITY ? top > -INFINITY : top > old + kMaxLag)) {
                             a = old == -INFINITY ? 0.f : ex2(old - top);
                             ref[lane] = top;
-                            sn[lane].y = (FP8 ? kBiasF16 : 0.f) - top;
+                            nr[lane] = (FP8 ? kBiasF16 : 0.f) - top;
                         }
                         alphas[lane] = a;
                         const bool left = __any_sync(kFull, live && ref[lane] == -INFINITY);
-                        if (lane == 0) *unset = left;
+                        const bool far = __any_sync(kFull, live && ref[lane] != -INFINITY && fabsf(ref[lane]) > kFusedTo);
+                        if (lane == 0) *unset = (left ? 1 : 0) + (far ? 2 : 0);
                     }
                     if (!first) {
                         // what has been accumulated follows, once the products under way
@@ -546,7 +577,8 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         ok = false;
                         break;
                     }
-                    pending = *unset != 0;
+                    pending = (*unset & 1) != 0;
+                    wide = (*unset & 2) != 0;
                     if (!first) {
 #pragma unroll
                         for (int k = 0; k < R; ++k) l[k] *= alphas[k];

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import tree_reference as R
 from test_gpu_tree import BS, Case
 
 pytestmark = pytest.mark.gpu
@@ -134,3 +135,80 @@ def test_a_limits_workspace_serves_every_smaller_call(pk, fp8):
         c = Case([300 + counts[0], 2000 + counts[1]], counts, 16, 2, 128, fp8, seed=counts[0])
         ws.fill_(255)
         c.check(c.run(pk, torch.float32, ws=ws))
+
+
+def scored(c):
+    """The formula's outputs, sum_j w_j |V_j| beside them, and of each row the scores of
+    all keys it sees, their values, and the largest |q_d k_d| times the scale."""
+    k, v = c.values()
+    q = c.q.double().numpy()
+    out, mean = np.zeros_like(q), np.zeros_like(q)
+    scores, top = {}, np.zeros(q.shape[:2])
+    G = c.Hq // c.Hkv
+    for s in range(len(c.lens)):
+        t0, n, L = int(c.starts[s]), int(c.counts[s]), int(c.lens[s])
+        pages = c.bt[s, :-(-L // BS)]
+        K, V = (x[pages].transpose(1, 0, 2, 3).reshape(c.Hkv, -1, c.D)[:, :L] for x in (k, v))
+        for i, seen in enumerate(R.ancestors(c.parents[t0:t0 + n])):
+            idx = np.concatenate([np.arange(L - n), L - n + np.array(sorted(seen), dtype=int)])
+            for h in range(c.Hq):
+                x = K[h // G, idx] @ q[t0 + i, h] * c.scale
+                w = np.exp(x - x.max())
+                out[t0 + i, h] = w @ V[h // G, idx] / w.sum()
+                mean[t0 + i, h] = w @ np.abs(V[h // G, idx]) / w.sum()
+                scores[t0 + i, h] = x, V[h // G, idx]
+                top[t0 + i, h] = np.abs(K[h // G, idx] * q[t0 + i, h]).max() * abs(c.scale)
+    return out, mean, scores, top
+
+
+def check_magnitudes(c, got, weight, score, element):
+    """Outputs of scores that are off by d at most, d = score * the largest product + element
+    * the sum of a row's element errors, and of weights that are off by `weight` of theirs:
+    by at most (weight + 2 (e^d - 1)) sum_j w_j |V_j|; where d is large, but the largest score
+    so far above the others that its weight is 1, that key's value."""
+    ref, mean, scores, top = scored(c)
+    assert np.isfinite(got).all()
+    q = c.q.double().numpy()
+    close = sharp = 0
+    for (t, h), (x, V) in scores.items():
+        d = score * top[t, h] + element * np.abs(q[t, h]).max()
+        two = np.sort(x)[-2:] if len(x) > 1 else np.array([-np.inf, x[0]])
+        if d < 0.05:
+            bound = (weight + 2 * np.expm1(d)) * mean[t, h] + 2.0 ** -22
+            close += 1
+        elif two[1] - two[0] > 2 * d + 30:       # the other weights together: len(x) e^-30
+            bound = weight * mean[t, h] + len(x) * np.exp(-30) * np.abs(V).max()
+            sharp += 1
+        else:
+            continue
+        assert (np.abs(got[t, h] - ref[t, h]) <= bound).all(), (t, h, d)
+    assert close + sharp > 0.95 * len(scores) and sharp > 0
+
+
+def magnitudes(counts, heads, D, fp8):
+    """Query rows of normal values times a power of two of their own, from the subnormals to
+    the largest, one row whose elements each have their own, and one with the largest."""
+    c = Case([300, 900 + counts[1]], counts, *heads, D, fp8, seed=3)
+    if fp8:
+        c.ks *= 2.0 ** -20
+    else:
+        c.k = (c.k.float() * 2.0 ** -20).to(torch.bfloat16)
+    rng = np.random.default_rng(7)
+    q = c.q.double().numpy()
+    q *= np.exp2(rng.choice([0, 17, 20, 23, 26, 40, 100, 124, -20, -130], size=q.shape[:2]))[..., None]
+    q[0, 1] = np.exp2(rng.integers(-130, 124, size=D)) * np.sign(q[0, 1])
+    q[1, 1, 5] = 3e38
+    c.q = torch.from_numpy(q).to(torch.bfloat16)
+    assert torch.isfinite(c.q.float()).all()
+    return c
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,heads", ROWS)
+def test_query_magnitudes_over_the_whole_bf16_range(pk, counts, heads, D):
+    """Scores up to 10^32.  A float32 sum of D products is off by at most D 2^-24 times D of
+    the largest; its roundings are independent, so a sixteenth of that is ample.  Weights:
+    two bf16 parts, 2^-16."""
+    c = magnitudes(counts, heads, D, False)
+    got = c.run(pk, torch.float32).double().cpu().numpy()
+    check_magnitudes(c, got, 2.0 ** -16, D * D * 2.0 ** -28, 0.0)
