@@ -577,11 +577,14 @@ int paged_tree_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int
  * of i.  A node that sees no position (a padding node, context_lens[s] == 0)
  * gets zeros; what is stored at positions a node does not see, infinities and
  * NaN among it, does not reach its output.  One node per sequence, a root,
- * gives paged_decode_attention's result up to summation order.
+ * gives paged_decode_attention's result up to the rounding stated here.
  * Supported: head_dim 64 or 128, any num_q_heads that is a multiple of
  * num_kv_heads with G = num_q_heads / num_kv_heads <= 128.  Deterministic as
- * paged_decode_attention.  Scores and the softmax's (max, sum) are float32;
- * weights are multiplied as two bf16 parts (16 bits; E4M3 caches: f16), but as
+ * paged_decode_attention.  Scores and the softmax's (max, sum) are float32.  Over
+ * E4M3 caches a query element is used exactly down to 2^-24 of the largest of its
+ * row (one node and head), and within 2^-31 of that largest below; the products'
+ * sums are the 8-bit matrix instructions', within 3 * 2^-20 of the largest product.
+ * Weights are multiplied as two bf16 parts (16 bits; E4M3 caches: f16), but as
  * one bf16 (8 bits, the sum being that of the rounded weights) for a bf16
  * output of a tree with more than 64 rows (n_s * G) over a bf16 cache.
  * Errors as paged_decode_attention; KV_ERR_INVALID_ARG also for max_nodes < 1 or

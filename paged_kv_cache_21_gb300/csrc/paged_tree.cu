@@ -105,14 +105,16 @@ struct Geo {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kBoxes = D / 64;                    // 128-byte column groups of a row
     static constexpr int kSlot = kBoxes * kRegion;           // K or V of a chunk, 2 bytes each
-    static constexpr int kQTile = kBoxes * kTile * 128;
+    static constexpr int kQTile = FP8 ? kQueryParts * kTile * D : kBoxes * kTile * 128;
+    static constexpr int kWords = kN / 32;                   // words of a node's bits
     static constexpr int kPageBytes = kBlock * D * (FP8 ? 1 : 2);
     static constexpr int kRawSlot = kPages * kBlock * D;     // E4M3 codes of K or V of a chunk
     static constexpr int kScale = 128 / D;
     // the two streams take the chunks in turn, or both take each
     static constexpr int kChunkStep = TILES == 1 ? 2 : 1;
-    static constexpr int kKSlots = (FP8 ? 3 : 2) * kScale, kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
-    static constexpr int kRawV = !FP8 ? 0 : 2 * kScale;
+    static constexpr int kKSlots = (FP8 && TILES == 1 ? 3 : 2) * kScale;
+    static constexpr int kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
+    static constexpr int kRawV = !FP8 ? 0 : (TILES == 1 ? 2 : 1) * kScale;
     static constexpr int kLoadBytes = FP8 ? kRawSlot : kSlot;
     static constexpr int kQOff = 0;
     static constexpr int kKOff = kQOff + TILES * kQTile;
@@ -278,15 +280,15 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const uint64_t qd = qdesc + (uint64_t)((TILES == 2 ? st * G::kQTile : 0) >> 4);
                     const uint64_t kd = sdesc + (uint64_t)((KR::slot(g) * G::kLoadBytes) >> 4);
                     const uint32_t keys16 = (uint32_t)(kBlock * w.chunk_pages(c));
-                    const uint32_t idesc = FP8 ? umma::idesc_f16_f32(kTile, keys16, false, false)
+                    const uint32_t idesc = FP8 ? umma::idesc_f8_f32(kTile, keys16, true, false)
                                                : umma::idesc_bf16_f32(kTile, keys16, false, false);
                     if constexpr (FP8) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                        for (int part = 0; part < kQueryParts; ++part)
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
-                                umma::mma_e4m3_ss(tS, qd + (uint64_t)((part * kTile * D + kk * 32) >> 4),
-                                                  kd + (uint64_t)((kk * 32) >> 4), idesc, part + kk > 0);
+                                umma::mma_f8_ss(tS, qd + (uint64_t)((part * kTile * D + kk * 32) >> 4),
+                                                kd + (uint64_t)((kk * 32) >> 4), idesc, part + kk > 0);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
@@ -394,12 +396,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if (r < rows) cp_async16(dst, src);
                 } else {
                     float up;
-                    uint2 first, second;
-                    query_e4m3<D>(__ldg(reinterpret_cast<const uint4*>(src)), first, second, up);
+                    uint2 parts[kQueryParts];
+                    query_e5m2<D>(__ldg(reinterpret_cast<const uint4*>(src)), parts, up);
                     if (r < rows) {
                         const uint32_t at = sb + (uint32_t)(G::kQOff + (rc >> 7) * G::kQTile) + code_off<D>(rc & 127, c);
-                        sts64(at, first);
-                        sts64(at + (uint32_t)(kTile * D), second);
+#pragma unroll
+                        for (int part = 0; part < kQueryParts; ++part) sts64(at + (uint32_t)(part * kTile * D), parts[part]);
                         if (c == 0)
                             reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * TILES * kTile + r] = up;
                     }
@@ -645,7 +647,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                     if (l == 0.f) {
-                        const bool lost = whole && in && !pad && sees_any(w.q, am);
+                        const bool lost = whole && in && !pad && sees_any<G::kWords>(w.q, am);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) v[k] = lost ? __uint_as_float(0x7fffffffu) : 0.f;
                     }

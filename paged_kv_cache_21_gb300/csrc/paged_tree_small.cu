@@ -67,7 +67,7 @@ struct SmallGeo {
     static constexpr int kAccs = kSplit ? 1 : 2;             // accumulators
     static constexpr int kPW = kLow ? 2 * N : N;
     static constexpr int kPBuf = kPW / 64 * kRegion;         // [column group of 64][128 keys][128 B]
-    static constexpr int kQBytes = FP8 ? 2 * N * D : kBoxes * N * 128;   // (FP8: two parts)
+    static constexpr int kQBytes = FP8 ? kQueryParts * N * D : kBoxes * N * 128;
     static constexpr int kScale = 128 / D;
     static constexpr int kKSlots = (FP8 ? 4 : 2) * kScale, kVSlots = (FP8 || N == 64 ? 2 : 3) * kScale;
     static constexpr int kRawV = !FP8 ? 0 : (N == 32 ? 3 : 2) * kScale;
@@ -105,9 +105,10 @@ struct SmallGeo {
     static constexpr int B_STALL = B_END + 2;                // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kAncOff = kMiscOff + 64;            // [2][kN][4] words
-    static constexpr int kPtrOff = kAncOff + 2 * kN * 16;    // [kN] words
-    static constexpr int kPadOff = kPtrOff + kN * 4;         // [2][4] words
+    static constexpr int kWords = N / 32;                    // words of a node's bits (a node has a row)
+    static constexpr int kAncOff = kMiscOff + 64;            // [2][N][kWords] words
+    static constexpr int kPtrOff = kAncOff + 2 * N * kWords * 4;     // [N] words
+    static constexpr int kPadOff = kPtrOff + N * 4;          // [2][4] words
     static constexpr int kBadOff = kPadOff + 32;             // [2][kPrepWarps][4] words
     static constexpr int kQfacOff = kBadOff + 2 * kPrepWarps * 16;   // [2][N] floats (FP8)
     static constexpr int kScOff = kQfacOff + 2 * N * 4;      // [group][row] floats: the scale
@@ -121,12 +122,12 @@ struct SmallGeo {
     static constexpr int kEnd = kUnsetOff + 16;
     static constexpr int kSmem = kEnd + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
-    // E4M3: the query's two parts are 2 N columns of one product, added by the groups
-    // (8 nodes x 4 heads of 32 x 8192 tokens: 134 -> 126 us), or, where the groups have
-    // no time left (64 rows: 151 -> 159 us), two products into the same columns.
+    // E4M3: the query's parts are 3 N columns of one product, added by the groups
+    // (two parts, 8 nodes x 4 heads of 32 x 8192 tokens: 134 -> 126 us), or, where the
+    // groups have no time left (64 rows: 151 -> 159 us), products into the same columns.
     static constexpr bool kSideBySide = FP8 && !kSplit;
     // tensor memory: four S^T buffers, then the accumulators
-    static constexpr int kScoreCols = kSideBySide ? 2 * N : N;
+    static constexpr int kScoreCols = kSideBySide ? kQueryParts * N : N;
     static constexpr uint32_t kColO = 4 * kScoreCols;
     static constexpr uint32_t kTmemCols = kColO + kAccs * kPW <= 256 ? 256 : 512;
     static_assert(kColO + kAccs * kPW <= 512, "tensor memory");
@@ -236,7 +237,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (lane == 0) {
             const uint64_t qdesc = FP8 ? code_desc<D>(sb + G::kQOff) : umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
             const uint64_t kdesc = FP8 ? code_desc<D>(sb + G::kKOff) : umma::smem_desc_sw128(sb + G::kKOff, 16, 1024);
-            constexpr uint32_t idesc_s = FP8 ? umma::idesc_f16_f32(128, G::kScoreCols, false, false)
+            constexpr uint32_t idesc_s = FP8 ? umma::idesc_f8_f32(128, G::kScoreCols, false, true)
                                              : umma::idesc_bf16_f32(128, N, false, false);
             using KR = typename G::KRing;
             int g = 0;                           // chunk of the CTA
@@ -260,12 +261,12 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const uint32_t d = tmem + (uint32_t)(G::kScoreCols * (g & 3));
                     if constexpr (FP8) {
 #pragma unroll
-                        for (int part = 0; part < (G::kSideBySide ? 1 : 2); ++part)
+                        for (int part = 0; part < (G::kSideBySide ? 1 : kQueryParts); ++part)
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
-                                umma::mma_e4m3_ss(d, kd + (uint64_t)((kk * 32) >> 4),
-                                                  qdesc + (uint64_t)((part * N * D + kk * 32) >> 4), idesc_s,
-                                                  part + kk > 0);
+                                umma::mma_f8_ss(d, kd + (uint64_t)((kk * 32) >> 4),
+                                                qdesc + (uint64_t)((part * N * D + kk * 32) >> 4), idesc_s,
+                                                part + kk > 0);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
@@ -361,12 +362,12 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if (r < rows) cp_async16(dst, src);
                 } else {
                     float up;
-                    uint2 first, second;
-                    query_e4m3<D>(__ldg(reinterpret_cast<const uint4*>(src)), first, second, up);
+                    uint2 parts[kQueryParts];
+                    query_e5m2<D>(__ldg(reinterpret_cast<const uint4*>(src)), parts, up);
                     if (r < rows) {
                         const uint32_t at = sb + (uint32_t)G::kQOff + code_off<D>(rc, c);
-                        sts64(at, first);
-                        sts64(at + (uint32_t)(N * D), second);
+#pragma unroll
+                        for (int part = 0; part < kQueryParts; ++part) sts64(at + (uint32_t)(part * N * D), parts[part]);
                         if (c == 0) reinterpret_cast<volatile float*>(gb + G::kQfacOff)[buf * N + r] = up;
                     }
                 }
@@ -423,7 +424,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (Walk w(p, misc, 0); ok && w.more(); w.next(p, 0)) {
             const int seg = w.seg, buf = seg & 1, nc = w.chunks();
             const int rows = w.q.n * p.G;
-            const uint32_t* anc = reinterpret_cast<const uint32_t*>(gb + G::kAncOff) + buf * kN * 4;
+            const uint32_t* anc = reinterpret_cast<const uint32_t*>(gb + G::kAncOff) + buf * N * G::kWords;
             const volatile uint32_t* padw = reinterpret_cast<const volatile uint32_t*>(gb + G::kPadOff) + buf * 4;
             const int plain = w.plain_chunks();
             float l[R];                          // each row's sum over this thread's keys
@@ -472,7 +473,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const int a = pos - w.q.base;
                         vis = 0u;
                         for (int r = row0; r < min(rows, row0 + R); ++r)
-                            vis |= ((anc[row_node(p, r) * 4 + (a >> 5)] >> (a & 31)) & 1u) << (r - row0);
+                            vis |= ((anc[row_node(p, r) * G::kWords + (a >> 5)] >> (a & 31)) & 1u) << (r - row0);
                     }
                 }
                 // 16 rows' scores as the products left them
@@ -480,11 +481,12 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                     uint32_t(&a)[16] = *reinterpret_cast<uint32_t(*)[16]>(x);
                     umma::tmem_ld16(tS + (uint32_t)k0, a);
                     if (G::kSideBySide) {
-                        uint32_t b[16];
+                        uint32_t b[16], c[16];
                         umma::tmem_ld16(tS + (uint32_t)(N + k0), b);
+                        umma::tmem_ld16(tS + (uint32_t)(2 * N + k0), c);
                         umma::tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] += __uint_as_float(b[k]);
+                        for (int k = 0; k < 16; ++k) x[k] += __uint_as_float(b[k]) + __uint_as_float(c[k]);
                     } else {
                         umma::tmem_wait_ld();
                     }
@@ -679,7 +681,7 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float L = s[0] * a0 + s[1] * a1;
                 float z = 1.f;
                 if (whole && L != 0.f) z = p.v_scale / L;
-                else if (whole) z = live && sees_any(w.q, anc + nd * 4) ? __uint_as_float(0x7fffffffu) : 0.f;
+                else if (whole) z = live && sees_any<G::kWords>(w.q, anc + nd * G::kWords) ? __uint_as_float(0x7fffffffu) : 0.f;
                 fac[tid] = make_float4(a0, a1, z, L);
                 rowat[tid] = whole ? (w.q.t0 + nd) * p.Hq + w.h * p.G + tid - nd * p.G : (int)(slot * N) + tid;
                 if (!whole && tid < rows) p.part_ml[slot * N + tid] = make_float2(M, L);
@@ -720,10 +722,10 @@ paged_tree_small_kernel(const __grid_constant__ CUtensorMap tm_k,
                         for (int k = 0; k < 16; ++k) {
                             const int nd = row_node(p, r0 + k);
                             if (r0 + k >= rows || ((padw[nd >> 5] >> (nd & 31)) & 1u)) continue;
-                            for (int k4 = 0; k4 < 4; ++k4) {
+                            for (int k4 = 0; k4 < G::kWords; ++k4) {
                                 uint32_t b = 0u;
                                 for (int q = 0; q < G::kPrepWarps; ++q) b |= badw[q * 4 + k4];
-                                for (b &= anc[nd * 4 + k4]; b != 0u; b &= b - 1u) {
+                                for (b &= anc[nd * G::kWords + k4]; b != 0u; b &= b - 1u) {
                                     const int pos = w.q.base + 32 * k4 + __ffs(b) - 1;
                                     const int blk = __ldg(p.bt + (size_t)w.s * p.max_blocks + pos / kBlock);
                                     if (blk < 0 || blk >= p.num_blocks) continue;

@@ -7,7 +7,7 @@
 // 1024-byte aligned base) and its barriers (B_..); both kernels consume K and V
 // in chunks of up to 8 pages, chunk g of a CTA from slot g % slots of a ring of K
 // and of one of V.  E4M3: the codes of K are multiplied as they are, with the
-// query in two E4M3 parts; V is widened from a ring of codes to one of f16.
+// query in three E5M2 parts; V is widened from a ring of codes to one of f16.
 #pragma once
 
 #include <cuda.h>
@@ -157,10 +157,11 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int s, int firs
 // Does a node that is not padding see any position?  `am`: the nodes it sees, as bits.
 // (A row that does, and whose weights sum to nothing, had scores of -inf alone: its
 // softmax is NaN.)
+template <int WORDS>
 __device__ __forceinline__ bool sees_any(const SeqInfo& q, const uint32_t* am)
 {
     bool any = q.base > 0;
-    for (int k = 0; k < kN / 32; ++k) {
+    for (int k = 0; k < WORDS; ++k) {
         const int lim = q.L - 32 * k;            // (nodes there is no room for are not cached)
         if (lim > 0) any = any || (lim < 32 ? am[k] & ((1u << lim) - 1u) : am[k]) != 0u;
     }
@@ -427,15 +428,16 @@ __device__ __forceinline__ void copy_role(const TreeParams& p, const CUtensorMap
 template <class G>
 __device__ __forceinline__ void tree_masks(const TreeParams& p, const Walk& w, uint8_t* gb, int lane)
 {
+    constexpr int W = G::kWords;             // words of bits: a tree here has at most 32 W nodes
     const int buf = w.seg & 1, n = w.q.n;
     uint32_t* anc = reinterpret_cast<uint32_t*>(gb + G::kAncOff);
     volatile uint32_t* padw = reinterpret_cast<volatile uint32_t*>(gb + G::kPadOff);
     volatile int* ptr = reinterpret_cast<volatile int*>(gb + G::kPtrOff);
-    volatile uint32_t* am = anc + buf * kN * 4;
-    int up[kN / 32];
-    uint32_t m[kN / 32][4];
+    volatile uint32_t* am = anc + buf * 32 * W * W;
+    int up[W];
+    uint32_t m[W][W];
 #pragma unroll
-    for (int k = 0; k < kN / 32; ++k) {
+    for (int k = 0; k < W; ++k) {
         const int i = 32 * k + lane;
         int par = -1;
         if (i < n)
@@ -446,34 +448,34 @@ __device__ __forceinline__ void tree_masks(const TreeParams& p, const Walk& w, u
         if (lane == 0) padw[buf * 4 + k] = pads;
         up[k] = i < n && !pad ? par : -1;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
+        for (int v = 0; v < W; ++v)
             m[k][v] = v == k && i < n && !pad ? 1u << lane : 0u;
     }
     for (int reach = 1; reach < n; reach *= 2) {
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kN / 32; ++k) {
+        for (int k = 0; k < W; ++k) {
             const int i = 32 * k + lane;
             ptr[i] = up[k];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) am[4 * i + v] = m[k][v];
+            for (int v = 0; v < W; ++v) am[W * i + v] = m[k][v];
         }
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kN / 32; ++k) {
+        for (int k = 0; k < W; ++k) {
             if (up[k] >= 0) {
                 const int a = up[k];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) m[k][v] |= am[4 * a + v];
+                for (int v = 0; v < W; ++v) m[k][v] |= am[W * a + v];
                 up[k] = ptr[a];
             }
         }
     }
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kN / 32; ++k)
+    for (int k = 0; k < W; ++k)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) am[4 * (32 * k + lane) + v] = m[k][v];
+        for (int v = 0; v < W; ++v) am[W * (32 * k + lane) + v] = m[k][v];
 }
 
 // Zero the V rows behind the context, and the infinities and NaN of the drafted
@@ -600,14 +602,30 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
     return true;
 }
 
-// A query row's 8 elements (16 bytes of bf16) as two E4M3 parts, for E4M3 keys:
+// Four E5M2 codes as four f16, of which they are the upper bytes.
+__device__ __forceinline__ void e5m2x4_to_f16x4(uint32_t x, __half2& lo, __half2& hi)
+{
+    const uint32_t l = __byte_perm(x, 0u, 0x1404), h = __byte_perm(x, 0u, 0x3424);
+    lo = *reinterpret_cast<const __half2*>(&l);
+    hi = *reinterpret_cast<const __half2*>(&h);
+}
+
+// A query row's 8 elements (16 bytes of bf16) as three E5M2 parts, for E4M3 keys:
 // the row is scaled by a power of two that brings its largest |element| into
-// [2^7, 2^8); the first part holds an element's leading four bits, the second what
-// is left, which bf16's eight bits leave exact down to 2^-14 of the largest, and
-// within 2^-17 of it below.  The scores are multiplied by `up` again.  A row with
-// infinities or NaN has up = NaN.  The row's D / 8 lanes call together.
+// [2^14, 2^15); each part is what the ones before leave, rounded to E5M2's three
+// bits.  Three parts hold bf16's eight bits exactly, down to 2^-24 of the row's
+// largest element (2^-9 here); below, where parts fall between E5M2's steps of
+// 2^-16, an element is off by at most 2^-17, 2^-31 of the largest.  (Two parts of
+// E4M3, four bits each but steps of 2^-9, were exact down to 2^-10 of the largest
+// only: an outlier cost the other elements theirs.  The third part takes
+// 8 nodes x 4 heads of 32 x 8192 tokens from 117 to 121 us, 16 nodes from 153 to 160, 64
+// from 388 to 437, half of that for the room it takes from the rings.)  The scores are
+// multiplied by `up` again.  A row with infinities or NaN has up = NaN.  The row's
+// D / 8 lanes call together.
+constexpr int kQueryParts = 3;
+
 template <int D>
-__device__ __forceinline__ void query_e4m3(uint4 v, uint2& first, uint2& second, float& up)
+__device__ __forceinline__ void query_e5m2(uint4 v, uint2 (&parts)[kQueryParts], float& up)
 {
     const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
     uint32_t big = 0;
@@ -615,35 +633,35 @@ __device__ __forceinline__ void query_e4m3(uint4 v, uint2& first, uint2& second,
     for (int k = 0; k < 4; ++k) big = max(big, max(q4[k] & 0x7fffu, (q4[k] >> 16) & 0x7fffu));
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kFull, big, o));
-    // (rows below 2^-93 keep their smaller elements)
-    const int e = big == 0 ? 0 : max((int)(big >> 7) - (127 + 7), -100);
+    // (both powers are normal floats; the smallest bf16 is 2^-7 at 2^126 times its value)
+    const int e = big == 0 ? 0 : max((int)(big >> 7) - (127 + 14), -126);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
     up = big >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 + e) << 23);
-    uint32_t a[2], b[2];
+    uint32_t codes[2][kQueryParts];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float x[4];
-        uint32_t codes = 0, rest = 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             x[2 * k] = bf16_lo(q4[2 * h + k]) * down;
             x[2 * k + 1] = bf16_hi(q4[2 * h + k]) * down;
-            codes |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * k], x[2 * k + 1]), __NV_SATFINITE, __NV_E4M3)
-                     << (16 * k);
         }
-        uint32_t lo, hi;
-        e4m3x4_to_f16x4(codes, lo, hi);
-        const __half2 h0 = *reinterpret_cast<const __half2*>(&lo), h1 = *reinterpret_cast<const __half2*>(&hi);
-        rest = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0] - __low2float(h0), x[1] - __high2float(h0)),
-                                                  __NV_SATFINITE, __NV_E4M3);
-        rest |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2] - __low2float(h1), x[3] - __high2float(h1)),
-                                                   __NV_SATFINITE, __NV_E4M3)
-                << 16;
-        a[h] = codes;
-        b[h] = rest;
+#pragma unroll
+        for (int part = 0; part < kQueryParts; ++part) {
+            const uint32_t c =
+                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E5M2) |
+                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E5M2) << 16;
+            __half2 lo, hi;
+            e5m2x4_to_f16x4(c, lo, hi);
+            x[0] -= __low2float(lo);
+            x[1] -= __high2float(lo);
+            x[2] -= __low2float(hi);
+            x[3] -= __high2float(hi);
+            codes[h][part] = c;
+        }
     }
-    first = make_uint2(a[0], a[1]);
-    second = make_uint2(b[0], b[1]);
+#pragma unroll
+    for (int part = 0; part < kQueryParts; ++part) parts[part] = make_uint2(codes[0][part], codes[1][part]);
 }
 
 // Byte offset of byte 8 c of row r of a tile of D-byte rows, with the swizzle that

@@ -169,10 +169,16 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
-// The same with 8-bit operands of kind::f8f6f4 (K = 32); E4M3 is type 0, so an
-// instruction descriptor is idesc_f16_f32's.  f32 sums, measured within 2^-20 of
+// The same with K-major 8-bit operands of kind::f8f6f4, E4M3 (type 0) or E5M2 (1).
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_e5m2, bool b_e5m2)
+{
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The product of 8-bit operands (K = 32).  f32 sums, measured within 2^-20 of
 // the largest product over 128.
-__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                             uint32_t idesc, bool accumulate)
 {
     asm volatile(

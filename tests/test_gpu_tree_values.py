@@ -212,3 +212,52 @@ def test_query_magnitudes_over_the_whole_bf16_range(pk, counts, heads, D):
     c = magnitudes(counts, heads, D, False)
     got = c.run(pk, torch.float32).double().cpu().numpy()
     check_magnitudes(c, got, 2.0 ** -16, D * D * 2.0 ** -28, 0.0)
+
+
+# A score over an E4M3 cache: a query element is exact down to 2^-24 of its row's largest and
+# off by at most 2^-31 of that below; the sums of the products of its three parts are within
+# 3 2^-20 of the largest product.  A weight is rounded to f16, half a step is 2^-11, and the
+# sum is that of the weights before.
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,heads", ROWS)
+def test_query_magnitudes_over_the_whole_bf16_range_e4m3(pk, counts, heads, D):
+    c = magnitudes(counts, heads, D, True)
+    got = c.run(pk, torch.float32).double().cpu().numpy()
+    check_magnitudes(c, got, 2.0 ** -11, 3 * 2.0 ** -20, D * 2.0 ** -31 * 448 * c.ks * c.scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,heads", ROWS)
+@pytest.mark.parametrize("big", [2.0 ** 9, 2.0 ** 11, 2.0 ** 13, 2.0 ** 16])
+def test_a_large_query_element_over_zero_codes_costs_the_others_nothing(pk, big, counts, heads, D):
+    """The others' products are at most 4.5 * 4.93 / 4, so that their sums are off by less than
+    2^-15; elements below 2^-24 of 2^16 are off by 2^-15, times 4.93 / 4: if all 128 were, by
+    0.005, and for the few that there are by less than 2^-13.  With the weights' 2^-11 and
+    twice the scores' that stays below 2^-10."""
+    c = Case([300, 40 + counts[1]], counts, *heads, D, True, seed=int(big) % 97)
+    c.k[..., 5] = 0
+    c.q[:, :, 5] = big
+    c.scale *= 8
+    ref, mean, _, _ = scored(c)
+    got = c.run(pk, torch.float32).double().cpu().numpy()
+    assert (np.abs(got - ref) <= 2.0 ** -10 * mean).all()
+
+
+def test_one_root_over_e4m3_is_a_decode_step_for_uneven_queries(pk):
+    """Both round weights to f16 and sum products in float32 (3 2^-20, and 2^-20 ample for
+    the other), so that they differ by at most the sum of their errors."""
+    for heads, D in (((32, 8), 128), ((8, 8), 64), ((64, 1), 128)):
+        c = Case([300, 17, 1, 2000], [1, 1, 1, 1], *heads, D, True, seed=11)
+        c.q[:, 0] *= 2.0 ** 14
+        c.q[:, 1, 3] = 2.0 ** 12
+        c.q[:, 2, ::2] *= 2.0 ** -12
+        c.k[..., 3] = 0
+        t = c.device()
+        got = c.run(pk, torch.float32, t)
+        ref = torch.empty_like(got)
+        pk.paged_decode_attention(ref, t["q"], t["kc"], t["vc"], t["bt"], t["lens"], c.scale,
+                                  pk.alloc_workspace(4, *heads, D, pk.FP8_E4M3), c.ks, c.vs)
+        _, mean, _, top = scored(c)
+        bound = (2 * 2.0 ** -11 + 2 * np.expm1(4 * 2.0 ** -20 * top))[..., None] * mean + 2.0 ** -22
+        assert (np.abs((got - ref).double().cpu().numpy()) <= bound).all()
