@@ -659,7 +659,8 @@ int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32_t* out_tok
  *                  leaves it); accept_lens: [num_seqs] int32
  * A path that breaks this raises KV_DEVERR_BAD_TREE and its sequence's moves
  * are left out; a move from or to a block id outside [0, num_blocks) raises
- * KV_DEVERR_BLOCK_OUT_OF_RANGE and is left out.  The blocks that hold the nodes
+ * KV_DEVERR_BLOCK_OUT_OF_RANGE and is left out.  A sequence without a context
+ * (context_lens[s] == 0) moves nothing, whatever its path.  The blocks that hold the nodes
  * must be private to their sequence (kv_tree_step's are).  Nothing else in the
  * caches changes.  One launch for up to 128 layers. */
 int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers,

@@ -59,8 +59,10 @@ __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
         const int L = __ldg(p.ctx + s);
         int m = __ldg(p.lens + s);
         const long long base = (long long)L - n;
+        // (nothing is cached of a sequence without a context: a padded batch's idle row)
+        if (L == 0) m = 0;
         // a path that is not strictly increasing within the tree moves nothing
-        bool ok = span_ok && m >= 0 && m <= n && (base >= 0 || n == 0);
+        bool ok = span_ok && m >= 0 && m <= n && (base >= 0 || n == 0 || L == 0);
         if (!ok) m = 0;
         int node[KV_TREE_MAX_NODES / 32];
 #pragma unroll

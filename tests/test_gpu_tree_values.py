@@ -261,3 +261,28 @@ def test_one_root_over_e4m3_is_a_decode_step_for_uneven_queries(pk):
         _, mean, _, top = scored(c)
         bound = (2 * 2.0 ** -11 + 2 * np.expm1(4 * 2.0 ** -20 * top))[..., None] * mean + 2.0 ** -22
         assert (np.abs((got - ref).double().cpu().numpy()) <= bound).all()
+
+
+def test_an_inactive_row_of_a_padded_batch_goes_through_a_step_without_a_flag(pk):
+    """Nodes, but no context: zeros from attention, a walk from verification, nothing moved."""
+    c = Case([20, 30, 30], [4, 4, 4], 4, 2, 64, seed=1)
+    c.lens[2] = 0
+    c.check(c.run(pk, torch.float32))
+    t = c.device()
+    g = torch.Generator().manual_seed(0)
+    prob = torch.softmax(torch.randn((12, 50), generator=g), 1).cuda()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    al, an, ot = i32(3), i32(3, 4), i32(3, 4)
+    u = torch.zeros(12, device="cuda")              # every first child is accepted
+    pk.kv_tree_verify(al, an, ot, prob, i32(12), t["parents"], t["starts"], u, u[:3])
+    assert al[2] >= 1
+    was = [t["kc"].clone(), t["vc"].clone()]
+    an[0, :2], al[0] = torch.tensor([0, 3], dtype=torch.int32), 2
+    an[1], al[1] = torch.tensor([0, 1, 2, 3], dtype=torch.int32), 4
+    pk.kv_tree_compact(pk.CacheLayers([t["kc"]], [t["vc"]]), t["bt"], t["lens"], t["starts"], an, al)
+    torch.cuda.synchronize()
+    assert pk.get_device_error()[0] == 0
+    bits = lambda x: x.view(torch.int16).cpu().numpy()  # noqa: E731
+    k, v = R.compact(bits(was[0]), bits(was[1]), c.bt, [20, 30, 4], c.starts, an.cpu().numpy(),
+                     [2, 4, 0])
+    assert np.array_equal(bits(t["kc"]), k) and np.array_equal(bits(t["vc"]), v)
