@@ -64,6 +64,7 @@ extern "C" {
 #define KV_ERR_NOT_FOUND (-5)     /* unknown sequence id */
 #define KV_ERR_EXISTS (-6)        /* sequence id already present */
 #define KV_ERR_TOO_LARGE (-7)     /* the request exceeds a fixed size limit of the library */
+#define KV_ERR_OUT_OF_MEMORY (-8) /* no host memory (kv_tree_step, kv_seq_truncate) */
 
 /* --------------------------------------------------------------- data types */
 #define KV_DTYPE_BF16 0     /* bfloat16 */
@@ -163,7 +164,7 @@ int kv_step(kv_alloc_t* a, const int64_t* seq_ids, int n, int64_t* slot_mapping,
  *     block_tables ([n][max_blocks], -1 padded) are the state after it.
  * num_nodes[i] == 1 for every row gives what kv_step gives.  All-or-nothing,
  * with kv_step's errors; KV_ERR_INVALID_ARG also for a negative count or a
- * total of 2^31 or more.  After the tokens are verified, kv_seq_truncate
+ * total of 2^31 or more, KV_ERR_OUT_OF_MEMORY without host memory.  After the tokens are verified, kv_seq_truncate
  * drops the rejected ones. */
 int kv_tree_step(kv_alloc_t* a, const int64_t* seq_ids, const int32_t* num_nodes, int n,
                  int64_t* slot_mapping, int32_t* block_tables, int max_blocks,
@@ -173,7 +174,8 @@ int kv_tree_step(kv_alloc_t* a, const int64_t* seq_ids, const int32_t* num_nodes
 /* Cut sequences to new_lens[i] <= len tokens: blocks past ceil(new_lens[i]/16)
  * lose one reference and return to the pool at zero (the tokens of a draft
  * that were not accepted, after kv_tree_compact).  seq_ids distinct and live;
- * on an error (KV_ERR_NOT_FOUND, KV_ERR_INVALID_ARG) nothing changes. */
+ * on an error (KV_ERR_NOT_FOUND, KV_ERR_INVALID_ARG, KV_ERR_OUT_OF_MEMORY)
+ * nothing changes. */
 int kv_seq_truncate(kv_alloc_t* a, const int64_t* seq_ids, const int64_t* new_lens, int n);
 
 /* Reorder the KV state of a batch of live sequences (beam search selection

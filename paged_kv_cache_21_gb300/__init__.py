@@ -28,6 +28,7 @@ KV_ERR_CUDA = -4
 KV_ERR_NOT_FOUND = -5
 KV_ERR_EXISTS = -6
 KV_ERR_TOO_LARGE = -7
+KV_ERR_OUT_OF_MEMORY = -8
 NOALLOC_WORKSPACE_BYTES = 16 << 20
 
 BF16 = 0
@@ -53,7 +54,7 @@ TRACE_FIELDS = len(TRACE_KEYS)
 _ERRNAMES = {KV_ERR_INVALID_ARG: "KV_ERR_INVALID_ARG", KV_ERR_OUT_OF_BLOCKS: "KV_ERR_OUT_OF_BLOCKS",
              KV_ERR_UNSUPPORTED: "KV_ERR_UNSUPPORTED", KV_ERR_CUDA: "KV_ERR_CUDA",
              KV_ERR_NOT_FOUND: "KV_ERR_NOT_FOUND", KV_ERR_EXISTS: "KV_ERR_EXISTS",
-             KV_ERR_TOO_LARGE: "KV_ERR_TOO_LARGE"}
+             KV_ERR_TOO_LARGE: "KV_ERR_TOO_LARGE", KV_ERR_OUT_OF_MEMORY: "KV_ERR_OUT_OF_MEMORY"}
 
 
 class KVError(RuntimeError):

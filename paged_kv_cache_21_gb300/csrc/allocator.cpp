@@ -276,8 +276,8 @@ try {
     }
     if (n_cow) *n_cow = ncow;
     return KV_OK;
-} catch (...) {      // out of host memory, before anything changed
-    return KV_ERR_INVALID_ARG;
+} catch (...) {      // before anything changed
+    return KV_ERR_OUT_OF_MEMORY;
 }
 
 int kv_seq_truncate(kv_alloc_t* a, const int64_t* seq_ids, const int64_t* new_lens, int n)
@@ -305,7 +305,7 @@ try {
     }
     return KV_OK;
 } catch (...) {
-    return KV_ERR_INVALID_ARG;
+    return KV_ERR_OUT_OF_MEMORY;
 }
 
 int kv_seq_reorder(kv_alloc_t* a, const int64_t* seq_ids, const int32_t* src_index, int n)
