@@ -642,14 +642,14 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_tables, context_lens, n
     torch = _torch or _load_torch()
     T, Hq, D = q.shape
     cache = k_cache.shape
-    NB, Hkv, _, D2 = cache
+    NB, Hkv, block, D2 = cache
     B, max_blocks = block_tables.shape
     f32 = out.dtype is torch.float32
     if (q.dtype is not torch.bfloat16 or not (f32 or out.dtype is torch.bfloat16)
-            or out.shape != q.shape or D != D2 or v_cache.shape != cache
+            or out.shape != q.shape or D != D2 or block != BLOCK_SIZE or v_cache.shape != cache
             or k_cache.dtype is not v_cache.dtype):
         raise ValueError("q must be bfloat16 [T, Hq, D], out bfloat16 or float32 of its shape, "
-                         "k_cache and v_cache alike")
+                         "k_cache and v_cache [NB, Hkv, 16, D], alike")
     dev = _place(k_cache)
     i32, n = torch.int32, q.numel()
     _check(_HOT_TREE_ATTENTION(

@@ -4,6 +4,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -44,3 +45,17 @@ def test_a_failed_host_allocation_has_a_code_of_its_own(pk):
                        timeout=120)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == [str(pk.KV_ERR_OUT_OF_MEMORY)] * 2
+
+
+@pytest.mark.parametrize("block", [8, 15, 32])
+def test_caches_of_other_blocks_are_refused(pk, block):
+    """Blocks of 16 tokens are what the kernels address: with 8 they would read behind the
+    cache's end."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16)
+    kc = torch.zeros((4, 2, block, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="16"):
+        pk.paged_tree_attention(torch.empty_like(q), q, kc, kc, i32(1, 2), i32(1), i32(2), i32(3), 3,
+                                0.1, torch.zeros(1024, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="16"):
+        pk.CacheLayers([kc], [kc])
