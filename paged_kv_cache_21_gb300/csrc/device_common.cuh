@@ -1,10 +1,13 @@
 // Small inline-PTX helpers shared by the kernels of libpagedkv (sm_103a).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include "paged_kv.h"
 
 namespace pkv {
 
@@ -24,6 +27,33 @@ __device__ __forceinline__ void raise_flag(DevErr* e, unsigned f, long long deta
     unsigned old = atomicOr(&e->flags, f);
     if (old == 0) e->detail = detail;
 }
+
+// Read one of them (a __device__ variable), and clear it if anything is set: a copy each,
+// of ~9 and ~3 us, so that the usual call makes no second one.
+inline int take_error(const DevErr& word, unsigned* flags, long long* detail)
+{
+    DevErr e;
+    if (cudaMemcpyFromSymbol(&e, word, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
+    const DevErr z = {0u, -1LL};
+    if (e.flags && cudaMemcpyToSymbol(word, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
+    *flags = e.flags;
+    *detail = e.flags ? e.detail : -1;
+    return KV_OK;
+}
+
+// Whether this process has launched (or captured) a kernel of the translation unit: the
+// word of one that it has not is not read.
+struct Launched {
+    std::atomic<bool> yes{false};
+    void note() { if (!yes.load(std::memory_order_relaxed)) yes.store(true, std::memory_order_relaxed); }
+    int take_error(const DevErr& word, unsigned* flags, long long* detail)
+    {
+        if (yes.load(std::memory_order_relaxed)) return pkv::take_error(word, flags, detail);
+        *flags = 0;
+        *detail = -1;
+        return KV_OK;
+    }
+};
 
 // ------------------------------------------------------------ shared memory
 __device__ __forceinline__ uint32_t smem_u32(const void* p)

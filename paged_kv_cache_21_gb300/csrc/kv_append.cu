@@ -90,16 +90,7 @@ __global__ void __launch_bounds__(256) kv_copy_blocks_kernel(uint4* __restrict__
     }
 }
 
-int append_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_append_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_append_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int append_read_error(unsigned* flags, long long* detail) { return take_error(g_append_err, flags, detail); }
 
 }  // namespace pkv
 

@@ -23,6 +23,7 @@
 namespace pkv {
 
 __device__ DevErr g_compact_err;
+static Launched g_launched;
 
 namespace {
 
@@ -147,16 +148,7 @@ static bool overlap(void* const* k, void* const* v, int n, uint64_t bytes)
     return hit != 0;
 }
 
-int compact_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_compact_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_compact_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int compact_read_error(unsigned* flags, long long* detail) { return g_launched.take_error(g_compact_err, flags, detail); }
 
 }  // namespace pkv
 
@@ -201,6 +193,7 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
     p.num_blocks = num_blocks;
     p.Hkv = num_kv_heads;
     p.chunks = (int)(row_bytes / 16);
+    g_launched.note();
     for (int l0 = 0; l0 < num_layers; l0 += kLayersPerLaunch) {
         const int nl = num_layers - l0 < kLayersPerLaunch ? num_layers - l0 : kLayersPerLaunch;
         for (int l = 0; l < nl; ++l) {

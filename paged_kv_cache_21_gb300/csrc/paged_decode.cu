@@ -2039,16 +2039,7 @@ int num_sms_current()
     return n;
 }
 
-int decode_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_decode_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_decode_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int decode_read_error(unsigned* flags, long long* detail) { return take_error(g_decode_err, flags, detail); }
 
 // ------------------------------------------------- fixed, library-owned scratch
 // Scratch of the allocation-free entry point: a file-scope device array that

@@ -914,15 +914,6 @@ cudaError_t wide_launch(const CUtensorMap& mk, const CUtensorMap& mv, const Wide
                : cudaLaunchKernelEx(&cfg, paged_decode_wide_kernel<128>, mk, mv, p);
 }
 
-int wide_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_wide_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_wide_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int wide_read_error(unsigned* flags, long long* detail) { return take_error(g_wide_err, flags, detail); }
 
 }  // namespace pkv

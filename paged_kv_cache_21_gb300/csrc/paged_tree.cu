@@ -914,16 +914,7 @@ cudaError_t launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const Tree
 
 }  // namespace
 
-int tree_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_tree_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_tree_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int tree_read_error(unsigned* flags, long long* detail) { return g_launched.take_error(g_tree_err, flags, detail); }
 
 }  // namespace pkv
 
@@ -1007,6 +998,7 @@ extern "C" int paged_tree_attention(void* out, int out_dtype, const void* q, con
     p.test_stall = test_stall_cycles();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Partials few = {}, many = {};
+    g_launched.note();
     if (t.few) {
         p.part_o = reinterpret_cast<float*>(ws + t.few_o);
         p.part_ml = reinterpret_cast<float2*>(ws + t.few_ml);

@@ -811,6 +811,7 @@ cudaError_t tree_small_launch(const CUtensorMap& mk, const CUtensorMap& mv, cons
                               bool fp8, int rows, cudaStream_t st)
 {
     const bool n32 = tree_small_rows(rows) == 32;
+    g_launched.note();
     if (D == 128) {
         if (fp8) return n32 ? launch<128, true, 32>(mk, mv, p, st) : launch<128, true, 64>(mk, mv, p, st);
         return n32 ? launch<128, false, 32>(mk, mv, p, st) : launch<128, false, 64>(mk, mv, p, st);
@@ -819,15 +820,6 @@ cudaError_t tree_small_launch(const CUtensorMap& mk, const CUtensorMap& mv, cons
     return n32 ? launch<64, false, 32>(mk, mv, p, st) : launch<64, false, 64>(mk, mv, p, st);
 }
 
-int tree_small_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_tree_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_tree_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int tree_small_read_error(unsigned* flags, long long* detail) { return g_launched.take_error(g_tree_err, flags, detail); }
 
 }  // namespace pkv

@@ -24,6 +24,7 @@
 namespace pkv {
 
 static __device__ DevErr g_tree_err;            // one per translation unit
+static Launched g_launched;
 
 namespace {
 

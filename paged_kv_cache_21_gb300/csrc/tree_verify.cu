@@ -46,6 +46,7 @@ namespace cg = cooperative_groups;
 namespace pkv {
 
 __device__ DevErr g_verify_err;
+static Launched g_launched;
 
 namespace {
 
@@ -689,16 +690,7 @@ cudaError_t launch_verify(const VerifyParams& p, int num_seqs, int cluster, cuda
 
 }  // namespace
 
-int verify_read_error(unsigned* flags, long long* detail)
-{
-    DevErr e;
-    if (cudaMemcpyFromSymbol(&e, g_verify_err, sizeof e) != cudaSuccess) return KV_ERR_CUDA;
-    DevErr z = {0u, -1LL};
-    if (cudaMemcpyToSymbol(g_verify_err, &z, sizeof z) != cudaSuccess) return KV_ERR_CUDA;
-    *flags = e.flags;
-    *detail = e.flags ? e.detail : -1;
-    return KV_OK;
-}
+int verify_read_error(unsigned* flags, long long* detail) { return g_launched.take_error(g_verify_err, flags, detail); }
 
 }  // namespace pkv
 
@@ -752,6 +744,7 @@ extern "C" int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32
     int cluster = kMaxCluster;
     while (cluster > 1 && (long long)num_seqs * cluster > kCtasPerSm * num_sms_current()) cluster /= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    g_launched.note();
     const cudaError_t err =
         bf16 ? (vec ? launch_verify<true, 8>(p, num_seqs, cluster, st)
                     : launch_verify<true, 1>(p, num_seqs, cluster, st))

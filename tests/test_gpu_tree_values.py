@@ -286,3 +286,32 @@ def test_an_inactive_row_of_a_padded_batch_goes_through_a_step_without_a_flag(pk
     k, v = R.compact(bits(was[0]), bits(was[1]), c.bt, [20, 30, 4], c.starts, an.cpu().numpy(),
                      [2, 4, 0])
     assert np.array_equal(bits(t["kc"]), k) and np.array_equal(bits(t["vc"]), v)
+
+
+def test_flags_of_every_call_are_read_and_cleared(pk):
+    """Each call's first bad table is seen, by the next reading only."""
+    def attend(counts):
+        c = Case([60 + n for n in counts], counts, 8, 2, 64, seed=1)
+        t = c.device()
+        t["lens"][0] = -5
+        c.run(pk, t=t)
+
+    def verify():
+        i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+        pk.kv_tree_verify(i32(1), i32(1, 3), i32(1, 3), torch.ones((3, 8), device="cuda"), i32(3),
+                          i32(3) + 3, torch.tensor([0, 3], dtype=torch.int32, device="cuda"),
+                          greedy=True)
+
+    def compact():
+        k = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        pk.kv_tree_compact(pk.CacheLayers([k], [k.clone()]), i32([[0]]), i32([9]), i32([0, 4]),
+                           i32([[0, 9, 9, 9]]), i32([2]))
+
+    for call, flag in ((lambda: attend([3]), pk.DEVERR_CONTEXT_TOO_LONG),
+                       (lambda: attend([40]), pk.DEVERR_CONTEXT_TOO_LONG),
+                       (verify, pk.DEVERR_BAD_TREE), (compact, pk.DEVERR_BAD_TREE)):
+        call()
+        torch.cuda.synchronize()
+        assert pk.get_device_error()[0] == flag
+        assert pk.get_device_error() == (0, -1)
