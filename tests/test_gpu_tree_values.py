@@ -315,3 +315,80 @@ def test_flags_of_every_call_are_read_and_cleared(pk):
         torch.cuda.synchronize()
         assert pk.get_device_error()[0] == flag
         assert pk.get_device_error() == (0, -1)
+
+
+# A weight in one bf16 is off by at most half a step, 2^-8 of it, and their sum is that of the
+# rounded ones, so that an output moves by sum_j w_j e_j (V_j - out) with |e_j| <= 2^-8, whose
+# mean square over roundings of either sign is at most 2^-16 / 3 sum_j w_j^2 (V_j - out)^2; the
+# output's own rounding adds at most 2^-16 / 3 out^2.  A key left out moves it by w_j (V_j - out).
+
+def mean_square(got, ref, w2):
+    """Mean square error, and what the roundings of weights and outputs may make of it."""
+    return float(((got - ref) ** 2).mean()), float((2.0 ** -16 / 3 * (w2 + ref ** 2)).mean())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,heads", [([20, 1], (8, 2)), ([40, 7], (8, 2)), ([72, 9], (16, 2))])
+@pytest.mark.parametrize("ctx", [100, 1000, 6000])
+def test_bf16_outputs_of_wide_trees_are_off_by_their_roundings_only(pk, ctx, counts, heads, D):
+    c = Case([ctx + counts[0], 30 + counts[1]], counts, *heads, D, seed=ctx + D)
+    got = c.run(pk).double().cpu().numpy()
+    ref, _, scores, _ = scored(c)
+    w2 = np.zeros_like(ref)
+    for (t, h), (x, V) in scores.items():
+        w = np.exp(x - x.max())
+        w2[t, h] = (w / w.sum()) ** 2 @ (V - ref[t, h]) ** 2
+    n = counts[0]                                   # the wide tree; and each of its rows alone
+    err, bound = mean_square(got[:n], ref[:n], w2[:n])
+    assert err <= bound
+    for t, h in np.ndindex(n, heads[0]):
+        # (of D columns alone: up to twice the mean)
+        err, bound = mean_square(got[t, h], ref[t, h], w2[t, h])
+        assert err <= 2 * bound, (t, h)
+    # with one key of a row left out, up to 1000 tokens, it would not hold
+    x, V = scores[n // 2, 0]
+    w = np.exp(x - x.max())
+    w /= w.sum()
+    j = np.argsort(w)[len(w) // 2]
+    lost = (ref[n // 2, 0] - w[j] * V[j]) / (1 - w[j])
+    err, bound = mean_square(lost, ref[n // 2, 0], w2[n // 2, 0])
+    assert err > 2 * bound or ctx > 1000
+
+
+@pytest.mark.parametrize("heads,n", [((32, 8), 20), ((32, 8), 64)])
+def test_bf16_outputs_of_a_full_gpu_of_long_contexts(pk, heads, n):
+    Hq, Hkv, D, B, L = heads[0], heads[1], 128, 24, 3000 + n
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    nb = -(-L // BS)
+    bt = torch.randperm(B * nb, generator=gen, device="cuda").to(torch.int32).view(B, nb)
+    k, v = (torch.randn((B * nb, Hkv, BS, D), generator=gen, device="cuda").to(torch.bfloat16)
+            for _ in range(2))
+    q = torch.randn((B * n, Hq, D), generator=gen, device="cuda").to(torch.bfloat16)
+    rng = np.random.default_rng(n)
+    par = np.concatenate([R.random_tree(rng, n, 3) for _ in range(B)]).astype(np.int32)
+    starts = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    ws = pk.alloc_tree_workspace(B, n, Hq, Hkv, D)
+    outs = []
+    for _ in range(8):
+        outs.append(torch.empty((B * n, Hq, D), dtype=torch.bfloat16, device="cuda"))
+        pk.paged_tree_attention(outs[-1], q, k, v, bt, lens, starts, torch.from_numpy(par).cuda(), n,
+                                D ** -0.5, ws)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    G = Hq // Hkv
+    for s in range(B):
+        K, V = (t[bt[s].long()].double().transpose(0, 1).reshape(Hkv, -1, D)[:, :L] for t in (k, v))
+        Q = q[s * n:(s + 1) * n].double().view(n, Hkv, G, D).transpose(0, 1).reshape(Hkv, n * G, D)
+        mask = torch.zeros((n, L), dtype=torch.float64)
+        mask[:, L - n:] = -np.inf
+        for i, seen in enumerate(R.ancestors(par[s * n:(s + 1) * n])):
+            mask[i, [L - n + j for j in seen]] = 0
+        w = torch.softmax(Q @ K.transpose(1, 2) * D ** -0.5
+                          + mask.cuda().repeat_interleave(G, 0)[None], -1)
+        ref = w @ V
+        # sum_j w_j^2 (V_j - out)^2
+        w2 = (w * w) @ (V * V) - 2 * ((w * w) @ V) * ref + (w * w).sum(-1, keepdim=True) * ref * ref
+        got = outs[0][s * n:(s + 1) * n].double().view(n, Hkv, G, D).transpose(0, 1).reshape(Hkv, n * G, D)
+        for h in range(Hkv):
+            err, bound = mean_square(got[h], ref[h], w2[h])
+            assert err <= bound, (s, h)
