@@ -584,7 +584,7 @@ int paged_tree_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int
  * num_kv_heads with G = num_q_heads / num_kv_heads <= 128.  Deterministic as
  * paged_decode_attention.  Scores and the softmax's (max, sum) are float32.  Over
  * E4M3 caches a query element is used exactly down to 2^-24 of the largest of its
- * row (one node and head), and within 2^-31 of that largest below; the products'
+ * row (one node and head), and within 2^-30 of that largest below; the products'
  * sums are the 8-bit matrix instructions', within 3 * 2^-20 of the largest product.
  * Weights are multiplied as two bf16 parts (16 bits; E4M3 caches: f16), but as
  * one bf16 (8 bits, the sum being that of the rounded weights) for a bf16

@@ -603,24 +603,16 @@ __device__ __forceinline__ bool widen(const TreeParams& p, const Walk& w, uint32
     return true;
 }
 
-// Four E5M2 codes as four f16, of which they are the upper bytes.
-__device__ __forceinline__ void e5m2x4_to_f16x4(uint32_t x, __half2& lo, __half2& hi)
-{
-    const uint32_t l = __byte_perm(x, 0u, 0x1404), h = __byte_perm(x, 0u, 0x3424);
-    lo = *reinterpret_cast<const __half2*>(&l);
-    hi = *reinterpret_cast<const __half2*>(&h);
-}
-
 // A query row's 8 elements (16 bytes of bf16) as three E5M2 parts, for E4M3 keys:
 // the row is scaled by a power of two that brings its largest |element| into
-// [2^14, 2^15); each part is what the ones before leave, rounded to E5M2's three
+// [2^14, 2^15).  As f16 an element is then exact down to 2^-17; E5M2 is an f16's upper
+// byte, so that a part is what the ones before leave with its lower byte cleared, three
 // bits.  Three parts hold bf16's eight bits exactly, down to 2^-24 of the row's
 // largest element (2^-9 here); below, where parts fall between E5M2's steps of
-// 2^-16, an element is off by at most 2^-17, 2^-31 of the largest.  (Two parts of
+// 2^-16, an element loses at most 2^-16, 2^-30 of the largest.  (Two parts of
 // E4M3, four bits each but steps of 2^-9, were exact down to 2^-10 of the largest
-// only: an outlier cost the other elements theirs.  The third part takes
-// 8 nodes x 4 heads of 32 x 8192 tokens from 117 to 121 us, 16 nodes from 153 to 160, 64
-// from 388 to 437, half of that for the room it takes from the rings.)  The scores are
+// only: an outlier cost the other elements theirs.  32 x 8192 tokens, 4 heads: 8 nodes 117
+// us then, 121 now; 16 nodes 153, 156; 64 nodes 388, 434.)  The scores are
 // multiplied by `up` again.  A row with infinities or NaN has up = NaN.  The row's
 // D / 8 lanes call together.
 constexpr int kQueryParts = 3;
@@ -638,31 +630,20 @@ __device__ __forceinline__ void query_e5m2(uint4 v, uint2 (&parts)[kQueryParts],
     const int e = big == 0 ? 0 : max((int)(big >> 7) - (127 + 14), -126);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
     up = big >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 + e) << 23);
-    uint32_t codes[2][kQueryParts];
+    uint32_t p[kQueryParts][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float x[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            x[2 * k] = bf16_lo(q4[2 * h + k]) * down;
-            x[2 * k + 1] = bf16_hi(q4[2 * h + k]) * down;
-        }
+    for (int k = 0; k < 4; ++k) {
+        uint32_t x = pack_f16x2(bf16_lo(q4[k]) * down, bf16_hi(q4[k]) * down);
 #pragma unroll
         for (int part = 0; part < kQueryParts; ++part) {
-            const uint32_t c =
-                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E5M2) |
-                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E5M2) << 16;
-            __half2 lo, hi;
-            e5m2x4_to_f16x4(c, lo, hi);
-            x[0] -= __low2float(lo);
-            x[1] -= __high2float(lo);
-            x[2] -= __low2float(hi);
-            x[3] -= __high2float(hi);
-            codes[h][part] = c;
+            p[part][k] = x & 0xff00ff00u;
+            const __half2 left = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&p[part][k]));
+            x = *reinterpret_cast<const uint32_t*>(&left);
         }
     }
 #pragma unroll
-    for (int part = 0; part < kQueryParts; ++part) parts[part] = make_uint2(codes[0][part], codes[1][part]);
+    for (int part = 0; part < kQueryParts; ++part)
+        parts[part] = make_uint2(__byte_perm(p[part][0], p[part][1], 0x7531), __byte_perm(p[part][2], p[part][3], 0x7531));
 }
 
 // Byte offset of byte 8 c of row r of a tile of D-byte rows, with the swizzle that
