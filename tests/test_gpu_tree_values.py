@@ -415,3 +415,49 @@ def test_bf16_outputs_of_a_full_gpu_of_long_contexts(pk, heads, n):
         for h in range(Hkv):
             err, bound = mean_square(got[h], ref[h], w2[h])
             assert err <= bound, (s, h)
+
+
+@pytest.mark.parametrize("bf16,V", [(False, 4096), (False, 50001), (True, 50001)])
+def test_the_drawn_token_is_that_of_the_exact_sums(pk, bf16, V):
+    """The number that the last token is drawn by is, of all float32, the one that comes
+    nearest to a border between two tokens: V borders beside 2^24 numbers leave about
+    2^-24 / V.  Sums within 2^-44 decide it as 64 bits do; float32 sums would miss every other
+    one.  One refused child, so that the sums are those of max(p - q, 0), and two, max(p - a q, 0)."""
+    B = 60
+    gen = torch.Generator().manual_seed(V)
+    logits = torch.randn((3 * B, V), generator=gen) * 2
+    dt = torch.bfloat16 if bf16 else torch.float32
+    target = torch.softmax(logits, 1).to(dt)
+    draft = torch.softmax(logits + torch.randn((3 * B, V), generator=gen), 1).to(dt)
+    tokens = np.zeros(3 * B, dtype=np.int32)
+    parents = np.tile(np.array([-1, 0, 0], dtype=np.int32), B)
+    parents[5::6] = -2                              # every other sequence has one child
+    starts = np.arange(0, 3 * B + 1, 3, dtype=np.int32)
+    u = np.full(3 * B, 1 - 2.0 ** -24, dtype=np.float32)
+    su = np.zeros(B, dtype=np.float32)
+    want = np.zeros(B, dtype=np.int64)
+    for s in range(B):
+        p, q = (x[3 * s].double().numpy().astype(np.longdouble) for x in (target, draft))
+        # tokens that are refused: the draft thinks more of them than the target does
+        worse = np.nonzero(q > p * 1.01)[0]
+        tokens[3 * s + 1:3 * s + 3] = worse[:2]
+        R = np.maximum(p - q, 0)
+        if parents[3 * s + 2] == 0:
+            assert not 1.0 * q[worse[1]] * R.sum() < R[worse[1]]
+            R = np.maximum(p - (1 + R.sum()) * q, 0)
+        cum = np.cumsum(R)
+        share = (cum / cum[-1])[:-1]
+        near = share.astype(np.float32)
+        gap = np.abs(near.astype(np.longdouble) - share)
+        gap[(near >= 1) | (near <= 0) | (gap < 2.0 ** -41)] = 1
+        i = int(np.argmin(gap))
+        su[s] = near[i]
+        want[s] = int(np.nonzero(cum > su[s].astype(np.longdouble) * cum[-1])[0][0])
+        assert gap[i] < 2.0 ** -30
+    c = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    al, an, ot = i32(B), i32(B, 3), i32(B, 3)
+    pk.kv_tree_verify(al, an, ot, target.cuda(), c(tokens), c(parents), c(starts), c(u), c(su),
+                      draft_probs=draft.cuda())
+    assert (al == 1).all()
+    assert np.array_equal(ot[:, 0].cpu().numpy(), want)
