@@ -10,8 +10,8 @@
 // (max, sum) softmax of its section "Numerical trick").
 //
 // What bounds it: with n nodes the K and V of a sequence are read once for all
-// n * G query rows of a KV head, so up to about 256 rows the time is that of the
-// bytes, beyond them that of the products and exponentials.
+// n * G query rows of a KV head.  Up to 64 rows the time is that of the bytes; 128 rows
+// take 1.5 times that, 256 rows twice, for the chain from scores to products (below).
 //
 // This file holds the kernel for more than 64 rows, the kernel that joins
 // partial results, and the entry points; paged_tree_small.cu the kernel for up
@@ -48,18 +48,18 @@
 //    P is f16 for an E4M3 cache (whose V is widened to f16, which holds every code
 //    exactly); for a bf16 cache it is bf16, in high and low parts (16 bits, two
 //    products) for a float32 output (LOW).  For a bf16 output the high part
-//    alone, since the second product costs a fifth (397 us against 323): 2^-8 of each
+//    alone, since the second product costs a fifth (402 us against 328): 2^-8 of each
 //    weight at most, of either sign, which over many keys comes to about what the
 //    output's own rounding does (the largest error of 32 x 8192 tokens, 64 nodes goes
 //    from 0.0017 to 0.0023).  The sum is that of the rounded weights.
-//  * Measured at 64 nodes x 4 heads of 32 x 8192 tokens: 323 us; the bytes take 164,
+//  * Measured at 64 nodes x 4 heads of 32 x 8192 tokens: 328 us; the bytes take 164,
 //    the products 149 at the tensor cores' rate, 117 the exponentials.  A 128-key
 //    chunk takes ~4900 clocks; a stream's chain is 590 to issue S, 230 until it is
 //    seen, ~2400 of softmax (200 until the scores are read, 360 maximum, 200 for
 //    the halves to meet, 900 weights; four warps share a scheduler), 650 to issue
 //    P V, 450 until its end is seen.  P in tensor memory of its own with S two
 //    chunks ahead removes the chain but has both softmax phases contend again (332),
-//    and takes two waits a chunk for a float32 output (846 against 397); 64-key
+//    and takes two waits a chunk for a float32 output (846 against 397 then); 64-key
 //    pieces of S cost as many MMA clocks as 128 (530 against 499 then); products of
 //    half the keys while the others are weighed cost what they gain (327).
 //  * Only the chunks that reach the drafted positions need masks; there a prep warp
@@ -113,6 +113,7 @@ struct Geo {
     static constexpr int kScale = 128 / D;
     // the two streams take the chunks in turn, or both take each
     static constexpr int kChunkStep = TILES == 1 ? 2 : 1;
+    // (E4M3: two tiles of queries in three parts leave room for less)
     static constexpr int kKSlots = (FP8 && TILES == 1 ? 3 : 2) * kScale;
     static constexpr int kVSlots = (!FP8 && TILES == 1 ? 3 : 2) * kScale;
     static constexpr int kRawV = !FP8 ? 0 : (TILES == 1 ? 2 : 1) * kScale;

@@ -11,10 +11,11 @@
 //                       product, added at the end: the low part costs nothing).
 // 16 products, ~1030 clocks, for 128 keys, whose bf16 K and V take ~2450 clocks
 // to arrive at 6.8 TB/s over 152 SMs (E4M3: ~1220): HBM is the bound.  Measured:
-// 32 x 8192 tokens, 8 nodes x 4 heads, bf16: 168 us (bytes: 159); 4 x 131072: 313
-// (316); E4M3, 8 nodes: 110 us, 16 nodes x 4 heads: 152 us (80), where shared memory
+// 32 x 8192 tokens, 8 nodes x 4 heads, bf16: 167 us (bytes: 159); 4 x 131072: 312
+// (316); E4M3, 8 nodes: 121 us, 16 nodes x 4 heads: 166 us (80), where shared memory
 // carries ~190 KB a chunk (~1500 clocks: codes, widened V, weights, the MMAs'
-// operands) and a group's weights take ~2300 clocks.
+// operands), a group's weights take ~2300 clocks, and the query's third part another
+// four products.
 //
 // Scores and products have an MMA thread each: one for both was busy ~2400 clocks a
 // chunk, of which the tensor cores 1024, with commits and waits of ~100 clocks (172

@@ -46,8 +46,8 @@ struct TreeParams {
 };
 
 // Query rows per KV head up to which a sequence is served by the kernel for few rows.
-// (32 x 8192 tokens, 4 heads per KV head, 36 and 64 rows: 169 and 171 us by that kernel,
-// 234 and 237 by the other; E4M3: 151 and 150 against 174 and 182.)
+// (32 x 8192 tokens, 4 heads per KV head, 36 and 64 rows: 168 and 172 us by that kernel,
+// 235 and 238 by the other; E4M3: 152 and 157 against 198 and 207.)
 constexpr int kSmallRows = 64;
 
 // The kernel for few rows: rows (32 or 64) of its instantiation for the most

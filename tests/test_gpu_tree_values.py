@@ -1,7 +1,8 @@
-"""Draft-tree attention and its neighbours on the GPU, at values and shapes where a result
-can be lost without a fault: infinities and NaN that a node sees.
+"""Draft-tree attention and its neighbours on the GPU, where a result can be lost without a
+fault: infinities and NaN that a node sees, queries of every magnitude, workspaces of another
+size, idle rows, single lost keys in bf16 outputs, numbers at the border of two tokens.
 
-Where an output is finite, the tolerances are those of test_gpu_tree.py."""
+Where nothing else is said, the tolerances are those of test_gpu_tree.py."""
 import numpy as np
 import pytest
 import torch
