@@ -15,8 +15,9 @@
  *   - Device buffers are plain device pointers owned by the caller; the
  *     library never allocates, frees or retains device memory.  Host
  *     buffers are plain host pointers, also caller-owned.  The per-step
- *     buffers of the decode entry points (q, k_new, v_new, block_tables,
- *     context_lens, prefix tables, out) may also be pinned host memory that
+ *     buffers of the decode and draft-tree entry points (q, k_new, v_new,
+ *     block_tables, context_lens, prefix and tree tables, probabilities,
+ *     tokens, numbers, out) may also be pinned host memory that
  *     the device can address (cudaHostAlloc / cudaHostRegister with unified
  *     addressing): the kernels then read and write them in place, over the
  *     coherent NVLink-C2C link of a Grace-Blackwell node, with no copy.  The
@@ -664,7 +665,8 @@ int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32_t* out_tok
  * KV_DEVERR_BLOCK_OUT_OF_RANGE and is left out.  A sequence without a context
  * (context_lens[s] == 0) moves nothing, whatever its path.  The blocks that hold the nodes
  * must be private to their sequence (kv_tree_step's are).  Nothing else in the
- * caches changes.  One launch for up to 128 layers. */
+ * caches changes.  One launch for up to 128 layers; more than 65535 sequences are
+ * KV_ERR_TOO_LARGE. */
 int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers,
                     const int32_t* block_tables, int max_blocks_per_seq,
                     const int32_t* context_lens, const int32_t* node_starts,

@@ -589,7 +589,7 @@ def _load_torch():
 def _place(t):
     """The device index the tensors of a call have to be on: that of `t`, which
     has to be the current device (a call launches there).  Host memory the device
-    can address (pinned) will do for any of them."""
+    can address (pinned) will do for all but the caches and the workspace."""
     i = t.get_device()
     if i < 0:
         if not t.is_pinned():
@@ -599,6 +599,14 @@ def _place(t):
         raise ValueError("tensor on cuda:%d, current device is cuda:%d"
                          % (i, _torch.cuda.current_device()))
     return i
+
+
+def _device_only(*tensors):
+    """Refuses caches and workspaces in host memory."""
+    for t in tensors:
+        if t.get_device() < 0:
+            raise ValueError("caches and workspace must be device memory (only a step's own "
+                             "tensors may be pinned host memory)")
 
 
 def _ptr(name, t, dtype, n, dev):
@@ -650,6 +658,7 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_tables, context_lens, n
             or k_cache.dtype is not v_cache.dtype):
         raise ValueError("q must be bfloat16 [T, Hq, D], out bfloat16 or float32 of its shape, "
                          "k_cache and v_cache [NB, Hkv, 16, D], alike")
+    _device_only(k_cache, v_cache, workspace)
     dev = _place(k_cache)
     i32, n = torch.int32, q.numel()
     _check(_HOT_TREE_ATTENTION(
@@ -749,9 +758,8 @@ def kv_tree_compact(layers, block_tables, context_lens, node_starts, accept_node
     torch = _torch or _load_torch()
     B, max_nodes = accept_nodes.shape
     max_blocks = block_tables.shape[1]
+    _device_only(layers.first)                                  # (the others are like it)
     dev, i32 = _place(layers.first), torch.int32
-    if layers.first.get_device() < 0 and not all(t.is_pinned() for x in layers.tensors for t in x):
-        raise ValueError("caches in host memory must be pinned")
     _check(_HOT_TREE_COMPACT(
         layers.k_ptrs, layers.v_ptrs, layers.num_layers,
         _ptr("block_tables", block_tables, i32, B * max_blocks, dev), max_blocks,

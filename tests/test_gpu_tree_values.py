@@ -462,3 +462,21 @@ def test_the_drawn_token_is_that_of_the_exact_sums(pk, bf16, V):
                       draft_probs=draft.cuda())
     assert (al == 1).all()
     assert np.array_equal(ot[:, 0].cpu().numpy(), want)
+
+
+def test_caches_and_workspaces_in_host_memory_are_refused(pk):
+    """They must be device memory: the others may be pinned host memory."""
+    c = Case([40], [3], 4, 2, 64, seed=2)
+    t = c.device()
+    ws = pk.alloc_tree_workspace(1, 3, 4, 2, 64)
+    for key in ("kc", "vc"):
+        bad = dict(t, **{key: t[key].cpu().pin_memory()})
+        with pytest.raises(ValueError, match="device memory"):
+            c.run(pk, t=bad, ws=ws)
+    with pytest.raises(ValueError, match="device memory"):
+        c.run(pk, t=t, ws=ws.cpu().pin_memory())
+    k = t["kc"].cpu().pin_memory()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError, match="device memory"):
+        pk.kv_tree_compact(pk.CacheLayers([k], [k.clone().pin_memory()]), t["bt"], t["lens"],
+                           t["starts"], i32(1, 3), i32(1))
