@@ -92,6 +92,12 @@ extern "C" {
  * is negative or the product overflows int64. */
 int64_t kv_bytes(int layers, int batch, int kv_heads, int64_t seq, int head_dim, int dtype_bytes);
 
+/* Bytes of the latent caches of a whole model, one row of `width` (latent_dim +
+ * rope_dim) elements a token and layer:
+ *     layers * batch * seq * width * dtype_bytes
+ * (an interface of this implementation).  -1 as kv_bytes. */
+int64_t kv_latent_bytes(int layers, int batch, int64_t seq, int width, int dtype_bytes);
+
 /* --------------------------------------------------- host block allocator */
 
 /* Library-owned host object: a pool of num_blocks 16-token blocks with a
@@ -106,7 +112,9 @@ typedef struct kv_alloc kv_alloc_t;
 /* Create an allocator.  block_size must be 16; num_kv_heads, head_dim and
  * kv_dtype are recorded for kv_alloc_stats and checks.  *out receives the
  * handle (NULL on failure).  The caller allocates the device caches itself
- * ([num_blocks][num_kv_heads][16][head_dim] per layer, K and V). */
+ * ([num_blocks][num_kv_heads][16][head_dim] per layer, K and V).  For latent
+ * caches ([num_blocks][16][width]) pass num_kv_heads 1 and head_dim width / 2:
+ * K and V of such a head are as many elements as one row. */
 int kv_cache_alloc(kv_alloc_t** out, int num_blocks, int num_kv_heads, int head_dim,
                    int block_size, int kv_dtype);
 
@@ -276,7 +284,9 @@ int kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
  * copy-on-write pairs reported by kv_step ("KV cache complete guide",
  * section "(4) PagedAttention": shared blocks are copy-on-write).  Ids
  * outside [0, num_blocks) are skipped and flag KV_DEVERR_BLOCK_OUT_OF_RANGE.
- * A dst that is also some src in the same call gives an unspecified result. */
+ * A dst that is also some src in the same call gives an unspecified result.
+ * v_cache may be NULL for a cache without a V of its own (a latent cache:
+ * num_kv_heads 1, head_dim its row's elements). */
 int kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int32_t* dst, int n,
                    int num_kv_heads, int head_dim, int num_blocks, int kv_dtype, void* stream);
 
@@ -656,7 +666,9 @@ int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32_t* out_tok
  * base + accept_nodes[s][i] go to position base + i (all KV heads), in place.
  *   k_caches, v_caches: host arrays of num_layers device pointers, the caches of
  *                  the layers, all of the same shape, dtype and block tables, no
- *                  two of them overlapping (else KV_ERR_INVALID_ARG)
+ *                  two of them overlapping (else KV_ERR_INVALID_ARG); v_caches may
+ *                  be NULL for caches without a V of their own (latent caches:
+ *                  num_kv_heads 1, head_dim their row's elements)
  *   accept_nodes:  [num_seqs][max_nodes] int32, strictly increasing over its first
  *                  accept_lens[s] entries, each less than n_s (as kv_tree_verify
  *                  leaves it); accept_lens: [num_seqs] int32
@@ -673,6 +685,141 @@ int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers
                     const int32_t* accept_nodes, const int32_t* accept_lens, int num_seqs,
                     int max_nodes, int num_kv_heads, int head_dim, int num_blocks, int kv_dtype,
                     void* stream);
+
+/* ------------------------------------------------ GPU: append with rotary positions */
+
+/* Rotary positions turn a vector by its token's position: with the pairs (a, b)
+ * of the vector's first rotary_dim elements,
+ *     (a, b) -> magnitude * (a cos t - b sin t, b cos t + a sin t),
+ *     t = position * inv_freq[i]   for pair i,
+ * and the elements behind rotary_dim stay as they are.  Pair i is elements i and
+ * i + rotary_dim / 2, or, with KV_ROTARY_INTERLEAVED, 2 i and 2 i + 1.  (The pages
+ * say that positions are part of the cached key, not how; these entry points are
+ * interfaces of this implementation.)  The angle is reduced by whole turns
+ * exactly, in integers: positions up to 2^31 lose nothing but the rounding of
+ * inv_freq, a float32, to 53 bits of a turn. */
+#define KV_ROTARY_INTERLEAVED 1u
+
+/* How kv_rotary_frequencies scales the frequencies f_i = theta^(-2 i / rotary_dim)
+ * for contexts longer than the model was trained on. */
+#define KV_ROTARY_PLAIN 0    /* f_i */
+#define KV_ROTARY_LINEAR 1   /* f_i / factor */
+#define KV_ROTARY_BASE 2     /* theta * factor^(rotary_dim / (rotary_dim - 2)) for theta */
+#define KV_ROTARY_PARTS 3    /* by parts, over pairs: f_i up to the pair that makes `high` turns
+                                over original_len (rounded down), f_i / factor from the one that
+                                makes `low` turns (rounded up), a linear blend between; the
+                                magnitude is 0.1 ln(factor) + 1 */
+#define KV_ROTARY_BANDS 4    /* by bands, over turns: with n_i = original_len f_i / 2 pi turns,
+                                f_i for n_i >= high, f_i / factor for n_i <= low, a blend
+                                linear in n_i between */
+
+/* Fill inv_freq[rotary_dim / 2] (host) with the frequencies and *magnitude (may be
+ * NULL) with the factor of the rotated values (1 but for KV_ROTARY_PARTS).
+ * rotary_dim even; theta > 0; factor >= 1 (not read for KV_ROTARY_PLAIN); low <
+ * high and original_len > 0 for PARTS and BANDS, not read otherwise.  Host only,
+ * in double. */
+int kv_rotary_frequencies(float* inv_freq, float* magnitude, int rotary_dim, double theta,
+                          int scaling, double factor, double low, double high,
+                          double original_len);
+
+/* kv_append with the rotation on the way: K is turned and appended, V appended,
+ * the queries turned into q_out (device pointers, or pinned host memory as for
+ * the decode entry points; the caches device memory):
+ *   q, q_out:      [num_tokens] rows of [num_q_heads][head_dim] bfloat16, the rows
+ *                  q_stride / q_out_stride elements apart; q_out may be q itself
+ *                  with the same stride (other overlaps are undefined);
+ *                  num_q_heads == 0: no queries (q, q_out NULL)
+ *   k, v:          rows of [num_kv_heads][head_dim] bfloat16, k_stride and v_stride
+ *                  elements apart (a projection's q, k and v side by side, say)
+ *   positions:     [num_tokens] int64
+ *   inv_freq:      [rotary_dim / 2] float32, finite
+ *   flags:         0 or KV_ROTARY_INTERLEAVED
+ * and slot_mapping, caches, kv_dtype and scales as kv_append; a token without a
+ * slot (slot < 0) has its query turned and appends nothing.  Rotation in float32,
+ * rounded once: to bfloat16, or K / k_scale to E4M3 (without a bfloat16 between).
+ * head_dim and rotary_dim multiples of 16; strides multiples of 8, at least a
+ * row.  One launch. */
+int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                     const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                     const int64_t* positions, const float* inv_freq, int rotary_dim,
+                     unsigned flags, float magnitude, int num_tokens, int num_q_heads,
+                     int num_kv_heads, int head_dim, int num_blocks, int kv_dtype, float k_scale,
+                     float v_scale, void* stream);
+
+/* ---------------------------------------------------------- GPU: latent caches */
+
+/* Latent attention keeps, instead of keys and values of every head, one vector a
+ * token that all query heads share: latent_dim elements from which a head's keys
+ * and values are linear maps, and rope_dim elements of a key that carries the
+ * position.  In the absorbed form those maps are applied to the queries and to the
+ * outputs, so that attention itself reads the cache as it is: the row is the key,
+ * its first latent_dim elements are the value.  (Interfaces of this
+ * implementation; the pages name the method only.)  A latent cache is, per layer,
+ * [num_blocks][16][latent_dim + rope_dim] bfloat16, under the same block tables,
+ * allocator and steps as the others (kv_step, kv_tree_step, kv_copy_blocks,
+ * kv_tree_verify, kv_tree_compact, kv_seq_truncate). */
+
+/* Append tokens to a latent cache: row = (norm(latent), turned key part), and turn the
+ * queries' rotary parts, in one launch (device pointers, or pinned host memory; the
+ * cache device memory):
+ *   latent, k_rope: rows of latent_dim and rope_dim bfloat16, latent_stride and
+ *                  k_rope_stride elements apart
+ *   norm_weight:   [latent_dim] bfloat16, or NULL for the latent as it is; norm(x) =
+ *                  x * norm_weight / sqrt(mean(x^2) + eps), in float32
+ *   q_rope, q_out: [num_tokens][num_q_heads] vectors of rope_dim bfloat16 by their
+ *                  strides, in elements; q_out, for example, the last rope_dim
+ *                  elements of paged_latent_attention's queries; may be q_rope itself
+ *                  with the same strides (other overlaps are undefined);
+ *                  num_q_heads == 0: none (NULL)
+ * and slot_mapping, positions, inv_freq [rope_dim / 2], flags and magnitude as
+ * kv_append_rotary (the whole of rope_dim is turned).  Every element is rounded
+ * once.  latent_dim a multiple of 8 up to 1024, rope_dim of 16 up to 512; strides
+ * multiples of 8, at least a vector (a token's at least its heads'). */
+int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                     const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+                     const void* latent, int64_t latent_stride, const void* k_rope,
+                     int64_t k_rope_stride, const void* norm_weight, float eps, void* cache,
+                     const int64_t* slot_mapping, const int64_t* positions,
+                     const float* inv_freq, unsigned flags, float magnitude, int num_tokens,
+                     int num_q_heads, int latent_dim, int rope_dim, int num_blocks,
+                     void* stream);
+
+/* Workspace bytes of paged_latent_attention for at most num_seqs sequences of at most
+ * max_nodes tokens on the current device: never less for a larger max_nodes.  As
+ * paged_decode's: no initialisation, nothing carried over, one per call in flight. */
+int paged_latent_workspace_bytes(int num_seqs, int max_nodes, int num_q_heads, int latent_dim,
+                                 int rope_dim, size_t* bytes);
+
+/* Attention over a latent cache in the absorbed form, for one token a sequence or a
+ * tree of drafted ones (device memory throughout but for the tables, which may be
+ * pinned host memory):
+ *   out:           [total_nodes][num_q_heads][latent_dim] bfloat16 (rows from
+ *                  node_starts[num_seqs] on are left as they were)
+ *   q:             [total_nodes][num_q_heads][latent_dim + rope_dim] bfloat16
+ *   cache:         [num_blocks][16][latent_dim + rope_dim] bfloat16
+ *   node_starts:   [num_seqs + 1] int32, or NULL: one token a sequence (total_nodes ==
+ *                  num_seqs, max_nodes 1)
+ *   parents:       [total_nodes] int32, or NULL: chains (node_starts NULL: not read)
+ *   context_lens:  [num_seqs] int32, cached tokens including the nodes
+ * For node i of sequence s, with c_j the cache's row at position j,
+ *     out[i][h] = sum_j softmax_j(scale * q[i][h] . c_j) c_j[0 .. latent_dim)
+ * over the positions that paged_tree_attention lets the node see, with its tables,
+ * their faults, and its rules for nodes that see nothing and for what is stored at
+ * positions a node does not see.  Scores, softmax (max, sum) and accumulators are
+ * float32; weights are multiplied as bfloat16, the sum being that of the rounded
+ * weights.  Deterministic as paged_decode_attention.
+ * Supported: latent_dim 256 or 512, rope_dim 32 or 64, num_q_heads up to 128
+ * (KV_ERR_UNSUPPORTED); max_nodes up to KV_TREE_MAX_NODES (KV_ERR_TOO_LARGE);
+ * total_nodes * num_q_heads and num_blocks * 16 below 2^31 - 256, and num_seqs *
+ * (row tiles of max_nodes * num_q_heads / 128) * (max_blocks_per_seq + 64) below 2^31
+ * (KV_ERR_UNSUPPORTED). */
+int paged_latent_attention(void* out, const void* q, const void* cache, int num_blocks,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* node_starts,
+                           const int32_t* parents, int num_seqs, int total_nodes, int max_nodes,
+                           int num_q_heads, int latent_dim, int rope_dim, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Read-only bandwidth ceiling (a measurement hook; the pages have no
  * counterpart): streams `bytes` of device memory at `buf` into shared memory

@@ -118,6 +118,16 @@ _SIGS = {
     "kv_tree_verify": (_i, [_p, _p, _p, _p, _i64, _p, _i64, _i, _p, _p, _p, _p, _p, _i, _i, _i,
                             _i, ctypes.c_uint, _p]),
     "kv_tree_compact": (_i, [_p, _p, _i, _p, _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
+    "kv_latent_bytes": (_i64, [_i, _i, _i64, _i, _i]),
+    "kv_rotary_frequencies": (_i, [_p, _p, _i, ctypes.c_double, _i, ctypes.c_double,
+                                   ctypes.c_double, ctypes.c_double, ctypes.c_double]),
+    "kv_append_rotary": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _i,
+                              ctypes.c_uint, _f, _i, _i, _i, _i, _i, _i, _f, _f, _p]),
+    "kv_latent_append": (_i, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _f, _p, _p,
+                              _p, _p, ctypes.c_uint, _f, _i, _i, _i, _i, _i, _p]),
+    "paged_latent_workspace_bytes": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "paged_latent_attention": (_i, [_p, _p, _p, _i, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i,
+                                    _f, _p, ctypes.c_size_t, _p]),
     "kv_read_ceiling": (_i, [_p, ctypes.c_size_t, _p, _p]),
     "kv_test_pipeline_stall": (_i, [ctypes.c_longlong]),
     "kv_get_device_error": (_i, [ctypes.POINTER(_i), ctypes.POINTER(_i64)]),
@@ -148,6 +158,9 @@ _HOT_KV_APPEND = _hot("kv_append")
 _HOT_TREE_ATTENTION = _hot("paged_tree_attention")
 _HOT_TREE_VERIFY = _hot("kv_tree_verify")
 _HOT_TREE_COMPACT = _hot("kv_tree_compact")
+_HOT_APPEND_ROTARY = _hot("kv_append_rotary")
+_HOT_LATENT_APPEND = _hot("kv_latent_append")
+_HOT_LATENT_ATTENTION = _hot("paged_latent_attention")
 
 
 def fast_path():
@@ -200,6 +213,17 @@ def _cache_dtype(t):
     raise ValueError("cache tensors must be bfloat16 or uint8 (E4M3 codes)")
 
 
+def _cache_shape(cache, latent):
+    """(blocks, KV heads, head dim) of a cache; a latent one ([NB, 16, W]) has one head."""
+    if latent:
+        NB, block, W = cache.shape
+        if block != BLOCK_SIZE:
+            raise ValueError("a latent cache must be [NB, 16, W]")
+        return NB, 1, W
+    NB, Hkv, _, D = cache.shape
+    return NB, Hkv, D
+
+
 # ------------------------------------------------------------------ sizing
 
 def kv_bytes(layers, batch, kv_heads, seq, head_dim, dtype_bytes):
@@ -207,6 +231,15 @@ def kv_bytes(layers, batch, kv_heads, seq, head_dim, dtype_bytes):
     r = _lib.kv_bytes(layers, batch, kv_heads, seq, head_dim, dtype_bytes)
     if r < 0:
         raise ValueError("kv_bytes: negative argument or overflow")
+    return r
+
+
+def latent_bytes(layers, batch, seq, width, dtype_bytes=2):
+    """layers x batch x seq x width x dtype_bytes: latent caches of rows of `width`
+    (latent_dim + rope_dim) elements (int)."""
+    r = _lib.kv_latent_bytes(layers, batch, seq, width, dtype_bytes)
+    if r < 0:
+        raise ValueError("kv_latent_bytes: negative argument or overflow")
     return r
 
 
@@ -386,9 +419,11 @@ def kv_append(k, v, k_cache, v_cache, slot_mapping, k_scale=1.0, v_scale=1.0, st
 
 
 def kv_copy_blocks(k_cache, v_cache, src, dst, stream=None):
-    """Copy whole blocks src[i] -> dst[i] (device int32 tensors)."""
-    NB, Hkv, _, D = k_cache.shape
-    _check(_lib.kv_copy_blocks(_dptr(k_cache), _dptr(v_cache), _dptr(src), _dptr(dst),
+    """Copy whole blocks src[i] -> dst[i] (device int32 tensors).  v_cache None:
+    k_cache is a latent cache ([NB, 16, W])."""
+    NB, Hkv, D = _cache_shape(k_cache, v_cache is None)
+    _check(_lib.kv_copy_blocks(_dptr(k_cache), _dptr(v_cache) if v_cache is not None else None,
+                               _dptr(src), _dptr(dst),
                                src.shape[0], Hkv, D, NB, _cache_dtype(k_cache),
                                _stream_ptr(stream)), "kv_copy_blocks")
 
@@ -729,25 +764,29 @@ def kv_tree_verify(accept_lens, accept_nodes, out_tokens, target_probs, tokens, 
 
 class CacheLayers:
     """The K and V caches of a model's layers, all of one shape, dtype and
-    device: what a program keeps to pass to kv_tree_compact."""
+    device: what a program keeps to pass to kv_tree_compact.  v_caches None:
+    latent caches ([NB, 16, W])."""
 
-    def __init__(self, k_caches, v_caches):
-        if not k_caches or len(k_caches) != len(v_caches):
+    def __init__(self, k_caches, v_caches=None):
+        latent = v_caches is None
+        if not k_caches or (not latent and len(k_caches) != len(v_caches)):
             raise ValueError("one K and one V cache per layer")
-        first = k_caches[0]
-        for t in list(k_caches) + list(v_caches):
+        first, vs = k_caches[0], [] if latent else list(v_caches)
+        for t in list(k_caches) + vs:
             if (t.shape != first.shape or t.dtype != first.dtype or t.device != first.device
-                    or not t.is_contiguous() or t.dim() != 4 or t.shape[2] != BLOCK_SIZE):
-                raise ValueError("caches must be contiguous [NB, Hkv, 16, D], all alike")
-        self.tensors = (list(k_caches), list(v_caches))     # keeps the memory alive
+                    or not t.is_contiguous() or t.dim() != (3 if latent else 4)
+                    or t.shape[-2] != BLOCK_SIZE):
+                raise ValueError("caches must be contiguous [NB, Hkv, 16, D] (latent caches: "
+                                 "[NB, 16, W]), all alike")
+        self.tensors = (list(k_caches), vs)                 # keeps the memory alive
         self.num_layers = len(k_caches)
-        self.num_blocks, self.num_kv_heads, _, self.head_dim = first.shape
+        self.num_blocks, self.num_kv_heads, self.head_dim = _cache_shape(first, latent)
         self.kv_dtype = _cache_dtype(first)
         self.first = first
         self._k = (_p * self.num_layers)(*[t.data_ptr() for t in k_caches])
-        self._v = (_p * self.num_layers)(*[t.data_ptr() for t in v_caches])
+        self._v = None if latent else (_p * self.num_layers)(*[t.data_ptr() for t in vs])
         self.k_ptrs = ctypes.addressof(self._k)
-        self.v_ptrs = ctypes.addressof(self._v)
+        self.v_ptrs = 0 if latent else ctypes.addressof(self._v)
 
 
 def kv_tree_compact(layers, block_tables, context_lens, node_starts, accept_nodes, accept_lens,
@@ -769,6 +808,163 @@ def kv_tree_compact(layers, block_tables, context_lens, node_starts, accept_node
         _ptr("accept_lens", accept_lens, i32, B, dev), B, max_nodes, layers.num_kv_heads,
         layers.head_dim, layers.num_blocks, layers.kv_dtype, _raw_stream(stream, dev)),
         "kv_tree_compact")
+
+
+# ------------------------------------------------ rotary positions, latent caches
+
+ROTARY_INTERLEAVED = 1      # KV_ROTARY_INTERLEAVED
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3, "bands": 4}      # KV_ROTARY_*
+
+
+def rotary_frequencies(rotary_dim, theta=10000.0, scaling="plain", factor=1.0, low=1.0, high=32.0,
+                       original_len=0.0):
+    """(inv_freq float32 numpy [rotary_dim / 2], magnitude) of rotary positions,
+    scaled for long contexts by `scaling` (kv_rotary_frequencies)."""
+    out = np.empty(max(int(rotary_dim), 0) // 2, dtype=np.float32)
+    mag = _f(1.0)
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROTARY_SCALINGS))
+    _check(_lib.kv_rotary_frequencies(_np_ptr(out), ctypes.byref(mag), int(rotary_dim),
+                                      float(theta), ROTARY_SCALINGS[scaling], float(factor),
+                                      float(low), float(high), float(original_len)),
+           "kv_rotary_frequencies")
+    return out, mag.value
+
+
+def _rows(name, t, dtype, shape, dev, inner=1):
+    """Address of a tensor of `shape` whose last `inner` dimensions are contiguous."""
+    if t.dtype is not dtype or tuple(t.shape) != shape or not (
+            t.get_device() == dev or (t.get_device() < 0 and t.is_pinned())):
+        raise ValueError("%s must be a %s tensor of shape %s on cuda:%d or in pinned host memory"
+                         % (name, dtype, shape, dev))
+    want = 1
+    for n, step in zip(reversed(shape[-inner:]), reversed(t.stride()[-inner:])):
+        if n > 1 and step != want:
+            raise ValueError("the last %d dimensions of %s must be contiguous" % (inner, name))
+        want *= n
+    return t.data_ptr()
+
+
+def _stride(t, dim, least):
+    """Stride of a dimension; of one of a single element, what an array would have."""
+    return t.stride(dim) if t.shape[dim] > 1 else max(least, t.stride(dim) // 8 * 8)
+
+
+def kv_append_rotary(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                     interleaved=False, magnitude=1.0, k_scale=1.0, v_scale=1.0, stream=None):
+    """kv_append with rotary positions on the way (kv_append_rotary): k [T, Hkv, D]
+    is turned and appended, v [T, Hkv, D] appended, q [T, Hq, D] turned into q_out
+    (which may be q; both None: no queries), all bfloat16, with any distance between
+    tokens (slices of one projection's output); slot_mapping and positions int64
+    [T]; inv_freq float32 [rotary_dim / 2], the first rotary_dim elements of a head
+    being turned."""
+    torch = _torch or _load_torch()
+    T, Hkv, D = k.shape
+    NB, H2, block, D2 = k_cache.shape
+    if (H2 != Hkv or D2 != D or block != BLOCK_SIZE or v_cache.shape != k_cache.shape
+            or v_cache.dtype is not k_cache.dtype or (q is None) != (q_out is None)):
+        raise ValueError("k and v must be [T, Hkv, D], k_cache and v_cache [NB, Hkv, 16, D], alike")
+    _device_only(k_cache, v_cache)
+    dev, bf16 = _place(k_cache), torch.bfloat16
+    Hq = q.shape[1] if q is not None else 0
+    qshape, kshape = (T, Hq, D), (T, Hkv, D)
+    _check(_HOT_APPEND_ROTARY(
+        _rows("q_out", q_out, bf16, qshape, dev, 2) if Hq else 0,
+        _stride(q_out, 0, Hq * D) if Hq else 0,
+        _rows("q", q, bf16, qshape, dev, 2) if Hq else 0, _stride(q, 0, Hq * D) if Hq else 0,
+        _rows("k", k, bf16, kshape, dev, 2), _stride(k, 0, Hkv * D),
+        _rows("v", v, bf16, kshape, dev, 2), _stride(v, 0, Hkv * D),
+        _ptr("k_cache", k_cache, k_cache.dtype, k_cache.numel(), dev),
+        _ptr("v_cache", v_cache, k_cache.dtype, k_cache.numel(), dev),
+        _ptr("slot_mapping", slot_mapping, torch.int64, T, dev),
+        _ptr("positions", positions, torch.int64, T, dev),
+        _ptr("inv_freq", inv_freq, torch.float32, inv_freq.numel(), dev), 2 * inv_freq.numel(),
+        ROTARY_INTERLEAVED if interleaved else 0, float(magnitude), T, Hq, Hkv, D, NB,
+        BF16 if k_cache.dtype is bf16 else _cache_dtype(k_cache), float(k_scale), float(v_scale),
+        _raw_stream(stream, dev)), "kv_append_rotary")
+
+
+def kv_latent_append(q_out, q_rope, latent, k_rope, cache, slot_mapping, positions, inv_freq,
+                     norm_weight=None, eps=1e-6, interleaved=False, magnitude=1.0, stream=None):
+    """Append rows to a latent cache [NB, 16, L + R] (kv_latent_append): latent
+    [T, L], normalised with norm_weight [L] if given, and k_rope [T, R], turned by
+    positions; the queries' rotary parts q_rope [T, H, R] are turned into q_out
+    [T, H, R] (a slice of the attention's queries, say; both None: no queries).
+    All bfloat16 with any distance between vectors; slot_mapping and positions
+    int64 [T], inv_freq float32 [R / 2]."""
+    torch = _torch or _load_torch()
+    T, L = latent.shape
+    R = k_rope.shape[1]
+    NB, _, W = _cache_shape(cache, True)
+    if W != L + R or cache.dtype is not torch.bfloat16 or (q_rope is None) != (q_out is None):
+        raise ValueError("cache must be bfloat16 [NB, 16, L + R]")
+    _device_only(cache)
+    dev, bf16 = _place(cache), torch.bfloat16
+    H = q_rope.shape[1] if q_rope is not None else 0
+    qs = []
+    for name, t in (("q_out", q_out), ("q_rope", q_rope)):
+        if not H:
+            qs += [0, 0, 0]
+            continue
+        p = _rows(name, t, bf16, (T, H, R), dev)
+        head = _stride(t, 1, R)
+        qs += [p, _stride(t, 0, (H - 1) * head + R), head]
+    _check(_HOT_LATENT_APPEND(
+        *qs, _rows("latent", latent, bf16, (T, L), dev), _stride(latent, 0, L),
+        _rows("k_rope", k_rope, bf16, (T, R), dev), _stride(k_rope, 0, R),
+        _ptr("norm_weight", norm_weight, bf16, L, dev) if norm_weight is not None else 0,
+        float(eps), _ptr("cache", cache, bf16, cache.numel(), dev),
+        _ptr("slot_mapping", slot_mapping, torch.int64, T, dev),
+        _ptr("positions", positions, torch.int64, T, dev),
+        _ptr("inv_freq", inv_freq, torch.float32, R // 2, dev),
+        ROTARY_INTERLEAVED if interleaved else 0, float(magnitude), T, H, L, R, NB,
+        _raw_stream(stream, dev)), "kv_latent_append")
+
+
+def latent_workspace_bytes(num_seqs, max_nodes, num_q_heads, latent_dim, rope_dim):
+    n = ctypes.c_size_t(0)
+    _check(_lib.paged_latent_workspace_bytes(num_seqs, max_nodes, num_q_heads, latent_dim,
+                                             rope_dim, ctypes.byref(n)),
+           "paged_latent_workspace_bytes")
+    return n.value
+
+
+def alloc_latent_workspace(num_seqs, max_nodes, num_q_heads, latent_dim, rope_dim, device=None):
+    import torch
+    nbytes = latent_workspace_bytes(num_seqs, max_nodes, num_q_heads, latent_dim, rope_dim)
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_latent_attention(out, q, cache, block_tables, context_lens, scale, workspace,
+                           node_starts=None, parents=None, max_nodes=1, stream=None):
+    """out [T, H, L] = attention of q [T, H, L + R] over a latent cache
+    [NB, 16, L + R], all bfloat16 (paged_latent_attention): keys are the cache's
+    rows, values their first L elements.  One token a sequence, or, with
+    node_starts int32 [B + 1], trees of up to max_nodes drafted tokens (parents
+    int32 [T], None: chains), as paged_tree_attention's; block_tables int32
+    [B, max_blocks], context_lens int32 [B] including the nodes; workspace from
+    alloc_latent_workspace."""
+    torch = _torch or _load_torch()
+    T, H, W = q.shape
+    L = out.shape[-1]
+    NB, _, W2 = _cache_shape(cache, True)
+    B, max_blocks = block_tables.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    if tuple(out.shape) != (T, H, L) or W2 != W or L >= W:
+        raise ValueError("q must be [T, H, L + R], out [T, H, L], cache [NB, 16, L + R]")
+    _device_only(out, q, cache, workspace)
+    dev = _place(cache)
+    _check(_HOT_LATENT_ATTENTION(
+        _ptr("out", out, bf16, out.numel(), dev), _ptr("q", q, bf16, q.numel(), dev),
+        _ptr("cache", cache, bf16, cache.numel(), dev), NB,
+        _ptr("block_tables", block_tables, i32, B * max_blocks, dev), max_blocks,
+        _ptr("context_lens", context_lens, i32, B, dev),
+        _ptr("node_starts", node_starts, i32, B + 1, dev) if node_starts is not None else 0,
+        _ptr("parents", parents, i32, T, dev) if parents is not None else 0, B, T, int(max_nodes),
+        H, L, W - L, float(scale), _ptr("workspace", workspace, workspace.dtype,
+                                        workspace.numel(), dev),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+        "paged_latent_attention")
 
 
 def read_ceiling(buf, sink, stream=None):

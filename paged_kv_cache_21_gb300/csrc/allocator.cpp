@@ -67,6 +67,16 @@ int64_t kv_bytes(int layers, int batch, int kv_heads, int64_t seq, int head_dim,
     return r;
 }
 
+int64_t kv_latent_bytes(int layers, int batch, int64_t seq, int width, int dtype_bytes)
+{
+    if (layers < 0 || batch < 0 || seq < 0 || width < 0 || dtype_bytes < 0) return -1;
+    int64_t r = 1;
+    const int64_t f[5] = {layers, batch, seq, width, dtype_bytes};
+    for (int64_t x : f)
+        if (__builtin_mul_overflow(r, x, &r)) return -1;
+    return r;
+}
+
 int kv_cache_alloc(kv_alloc_t** out, int num_blocks, int num_kv_heads, int head_dim,
                    int block_size, int kv_dtype)
 {

@@ -17,6 +17,8 @@ int decode_read_error(unsigned* flags, long long* detail);
 int tree_read_error(unsigned* flags, long long* detail);
 int verify_read_error(unsigned* flags, long long* detail);
 int compact_read_error(unsigned* flags, long long* detail);
+int rotary_read_error(unsigned* flags, long long* detail);
+int latent_read_error(unsigned* flags, long long* detail);
 
 // The decision of kv_prefix_plan for a given number of resident warps of the
 // split-KV kernel (host only; allocator.cpp).

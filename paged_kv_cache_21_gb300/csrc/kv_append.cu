@@ -64,16 +64,17 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint4* __restrict_
     }
 }
 
-// Copy whole (block, all heads) tiles: chunk space [tensor][pair][16-byte chunk].
+// Copy whole (block, all heads) tiles: chunk space [tensor][pair][16-byte chunk]
+// (`tensors` 1: K only).
 __global__ void __launch_bounds__(256) kv_copy_blocks_kernel(uint4* __restrict__ k_cache,
                                                              uint4* __restrict__ v_cache,
                                                              const int32_t* __restrict__ src,
                                                              const int32_t* __restrict__ dst,
                                                              int n, int chunks_per_block,
-                                                             int num_blocks)
+                                                             int num_blocks, int tensors)
 {
     const long long per_tensor = (long long)n * chunks_per_block;
-    const long long total = 2 * per_tensor;
+    const long long total = tensors * per_tensor;
     for (long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x; idx < total;
          idx += (long long)gridDim.x * blockDim.x) {
         const bool is_v = idx >= per_tensor;
@@ -139,18 +140,20 @@ extern "C" int kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src,
     if (n < 0 || num_kv_heads <= 0 || num_blocks <= 0 || head_dim <= 0) return KV_ERR_INVALID_ARG;
     if (kv_dtype != KV_DTYPE_BF16 && kv_dtype != KV_DTYPE_FP8_E4M3) return KV_ERR_UNSUPPORTED;
     if (n == 0) return KV_OK;
-    if (!k_cache || !v_cache || !src || !dst) return KV_ERR_INVALID_ARG;
+    if (!k_cache || !src || !dst) return KV_ERR_INVALID_ARG;
     if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15) return KV_ERR_INVALID_ARG;
     const long long block_bytes =
         (long long)num_kv_heads * kBlock * head_dim * (kv_dtype == KV_DTYPE_BF16 ? 2 : 1);
     if (block_bytes % 16) return KV_ERR_UNSUPPORTED;
     const int chunks_per_block = (int)(block_bytes / 16);
-    const long long total = 2LL * n * chunks_per_block;
+    const int tensors = v_cache ? 2 : 1;
+    const long long total = (long long)tensors * n * chunks_per_block;
     const int threads = 256;
     long long blocks = (total + threads - 1) / threads;
     const long long cap = (long long)num_sms_current() * 8;
     if (blocks > cap) blocks = cap;
     kv_copy_blocks_kernel<<<(unsigned)blocks, threads, 0, static_cast<cudaStream_t>(stream)>>>(
-        (uint4*)k_cache, (uint4*)v_cache, src, dst, n, chunks_per_block, num_blocks);
+        (uint4*)k_cache, (uint4*)v_cache, src, dst, n, chunks_per_block, num_blocks,
+        tensors);
     return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }

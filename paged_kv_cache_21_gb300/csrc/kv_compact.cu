@@ -41,7 +41,8 @@ struct CompactParams {
     int max_blocks, max_nodes, num_blocks;
     int Hkv;
     int chunks;                          // 16-byte chunks of one head's vector
-    int columns;                         // layers * 2 * Hkv * chunks
+    int tensors;                         // of a layer: K and V, or K alone
+    int columns;                         // layers * tensors * Hkv * chunks
 };
 
 __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
     for (int col = blockIdx.x * kThreads + tid; col < p.columns; col += gridDim.x * kThreads) {
         const int c = col % p.chunks, r = col / p.chunks;
         const int h = r % p.Hkv, lt = r / p.Hkv;
-        uint4* cache = p.cache[lt & 1][lt >> 1] + (size_t)h * kBlock * p.chunks + c;
+        uint4* cache = (p.tensors == 2 ? p.cache[lt & 1][lt >> 1] : p.cache[0][lt]) + (size_t)h * kBlock * p.chunks + c;
         for (int i0 = 0; i0 < moves; i0 += kBatch) {
             uint4 v[kBatch];
 #pragma unroll
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) kv_tree_compact_kernel(
 
 }  // namespace
 
-// Do any two of the caches (n of K, then n of V, of `bytes` each) overlap?
+// Do any two of the caches (n of K, then n of V unless `v` is null, of `bytes` each) overlap?
 // (All pairs: 2016 for 32 layers, in loops without branches.)
 static bool overlap(void* const* k, void* const* v, int n, uint64_t bytes)
 {
@@ -142,6 +143,7 @@ static bool overlap(void* const* k, void* const* v, int n, uint64_t bytes)
     };
     for (int i = 0; i < n; ++i) {
         among((uint64_t)k[i], k, i);
+        if (!v) continue;
         among((uint64_t)v[i], v, i);
         among((uint64_t)v[i], k, n);
     }
@@ -169,18 +171,19 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
     const long long row_bytes = (long long)head_dim * (kv_dtype == KV_DTYPE_BF16 ? 2 : 1);
     if (row_bytes % 16 != 0) return KV_ERR_UNSUPPORTED;
     if (num_layers == 0 || num_seqs == 0) return KV_OK;
-    if (!k_caches || !v_caches || !block_tables || !context_lens || !node_starts ||
+    if (!k_caches || !block_tables || !context_lens || !node_starts ||
         !accept_nodes || !accept_lens)
         return KV_ERR_INVALID_ARG;
     for (int l = 0; l < num_layers; ++l)
-        if (!k_caches[l] || !v_caches[l] ||
-            (((uintptr_t)k_caches[l] | (uintptr_t)v_caches[l]) & 15) != 0)
+        if (!k_caches[l] || ((uintptr_t)k_caches[l] & 15) != 0 ||
+            (v_caches && (!v_caches[l] || ((uintptr_t)v_caches[l] & 15) != 0)))
             return KV_ERR_INVALID_ARG;
     // (a move done twice could read what the first one has written)
     if (overlap(k_caches, v_caches, num_layers, (uint64_t)num_blocks * num_kv_heads * kBlock * row_bytes))
         return KV_ERR_INVALID_ARG;
     if (num_seqs > 65535) return KV_ERR_TOO_LARGE;      // one grid row per sequence
-    const long long per_layer = 2LL * num_kv_heads * (row_bytes / 16);
+    const int tensors = v_caches ? 2 : 1;
+    const long long per_layer = (long long)tensors * num_kv_heads * (row_bytes / 16);
     if (per_layer * kLayersPerLaunch > INT32_MAX / 2) return KV_ERR_UNSUPPORTED;
     CompactParams p;
     p.bt = block_tables;
@@ -193,12 +196,13 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
     p.num_blocks = num_blocks;
     p.Hkv = num_kv_heads;
     p.chunks = (int)(row_bytes / 16);
+    p.tensors = tensors;
     g_launched.note();
     for (int l0 = 0; l0 < num_layers; l0 += kLayersPerLaunch) {
         const int nl = num_layers - l0 < kLayersPerLaunch ? num_layers - l0 : kLayersPerLaunch;
         for (int l = 0; l < nl; ++l) {
             p.cache[0][l] = static_cast<uint4*>(k_caches[l0 + l]);
-            p.cache[1][l] = static_cast<uint4*>(v_caches[l0 + l]);
+            p.cache[1][l] = v_caches ? static_cast<uint4*>(v_caches[l0 + l]) : nullptr;
         }
         p.columns = (int)(per_layer * nl);
         // no more CTAs than run at once, so that the tables are looked up in one wave

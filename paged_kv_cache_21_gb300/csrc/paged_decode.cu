@@ -2218,7 +2218,8 @@ extern "C" int kv_get_device_error(int* flags, int64_t* detail)
     int (*const words[])(unsigned*, long long*) = {append_read_error, decode_read_error,
                                                    wide_read_error, tree_read_error,
                                                    tree_small_read_error, verify_read_error,
-                                                   compact_read_error};
+                                                   compact_read_error, rotary_read_error,
+                                                   latent_read_error};
     unsigned all = 0;
     long long first = -1;
     for (auto read : words) {
