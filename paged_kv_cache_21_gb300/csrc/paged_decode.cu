@@ -2025,6 +2025,8 @@ int cache_tensor_map(CUtensorMap* map, const void* base, int D, bool fp8, int nu
     return make_cache_map(map, base, D, fp8, num_blocks, Hkv);
 }
 
+int map_encoder(PFN_cuTensorMapEncodeTiled_v12000& fn) { return tensor_map_encoder(fn); }
+
 long long test_stall_cycles() { return g_test_stall.load(std::memory_order_relaxed); }
 
 int num_sms_current()

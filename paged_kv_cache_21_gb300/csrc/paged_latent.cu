@@ -3,144 +3,1096 @@
 //
 //     out[i][h] = sum_j softmax_j(scale * q[i][h] . c_j) c_j[0 .. L)
 //
-// One CTA per (node, head); its warps take the positions in turn, each with a running
-// maximum and sum, and are joined at the end.
+// Row r of a sequence's n * H rows is head r % H of node r / H.  A pair of CTAs (a
+// cluster of two SMs) takes a tile of 128 rows, 64 each, and goes over pages of the
+// context in chunks of 128 tokens (8 pages), with the products on the tensor cores of
+// both together (tcgen05.mma.cta_group::2, M = 128):
+//     S = Q K^T   (128 rows x 128 tokens; each CTA holds its 64 rows of Q and its 64
+//                 tokens of K),
+//     O += P V    (128 rows x L; each CTA holds its 64 rows of P and its half of V's
+//                 columns, 128 of each 256, over all 128 tokens).
+//
+// Why a pair: 128 rows x 512 columns of O in float32 fill one SM's tensor memory, with no
+// room for S, and 128 rows of Q (147 KB) with a chunk (147 KB) its shared memory.  Split
+// so, a CTA holds Q 74 KB, K 74 KB, V 66 KB, P 16 KB; O takes 256 of its 512 columns of
+// tensor memory, two buffers of S 128.  A tcgen05.mma takes 45 clocks at least (measured:
+// cta_group::2, M 128, K 16: N 64 45, N 128 47, N 256 65), so tokens come 128 at a time:
+// 36 products of N 128 and 16 of N 256, ~2700 clocks a chunk for both SMs, where HBM
+// brings a chunk's 147 KB to two SMs in ~3200 (6.7 TB/s, 152 SMs, 1.9 GHz).
+//
+// How:
+//  * Each byte of the cache is copied twice, as K to one CTA and as V to the other or the
+//    same one (L2 serves the second).  K goes by groups of four 64-element columns, with a
+//    barrier each, so that a group's room is filled again as soon as its products are done;
+//    V by halves of a chunk.
+//  * Warps: eight weigh (a thread per row, half of the chunk's tokens of a row's pair and 32
+//    of its columns), one copies Q and K, one V, one issues the MMAs (of the first CTA: for
+//    both), and one clears what must not be multiplied in V: rows behind the context, and
+//    infinities and NaN of drafted rows that some node does not see (0 * inf).
+//  * The scores of chunk c + 1 are computed while chunk c is weighed: S(c + 1), then O(c).
+//  * The reference maximum of a row moves only when a score is more than 2^8 above it; then,
+//    seldom, O's columns and the sums are scaled.
+//  * Pairs of CTAs get equal shares of all the (sequence, tile, page)s; a sequence's parts
+//    are joined by a second kernel.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 
+#include "cache_map.h"
 #include "device_common.cuh"
 #include "internal.h"
 #include "paged_kv.h"
 #include "tree_common.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 
-__device__ DevErr g_latent_err;
+static __device__ DevErr g_latent_err;
 static Launched g_launched;
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMaxL = 512;
+constexpr int kPages = 8;                       // pages of a chunk
+constexpr int kRows = 64;                       // rows of a CTA
+constexpr int kTile = 2 * kRows;                // rows of a pair
+constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
+constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
+constexpr int kMinPages = 16;                   // least range of a pair of CTAs
+constexpr int kExtraPages = 32;                 // what a (sequence, tile) costs beside its pages
+
+// misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
+// per pair, first sequence, tile and page
+enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_T0, M_J0, M_WORDS };
 
 struct LatentParams {
-    const uint16_t* q;
+    uint16_t* out;              // bf16 [total][H][L]
     const uint16_t* cache;
-    uint16_t* out;
     const int32_t* bt;
     const int32_t* ctx;
-    const int32_t* starts;
+    const int32_t* starts;      // or null: node s is sequence s
     const int32_t* parents;
-    int B, total, max_nodes, H, L, R, max_blocks, num_blocks;
+    float* part_o;              // [pairs][2][128][L]
+    float2* part_ml;            // [pairs][2][128]: (max in log2 units, sum)
+    int4* meta;                 // [pairs]: (sequence, tile, partials, rows)
+    int B, total, max_nodes, H, R, max_blocks, num_blocks;
+    int pairs;
+    uint32_t h_magic;           // ceil(2^32 / H), 0 for H == 1
     float sl2;
+    long long test_stall;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) paged_latent_kernel(const LatentParams p)
+template <int LAT>
+struct Geo {
+    static constexpr int kCols = LAT / 64;               // 64-element columns of the latent part
+    static constexpr int kGroups = kCols / 4;            // groups of K columns; the rotary part is one more
+    static constexpr int kHalves = LAT / 256;            // products of N 256 for a page
+    static constexpr int kSlots = LAT == 512 ? 1 : 2;    // chunks of K and of V in shared memory
+    static constexpr int kWeighWarps = 8, kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kFixWarp = 11;
+    static constexpr int kThreads = 12 * 32;
+    static constexpr int kQBytes = (kCols + 1) * kRows * 128;
+    static constexpr int kGroupBytes = kRows * 4 * 128;  // 64 tokens x 4 columns
+    static constexpr int kRopeBytes = kRows * 128;
+    static constexpr int kKSlot = kGroups * kGroupBytes + kRopeBytes;
+    static constexpr int kVPage = kHalves * 4096;        // [256-column block][2 columns][16 tokens][128 B]
+    static constexpr int kVSlot = kPages * kVPage;
+    static constexpr int kPBytes = 2 * kRows * 128;      // [64 tokens][64 rows][128 B]
+    static constexpr int kQOff = 0;
+    static constexpr int kKOff = kQOff + kQBytes;
+    static constexpr int kVOff = kKOff + kSlots * kKSlot;
+    static constexpr int kPOff = kVOff + kSlots * kVSlot;
+    static constexpr int kBarOff = kPOff + kPBytes;
+    // barriers; (L): the first CTA's is the one that counts
+    static constexpr int kG1 = kGroups + 1;
+    static constexpr int B_QFULL = 0;                            // (L) Q of both CTAs has landed
+    static constexpr int B_QFREE = B_QFULL + 1;                  // the segment's last scores are computed
+    static constexpr int B_KFULL = B_QFREE + 1;                  // (L) + slot * kG1 + group: K of both CTAs
+    static constexpr int B_KFREE = B_KFULL + kSlots * kG1;       // + slot * kG1 + group
+    static constexpr int B_VFULL = B_KFREE + kSlots * kG1;       // + slot * 2 + half of the chunk
+    static constexpr int B_VREADY = B_VFULL + kSlots * 2;        // (L) likewise: of both CTAs, cleared
+    static constexpr int B_VFREE = B_VREADY + kSlots * 2;        // likewise: its products are done
+    static constexpr int B_SFULL = B_VFREE + kSlots * 2;         // + buffer: scores
+    static constexpr int B_PFULL = B_SFULL + 2;                  // (L) weights of both CTAs
+    static constexpr int B_OFREE = B_PFULL + 1;                  // (L) both have read the accumulators
+    static constexpr int B_EPI = B_OFREE + 1;                    // + segment & 1: likewise, for the clearing warps
+    static constexpr int B_END = B_EPI + 2;
+    static constexpr int B_STALL = B_END + 1;                    // nothing arrives (the test hook)
+    static constexpr int kNumBars = B_STALL + 1;
+    static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kBadOff = kMiscOff + (M_WORDS * 4 + 15) / 16 * 16;      // [2][CTA of the pair][4] words
+    static constexpr int kRedOff = kBadOff + 64;                 // [4][64] floats: maxima, sums
+    static constexpr int kEnd = kRedOff + 4 * kRows * 4;
+    static constexpr int kSmem = kEnd;
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+    // tensor memory: two buffers of S, then O
+    static constexpr uint32_t kColO = 128, kTmemCols = kColO + kHalves * 128 <= 256 ? 256 : 512;
+};
+
+__device__ __forceinline__ float ex2(float x)
 {
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][kMaxL];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int node = blockIdx.x / p.H, h = blockIdx.x % p.H;
-    pdl_wait();
-    // the sequence of the node
-    int s = -1, t0 = 0, n = 0;
-    if (!p.starts) {
-        s = t0 = node;
-        n = 1;
-    } else {
-        for (int x = 0; x < p.B; ++x) {
-            int bad = 0;
-            if (!tree_span(p.starts, x, p.total, p.max_nodes, t0, n, bad)) {
-                if (blockIdx.x == 0 && tid == 0) raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, bad);
-                continue;
-            }
-            if (node >= t0 && node < t0 + n) {
-                s = x;
-                break;
-            }
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// a += the lower, b += the upper of two bf16.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x));
+}
+
+// ---------------------------------------------------------------- pairs of CTAs
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The same shared-memory address in CTA `rank` of the pair.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on a barrier of either CTA.  What the other CTA's threads or MMAs then rely on is in
+// this CTA's own shared and tensor memory, complete by the proxy fence and the tcgen05 waits
+// before; a release at cluster scope, which waits for all that the thread has under way, took
+// ~1400 clocks a chunk.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Stores to the other CTA's shared memory are performed before what follows.
+__device__ __forceinline__ void fence_cluster()
+{
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
+// Tiled copies whose bytes count on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t cluster_bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t cluster_bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(cluster_bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Arrive on this barrier of both CTAs when every MMA issued before has completed.
+__device__ __forceinline__ void commit2(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void give_up(volatile int* misc)
+{
+    misc[M_ABORT] = 1;
+    const uint32_t there = map_rank(smem_u32(const_cast<int*>(misc) + M_ABORT), cluster_rank() ^ 1u);
+    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(there) : "memory");
+    raise_flag(&g_latent_err, KV_DEVERR_PIPELINE_TIMEOUT, blockIdx.x);
+}
+
+// Bounded wait that also gives up when another role of the pair has given up.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* misc)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (misc[M_ABORT]) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            give_up(misc);
+            return false;
         }
     }
-    if (s < 0) return;
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* misc)
+{
+    return __all_sync(kFull, wait_bar(bar, parity, misc));
+}
+
+// ------------------------------------------------------------------------- work
+
+struct SeqInfo {
+    int t0, n, L, base, nb, tiles;      // nb: pages, tiles: of 128 rows; 0 without nodes or context
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const LatentParams& p, int s, bool flag)
+{
+    SeqInfo q;
+    int bad = 0;
+    if (!p.starts) {
+        q.t0 = s;
+        q.n = 1;
+    } else if (!tree_span(p.starts, s, p.total, p.max_nodes, q.t0, q.n, bad) && flag) {
+        raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, bad);
+    }
     int L = __ldg(p.ctx + s);
-    const int cap = p.max_blocks * kBlock, i = node - t0;
-    const bool flag = tid == 0 && h == 0 && i == 0;
+    const int cap = p.max_blocks * kBlock;
     if (L < 0 || L > cap) {
         if (flag) raise_flag(&g_latent_err, KV_DEVERR_CONTEXT_TOO_LONG, L);
         L = L < 0 ? 0 : cap;
     }
-    if (flag && L > 0 && L < n) raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, L);
-    const int base = L > n ? L - n : 0;
-    // the nodes that this one sees, as bits
-    uint32_t seen[4] = {0u, 0u, 0u, 0u};
-    const int32_t* parents = p.starts ? p.parents : nullptr;
-    bool pad = false;
-    for (int a = i; a >= 0;) {
-        const int up = tree_parent(parents, t0, a, h == 0 && tid == 0 ? &g_latent_err : nullptr);
-        if (up == KV_TREE_PAD) {
-            pad = a == i;
-            break;
+    if (flag && L > 0 && L < q.n) raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, L);
+    q.L = L;
+    q.base = L > q.n ? L - q.n : 0;
+    q.tiles = (q.n * p.H + kTile - 1) / kTile;
+    q.nb = q.n > 0 ? (L + kBlock - 1) / kBlock : 0;
+    return q;
+}
+
+// The segments of a pair's range: the pages [j, j + np) of one (sequence, tile) each.
+// Every role of both CTAs walks the same list.
+struct Walk {
+    int s, tile, j, rem, seg, np;
+    SeqInfo q;
+    __device__ __forceinline__ Walk(const LatentParams& p, const volatile int* misc)
+    {
+        s = misc[M_S0];
+        tile = misc[M_T0];
+        j = misc[M_J0];
+        rem = misc[M_CNT];
+        seg = 0;
+        np = 0;
+        if (rem > 0) {
+            q = seq_info(p, s, false);
+            np = min(q.nb - j, rem);
         }
-        seen[a >> 5] |= 1u << (a & 31);
-        a = up;
     }
-    const int W = p.L + p.R, pieces = W / 8;
-    const uint16_t* q = p.q + ((size_t)node * p.H + h) * W;
-    float x[3][8], o[3][8];
-    for (int k = 0; k < 3; ++k) {
-        for (int e = 0; e < 8; ++e) x[k][e] = o[k][e] = 0.f;
-        const int c = lane + 32 * k;
-        if (c < pieces)
-            for (int e = 0; e < 8; ++e) x[k][e] = __uint_as_float((uint32_t)q[c * 8 + e] << 16);
+    __device__ __forceinline__ bool more() const { return rem > 0; }
+    __device__ __forceinline__ int chunks() const { return (np + kPages - 1) / kPages; }
+    __device__ __forceinline__ int chunk_pages(int c) const { return min(kPages, np - c * kPages); }
+    // does chunk c reach the drafted positions, or the context's end?
+    __device__ __forceinline__ bool drafted(int c) const
+    {
+        return (j + c * kPages + chunk_pages(c)) * kBlock > q.base;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j = warp; j < L && !pad; j += kWarps) {
-        if (j >= base && !((seen[(j - base) >> 5] >> ((j - base) & 31)) & 1u)) continue;
-        const int blk = __ldg(p.bt + (size_t)s * p.max_blocks + j / kBlock);
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) raise_flag(&g_latent_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, blk);
-            continue;
+    __device__ __forceinline__ bool whole() const { return j == 0 && np == q.nb; }
+    __device__ __forceinline__ void next(const LatentParams& p)
+    {
+        rem -= np;
+        ++seg;
+        if (rem <= 0) return;
+        j = 0;
+        if (++tile == q.tiles) {
+            tile = 0;
+            do {
+                if (++s >= p.B) {
+                    rem = 0;
+                    return;
+                }
+                q = seq_info(p, s, false);
+            } while (q.nb == 0);
         }
-        const uint16_t* row = p.cache + ((size_t)blk * kBlock + j % kBlock) * W;
-        float v[3][8], dot = 0.f;
-        for (int k = 0; k < 3; ++k) {
-            const int c = lane + 32 * k;
-            for (int e = 0; e < 8; ++e) v[k][e] = c < pieces ? __uint_as_float((uint32_t)row[c * 8 + e] << 16) : 0.f;
-            if (c < pieces)
-                for (int e = 0; e < 8; ++e) dot += x[k][e] * v[k][e];
+        np = min(q.nb, rem);
+    }
+};
+
+// This pair's range of the list of pages, by sequence and tile: equal shares of at least
+// kMinPages units, where a page is a unit and each (sequence, tile) costs kExtraPages more
+// before its first page.  One warp.
+__device__ __forceinline__ void cut_work(const LatentParams& p, volatile int* misc, int pair, bool flag, int lane)
+{
+    long long total = 0;
+    for (int b = 0; b < p.B; b += 32) {
+        long long u = 0;
+        if (b + lane < p.B) {
+            const SeqInfo q = seq_info(p, b + lane, flag);
+            u = q.nb > 0 ? (long long)(q.nb + kExtraPages) * q.tiles : 0;
         }
-        for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
-        dot *= p.sl2;
-        const float top = fmaxf(m, dot);
-        const float a = m == -INFINITY ? 0.f : exp2f(m - top), w = dot == -INFINITY ? 0.f : exp2f(dot - top);
-        m = top;
-        l = l * a + (dot != dot ? dot : w);
-        for (int k = 0; k < 3; ++k)
-            for (int e = 0; e < 8; ++e) o[k][e] = o[k][e] * a + (dot != dot ? dot : w) * v[k][e];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
+        total += u;
     }
-    for (int k = 0; k < 3; ++k) {
-        const int c = lane + 32 * k;
-        if (c * 8 < p.L)
-            for (int e = 0; e < 8; ++e) s_o[warp][c * 8 + e] = o[k][e];
+    long long share = (total + p.pairs - 1) / p.pairs;
+    if (share < kMinPages) share = kMinPages;
+    // the first page at or behind unit x: its sequence, tile and index, its unit, and how
+    // many pages are before it
+    struct At {
+        int s, tile, j;
+        long long unit, pages;
+    };
+    const long long lo = min((long long)pair * share, total), hi = min(lo + share, total);
+    At at[2] = {{0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}};
+    bool found[2] = {false, false};
+    long long units = 0, pages = 0;              // up to the 32 sequences at hand
+    for (int b = 0; b < p.B && !(found[0] && found[1]); b += 32) {
+        int nb = 0, tiles = 0;
+        if (b + lane < p.B) {
+            const SeqInfo q = seq_info(p, b + lane, false);
+            nb = q.nb;
+            tiles = q.tiles;
+        }
+        const long long u = nb > 0 ? (long long)(nb + kExtraPages) * tiles : 0, n = (long long)nb * tiles;
+        long long iu = u, in = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
+            if (lane >= o) {
+                iu += tu;
+                in += tn;
+            }
+        }
+        iu += units;
+        in += pages;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long x = e == 0 ? lo : hi;
+            const unsigned m = __ballot_sync(kFull, iu > x);
+            if (found[e] || !m) continue;
+            found[e] = true;
+            const int src = __ffs(m) - 1;
+            const int nbs = __shfl_sync(kFull, nb, src), v = nbs + kExtraPages;
+            const long long before = __shfl_sync(kFull, iu - u, src);
+            const int off = (int)(x - before), t = off / v, j = max(0, off - t * v - kExtraPages);
+            at[e] = {b + src, t, j, before + (long long)t * v + kExtraPages + j,
+                     __shfl_sync(kFull, in - n, src) + (long long)t * nbs + j};
+        }
+        units = __shfl_sync(kFull, iu, 31);
+        pages = __shfl_sync(kFull, in, 31);
     }
+    if (!found[1]) at[1].pages = pages;          // (hi is the end of the list)
     if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
-    __syncthreads();
-    float M = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    for (int w = 0; w < kWarps; ++w) sum += s_m[w] == -INFINITY ? (s_l[w] != s_l[w] ? s_l[w] : 0.f) : s_l[w] * exp2f(s_m[w] - M);
-    bool any = !pad && base > 0;
-    for (int a = 0; a < n && !pad; ++a) any = any || (a < L && ((seen[a >> 5] >> (a & 31)) & 1u));
-    for (int d = tid; d < p.L; d += kWarps * 32) {
-        float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += s_m[w] == -INFINITY ? 0.f : s_o[w][d] * exp2f(s_m[w] - M);
-        v = sum != 0.f ? v / sum : any ? __uint_as_float(0x7fffffffu) : 0.f;
-        reinterpret_cast<__nv_bfloat16*>(p.out)[((size_t)node * p.H + h) * p.L + d] = __float2bfloat16_rn(v);
+        misc[M_B0] = (int)at[0].unit;
+        misc[M_CNT] = found[0] ? (int)(at[1].pages - at[0].pages) : 0;
+        misc[M_Q] = (int)share;
+        misc[M_S0] = at[0].s;
+        misc[M_T0] = at[0].tile;
+        misc[M_J0] = at[0].j;
     }
 }
+
+// Node (within the sequence) of row r of its rows.
+__device__ __forceinline__ int row_node(const LatentParams& p, int r)
+{
+    return p.h_magic ? (int)__umulhi((uint32_t)r, p.h_magic) : r;
+}
+
+// The nodes that node i sees, as bits; false for a padding node.
+__device__ __forceinline__ bool seen_nodes(const LatentParams& p, int t0, int i, DevErr* e, uint32_t (&m)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = 0u;
+    if (!p.starts || !p.parents) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = i >= 32 * k + 31 ? ~0u : i >= 32 * k ? (2u << (i - 32 * k)) - 1u : 0u;
+        return true;
+    }
+    for (int a = i; a >= 0;) {
+        const int up = tree_parent(p.parents, t0, a, e);
+        if (up == KV_TREE_PAD) return a != i;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] |= (a >> 5) == k ? 1u << (a & 31) : 0u;
+        a = up;
+    }
+    return true;
+}
+
+// Bits [at, at + 32) of a string of 128, zero outside it.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t (&m)[4], int at)
+{
+    if (at <= -32 || at >= 128) return 0u;
+    auto word = [&](int k) { return k == 0 ? m[0] : k == 1 ? m[1] : k == 2 ? m[2] : k == 3 ? m[3] : 0u; };
+    if (at < 0) return m[0] << -at;
+    return __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// ------------------------------------------------------------------------ kernel
+
+template <int LAT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<LAT>::kThreads, 1)
+paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+                    const __grid_constant__ CUtensorMap tm_v, const LatentParams p)
+{
+    using G = Geo<LAT>;
+    extern __shared__ __align__(1024) uint8_t gb[];
+    const uint32_t sb = smem_u32(gb);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    volatile int* misc = reinterpret_cast<volatile int*>(gb + G::kMiscOff);
+    // (the swizzle wants the base that the launch gives where there is no static shared memory)
+    if (sb & 1023u) {
+        if (tid == 0) raise_flag(&g_latent_err, KV_DEVERR_PIPELINE_TIMEOUT, sb);
+        return;
+    }
+    auto bar = [&](int i) -> uint32_t { return sb + (uint32_t)(G::kBarOff + 8 * i); };
+    auto lead = [&](int i) -> uint32_t { return map_rank(bar(i), 0u); };
+    // chunk g: its slot and the parity of its pass
+    auto slot = [](int g) -> int { return (int)((uint32_t)g % G::kSlots); };
+    auto pass = [](int g) -> uint32_t { return (uint32_t)g / G::kSlots & 1u; };
+    // its products are done
+    auto done = [&](int g) -> uint32_t { return bar(G::B_VFREE + slot(g) * 2 + 1); };
+
+    if (tid == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        mbar_init(bar(G::B_QFULL), 1);
+        mbar_init(bar(G::B_QFREE), 1);
+        for (int i = 0; i < G::kSlots * G::kG1; ++i) {
+            mbar_init(bar(G::B_KFULL + i), 1);
+            mbar_init(bar(G::B_KFREE + i), 1);
+        }
+        for (int i = 0; i < G::kSlots * 2; ++i) {
+            mbar_init(bar(G::B_VFULL + i), 1);
+            mbar_init(bar(G::B_VREADY + i), 2);
+            mbar_init(bar(G::B_VFREE + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(G::B_SFULL + i), 1);
+            mbar_init(bar(G::B_EPI + i), 2 * G::kWeighWarps);
+        }
+        mbar_init(bar(G::B_PFULL), 2 * G::kWeighWarps);
+        mbar_init(bar(G::B_OFREE), 2 * G::kWeighWarps);
+        mbar_init(bar(G::B_END), 1);
+        mbar_init(bar(G::B_STALL), 1);
+        misc[M_ABORT] = 0;
+        fence_mbar_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == G::kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         sb + G::kMiscOff + 4 * M_TMEM),
+                     "r"(G::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == G::kKWarp) cut_work(p, misc, pair, blockIdx.x == 0, lane);
+    umma::fence_before_sync();
+    __syncthreads();
+    cluster_sync();                      // the barriers of both CTAs are there
+    umma::fence_after_sync();
+    const uint32_t tmem = (uint32_t)misc[M_TMEM];
+
+    if (warp == G::kKWarp) {
+        // ------------------------------------------------------------- Q and K
+        int g = 0;
+        bool ok = true;
+        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+            if (w.seg > 0) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((w.seg - 1) & 1), misc);
+            if (!ok) break;
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive_expect_tx(bar(G::B_QFULL), 2u * G::kQBytes);
+                const int row = w.q.t0 * p.H + w.tile * kTile + (int)rank * kRows;
+                const uint32_t qf = lead(G::B_QFULL);
+#pragma unroll
+                for (int k = 0; k < G::kGroups; ++k)
+                    tma2_load_3d(sb + (uint32_t)(G::kQOff + k * 4 * kRows * 128), &tm_q, 0, row, 4 * k, qf);
+                tma2_load_2d(sb + (uint32_t)(G::kQOff + G::kCols * kRows * 128), &tm_qr, LAT, row, qf);
+            }
+            const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
+            const int nc = w.chunks();
+            int ids = lane < w.np ? __ldg(row + lane) : -1;           // pages 0..31 of the segment
+            int ahead = 32 + lane < w.np ? __ldg(row + 32 + lane) : -1;
+            for (int c = 0; ok && c < nc; ++c, ++g) {
+                if (c > 0 && (c & 3) == 0) {
+                    ids = ahead;
+                    const int at = (c + 4) * kPages + lane;
+                    ahead = at < w.np ? __ldg(row + at) : -1;
+                }
+                // lanes 0..7: the chunk's pages; this CTA's four go by 8 token rows
+                const int id8 = __shfl_sync(kFull, ids, (c & 3) * kPages + (lane & 7));
+                const bool in = lane < w.chunk_pages(c) && lane < kPages;
+                const bool valid = in && id8 >= 0 && id8 < p.num_blocks;
+                if (in && !valid && rank == 0) raise_flag(&g_latent_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, id8);
+                const unsigned all = __ballot_sync(kFull, valid);
+                const int mypage = 4 * (int)rank + ((lane & 7) >> 1);
+                const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + mypage);
+                const bool mine = lane < 8 && ((all >> mypage) & 1u);
+                const int n = __popc(all), sl = slot(g);
+#pragma unroll
+                for (int k = 0; k <= G::kGroups; ++k) {
+                    const int b = sl * G::kG1 + k;
+                    if (g >= G::kSlots && !wait_warp(bar(G::B_KFREE + b), pass(g) ^ 1u, misc)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool rope = k == G::kGroups;
+                    if (lane == 0 && rank == 0) {
+                        if (n > 0) mbar_arrive_expect_tx(bar(G::B_KFULL + b), (uint32_t)(n * (rope ? 2048 : 8192)));
+                        else mbar_arrive(bar(G::B_KFULL + b));
+                    }
+                    __syncwarp();
+                    const uint32_t kb = sb + (uint32_t)(G::kKOff + sl * G::kKSlot);
+                    const uint32_t kf = lead(G::B_KFULL + b);
+                    if (!rope) {
+                        if (mine)
+                            tma2_load_3d(kb + (uint32_t)(k * G::kGroupBytes + lane * 4096), &tm_k, 0,
+                                         id * kBlock + 8 * (lane & 1), 4 * k, kf);
+                    } else if (mine && !(lane & 1)) {
+                        tma2_load_2d(kb + (uint32_t)(G::kGroups * G::kGroupBytes + (lane >> 1) * 2048), &tm_kr, LAT,
+                                     id * kBlock, kf);
+                    }
+                }
+            }
+        }
+        // every copy lands before the pair can end: those of a pair that ran to its end were
+        // all waited for by the MMA warp; one that gave up leaves them time
+        if (!ok) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < 400000) __nanosleep(1000);
+        }
+        __syncwarp();
+    } else if (warp == G::kVWarp) {
+        // ------------------------------------------------------------------- V
+        int g = 0;
+        bool ok = true;
+        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+            const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
+            const int nc = w.chunks();
+            int ids = lane < w.np ? __ldg(row + lane) : -1;
+            int ahead = 32 + lane < w.np ? __ldg(row + 32 + lane) : -1;
+            for (int c = 0; ok && c < nc; ++c, ++g) {
+                if (c > 0 && (c & 3) == 0) {
+                    ids = ahead;
+                    const int at = (c + 4) * kPages + lane;
+                    ahead = at < w.np ? __ldg(row + at) : -1;
+                }
+                const int sl = slot(g);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // lanes 0 .. 4 * halves - 1: page and 256-column block
+                    const int page = 4 * h + lane / G::kHalves % 4, t = lane % G::kHalves;
+                    const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + page);
+                    const bool mine = lane < 4 * G::kHalves && page < w.chunk_pages(c) && id >= 0 && id < p.num_blocks;
+                    const int n = __popc(__ballot_sync(kFull, mine));
+                    const int b = sl * 2 + h;
+                    if (g >= G::kSlots && !wait_warp(bar(G::B_VFREE + b), pass(g) ^ 1u, misc)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (n > 0) mbar_arrive_expect_tx(bar(G::B_VFULL + b), (uint32_t)(n * 4096));
+                        else mbar_arrive(bar(G::B_VFULL + b));
+                    }
+                    __syncwarp();
+                    if (mine)
+                        tma_load_3d(sb + (uint32_t)(G::kVOff + sl * G::kVSlot + page * G::kVPage + t * 4096), &tm_v, 0,
+                                    id * kBlock, 4 * t + 2 * (int)rank, bar(G::B_VFULL + b));
+                }
+            }
+        }
+        if (!ok) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < 400000) __nanosleep(1000);
+        }
+        __syncwarp();
+    } else if (warp == G::kMmaWarp) {
+        // -------------------------------------------------------------- products
+        if (rank == 0 && lane == 0) {
+            const uint64_t qdesc = umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
+            const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kKOff, 16, 4096);
+            const uint64_t rdesc = umma::smem_desc_sw128(sb + G::kKOff + G::kGroups * G::kGroupBytes, 16, 1024);
+            const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, 16, 1024);
+            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, 2048, 1024);
+            constexpr uint32_t idesc_s = umma::idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t idesc_o = umma::idesc_bf16_f32(128, 256, false, true);
+            bool ok = true;
+            if (p.test_stall > 0 && misc[M_CNT] > 0 && !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
+                give_up(misc);
+                ok = false;
+            }
+            auto scores = [&](int g) -> bool {
+                const int sl = slot(g);
+                const uint32_t d = tmem + (uint32_t)(64 * (g & 1));
+                const uint64_t ks = (uint64_t)((sl * G::kKSlot) >> 4);
+#pragma unroll
+                for (int k = 0; k <= G::kGroups; ++k) {
+                    const int b = sl * G::kG1 + k;
+                    if (!wait_bar(bar(G::B_KFULL + b), pass(g), misc)) return false;
+                    umma::fence_after_sync();
+                    if (k < G::kGroups) {
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk)
+                            mma2(d, qdesc + (uint64_t)(((k * 4 + (kk >> 2)) * kRows * 128 + (kk & 3) * 32) >> 4),
+                                 kdesc + ks + (uint64_t)((k * G::kGroupBytes + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                                 idesc_s, k + kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma2(d, qdesc + (uint64_t)((G::kCols * kRows * 128 + kk * 32) >> 4),
+                                 rdesc + ks + (uint64_t)((kk * 32) >> 4), idesc_s, true);
+                    }
+                    commit2(bar(G::B_KFREE + b));
+                }
+                commit2(bar(G::B_SFULL + (g & 1)));
+                return true;
+            };
+            // the products of chunk g, the segment's chunk c of np pages
+            auto products = [&](int g, int c, int np) -> bool {
+                const int sl = slot(g);
+                if (!wait_bar(bar(G::B_PFULL), (uint32_t)(g & 1), misc)) return false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int b = sl * 2 + h;
+                    if (!wait_bar(bar(G::B_VREADY + b), pass(g), misc)) return false;
+                    umma::fence_after_sync();
+                    const int to = min(np, 4 * h + 4);
+                    for (int k = 4 * h; k < to; ++k)
+#pragma unroll
+                        for (int t = 0; t < G::kHalves; ++t)
+                            mma2(tmem + G::kColO + (uint32_t)(128 * t),
+                                 pdesc + (uint64_t)(((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
+                                 vdesc + (uint64_t)((sl * G::kVSlot + k * G::kVPage + t * 4096) >> 4), idesc_o,
+                                 c + k > 0);
+                    commit2(bar(G::B_VFREE + b));
+                }
+                return true;
+            };
+            int g = 0;
+            for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+                const int nc = w.chunks();
+                ok = wait_bar(bar(G::B_QFULL), (uint32_t)(w.seg & 1), misc);
+                for (int c = 0; ok && c < nc; ++c) {
+                    ok = scores(g + c);
+                    if (!ok) break;
+                    if (c + 1 == nc) commit2(bar(G::B_QFREE));
+                    // the accumulators of the segment before have been read
+                    if (c == 1 || (nc == 1 && c == 0))
+                        ok = w.seg == 0 || wait_bar(bar(G::B_OFREE), (uint32_t)((w.seg - 1) & 1), misc);
+                    if (ok && c > 0) ok = products(g + c - 1, c - 1, kPages);
+                }
+                ok = ok && products(g + nc - 1, nc - 1, w.chunk_pages(nc - 1));
+                g += nc;
+            }
+            // every MMA issued by this thread is complete before the pair ends
+            commit2(bar(G::B_END));
+            mbar_wait_bounded(bar(G::B_END), 0u, kWaitLimit);
+        }
+        __syncwarp();
+    } else if (warp == G::kFixWarp) {
+        // -------------------------------------- V rows that must not be multiplied
+        int g = 0;
+        bool ok = true;
+        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+            const int nc = w.chunks(), buf = w.seg & 1;
+            if (w.seg >= 2) ok = wait_warp(bar(G::B_EPI + buf), (uint32_t)(((w.seg - 2) >> 1) & 1), misc);
+            if (!ok) break;
+            uint32_t bad[4] = {0u, 0u, 0u, 0u};          // drafted rows where something was cleared
+            for (int c = 0; ok && c < nc; ++c, ++g) {
+                const int sl = slot(g), p0 = (w.j + c * kPages) * kBlock;
+                for (int h = 0; ok && h < 2; ++h) {
+                    const int b = sl * 2 + h;
+                    ok = wait_warp(bar(G::B_VFULL + b), pass(g), misc);
+                    if (!ok) break;
+                    if (w.drafted(c)) {
+                        const int lo = max(64 * h, w.q.base - p0), hi = min(64 * (h + 1), w.chunk_pages(c) * kBlock);
+                        // a row's 16-byte pieces, 16 of each 256-column block
+                        for (int r = lo; r < hi; ++r) {
+                            const bool tail = p0 + r >= w.q.L;
+                            for (int x = lane; x < 16 * G::kHalves; x += 32) {
+                                const int t = x >> 4, col = (x >> 3) & 1, ch = x & 7, rr = r & 15;
+                                const uint32_t at = sb + (uint32_t)(G::kVOff + sl * G::kVSlot + (r >> 4) * G::kVPage +
+                                                                    t * 4096 + col * 2048 + rr * 128 + ((ch ^ (rr & 7)) * 16));
+                                uint32_t v[4] = {0u, 0u, 0u, 0u}, any = 0u;
+                                if (!tail) {
+                                    lds128(v, at);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const uint32_t m = __vcmpeq2(v[k] & 0x7f807f80u, 0x7f807f80u);
+                                        v[k] &= ~m;
+                                        any |= m;
+                                    }
+                                }
+                                if (tail || any) sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
+                                const int a = p0 + r - w.q.base;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) bad[k] |= any && (a >> 5) == k ? 1u << (a & 31) : 0u;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        // both CTAs' rows have all columns, so both are told
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            bad[k] = __reduce_or_sync(kFull, bad[k]);
+                            if (lane < 2) {
+                                const uint32_t at = sb + (uint32_t)(G::kBadOff + ((buf * 2 + (int)rank) * 4 + k) * 4);
+                                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)lane)),
+                                             "r"(bad[k])
+                                             : "memory");
+                            }
+                        }
+                        fence_cluster();
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(lead(G::B_VREADY + b));
+                }
+            }
+        }
+    } else {
+        // --------------------------------------------------- weights and output
+        const int wq = warp & 3, wg = warp >> 2;
+        const int row = (wq & 1) * 32 + lane;    // of the CTA's 64
+        const int kh = wq >> 1;                  // half of the chunk's tokens, and of an O block's columns
+        const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+        float* red = reinterpret_cast<float*>(gb + G::kRedOff);
+        const volatile uint32_t* badw = reinterpret_cast<const volatile uint32_t*>(gb + G::kBadOff);
+        // sequences without a context: zeros for their nodes
+        for (int s = blockIdx.x; s < p.B; s += gridDim.x) {
+            const SeqInfo q = seq_info(p, s, false);
+            if (q.L > 0 || q.n == 0) continue;
+            uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)q.t0 * p.H * LAT);
+            for (size_t i = tid; i < (size_t)q.n * p.H * LAT / 8; i += G::kWeighWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (rank == 0 && tid == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
+        int g0 = 0, flat = misc[M_B0];
+        bool ok = true;
+        // The CTA's eight warps meet: is `x` true anywhere?  Every warp comes to every
+        // meeting, also one whose waits have run out, which the others learn there.
+        auto meet = [&](bool x) -> bool {
+            int r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"(x ? 1 : 0)
+                : "memory");
+            return r != 0;
+        };
+        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+            const int seg = w.seg, buf = seg & 1, nc = w.chunks(), rows = w.q.n * p.H;
+            const int r = w.tile * kTile + (int)rank * kRows + row;       // of the sequence's rows
+            uint32_t seen[4];
+            bool live = r < rows;
+            {
+                const int i = live ? row_node(p, r) : 0;
+                // (a node's entry is read by the thread of its first head here, for one flag)
+                live = seen_nodes(p, w.q.t0, i, w.j == 0 && live ? &g_latent_err : nullptr, seen) && live;
+            }
+            const bool warp_live = __any_sync(kFull, live);
+            const bool cta_live = w.tile * kTile + (int)rank * kRows < rows;
+            float ref = -INFINITY, nref = live ? 0.f : -INFINITY, l[4] = {0.f, 0.f, 0.f, 0.f};
+            bool pending = true;                 // a row has no reference yet
+            for (int c = 0; c < nc; ++c) {
+                const int g = g0 + c;
+                ok = __all_sync(kFull, ok && wait_bar(bar(G::B_SFULL + (g & 1)), (uint32_t)((g >> 1) & 1), misc));
+                umma::fence_after_sync();
+                if (!cta_live) {                 // nothing here weighs anything
+                    // (an arrival before the last chunk's weights are used would count for them)
+                    if (g > 0) ok = __all_sync(kFull, ok && wait_bar(done(g - 1), pass(g - 1), misc));
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (ok && lane == 0) arrive_remote(lead(G::B_PFULL));
+                    continue;
+                }
+                float t[32];
+                uint32_t vis = ~0u;
+                const int np = w.chunk_pages(c), k0 = kh * 64 + wg * 32;  // this thread's first token
+                const bool masked = w.drafted(c) || np < kPages;
+                float most = -INFINITY;
+                if (warp_live) {
+                    umma::tmem_ld32(lanes + (uint32_t)(64 * (g & 1) + 32 * wg), *reinterpret_cast<uint32_t(*)[32]>(&t[0]));
+                    umma::tmem_wait_ld();
+                    // (the product rounded before the sum: the reference is such a product, and a
+                    // fused remainder would grow with it)
+                    const u64 f = pack2(p.sl2, p.sl2);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) unpack2(mul2(pack2(t[k], t[k + 1]), f), t[k], t[k + 1]);
+                    if (masked) {
+                        const int pos = (w.j + c * kPages) * kBlock + k0;
+                        vis = (low_bits(w.q.base - pos) | bits_at(seen, pos - w.q.base)) & low_bits(min(w.q.L - pos, np * kBlock - k0));
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) t[k] = (vis >> k) & 1u ? t[k] : -INFINITY;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], t[k], t[k + 1]);
+                    most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) + nref;
+                }
+                // does any row's reference lag too far behind, or has a wait run out?
+                if (meet(!ok || most > kMaxLag || pending)) {
+                    if (meet(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    // ---- new references: the largest score of each row in the chunk
+                    float top = -INFINITY;
+                    if (warp_live) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) top = max_nan(top, t[k]);
+                    }
+                    red[(wg * 2 + kh) * kRows + row] = top;
+                    meet(false);
+                    top = max_nan(max_nan(red[row], red[kRows + row]), max_nan(red[2 * kRows + row], red[3 * kRows + row]));
+                    // a row whose first scores hold NaN is NaN whatever its reference: 0
+                    if (ref == -INFINITY && top != top) top = 0.f;
+                    float a = 1.f;
+                    if (live && (ref == -INFINITY ? top > -INFINITY : top > ref + kMaxLag)) {
+                        a = ref == -INFINITY ? 0.f : ex2(ref - top);
+                        ref = top;
+                        nref = -top;
+                    }
+                    // what has been accumulated follows, once the products under way are done
+                    const bool moved = meet(a != 1.f) && c > 0;
+                    if (moved) ok = wait_warp(done(g - 1), pass(g - 1), misc);
+                    pending = meet(live && ref == -INFINITY);
+                    if (meet(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (moved) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) l[k] *= a;
+                        umma::fence_after_sync();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < G::kHalves * 64; c0 += 16) {
+                            const uint32_t at = lanes + G::kColO + (uint32_t)(wg * G::kHalves * 64 + c0);
+                            uint32_t o[16];
+                            umma::tmem_ld16(at, o);
+                            umma::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                            umma::tmem_st16(at, o);
+                        }
+                        umma::tmem_wait_st();
+                    }
+                }
+                // ---- the weights
+                uint32_t hi[16];
+                if (warp_live) {
+                    const u64 n2 = pack2(nref, nref);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float a, b;
+                        unpack2(add2(pack2(t[k], t[k + 1]), n2), a, b);
+                        hi[k / 2] = pack_bf16x2(ex2(a), ex2(b));
+                        add_bf16x2(l[k & 2], l[(k & 2) + 1], hi[k / 2]);
+                    }
+                }
+                // the buffer of P: the products of the chunk before are done.  (A wait that
+                // runs out is told at the next meeting; nothing is written then.)
+                if (g > 0) ok = __all_sync(kFull, ok && wait_bar(done(g - 1), pass(g - 1), misc));
+                if (ok && warp_live) {
+                    const uint32_t pb = sb + (uint32_t)(G::kPOff + kh * kRows * 128 + row * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts128(pb + (uint32_t)(((wg * 4 + k) ^ (row & 7)) * 16),
+                               make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]));
+                }
+                fence_proxy_async_smem();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (ok && lane == 0) arrive_remote(lead(G::B_PFULL));
+            }
+            // the warps go on together, or not at all
+            if (meet(!ok)) ok = false;
+            if (!ok) break;
+            // ---- the segment's result
+            ok = wait_warp(done(g0 + nc - 1), pass(g0 + nc - 1), misc);
+            umma::fence_after_sync();
+            red[(wg * 2 + kh) * kRows + row] = (l[0] + l[1]) + (l[2] + l[3]);
+            if (meet(!ok)) ok = false;
+            if (!ok) break;
+            const float sum = (red[row] + red[kRows + row]) + (red[2 * kRows + row] + red[3 * kRows + row]);
+            const bool whole = w.whole(), in = r < rows;
+            const size_t prow = ((size_t)pair * 2 + (w.j == 0 ? 1 : 0)) * kTile + rank * kRows + row;
+            float z = 1.f;
+            if (whole) {
+                bool any = w.q.base > 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) any = any || (seen[k] & low_bits(w.q.L - 32 * k)) != 0u;
+                // (a row that sees something and weighs nothing had scores of -inf alone)
+                z = live && sum != 0.f ? 1.f / sum : live && any ? __uint_as_float(0x7fffffffu) : 0.f;
+            } else if (in && wg == 0 && kh == 0) {
+                p.part_ml[prow] = make_float2(live ? ref : -INFINITY, live ? sum : 0.f);
+            }
+            // drafted elements that were cleared as infinities or NaN
+            uint32_t back = 0u;
+            if (w.drafted(nc - 1)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) back |= badw[buf * 8 + k];
+            }
+            if (__any_sync(kFull, in)) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < G::kHalves * 64; c0 += 16) {
+                    const int col = wg * G::kHalves * 64 + c0;            // of O's columns here
+                    const int d = (col >> 7) * 256 + kh * 128 + (col & 127);
+                    uint32_t o[16];
+                    umma::tmem_ld16(lanes + G::kColO + (uint32_t)col, o);
+                    umma::tmem_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = live ? __uint_as_float(o[k]) * z : 0.f;
+                    if (back && live) {
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            uint32_t b = (badw[buf * 8 + k4] | badw[buf * 8 + 4 + k4]) & bits_at(seen, 32 * k4);
+                            for (; b != 0u; b &= b - 1u) {
+                                const int pos = w.q.base + 32 * k4 + __ffs(b) - 1;
+                                const int blk = __ldg(p.bt + (size_t)w.s * p.max_blocks + pos / kBlock);
+                                if (blk < 0 || blk >= p.num_blocks) continue;
+                                const uint16_t* src = p.cache + ((size_t)blk * kBlock + pos % kBlock) * (LAT + p.R) + d;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if ((__ldg(src + k) & 0x7f80u) == 0x7f80u) v[k] = __uint_as_float(0x7fffffffu);
+                            }
+                        }
+                    }
+                    if (!in) continue;
+                    if (whole) {
+                        uint16_t* dst = p.out + ((size_t)w.q.t0 * p.H + r) * LAT + d;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 8)
+                            *reinterpret_cast<uint4*>(dst + k) =
+                                make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                                           pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+                    } else {
+                        float* dst = p.part_o + prow * LAT + d;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    }
+                }
+            }
+            if (tid == 0 && rank == 0 && w.j == 0 && !whole) {
+                // the pair with the first pages says where the partials are
+                const int last = (int)(((long long)flat + w.q.nb - 1) / misc[M_Q]);
+                p.meta[pair] = make_int4(w.s, w.tile, last - pair + 1, min(rows - w.tile * kTile, kTile));
+            }
+            flat += w.np + kExtraPages;
+            g0 += nc;
+            umma::fence_before_sync();
+            // (the sums have been read before the next maxima are written: the meetings between)
+            __syncwarp();
+            if (lane == 0) {
+                arrive_remote(lead(G::B_OFREE));
+                arrive_remote(map_rank(bar(G::B_EPI + buf), 0u));
+                arrive_remote(map_rank(bar(G::B_EPI + buf), 1u));
+            }
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    cluster_sync();                      // nothing of the pair is under way in either's memory
+    if (warp == G::kMmaWarp) {
+        umma::fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------------- merge
+
+constexpr int kMergeWarps = 8;
+
+// CTA (x, y): rows 8 y .. 8 y + 7 of the tile whose first partial pair x wrote; one warp a
+// row, the partials in the pairs' order.
+template <int LAT>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_latent_merge_kernel(const LatentParams p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int x = blockIdx.x, lane = threadIdx.x & 31;
+    const int4 meta = p.meta[x];
+    const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    const int parts = meta.z;
+    if (parts <= 1 || row >= meta.w) return;
+    constexpr int V = LAT / 128;             // float4s of a lane
+    // partial i: the first pair's second slot, then the first slots
+    auto slot = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * kTile + row; };
+    float M = -INFINITY;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float acc[V][4], l = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < parts; ++i) {
+        const float2 ml = p.part_ml[slot(i)];
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(i) * LAT) + lane;
+        float4 o[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = src[32 * k];
+        // a partial that saw nothing weighs nothing (its maximum is -inf)
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        l += ml.y * w;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            acc[k][0] += o[k].x * w;
+            acc[k][1] += o[k].y * w;
+            acc[k][2] += o[k].z * w;
+            acc[k][3] += o[k].w * w;
+        }
+    }
+    const SeqInfo q = seq_info(p, meta.x, false);
+    const int r = meta.y * kTile + row;
+    float none = 0.f;                        // the result of a row without weight
+    if (l == 0.f) {
+        uint32_t seen[4];
+        if (seen_nodes(p, q.t0, row_node(p, r), nullptr, seen)) {
+            bool any = q.base > 0;
+            for (int k = 0; k < 4; ++k) any = any || (seen[k] & low_bits(q.L - 32 * k)) != 0u;
+            if (any) none = __uint_as_float(0x7fffffffu);
+        }
+    }
+    const float inv = 1.f / l;
+    uint2* dst = reinterpret_cast<uint2*>(p.out + ((size_t)q.t0 * p.H + r) * LAT) + lane;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = l == 0.f ? none : acc[k][e] * inv;
+        dst[32 * k] = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+}
+
+// -------------------------------------------------------------------------- host
 
 int check_latent_shape(int num_seqs, int max_nodes, int H, int L, int R)
 {
@@ -148,6 +1100,103 @@ int check_latent_shape(int num_seqs, int max_nodes, int H, int L, int R)
     if (max_nodes > KV_TREE_MAX_NODES) return KV_ERR_TOO_LARGE;
     if (H > 128 || (L != 256 && L != 512) || (R != 32 && R != 64)) return KV_ERR_UNSUPPORTED;
     return KV_OK;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct LatentPlan {
+    int pairs;
+    size_t o, ml, meta, total;
+};
+
+LatentPlan latent_plan(int L)
+{
+    LatentPlan t;
+    t.pairs = std::max(1, num_sms_current() / 2);
+    const size_t slots = (size_t)t.pairs * 2 * kTile;
+    t.o = 0;
+    t.ml = t.o + up256(slots * L * sizeof(float));
+    t.meta = t.ml + up256(slots * sizeof(float2));
+    t.total = t.meta + up256((size_t)t.pairs * sizeof(int4));
+    return t;
+}
+
+// Rows of W elements, as boxes of box_rows rows x box_cols 64-element columns with the
+// 128-byte swizzle: column by column in shared memory.
+int column_map(CUtensorMap* map, const void* base, long long rows, int W, int cols, int box_rows, int box_cols)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int rc = map_encoder(enc)) return rc;
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols};
+    cuuint64_t strides[2] = {(cuuint64_t)W * 2, 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_cols};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KV_OK
+               : KV_ERR_CUDA;
+}
+
+// The same rows as they are, in boxes of 64 elements: of the one that starts at W - R, what
+// lies behind the row is zeros.
+int row_map(CUtensorMap* map, const void* base, long long rows, int W, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int rc = map_encoder(enc)) return rc;
+    cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)W * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KV_OK
+               : KV_ERR_CUDA;
+}
+
+std::mutex g_latent_mu;
+
+template <int LAT>
+int launch_latent(const LatentParams& p, const void* q, const void* cache, cudaStream_t st)
+{
+    using G = Geo<LAT>;
+    const int W = LAT + p.R;
+    const long long qrows = (long long)p.total * p.H, krows = (long long)p.num_blocks * kBlock;
+    CUtensorMap mq, mqr, mk, mkr, mv;
+    if (int rc = column_map(&mq, q, qrows, W, G::kCols, kRows, 4)) return rc;
+    if (int rc = row_map(&mqr, q, qrows, W, kRows)) return rc;
+    if (int rc = column_map(&mk, cache, krows, W, G::kCols, 8, 4)) return rc;
+    if (int rc = row_map(&mkr, cache, krows, W, kBlock)) return rc;
+    if (int rc = column_map(&mv, cache, krows, W, G::kCols, kBlock, 2)) return rc;
+    static bool ready[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KV_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_latent_mu);
+        if (!ready[dev]) {
+            if (cudaFuncSetAttribute(paged_latent_kernel<LAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem) !=
+                cudaSuccess)
+                return KV_ERR_CUDA;
+            ready[dev] = true;
+        }
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * p.pairs));
+    cfg.blockDim = dim3(G::kThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, paged_latent_kernel<LAT>, mq, mqr, mk, mkr, mv, p) != cudaSuccess) return KV_ERR_CUDA;
+    const int rows = std::min(p.max_nodes * p.H, kTile);
+    cfg.gridDim = dim3((unsigned)p.pairs, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, paged_latent_merge_kernel<LAT>, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
 }  // namespace
@@ -166,7 +1215,7 @@ extern "C" int paged_latent_workspace_bytes(int num_seqs, int max_nodes, int num
     if (int rc = check_latent_shape(num_seqs, max_nodes, num_q_heads, latent_dim, rope_dim)) return rc;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
-    *bytes = 256;
+    *bytes = latent_plan(latent_dim).total;
     return KV_OK;
 }
 
@@ -185,28 +1234,37 @@ extern "C" int paged_latent_attention(void* out, const void* q, const void* cach
     if ((((uintptr_t)q | (uintptr_t)cache | (uintptr_t)workspace | (uintptr_t)out) & 15) != 0)
         return KV_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return KV_ERR_INVALID_ARG;
+    // flat work indices, tensor-map rows and positions must fit in int32
+    const long long tiles = ((long long)max_nodes * num_q_heads + kTile - 1) / kTile;
     if ((long long)total_nodes * num_q_heads >= INT_MAX - 256 || (long long)num_blocks * kBlock >= INT_MAX - 256 ||
-        (long long)max_blocks_per_seq * kBlock >= INT_MAX)
+        (long long)max_blocks_per_seq * kBlock >= INT_MAX ||
+        ((long long)max_blocks_per_seq + 2 * kExtraPages) * num_seqs >= INT_MAX / tiles)
         return KV_ERR_UNSUPPORTED;
-    if (workspace_bytes < 256) return KV_ERR_INVALID_ARG;
+    const LatentPlan t = latent_plan(latent_dim);
+    if (workspace_bytes < t.total) return KV_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     LatentParams p;
-    p.q = static_cast<const uint16_t*>(q);
-    p.cache = static_cast<const uint16_t*>(cache);
     p.out = static_cast<uint16_t*>(out);
+    p.cache = static_cast<const uint16_t*>(cache);
     p.bt = block_tables;
     p.ctx = context_lens;
     p.starts = node_starts;
-    p.parents = parents;
+    p.parents = node_starts ? parents : nullptr;
+    p.part_o = reinterpret_cast<float*>(ws + t.o);
+    p.part_ml = reinterpret_cast<float2*>(ws + t.ml);
+    p.meta = reinterpret_cast<int4*>(ws + t.meta);
     p.B = num_seqs;
     p.total = total_nodes;
     p.max_nodes = max_nodes;
     p.H = num_q_heads;
-    p.L = latent_dim;
     p.R = rope_dim;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
+    p.pairs = t.pairs;
+    p.h_magic = num_q_heads == 1 ? 0u : 0xffffffffu / (uint32_t)num_q_heads + 1u;
     p.sl2 = scale * 1.4426950408889634f;
+    p.test_stall = test_stall_cycles();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     g_launched.note();
-    paged_latent_kernel<<<(unsigned)(total_nodes * num_q_heads), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    return latent_dim == 512 ? launch_latent<512>(p, q, cache, st) : launch_latent<256>(p, q, cache, st);
 }
