@@ -92,7 +92,7 @@ struct Geo {
     static constexpr int kGroups = kCols / 4;            // groups of K columns; the rotary part is one more
     static constexpr int kHalves = LAT / 256;            // products of N 256 for a page
     static constexpr int kSlots = LAT == 512 ? 1 : 2;    // chunks of K and of V in shared memory
-    static constexpr int kWeighWarps = 8, kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kFixWarp = 11;
+    static constexpr int kWeighWarps = 8, kKWarp = 8, kVWarp = 9, kMmaWarp = 10;
     static constexpr int kThreads = 12 * 32;
     static constexpr int kQBytes = (kCols + 1) * kRows * 128;
     static constexpr int kGroupBytes = kRows * 4 * 128;  // 64 tokens x 4 columns
@@ -112,15 +112,16 @@ struct Geo {
     static constexpr int B_QFREE = B_QFULL + 1;                  // the segment's last scores are computed
     static constexpr int B_KFULL = B_QFREE + 1;                  // (L) + slot * kG1 + group: K of both CTAs
     static constexpr int B_KFREE = B_KFULL + kSlots * kG1;       // + slot * kG1 + group
-    static constexpr int B_VFULL = B_KFREE + kSlots * kG1;       // + slot * 2 + half of the chunk
-    static constexpr int B_VREADY = B_VFULL + kSlots * 2;        // (L) likewise: of both CTAs, cleared
+    static constexpr int B_VREADY = B_KFREE + kSlots * kG1;      // (L) + slot * 2 + half of the chunk: V of both CTAs
     static constexpr int B_VFREE = B_VREADY + kSlots * 2;        // likewise: its products are done
-    static constexpr int B_SFULL = B_VFREE + kSlots * 2;         // + buffer: scores
-    static constexpr int B_PFULL = B_SFULL + 2;                  // (L) weights of both CTAs
+    static constexpr int B_VFIX = B_VFREE + kSlots * 2;          // a half that has to be cleared has landed here
+    static constexpr int B_SFULL = B_VFIX + 1;                   // + buffer: scores
+    static constexpr int B_SFREE = B_SFULL + 2;                  // (L) + buffer: both have read them
+    static constexpr int B_PFULL = B_SFREE + 2;                  // (L) weights of both CTAs
     static constexpr int B_OFREE = B_PFULL + 1;                  // (L) both have read the accumulators
     static constexpr int B_EPI = B_OFREE + 1;                    // + segment & 1: likewise, for the clearing warps
-    static constexpr int B_END = B_EPI + 2;
-    static constexpr int B_STALL = B_END + 1;                    // nothing arrives (the test hook)
+    static constexpr int B_END = B_EPI + 2;                      // + MMA warp
+    static constexpr int B_STALL = B_END + 2;                    // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kBadOff = kMiscOff + (M_WORDS * 4 + 15) / 16 * 16;      // [2][CTA of the pair][4] words
@@ -490,17 +491,18 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             mbar_init(bar(G::B_KFREE + i), 1);
         }
         for (int i = 0; i < G::kSlots * 2; ++i) {
-            mbar_init(bar(G::B_VFULL + i), 1);
             mbar_init(bar(G::B_VREADY + i), 2);
             mbar_init(bar(G::B_VFREE + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(G::B_SFULL + i), 1);
+            mbar_init(bar(G::B_SFREE + i), 2 * G::kWeighWarps);
+            mbar_init(bar(G::B_END + i), 1);
             mbar_init(bar(G::B_EPI + i), 2 * G::kWeighWarps);
         }
         mbar_init(bar(G::B_PFULL), 2 * G::kWeighWarps);
         mbar_init(bar(G::B_OFREE), 2 * G::kWeighWarps);
-        mbar_init(bar(G::B_END), 1);
+        mbar_init(bar(G::B_VFIX), 1);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
         fence_mbar_init();
@@ -591,12 +593,17 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         __syncwarp();
     } else if (warp == G::kVWarp) {
-        // ------------------------------------------------------------------- V
-        int g = 0;
+        // ------------- V; and what of it must not be multiplied: rows behind the context, and
+        // infinities and NaN of drafted rows
+        int g = 0, fixes = 0;
         bool ok = true;
         for (Walk w(p, misc); ok && w.more(); w.next(p)) {
             const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
-            const int nc = w.chunks();
+            const int nc = w.chunks(), buf = w.seg & 1;
+            // the notes of what is cleared were last read two segments ago
+            if (w.seg >= 2) ok = wait_warp(bar(G::B_EPI + buf), (uint32_t)(((w.seg - 2) >> 1) & 1), misc);
+            if (!ok) break;
+            uint32_t bad[4] = {0u, 0u, 0u, 0u};          // drafted rows where something was cleared
             int ids = lane < w.np ? __ldg(row + lane) : -1;
             int ahead = 32 + lane < w.np ? __ldg(row + 32 + lane) : -1;
             for (int c = 0; ok && c < nc; ++c, ++g) {
@@ -606,6 +613,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     ahead = at < w.np ? __ldg(row + at) : -1;
                 }
                 const int sl = slot(g);
+                const bool fix = w.drafted(c);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // lanes 0 .. 4 * halves - 1: page and 256-column block
@@ -618,14 +626,61 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         ok = false;
                         break;
                     }
+                    const uint32_t ready = lead(G::B_VREADY + b), full = fix ? bar(G::B_VFIX) : ready;
                     if (lane == 0) {
-                        if (n > 0) mbar_arrive_expect_tx(bar(G::B_VFULL + b), (uint32_t)(n * 4096));
-                        else mbar_arrive(bar(G::B_VFULL + b));
+                        // (the first CTA expects both CTAs' bytes where they count there)
+                        if (fix) mbar_arrive_expect_tx(full, (uint32_t)(n * 4096));
+                        else if (rank == 0) mbar_arrive_expect_tx(bar(G::B_VREADY + b), (uint32_t)(n * 8192));
+                        else arrive_remote(ready);
                     }
                     __syncwarp();
                     if (mine)
-                        tma_load_3d(sb + (uint32_t)(G::kVOff + sl * G::kVSlot + page * G::kVPage + t * 4096), &tm_v, 0,
-                                    id * kBlock, 4 * t + 2 * (int)rank, bar(G::B_VFULL + b));
+                        tma2_load_3d(sb + (uint32_t)(G::kVOff + sl * G::kVSlot + page * G::kVPage + t * 4096), &tm_v, 0,
+                                     id * kBlock, 4 * t + 2 * (int)rank, full);
+                    if (!fix) continue;
+                    if (!wait_warp(full, (uint32_t)(fixes++ & 1), misc)) {
+                        ok = false;
+                        break;
+                    }
+                    const int p0 = (w.j + c * kPages) * kBlock;
+                    const int lo = max(64 * h, w.q.base - p0), hi = min(64 * (h + 1), w.chunk_pages(c) * kBlock);
+                    // a row's 16-byte pieces, 16 of each 256-column block
+                    for (int r = lo; r < hi; ++r) {
+                        const bool tail = p0 + r >= w.q.L;
+                        for (int x = lane; x < 16 * G::kHalves; x += 32) {
+                            const int tt = x >> 4, col = (x >> 3) & 1, ch = x & 7, rr = r & 15;
+                            const uint32_t at = sb + (uint32_t)(G::kVOff + sl * G::kVSlot + (r >> 4) * G::kVPage +
+                                                                tt * 4096 + col * 2048 + rr * 128 + ((ch ^ (rr & 7)) * 16));
+                            uint32_t v[4] = {0u, 0u, 0u, 0u}, any = 0u;
+                            if (!tail) {
+                                lds128(v, at);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t m = __vcmpeq2(v[k] & 0x7f807f80u, 0x7f807f80u);
+                                    v[k] &= ~m;
+                                    any |= m;
+                                }
+                            }
+                            if (tail || any) sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
+                            const int a = p0 + r - w.q.base;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) bad[k] |= any && (a >> 5) == k ? 1u << (a & 31) : 0u;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    // both CTAs' rows have all columns, so both are told
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        bad[k] = __reduce_or_sync(kFull, bad[k]);
+                        if (lane < 2) {
+                            const uint32_t at = sb + (uint32_t)(G::kBadOff + ((buf * 2 + (int)rank) * 4 + k) * 4);
+                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)lane)), "r"(bad[k])
+                                         : "memory");
+                        }
+                    }
+                    fence_cluster();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(ready);
                 }
             }
         }
@@ -635,147 +690,93 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         __syncwarp();
     } else if (warp == G::kMmaWarp) {
-        // -------------------------------------------------------------- products
+        // ---------------------------------------------------------------- scores
         if (rank == 0 && lane == 0) {
             const uint64_t qdesc = umma::smem_desc_sw128(sb + G::kQOff, 16, 1024);
             const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kKOff, 16, 4096);
             const uint64_t rdesc = umma::smem_desc_sw128(sb + G::kKOff + G::kGroups * G::kGroupBytes, 16, 1024);
-            const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, 16, 1024);
-            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, 2048, 1024);
-            constexpr uint32_t idesc_s = umma::idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t idesc_o = umma::idesc_bf16_f32(128, 256, false, true);
+            constexpr uint32_t idesc = umma::idesc_bf16_f32(128, 128, false, false);
             bool ok = true;
             if (p.test_stall > 0 && misc[M_CNT] > 0 && !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
                 give_up(misc);
                 ok = false;
             }
-            auto scores = [&](int g) -> bool {
-                const int sl = slot(g);
-                const uint32_t d = tmem + (uint32_t)(64 * (g & 1));
-                const uint64_t ks = (uint64_t)((sl * G::kKSlot) >> 4);
-#pragma unroll
-                for (int k = 0; k <= G::kGroups; ++k) {
-                    const int b = sl * G::kG1 + k;
-                    if (!wait_bar(bar(G::B_KFULL + b), pass(g), misc)) return false;
-                    umma::fence_after_sync();
-                    if (k < G::kGroups) {
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk)
-                            mma2(d, qdesc + (uint64_t)(((k * 4 + (kk >> 2)) * kRows * 128 + (kk & 3) * 32) >> 4),
-                                 kdesc + ks + (uint64_t)((k * G::kGroupBytes + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                                 idesc_s, k + kk > 0);
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma2(d, qdesc + (uint64_t)((G::kCols * kRows * 128 + kk * 32) >> 4),
-                                 rdesc + ks + (uint64_t)((kk * 32) >> 4), idesc_s, true);
-                    }
-                    commit2(bar(G::B_KFREE + b));
-                }
-                commit2(bar(G::B_SFULL + (g & 1)));
-                return true;
-            };
-            // the products of chunk g, the segment's chunk c of np pages
-            auto products = [&](int g, int c, int np) -> bool {
-                const int sl = slot(g);
-                if (!wait_bar(bar(G::B_PFULL), (uint32_t)(g & 1), misc)) return false;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int b = sl * 2 + h;
-                    if (!wait_bar(bar(G::B_VREADY + b), pass(g), misc)) return false;
-                    umma::fence_after_sync();
-                    const int to = min(np, 4 * h + 4);
-                    for (int k = 4 * h; k < to; ++k)
-#pragma unroll
-                        for (int t = 0; t < G::kHalves; ++t)
-                            mma2(tmem + G::kColO + (uint32_t)(128 * t),
-                                 pdesc + (uint64_t)(((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
-                                 vdesc + (uint64_t)((sl * G::kVSlot + k * G::kVPage + t * 4096) >> 4), idesc_o,
-                                 c + k > 0);
-                    commit2(bar(G::B_VFREE + b));
-                }
-                return true;
-            };
             int g = 0;
             for (Walk w(p, misc); ok && w.more(); w.next(p)) {
                 const int nc = w.chunks();
                 ok = wait_bar(bar(G::B_QFULL), (uint32_t)(w.seg & 1), misc);
-                for (int c = 0; ok && c < nc; ++c) {
-                    ok = scores(g + c);
+                for (int c = 0; ok && c < nc; ++c, ++g) {
+                    // the buffer was read for chunk g - 2
+                    if (g >= 2) ok = wait_bar(bar(G::B_SFREE + (g & 1)), (uint32_t)((g >> 1) - 1) & 1u, misc);
+                    const int sl = slot(g);
+                    const uint32_t d = tmem + (uint32_t)(64 * (g & 1));
+                    const uint64_t ks = (uint64_t)((sl * G::kKSlot) >> 4);
+#pragma unroll
+                    for (int k = 0; k <= G::kGroups; ++k) {
+                        const int b = sl * G::kG1 + k;
+                        ok = ok && wait_bar(bar(G::B_KFULL + b), pass(g), misc);
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        if (k < G::kGroups) {
+#pragma unroll
+                            for (int kk = 0; kk < 16; ++kk)
+                                mma2(d, qdesc + (uint64_t)(((k * 4 + (kk >> 2)) * kRows * 128 + (kk & 3) * 32) >> 4),
+                                     kdesc + ks + (uint64_t)((k * G::kGroupBytes + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                                     idesc, k + kk > 0);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma2(d, qdesc + (uint64_t)((G::kCols * kRows * 128 + kk * 32) >> 4),
+                                     rdesc + ks + (uint64_t)((kk * 32) >> 4), idesc, true);
+                        }
+                        commit2(bar(G::B_KFREE + b));
+                    }
                     if (!ok) break;
+                    commit2(bar(G::B_SFULL + (g & 1)));
                     if (c + 1 == nc) commit2(bar(G::B_QFREE));
-                    // the accumulators of the segment before have been read
-                    if (c == 1 || (nc == 1 && c == 0))
-                        ok = w.seg == 0 || wait_bar(bar(G::B_OFREE), (uint32_t)((w.seg - 1) & 1), misc);
-                    if (ok && c > 0) ok = products(g + c - 1, c - 1, kPages);
                 }
-                ok = ok && products(g + nc - 1, nc - 1, w.chunk_pages(nc - 1));
-                g += nc;
             }
             // every MMA issued by this thread is complete before the pair ends
             commit2(bar(G::B_END));
             mbar_wait_bounded(bar(G::B_END), 0u, kWaitLimit);
         }
         __syncwarp();
-    } else if (warp == G::kFixWarp) {
-        // -------------------------------------- V rows that must not be multiplied
-        int g = 0;
-        bool ok = true;
-        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
-            const int nc = w.chunks(), buf = w.seg & 1;
-            if (w.seg >= 2) ok = wait_warp(bar(G::B_EPI + buf), (uint32_t)(((w.seg - 2) >> 1) & 1), misc);
-            if (!ok) break;
-            uint32_t bad[4] = {0u, 0u, 0u, 0u};          // drafted rows where something was cleared
-            for (int c = 0; ok && c < nc; ++c, ++g) {
-                const int sl = slot(g), p0 = (w.j + c * kPages) * kBlock;
-                for (int h = 0; ok && h < 2; ++h) {
-                    const int b = sl * 2 + h;
-                    ok = wait_warp(bar(G::B_VFULL + b), pass(g), misc);
-                    if (!ok) break;
-                    if (w.drafted(c)) {
-                        const int lo = max(64 * h, w.q.base - p0), hi = min(64 * (h + 1), w.chunk_pages(c) * kBlock);
-                        // a row's 16-byte pieces, 16 of each 256-column block
-                        for (int r = lo; r < hi; ++r) {
-                            const bool tail = p0 + r >= w.q.L;
-                            for (int x = lane; x < 16 * G::kHalves; x += 32) {
-                                const int t = x >> 4, col = (x >> 3) & 1, ch = x & 7, rr = r & 15;
-                                const uint32_t at = sb + (uint32_t)(G::kVOff + sl * G::kVSlot + (r >> 4) * G::kVPage +
-                                                                    t * 4096 + col * 2048 + rr * 128 + ((ch ^ (rr & 7)) * 16));
-                                uint32_t v[4] = {0u, 0u, 0u, 0u}, any = 0u;
-                                if (!tail) {
-                                    lds128(v, at);
+    } else if (warp == G::kMmaWarp + 1) {
+        // -------------------------------------------------------------- products
+        if (rank == 0 && lane == 0) {
+            const uint64_t pdesc = umma::smem_desc_sw128(sb + G::kPOff, 16, 1024);
+            const uint64_t vdesc = umma::smem_desc_sw128(sb + G::kVOff, 2048, 1024);
+            constexpr uint32_t idesc = umma::idesc_bf16_f32(128, 256, false, true);
+            bool ok = true;
+            int g = 0;
+            for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+                const int nc = w.chunks();
+                // the accumulators of the segment before have been read
+                if (w.seg > 0) ok = wait_bar(bar(G::B_OFREE), (uint32_t)((w.seg - 1) & 1), misc);
+                for (int c = 0; ok && c < nc; ++c, ++g) {
+                    const int sl = slot(g), np = w.chunk_pages(c);
+                    ok = wait_bar(bar(G::B_PFULL), (uint32_t)(g & 1), misc);
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const uint32_t m = __vcmpeq2(v[k] & 0x7f807f80u, 0x7f807f80u);
-                                        v[k] &= ~m;
-                                        any |= m;
-                                    }
-                                }
-                                if (tail || any) sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
-                                const int a = p0 + r - w.q.base;
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = sl * 2 + h;
+                        ok = ok && wait_bar(bar(G::B_VREADY + b), pass(g), misc);
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        const int to = min(np, 4 * h + 4);
+                        for (int k = 4 * h; k < to; ++k)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) bad[k] |= any && (a >> 5) == k ? 1u << (a & 31) : 0u;
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        // both CTAs' rows have all columns, so both are told
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            bad[k] = __reduce_or_sync(kFull, bad[k]);
-                            if (lane < 2) {
-                                const uint32_t at = sb + (uint32_t)(G::kBadOff + ((buf * 2 + (int)rank) * 4 + k) * 4);
-                                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)lane)),
-                                             "r"(bad[k])
-                                             : "memory");
-                            }
-                        }
-                        fence_cluster();
+                            for (int t = 0; t < G::kHalves; ++t)
+                                mma2(tmem + G::kColO + (uint32_t)(128 * t),
+                                     pdesc + (uint64_t)(((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
+                                     vdesc + (uint64_t)((sl * G::kVSlot + k * G::kVPage + t * 4096) >> 4), idesc, c + k > 0);
+                        commit2(bar(G::B_VFREE + b));
                     }
-                    __syncwarp();
-                    if (lane == 0) arrive_remote(lead(G::B_VREADY + b));
                 }
             }
+            commit2(bar(G::B_END + 1));
+            mbar_wait_bounded(bar(G::B_END + 1), 0u, kWaitLimit);
         }
+        __syncwarp();
     } else {
         // --------------------------------------------------- weights and output
         const int wq = warp & 3, wg = warp >> 2;
@@ -829,7 +830,10 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (g > 0) ok = __all_sync(kFull, ok && wait_bar(done(g - 1), pass(g - 1), misc));
                     umma::fence_before_sync();
                     __syncwarp();
-                    if (ok && lane == 0) arrive_remote(lead(G::B_PFULL));
+                    if (ok && lane == 0) {
+                        arrive_remote(lead(G::B_SFREE + (g & 1)));
+                        arrive_remote(lead(G::B_PFULL));
+                    }
                     continue;
                 }
                 float t[32];
@@ -840,6 +844,11 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (warp_live) {
                     umma::tmem_ld32(lanes + (uint32_t)(64 * (g & 1) + 32 * wg), *reinterpret_cast<uint32_t(*)[32]>(&t[0]));
                     umma::tmem_wait_ld();
+                }
+                umma::fence_before_sync();
+                __syncwarp();
+                if (ok && lane == 0) arrive_remote(lead(G::B_SFREE + (g & 1)));
+                if (warp_live) {
                     // (the product rounded before the sum: the reference is such a product, and a
                     // fused remainder would grow with it)
                     const u64 f = pack2(p.sl2, p.sl2);
