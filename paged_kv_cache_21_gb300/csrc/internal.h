@@ -19,6 +19,7 @@ int verify_read_error(unsigned* flags, long long* detail);
 int compact_read_error(unsigned* flags, long long* detail);
 int rotary_read_error(unsigned* flags, long long* detail);
 int latent_read_error(unsigned* flags, long long* detail);
+int latent_small_read_error(unsigned* flags, long long* detail);
 
 // The decision of kv_prefix_plan for a given number of resident warps of the
 // split-KV kernel (host only; allocator.cpp).

@@ -1,0 +1,274 @@
+// What the kernels of paged_latent_attention share (paged_latent.cu, for many query
+// rows, and paged_latent_small.cu, for few): bounded waits, the cut of the work over
+// workers, and the visibility of drafted tokens.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "latent_launch.h"
+#include "paged_kv.h"
+#include "tree_common.cuh"
+#include "umma.cuh"
+
+namespace pkv {
+
+static __device__ DevErr g_latent_err;           // one per translation unit
+static Launched g_launched;
+
+namespace {
+
+constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
+constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
+
+// misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
+// per worker, first sequence, tile and page; that sequence's nodes, context and first node
+enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_T0, M_J0, M_N0, M_L0, M_NODE0, M_WORDS };
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// a += the lower, b += the upper of two bf16.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x));
+}
+
+// Sequences without a context get zeros for their nodes (threads 0 .. nthreads - 1 of the
+// CTAs of the kernel that does it).
+template <int LAT, typename SeqInfo>
+__device__ __forceinline__ void zero_nodes(const LatentParams& p, const SeqInfo& q, int tid, int nthreads)
+{
+    uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)q.t0 * p.H * LAT);
+    for (size_t i = tid; i < (size_t)q.n * p.H * LAT / 8; i += nthreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ------------------------------------------------------------------------- work
+
+struct SeqInfo {
+    int t0, n, L, base, nb, tiles;      // nb: pages, 0 without nodes; tiles of rows
+};
+
+// What follows from a sequence's nodes and context.
+__device__ __forceinline__ void seq_work(const LatentParams& p, SeqInfo& q)
+{
+    q.base = q.L > q.n ? q.L - q.n : 0;
+    const int rows = q.n * p.H;
+    q.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+    q.nb = q.n > 0 ? (q.L + kBlock - 1) / kBlock : 0;
+}
+
+__device__ __forceinline__ SeqInfo seq_info(const LatentParams& p, int s, bool flag)
+{
+    SeqInfo q;
+    int bad = 0;
+    int L = __ldg(p.ctx + s);
+    if (!p.starts) {
+        q.t0 = s;
+        q.n = 1;
+    } else if (!tree_span(p.starts, s, p.total, p.max_nodes, q.t0, q.n, bad) && flag) {
+        raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, bad);
+    }
+    const int cap = p.max_blocks * kBlock;
+    if (L < 0 || L > cap) {
+        if (flag) raise_flag(&g_latent_err, KV_DEVERR_CONTEXT_TOO_LONG, L);
+        L = L < 0 ? 0 : cap;
+    }
+    if (flag && L > 0 && L < q.n) raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, L);
+    q.L = L;
+    seq_work(p, q);
+    return q;
+}
+
+// The segments of a worker's range: the pages [j, j + np) of one (sequence, tile) each.
+// Every role walks the same list, in chunks of kPages pages.
+template <int kPages>
+struct Walk {
+    int s, tile, j, rem, seg, np;
+    SeqInfo q;
+    __device__ __forceinline__ Walk(const LatentParams& p, const volatile int* misc)
+    {
+        s = misc[M_S0];
+        tile = misc[M_T0];
+        j = misc[M_J0];
+        rem = misc[M_CNT];
+        seg = 0;
+        np = 0;
+        if (rem > 0) {
+            q.t0 = misc[M_NODE0];
+            q.n = misc[M_N0];
+            q.L = misc[M_L0];
+            seq_work(p, q);
+            np = min(q.nb - j, rem);
+        }
+    }
+    __device__ __forceinline__ bool more() const { return rem > 0; }
+    __device__ __forceinline__ int chunks() const { return (np + kPages - 1) / kPages; }
+    __device__ __forceinline__ int chunk_pages(int c) const { return min(kPages, np - c * kPages); }
+    // does chunk c reach the drafted positions, or the context's end?
+    __device__ __forceinline__ bool drafted(int c) const
+    {
+        return (j + c * kPages + chunk_pages(c)) * kBlock > q.base;
+    }
+    __device__ __forceinline__ bool whole() const { return j == 0 && np == q.nb; }
+    __device__ __forceinline__ void next(const LatentParams& p)
+    {
+        rem -= np;
+        ++seg;
+        if (rem <= 0) return;
+        j = 0;
+        if (++tile == q.tiles) {
+            tile = 0;
+            do {
+                if (++s >= p.B) {
+                    rem = 0;
+                    return;
+                }
+                q = seq_info(p, s, false);
+            } while (q.nb == 0);
+        }
+        np = min(q.nb, rem);
+    }
+};
+
+// This worker's range of the list of pages, by sequence and tile: equal shares of at least
+// min_q units, where a page is a unit and each (sequence, tile) costs extra more
+// before its first page.  One warp.
+__device__ __forceinline__ void cut_work(const LatentParams& p, volatile int* misc, int min_q, int extra, int worker, bool flag, int lane)
+{
+    // (the sequences at hand stay in registers where one pass over them is all there is)
+    const bool once = p.B <= 32;
+    SeqInfo q = {0, 0, 0, 0, 0, 0};
+    long long total = 0;
+    for (int b = 0; b < p.B; b += 32) {
+        long long u = 0;
+        if (b + lane < p.B) {
+            q = seq_info(p, b + lane, flag);
+            u = q.nb > 0 ? (long long)(q.nb + extra) * q.tiles : 0;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
+        total += u;
+    }
+    // (all units are less than 2^31: the host has checked)
+    int share = (int)((uint32_t)(total + p.workers - 1) / (uint32_t)p.workers);
+    if (share < min_q) share = min_q;
+    // the first page at or behind unit x: its sequence, tile and index, its unit, and how
+    // many pages are before it
+    struct At {
+        int s, tile, j, unit, pages;
+        int n, L, t0;
+    };
+    const int lo = (int)min((long long)worker * share, total), hi = (int)min((long long)lo + share, total);
+    At at[2] = {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0}};
+    bool found[2] = {false, false};
+    int units = 0, pages = 0;                    // up to the 32 sequences at hand
+    for (int b = 0; b < p.B && !(found[0] && found[1]); b += 32) {
+        if (!once) {
+            q = {0, 0, 0, 0, 0, 0};
+            if (b + lane < p.B) q = seq_info(p, b + lane, false);
+        }
+        const int u = q.nb > 0 ? (q.nb + extra) * q.tiles : 0, n = q.nb * q.tiles;
+        int iu = u, in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
+            if (lane >= o) {
+                iu += tu;
+                in += tn;
+            }
+        }
+        iu += units;
+        in += pages;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x = e == 0 ? lo : hi;
+            const unsigned m = __ballot_sync(kFull, iu > x);
+            if (found[e] || !m) continue;
+            found[e] = true;
+            const int src = __ffs(m) - 1;
+            const int nbs = __shfl_sync(kFull, q.nb, src), v = nbs + extra;
+            const int before = __shfl_sync(kFull, iu - u, src);
+            const int off = x - before, t = off / v, j = max(0, off - t * v - extra);
+            at[e] = {b + src, t, j, before + t * v + extra + j, __shfl_sync(kFull, in - n, src) + t * nbs + j,
+                     __shfl_sync(kFull, q.n, src), __shfl_sync(kFull, q.L, src), __shfl_sync(kFull, q.t0, src)};
+        }
+        units = __shfl_sync(kFull, iu, 31);
+        pages = __shfl_sync(kFull, in, 31);
+    }
+    if (!found[1]) at[1].pages = pages;          // (hi is the end of the list)
+    if (lane == 0) {
+        misc[M_B0] = at[0].unit;
+        misc[M_CNT] = found[0] ? at[1].pages - at[0].pages : 0;
+        misc[M_Q] = share;
+        misc[M_S0] = at[0].s;
+        misc[M_T0] = at[0].tile;
+        misc[M_J0] = at[0].j;
+        misc[M_N0] = at[0].n;
+        misc[M_L0] = at[0].L;
+        misc[M_NODE0] = at[0].t0;
+    }
+}
+
+// Node (within the sequence) of row r of its rows.
+__device__ __forceinline__ int row_node(const LatentParams& p, int r)
+{
+    return p.h_magic ? (int)__umulhi((uint32_t)r, p.h_magic) : r;
+}
+
+// The nodes that node i sees, as bits; false for a padding node.
+__device__ __forceinline__ bool seen_nodes(const LatentParams& p, int t0, int i, DevErr* e, uint32_t (&m)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = 0u;
+    if (!p.starts || !p.parents) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = i >= 32 * k + 31 ? ~0u : i >= 32 * k ? (2u << (i - 32 * k)) - 1u : 0u;
+        return true;
+    }
+    for (int a = i; a >= 0;) {
+        const int up = tree_parent(p.parents, t0, a, e);
+        if (up == KV_TREE_PAD) return a != i;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] |= (a >> 5) == k ? 1u << (a & 31) : 0u;
+        a = up;
+    }
+    return true;
+}
+
+// Bits [at, at + 32) of a string of 128, zero outside it.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t (&m)[4], int at)
+{
+    if (at <= -32 || at >= 128) return 0u;
+    auto word = [&](int k) { return k == 0 ? m[0] : k == 1 ? m[1] : k == 2 ? m[2] : k == 3 ? m[3] : 0u; };
+    if (at < 0) return m[0] << -at;
+    return __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+}  // namespace
+}  // namespace pkv

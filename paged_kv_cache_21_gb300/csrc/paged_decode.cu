@@ -2221,7 +2221,7 @@ extern "C" int kv_get_device_error(int* flags, int64_t* detail)
                                                    wide_read_error, tree_read_error,
                                                    tree_small_read_error, verify_read_error,
                                                    compact_read_error, rotary_read_error,
-                                                   latent_read_error};
+                                                   latent_read_error, latent_small_read_error};
     unsigned all = 0;
     long long first = -1;
     for (auto read : words) {

@@ -44,48 +44,18 @@
 #include <mutex>
 
 #include "cache_map.h"
-#include "device_common.cuh"
 #include "internal.h"
-#include "paged_kv.h"
-#include "tree_common.cuh"
-#include "umma.cuh"
+#include "latent_kernel.cuh"
 
 namespace pkv {
-
-static __device__ DevErr g_latent_err;
-static Launched g_launched;
 
 namespace {
 
 constexpr int kPages = 8;                       // pages of a chunk
 constexpr int kRows = 64;                       // rows of a CTA
 constexpr int kTile = 2 * kRows;                // rows of a pair
-constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
-constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
 constexpr int kMinPages = 16;                   // least range of a pair of CTAs
 constexpr int kExtraPages = 32;                 // what a (sequence, tile) costs beside its pages
-
-// misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
-// per pair, first sequence, tile and page
-enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_T0, M_J0, M_WORDS };
-
-struct LatentParams {
-    uint16_t* out;              // bf16 [total][H][L]
-    const uint16_t* cache;
-    const int32_t* bt;
-    const int32_t* ctx;
-    const int32_t* starts;      // or null: node s is sequence s
-    const int32_t* parents;
-    float* part_o;              // [pairs][2][128][L]
-    float2* part_ml;            // [pairs][2][128]: (max in log2 units, sum)
-    int4* meta;                 // [pairs]: (sequence, tile, partials, rows)
-    int B, total, max_nodes, H, R, max_blocks, num_blocks;
-    int pairs;
-    uint32_t h_magic;           // ceil(2^32 / H), 0 for H == 1
-    float sl2;
-    long long test_stall;
-};
-
 template <int LAT>
 struct Geo {
     static constexpr int kCols = LAT / 64;               // 64-element columns of the latent part
@@ -132,36 +102,6 @@ struct Geo {
     // tensor memory: two buffers of S, then O
     static constexpr uint32_t kColO = 128, kTmemCols = kColO + kHalves * 128 <= 256 ? 256 : 512;
 };
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
-// a += the lower, b += the upper of two bf16.
-__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x)
-{
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "add.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "r"(x));
-}
 
 // ---------------------------------------------------------------- pairs of CTAs
 
@@ -266,193 +206,6 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(kFull, wait_bar(bar, parity, misc));
 }
 
-// ------------------------------------------------------------------------- work
-
-struct SeqInfo {
-    int t0, n, L, base, nb, tiles;      // nb: pages, tiles: of 128 rows; 0 without nodes or context
-};
-
-__device__ __forceinline__ SeqInfo seq_info(const LatentParams& p, int s, bool flag)
-{
-    SeqInfo q;
-    int bad = 0;
-    if (!p.starts) {
-        q.t0 = s;
-        q.n = 1;
-    } else if (!tree_span(p.starts, s, p.total, p.max_nodes, q.t0, q.n, bad) && flag) {
-        raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, bad);
-    }
-    int L = __ldg(p.ctx + s);
-    const int cap = p.max_blocks * kBlock;
-    if (L < 0 || L > cap) {
-        if (flag) raise_flag(&g_latent_err, KV_DEVERR_CONTEXT_TOO_LONG, L);
-        L = L < 0 ? 0 : cap;
-    }
-    if (flag && L > 0 && L < q.n) raise_flag(&g_latent_err, KV_DEVERR_BAD_TREE, L);
-    q.L = L;
-    q.base = L > q.n ? L - q.n : 0;
-    q.tiles = (q.n * p.H + kTile - 1) / kTile;
-    q.nb = q.n > 0 ? (L + kBlock - 1) / kBlock : 0;
-    return q;
-}
-
-// The segments of a pair's range: the pages [j, j + np) of one (sequence, tile) each.
-// Every role of both CTAs walks the same list.
-struct Walk {
-    int s, tile, j, rem, seg, np;
-    SeqInfo q;
-    __device__ __forceinline__ Walk(const LatentParams& p, const volatile int* misc)
-    {
-        s = misc[M_S0];
-        tile = misc[M_T0];
-        j = misc[M_J0];
-        rem = misc[M_CNT];
-        seg = 0;
-        np = 0;
-        if (rem > 0) {
-            q = seq_info(p, s, false);
-            np = min(q.nb - j, rem);
-        }
-    }
-    __device__ __forceinline__ bool more() const { return rem > 0; }
-    __device__ __forceinline__ int chunks() const { return (np + kPages - 1) / kPages; }
-    __device__ __forceinline__ int chunk_pages(int c) const { return min(kPages, np - c * kPages); }
-    // does chunk c reach the drafted positions, or the context's end?
-    __device__ __forceinline__ bool drafted(int c) const
-    {
-        return (j + c * kPages + chunk_pages(c)) * kBlock > q.base;
-    }
-    __device__ __forceinline__ bool whole() const { return j == 0 && np == q.nb; }
-    __device__ __forceinline__ void next(const LatentParams& p)
-    {
-        rem -= np;
-        ++seg;
-        if (rem <= 0) return;
-        j = 0;
-        if (++tile == q.tiles) {
-            tile = 0;
-            do {
-                if (++s >= p.B) {
-                    rem = 0;
-                    return;
-                }
-                q = seq_info(p, s, false);
-            } while (q.nb == 0);
-        }
-        np = min(q.nb, rem);
-    }
-};
-
-// This pair's range of the list of pages, by sequence and tile: equal shares of at least
-// kMinPages units, where a page is a unit and each (sequence, tile) costs kExtraPages more
-// before its first page.  One warp.
-__device__ __forceinline__ void cut_work(const LatentParams& p, volatile int* misc, int pair, bool flag, int lane)
-{
-    long long total = 0;
-    for (int b = 0; b < p.B; b += 32) {
-        long long u = 0;
-        if (b + lane < p.B) {
-            const SeqInfo q = seq_info(p, b + lane, flag);
-            u = q.nb > 0 ? (long long)(q.nb + kExtraPages) * q.tiles : 0;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
-        total += u;
-    }
-    long long share = (total + p.pairs - 1) / p.pairs;
-    if (share < kMinPages) share = kMinPages;
-    // the first page at or behind unit x: its sequence, tile and index, its unit, and how
-    // many pages are before it
-    struct At {
-        int s, tile, j;
-        long long unit, pages;
-    };
-    const long long lo = min((long long)pair * share, total), hi = min(lo + share, total);
-    At at[2] = {{0, 0, 0, 0, 0}, {0, 0, 0, 0, 0}};
-    bool found[2] = {false, false};
-    long long units = 0, pages = 0;              // up to the 32 sequences at hand
-    for (int b = 0; b < p.B && !(found[0] && found[1]); b += 32) {
-        int nb = 0, tiles = 0;
-        if (b + lane < p.B) {
-            const SeqInfo q = seq_info(p, b + lane, false);
-            nb = q.nb;
-            tiles = q.tiles;
-        }
-        const long long u = nb > 0 ? (long long)(nb + kExtraPages) * tiles : 0, n = (long long)nb * tiles;
-        long long iu = u, in = n;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
-            if (lane >= o) {
-                iu += tu;
-                in += tn;
-            }
-        }
-        iu += units;
-        in += pages;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const long long x = e == 0 ? lo : hi;
-            const unsigned m = __ballot_sync(kFull, iu > x);
-            if (found[e] || !m) continue;
-            found[e] = true;
-            const int src = __ffs(m) - 1;
-            const int nbs = __shfl_sync(kFull, nb, src), v = nbs + kExtraPages;
-            const long long before = __shfl_sync(kFull, iu - u, src);
-            const int off = (int)(x - before), t = off / v, j = max(0, off - t * v - kExtraPages);
-            at[e] = {b + src, t, j, before + (long long)t * v + kExtraPages + j,
-                     __shfl_sync(kFull, in - n, src) + (long long)t * nbs + j};
-        }
-        units = __shfl_sync(kFull, iu, 31);
-        pages = __shfl_sync(kFull, in, 31);
-    }
-    if (!found[1]) at[1].pages = pages;          // (hi is the end of the list)
-    if (lane == 0) {
-        misc[M_B0] = (int)at[0].unit;
-        misc[M_CNT] = found[0] ? (int)(at[1].pages - at[0].pages) : 0;
-        misc[M_Q] = (int)share;
-        misc[M_S0] = at[0].s;
-        misc[M_T0] = at[0].tile;
-        misc[M_J0] = at[0].j;
-    }
-}
-
-// Node (within the sequence) of row r of its rows.
-__device__ __forceinline__ int row_node(const LatentParams& p, int r)
-{
-    return p.h_magic ? (int)__umulhi((uint32_t)r, p.h_magic) : r;
-}
-
-// The nodes that node i sees, as bits; false for a padding node.
-__device__ __forceinline__ bool seen_nodes(const LatentParams& p, int t0, int i, DevErr* e, uint32_t (&m)[4])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m[k] = 0u;
-    if (!p.starts || !p.parents) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = i >= 32 * k + 31 ? ~0u : i >= 32 * k ? (2u << (i - 32 * k)) - 1u : 0u;
-        return true;
-    }
-    for (int a = i; a >= 0;) {
-        const int up = tree_parent(p.parents, t0, a, e);
-        if (up == KV_TREE_PAD) return a != i;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] |= (a >> 5) == k ? 1u << (a & 31) : 0u;
-        a = up;
-    }
-    return true;
-}
-
-// Bits [at, at + 32) of a string of 128, zero outside it.
-__device__ __forceinline__ uint32_t bits_at(const uint32_t (&m)[4], int at)
-{
-    if (at <= -32 || at >= 128) return 0u;
-    auto word = [&](int k) { return k == 0 ? m[0] : k == 1 ? m[1] : k == 2 ? m[2] : k == 3 ? m[3] : 0u; };
-    if (at < 0) return m[0] << -at;
-    return __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
-}
-
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
 // ------------------------------------------------------------------------ kernel
 
 template <int LAT>
@@ -516,7 +269,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (warp == G::kKWarp) cut_work(p, misc, pair, blockIdx.x == 0, lane);
+    if (warp == G::kKWarp) cut_work(p, misc, kMinPages, kExtraPages, pair, blockIdx.x == 0, lane);
     umma::fence_before_sync();
     __syncthreads();
     cluster_sync();                      // the barriers of both CTAs are there
@@ -527,7 +280,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ------------------------------------------------------------- Q and K
         int g = 0;
         bool ok = true;
-        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+        for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
             if (w.seg > 0) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((w.seg - 1) & 1), misc);
             if (!ok) break;
             if (lane == 0) {
@@ -597,7 +350,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // infinities and NaN of drafted rows
         int g = 0, fixes = 0;
         bool ok = true;
-        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+        for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
             const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
             const int nc = w.chunks(), buf = w.seg & 1;
             // the notes of what is cleared were last read two segments ago
@@ -702,7 +455,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 ok = false;
             }
             int g = 0;
-            for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+            for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
                 const int nc = w.chunks();
                 ok = wait_bar(bar(G::B_QFULL), (uint32_t)(w.seg & 1), misc);
                 for (int c = 0; ok && c < nc; ++c, ++g) {
@@ -749,7 +502,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             constexpr uint32_t idesc = umma::idesc_bf16_f32(128, 256, false, true);
             bool ok = true;
             int g = 0;
-            for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+            for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
                 const int nc = w.chunks();
                 // the accumulators of the segment before have been read
                 if (w.seg > 0) ok = wait_bar(bar(G::B_OFREE), (uint32_t)((w.seg - 1) & 1), misc);
@@ -788,9 +541,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // sequences without a context: zeros for their nodes
         for (int s = blockIdx.x; s < p.B; s += gridDim.x) {
             const SeqInfo q = seq_info(p, s, false);
-            if (q.L > 0 || q.n == 0) continue;
-            uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)q.t0 * p.H * LAT);
-            for (size_t i = tid; i < (size_t)q.n * p.H * LAT / 8; i += G::kWeighWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (q.L == 0 && q.n > 0) zero_nodes<LAT>(p, q, tid, G::kWeighWarps * 32);
         }
         if (rank == 0 && tid == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
         int g0 = 0, flat = misc[M_B0];
@@ -807,7 +558,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 : "memory");
             return r != 0;
         };
-        for (Walk w(p, misc); ok && w.more(); w.next(p)) {
+        for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
             const int seg = w.seg, buf = seg & 1, nc = w.chunks(), rows = w.q.n * p.H;
             const int r = w.tile * kTile + (int)rank * kRows + row;       // of the sequence's rows
             uint32_t seen[4];
@@ -1002,10 +753,12 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                 make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
                                            pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
                     } else {
-                        float* dst = p.part_o + prow * LAT + d;
+                        // (four elements of a row, then those of the next: lanes are rows)
+                        float4* dst = reinterpret_cast<float4*>(p.part_o) + (prow - rank * kRows - row) * (LAT / 4) +
+                                      (d / 4) * kTile + rank * kRows + row;
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        for (int k = 0; k < 4; ++k)
+                            dst[k * kTile] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                     }
                 }
             }
@@ -1037,67 +790,143 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
 // ------------------------------------------------------------------------- merge
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
+constexpr int kMaxWorkers = 256;
+// Parts of a tile, by workers and tiles, from which the warps share them out.
+constexpr int kMergeSplit = 8;
 
-// CTA (x, y): rows 8 y .. 8 y + 7 of the tile whose first partial pair x wrote; one warp a
-// row, the partials in the pairs' order.
-template <int LAT>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_latent_merge_kernel(const LatentParams p)
+// What a row gets that has no weight: NaN if it sees a position (its scores were -inf alone).
+__device__ __forceinline__ float weightless(const LatentParams& p, int s, int r)
 {
+    const SeqInfo q = seq_info(p, s, false);
+    uint32_t seen[4];
+    if (!seen_nodes(p, q.t0, row_node(p, r), nullptr, seen)) return 0.f;
+    bool any = q.base > 0;
+    for (int k = 0; k < 4; ++k) any = any || (seen[k] & low_bits(q.L - 32 * k)) != 0u;
+    return any ? __uint_as_float(0x7fffffffu) : 0.f;
+}
+
+// CTA (e, piece): a piece of the e-th tile that has parts, in the order of the workers that
+// wrote its first part.  A warp reads 64 elements of 8 rows, where fours of the rows'
+// elements lie together, or a row (BY_ROW), where its elements do, two parts at a time with
+// a running (max, sum).  Few parts: the warps have different elements.  Many (SPLIT): they
+// take the parts in turn, and their four results are joined in the warps' order.
+template <int LAT, bool BY_ROW, bool SPLIT>
+__global__ void __launch_bounds__(kMergeWarps * 32, 8) paged_latent_merge_kernel(const LatentParams p)
+{
+    constexpr int kFours = LAT / 4, kN = BY_ROW ? LAT / 128 : 4;     // fours of a row; of a lane
+    constexpr int kRounds = kMaxWorkers / (kMergeWarps * 32);
+    __shared__ int4 s_meta;
+    __shared__ int s_x, s_count[kRounds][kMergeWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.tile_rows;
     pdl_wait();
     pdl_launch_dependents();
-    const int x = blockIdx.x, lane = threadIdx.x & 31;
-    const int4 meta = p.meta[x];
-    const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    int4 mine[kRounds];
+    unsigned first[kRounds];                             // workers that wrote the first part of a tile
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        const int x = q * kMergeWarps * 32 + tid;
+        mine[q] = x < p.workers ? p.meta[x] : make_int4(0, 0, 0, 0);
+        first[q] = __ballot_sync(kFull, mine[q].z > 1);
+        if (lane == 0) s_count[q][warp] = __popc(first[q]);
+    }
+    if (tid == 0) s_x = -1;
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q)
+#pragma unroll
+        for (int v = 0; v < kMergeWarps; ++v) {
+            if (v == warp && ((first[q] >> lane) & 1u) &&
+                n + __popc(first[q] & ((1u << lane) - 1u)) == (int)blockIdx.x) {
+                s_meta = mine[q];
+                s_x = q * kMergeWarps * 32 + tid;
+            }
+            n += s_count[q][v];
+        }
+    __syncthreads();
+    const int x = s_x;
+    if (x < 0) return;
+    const int4 meta = s_meta;
     const int parts = meta.z;
-    if (parts <= 1 || row >= meta.w) return;
-    constexpr int V = LAT / 128;             // float4s of a lane
-    // partial i: the first pair's second slot, then the first slots
-    auto slot = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * kTile + row; };
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+    // this warp's piece; this lane's row, its first four of elements and the next ones' distance
+    const int sub = SPLIT ? blockIdx.y : blockIdx.y * kMergeWarps + warp;
+    constexpr int kStep = BY_ROW ? 32 : 4;
+    const int row = BY_ROW ? sub : sub / (LAT / 64) * 8 + (lane & 7);
+    const int four = BY_ROW ? lane : sub % (LAT / 64) * 16 + (lane >> 3);
+    const bool any_row = (BY_ROW ? row : row & ~7) < meta.w;
+    const int t0 = p.starts ? __ldg(p.starts + meta.x) : meta.x;
+    // part i: the first worker's second slot, then the first slots
+    auto slot = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * R; };
+    float M = -INFINITY, l = 0.f, acc[kN][4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float acc[V][4], l = 0.f;
+    for (int k = 0; k < kN; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+    constexpr int kStride = SPLIT ? kMergeWarps : 1;
+    for (int i = SPLIT ? warp : 0; any_row && i < parts; i += 2 * kStride) {
+        float2 ml[2];
+        float4 o[2][kN];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < parts; ++i) {
-        const float2 ml = p.part_ml[slot(i)];
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(i) * LAT) + lane;
-        float4 o[V];
+        for (int h = 0; h < 2; ++h) {
+            const bool there = i + h * kStride < parts;
+            const size_t at = slot(there ? i + h * kStride : i);
+            ml[h] = there ? p.part_ml[at + row] : make_float2(-INFINITY, 0.f);
+            const float4* src = reinterpret_cast<const float4*>(p.part_o) + at * kFours;
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = src[32 * k];
-        // a partial that saw nothing weighs nothing (its maximum is -inf)
-        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        l += ml.y * w;
+            for (int k = 0; k < kN; ++k) {
+                const int f = four + kStep * k;
+                o[h][k] = there ? src[BY_ROW ? row * kFours + f : f * R + row] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        const float top = fmaxf(M, fmaxf(ml[0].x, ml[1].x));
+        // a part that saw nothing weighs nothing (its maximum is -inf)
+        const float w = M == -INFINITY ? 0.f : ex2(M - top), a = ml[0].x == -INFINITY ? 0.f : ex2(ml[0].x - top);
+        const float b = ml[1].x == -INFINITY ? 0.f : ex2(ml[1].x - top);
+        M = top;
+        l = l * w + ml[0].y * a + ml[1].y * b;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            acc[k][0] += o[k].x * w;
-            acc[k][1] += o[k].y * w;
-            acc[k][2] += o[k].z * w;
-            acc[k][3] += o[k].w * w;
+        for (int k = 0; k < kN; ++k) {
+            acc[k][0] = acc[k][0] * w + o[0][k].x * a + o[1][k].x * b;
+            acc[k][1] = acc[k][1] * w + o[0][k].y * a + o[1][k].y * b;
+            acc[k][2] = acc[k][2] * w + o[0][k].z * a + o[1][k].z * b;
+            acc[k][3] = acc[k][3] * w + o[0][k].w * a + o[1][k].w * b;
         }
     }
-    const SeqInfo q = seq_info(p, meta.x, false);
-    const int r = meta.y * kTile + row;
-    float none = 0.f;                        // the result of a row without weight
-    if (l == 0.f) {
-        uint32_t seen[4];
-        if (seen_nodes(p, q.t0, row_node(p, r), nullptr, seen)) {
-            bool any = q.base > 0;
-            for (int k = 0; k < 4; ++k) any = any || (seen[k] & low_bits(q.L - 32 * k)) != 0u;
-            if (any) none = __uint_as_float(0x7fffffffu);
+    if constexpr (SPLIT) {
+        __shared__ float4 s_acc[kMergeWarps][kN][32];
+        __shared__ float2 s_ml[kMergeWarps][32];
+#pragma unroll
+        for (int k = 0; k < kN; ++k) s_acc[warp][k][lane] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+        s_ml[warp][lane] = make_float2(M, l);
+        __syncthreads();
+        M = fmaxf(fmaxf(s_ml[0][lane].x, s_ml[1][lane].x), fmaxf(s_ml[2][lane].x, s_ml[3][lane].x));
+        l = 0.f;
+        acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
+        // (warp k joins the warps' k-th fours)
+#pragma unroll
+        for (int q = 0; q < kMergeWarps; ++q) {
+            const float2 ml = s_ml[q][lane];
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            l += ml.y * w;
+            if (warp < kN) {
+                const float4 o = s_acc[q][warp < kN ? warp : 0][lane];
+                acc[0][0] += o.x * w;
+                acc[0][1] += o.y * w;
+                acc[0][2] += o.z * w;
+                acc[0][3] += o.w * w;
+            }
         }
     }
-    const float inv = 1.f / l;
-    uint2* dst = reinterpret_cast<uint2*>(p.out + ((size_t)q.t0 * p.H + r) * LAT) + lane;
+    if (row >= meta.w) return;
+    const int r = meta.y * R + row;
+    const float none = l == 0.f ? weightless(p, meta.x, r) : 0.f, inv = 1.f / l;
+    uint2* dst = reinterpret_cast<uint2*>(p.out + ((size_t)t0 * p.H + r) * LAT);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
+    for (int k = 0; k < (SPLIT ? 1 : kN); ++k) {
+        if (SPLIT && warp >= kN) break;
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = l == 0.f ? none : acc[k][e] * inv;
-        dst[32 * k] = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        dst[four + kStep * (SPLIT ? warp : k)] = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
 }
 
@@ -1113,71 +942,45 @@ int check_latent_shape(int num_seqs, int max_nodes, int H, int L, int R)
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The kernel that serves a shape, by its rows, and the workspace: partial outputs, their
+// (max, sum) and the table of them.
 struct LatentPlan {
-    int pairs;
+    bool few;
+    int workers, rows;          // CTAs or pairs of them, rows of their tiles
     size_t o, ml, meta, total;
 };
 
-LatentPlan latent_plan(int L)
+LatentPlan latent_plan(int max_nodes, int H, int L)
 {
     LatentPlan t;
-    t.pairs = std::max(1, num_sms_current() / 2);
-    const size_t slots = (size_t)t.pairs * 2 * kTile;
+    const int sms = num_sms_current();
+    t.few = max_nodes * H <= kLatentFew;
+    t.rows = t.few ? kLatentFew : kTile;
+    t.workers = std::min(kMaxWorkers, t.few ? sms : std::max(1, sms / 2));
+    // (the rows of all workers' tiles are as many by either, so that a workspace for more
+    // nodes serves fewer)
+    const size_t slots = (size_t)std::max(2, sms) * 2 * kLatentFew;
     t.o = 0;
     t.ml = t.o + up256(slots * L * sizeof(float));
     t.meta = t.ml + up256(slots * sizeof(float2));
-    t.total = t.meta + up256((size_t)t.pairs * sizeof(int4));
+    t.total = t.meta + up256((size_t)sms * sizeof(int4));
     return t;
-}
-
-// Rows of W elements, as boxes of box_rows rows x box_cols 64-element columns with the
-// 128-byte swizzle: column by column in shared memory.
-int column_map(CUtensorMap* map, const void* base, long long rows, int W, int cols, int box_rows, int box_cols)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 enc;
-    if (int rc = map_encoder(enc)) return rc;
-    cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols};
-    cuuint64_t strides[2] = {(cuuint64_t)W * 2, 128};
-    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_cols};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? KV_OK
-               : KV_ERR_CUDA;
-}
-
-// The same rows as they are, in boxes of 64 elements: of the one that starts at W - R, what
-// lies behind the row is zeros.
-int row_map(CUtensorMap* map, const void* base, long long rows, int W, int box_rows)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 enc;
-    if (int rc = map_encoder(enc)) return rc;
-    cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)W * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? KV_OK
-               : KV_ERR_CUDA;
 }
 
 std::mutex g_latent_mu;
 
 template <int LAT>
-int launch_latent(const LatentParams& p, const void* q, const void* cache, cudaStream_t st)
+int launch_many(const LatentParams& p, const void* q, const void* cache, cudaStream_t st)
 {
     using G = Geo<LAT>;
     const int W = LAT + p.R;
     const long long qrows = (long long)p.total * p.H, krows = (long long)p.num_blocks * kBlock;
     CUtensorMap mq, mqr, mk, mkr, mv;
-    if (int rc = column_map(&mq, q, qrows, W, G::kCols, kRows, 4)) return rc;
-    if (int rc = row_map(&mqr, q, qrows, W, kRows)) return rc;
-    if (int rc = column_map(&mk, cache, krows, W, G::kCols, 8, 4)) return rc;
-    if (int rc = row_map(&mkr, cache, krows, W, kBlock)) return rc;
-    if (int rc = column_map(&mv, cache, krows, W, G::kCols, kBlock, 2)) return rc;
+    if (int rc = latent_column_map(&mq, q, qrows, W, G::kCols, kRows, 4)) return rc;
+    if (int rc = latent_row_map(&mqr, q, qrows, W, kRows)) return rc;
+    if (int rc = latent_column_map(&mk, cache, krows, W, G::kCols, 8, 4)) return rc;
+    if (int rc = latent_row_map(&mkr, cache, krows, W, kBlock)) return rc;
+    if (int rc = latent_column_map(&mv, cache, krows, W, G::kCols, kBlock, 2)) return rc;
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KV_ERR_CUDA;
@@ -1194,21 +997,83 @@ int launch_latent(const LatentParams& p, const void* q, const void* cache, cudaS
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * p.pairs));
+    cfg.gridDim = dim3((unsigned)(2 * p.workers));
     cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = G::kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_latent_kernel<LAT>, mq, mqr, mk, mkr, mv, p) != cudaSuccess) return KV_ERR_CUDA;
-    const int rows = std::min(p.max_nodes * p.H, kTile);
-    cfg.gridDim = dim3((unsigned)p.pairs, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps));
+    return cudaLaunchKernelEx(&cfg, paged_latent_kernel<LAT>, mq, mqr, mk, mkr, mv, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+template <int LAT, bool BY_ROW, bool SPLIT>
+int launch_merge(const LatentParams& p, int tiles, int rows, cudaStream_t st)
+{
+    const int pieces = BY_ROW ? rows : (rows + 7) / 8 * (LAT / 64);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)(SPLIT ? pieces : (pieces + kMergeWarps - 1) / kMergeWarps));
     cfg.blockDim = dim3(kMergeWarps * 32);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, paged_latent_merge_kernel<LAT>, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_latent_merge_kernel<LAT, BY_ROW, SPLIT>, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+template <int LAT>
+int launch_all(const LatentParams& p, bool few, const void* q, const void* cache, cudaStream_t st)
+{
+    if (few) {
+        if (latent_small_launch(p, q, cache, LAT, st) != cudaSuccess) return KV_ERR_CUDA;
+    } else if (int rc = launch_many<LAT>(p, q, cache, st)) {
+        return rc;
+    }
+    // the tiles that may have parts: no more than there are, nor than workers
+    const long long all = (long long)p.B * ((p.max_nodes * p.H + p.tile_rows - 1) / p.tile_rows);
+    const int tiles = (int)std::min<long long>(all, p.workers), rows = std::min(p.max_nodes * p.H, p.tile_rows);
+    const bool split = p.workers / tiles >= kMergeSplit;
+    if (few)
+        return split ? launch_merge<LAT, true, true>(p, tiles, rows, st) : launch_merge<LAT, true, false>(p, tiles, rows, st);
+    return split ? launch_merge<LAT, false, true>(p, tiles, rows, st) : launch_merge<LAT, false, false>(p, tiles, rows, st);
 }
 
 }  // namespace
+
+// Rows of W elements, as boxes of box_rows rows x box_cols 64-element columns with the
+// 128-byte swizzle: column by column in shared memory.
+int latent_column_map(CUtensorMap* map, const void* base, long long rows, int W, int cols, int box_rows, int box_cols)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int rc = map_encoder(enc)) return rc;
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols};
+    cuuint64_t strides[2] = {(cuuint64_t)W * 2, 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_cols};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KV_OK
+               : KV_ERR_CUDA;
+}
+
+// The same rows as they are, in boxes of 64 elements: of the one that starts at W - R, what
+// lies behind the row is zeros.
+int latent_row_map(CUtensorMap* map, const void* base, long long rows, int W, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int rc = map_encoder(enc)) return rc;
+    cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)W * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KV_OK
+               : KV_ERR_CUDA;
+}
 
 int latent_read_error(unsigned* flags, long long* detail) { return g_launched.take_error(g_latent_err, flags, detail); }
 
@@ -1224,7 +1089,7 @@ extern "C" int paged_latent_workspace_bytes(int num_seqs, int max_nodes, int num
     if (int rc = check_latent_shape(num_seqs, max_nodes, num_q_heads, latent_dim, rope_dim)) return rc;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
-    *bytes = latent_plan(latent_dim).total;
+    *bytes = latent_plan(max_nodes, num_q_heads, latent_dim).total;
     return KV_OK;
 }
 
@@ -1249,7 +1114,7 @@ extern "C" int paged_latent_attention(void* out, const void* q, const void* cach
         (long long)max_blocks_per_seq * kBlock >= INT_MAX ||
         ((long long)max_blocks_per_seq + 2 * kExtraPages) * num_seqs >= INT_MAX / tiles)
         return KV_ERR_UNSUPPORTED;
-    const LatentPlan t = latent_plan(latent_dim);
+    const LatentPlan t = latent_plan(max_nodes, num_q_heads, latent_dim);
     if (workspace_bytes < t.total) return KV_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     LatentParams p;
@@ -1259,9 +1124,6 @@ extern "C" int paged_latent_attention(void* out, const void* q, const void* cach
     p.ctx = context_lens;
     p.starts = node_starts;
     p.parents = node_starts ? parents : nullptr;
-    p.part_o = reinterpret_cast<float*>(ws + t.o);
-    p.part_ml = reinterpret_cast<float2*>(ws + t.ml);
-    p.meta = reinterpret_cast<int4*>(ws + t.meta);
     p.B = num_seqs;
     p.total = total_nodes;
     p.max_nodes = max_nodes;
@@ -1269,11 +1131,15 @@ extern "C" int paged_latent_attention(void* out, const void* q, const void* cach
     p.R = rope_dim;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
-    p.pairs = t.pairs;
     p.h_magic = num_q_heads == 1 ? 0u : 0xffffffffu / (uint32_t)num_q_heads + 1u;
     p.sl2 = scale * 1.4426950408889634f;
     p.test_stall = test_stall_cycles();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     g_launched.note();
-    return latent_dim == 512 ? launch_latent<512>(p, q, cache, st) : launch_latent<256>(p, q, cache, st);
+    p.part_o = reinterpret_cast<float*>(ws + t.o);
+    p.part_ml = reinterpret_cast<float2*>(ws + t.ml);
+    p.meta = reinterpret_cast<int4*>(ws + t.meta);
+    p.workers = t.workers;
+    p.tile_rows = t.rows;
+    return latent_dim == 512 ? launch_all<512>(p, t.few, q, cache, st) : launch_all<256>(p, t.few, q, cache, st);
 }
