@@ -62,8 +62,8 @@ struct Geo {
     static constexpr int kGroups = kCols / 4;            // groups of K columns; the rotary part is one more
     static constexpr int kHalves = LAT / 256;            // products of N 256 for a page
     static constexpr int kSlots = LAT == 512 ? 1 : 2;    // chunks of K and of V in shared memory
-    static constexpr int kWeighWarps = 8, kKWarp = 8, kVWarp = 9, kMmaWarp = 10;
-    static constexpr int kThreads = 12 * 32;
+    static constexpr int kWeighWarps = 8, kKWarp = 8, kVWarp = 11, kMmaWarp = 13;
+    static constexpr int kThreads = 16 * 32;             // (a warp a group of K, a half of V; one idle)
     static constexpr int kQBytes = (kCols + 1) * kRows * 128;
     static constexpr int kGroupBytes = kRows * 4 * 128;  // 64 tokens x 4 columns
     static constexpr int kRopeBytes = kRows * 128;
@@ -84,8 +84,8 @@ struct Geo {
     static constexpr int B_KFREE = B_KFULL + kSlots * kG1;       // + slot * kG1 + group
     static constexpr int B_VREADY = B_KFREE + kSlots * kG1;      // (L) + slot * 2 + half of the chunk: V of both CTAs
     static constexpr int B_VFREE = B_VREADY + kSlots * 2;        // likewise: its products are done
-    static constexpr int B_VFIX = B_VFREE + kSlots * 2;          // a half that has to be cleared has landed here
-    static constexpr int B_SFULL = B_VFIX + 1;                   // + buffer: scores
+    static constexpr int B_VFIX = B_VFREE + kSlots * 2;          // + half: it has to be cleared and has landed here
+    static constexpr int B_SFULL = B_VFIX + 2;                   // + buffer: scores
     static constexpr int B_SFREE = B_SFULL + 2;                  // (L) + buffer: both have read them
     static constexpr int B_PFULL = B_SFREE + 2;                  // (L) weights of both CTAs
     static constexpr int B_OFREE = B_PFULL + 1;                  // (L) both have read the accumulators
@@ -94,8 +94,8 @@ struct Geo {
     static constexpr int B_STALL = B_END + 2;                    // nothing arrives (the test hook)
     static constexpr int kNumBars = B_STALL + 1;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kBadOff = kMiscOff + (M_WORDS * 4 + 15) / 16 * 16;      // [2][CTA of the pair][4] words
-    static constexpr int kRedOff = kBadOff + 64;                 // [4][64] floats: maxima, sums
+    static constexpr int kBadOff = kMiscOff + (M_WORDS * 4 + 15) / 16 * 16;      // [2][CTA of the pair][half][4] words
+    static constexpr int kRedOff = kBadOff + 128;                 // [4][64] floats: maxima, sums
     static constexpr int kEnd = kRedOff + 4 * kRows * 4;
     static constexpr int kSmem = kEnd;
     static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -255,7 +255,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         mbar_init(bar(G::B_PFULL), 2 * G::kWeighWarps);
         mbar_init(bar(G::B_OFREE), 2 * G::kWeighWarps);
-        mbar_init(bar(G::B_VFIX), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(bar(G::B_VFIX + i), 1);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
         fence_mbar_init();
@@ -276,20 +276,22 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     umma::fence_after_sync();
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
-    if (warp == G::kKWarp) {
-        // ------------------------------------------------------------- Q and K
+    if (warp >= G::kKWarp && warp < G::kKWarp + G::kG1) {
+        // ------------------------- Q and K: a warp for each group of K's columns
+        const int k = warp - G::kKWarp;
+        const bool rope = k == G::kGroups;
         int g = 0;
         bool ok = true;
         for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
-            if (w.seg > 0) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((w.seg - 1) & 1), misc);
+            if (k == 0 && w.seg > 0) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((w.seg - 1) & 1), misc);
             if (!ok) break;
-            if (lane == 0) {
+            if (k == 0 && lane == 0) {
                 if (rank == 0) mbar_arrive_expect_tx(bar(G::B_QFULL), 2u * G::kQBytes);
                 const int row = w.q.t0 * p.H + w.tile * kTile + (int)rank * kRows;
                 const uint32_t qf = lead(G::B_QFULL);
 #pragma unroll
-                for (int k = 0; k < G::kGroups; ++k)
-                    tma2_load_3d(sb + (uint32_t)(G::kQOff + k * 4 * kRows * 128), &tm_q, 0, row, 4 * k, qf);
+                for (int x = 0; x < G::kGroups; ++x)
+                    tma2_load_3d(sb + (uint32_t)(G::kQOff + x * 4 * kRows * 128), &tm_q, 0, row, 4 * x, qf);
                 tma2_load_2d(sb + (uint32_t)(G::kQOff + G::kCols * kRows * 128), &tm_qr, LAT, row, qf);
             }
             const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
@@ -306,35 +308,30 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 const int id8 = __shfl_sync(kFull, ids, (c & 3) * kPages + (lane & 7));
                 const bool in = lane < w.chunk_pages(c) && lane < kPages;
                 const bool valid = in && id8 >= 0 && id8 < p.num_blocks;
-                if (in && !valid && rank == 0) raise_flag(&g_latent_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, id8);
+                if (in && !valid && rank == 0 && k == 0) raise_flag(&g_latent_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, id8);
                 const unsigned all = __ballot_sync(kFull, valid);
                 const int mypage = 4 * (int)rank + ((lane & 7) >> 1);
                 const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + mypage);
                 const bool mine = lane < 8 && ((all >> mypage) & 1u);
-                const int n = __popc(all), sl = slot(g);
-#pragma unroll
-                for (int k = 0; k <= G::kGroups; ++k) {
-                    const int b = sl * G::kG1 + k;
-                    if (g >= G::kSlots && !wait_warp(bar(G::B_KFREE + b), pass(g) ^ 1u, misc)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool rope = k == G::kGroups;
-                    if (lane == 0 && rank == 0) {
-                        if (n > 0) mbar_arrive_expect_tx(bar(G::B_KFULL + b), (uint32_t)(n * (rope ? 2048 : 8192)));
-                        else mbar_arrive(bar(G::B_KFULL + b));
-                    }
-                    __syncwarp();
-                    const uint32_t kb = sb + (uint32_t)(G::kKOff + sl * G::kKSlot);
-                    const uint32_t kf = lead(G::B_KFULL + b);
-                    if (!rope) {
-                        if (mine)
-                            tma2_load_3d(kb + (uint32_t)(k * G::kGroupBytes + lane * 4096), &tm_k, 0,
-                                         id * kBlock + 8 * (lane & 1), 4 * k, kf);
-                    } else if (mine && !(lane & 1)) {
-                        tma2_load_2d(kb + (uint32_t)(G::kGroups * G::kGroupBytes + (lane >> 1) * 2048), &tm_kr, LAT,
-                                     id * kBlock, kf);
-                    }
+                const int n = __popc(all), sl = slot(g), b = sl * G::kG1 + k;
+                if (g >= G::kSlots && !wait_warp(bar(G::B_KFREE + b), pass(g) ^ 1u, misc)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0 && rank == 0) {
+                    if (n > 0) mbar_arrive_expect_tx(bar(G::B_KFULL + b), (uint32_t)(n * (rope ? 2048 : 8192)));
+                    else mbar_arrive(bar(G::B_KFULL + b));
+                }
+                __syncwarp();
+                const uint32_t kb = sb + (uint32_t)(G::kKOff + sl * G::kKSlot);
+                const uint32_t kf = lead(G::B_KFULL + b);
+                if (!rope) {
+                    if (mine)
+                        tma2_load_3d(kb + (uint32_t)(k * G::kGroupBytes + lane * 4096), &tm_k, 0,
+                                     id * kBlock + 8 * (lane & 1), 4 * k, kf);
+                } else if (mine && !(lane & 1)) {
+                    tma2_load_2d(kb + (uint32_t)(G::kGroups * G::kGroupBytes + (lane >> 1) * 2048), &tm_kr, LAT,
+                                 id * kBlock, kf);
                 }
             }
         }
@@ -345,9 +342,10 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             while (clock64() - t0 < 400000) __nanosleep(1000);
         }
         __syncwarp();
-    } else if (warp == G::kVWarp) {
-        // ------------- V; and what of it must not be multiplied: rows behind the context, and
+    } else if (warp == G::kVWarp || warp == G::kVWarp + 1) {
+        // ------------- V, a warp for each half of a chunk; and what of it must not be multiplied: rows behind the context, and
         // infinities and NaN of drafted rows
+        const int h = warp - G::kVWarp;
         int g = 0, fixes = 0;
         bool ok = true;
         for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
@@ -367,74 +365,71 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 const int sl = slot(g);
                 const bool fix = w.drafted(c);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // lanes 0 .. 4 * halves - 1: page and 256-column block
-                    const int page = 4 * h + lane / G::kHalves % 4, t = lane % G::kHalves;
-                    const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + page);
-                    const bool mine = lane < 4 * G::kHalves && page < w.chunk_pages(c) && id >= 0 && id < p.num_blocks;
-                    const int n = __popc(__ballot_sync(kFull, mine));
-                    const int b = sl * 2 + h;
-                    if (g >= G::kSlots && !wait_warp(bar(G::B_VFREE + b), pass(g) ^ 1u, misc)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t ready = lead(G::B_VREADY + b), full = fix ? bar(G::B_VFIX) : ready;
-                    if (lane == 0) {
-                        // (the first CTA expects both CTAs' bytes where they count there)
-                        if (fix) mbar_arrive_expect_tx(full, (uint32_t)(n * 4096));
-                        else if (rank == 0) mbar_arrive_expect_tx(bar(G::B_VREADY + b), (uint32_t)(n * 8192));
-                        else arrive_remote(ready);
-                    }
-                    __syncwarp();
-                    if (mine)
-                        tma2_load_3d(sb + (uint32_t)(G::kVOff + sl * G::kVSlot + page * G::kVPage + t * 4096), &tm_v, 0,
-                                     id * kBlock, 4 * t + 2 * (int)rank, full);
-                    if (!fix) continue;
-                    if (!wait_warp(full, (uint32_t)(fixes++ & 1), misc)) {
-                        ok = false;
-                        break;
-                    }
-                    const int p0 = (w.j + c * kPages) * kBlock;
-                    const int lo = max(64 * h, w.q.base - p0), hi = min(64 * (h + 1), w.chunk_pages(c) * kBlock);
-                    // a row's 16-byte pieces, 16 of each 256-column block
-                    for (int r = lo; r < hi; ++r) {
-                        const bool tail = p0 + r >= w.q.L;
-                        for (int x = lane; x < 16 * G::kHalves; x += 32) {
-                            const int tt = x >> 4, col = (x >> 3) & 1, ch = x & 7, rr = r & 15;
-                            const uint32_t at = sb + (uint32_t)(G::kVOff + sl * G::kVSlot + (r >> 4) * G::kVPage +
-                                                                tt * 4096 + col * 2048 + rr * 128 + ((ch ^ (rr & 7)) * 16));
-                            uint32_t v[4] = {0u, 0u, 0u, 0u}, any = 0u;
-                            if (!tail) {
-                                lds128(v, at);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint32_t m = __vcmpeq2(v[k] & 0x7f807f80u, 0x7f807f80u);
-                                    v[k] &= ~m;
-                                    any |= m;
-                                }
-                            }
-                            if (tail || any) sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
-                            const int a = p0 + r - w.q.base;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) bad[k] |= any && (a >> 5) == k ? 1u << (a & 31) : 0u;
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    // both CTAs' rows have all columns, so both are told
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        bad[k] = __reduce_or_sync(kFull, bad[k]);
-                        if (lane < 2) {
-                            const uint32_t at = sb + (uint32_t)(G::kBadOff + ((buf * 2 + (int)rank) * 4 + k) * 4);
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)lane)), "r"(bad[k])
-                                         : "memory");
-                        }
-                    }
-                    fence_cluster();
-                    __syncwarp();
-                    if (lane == 0) arrive_remote(ready);
+                // lanes 0 .. 4 * halves - 1: page and 256-column block
+                const int page = 4 * h + lane / G::kHalves % 4, t = lane % G::kHalves;
+                const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + page);
+                const bool mine = lane < 4 * G::kHalves && page < w.chunk_pages(c) && id >= 0 && id < p.num_blocks;
+                const int n = __popc(__ballot_sync(kFull, mine));
+                const int b = sl * 2 + h;
+                if (g >= G::kSlots && !wait_warp(bar(G::B_VFREE + b), pass(g) ^ 1u, misc)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t ready = lead(G::B_VREADY + b), full = fix ? bar(G::B_VFIX + h) : ready;
+                if (lane == 0) {
+                    // (the first CTA expects both CTAs' bytes where they count there)
+                    if (fix) mbar_arrive_expect_tx(full, (uint32_t)(n * 4096));
+                    else if (rank == 0) mbar_arrive_expect_tx(bar(G::B_VREADY + b), (uint32_t)(n * 8192));
+                    else arrive_remote(ready);
+                }
+                __syncwarp();
+                if (mine)
+                    tma2_load_3d(sb + (uint32_t)(G::kVOff + sl * G::kVSlot + page * G::kVPage + t * 4096), &tm_v, 0,
+                                 id * kBlock, 4 * t + 2 * (int)rank, full);
+                if (!fix) continue;
+                if (!wait_warp(full, (uint32_t)(fixes++ & 1), misc)) {
+                    ok = false;
+                    break;
+                }
+                const int p0 = (w.j + c * kPages) * kBlock;
+                const int lo = max(64 * h, w.q.base - p0), hi = min(64 * (h + 1), w.chunk_pages(c) * kBlock);
+                // a row's 16-byte pieces, 16 of each 256-column block
+                for (int r = lo; r < hi; ++r) {
+                    const bool tail = p0 + r >= w.q.L;
+                    for (int x = lane; x < 16 * G::kHalves; x += 32) {
+                        const int tt = x >> 4, col = (x >> 3) & 1, ch = x & 7, rr = r & 15;
+                        const uint32_t at = sb + (uint32_t)(G::kVOff + sl * G::kVSlot + (r >> 4) * G::kVPage +
+                                                            tt * 4096 + col * 2048 + rr * 128 + ((ch ^ (rr & 7)) * 16));
+                        uint32_t v[4] = {0u, 0u, 0u, 0u}, any = 0u;
+                        if (!tail) {
+                            lds128(v, at);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t m = __vcmpeq2(v[k] & 0x7f807f80u, 0x7f807f80u);
+                                v[k] &= ~m;
+                                any |= m;
+                            }
+                        }
+                        if (tail || any) sts128(at, make_uint4(v[0], v[1], v[2], v[3]));
+                        const int a = p0 + r - w.q.base;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) bad[k] |= any && (a >> 5) == k ? 1u << (a & 31) : 0u;
+                    }
+                }
+                fence_proxy_async_smem();
+                // both CTAs' rows have all columns, so both are told
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bad[k] = __reduce_or_sync(kFull, bad[k]);
+                    if (lane < 2) {
+                        const uint32_t at = sb + (uint32_t)(G::kBadOff + (((buf * 2 + (int)rank) * 2 + h) * 4 + k) * 4);
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)lane)), "r"(bad[k])
+                                     : "memory");
+                    }
+                }
+                fence_cluster();
+                __syncwarp();
+                if (lane == 0) arrive_remote(ready);
             }
         }
         if (!ok) {
@@ -530,7 +525,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             mbar_wait_bounded(bar(G::B_END + 1), 0u, kWaitLimit);
         }
         __syncwarp();
-    } else {
+    } else if (warp < G::kWeighWarps) {
         // --------------------------------------------------- weights and output
         const int wq = warp & 3, wg = warp >> 2;
         const int row = (wq & 1) * 32 + lane;    // of the CTA's 64
@@ -717,7 +712,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             uint32_t back = 0u;
             if (w.drafted(nc - 1)) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) back |= badw[buf * 8 + k];
+                for (int k = 0; k < 16; ++k) back |= badw[buf * 16 + k];
             }
             if (__any_sync(kFull, in)) {
 #pragma unroll 1
@@ -732,7 +727,8 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     for (int k = 0; k < 16; ++k) v[k] = live ? __uint_as_float(o[k]) * z : 0.f;
                     if (back && live) {
                         for (int k4 = 0; k4 < 4; ++k4) {
-                            uint32_t b = (badw[buf * 8 + k4] | badw[buf * 8 + 4 + k4]) & bits_at(seen, 32 * k4);
+                            uint32_t b = (badw[buf * 16 + k4] | badw[buf * 16 + 4 + k4] | badw[buf * 16 + 8 + k4] | badw[buf * 16 + 12 + k4]) &
+                                         bits_at(seen, 32 * k4);
                             for (; b != 0u; b &= b - 1u) {
                                 const int pos = w.q.base + 32 * k4 + __ffs(b) - 1;
                                 const int blk = __ldg(p.bt + (size_t)w.s * p.max_blocks + pos / kBlock);
