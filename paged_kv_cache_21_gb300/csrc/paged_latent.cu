@@ -54,6 +54,7 @@ namespace {
 constexpr int kPages = 8;                       // pages of a chunk
 constexpr int kRows = 64;                       // rows of a CTA
 constexpr int kTile = 2 * kRows;                // rows of a pair
+constexpr int kAheadChunks = 2;                 // chunks that are brought to L2 ahead of their copies
 constexpr int kMinPages = 16;                   // least range of a pair of CTAs
 constexpr int kExtraPages = 32;                 // what a (sequence, tile) costs beside its pages
 template <int LAT>
@@ -525,6 +526,28 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             mbar_wait_bounded(bar(G::B_END + 1), 0u, kWaitLimit);
         }
         __syncwarp();
+    } else if (warp == G::kMmaWarp + 2) {
+        // --------- this CTA's pages of the chunks to come, to L2, a few chunks ahead of the copies
+        int g = 0;
+        bool ok = true;
+        for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
+            const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
+            const int nc = w.chunks();
+            for (int c = 0; ok && c < nc; ++c, ++g) {
+                const int from = c == 0 ? 1 : c + kAheadChunks, to = min(nc, c + kAheadChunks + 1);
+                for (int a = from; a < to; ++a) {
+                    const int page = a * kPages + 4 * (int)rank + (lane & 3);
+                    const int id = page < w.np ? __ldg(row + page) : -1;
+                    const bool valid = id >= 0 && id < p.num_blocks;
+                    const char* src = reinterpret_cast<const char*>(p.cache + (size_t)(valid ? id : 0) * kBlock * (LAT + p.R));
+                    const int bytes = kBlock * (LAT + p.R) * 2;
+                    if (valid)
+                        for (int x = (lane >> 2) * 128; x < bytes; x += 8 * 128)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + x));
+                }
+                ok = wait_warp(bar(G::B_SFULL + (g & 1)), (uint32_t)((g >> 1) & 1), misc);
+            }
+        }
     } else if (warp < G::kWeighWarps) {
         // --------------------------------------------------- weights and output
         const int wq = warp & 3, wg = warp >> 2;
