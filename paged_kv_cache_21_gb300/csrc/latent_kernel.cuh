@@ -24,8 +24,9 @@ constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
 constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
 
 // misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
-// per worker, first sequence, tile and page; that sequence's nodes, context and first node
-enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_T0, M_J0, M_N0, M_L0, M_NODE0, M_WORDS };
+// per worker, first sequence, tile and page; that sequence's nodes, context and first node;
+// chunks whose scores have been seen
+enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_T0, M_J0, M_N0, M_L0, M_NODE0, M_SEEN, M_WORDS };
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -55,6 +56,27 @@ __device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x)
         "add.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
         : "+f"(a), "+f"(b)
         : "r"(x));
+}
+
+// Wait until the scores of chunk g have been seen: a count, not a barrier, whose phases one
+// that lags behind could mistake for each other.
+__device__ __forceinline__ bool wait_seen(int g, volatile int* misc)
+{
+    const long long t0 = clock64();
+    while (misc[M_SEEN] <= g) {
+        if (misc[M_ABORT] || clock64() - t0 > kWaitLimit) return false;
+        __nanosleep(100);
+    }
+    return true;
+}
+
+// Bring page `id` of the cache to L2: this lane's lines of it, one of 8 lanes'.
+__device__ __forceinline__ void prefetch_page(const LatentParams& p, int id, int row_elems, int eighth)
+{
+    if (id < 0 || id >= p.num_blocks) return;
+    const char* src = reinterpret_cast<const char*>(p.cache + (size_t)id * kBlock * row_elems);
+    for (int x = eighth * 128; x < kBlock * row_elems * 2; x += 8 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + x));
 }
 
 // Sequences without a context get zeros for their nodes (threads 0 .. nthreads - 1 of the

@@ -54,7 +54,7 @@ namespace {
 constexpr int kPages = 8;                       // pages of a chunk
 constexpr int kRows = 64;                       // rows of a CTA
 constexpr int kTile = 2 * kRows;                // rows of a pair
-constexpr int kAheadChunks = 2;                 // chunks that are brought to L2 ahead of their copies
+constexpr int kAheadChunks = 1;                 // chunks that are brought to L2 ahead of their copies
 constexpr int kMinPages = 16;                   // least range of a pair of CTAs
 constexpr int kExtraPages = 32;                 // what a (sequence, tile) costs beside its pages
 template <int LAT>
@@ -259,6 +259,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int i = 0; i < 2; ++i) mbar_init(bar(G::B_VFIX + i), 1);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
+        misc[M_SEEN] = 0;
         fence_mbar_init();
     }
     pdl_launch_dependents();
@@ -533,20 +534,13 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
             const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
             const int nc = w.chunks();
-            for (int c = 0; ok && c < nc; ++c, ++g) {
-                const int from = c == 0 ? 1 : c + kAheadChunks, to = min(nc, c + kAheadChunks + 1);
-                for (int a = from; a < to; ++a) {
-                    const int page = a * kPages + 4 * (int)rank + (lane & 3);
-                    const int id = page < w.np ? __ldg(row + page) : -1;
-                    const bool valid = id >= 0 && id < p.num_blocks;
-                    const char* src = reinterpret_cast<const char*>(p.cache + (size_t)(valid ? id : 0) * kBlock * (LAT + p.R));
-                    const int bytes = kBlock * (LAT + p.R) * 2;
-                    if (valid)
-                        for (int x = (lane >> 2) * 128; x < bytes; x += 8 * 128)
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + x));
-                }
-                ok = wait_warp(bar(G::B_SFULL + (g & 1)), (uint32_t)((g >> 1) & 1), misc);
+            // (the first chunks are copied at once)
+            for (int a = 1; ok && a < nc; ++a) {
+                if (a > kAheadChunks) ok = __all_sync(kFull, wait_seen(g + a - kAheadChunks - 1, misc));
+                const int page = a * kPages + 4 * (int)rank + (lane & 3);
+                if (ok) prefetch_page(p, page < w.np ? __ldg(row + page) : -1, LAT + p.R, lane >> 2);
             }
+            g += nc;
         }
     } else if (warp < G::kWeighWarps) {
         // --------------------------------------------------- weights and output
@@ -593,6 +587,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             for (int c = 0; c < nc; ++c) {
                 const int g = g0 + c;
                 ok = __all_sync(kFull, ok && wait_bar(bar(G::B_SFULL + (g & 1)), (uint32_t)((g >> 1) & 1), misc));
+                if (tid == 0) misc[M_SEEN] = g + 1;
                 umma::fence_after_sync();
                 if (!cta_live) {                 // nothing here weighs anything
                     // (an arrival before the last chunk's weights are used would count for them)

@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kPages = 4;                       // pages of a group
 constexpr int kRows = kLatentFew;
+constexpr int kAheadGroups = 1;                 // groups that are brought to L2 ahead of their copies
 constexpr int kMinPages = 8;                    // least range of a CTA
 constexpr int kExtraPages = 12;                 // what a sequence costs beside its pages
 
@@ -42,8 +43,8 @@ struct SmallGeo {
     static constexpr int kCols = LAT / 64, kCols1 = kCols + 1;   // 64-element columns; the rotary one
     static constexpr int kTiles = LAT / 128;             // products of M 128 for a page
     static constexpr int kSlots = LAT == 512 ? 2 : 4;    // groups in shared memory
-    static constexpr int kWeighWarps = 8, kCopyWarp = 8, kMmaWarp = 10;
-    static constexpr int kThreads = 12 * 32;
+    static constexpr int kWeighWarps = 8, kCopyWarp = 8, kMmaWarp = 12, kAheadWarp = 14;
+    static constexpr int kThreads = 16 * 32;             // (one warp is idle: registers go by four)
     static constexpr int kEight = kCols1 * 1024;         // eight tokens: [column][8 tokens][128 B]
     static constexpr int kPage = 2 * kEight;
     static constexpr int kSlot = kPages * kPage;
@@ -144,6 +145,7 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
         mbar_init(bar(G::B_OFREE), G::kWeighWarps);
         mbar_init(bar(G::B_STALL), 1);
         misc[M_ABORT] = 0;
+        misc[M_SEEN] = 0;
         fence_mbar_init();
     }
     pdl_launch_dependents();
@@ -158,13 +160,13 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
     umma::fence_after_sync();
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
-    if (warp == G::kCopyWarp || warp == G::kCopyWarp + 1) {
-        // --------------------- Q, and the pages: each of two warps every other one
-        const int part = warp - G::kCopyWarp;
+    if (warp >= G::kCopyWarp && warp < G::kCopyWarp + kPages) {
+        // --------------------- Q, and the pages: a warp for each of a group's
+        const int page = warp - G::kCopyWarp;
         int g = 0;
         bool ok = true;
         for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
-            if (part == 0) {
+            if (page == 0) {
                 if (w.seg > 0) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((w.seg - 1) & 1), misc);
                 if (!ok) break;
                 if (lane == 0) {
@@ -188,28 +190,24 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
                     ahead = at < w.np ? __ldg(row + at) : -1;
                 }
                 const int sl = slot(g);
-#pragma unroll
-                for (int k = 0; k < kPages / 2; ++k) {
-                    const int page = 2 * k + part;
-                    const int id = __shfl_sync(kFull, ids, (c & 7) * kPages + page);
-                    const bool in = page < w.chunk_pages(c), valid = in && id >= 0 && id < p.num_blocks;
-                    if (g >= G::kSlots && !wait_warp(bar(G::B_FREE + sl * kPages + page), pass(g) ^ 1u, misc)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        if (in && !valid) raise_flag(&g_latent_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, id);
-                        if (valid) mbar_arrive_expect_tx(bar(G::B_FULL + sl), (uint32_t)G::kPage);
-                        else mbar_arrive(bar(G::B_FULL + sl));
-                    }
-                    __syncwarp();
-                    if (valid && lane < 4) {
-                        // the page's two eights: latent columns, rotary column
-                        const uint32_t dst = sb + (uint32_t)(G::kRingOff + sl * G::kSlot + page * G::kPage + (lane & 1) * G::kEight);
-                        const int y = id * kBlock + 8 * (lane & 1);
-                        if (lane < 2) tma_load_3d(dst, &tm_k, 0, y, 0, bar(G::B_FULL + sl));
-                        else tma_load_2d(dst + (uint32_t)(G::kCols * 1024), &tm_kr, LAT, y, bar(G::B_FULL + sl));
-                    }
+                const int id = __shfl_sync(kFull, ids, (c & 7) * kPages + page);
+                const bool in = page < w.chunk_pages(c), valid = in && id >= 0 && id < p.num_blocks;
+                if (g >= G::kSlots && !wait_warp(bar(G::B_FREE + sl * kPages + page), pass(g) ^ 1u, misc)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (in && !valid) raise_flag(&g_latent_err, KV_DEVERR_BLOCK_OUT_OF_RANGE, id);
+                    if (valid) mbar_arrive_expect_tx(bar(G::B_FULL + sl), (uint32_t)G::kPage);
+                    else mbar_arrive(bar(G::B_FULL + sl));
+                }
+                __syncwarp();
+                if (valid && lane < 4) {
+                    // the page's two eights: latent columns, rotary column
+                    const uint32_t dst = sb + (uint32_t)(G::kRingOff + sl * G::kSlot + page * G::kPage + (lane & 1) * G::kEight);
+                    const int y = id * kBlock + 8 * (lane & 1);
+                    if (lane < 2) tma_load_3d(dst, &tm_k, 0, y, 0, bar(G::B_FULL + sl));
+                    else tma_load_2d(dst + (uint32_t)(G::kCols * 1024), &tm_kr, LAT, y, bar(G::B_FULL + sl));
                 }
             }
         }
@@ -292,7 +290,22 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
             mbar_wait_bounded(bar(G::B_END + 1), 0u, kWaitLimit);
         }
         __syncwarp();
-    } else {
+    } else if (warp == G::kAheadWarp) {
+        // ------------------ pages of the groups to come, to L2, a few groups ahead of the copies
+        int g = 0;
+        bool ok = true;
+        for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
+            const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
+            const int nc = w.chunks();
+            // (the first chunks are copied at once)
+            for (int a = G::kSlots; ok && a < nc; ++a) {
+                if (a > kAheadGroups) ok = __all_sync(kFull, wait_seen(g + a - kAheadGroups - 1, misc));
+                const int page = a * kPages + (lane & 3);
+                if (ok) prefetch_page(p, page < w.np ? __ldg(row + page) : -1, LAT + p.R, lane >> 2);
+            }
+            g += nc;
+        }
+    } else if (warp < G::kWeighWarps) {
         // --------------------------------------------------- weights and output
         const int wq = warp & 3, wg = warp >> 2;
         const int row = wq * 16 + (lane & 15);   // lanes 16..31 have none
@@ -337,6 +350,7 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
             for (int c = 0; c < nc; ++c) {
                 const int g = g0 + c;
                 ok = __all_sync(kFull, ok && wait_bar(bar(G::B_SFULL + (g & 1)), (uint32_t)((g >> 1) & 1), misc));
+                if (tid == 0) misc[M_SEEN] = g + 1;
                 umma::fence_after_sync();
                 float t[32];
                 const int np = w.chunk_pages(c), k0 = wg * 32;           // this thread's first token
