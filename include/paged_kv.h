@@ -696,8 +696,7 @@ int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers
  * i + rotary_dim / 2, or, with KV_ROTARY_INTERLEAVED, 2 i and 2 i + 1.  (The pages
  * say that positions are part of the cached key, not how; these entry points are
  * interfaces of this implementation.)  The angle is reduced by whole turns
- * exactly, in integers: positions up to 2^31 lose nothing but the rounding of
- * inv_freq, a float32, to 53 bits of a turn. */
+ * exactly, in integers: a position of p loses p 2^-64 turns.  inv_freq below 2^48. */
 #define KV_ROTARY_INTERLEAVED 1u
 
 /* How kv_rotary_frequencies scales the frequencies f_i = theta^(-2 i / rotary_dim)
@@ -737,8 +736,8 @@ int kv_rotary_frequencies(float* inv_freq, float* magnitude, int rotary_dim, dou
  * and slot_mapping, caches, kv_dtype and scales as kv_append; a token without a
  * slot (slot < 0) has its query turned and appends nothing.  Rotation in float32,
  * rounded once: to bfloat16, or K / k_scale to E4M3 (without a bfloat16 between).
- * head_dim and rotary_dim multiples of 16; strides multiples of 8, at least a
- * row.  One launch. */
+ * head_dim and rotary_dim multiples of 16, up to 512 and 256; strides multiples of 8,
+ * at least a row.  One launch. */
 int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                      void* k_cache, void* v_cache, const int64_t* slot_mapping,
@@ -774,7 +773,7 @@ int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q, int64_t q
  *                  num_q_heads == 0: none (NULL)
  * and slot_mapping, positions, inv_freq [rope_dim / 2], flags and magnitude as
  * kv_append_rotary (the whole of rope_dim is turned).  Every element is rounded
- * once.  latent_dim a multiple of 8 up to 1024, rope_dim of 16 up to 512; strides
+ * once.  latent_dim a multiple of 8 up to 1024, rope_dim of 16 up to 256; strides
  * multiples of 8, at least a vector (a token's at least its heads'). */
 int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
                      const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,

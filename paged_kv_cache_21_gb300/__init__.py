@@ -845,9 +845,37 @@ def _rows(name, t, dtype, shape, dev, inner=1):
     return t.data_ptr()
 
 
-def _stride(t, dim, least):
-    """Stride of a dimension; of one of a single element, what an array would have."""
-    return t.stride(dim) if t.shape[dim] > 1 else max(least, t.stride(dim) // 8 * 8)
+def _heads(name, t, dtype, shape, dev):
+    """(address, elements from one token to the next) of a [T, heads, D] tensor whose
+    tokens may be apart."""
+    T, n, D = shape
+    token, head, step = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and step == 1
+            and (head == D or n == 1)):
+        _rows(name, t, dtype, tuple(shape), dev, 2)
+    # (of one token, what a tensor of several would have at least)
+    return t.data_ptr(), token if T > 1 else n * D
+
+
+def _vectors(name, t, dtype, shape, dev):
+    """Address of a tensor of vectors that may be apart."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.stride(-1) == 1):
+        _rows(name, t, dtype, tuple(shape), dev)
+    return t.data_ptr()
+
+
+def _head_vectors(name, t, dtype, shape, dev):
+    """(address, strides of tokens and heads) of a [T, H, R] tensor of vectors that may be
+    apart."""
+    T, H, R = shape
+    token, head, step = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and step == 1):
+        _rows(name, t, dtype, tuple(shape), dev)
+    # (of a single one, what a tensor of several would have at least)
+    if H == 1:
+        head = R
+    return t.data_ptr(), token if T > 1 else (H - 1) * head + R, head
 
 
 def kv_append_rotary(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq,
@@ -859,28 +887,35 @@ def kv_append_rotary(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     [T]; inv_freq float32 [rotary_dim / 2], the first rotary_dim elements of a head
     being turned."""
     torch = _torch or _load_torch()
-    T, Hkv, D = k.shape
-    NB, H2, block, D2 = k_cache.shape
-    if (H2 != Hkv or D2 != D or block != BLOCK_SIZE or v_cache.shape != k_cache.shape
-            or v_cache.dtype is not k_cache.dtype or (q is None) != (q_out is None)):
+    kshape = k.shape
+    T, Hkv, D = kshape
+    cshape, cdtype, bf16 = k_cache.shape, k_cache.dtype, torch.bfloat16
+    NB, H2, block, D2 = cshape
+    if (H2 != Hkv or D2 != D or block != BLOCK_SIZE or v_cache.shape != cshape
+            or v_cache.dtype is not cdtype or (q is None) != (q_out is None)):
         raise ValueError("k and v must be [T, Hkv, D], k_cache and v_cache [NB, Hkv, 16, D], alike")
     _device_only(k_cache, v_cache)
-    dev, bf16 = _place(k_cache), torch.bfloat16
-    Hq = q.shape[1] if q is not None else 0
-    qshape, kshape = (T, Hq, D), (T, Hkv, D)
+    dev = _place(k_cache)
+    Hq = po = so = pq = sq = 0
+    if q is not None:
+        qshape = q.shape
+        Hq = qshape[1]
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != D:
+            raise ValueError("q must be [T, Hq, D]")
+        if Hq:
+            pq, sq = _heads("q", q, bf16, qshape, dev)
+            po, so = _heads("q_out", q_out, bf16, qshape, dev)
+    pk, sk = _heads("k", k, bf16, kshape, dev)
+    pv, sv = _heads("v", v, bf16, kshape, dev)
+    n = inv_freq.numel()
     _check(_HOT_APPEND_ROTARY(
-        _rows("q_out", q_out, bf16, qshape, dev, 2) if Hq else 0,
-        _stride(q_out, 0, Hq * D) if Hq else 0,
-        _rows("q", q, bf16, qshape, dev, 2) if Hq else 0, _stride(q, 0, Hq * D) if Hq else 0,
-        _rows("k", k, bf16, kshape, dev, 2), _stride(k, 0, Hkv * D),
-        _rows("v", v, bf16, kshape, dev, 2), _stride(v, 0, Hkv * D),
-        _ptr("k_cache", k_cache, k_cache.dtype, k_cache.numel(), dev),
-        _ptr("v_cache", v_cache, k_cache.dtype, k_cache.numel(), dev),
+        po, so, pq, sq, pk, sk, pv, sv, _ptr("k_cache", k_cache, cdtype, k_cache.numel(), dev),
+        _ptr("v_cache", v_cache, cdtype, v_cache.numel(), dev),
         _ptr("slot_mapping", slot_mapping, torch.int64, T, dev),
         _ptr("positions", positions, torch.int64, T, dev),
-        _ptr("inv_freq", inv_freq, torch.float32, inv_freq.numel(), dev), 2 * inv_freq.numel(),
+        _ptr("inv_freq", inv_freq, torch.float32, n, dev), 2 * n,
         ROTARY_INTERLEAVED if interleaved else 0, float(magnitude), T, Hq, Hkv, D, NB,
-        BF16 if k_cache.dtype is bf16 else _cache_dtype(k_cache), float(k_scale), float(v_scale),
+        BF16 if cdtype is bf16 else _cache_dtype(k_cache), float(k_scale), float(v_scale),
         _raw_stream(stream, dev)), "kv_append_rotary")
 
 
@@ -893,25 +928,26 @@ def kv_latent_append(q_out, q_rope, latent, k_rope, cache, slot_mapping, positio
     All bfloat16 with any distance between vectors; slot_mapping and positions
     int64 [T], inv_freq float32 [R / 2]."""
     torch = _torch or _load_torch()
-    T, L = latent.shape
+    bf16 = torch.bfloat16
+    T, L = lshape = latent.shape
     R = k_rope.shape[1]
     NB, _, W = _cache_shape(cache, True)
-    if W != L + R or cache.dtype is not torch.bfloat16 or (q_rope is None) != (q_out is None):
+    if W != L + R or cache.dtype is not bf16 or (q_rope is None) != (q_out is None):
         raise ValueError("cache must be bfloat16 [NB, 16, L + R]")
     _device_only(cache)
-    dev, bf16 = _place(cache), torch.bfloat16
-    H = q_rope.shape[1] if q_rope is not None else 0
-    qs = []
-    for name, t in (("q_out", q_out), ("q_rope", q_rope)):
-        if not H:
-            qs += [0, 0, 0]
-            continue
-        p = _rows(name, t, bf16, (T, H, R), dev)
-        head = _stride(t, 1, R)
-        qs += [p, _stride(t, 0, (H - 1) * head + R), head]
+    dev = _place(cache)
+    H, qs = 0, (0, 0, 0, 0, 0, 0)
+    if q_rope is not None:
+        qshape = q_rope.shape
+        H = qshape[1]
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != R:
+            raise ValueError("q_rope must be [T, H, R]")
+        if H:
+            qs = (_head_vectors("q_out", q_out, bf16, qshape, dev)
+                  + _head_vectors("q_rope", q_rope, bf16, qshape, dev))
     _check(_HOT_LATENT_APPEND(
-        *qs, _rows("latent", latent, bf16, (T, L), dev), _stride(latent, 0, L),
-        _rows("k_rope", k_rope, bf16, (T, R), dev), _stride(k_rope, 0, R),
+        *qs, _vectors("latent", latent, bf16, lshape, dev), latent.stride(0) if T > 1 else L,
+        _vectors("k_rope", k_rope, bf16, (T, R), dev), k_rope.stride(0) if T > 1 else R,
         _ptr("norm_weight", norm_weight, bf16, L, dev) if norm_weight is not None else 0,
         float(eps), _ptr("cache", cache, bf16, cache.numel(), dev),
         _ptr("slot_mapping", slot_mapping, torch.int64, T, dev),

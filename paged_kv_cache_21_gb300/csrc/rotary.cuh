@@ -1,12 +1,11 @@
 // Rotary positions, shared by the kernels that rotate queries and keys on their way
-// into a cache or a query buffer (kv_append.cu, latent_append.cu).
+// into a cache or a query buffer (rotary_append.cu).
 //
 // Pair i of a vector is turned by the angle position * inv_freq[i].  At a position of
 // a million the angle itself, in binary32, would be off by 0.03 radians; only its
 // fraction of a turn matters, so that the frequency is held as a 64-bit fraction of a
 // turn a position (2^64 = one turn) and the product with the position wraps: exact but
-// for the frequency's rounding, position * 2^-53 of a radian's share (a position of
-// 2^24 and a frequency of one: 2^-29 turns).
+// for the frequency's rounding, 2^-64 of a turn a position.
 #pragma once
 
 #include <cstdint>
@@ -19,12 +18,20 @@ namespace pkv {
 
 constexpr int kRotaryUnit = 16;          // elements, eight pairs, that a thread turns together
 
-// Turns a position, of 2^64, for a frequency in radians.
+// Turns a position, of 2^64, for a frequency in radians: m 2^e of the float times
+// 2^88 / (2 pi), a constant of 86 bits, in integers (FP64 runs at 1/64 of FP32's rate here:
+// in doubles the angles of 8192 tokens took 24 us of the kernel's 57).  Frequencies of 2^48
+// and above, and what is not a number, count as zero.
 __device__ __forceinline__ uint64_t rotary_step(float inv_freq)
 {
-    const double turns = (double)inv_freq * 0.15915494309189533577;      // 1 / (2 pi)
-    const double frac = turns - floor(turns);
-    return (uint64_t)(frac * 18446744073709551616.0);                    // (1.0 saturates)
+    constexpr uint64_t kHi = 0x28be60ull, kLo = 0xdb9391054a7f09d5ull;       // 2^88 / (2 pi)
+    const uint32_t bits = __float_as_uint(inv_freq), ex = (bits >> 23) & 255u;
+    const uint64_t m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const int shift = 174 - (int)(ex ? ex : 1u);         // 24 - e, e = ex - 150
+    if (shift <= 0 || shift >= 128) return 0ull;
+    const uint64_t lo = m * kLo, hi = m * kHi + __umul64hi(m, kLo);
+    const uint64_t step = shift >= 64 ? hi >> (shift - 64) : (hi << (64 - shift)) | (lo >> shift);
+    return bits >> 31 ? 0ull - step : step;
 }
 
 // magnitude * (cos, sin) of position * step.
@@ -47,6 +54,29 @@ __device__ __forceinline__ void rotary_pieces(int u, int rot, bool interleaved, 
     } else {
         first = u * kRotaryUnit;
         second = first + 8;
+    }
+}
+
+// (cos, sin) of the n angles of a position, by a warp, for its lanes to take eights of.
+__device__ __forceinline__ void rotary_table(const float* __restrict__ inv_freq, int n, int64_t position, float magnitude,
+                                             float* cs, float* sn, int lane)
+{
+    for (int i = lane; i < n; i += 32) {
+        float c, s;
+        rotary_angle(rotary_step(__ldg(inv_freq + i)), position, magnitude, c, s);
+        cs[i] = c;
+        sn[i] = s;
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void rotary_take(const float* cs, const float* sn, int u, float (&c)[8], float (&s)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(cs + 8 * u + i), b = *reinterpret_cast<const float4*>(sn + 8 * u + i);
+        c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
+        s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
     }
 }
 

@@ -2,9 +2,10 @@
 // their positions on the way into the query buffer and the paged caches.
 //
 // Both kernels stream: each input is read once, in 16-byte pieces, each output written
-// once.  A thread keeps one unit of a vector (16 elements, eight pairs: rotary.cuh) and
-// goes over heads with it, so that an angle's sine and cosine serve all the heads that
-// the thread has; the heads are cut into so many slices that the threads fill the device.
+// once.  A warp has a token: it works out the token's angles together, an angle a lane and
+// step, and its lanes then go over the heads' units (16 elements, eight pairs: rotary.cuh)
+// with four units' loads under way each.  Few tokens: their heads are shared out over more
+// warps, which each work out the angles.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -25,7 +26,12 @@ static Launched g_launched;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kCtas = 5;                 // of an SM
+
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxDim = 256;             // elements of a head that are turned, at most
+constexpr int kAhead = 4;                // units whose loads a lane has under way
 
 struct RotaryParams {
     const uint16_t* x[3];                // q, k, v: [T] rows of heads, D elements each
@@ -37,55 +43,56 @@ struct RotaryParams {
     const int64_t* positions;
     const float* inv_freq;
     long long num_slots;
-    int T, Hq, Hkv, D, rot, units, slices;
+    int T, Hq, Hkv, D, rot, units, share;        // share: warps of a token
     float magnitude, k_scale, v_scale;
 };
 
-// Thread: unit u (fastest) of the heads slice, slice + slices, ... of one token; the heads
-// are q's, then k's, then v's.
+// The heads are q's, then k's, then v's; a warp's lanes take 32 / units heads at a time, a
+// unit each.
 template <bool FP8, bool INTER>
-__global__ void __launch_bounds__(kThreads) kv_append_rotary_kernel(const __grid_constant__ RotaryParams p)
+__global__ void __launch_bounds__(kThreads, kCtas) kv_append_rotary_kernel(const __grid_constant__ RotaryParams p)
 {
+    __shared__ float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];
     pdl_wait();
-    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int u = (int)(idx % p.units);
-    const long long r = idx / p.units;
-    const int slice = (int)(r % p.slices);
-    const long long t = r / p.slices;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long job = (long long)blockIdx.x * kWarps + warp;
+    const long long t = job / p.share;
     if (t >= p.T) return;
-    const bool turned = u * kRotaryUnit < p.rot;
+    const int64_t pos = __ldg(p.positions + t);
+    const long long slot = __ldg(p.slots + t);
+    const int per = 32 / p.units, u = lane % p.units, first = lane / p.units;    // heads at a time
+    const int part = (int)(job - t * p.share), heads = p.Hq + 2 * p.Hkv, step = per * p.share;
     int a, b;
     rotary_pieces(u, p.rot, INTER, a, b);
-    float c[8], s[8];
-    if (turned) {
-        const int64_t pos = __ldg(p.positions + t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rotary_angle(rotary_step(__ldg(p.inv_freq + u * 8 + i)), pos, p.magnitude, c[i], s[i]);
-    }
-    const long long slot = __ldg(p.slots + t);
-    const bool live = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && u == 0 && slice == 0) raise_flag(&g_rotary_err, KV_DEVERR_SLOT_OUT_OF_RANGE, slot);
-    const long long blk = slot >> 4, off = slot & 15;
-    const int heads = p.Hq + (live ? 2 * p.Hkv : 0);
-    constexpr int kAhead = 4;                            // heads whose loads are in flight at once
-    for (int h0 = slice; h0 < heads; h0 += kAhead * p.slices) {
-        uint4 xa[kAhead], xb[kAhead];
+    const bool turned = u * kRotaryUnit < p.rot;
+    auto which = [&](int h) { return h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2; };
+    auto within = [&](int h, int w) { return h - (w == 0 ? 0 : w == 1 ? p.Hq : p.Hq + p.Hkv); };
+    uint4 xa[kAhead], xb[kAhead];
+    int h0 = first < per ? part * per + first : heads;
+    auto load = [&]() {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int h = h0 + k * p.slices;
+            const int h = h0 + k * step;
             if (h >= heads) continue;
-            const int w = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
-            const int hh = h - (w == 0 ? 0 : w == 1 ? p.Hq : p.Hq + p.Hkv);
-            const uint16_t* src = p.x[w] + t * p.stride[w] + (long long)hh * p.D;
+            const int w = which(h);
+            const uint16_t* src = p.x[w] + t * p.stride[w] + (long long)within(h, w) * p.D;
             xa[k] = *reinterpret_cast<const uint4*>(src + a);
             xb[k] = *reinterpret_cast<const uint4*>(src + b);
         }
+    };
+    load();                              // (on their way while the angles are worked out)
+    rotary_table(p.inv_freq, p.rot / 2, pos, p.magnitude, s_cos[warp], s_sin[warp], lane);
+    float c[8], s[8];
+    if (turned) rotary_take(s_cos[warp], s_sin[warp], u, c, s);
+    const bool live = slot >= 0 && slot < p.num_slots;
+    if (slot >= p.num_slots && lane == 0 && part == 0) raise_flag(&g_rotary_err, KV_DEVERR_SLOT_OUT_OF_RANGE, slot);
+    const long long blk = slot >> 4, off = slot & 15;
+    while (h0 < heads) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int h = h0 + k * p.slices;
+            const int h = h0 + k * step;
             if (h >= heads) continue;
-            const int w = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
-            const int hh = h - (w == 0 ? 0 : w == 1 ? p.Hq : p.Hq + p.Hkv);
+            const int w = which(h), hh = within(h, w);
             float y[16];
             const bool turn = turned && w < 2;
             if (turn) {
@@ -100,6 +107,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_rotary_kernel(const __grid
                 *reinterpret_cast<uint4*>(dst + b) = turn ? pack8(y + 8) : xb[k];
                 continue;
             }
+            if (!live) continue;
             uint8_t* cache = p.cache[w - 1];
             const long long at = ((blk * p.Hkv + hh) * kBlock + off) * p.D;
             if (!FP8) {
@@ -112,6 +120,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_rotary_kernel(const __grid
                 *reinterpret_cast<uint2*>(cache + at + b) = turn ? quantize8_f32(y + 8, scale) : quantize8_e4m3(xb[k], scale);
             }
         }
+        h0 += kAhead * step;
+        load();
     }
 }
 
@@ -128,7 +138,7 @@ struct LatentAppendParams {
     const int64_t* positions;
     const float* inv_freq;
     long long latent_stride, rope_stride, q_token, q_head, out_token, out_head, num_slots;
-    int T, H, L, R, slices;
+    int T, H, L, R, share;               // share: warps of a token's queries
     int row_blocks;                      // CTAs that write cache rows, a warp a token; the others turn queries
     float eps, magnitude;
 };
@@ -136,40 +146,44 @@ struct LatentAppendParams {
 constexpr int kLatentMax = 1024;         // elements of a latent vector
 
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads) kv_latent_append_kernel(const __grid_constant__ LatentAppendParams p)
+__global__ void __launch_bounds__(kThreads, kCtas) kv_latent_append_kernel(const __grid_constant__ LatentAppendParams p)
 {
+    __shared__ float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];
     pdl_wait();
-    const int units = p.R / kRotaryUnit;
+    const int units = p.R / kRotaryUnit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* cs = s_cos[warp];
+    float* sn = s_sin[warp];
     if ((int)blockIdx.x < p.row_blocks) {
-        const int lane = threadIdx.x & 31;
-        const long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+        const long long t = (long long)blockIdx.x * kWarps + warp;
         if (t >= p.T) return;
+        const int64_t pos = __ldg(p.positions + t);
         const long long slot = __ldg(p.slots + t);
+        // the latent vector: 16-byte pieces lane, lane + 32, ...; the key part: a lane a unit
+        constexpr int kPieces = kLatentMax / 256;
+        uint4 v[kPieces], xa, xb;
+        const uint16_t* src = p.latent + t * p.latent_stride;
+        const uint16_t* kr = p.k_rope + t * p.rope_stride;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+            if ((lane + 32 * k) * 8 < p.L) v[k] = *reinterpret_cast<const uint4*>(src + (lane + 32 * k) * 8);
+        int a, b;
+        rotary_pieces(lane, p.R, INTER, a, b);
+        if (lane < units) {
+            xa = *reinterpret_cast<const uint4*>(kr + a);
+            xb = *reinterpret_cast<const uint4*>(kr + b);
+        }
         if (slot < 0) return;                             // padding token
         if (slot >= p.num_slots) {
             if (lane == 0) raise_flag(&g_rotary_err, KV_DEVERR_SLOT_OUT_OF_RANGE, slot);
             return;
         }
         uint16_t* row = p.cache + slot * (p.L + p.R);
-        // the latent vector: 16-byte pieces lane, lane + 32, ...
-        constexpr int kPieces = kLatentMax / 256;
-        uint4 v[kPieces];
-        const uint16_t* src = p.latent + t * p.latent_stride;
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k)
-            if ((lane + 32 * k) * 8 < p.L) v[k] = *reinterpret_cast<const uint4*>(src + (lane + 32 * k) * 8);
-        // the key's rotary part: a lane per unit
+        rotary_table(p.inv_freq, p.R / 2, pos, p.magnitude, cs, sn, lane);
         if (lane < units) {
-            int a, b;
-            rotary_pieces(lane, p.R, INTER, a, b);
-            const uint16_t* kr = p.k_rope + t * p.rope_stride;
             float x[16], y[16], c[8], s[8];
-            unpack8(*reinterpret_cast<const uint4*>(kr + a), x);
-            unpack8(*reinterpret_cast<const uint4*>(kr + b), x + 8);
-            const int64_t pos = __ldg(p.positions + t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                rotary_angle(rotary_step(__ldg(p.inv_freq + lane * 8 + i)), pos, p.magnitude, c[i], s[i]);
+            rotary_take(cs, sn, lane, c, s);
+            unpack8(xa, x);
+            unpack8(xb, x + 8);
             rotary_turn(x, c, s, INTER, y);
             *reinterpret_cast<uint4*>(row + p.L + a) = pack8(y);
             *reinterpret_cast<uint4*>(row + p.L + b) = pack8(y + 8);
@@ -205,33 +219,35 @@ __global__ void __launch_bounds__(kThreads) kv_latent_append_kernel(const __grid
         }
         return;
     }
-    // ---- queries: unit u (fastest) of the heads slice, slice + slices, ... of one token
-    const long long idx = (long long)(blockIdx.x - p.row_blocks) * kThreads + threadIdx.x;
-    const int u = (int)(idx % units);
-    const long long r = idx / units;
-    const int slice = (int)(r % p.slices);
-    const long long t = r / p.slices;
+    // ---- queries: a warp's lanes take 32 / units heads at a time, a unit each
+    const long long job = (long long)(blockIdx.x - p.row_blocks) * kWarps + warp;
+    const long long t = job / p.share;
     if (t >= p.T) return;
+    const int64_t pos = __ldg(p.positions + t);
+    const int per = 32 / units, u = lane % units, first = lane / units;
+    const int part = (int)(job - t * p.share), step = per * p.share;
     int a, b;
     rotary_pieces(u, p.R, INTER, a, b);
-    float c[8], s[8];
-    const int64_t pos = __ldg(p.positions + t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rotary_angle(rotary_step(__ldg(p.inv_freq + u * 8 + i)), pos, p.magnitude, c[i], s[i]);
-    constexpr int kAhead = 4;
-    for (int h0 = slice; h0 < p.H; h0 += kAhead * p.slices) {
-        uint4 xa[kAhead], xb[kAhead];
+    uint4 xa[kAhead], xb[kAhead];
+    int h0 = first < per ? part * per + first : p.H;
+    auto load = [&]() {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int h = h0 + k * p.slices;
+            const int h = h0 + k * step;
             if (h >= p.H) continue;
             const uint16_t* src = p.q + t * p.q_token + h * p.q_head;
             xa[k] = *reinterpret_cast<const uint4*>(src + a);
             xb[k] = *reinterpret_cast<const uint4*>(src + b);
         }
+    };
+    load();                              // (on their way while the angles are worked out)
+    rotary_table(p.inv_freq, p.R / 2, pos, p.magnitude, cs, sn, lane);
+    float c[8], s[8];
+    rotary_take(cs, sn, u, c, s);
+    while (h0 < p.H) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int h = h0 + k * p.slices;
+            const int h = h0 + k * step;
             if (h >= p.H) continue;
             float x[16], y[16];
             unpack8(xa[k], x);
@@ -241,16 +257,18 @@ __global__ void __launch_bounds__(kThreads) kv_latent_append_kernel(const __grid
             *reinterpret_cast<uint4*>(dst + a) = pack8(y);
             *reinterpret_cast<uint4*>(dst + b) = pack8(y + 8);
         }
+        h0 += kAhead * step;
+        load();
     }
 }
 
-// So many slices of `heads` heads that units * slices * T threads fill the device, but no
-// more than there are heads.
-int head_slices(long long threads_per_slice, int heads)
+// Warps of a token: one where the tokens fill the device, more where they do not, but no
+// more than there are steps of its heads.
+int warps_of_token(int tokens, int heads, int heads_at_a_time)
 {
-    const long long want = (long long)num_sms_current() * 2048;
-    const long long s = (want + threads_per_slice - 1) / threads_per_slice;
-    return (int)(s < 1 ? 1 : s > heads ? heads : s);
+    const long long want = (long long)num_sms_current() * kCtas * kWarps;
+    const long long s = (want + tokens - 1) / tokens, most = (heads + heads_at_a_time - 1) / heads_at_a_time;
+    return (int)(s < 1 ? 1 : s > most ? most : s);
 }
 
 template <typename P>
@@ -299,7 +317,8 @@ extern "C" int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q
     if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks <= 0 || head_dim <= 0 ||
         rotary_dim <= 0 || rotary_dim > head_dim || (flags & ~KV_ROTARY_INTERLEAVED) || !std::isfinite(magnitude))
         return KV_ERR_INVALID_ARG;
-    if (head_dim % kRotaryUnit || rotary_dim % kRotaryUnit) return KV_ERR_UNSUPPORTED;
+    if (head_dim % kRotaryUnit || rotary_dim % kRotaryUnit || head_dim > 32 * kRotaryUnit || rotary_dim > kMaxDim)
+        return KV_ERR_UNSUPPORTED;
     if (kv_dtype != KV_DTYPE_BF16 && kv_dtype != KV_DTYPE_FP8_E4M3) return KV_ERR_UNSUPPORTED;
     const int64_t qrow = (int64_t)num_q_heads * head_dim, kvrow = (int64_t)num_kv_heads * head_dim;
     if (qrow > INT32_MAX / 4 || kvrow > INT32_MAX / 4) return KV_ERR_UNSUPPORTED;
@@ -334,11 +353,11 @@ extern "C" int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q
     p.D = head_dim;
     p.rot = rotary_dim;
     p.units = head_dim / kRotaryUnit;
-    p.slices = head_slices((long long)num_tokens * p.units, num_q_heads + 2 * num_kv_heads);
+    p.share = warps_of_token(num_tokens, num_q_heads + 2 * num_kv_heads, 32 / p.units);
     p.magnitude = magnitude;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    const long long threads = (long long)num_tokens * p.units * p.slices, blocks = (threads + kThreads - 1) / kThreads;
+    const long long blocks = ((long long)num_tokens * p.share + kWarps - 1) / kWarps;
     const bool inter = flags & KV_ROTARY_INTERLEAVED;
     auto* kernel = fp8 ? (inter ? kv_append_rotary_kernel<true, true> : kv_append_rotary_kernel<true, false>)
                        : (inter ? kv_append_rotary_kernel<false, true> : kv_append_rotary_kernel<false, false>);
@@ -357,7 +376,7 @@ extern "C" int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t
     if (num_tokens < 0 || num_q_heads < 0 || latent_dim <= 0 || rope_dim <= 0 || num_blocks <= 0 ||
         (flags & ~KV_ROTARY_INTERLEAVED) || !std::isfinite(magnitude))
         return KV_ERR_INVALID_ARG;
-    if (latent_dim % 8 || latent_dim > kLatentMax || rope_dim % kRotaryUnit || rope_dim > 32 * kRotaryUnit)
+    if (latent_dim % 8 || latent_dim > kLatentMax || rope_dim % kRotaryUnit || rope_dim > kMaxDim)
         return KV_ERR_UNSUPPORTED;
     if (norm_weight && !(eps >= 0.f && std::isfinite(eps))) return KV_ERR_INVALID_ARG;
     if (num_tokens == 0) return KV_OK;
@@ -399,10 +418,9 @@ extern "C" int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t
     p.eps = eps;
     p.magnitude = magnitude;
     const int units = rope_dim / kRotaryUnit;
-    p.row_blocks = (num_tokens + kThreads / 32 - 1) / (kThreads / 32);
-    p.slices = num_q_heads > 0 ? head_slices((long long)num_tokens * units, num_q_heads) : 0;
-    const long long threads = (long long)num_tokens * units * p.slices;
-    const long long blocks = p.row_blocks + (threads + kThreads - 1) / kThreads;
+    p.row_blocks = (num_tokens + kWarps - 1) / kWarps;
+    p.share = num_q_heads > 0 ? warps_of_token(num_tokens, num_q_heads, 32 / units) : 0;
+    const long long blocks = p.row_blocks + ((long long)num_tokens * p.share + kWarps - 1) / kWarps;
     return launch(flags & KV_ROTARY_INTERLEAVED ? kv_latent_append_kernel<true> : kv_latent_append_kernel<false>, blocks,
                   p, stream);
 }

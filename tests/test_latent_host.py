@@ -90,7 +90,7 @@ def rotary(pk, q_out=A, so=512, q=A, sq=512, k=A, sk=128, v=A, sv=128, kc=A, vc=
 @pytest.mark.parametrize("bad,code", [
     (dict(T=-1), -1), (dict(hq=-1), -1), (dict(hkv=0), -1), (dict(nb=0), -1), (dict(rot=0), -1),
     (dict(rot=80), -1), (dict(flags=2), -1), (dict(mag=float("inf")), -1), (dict(d=72), -3),
-    (dict(rot=24), -3), (dict(dtype=2), -3), (dict(k=None), -1), (dict(q=None), -1),
+    (dict(rot=24), -3), (dict(d=528, sq=9000, so=9000, sk=2000, sv=2000), -3), (dict(dtype=2), -3), (dict(k=None), -1), (dict(q=None), -1),
     (dict(q_out=None), -1), (dict(pos=None), -1), (dict(freq=None), -1), (dict(slots=None), -1),
     (dict(vc=None), -1), (dict(q=P(4104)), -1), (dict(v=P(4098)), -1), (dict(sk=64), -1),
     (dict(sv=132), -1), (dict(sq=504), -1), (dict(so=0), -1), (dict(dtype=1, ks=0.0), -1),
@@ -109,7 +109,7 @@ def lappend(pk, qo=A, ot=512, oh=64, q=A, qt=512, qh=64, latent=A, sl=576, kr=A,
 
 @pytest.mark.parametrize("bad,code", [
     (dict(T=-1), -1), (dict(h=-1), -1), (dict(l=0), -1), (dict(r=0), -1), (dict(nb=0), -1),
-    (dict(flags=4), -1), (dict(l=1032), -3), (dict(l=508), -3), (dict(r=24), -3), (dict(r=528), -3),
+    (dict(flags=4), -1), (dict(l=1032), -3), (dict(l=508), -3), (dict(r=24), -3), (dict(r=272), -3),
     (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(latent=None), -1), (dict(kr=None), -1),
     (dict(cache=None), -1), (dict(q=None), -1), (dict(qo=None), -1), (dict(sl=504), -1),
     (dict(sr=63), -1), (dict(qh=32), -1), (dict(oh=60), -1), (dict(qt=448), -1), (dict(ot=504), -1),
