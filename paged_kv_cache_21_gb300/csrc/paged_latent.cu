@@ -262,8 +262,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         misc[M_SEEN] = 0;
         fence_mbar_init();
     }
-    pdl_launch_dependents();
-    pdl_wait();
+    // (all this while the kernel before drains)
     if (warp == G::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          sb + G::kMiscOff + 4 * M_TMEM),
@@ -271,11 +270,13 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (warp == G::kKWarp) cut_work(p, misc, kMinPages, kExtraPages, pair, blockIdx.x == 0, lane);
     umma::fence_before_sync();
-    __syncthreads();
     cluster_sync();                      // the barriers of both CTAs are there
     umma::fence_after_sync();
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == G::kKWarp) cut_work(p, misc, kMinPages, kExtraPages, pair, blockIdx.x == 0, lane);
+    __syncthreads();
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
     if (warp >= G::kKWarp && warp < G::kKWarp + G::kG1) {

@@ -148,16 +148,18 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
         misc[M_SEEN] = 0;
         fence_mbar_init();
     }
-    pdl_launch_dependents();
-    pdl_wait();
+    // (all this while the kernel before drains)
     if (warp == G::kMmaWarp) {
         umma::tmem_alloc(sb + G::kMiscOff + 4 * M_TMEM, G::kTmemCols);
         umma::tmem_relinquish();
     }
-    if (warp == G::kCopyWarp) cut_work(p, misc, kMinPages, kExtraPages, cta, cta == 0, lane);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == G::kCopyWarp) cut_work(p, misc, kMinPages, kExtraPages, cta, cta == 0, lane);
+    __syncthreads();
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
     if (warp >= G::kCopyWarp && warp < G::kCopyWarp + kPages) {

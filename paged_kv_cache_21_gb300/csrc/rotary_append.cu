@@ -143,10 +143,12 @@ struct LatentAppendParams {
     float eps, magnitude;
 };
 
+constexpr int kLatentCtas = 8;           // of an SM: little work a warp, so many warps
+constexpr int kLatentAhead = 2;
 constexpr int kLatentMax = 1024;         // elements of a latent vector
 
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads, kCtas) kv_latent_append_kernel(const __grid_constant__ LatentAppendParams p)
+__global__ void __launch_bounds__(kThreads, kLatentCtas) kv_latent_append_kernel(const __grid_constant__ LatentAppendParams p)
 {
     __shared__ float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];
     pdl_wait();
@@ -228,11 +230,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_latent_append_kernel(const
     const int part = (int)(job - t * p.share), step = per * p.share;
     int a, b;
     rotary_pieces(u, p.R, INTER, a, b);
-    uint4 xa[kAhead], xb[kAhead];
+    uint4 xa[kLatentAhead], xb[kLatentAhead];
     int h0 = first < per ? part * per + first : p.H;
     auto load = [&]() {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < kLatentAhead; ++k) {
             const int h = h0 + k * step;
             if (h >= p.H) continue;
             const uint16_t* src = p.q + t * p.q_token + h * p.q_head;
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_latent_append_kernel(const
     rotary_take(cs, sn, u, c, s);
     while (h0 < p.H) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < kLatentAhead; ++k) {
             const int h = h0 + k * step;
             if (h >= p.H) continue;
             float x[16], y[16];
@@ -257,16 +259,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_latent_append_kernel(const
             *reinterpret_cast<uint4*>(dst + a) = pack8(y);
             *reinterpret_cast<uint4*>(dst + b) = pack8(y + 8);
         }
-        h0 += kAhead * step;
+        h0 += kLatentAhead * step;
         load();
     }
 }
 
 // Warps of a token: one where the tokens fill the device, more where they do not, but no
 // more than there are steps of its heads.
-int warps_of_token(int tokens, int heads, int heads_at_a_time)
+int warps_of_token(int tokens, int heads, int heads_at_a_time, int ctas)
 {
-    const long long want = (long long)num_sms_current() * kCtas * kWarps;
+    const long long want = (long long)num_sms_current() * ctas * kWarps;
     const long long s = (want + tokens - 1) / tokens, most = (heads + heads_at_a_time - 1) / heads_at_a_time;
     return (int)(s < 1 ? 1 : s > most ? most : s);
 }
@@ -353,7 +355,7 @@ extern "C" int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q
     p.D = head_dim;
     p.rot = rotary_dim;
     p.units = head_dim / kRotaryUnit;
-    p.share = warps_of_token(num_tokens, num_q_heads + 2 * num_kv_heads, 32 / p.units);
+    p.share = warps_of_token(num_tokens, num_q_heads + 2 * num_kv_heads, 32 / p.units, kCtas);
     p.magnitude = magnitude;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
@@ -419,7 +421,7 @@ extern "C" int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t
     p.magnitude = magnitude;
     const int units = rope_dim / kRotaryUnit;
     p.row_blocks = (num_tokens + kWarps - 1) / kWarps;
-    p.share = num_q_heads > 0 ? warps_of_token(num_tokens, num_q_heads, 32 / units) : 0;
+    p.share = num_q_heads > 0 ? warps_of_token(num_tokens, num_q_heads, 32 / units, kLatentCtas) : 0;
     const long long blocks = p.row_blocks + ((long long)num_tokens * p.share + kWarps - 1) / kWarps;
     return launch(flags & KV_ROTARY_INTERLEAVED ? kv_latent_append_kernel<true> : kv_latent_append_kernel<false>, blocks,
                   p, stream);
