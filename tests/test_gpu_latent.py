@@ -62,6 +62,82 @@ def rotary_inputs(T, Hq, Hkv, D, rot, packed, far, seed=0):
     return gen, q, k, v, NB, slots, positions, freq
 
 
+def test_appends_from_pinned_host_memory_and_in_place(pk):
+    """A step's own tensors in pinned host memory, as the decode entry points take them; queries
+    turned where they are; negative positions, which turn the other way."""
+    T, Hq, Hkv, D = 5, 4, 2, 64
+    _, q, k, v, NB, slots, positions, freq = rotary_inputs(T, Hq, Hkv, D, 64, False, 900)
+    positions[2] = -700
+    outs = []
+    for place in (lambda t: t.cuda(), lambda t: t.contiguous().pin_memory()):
+        kc, vc = (torch.zeros((NB, Hkv, 16, D), dtype=BF, device="cuda") for _ in range(2))
+        q_out = place(torch.empty_like(q))
+        pk.kv_append_rotary(q_out, place(q), place(k), place(v), kc, vc, place(slots),
+                            place(positions), place(freq))
+        torch.cuda.synchronize()
+        outs.append((q_out.cpu(), kc.cpu(), vc.cpu()))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    want, size = R.turn(q, positions, freq, 1.0, False)
+    check(outs[0][0], want, R.HALF_BF16 * want.abs() + R.turn_error(size), "q")
+    L, rope = 256, 32
+    gen = torch.Generator().manual_seed(9)
+    latent, kr, qr = randn(gen, T, L).to(BF), randn(gen, T, rope).to(BF), randn(gen, T, 1, rope).to(BF)
+    freq = torch.from_numpy(pk.rotary_frequencies(rope)[0])
+    outs = []
+    for place in (lambda t: t.cuda(), lambda t: t.contiguous().pin_memory()):
+        cache = torch.zeros((NB, 16, L + rope), dtype=BF, device="cuda")
+        dq = place(qr.clone())
+        pk.kv_latent_append(dq, dq, place(latent), place(kr), cache, place(slots), place(positions),
+                            place(freq))
+        torch.cuda.synchronize()
+        outs.append((dq.cpu(), cache.cpu()))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    want, size = R.turn(qr, positions, freq, 1.0, False)
+    check(outs[0][0], want, R.HALF_BF16 * want.abs() + R.turn_error(size), "q in place")
+    assert pk.get_device_error()[0] == 0
+
+
+def test_frequencies_of_any_size(pk):
+    """Frequencies from 2^-140 to above a turn a position, zero and below: the angle's fraction of
+    a turn in exact integers."""
+    f = [0.0, 1e-42, 2.0 ** -100, 1e-20, 3e-9, 0.7, 1.0, 3.25, 6.2831855, 7.5, 1000.123, 3e7, -0.3, -9.0,
+         2.0 ** -30, 12345.678]
+    freq = torch.tensor(f, dtype=torch.float32)
+    n, D = len(f), 2 * len(f)
+    positions = torch.tensor([0, 1, 3, 1000, 123456789, 2 ** 40 + 1, -5], dtype=torch.int64)
+    T = len(positions)
+    q = torch.zeros((T, 1, D), dtype=BF)
+    q[..., :n] = 1.0                     # turned: the cosines, then the sines
+    kc, vc = (torch.zeros((1, 1, 16, D), dtype=BF, device="cuda") for _ in range(2))
+    out = torch.empty((T, 1, D), dtype=BF, device="cuda")
+    zero = torch.zeros((T, 1, D), dtype=BF, device="cuda")
+    pk.kv_append_rotary(out, q.cuda(), zero, zero, kc, vc, torch.full((T,), -1).cuda(),
+                        positions.cuda(), freq.cuda())
+    # 2 pi to 220 bits, by Machin's formula; angles as fractions of a turn in 2^-64
+    unit = 1 << 240
+
+    def arctan_of_inverse(x):
+        total = term = unit // x
+        k, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // k)
+            k, sign = k + 2, -sign
+        return total
+
+    two_pi = 8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))
+    want = torch.zeros((T, 1, D), dtype=torch.float64)
+    for t, p in enumerate(positions.tolist()):
+        for i, x in enumerate(freq.tolist()):
+            num, den = float(x).as_integer_ratio()
+            turn = (p * num * unit << 64) // (den * two_pi) % (1 << 64)
+            a = torch.tensor(turn / 2.0 ** 64 * 2 * np.pi, dtype=torch.float64)
+            want[t, 0, i], want[t, 0, n + i] = torch.cos(a), torch.sin(a)
+    # (a frequency is held to 2^-64 of a turn a position)
+    lost = positions.abs().double()[:, None, None] * 2.0 ** -64 * 2 * np.pi
+    check(out, want, R.HALF_BF16 * want.abs() + R.turn_error(torch.ones_like(want)) + lost, "turns")
+
+
 @pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,packed,fp8,far", ROTARY)
 def test_rotary_append(pk, T, Hq, Hkv, D, rot, inter, packed, fp8, far):
     gen, q, k, v, NB, slots, positions, freq = rotary_inputs(T, Hq, Hkv, D, rot, packed, far)
@@ -258,6 +334,10 @@ SIZES = [
     ([77, 130, 10], [20, 6, 5], 33, 512, 64, "pads"),
     ([64], [128], 5, 512, 64, "tree"),
     ([1500], [40], 128, 512, 64, "tree"),
+    # contexts that many workers share: parts by the dozen, with rows for either kernel
+    ([20000], None, 16, 512, 64, "chain"),
+    ([12000], [2], 100, 512, 64, "chain"),
+    ([7000, 3000], [3, 1], 60, 256, 32, "tree"),
 ]
 
 
@@ -420,6 +500,36 @@ def test_latent_attention_repeats_and_streams(pk):
     assert torch.equal(outs[2].cpu(), first)
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_latent_attention_gives_up_a_wait_that_runs_out(pk, H):
+    """The test hook: a wait of the kernel's scores runs out, the flag says so, and the next call
+    is right."""
+    c = Case([700, 90], None, H, 512, 64, seed=H)
+    pk.set_pipeline_stall(1000)
+    try:
+        c.run(pk)
+    finally:
+        pk.set_pipeline_stall(0)
+    assert pk.get_device_error()[0] & pk.DEVERR_PIPELINE_TIMEOUT
+    c.check(c.run(pk))
+    assert pk.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("H,n", [(16, 1), (64, 2)])
+def test_latent_attention_large_and_tiny_scores(pk, H, n):
+    """Scores above 2^21, whose products are rounded by 2^-3 and more, and weights that all but
+    one lose: the weight of the largest is one whatever its rounding."""
+    c = Case([300], [n], H, 256, 64, seed=7)
+    flat = c.cache.flatten(0, 1)
+    c.q = torch.full_like(c.q, 64.0)
+    flat[:] = torch.randn(flat.shape, generator=torch.Generator().manual_seed(1)).to(BF) * 0.01
+    hot = 123
+    flat[int(c.bt[0, hot // 16]) * 16 + hot % 16] = 500.0
+    c.scale = 3.0                        # 64 * 500 * 320 * 3 = 3.1e7 for the one
+    out = c.run(pk).cpu()
+    assert (out == 500.0).all()
+
+
 # ------------------------------------------------------------------------- used together
 
 def test_a_run_of_steps_over_latent_caches(pk):
@@ -533,9 +643,24 @@ def test_rotary_append_then_decode(pk):
         for s in range(B):
             keys[s].append(k64[s])
             vals[s].append(x[s, Hq + Hkv:].double())
-    out = torch.empty((B, Hq, D), dtype=torch.float32, device="cuda")
-    pk.paged_decode_attention(out, q, kc, vc, torch.from_numpy(bt).cuda(),
-                              torch.from_numpy(lens).cuda(), D ** -0.5, ws)
+    out, early = (torch.empty((B, Hq, D), dtype=torch.float32, device="cuda") for _ in range(2))
+    tables = torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda()
+    pk.paged_decode_attention(out, q, kc, vc, *tables, D ** -0.5, ws)
+    # the last append again and, directly behind it, the step that reads the cache early
+    torch.cuda.synchronize()
+    slots, p = torch.from_numpy(slots).cuda(), p.cuda()
+    kc2, vc2 = kc.clone(), vc.clone()
+    freq = freq.cuda()
+    for cache in (kc2, vc2):
+        for s in range(B):
+            cache[int(slots[s]) // 16, :, int(slots[s]) % 16] = 7.0
+    torch.cuda.synchronize()
+    q2 = torch.empty_like(q)
+    pk.kv_append_rotary(q2, d[:, :Hq], d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], kc2, vc2, slots, p, freq,
+                        magnitude=mag)
+    pk.paged_decode(early, q2, kc2, vc2, *tables, D ** -0.5, ws, early_inputs=True)
+    assert torch.equal(early.cpu(), out.cpu()) and torch.equal(kc2.cpu(), kc.cpu())
+    p, freq = p.cpu(), freq.cpu()
     q64, _ = R.turn(x[:, :Hq], p, freq, mag, False)
     G = Hq // Hkv
     for s in range(B):
