@@ -805,10 +805,11 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
 // ------------------------------------------------------------------------- merge
 
-constexpr int kMergeWarps = 4;
 constexpr int kMaxWorkers = 256;
 // Parts of a tile, by workers and tiles, from which the warps share them out.
 constexpr int kMergeSplit = 8;
+
+constexpr int merge_warps(bool split) { return split ? 8 : 4; }
 
 // What a row gets that has no weight: NaN if it sees a position (its scores were -inf alone).
 __device__ __forceinline__ float weightless(const LatentParams& p, int s, int r)
@@ -825,12 +826,13 @@ __device__ __forceinline__ float weightless(const LatentParams& p, int s, int r)
 // wrote its first part.  A warp reads 64 elements of 8 rows, where fours of the rows'
 // elements lie together, or a row (BY_ROW), where its elements do, two parts at a time with
 // a running (max, sum).  Few parts: the warps have different elements.  Many (SPLIT): they
-// take the parts in turn, and their four results are joined in the warps' order.
+// take the parts in turn, and their results are joined in the warps' order.
 template <int LAT, bool BY_ROW, bool SPLIT>
-__global__ void __launch_bounds__(kMergeWarps * 32, 8) paged_latent_merge_kernel(const LatentParams p)
+__global__ void __launch_bounds__(merge_warps(SPLIT) * 32, SPLIT ? 4 : 8) paged_latent_merge_kernel(const LatentParams p)
 {
+    constexpr int kMergeWarps = merge_warps(SPLIT);
     constexpr int kFours = LAT / 4, kN = BY_ROW ? LAT / 128 : 4;     // fours of a row; of a lane
-    constexpr int kRounds = kMaxWorkers / (kMergeWarps * 32);
+    constexpr int kRounds = (kMaxWorkers + kMergeWarps * 32 - 1) / (kMergeWarps * 32);
     __shared__ int4 s_meta;
     __shared__ int s_x, s_count[kRounds][kMergeWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.tile_rows;
@@ -913,7 +915,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) paged_latent_merge_kernel
         for (int k = 0; k < kN; ++k) s_acc[warp][k][lane] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
         s_ml[warp][lane] = make_float2(M, l);
         __syncthreads();
-        M = fmaxf(fmaxf(s_ml[0][lane].x, s_ml[1][lane].x), fmaxf(s_ml[2][lane].x, s_ml[3][lane].x));
+        M = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kMergeWarps; ++q) M = fmaxf(M, s_ml[q][lane].x);
         l = 0.f;
         acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
         // (warp k joins the warps' k-th fours)
@@ -931,13 +935,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) paged_latent_merge_kernel
             }
         }
     }
-    if (row >= meta.w) return;
+    if (row >= meta.w || (SPLIT && warp >= kN)) return;
     const int r = meta.y * R + row;
     const float none = l == 0.f ? weightless(p, meta.x, r) : 0.f, inv = 1.f / l;
     uint2* dst = reinterpret_cast<uint2*>(p.out + ((size_t)t0 * p.H + r) * LAT);
 #pragma unroll
     for (int k = 0; k < (SPLIT ? 1 : kN); ++k) {
-        if (SPLIT && warp >= kN) break;
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = l == 0.f ? none : acc[k][e] * inv;
@@ -1024,6 +1027,7 @@ int launch_many(const LatentParams& p, const void* q, const void* cache, cudaStr
 template <int LAT, bool BY_ROW, bool SPLIT>
 int launch_merge(const LatentParams& p, int tiles, int rows, cudaStream_t st)
 {
+    constexpr int kMergeWarps = merge_warps(SPLIT);
     const int pieces = BY_ROW ? rows : (rows + 7) / 8 * (LAT / 64);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
