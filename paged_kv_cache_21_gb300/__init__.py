@@ -878,6 +878,19 @@ def _head_vectors(name, t, dtype, shape, dev):
     return t.data_ptr(), token if T > 1 else (H - 1) * head + R, head
 
 
+def _tables(slot_mapping, positions, inv_freq, T, n, dev):
+    """Addresses of an append's slots, positions and frequencies."""
+    i64, f32 = _torch.int64, _torch.float32
+    if (slot_mapping.dtype is i64 and positions.dtype is i64 and inv_freq.dtype is f32
+            and slot_mapping.numel() == T and positions.numel() == T and inv_freq.numel() == n
+            and slot_mapping.get_device() == dev and positions.get_device() == dev
+            and inv_freq.get_device() == dev and slot_mapping.is_contiguous()
+            and positions.is_contiguous() and inv_freq.is_contiguous()):
+        return slot_mapping.data_ptr(), positions.data_ptr(), inv_freq.data_ptr()
+    return (_ptr("slot_mapping", slot_mapping, i64, T, dev),
+            _ptr("positions", positions, i64, T, dev), _ptr("inv_freq", inv_freq, f32, n, dev))
+
+
 def kv_append_rotary(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq,
                      interleaved=False, magnitude=1.0, k_scale=1.0, v_scale=1.0, stream=None):
     """kv_append with rotary positions on the way (kv_append_rotary): k [T, Hkv, D]
@@ -911,9 +924,7 @@ def kv_append_rotary(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     _check(_HOT_APPEND_ROTARY(
         po, so, pq, sq, pk, sk, pv, sv, _ptr("k_cache", k_cache, cdtype, k_cache.numel(), dev),
         _ptr("v_cache", v_cache, cdtype, v_cache.numel(), dev),
-        _ptr("slot_mapping", slot_mapping, torch.int64, T, dev),
-        _ptr("positions", positions, torch.int64, T, dev),
-        _ptr("inv_freq", inv_freq, torch.float32, n, dev), 2 * n,
+        *_tables(slot_mapping, positions, inv_freq, T, n, dev), 2 * n,
         ROTARY_INTERLEAVED if interleaved else 0, float(magnitude), T, Hq, Hkv, D, NB,
         BF16 if cdtype is bf16 else _cache_dtype(k_cache), float(k_scale), float(v_scale),
         _raw_stream(stream, dev)), "kv_append_rotary")
@@ -950,9 +961,7 @@ def kv_latent_append(q_out, q_rope, latent, k_rope, cache, slot_mapping, positio
         _vectors("k_rope", k_rope, bf16, (T, R), dev), k_rope.stride(0) if T > 1 else R,
         _ptr("norm_weight", norm_weight, bf16, L, dev) if norm_weight is not None else 0,
         float(eps), _ptr("cache", cache, bf16, cache.numel(), dev),
-        _ptr("slot_mapping", slot_mapping, torch.int64, T, dev),
-        _ptr("positions", positions, torch.int64, T, dev),
-        _ptr("inv_freq", inv_freq, torch.float32, R // 2, dev),
+        *_tables(slot_mapping, positions, inv_freq, T, R // 2, dev),
         ROTARY_INTERLEAVED if interleaved else 0, float(magnitude), T, H, L, R, NB,
         _raw_stream(stream, dev)), "kv_latent_append")
 

@@ -1,5 +1,6 @@
 // paged_latent_attention: attention of one token, or a tree of drafted tokens, over a
-// cache that holds one row of L + R elements a token for all query heads.
+// cache that holds one row of L + R elements a token for all query heads.  Here: calls
+// with more than 64 query rows a sequence, the merge of partial results, and the host side.
 //
 //     out[i][h] = sum_j softmax_j(scale * q[i][h] . c_j) c_j[0 .. L)
 //
@@ -15,25 +16,44 @@
 // Why a pair: 128 rows x 512 columns of O in float32 fill one SM's tensor memory, with no
 // room for S, and 128 rows of Q (147 KB) with a chunk (147 KB) its shared memory.  Split
 // so, a CTA holds Q 74 KB, K 74 KB, V 66 KB, P 16 KB; O takes 256 of its 512 columns of
-// tensor memory, two buffers of S 128.  A tcgen05.mma takes 45 clocks at least (measured:
-// cta_group::2, M 128, K 16: N 64 45, N 128 47, N 256 65), so tokens come 128 at a time:
-// 36 products of N 128 and 16 of N 256, ~2700 clocks a chunk for both SMs, where HBM
-// brings a chunk's 147 KB to two SMs in ~3200 (6.7 TB/s, 152 SMs, 1.9 GHz).
+// tensor memory, two buffers of S 128.
+//
+// What bounds it (L = 512, R = 64).  A chunk's 147 KB take HBM 1.68 us to two SMs (6.7
+// TB/s, 152 SMs), ~3300 clocks.  A chunk's 36 products of N 128 and 16 of N 256 with their
+// commits take ~3010 clocks (measured; one of N 128 takes 53, 45 at least whatever its N,
+// one of N 256 65).  In the loop a chunk takes ~3500: 94 % of HBM's rate.  32 x 8192 tokens,
+// 128 heads: 78 us, of which ~50 are HBM's at its rate, ~6 until the first keys are there
+// (tables, the cut, block ids and a first copy, each behind the one before), ~5 the last
+// chunk's products and its 131 KB of partial results a CTA, ~8 the merge.  Four tokens x 128
+// heads over 32 x 2048: 87 us, tensor cores and the ends of 2.7 tiles a pair.
 //
 // How:
-//  * Each byte of the cache is copied twice, as K to one CTA and as V to the other or the
-//    same one (L2 serves the second).  K goes by groups of four 64-element columns, with a
-//    barrier each, so that a group's room is filled again as soon as its products are done;
-//    V by halves of a chunk.
-//  * Warps: eight weigh (a thread per row, half of the chunk's tokens of a row's pair and 32
-//    of its columns), one copies Q and K, one V, one issues the MMAs (of the first CTA: for
-//    both), and one clears what must not be multiplied in V: rows behind the context, and
-//    infinities and NaN of drafted rows that some node does not see (0 * inf).
-//  * The scores of chunk c + 1 are computed while chunk c is weighed: S(c + 1), then O(c).
+//  * Each byte of the cache is copied twice, as K to one CTA and as V to either, and shared
+//    memory has room for one chunk: a group of K's columns is copied again as soon as its
+//    products are done, by a warp of its own (one warp for all groups and one for V: 92.6
+//    us for the four tokens; so 88.4).  To have the second copy, and the first, find
+//    their bytes in L2, a warp prefetches pages a chunk ahead, line by line (82.8 -> 78.6 us
+//    against two chunks ahead, 84.7 without; by bulk copies to L2, which wait behind the
+//    others in the copy unit: 95).
+//  * Warps: eight weigh (two threads and two halves of O's columns a row), three copy K (the
+//    first also Q), two V, two issue the MMAs of both CTAs (scores; products), one prefetches.
+//  * The warps that copy V clear what must not be multiplied (0 * inf): rows behind the
+//    context, and infinities and NaN of drafted rows, which some node may not see; the
+//    latter come back as NaN to the rows that see them when the result is written.
+//  * The scores of chunk c + 1 are computed while chunk c is weighed.
 //  * The reference maximum of a row moves only when a score is more than 2^8 above it; then,
 //    seldom, O's columns and the sums are scaled.
-//  * Pairs of CTAs get equal shares of all the (sequence, tile, page)s; a sequence's parts
-//    are joined by a second kernel.
+//  * Pairs of CTAs get equal shares of all the (sequence, tile, page)s.  The parts of a
+//    (sequence, tile) go to the workspace in an order that the lanes, which are rows, write
+//    together (6.6 -> 3 us), and are joined by a second kernel.
+//  * Arrivals at the other CTA's barriers have no cluster-wide release (arrive_remote).
+//
+// Weights are rounded to bfloat16, and so sum up: an output is off by at most 2^-8 of the
+// weighted absolute values, as its own rounding is; a second part would double the products.
+//
+// Chunks of 256 tokens (N 256 for the scores: 2206 clocks for 128 tokens), with K through a
+// ring of columns and V through one of pages, were slower (98 us against 89 then): each
+// column's copy, barrier and commit is on its own, and the rings hold less ahead.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,9 +74,14 @@ namespace {
 constexpr int kPages = 8;                       // pages of a chunk
 constexpr int kRows = 64;                       // rows of a CTA
 constexpr int kTile = 2 * kRows;                // rows of a pair
-constexpr int kAheadChunks = 1;                 // chunks that are brought to L2 ahead of their copies
+// Chunks that are brought to L2 ahead of their copies.  (32 x 8192 tokens, 128 heads: 78.6 us
+// with 1, 80.9 with 2, 84.2 with 3, 84.7 without.)
+constexpr int kAheadChunks = 1;
 constexpr int kMinPages = 16;                   // least range of a pair of CTAs
-constexpr int kExtraPages = 32;                 // what a (sequence, tile) costs beside its pages
+// What a (sequence, tile) costs beside its pages: its queries, pipeline and results.  (Ragged 64
+// contexts: 65.6 us with 24, 64.1 with 32, 65.5 with 40; 81 with 16, 104 with 8 before the
+// results were written together.)
+constexpr int kExtraPages = 32;
 template <int LAT>
 struct Geo {
     static constexpr int kCols = LAT / 64;               // 64-element columns of the latent part
@@ -806,7 +831,9 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 // ------------------------------------------------------------------------- merge
 
 constexpr int kMaxWorkers = 256;
-// Parts of a tile, by workers and tiles, from which the warps share them out.
+// Parts of a tile, by workers and tiles, from which the warps share them out.  (4 x 131072 tokens,
+// 39 parts: four warps, each all parts of a quarter of the row 139 us, a part each in turn 137,
+// eight warps 125; 32 x 8192, 3 to 4 parts: a CTA for four pieces 85, for one 88.)
 constexpr int kMergeSplit = 8;
 
 constexpr int merge_warps(bool split) { return split ? 8 : 4; }
