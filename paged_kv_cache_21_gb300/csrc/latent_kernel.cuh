@@ -23,10 +23,20 @@ namespace {
 constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
 constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
 
-// misc words: tensor-memory base; abort; the range: its first page's unit, pages, units
-// per worker, first sequence, tile and page; that sequence's nodes, context and first node;
-// chunks whose scores have been seen
-enum Misc { M_TMEM = 0, M_ABORT, M_B0, M_CNT, M_Q, M_S0, M_T0, M_J0, M_N0, M_L0, M_NODE0, M_SEEN, M_WORDS };
+// misc words: tensor-memory base; abort; chunks whose scores have been seen; the range: the
+// pages before it (-1: no range) and before its end, its first page's sequence, tile, index
+// and unit, that sequence's nodes, context and first node, the units of a share; the warps'
+// units and pages while it is cut
+enum Misc {
+    M_TMEM = 0, M_ABORT, M_SEEN, M_P0, M_P1, M_S0, M_T0, M_J0, M_B0, M_N0, M_L0, M_NODE0, M_Q, M_SUMS,
+    M_WORDS = M_SUMS + 2 * 16
+};
+
+// Pages of this worker's range.
+__device__ __forceinline__ int range_pages(const volatile int* misc)
+{
+    return misc[M_P0] < 0 ? 0 : misc[M_P1] - misc[M_P0];
+}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -136,7 +146,7 @@ struct Walk {
         s = misc[M_S0];
         tile = misc[M_T0];
         j = misc[M_J0];
-        rem = misc[M_CNT];
+        rem = range_pages(misc);
         seg = 0;
         np = 0;
         if (rem > 0) {
@@ -176,83 +186,100 @@ struct Walk {
     }
 };
 
-// This worker's range of the list of pages, by sequence and tile: equal shares of at least
-// min_q units, where a page is a unit and each (sequence, tile) costs extra more
-// before its first page.  One warp.
-__device__ __forceinline__ void cut_work(const LatentParams& p, volatile int* misc, int min_q, int extra, int worker, bool flag, int lane)
+// This worker's range: the list of pages, by sequence and tile, is cut into equal shares of at
+// least min_q units, where a page is a unit and each (sequence, tile) costs extra more before its
+// first page.  One warp where its lanes have a sequence each; else the CTA's threads together
+// (a warp alone: 42.6 us for 256 sequences of 256 tokens, 16 heads; so 38.5).
+template <int kThreads>
+__device__ __forceinline__ void cut_work(const LatentParams& p, volatile int* misc, int min_q, int extra, int worker, bool flag, int tid)
 {
-    // (the sequences at hand stay in registers where one pass over them is all there is)
-    const bool once = p.B <= 32;
-    SeqInfo q = {0, 0, 0, 0, 0, 0};
-    long long total = 0;
-    for (int b = 0; b < p.B; b += 32) {
-        long long u = 0;
-        if (b + lane < p.B) {
-            q = seq_info(p, b + lane, flag);
-            u = q.nb > 0 ? (long long)(q.nb + extra) * q.tiles : 0;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
-        total += u;
-    }
-    // (all units are less than 2^31: the host has checked)
-    int share = (int)((uint32_t)(total + p.workers - 1) / (uint32_t)p.workers);
-    if (share < min_q) share = min_q;
-    // the first page at or behind unit x: its sequence, tile and index, its unit, and how
-    // many pages are before it
-    struct At {
-        int s, tile, j, unit, pages;
-        int n, L, t0;
-    };
-    const int lo = (int)min((long long)worker * share, total), hi = (int)min((long long)lo + share, total);
-    At at[2] = {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0}};
-    bool found[2] = {false, false};
-    int units = 0, pages = 0;                    // up to the 32 sequences at hand
-    for (int b = 0; b < p.B && !(found[0] && found[1]); b += 32) {
-        if (!once) {
-            q = {0, 0, 0, 0, 0, 0};
-            if (b + lane < p.B) q = seq_info(p, b + lane, false);
-        }
-        const int u = q.nb > 0 ? (q.nb + extra) * q.tiles : 0, n = q.nb * q.tiles;
-        int iu = u, in = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
-            if (lane >= o) {
-                iu += tu;
-                in += tn;
+    constexpr int kWarps = kThreads / 32;
+    static_assert(kWarps <= 16, "misc words");
+    const int lane = tid & 31, warp = tid >> 5;
+    const bool alone = p.B <= 32;
+    if (!alone || warp == 0) {
+        SeqInfo q;
+        int u, n, iu, in;                        // this thread's sequence's units and pages; with those before
+        int units, pages;                        // of the sequences at hand
+        auto take = [&](int b, bool raise) {
+            u = n = 0;
+            if (b + tid < p.B) {
+                q = seq_info(p, b + tid, raise);
+                u = q.nb > 0 ? (q.nb + extra) * q.tiles : 0;
+                n = q.nb * q.tiles;
             }
-        }
-        iu += units;
-        in += pages;
+            iu = u;
+            in = n;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int x = e == 0 ? lo : hi;
-            const unsigned m = __ballot_sync(kFull, iu > x);
-            if (found[e] || !m) continue;
-            found[e] = true;
-            const int src = __ffs(m) - 1;
-            const int nbs = __shfl_sync(kFull, q.nb, src), v = nbs + extra;
-            const int before = __shfl_sync(kFull, iu - u, src);
-            const int off = x - before, t = off / v, j = max(0, off - t * v - extra);
-            at[e] = {b + src, t, j, before + t * v + extra + j, __shfl_sync(kFull, in - n, src) + t * nbs + j,
-                     __shfl_sync(kFull, q.n, src), __shfl_sync(kFull, q.L, src), __shfl_sync(kFull, q.t0, src)};
+            for (int o = 1; o < 32; o <<= 1) {
+                const int tu = __shfl_up_sync(kFull, iu, o), tn = __shfl_up_sync(kFull, in, o);
+                if (lane >= o) {
+                    iu += tu;
+                    in += tn;
+                }
+            }
+            units = __shfl_sync(kFull, iu, 31);
+            pages = __shfl_sync(kFull, in, 31);
+            if (alone) {
+                __syncwarp();
+                return;
+            }
+            __syncthreads();                     // (the sums before have been read)
+            if (lane == 0) {
+                misc[M_SUMS + warp] = units;
+                misc[M_SUMS + 16 + warp] = pages;
+            }
+            __syncthreads();
+            units = pages = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const int tu = misc[M_SUMS + w], tn = misc[M_SUMS + 16 + w];
+                iu += w < warp ? tu : 0;
+                in += w < warp ? tn : 0;
+                units += tu;
+                pages += tn;
+            }
+        };
+        if (tid == 0) misc[M_P0] = -1;           // (take's barriers are between this and the range's)
+        // (all units are less than 2^31: the host has checked)
+        int total = 0, all = 0;
+        for (int b = 0; b < p.B; b += kThreads) {
+            take(b, flag);
+            total += units;
+            all += pages;
         }
-        units = __shfl_sync(kFull, iu, 31);
-        pages = __shfl_sync(kFull, in, 31);
+        const int share = max(min_q, (int)(((uint32_t)total + (uint32_t)p.workers - 1u) / (uint32_t)p.workers));
+        const int lo = (int)min((long long)worker * share, (long long)total);
+        const int hi = (int)min((long long)lo + share, (long long)total);
+        int units0 = 0, pages0 = 0;              // before the sequences at hand
+        for (int b = 0; b < p.B; b += kThreads) {
+            if (p.B > kThreads) take(b, false);
+            // the first page at or behind the range's ends
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int off = (e == 0 ? lo : hi) - (units0 + iu - u);
+                if (off < 0 || off >= u) continue;
+                const int v = q.nb + extra, t = off / v, j = max(0, off - t * v - extra);
+                const int before = pages0 + in - n + t * q.nb + j;
+                misc[e == 0 ? M_P0 : M_P1] = before;
+                if (e == 1) continue;
+                misc[M_S0] = b + tid;
+                misc[M_T0] = t;
+                misc[M_J0] = j;
+                misc[M_B0] = units0 + iu - u + t * v + extra + j;
+                misc[M_N0] = q.n;
+                misc[M_L0] = q.L;
+                misc[M_NODE0] = q.t0;
+            }
+            units0 += units;
+            pages0 += pages;
+        }
+        if (tid == 0) {
+            misc[M_Q] = share;
+            if (hi >= total) misc[M_P1] = all;
+        }
     }
-    if (!found[1]) at[1].pages = pages;          // (hi is the end of the list)
-    if (lane == 0) {
-        misc[M_B0] = at[0].unit;
-        misc[M_CNT] = found[0] ? at[1].pages - at[0].pages : 0;
-        misc[M_Q] = share;
-        misc[M_S0] = at[0].s;
-        misc[M_T0] = at[0].tile;
-        misc[M_J0] = at[0].j;
-        misc[M_N0] = at[0].n;
-        misc[M_L0] = at[0].L;
-        misc[M_NODE0] = at[0].t0;
-    }
+    __syncthreads();
 }
 
 // Node (within the sequence) of row r of its rows.

@@ -300,8 +300,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     umma::fence_after_sync();
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == G::kKWarp) cut_work(p, misc, kMinPages, kExtraPages, pair, blockIdx.x == 0, lane);
-    __syncthreads();
+    cut_work<G::kThreads>(p, misc, kMinPages, kExtraPages, pair, blockIdx.x == 0, tid);
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
     if (warp >= G::kKWarp && warp < G::kKWarp + G::kG1) {
@@ -473,7 +472,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             const uint64_t rdesc = umma::smem_desc_sw128(sb + G::kKOff + G::kGroups * G::kGroupBytes, 16, 1024);
             constexpr uint32_t idesc = umma::idesc_bf16_f32(128, 128, false, false);
             bool ok = true;
-            if (p.test_stall > 0 && misc[M_CNT] > 0 && !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
+            if (p.test_stall > 0 && range_pages(misc) > 0 && !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
                 give_up(misc);
                 ok = false;
             }

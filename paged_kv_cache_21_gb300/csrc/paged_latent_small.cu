@@ -168,8 +168,7 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
     umma::fence_after_sync();
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == G::kCopyWarp) cut_work(p, misc, kMinPages, kExtraPages, cta, cta == 0, lane);
-    __syncthreads();
+    cut_work<G::kThreads>(p, misc, kMinPages, kExtraPages, cta, cta == 0, tid);
     const uint32_t tmem = (uint32_t)misc[M_TMEM];
 
     if (warp >= G::kCopyWarp && warp < G::kCopyWarp + kPages) {
@@ -237,7 +236,7 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
             const uint64_t kdesc = umma::smem_desc_sw128(sb + G::kRingOff, 16, G::kEight);
             constexpr uint32_t idesc = umma::idesc_bf16_f32(64, 64, false, false);
             bool ok = true;
-            if (p.test_stall > 0 && misc[M_CNT] > 0 && !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
+            if (p.test_stall > 0 && range_pages(misc) > 0 && !mbar_wait_bounded(bar(G::B_STALL), 0u, p.test_stall)) {
                 misc[M_ABORT] = 1;
                 raise_flag(&g_latent_err, KV_DEVERR_PIPELINE_TIMEOUT, blockIdx.x);
                 ok = false;

@@ -674,3 +674,25 @@ def test_rotary_append_then_decode(pk):
             size = w @ v[:, h // G].abs()
             assert ((out[s, h].cpu().double() - w @ v[:, h // G]).abs()
                     <= (torch.exp(2 * off) - 1 + 2.0 ** -8) * size).all()
+
+
+@pytest.mark.parametrize("B,H,nodes", [(32, 16, 0), (33, 16, 0), (512, 8, 0), (513, 8, 2), (1100, 4, 0),
+                                       (600, 70, 2)])
+def test_latent_attention_shares_of_any_batch(pk, B, H, nodes):
+    """The work is cut by one warp, by all of a CTA, or by it in turns, as the batch has it; some
+    sequences have no context, and some no nodes."""
+    rng = np.random.default_rng(B)
+    counts = None if nodes == 0 else rng.integers(0, nodes + 1, size=B)
+    c = Case(rng.integers(0, 40, size=B), counts, H, 256, 32, seed=B)
+    c.lens[3 % B] = 0 if counts is None else c.lens[3 % B]
+    c.lens[B - 1] = 0 if counts is None else c.lens[B - 1]
+    c.check(c.run(pk))
+    assert pk.get_device_error()[0] == 0
+
+
+def test_latent_attention_one_long_among_many_empty(pk):
+    """Behind a thousand sequences without a context, the last one's pages are shared out."""
+    c = Case(np.concatenate([np.zeros(1030, dtype=int), [2500]]), None, 16, 256, 32, seed=3)
+    c.lens[:1030] = 0
+    c.check(c.run(pk))
+    assert pk.get_device_error()[0] == 0
