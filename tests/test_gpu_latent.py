@@ -696,3 +696,69 @@ def test_latent_attention_one_long_among_many_empty(pk):
     c.lens[:1030] = 0
     c.check(c.run(pk))
     assert pk.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_blocks_far_into_a_large_cache(pk, H):
+    """Blocks whose bytes and elements are behind 2^32, appended to and attended over."""
+    L, rope = 512, 64
+    W = L + rope
+    NB = 2 ** 32 // (16 * W) + 40                    # 8.6 GB, of which only the last pages are used
+    cache = torch.empty((NB, 16, W), dtype=BF, device="cuda")
+    c = Case([150], None, H, L, rope, seed=H)
+    n = int(c.lens[0])
+    blocks = NB - 1 - np.arange(-(-n // 16)) * 2
+    gen = torch.Generator().manual_seed(1)
+    rows = randn(gen, n, W).to(BF)
+    slots = torch.from_numpy(blocks[np.arange(n) // 16] * 16 + np.arange(n) % 16)
+    assert int(slots.max()) * W > 2 ** 32
+    still = torch.zeros(n, dtype=torch.int64)        # (position 0 turns nothing)
+    pk.kv_latent_append(None, None, rows[:, :L].cuda(), rows[:, L:].cuda(), cache, slots.cuda(),
+                        still.cuda(), torch.ones(rope // 2).cuda())
+    used = torch.from_numpy(blocks).cuda()
+    small = cache[used].cpu()
+    assert torch.equal(small.flatten(0, 1)[:n], rows)
+    bt = torch.from_numpy(blocks.astype(np.int32))[None].cuda()
+    out = torch.empty((1, H, L), dtype=BF, device="cuda")
+    ws = pk.alloc_latent_workspace(1, 1, H, L, rope)
+    pk.paged_latent_attention(out, c.q.cuda(), cache, bt, torch.tensor([n], dtype=torch.int32).cuda(),
+                              c.scale, ws)
+    want, bound = R.attention(c.q, small, np.arange(len(blocks))[None], [n], [0, 1], None, c.scale, L)
+    check(out, want, bound, "attention")
+    assert pk.get_device_error()[0] == 0
+
+
+def test_latent_attention_tables_in_pinned_memory(pk):
+    for H in (9, 100):
+        c = Case([90, 0, 259], [4, 3, 1], H, 256, 64, "tree", seed=H)
+        first = c.run(pk).cpu()
+        pin = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).pin_memory()  # noqa: E731
+        out = torch.empty((c.total, H, 256), dtype=BF, device="cuda")
+        ws = pk.alloc_latent_workspace(3, 4, H, 256, 64)
+        tables = pin(c.bt), pin(c.lens), pin(c.starts), pin(c.parents)
+        pk.paged_latent_attention(out, c.q.cuda(), c.cache.cuda(), tables[0], tables[1], c.scale, ws,
+                                  node_starts=tables[2], parents=tables[3], max_nodes=4)
+        assert torch.equal(out.cpu(), first)
+
+
+def test_calls_of_both_kernels_share_a_workspace_one_after_the_other(pk):
+    """Back to back on a stream, each launched while the one before drains: few rows, many rows,
+    split and whole, with the workspace of the largest."""
+    cases = [Case([5000], None, 16, 512, 64, seed=1), Case([3000, 40], [3, 2], 50, 512, 64, seed=2),
+             Case([20], None, 128, 512, 64, seed=3), Case([700, 900], [1, 2], 20, 512, 64, seed=4)]
+    want = [c.run(pk).cpu() for c in cases]
+    ws = pk.alloc_latent_workspace(2, 128, 128, 512, 64)
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    calls = []
+    for c in cases:
+        calls.append(((c.q.cuda(), c.cache.cuda(), i32(c.bt), i32(c.lens), c.scale, ws),
+                      dict(node_starts=None if c.single else i32(c.starts), max_nodes=c.max_nodes)))
+    outs = [[torch.empty_like(w, device="cuda") for w in want] for _ in range(6)]
+    torch.cuda.synchronize()
+    for r in outs:
+        for out, (args, kw) in zip(r, calls):
+            pk.paged_latent_attention(out, *args, **kw)
+    torch.cuda.synchronize()
+    for r in outs:
+        for out, w in zip(r, want):
+            assert torch.equal(out.cpu(), w)
