@@ -842,7 +842,8 @@ int kv_read_ceiling(const void* buf, size_t bytes, unsigned* sink, void* stream)
  * than 32 rows, bf16 cache, head_dim 128) the score-MMA warp of every CTA does so on its first wait, and every
  * role of the CTA then stops (copies and MMAs in flight are waited for and
  * tensor memory is freed before the CTA ends); so does the MMA warp of
- * paged_tree_attention's kernels.  It lets a test see the flag without a
+ * paged_tree_attention's kernels, and the score-MMA warp of
+ * paged_latent_attention's.  It lets a test see the flag without a
  * copy that really never arrives.  0 (the default) turns it off; a value
  * outside [0, 2^31] returns KV_ERR_INVALID_ARG.  Process-wide. */
 int kv_test_pipeline_stall(long long cycles);

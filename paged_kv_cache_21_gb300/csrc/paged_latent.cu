@@ -22,10 +22,11 @@
 // TB/s, 152 SMs), ~3300 clocks.  A chunk's 36 products of N 128 and 16 of N 256 with their
 // commits take ~3010 clocks (measured; one of N 128 takes 53, 45 at least whatever its N,
 // one of N 256 65).  In the loop a chunk takes ~3500: 94 % of HBM's rate.  32 x 8192 tokens,
-// 128 heads: 78 us, of which ~50 are HBM's at its rate, ~6 until the first keys are there
+// 128 heads: 79 us, of which ~50 are HBM's at its rate, ~6 until the first keys are there
 // (tables, the cut, block ids and a first copy, each behind the one before), ~5 the last
 // chunk's products and its 131 KB of partial results a CTA, ~8 the merge.  Four tokens x 128
-// heads over 32 x 2048: 87 us, tensor cores and the ends of 2.7 tiles a pair.
+// heads over 32 x 2048: 87 us, tensor cores and the ends of 2.7 tiles a pair.  1024 x 256, 128
+// heads: 187 (HBM 88), the sequences' ends.
 //
 // How:
 //  * Each byte of the cache is copied twice, as K to one CTA and as V to either, and shared
