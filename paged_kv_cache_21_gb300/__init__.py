@@ -845,32 +845,41 @@ def _rows(name, t, dtype, shape, dev, inner=1):
     return t.data_ptr()
 
 
+def _current(t):
+    """The device index of a cache, which has to be the current device's memory."""
+    i = t.get_device()
+    if i < 0 or i != _torch._C._cuda_getDevice():
+        _device_only(t)
+        _place(t)
+    return i
+
+
 def _heads(name, t, dtype, shape, dev):
-    """(address, elements from one token to the next) of a [T, heads, D] tensor whose
-    tokens may be apart."""
+    """(address, elements from one token to the next) of a [T, heads, D] tensor, of the shape
+    that has been read from it or compared with it, whose tokens may be apart."""
     T, n, D = shape
     token, head, step = t.stride()
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and step == 1
-            and (head == D or n == 1)):
+    if not (t.dtype is dtype and t.get_device() == dev and step == 1 and (head == D or n == 1)):
         _rows(name, t, dtype, tuple(shape), dev, 2)
     # (of one token, what a tensor of several would have at least)
     return t.data_ptr(), token if T > 1 else n * D
 
 
 def _vectors(name, t, dtype, shape, dev):
-    """Address of a tensor of vectors that may be apart."""
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.stride(-1) == 1):
+    """(address, elements from one vector to the next) of a [T, n] tensor of vectors, of the
+    shape that has been read from it or compared with it, that may be apart."""
+    row, step = t.stride()
+    if not (t.dtype is dtype and t.get_device() == dev and step == 1):
         _rows(name, t, dtype, tuple(shape), dev)
-    return t.data_ptr()
+    return t.data_ptr(), row if shape[0] > 1 else shape[1]
 
 
 def _head_vectors(name, t, dtype, shape, dev):
-    """(address, strides of tokens and heads) of a [T, H, R] tensor of vectors that may be
-    apart."""
+    """(address, strides of tokens and heads) of a [T, H, R] tensor of vectors, of the shape
+    that has been read from it or compared with it, that may be apart."""
     T, H, R = shape
     token, head, step = t.stride()
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and step == 1):
+    if not (t.dtype is dtype and t.get_device() == dev and step == 1):
         _rows(name, t, dtype, tuple(shape), dev)
     # (of a single one, what a tensor of several would have at least)
     if H == 1:
@@ -904,17 +913,19 @@ def kv_append_rotary(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     T, Hkv, D = kshape
     cshape, cdtype, bf16 = k_cache.shape, k_cache.dtype, torch.bfloat16
     NB, H2, block, D2 = cshape
-    if (H2 != Hkv or D2 != D or block != BLOCK_SIZE or v_cache.shape != cshape
-            or v_cache.dtype is not cdtype or (q is None) != (q_out is None)):
+    if (H2 != Hkv or D2 != D or block != BLOCK_SIZE or v.shape != kshape
+            or v_cache.shape != cshape or v_cache.dtype is not cdtype
+            or (q is None) != (q_out is None)):
         raise ValueError("k and v must be [T, Hkv, D], k_cache and v_cache [NB, Hkv, 16, D], alike")
-    _device_only(k_cache, v_cache)
-    dev = _place(k_cache)
+    dev = _current(k_cache)
+    if v_cache.get_device() != dev:
+        _device_only(v_cache)
     Hq = po = so = pq = sq = 0
     if q is not None:
         qshape = q.shape
         Hq = qshape[1]
-        if len(qshape) != 3 or qshape[0] != T or qshape[2] != D:
-            raise ValueError("q must be [T, Hq, D]")
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != D or q_out.shape != qshape:
+            raise ValueError("q and q_out must be [T, Hq, D]")
         if Hq:
             pq, sq = _heads("q", q, bf16, qshape, dev)
             po, so = _heads("q_out", q_out, bf16, qshape, dev)
@@ -941,24 +952,23 @@ def kv_latent_append(q_out, q_rope, latent, k_rope, cache, slot_mapping, positio
     torch = _torch or _load_torch()
     bf16 = torch.bfloat16
     T, L = lshape = latent.shape
-    R = k_rope.shape[1]
+    T2, R = rshape = k_rope.shape
     NB, _, W = _cache_shape(cache, True)
-    if W != L + R or cache.dtype is not bf16 or (q_rope is None) != (q_out is None):
-        raise ValueError("cache must be bfloat16 [NB, 16, L + R]")
-    _device_only(cache)
-    dev = _place(cache)
+    if T2 != T or W != L + R or cache.dtype is not bf16 or (q_rope is None) != (q_out is None):
+        raise ValueError("latent must be [T, L], k_rope [T, R], cache bfloat16 [NB, 16, L + R]")
+    dev = _current(cache)
     H, qs = 0, (0, 0, 0, 0, 0, 0)
     if q_rope is not None:
         qshape = q_rope.shape
         H = qshape[1]
-        if len(qshape) != 3 or qshape[0] != T or qshape[2] != R:
-            raise ValueError("q_rope must be [T, H, R]")
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != R or q_out.shape != qshape:
+            raise ValueError("q_rope and q_out must be [T, H, R]")
         if H:
             qs = (_head_vectors("q_out", q_out, bf16, qshape, dev)
                   + _head_vectors("q_rope", q_rope, bf16, qshape, dev))
     _check(_HOT_LATENT_APPEND(
-        *qs, _vectors("latent", latent, bf16, lshape, dev), latent.stride(0) if T > 1 else L,
-        _vectors("k_rope", k_rope, bf16, (T, R), dev), k_rope.stride(0) if T > 1 else R,
+        *qs, *_vectors("latent", latent, bf16, lshape, dev),
+        *_vectors("k_rope", k_rope, bf16, rshape, dev),
         _ptr("norm_weight", norm_weight, bf16, L, dev) if norm_weight is not None else 0,
         float(eps), _ptr("cache", cache, bf16, cache.numel(), dev),
         *_tables(slot_mapping, positions, inv_freq, T, R // 2, dev),
@@ -997,8 +1007,8 @@ def paged_latent_attention(out, q, cache, block_tables, context_lens, scale, wor
     bf16, i32 = torch.bfloat16, torch.int32
     if tuple(out.shape) != (T, H, L) or W2 != W or L >= W:
         raise ValueError("q must be [T, H, L + R], out [T, H, L], cache [NB, 16, L + R]")
-    _device_only(out, q, cache, workspace)
-    dev = _place(cache)
+    _device_only(out, q, workspace)
+    dev = _current(cache)
     _check(_HOT_LATENT_ATTENTION(
         _ptr("out", out, bf16, out.numel(), dev), _ptr("q", q, bf16, q.numel(), dev),
         _ptr("cache", cache, bf16, cache.numel(), dev), NB,
