@@ -762,3 +762,55 @@ def test_calls_of_both_kernels_share_a_workspace_one_after_the_other(pk):
     for r in outs:
         for out, w in zip(r, want):
             assert torch.equal(out.cpu(), w)
+
+
+@pytest.mark.parametrize("H,n", [(16, 1), (40, 3)])
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+def test_latent_attention_scales_of_any_sign(pk, H, n, scale):
+    c = Case([400, 30], [n, 1], H, 256, 64, "tree", seed=H, scale=scale)
+    c.check(c.run(pk))
+
+
+@pytest.mark.parametrize("H,n", [(16, 1), (40, 3)])
+def test_latent_attention_rows_do_not_reach_each_other(pk, H, n):
+    """NaN, infinities and the largest values in some queries change no other row's bits, in
+    sequences of one part and of several."""
+    c = Case([4000, 300, 30], [n, n, 1], H, 512, 64, seed=H)
+    clean = c.run(pk).cpu()
+    c.check(clean)
+    bad = {(0, 1): float("nan"), (0, H - 1): float("inf"), (n, 5): -float("inf"),
+           (n, 7): 3.3e38, (2 * n, 0): float("nan")}
+    for (t, h), x in bad.items():
+        c.q[t, h, 3] = x
+    got = c.run(pk).cpu()
+    for (t, h), x in bad.items():
+        if x != x:
+            assert torch.isnan(got[t, h]).all()
+        got[t, h] = clean[t, h]
+    assert torch.equal(got, clean)
+    assert pk.get_device_error()[0] == 0
+
+
+def test_no_tokens_and_no_sequences(pk):
+    cache = torch.full((4, 16, 288), 2.0, dtype=BF, device="cuda")
+    kc = torch.full((4, 2, 16, 64), 2.0, dtype=BF, device="cuda")
+    e = lambda *s, t=BF: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    none = e(0, t=torch.int64)
+    pk.kv_append_rotary(e(0, 4, 64), e(0, 4, 64), e(0, 2, 64), e(0, 2, 64), kc, kc.clone(), none, none,
+                        e(32, t=torch.float32))
+    pk.kv_latent_append(e(0, 4, 32), e(0, 4, 32), e(0, 256), e(0, 32), cache, none, none,
+                        e(16, t=torch.float32))
+    ws = pk.alloc_latent_workspace(0, 1, 4, 256, 32)
+    i32 = torch.int32
+    pk.paged_latent_attention(e(0, 4, 256), e(0, 4, 288), cache, e(0, 3, t=i32), e(0, t=i32), 0.1, ws)
+    torch.cuda.synchronize()
+    assert (cache == 2.0).all() and (kc == 2.0).all()
+    # nodes without sequences' contexts, sequences without nodes
+    out = torch.full((1, 4, 256), 5.0, dtype=BF, device="cuda")
+    starts = torch.tensor([0, 0, 0], dtype=i32, device="cuda")
+    bt = torch.zeros((2, 2), dtype=i32, device="cuda")
+    pk.paged_latent_attention(out, torch.ones((1, 4, 288), dtype=BF, device="cuda"), cache, bt,
+                              torch.tensor([20, 0], dtype=i32, device="cuda"), 0.1, ws,
+                              node_starts=starts)
+    assert (out == 5.0).all()
+    assert pk.get_device_error()[0] == 0
