@@ -838,6 +838,13 @@ constexpr int kMergeSplit = 8;
 
 constexpr int merge_warps(bool split) { return split ? 8 : 4; }
 
+// Parts of a tile of few rows, likewise, from which a lane has more parts' loads under way, eight
+// instead of two, and a CTA more registers.  (32 x 8192, 16 heads, 5 to 6 parts: 65.7 us with eight, 1
+// more with four, 69 with two; 64 x 4096, 64 heads, 2 to 3 parts: 3 more with eight than with two.)
+constexpr int kMergeWide = 4;
+
+constexpr int merge_parts(bool wide) { return wide ? 8 : 2; }
+
 // What a row gets that has no weight: NaN if it sees a position (its scores were -inf alone).
 __device__ __forceinline__ float weightless(const LatentParams& p, int s, int r)
 {
@@ -851,11 +858,11 @@ __device__ __forceinline__ float weightless(const LatentParams& p, int s, int r)
 
 // CTA (e, piece): a piece of the e-th tile that has parts, in the order of the workers that
 // wrote its first part.  A warp reads 64 elements of 8 rows, where fours of the rows'
-// elements lie together, or a row (BY_ROW), where its elements do, two parts at a time with
-// a running (max, sum).  Few parts: the warps have different elements.  Many (SPLIT): they
+// elements lie together, or a row (BY_ROW), where its elements do, a few parts at a time
+// with a running (max, sum).  Few parts: the warps have different elements.  Many (SPLIT): they
 // take the parts in turn, and their results are joined in the warps' order.
-template <int LAT, bool BY_ROW, bool SPLIT>
-__global__ void __launch_bounds__(merge_warps(SPLIT) * 32, SPLIT ? 4 : 8) paged_latent_merge_kernel(const LatentParams p)
+template <int LAT, bool BY_ROW, bool SPLIT, bool WIDE>
+__global__ void __launch_bounds__(merge_warps(SPLIT) * 32, SPLIT ? 4 : WIDE ? 2 : 8) paged_latent_merge_kernel(const LatentParams p)
 {
     constexpr int kMergeWarps = merge_warps(SPLIT);
     constexpr int kFours = LAT / 4, kN = BY_ROW ? LAT / 128 : 4;     // fours of a row; of a lane
@@ -905,12 +912,12 @@ __global__ void __launch_bounds__(merge_warps(SPLIT) * 32, SPLIT ? 4 : 8) paged_
     float M = -INFINITY, l = 0.f, acc[kN][4];
 #pragma unroll
     for (int k = 0; k < kN; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-    constexpr int kStride = SPLIT ? kMergeWarps : 1;
-    for (int i = SPLIT ? warp : 0; any_row && i < parts; i += 2 * kStride) {
-        float2 ml[2];
-        float4 o[2][kN];
+    constexpr int kStride = SPLIT ? kMergeWarps : 1, kParts = merge_parts(WIDE);
+    for (int i = SPLIT ? warp : 0; any_row && i < parts; i += kParts * kStride) {
+        float2 ml[kParts];
+        float4 o[kParts][kN];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kParts; ++h) {
             const bool there = i + h * kStride < parts;
             const size_t at = slot(there ? i + h * kStride : i);
             ml[h] = there ? p.part_ml[at + row] : make_float2(-INFINITY, 0.f);
@@ -921,18 +928,29 @@ __global__ void __launch_bounds__(merge_warps(SPLIT) * 32, SPLIT ? 4 : 8) paged_
                 o[h][k] = there ? src[BY_ROW ? row * kFours + f : f * R + row] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
-        const float top = fmaxf(M, fmaxf(ml[0].x, ml[1].x));
+        float top = M, a[kParts];
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) top = fmaxf(top, ml[h].x);
         // a part that saw nothing weighs nothing (its maximum is -inf)
-        const float w = M == -INFINITY ? 0.f : ex2(M - top), a = ml[0].x == -INFINITY ? 0.f : ex2(ml[0].x - top);
-        const float b = ml[1].x == -INFINITY ? 0.f : ex2(ml[1].x - top);
+        const float w = M == -INFINITY ? 0.f : ex2(M - top);
         M = top;
-        l = l * w + ml[0].y * a + ml[1].y * b;
+        l *= w;
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            a[h] = ml[h].x == -INFINITY ? 0.f : ex2(ml[h].x - top);
+            l += ml[h].y * a[h];
+        }
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            acc[k][0] = acc[k][0] * w + o[0][k].x * a + o[1][k].x * b;
-            acc[k][1] = acc[k][1] * w + o[0][k].y * a + o[1][k].y * b;
-            acc[k][2] = acc[k][2] * w + o[0][k].z * a + o[1][k].z * b;
-            acc[k][3] = acc[k][3] * w + o[0][k].w * a + o[1][k].w * b;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[k][e] *= w;
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) {
+                acc[k][0] += o[h][k].x * a[h];
+                acc[k][1] += o[h][k].y * a[h];
+                acc[k][2] += o[h][k].z * a[h];
+                acc[k][3] += o[h][k].w * a[h];
+            }
         }
     }
     if constexpr (SPLIT) {
@@ -1051,7 +1069,7 @@ int launch_many(const LatentParams& p, const void* q, const void* cache, cudaStr
     return cudaLaunchKernelEx(&cfg, paged_latent_kernel<LAT>, mq, mqr, mk, mkr, mv, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
-template <int LAT, bool BY_ROW, bool SPLIT>
+template <int LAT, bool BY_ROW, bool SPLIT, bool WIDE = false>
 int launch_merge(const LatentParams& p, int tiles, int rows, cudaStream_t st)
 {
     constexpr int kMergeWarps = merge_warps(SPLIT);
@@ -1065,7 +1083,7 @@ int launch_merge(const LatentParams& p, int tiles, int rows, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_latent_merge_kernel<LAT, BY_ROW, SPLIT>, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_latent_merge_kernel<LAT, BY_ROW, SPLIT, WIDE>, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
 template <int LAT>
@@ -1080,6 +1098,7 @@ int launch_all(const LatentParams& p, bool few, const void* q, const void* cache
     const long long all = (long long)p.B * ((p.max_nodes * p.H + p.tile_rows - 1) / p.tile_rows);
     const int tiles = (int)std::min<long long>(all, p.workers), rows = std::min(p.max_nodes * p.H, p.tile_rows);
     const bool split = p.workers / tiles >= kMergeSplit;
+    if (few && !split && p.workers / tiles >= kMergeWide) return launch_merge<LAT, true, false, true>(p, tiles, rows, st);
     if (few)
         return split ? launch_merge<LAT, true, true>(p, tiles, rows, st) : launch_merge<LAT, true, false>(p, tiles, rows, st);
     return split ? launch_merge<LAT, false, true>(p, tiles, rows, st) : launch_merge<LAT, false, false>(p, tiles, rows, st);

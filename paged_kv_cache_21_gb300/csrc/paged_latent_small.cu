@@ -10,8 +10,8 @@
 // What bounds it (L = 512, R = 64): a group's 74 KB take HBM 1.68 us to one SM (6.7 TB/s, 152
 // SMs), ~3300 clocks; its products, 36 of M 64, N 64 (45 clocks each at least, measured, 50
 // to 58 beside the others) and 16 of M 128, N 64 (49), ~2400 at least.  In the loop a group
-// takes ~3650: 90 % of HBM's rate.  32 x 8192 tokens, 16 heads: 69 us (HBM 45; ~6 until the
-// first keys are there, ~6 for the ends and the merge); 4 x 131072, 64 rows: 125 (91); one
+// takes ~3650: 90 % of HBM's rate.  32 x 8192 tokens, 16 heads: 66 us (HBM 45; ~6 until the
+// first keys are there, ~5 for the ends and the merge); 4 x 131072, 64 rows: 125 (91); one
 // context of 128 tokens: 11, a chain of short steps.  paged_latent.cu's kernel copies every
 // byte twice: 78 and 147 us for the first two then, 71 and 139 with this one.
 //
@@ -21,8 +21,8 @@
 //    group's rows are at one stride for the scores, and each page, at the same stride, is
 //    one step of the products.  A page is copied anew as soon as its products are done, by a
 //    warp of its own; with two groups only, the time from there to the next scores counts,
-//    so pages are prefetched to L2 shortly before (69.1 us; 71.2 without, 70.2 two groups
-//    ahead, 73 three).
+//    so pages are prefetched to L2 shortly before (with a slower merge 69.1 us; 71.2 without,
+//    70.2 two groups ahead, 73 three).
 //  * An accumulator of M = 64 has row r in lane 32 (r / 16) + r % 16: each warp weighs 16
 //    rows, two threads a row with 32 tokens each.
 //  * What must not be multiplied in V is cleared where it lies after the group's scores are
@@ -44,8 +44,8 @@ constexpr int kPages = 4;                       // pages of a group
 constexpr int kRows = kLatentFew;
 constexpr int kAheadGroups = 1;                 // groups that are brought to L2 ahead of their copies (above)
 constexpr int kMinPages = 8;                    // least range of a CTA
-// What a sequence costs beside its pages.  (32 x 8192 tokens: 69.0 us with 6, 69.2 with 12, 70.4
-// with 20; 8 x 4096 at L = 256: 18.0, 16.6 to 17.0, 17.0.)
+// What a sequence costs beside its pages.  (32 x 8192 tokens, with a slower merge: 69.0 us with 6, 69.2 with 12,
+// 70.4 with 20; 8 x 4096 at L = 256: 18.0, 16.6 to 17.0, 17.0.)
 constexpr int kExtraPages = 12;
 
 template <int LAT>

@@ -11,7 +11,7 @@
 // HBM bounds the large calls and the launch the small ones.  8192 tokens, 32 q / 8 KV heads,
 // d128: 32.5 us, 6.2 TB/s of its 201 MB; 256 tokens to E4M3: 4.6 us on the device (8.7 a call:
 // the host); one token: 2.1 (8.3).  Latent rows of 512 + 64 and 16 heads, 8192 tokens: 9 us
-// on the device, 16 a call; 32 tokens, 128 heads: 2.2 and 14.
+// on the device, 17 a call; 32 tokens, 128 heads: 2.2 and 14.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
