@@ -22,14 +22,16 @@ namespace {
 
 constexpr long long kWaitLimit = 1LL << 31;     // ~1 s of SM clocks
 constexpr float kMaxLag = 8.f;                  // the reference maximum may lag by 2^8
+constexpr int kCopiers = 6;                     // entries of M_ISSUED: of a CTA, and of the other CTA of a pair
 
 // misc words: tensor-memory base; abort; chunks whose scores have been seen; the range: the
 // pages before it (-1: no range) and before its end, its first page's sequence, tile, index
 // and unit, that sequence's nodes, context and first node, the units of a share; the warps'
-// units and pages while it is cut
+// units and pages while it is cut; how many chunks (queries: segments) each copying warp has
+// arrived for
 enum Misc {
     M_TMEM = 0, M_ABORT, M_SEEN, M_P0, M_P1, M_S0, M_T0, M_J0, M_B0, M_N0, M_L0, M_NODE0, M_Q, M_SUMS,
-    M_WORDS = M_SUMS + 2 * 16
+    M_ISSUED = M_SUMS + 2 * 16, M_WORDS = M_ISSUED + 2 * kCopiers
 };
 
 // Pages of this worker's range.
@@ -78,6 +80,22 @@ __device__ __forceinline__ bool wait_seen(int g, volatile int* misc)
         __nanosleep(100);
     }
     return true;
+}
+
+// After a wait has run out, with every role at its end: the copies under way land.  Each phase of
+// a barrier that counts copies has an arrival, with the bytes, of each of n copying warps, which
+// have arrived for the first issued[0 .. n) of its chunks; where one of them has come further
+// than another, the arrivals that are missing are made here, so that the phases end with the
+// bytes.  (None is ahead by more than the ring: it waits there for products of what all have
+// copied.)  One thread.
+template <int kSlots, typename Bar>
+__device__ __forceinline__ void land(const volatile int* issued, int n, Bar bar)
+{
+    int most = 0;
+    for (int i = 0; i < n; ++i) most = max(most, issued[i]);
+    for (int i = 0; i < n; ++i)
+        for (int g = issued[i]; g < most; ++g) mbar_arrive(bar(g));
+    for (int g = max(0, most - kSlots); g < most; ++g) mbar_wait_bounded(bar(g), (uint32_t)g / kSlots & 1u, kWaitLimit);
 }
 
 // Bring page `id` of the cache to L2: this lane's lines of it, one of 8 lanes'.

@@ -105,6 +105,7 @@ struct Geo {
     static constexpr int kBarOff = kPOff + kPBytes;
     // barriers; (L): the first CTA's is the one that counts
     static constexpr int kG1 = kGroups + 1;
+    // (B_QFULL, B_KFULL, B_VREADY: an arrival of either CTA, with the bytes that it copies)
     static constexpr int B_QFULL = 0;                            // (L) Q of both CTAs has landed
     static constexpr int B_QFREE = B_QFULL + 1;                  // the segment's last scores are computed
     static constexpr int B_KFULL = B_QFREE + 1;                  // (L) + slot * kG1 + group: K of both CTAs
@@ -126,6 +127,7 @@ struct Geo {
     static constexpr int kEnd = kRedOff + 4 * kRows * 4;
     static constexpr int kSmem = kEnd;
     static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(1 + kG1 + 2 <= kCopiers, "misc words");
     // tensor memory: two buffers of S, then O
     static constexpr uint32_t kColO = 128, kTmemCols = kColO + kHalves * 128 <= 256 ? 256 : 512;
 };
@@ -159,6 +161,17 @@ __device__ __forceinline__ void cluster_sync()
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// The same, with bytes that this CTA's copies are going to count there.
+__device__ __forceinline__ void arrive_remote_expect(uint32_t cluster_bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, uint32_t x)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
 }
 
 // Stores to the other CTA's shared memory are performed before what follows.
@@ -208,8 +221,7 @@ __device__ __forceinline__ void commit2(uint32_t bar)
 __device__ __forceinline__ void give_up(volatile int* misc)
 {
     misc[M_ABORT] = 1;
-    const uint32_t there = map_rank(smem_u32(const_cast<int*>(misc) + M_ABORT), cluster_rank() ^ 1u);
-    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(there) : "memory");
+    store_remote(map_rank(smem_u32(const_cast<int*>(misc) + M_ABORT), cluster_rank() ^ 1u), 1u);
     raise_flag(&g_latent_err, KV_DEVERR_PIPELINE_TIMEOUT, blockIdx.x);
 }
 
@@ -260,14 +272,18 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     auto pass = [](int g) -> uint32_t { return (uint32_t)g / G::kSlots & 1u; };
     // its products are done
     auto done = [&](int g) -> uint32_t { return bar(G::B_VFREE + slot(g) * 2 + 1); };
+    // the first CTA is told how far copying warp i of this one has come: Q, groups of K, halves of V
+    auto issued = [&](int i, int n) {
+        store_remote(map_rank(sb + (uint32_t)(G::kMiscOff + 4 * (M_ISSUED + 2 * i + (int)rank)), 0u), (uint32_t)n);
+    };
 
     if (tid == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        mbar_init(bar(G::B_QFULL), 1);
+        mbar_init(bar(G::B_QFULL), 2);
         mbar_init(bar(G::B_QFREE), 1);
         for (int i = 0; i < G::kSlots * G::kG1; ++i) {
-            mbar_init(bar(G::B_KFULL + i), 1);
+            mbar_init(bar(G::B_KFULL + i), 2);
             mbar_init(bar(G::B_KFREE + i), 1);
         }
         for (int i = 0; i < G::kSlots * 2; ++i) {
@@ -308,20 +324,21 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ------------------------- Q and K: a warp for each group of K's columns
         const int k = warp - G::kKWarp;
         const bool rope = k == G::kGroups;
-        int g = 0;
+        int g = 0, queries = 0;
         bool ok = true;
         for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
             if (k == 0 && w.seg > 0) ok = wait_warp(bar(G::B_QFREE), (uint32_t)((w.seg - 1) & 1), misc);
             if (!ok) break;
             if (k == 0 && lane == 0) {
-                if (rank == 0) mbar_arrive_expect_tx(bar(G::B_QFULL), 2u * G::kQBytes);
                 const int row = w.q.t0 * p.H + w.tile * kTile + (int)rank * kRows;
                 const uint32_t qf = lead(G::B_QFULL);
+                arrive_remote_expect(qf, (uint32_t)G::kQBytes);
 #pragma unroll
                 for (int x = 0; x < G::kGroups; ++x)
                     tma2_load_3d(sb + (uint32_t)(G::kQOff + x * 4 * kRows * 128), &tm_q, 0, row, 4 * x, qf);
                 tma2_load_2d(sb + (uint32_t)(G::kQOff + G::kCols * kRows * 128), &tm_qr, LAT, row, qf);
             }
+            ++queries;
             const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
             const int nc = w.chunks();
             int ids = lane < w.np ? __ldg(row + lane) : -1;           // pages 0..31 of the segment
@@ -341,18 +358,15 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 const int mypage = 4 * (int)rank + ((lane & 7) >> 1);
                 const int id = __shfl_sync(kFull, ids, (c & 3) * kPages + mypage);
                 const bool mine = lane < 8 && ((all >> mypage) & 1u);
-                const int n = __popc(all), sl = slot(g), b = sl * G::kG1 + k;
+                const int n = __popc(__ballot_sync(kFull, mine)), sl = slot(g), b = sl * G::kG1 + k;
                 if (g >= G::kSlots && !wait_warp(bar(G::B_KFREE + b), pass(g) ^ 1u, misc)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0 && rank == 0) {
-                    if (n > 0) mbar_arrive_expect_tx(bar(G::B_KFULL + b), (uint32_t)(n * (rope ? 2048 : 8192)));
-                    else mbar_arrive(bar(G::B_KFULL + b));
-                }
-                __syncwarp();
                 const uint32_t kb = sb + (uint32_t)(G::kKOff + sl * G::kKSlot);
                 const uint32_t kf = lead(G::B_KFULL + b);
+                if (lane == 0) arrive_remote_expect(kf, (uint32_t)(n * (rope ? 1024 : 4096)));
+                __syncwarp();
                 if (!rope) {
                     if (mine)
                         tma2_load_3d(kb + (uint32_t)(k * G::kGroupBytes + lane * 4096), &tm_k, 0,
@@ -363,11 +377,9 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
         }
-        // every copy lands before the pair can end: those of a pair that ran to its end were
-        // all waited for by the MMA warp; one that gave up leaves them time
-        if (!ok) {
-            const long long t0 = clock64();
-            while (clock64() - t0 < 400000) __nanosleep(1000);
+        if (lane == 0) {
+            issued(1 + k, g);
+            if (k == 0) issued(0, queries);
         }
         __syncwarp();
     } else if (warp == G::kVWarp || warp == G::kVWarp + 1) {
@@ -405,17 +417,17 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 const uint32_t ready = lead(G::B_VREADY + b), full = fix ? bar(G::B_VFIX + h) : ready;
                 if (lane == 0) {
-                    // (the first CTA expects both CTAs' bytes where they count there)
                     if (fix) mbar_arrive_expect_tx(full, (uint32_t)(n * 4096));
-                    else if (rank == 0) mbar_arrive_expect_tx(bar(G::B_VREADY + b), (uint32_t)(n * 8192));
-                    else arrive_remote(ready);
+                    else arrive_remote_expect(ready, (uint32_t)(n * 4096));
                 }
                 __syncwarp();
                 if (mine)
                     tma2_load_3d(sb + (uint32_t)(G::kVOff + sl * G::kVSlot + page * G::kVPage + t * 4096), &tm_v, 0,
                                  id * kBlock, 4 * t + 2 * (int)rank, full);
                 if (!fix) continue;
-                if (!wait_warp(full, (uint32_t)(fixes++ & 1), misc)) {
+                // (they are this warp's copies alone, which land whatever the other roles do)
+                if (!__all_sync(kFull, mbar_wait_bounded(full, (uint32_t)(fixes++ & 1), kWaitLimit))) {
+                    if (lane == 0) give_up(misc);
                     ok = false;
                     break;
                 }
@@ -451,8 +463,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     bad[k] = __reduce_or_sync(kFull, bad[k]);
                     if (lane < 2) {
                         const uint32_t at = sb + (uint32_t)(G::kBadOff + (((buf * 2 + (int)rank) * 2 + h) * 4 + k) * 4);
-                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)lane)), "r"(bad[k])
-                                     : "memory");
+                        store_remote(map_rank(at, (uint32_t)lane), bad[k]);
                     }
                 }
                 fence_cluster();
@@ -460,10 +471,7 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (lane == 0) arrive_remote(ready);
             }
         }
-        if (!ok) {
-            const long long t0 = clock64();
-            while (clock64() - t0 < 400000) __nanosleep(1000);
-        }
+        if (lane == 0) issued(1 + G::kG1 + h, g);
         __syncwarp();
     } else if (warp == G::kMmaWarp) {
         // ---------------------------------------------------------------- scores
@@ -821,7 +829,21 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     umma::fence_before_sync();
     __syncthreads();
-    cluster_sync();                      // nothing of the pair is under way in either's memory
+    cluster_sync();
+    // nothing is under way in either CTA's memory when the pair ends: the copies of a pair that ran
+    // to its end were all waited for by the MMA warps, and count on the first CTA's barriers
+    if (misc[M_ABORT]) {                 // (give_up: both CTAs')
+        if (rank == 0 && warp == G::kKWarp && lane == 0) {
+            const volatile int* n = misc + M_ISSUED;
+            land<1>(n, 2, [&](int) { return bar(G::B_QFULL); });
+            for (int k = 0; k < G::kG1; ++k)
+                land<G::kSlots>(n + 2 * (1 + k), 2, [&](int g) { return bar(G::B_KFULL + slot(g) * G::kG1 + k); });
+            for (int h = 0; h < 2; ++h)
+                land<G::kSlots>(n + 2 * (1 + G::kG1 + h), 2, [&](int g) { return bar(G::B_VREADY + slot(g) * 2 + h); });
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == G::kMmaWarp) {
         umma::fence_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols) : "memory");

@@ -83,6 +83,7 @@ struct SmallGeo {
     static constexpr int kEnd = kFacOff + kRows * 4;
     static constexpr int kSmem = kEnd;
     static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(kPages + 1 <= kCopiers, "misc words");
     // tensor memory: two buffers of S, then O^T
     static constexpr uint32_t kColO = 128, kTmemCols = kColO + kTiles * kRows <= 256 ? 256 : 512;
 };
@@ -174,7 +175,7 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
     if (warp >= G::kCopyWarp && warp < G::kCopyWarp + kPages) {
         // --------------------- Q, and the pages: a warp for each of a group's
         const int page = warp - G::kCopyWarp;
-        int g = 0;
+        int g = 0, queries = 0;
         bool ok = true;
         for (Walk<kPages> w(p, misc); ok && w.more(); w.next(p)) {
             if (page == 0) {
@@ -188,6 +189,7 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
                         tma_load_3d(sb + (uint32_t)(G::kQOff + k * kRows * 128), &tm_q, 0, row, k, bar(G::B_QFULL));
                     tma_load_2d(sb + (uint32_t)(G::kQOff + G::kCols * kRows * 128), &tm_qr, LAT, row, bar(G::B_QFULL));
                 }
+                ++queries;
                 __syncwarp();
             }
             const int32_t* row = p.bt + (size_t)w.s * p.max_blocks + w.j;
@@ -222,11 +224,9 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
                 }
             }
         }
-        // every copy lands before the CTA can end: those of a CTA that ran to its end were all
-        // waited for by the MMA warps; one that gave up leaves them time
-        if (!ok) {
-            const long long t0 = clock64();
-            while (clock64() - t0 < 400000) __nanosleep(1000);
+        if (lane == 0) {
+            misc[M_ISSUED + page] = g;
+            if (page == 0) misc[M_ISSUED + kPages] = queries;
         }
         __syncwarp();
     } else if (warp == G::kMmaWarp) {
@@ -595,6 +595,12 @@ paged_latent_small_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
     }
     umma::fence_before_sync();
     __syncthreads();
+    // every copy lands before the CTA can end: those of a CTA that ran to its end were all
+    // waited for by the MMA warps
+    if (misc[M_ABORT] && warp == G::kCopyWarp && lane == 0) {
+        land<G::kSlots>(misc + M_ISSUED, kPages, [&](int g) { return bar(G::B_FULL + slot(g)); });
+        land<1>(misc + M_ISSUED + kPages, 1, [&](int) { return bar(G::B_QFULL); });
+    }
     if (warp == G::kMmaWarp) {
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, G::kTmemCols);
