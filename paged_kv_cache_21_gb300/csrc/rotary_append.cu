@@ -58,7 +58,7 @@ struct RotaryParams {
 template <bool FP8, bool INTER>
 __global__ void __launch_bounds__(kThreads, kCtas) kv_append_rotary_kernel(const __grid_constant__ RotaryParams p)
 {
-    __shared__ float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];
+    __shared__ __align__(16) float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];     // (rotary_take: by fours)
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * kWarps + warp;
@@ -156,7 +156,7 @@ constexpr int kLatentMax = 1024;         // elements of a latent vector
 template <bool INTER>
 __global__ void __launch_bounds__(kThreads, kLatentCtas) kv_latent_append_kernel(const __grid_constant__ LatentAppendParams p)
 {
-    __shared__ float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];
+    __shared__ __align__(16) float s_cos[kWarps][kMaxDim / 2], s_sin[kWarps][kMaxDim / 2];     // (rotary_take: by fours)
     pdl_wait();
     const int units = p.R / kRotaryUnit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* cs = s_cos[warp];
