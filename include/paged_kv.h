@@ -736,8 +736,9 @@ int kv_rotary_frequencies(float* inv_freq, float* magnitude, int rotary_dim, dou
  * and slot_mapping, caches, kv_dtype and scales as kv_append; a token without a
  * slot (slot < 0) has its query turned and appends nothing.  Rotation in float32,
  * rounded once: to bfloat16, or K / k_scale to E4M3 (without a bfloat16 between).
- * head_dim and rotary_dim multiples of 16, up to 512 and 256; strides multiples of 8,
- * at least a row.  One launch. */
+ * head_dim and rotary_dim multiples of 16, up to 512 and 256, a token's heads of q and of
+ * k below 2^29 elements (KV_ERR_UNSUPPORTED); strides multiples of 8, at least a row.  One
+ * launch. */
 int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                      void* k_cache, void* v_cache, const int64_t* slot_mapping,
@@ -773,8 +774,9 @@ int kv_append_rotary(void* q_out, int64_t q_out_stride, const void* q, int64_t q
  *                  num_q_heads == 0: none (NULL)
  * and slot_mapping, positions, inv_freq [rope_dim / 2], flags and magnitude as
  * kv_append_rotary (the whole of rope_dim is turned).  Every element is rounded
- * once.  latent_dim a multiple of 8 up to 1024, rope_dim of 16 up to 256; strides
- * multiples of 8, at least a vector (a token's at least its heads'). */
+ * once.  latent_dim a multiple of 8 up to 1024, rope_dim of 16 up to 256, num_q_heads *
+ * rope_dim below 2^29 (KV_ERR_UNSUPPORTED); strides multiples of 8, at least a vector (a
+ * token's at least its heads'). */
 int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
                      const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,
                      const void* latent, int64_t latent_stride, const void* k_rope,

@@ -386,6 +386,7 @@ extern "C" int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t
         return KV_ERR_INVALID_ARG;
     if (latent_dim % 8 || latent_dim > kLatentMax || rope_dim % kRotaryUnit || rope_dim > kMaxDim)
         return KV_ERR_UNSUPPORTED;
+    if ((int64_t)num_q_heads * rope_dim > INT32_MAX / 4) return KV_ERR_UNSUPPORTED;
     if (norm_weight && !(eps >= 0.f && std::isfinite(eps))) return KV_ERR_INVALID_ARG;
     if (num_tokens == 0) return KV_OK;
     if (!latent || !k_rope || !cache || !slot_mapping || !positions || !inv_freq) return KV_ERR_INVALID_ARG;
@@ -426,7 +427,7 @@ extern "C" int kv_latent_append(void* q_out, int64_t q_out_token_stride, int64_t
     p.eps = eps;
     p.magnitude = magnitude;
     const int units = rope_dim / kRotaryUnit;
-    p.row_blocks = (num_tokens + kWarps - 1) / kWarps;
+    p.row_blocks = (num_tokens - 1) / kWarps + 1;
     p.share = num_q_heads > 0 ? warps_of_token(num_tokens, num_q_heads, 32 / units, kLatentCtas) : 0;
     const long long blocks = p.row_blocks + ((long long)num_tokens * p.share + kWarps - 1) / kWarps;
     return launch(flags & KV_ROTARY_INTERLEAVED ? kv_latent_append_kernel<true> : kv_latent_append_kernel<false>, blocks,

@@ -179,3 +179,11 @@ def test_caches_without_values(pk):
     one = (ctypes.c_void_p * 2)(4096, 4096)
     assert pk._lib.kv_tree_compact(one, None, 2, A, 4, A, A, A, A, 2, 4, 1, 576, 9, 0, None) == -1
     assert pk._lib.kv_tree_compact(None, None, 2, A, 4, A, A, A, A, 2, 4, 1, 576, 9, 0, None) == -1
+
+
+@pytest.mark.parametrize("bad", [
+    dict(h=2 ** 26, r=64, qh=64, oh=64, qt=2 ** 32, ot=2 ** 32),
+    dict(h=2 ** 31 - 1, r=16, qh=16, oh=16, qt=2 ** 36, ot=2 ** 36)])
+def test_latent_append_refuses_heads_that_its_indexes_do_not_hold(pk, bad):
+    """As kv_append_rotary does: 2^29 elements of a token's heads and more."""
+    assert lappend(pk, **bad) == pk.KV_ERR_UNSUPPORTED
