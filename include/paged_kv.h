@@ -695,8 +695,9 @@ int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers
  * and the elements behind rotary_dim stay as they are.  Pair i is elements i and
  * i + rotary_dim / 2, or, with KV_ROTARY_INTERLEAVED, 2 i and 2 i + 1.  (The pages
  * say that positions are part of the cached key, not how; these entry points are
- * interfaces of this implementation.)  The angle is reduced by whole turns
- * exactly, in integers: a position of p loses p 2^-64 turns.  inv_freq below 2^48. */
+ * interfaces of this implementation.)  The angle is reduced by whole turns in
+ * integers: a position of p loses less than p 2^-63 turns, and the fraction that is
+ * left is cut to 2^-32.  inv_freq between -2^48 and 2^48, neither included. */
 #define KV_ROTARY_INTERLEAVED 1u
 
 /* How kv_rotary_frequencies scales the frequencies f_i = theta^(-2 i / rotary_dim)

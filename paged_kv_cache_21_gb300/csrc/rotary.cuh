@@ -5,7 +5,8 @@
 // a million the angle itself, in binary32, would be off by 0.03 radians; only its
 // fraction of a turn matters, so that the frequency is held as a 64-bit fraction of a
 // turn a position (2^64 = one turn) and the product with the position wraps: exact but
-// for the frequency's rounding, 2^-64 of a turn a position.
+// for the frequency's rounding, less than 2^-63 of a turn a position.  Of the fraction,
+// 32 bits go on to binary32's sine and cosine.
 #pragma once
 
 #include <cstdint>
@@ -19,18 +20,19 @@ namespace pkv {
 constexpr int kRotaryUnit = 16;          // elements, eight pairs, that a thread turns together
 
 // Turns a position, of 2^64, for a frequency in radians: m 2^e of the float times
-// 2^88 / (2 pi), a constant of 86 bits, in integers (FP64 runs at 1/64 of FP32's rate here:
-// in doubles the angles of 8192 tokens took 24 us of the kernel's 57).  Frequencies of 2^48
+// 2^88 / (2 pi), with 32 bits behind the point, in integers (FP64 runs at 1/64 of FP32's rate
+// here: in doubles the angles of 8192 tokens took 24 us of the kernel's 57).  Frequencies of 2^48
 // and above, and what is not a number, count as zero.
 __device__ __forceinline__ uint64_t rotary_step(float inv_freq)
 {
-    constexpr uint64_t kHi = 0x28be60ull, kLo = 0xdb9391054a7f09d5ull;       // 2^88 / (2 pi)
+    constexpr uint64_t kHi = 0x28be60ull, kLo = 0xdb9391054a7f09d5ull, kBehind = 0xf47d4d37ull;
     const uint32_t bits = __float_as_uint(inv_freq), ex = (bits >> 23) & 255u;
     const uint64_t m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
     const int shift = 174 - (int)(ex ? ex : 1u);         // 24 - e, e = ex - 150
-    if (shift <= 0 || shift >= 128) return 0ull;
-    const uint64_t lo = m * kLo, hi = m * kHi + __umul64hi(m, kLo);
-    const uint64_t step = shift >= 64 ? hi >> (shift - 64) : (hi << (64 - shift)) | (lo >> shift);
+    if (shift < 0 || shift >= 128) return 0ull;
+    const uint64_t low = m * kLo, lo = low + (m * kBehind >> 32);
+    const uint64_t hi = m * kHi + __umul64hi(m, kLo) + (lo < low ? 1u : 0u);
+    const uint64_t step = shift >= 64 ? hi >> (shift - 64) : shift == 0 ? lo : (hi << (64 - shift)) | (lo >> shift);
     return bits >> 31 ? 0ull - step : step;
 }
 
