@@ -286,7 +286,8 @@ int kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
  * outside [0, num_blocks) are skipped and flag KV_DEVERR_BLOCK_OUT_OF_RANGE.
  * A dst that is also some src in the same call gives an unspecified result.
  * v_cache may be NULL for a cache without a V of its own (a latent cache:
- * num_kv_heads 1, head_dim its row's elements). */
+ * num_kv_heads 1, head_dim its row's elements); with more heads NULL is
+ * KV_ERR_INVALID_ARG. */
 int kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int32_t* dst, int n,
                    int num_kv_heads, int head_dim, int num_blocks, int kv_dtype, void* stream);
 
@@ -668,7 +669,8 @@ int kv_tree_verify(int32_t* accept_lens, int32_t* accept_nodes, int32_t* out_tok
  *                  the layers, all of the same shape, dtype and block tables, no
  *                  two of them overlapping (else KV_ERR_INVALID_ARG); v_caches may
  *                  be NULL for caches without a V of their own (latent caches:
- *                  num_kv_heads 1, head_dim their row's elements)
+ *                  num_kv_heads 1, head_dim their row's elements; with more heads
+ *                  NULL is KV_ERR_INVALID_ARG)
  *   accept_nodes:  [num_seqs][max_nodes] int32, strictly increasing over its first
  *                  accept_lens[s] entries, each less than n_s (as kv_tree_verify
  *                  leaves it); accept_lens: [num_seqs] int32

@@ -140,7 +140,7 @@ extern "C" int kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src,
     if (n < 0 || num_kv_heads <= 0 || num_blocks <= 0 || head_dim <= 0) return KV_ERR_INVALID_ARG;
     if (kv_dtype != KV_DTYPE_BF16 && kv_dtype != KV_DTYPE_FP8_E4M3) return KV_ERR_UNSUPPORTED;
     if (n == 0) return KV_OK;
-    if (!k_cache || !src || !dst) return KV_ERR_INVALID_ARG;
+    if (!k_cache || !src || !dst || (!v_cache && num_kv_heads != 1)) return KV_ERR_INVALID_ARG;
     if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15) return KV_ERR_INVALID_ARG;
     const long long block_bytes =
         (long long)num_kv_heads * kBlock * head_dim * (kv_dtype == KV_DTYPE_BF16 ? 2 : 1);

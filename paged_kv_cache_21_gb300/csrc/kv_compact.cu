@@ -171,7 +171,7 @@ extern "C" int kv_tree_compact(void* const* k_caches, void* const* v_caches, int
     const long long row_bytes = (long long)head_dim * (kv_dtype == KV_DTYPE_BF16 ? 2 : 1);
     if (row_bytes % 16 != 0) return KV_ERR_UNSUPPORTED;
     if (num_layers == 0 || num_seqs == 0) return KV_OK;
-    if (!k_caches || !block_tables || !context_lens || !node_starts ||
+    if (!k_caches || (!v_caches && num_kv_heads != 1) || !block_tables || !context_lens || !node_starts ||
         !accept_nodes || !accept_lens)
         return KV_ERR_INVALID_ARG;
     for (int l = 0; l < num_layers; ++l)

@@ -181,6 +181,16 @@ def test_caches_without_values(pk):
     assert pk._lib.kv_tree_compact(None, None, 2, A, 4, A, A, A, A, 2, 4, 1, 576, 9, 0, None) == -1
 
 
+@pytest.mark.parametrize("heads", [2, 8])
+def test_a_missing_v_of_caches_with_several_heads_is_refused(pk, heads):
+    """Only a latent cache, of one head, has no V: another's pointer was lost on the way."""
+    assert pk._lib.kv_copy_blocks(A, None, A, A, 2, heads, 64, 9, 0, None) == pk.KV_ERR_INVALID_ARG
+    assert pk._lib.kv_copy_blocks(A, None, A, A, 0, heads, 64, 9, 0, None) == pk.KV_OK
+    two = (ctypes.c_void_p * 2)(4096, 1 << 30)
+    assert pk._lib.kv_tree_compact(two, None, 2, A, 4, A, A, A, A, 2, 4, heads, 64, 9, 0,
+                                   None) == pk.KV_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("bad", [
     dict(h=2 ** 26, r=64, qh=64, oh=64, qt=2 ** 32, ot=2 ** 32),
     dict(h=2 ** 31 - 1, r=16, qh=16, oh=16, qt=2 ** 36, ot=2 ** 36)])
