@@ -57,3 +57,192 @@ def test_frequencies_up_to_the_end_of_their_range(pk):  # noqa: F811
     lost = positions.abs().double()[:, None, None] * 2.0 ** -63 * 2 * np.pi
     check(out, want, R.HALF_BF16 * want.abs() + R.turn_error(torch.ones_like(want)) + lost, "turns")
     assert pk.get_device_error()[0] == 0
+
+
+# ------------------------------------------------------- what must not be multiplied
+
+# both kernels (up to 64 rows a sequence, and more), both depths of their rings, contexts of one part
+# and of many, nodes within a page and over the border of the pages that are weighed together
+SEEN = [
+    ([100, 0, 259, 31], [6, 5, 3, 1], 8, 512, 64), ([100, 0, 259, 31], [6, 5, 3, 1], 8, 256, 32),
+    ([100, 0, 259, 31], [6, 5, 3, 1], 48, 256, 64), ([44, 90], [60, 9], 1, 512, 64),
+    ([40, 90], [60, 9], 1, 256, 32), ([4000, 700], [41, 3], 1, 512, 32), ([4030, 9000], [40, 2], 1, 256, 64),
+    ([6100, 700], [20, 3], 3, 512, 64), ([4000, 700], [60, 3], 4, 512, 64), ([5000, 700], [128, 3], 1, 256, 32),
+    ([4100, 9000], [37, 2], 6, 256, 64), ([7990], [3], 100, 512, 64)]
+
+
+def ancestors(par):
+    seen = []
+    for i in range(len(par)):
+        a, mine = i, set()
+        while a >= 0 and par[a] != -2:
+            mine.add(a)
+            a = int(par[a])
+        seen.append(mine if par[i] != -2 else set())
+    return seen
+
+
+def row_of(c, s, pos):
+    return int(c.bt[s, pos // 16]) * 16 + pos % 16
+
+
+@pytest.mark.parametrize("bases,counts,H,L,rope", SEEN)
+def test_what_a_node_does_not_see_does_not_reach_it(pk, bases, counts, H, L, rope):  # noqa: F811
+    c = Case(bases, counts, H, L, rope, "tree", seed=H + L)
+    clean = c.run(pk).cpu()
+    c.check(clean)
+    flat = c.cache.flatten(0, 1)
+    for s, n in enumerate(c.lens):                       # the rest of each last page
+        for pos in range(int(n), -(-int(n) // 16) * 16):
+            flat[row_of(c, s, pos)] = float("nan") if pos % 2 else float("-inf")
+    assert torch.equal(c.run(pk).cpu(), clean)
+    # NaN and infinities in two drafted rows of the first sequence, one of them in the part that is turned
+    n, base = int(counts[0]), int(bases[0])
+    seen = ancestors(c.parents[:n])
+    one, other = 1, n - 1 - n // 4
+    keep = flat.clone()
+    flat[row_of(c, 0, base + one), L - 9] = float("nan")
+    flat[row_of(c, 0, base + other), L + 3] = float("inf")
+    got = c.run(pk).cpu()
+    hit = [one in seen[i] or other in seen[i] for i in range(n)]
+    assert any(hit) and not all(hit)
+    # (a NaN among a row's scores, or an infinite one, makes all of it NaN; -inf is a weight of zero)
+    nan = torch.zeros((n, H), dtype=torch.bool)
+    for i in range(n):
+        nan[i] = one in seen[i]
+        if other in seen[i]:
+            nan[i] |= c.q[i, :, L + 3] > 0
+        if not hit[i]:
+            assert torch.equal(got[i], clean[i]), i
+    assert torch.equal(torch.isnan(got[:n]), nan[..., None].expand(n, H, L))
+    assert torch.equal(got[n:], clean[n:])
+    # infinities whose scores are -inf: weight zero, but the elements themselves are NaN
+    flat.copy_(keep)
+    for node, col in ((one, 5), (other, L - 70)):
+        flat[row_of(c, 0, base + node)] = 0.0
+        flat[row_of(c, 0, base + node), col] = float("inf")
+        c.q[:, :, col] = -1.0
+    got = c.run(pk).cpu()
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    for i in range(n):
+        nan[i, :, 5] |= one in seen[i]
+        nan[i, :, L - 70] |= other in seen[i]
+    assert torch.equal(torch.isnan(got), nan)
+    # the rest is as with scores that are far below the others
+    for node in (one, other):
+        flat[row_of(c, 0, base + node)] = 0.0
+        flat[row_of(c, 0, base + node), (5 if node == one else L - 70)] = 1e30
+    want, bound = R.attention(c.q, c.cache, c.bt, c.lens, c.starts, c.parents, c.scale, L)
+    fine = ~nan & torch.isfinite(bound) & (bound < 1e20)
+    assert fine[n:].all() and fine[~torch.tensor(hit + [False] * (len(got) - n))].all()
+    over = (got.double() - want).abs() - bound
+    assert (over[fine] <= 0).all()
+    assert pk.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("H,L,rope", [(6, 512, 64), (9, 256, 32), (33, 512, 64), (40, 256, 64)])
+def test_padding_nodes_rows_reach_nobody(pk, H, L, rope):  # noqa: F811
+    c = Case([77, 2100, 10], [6, 7, 5], H, L, rope, "pads", seed=H)
+    c.parents[2], c.parents[6 + 3], c.parents[6 + 4] = -2, -2, 3
+    clean = c.run(pk).cpu()
+    c.check(clean)
+    flat = c.cache.flatten(0, 1)
+    for t in np.nonzero(c.parents == -2)[0]:
+        s = int(np.searchsorted(c.starts, t, side="right")) - 1
+        flat[row_of(c, s, int(c.lens[s]) - int(c.starts[s + 1]) + int(t))] = float("nan")
+        assert (clean[t] == 0).all()
+    assert torch.equal(c.run(pk).cpu(), clean)
+    assert pk.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("H,L,rope", [(16, 512, 64), (16, 256, 32), (128, 512, 64), (128, 256, 64)])
+def test_nothing_of_the_call_before_is_left_in_shared_memory(pk, H, L, rope):  # noqa: F811
+    """A call over NaN alone, then contexts of a few tokens, whose pages fill a part of the places."""
+    bad = Case([3000] * 30, None, H, L, rope, seed=1, spread=float("nan"))
+    c = Case([0, 3, 15, 16, 40, 63, 70, 130, 200], None, H, L, rope, seed=2)
+    c.check(c.run(pk))
+    want = c.run(pk).cpu()
+    assert torch.isnan(bad.run(pk)).all()
+    assert torch.equal(c.run(pk).cpu(), want)
+    assert pk.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("H", [8, 100])
+def test_contexts_shorter_than_their_nodes(pk, H):  # noqa: F811
+    """As many of the first nodes as there is room for count; the flag tells of it."""
+    c = Case([5, 40], [6, 3], H, 256, 64, seed=H)
+    c.lens[0] = 4
+    got = c.run(pk).cpu().double()
+    assert pk.get_device_error() == (pk.DEVERR_BAD_TREE, 4)
+    rows = c.cache.flatten(0, 1)[[row_of(c, 0, pos) for pos in range(4)]].double()
+    for i in range(6):
+        sees = rows[:i + 1]
+        x = c.q[i].double() @ sees.T * c.scale
+        want = torch.softmax(x, dim=1) @ sees[:, :256]
+        size = torch.softmax(x, dim=1) @ sees[:, :256].abs()
+        off = (c.scale * (c.q[i].double().abs() @ sees.abs().T)).amax(dim=1, keepdim=True)
+        # (latent_reference.attention's bound)
+        bound = 2 * R.HALF_BF16 * want.abs() + (R.HALF_BF16 + 72 * 2.0 ** -23 * off + 2.0 ** -19) * size
+        assert ((got[i] - want).abs() <= bound * 1.01).all(), i
+
+
+# ------------------------------------------------------------------------ captured steps
+
+def test_a_captured_step_of_appends_and_attention(pk):  # noqa: F811
+    """Two layers' latent append and attention, and a rotary append, in one graph; replayed with other
+    tokens, positions, slots and lengths in the same tensors, against the same calls made one by one."""
+    B, H, L, rope, NB = 3, 16, 512, 64, 60
+    W = L + rope
+    gen = torch.Generator().manual_seed(4)
+    freq = torch.from_numpy(pk.rotary_frequencies(rope)[0]).cuda()
+    weight = (1 + 0.2 * randn(gen, L)).to(BF).cuda()
+    start = [randn(gen, NB, 16, W).to(BF).cuda() for _ in range(2)]
+    kv0 = randn(gen, NB, 2, 16, rope).to(BF).cuda()
+    bt = torch.randperm(NB, generator=gen)[:B * 20].reshape(B, 20).int().cuda()
+    down, qr = torch.empty((2, B, W), dtype=BF, device="cuda"), torch.empty((2, B, H, rope), dtype=BF, device="cuda")
+    q, out = torch.empty((2, B, H, W), dtype=BF, device="cuda"), torch.empty((2, B, H, L), dtype=BF, device="cuda")
+    k = torch.empty((B, 2, rope), dtype=BF, device="cuda")
+    qk, qo = torch.empty((B, 4, rope), dtype=BF, device="cuda"), torch.empty((B, 4, rope), dtype=BF, device="cuda")
+    slots, positions = (torch.empty(B, dtype=torch.int64, device="cuda") for _ in range(2))
+    lens = torch.empty(B, dtype=torch.int32, device="cuda")
+    ws = pk.alloc_latent_workspace(B, 1, H, L, rope)
+    caches, kc, vc = [t.clone() for t in start], kv0.clone(), kv0.clone()
+
+    def step():
+        pk.kv_append_rotary(qo, qk, k, k, kc, vc, slots, positions, freq)
+        for x in range(2):
+            pk.kv_latent_append(q[x][..., L:], qr[x], down[x][:, :L], down[x][:, L:], caches[x], slots, positions,
+                                freq, norm_weight=weight)
+            pk.paged_latent_attention(out[x], q[x], caches[x], bt, lens, 0.1, ws)
+
+    def fill(seed, pos):
+        g = torch.Generator().manual_seed(seed)
+        for t in (down, qr, q, k, qk):
+            t.copy_(randn(g, *t.shape).to(BF))
+        p = torch.tensor(pos)
+        positions.copy_(p)
+        lens.copy_(p.int() + 1)
+        slots.copy_(bt.cpu()[torch.arange(B), p // 16].long() * 16 + p % 16)
+
+    fill(0, [5, 250, 100])
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    results = []
+    for captured in (True, False):
+        for t, t0 in zip(caches + [kc, vc], start + [kv0, kv0]):
+            t.copy_(t0)
+        for i, pos in enumerate(([6, 251, 101], [7, 31, 318], [0, 15, 16])):
+            fill(10 + i, pos)
+            torch.cuda.synchronize()
+            graph.replay() if captured else step()
+            torch.cuda.synchronize()
+            results.append([t.cpu().clone() for t in (out, q, qo, kc, vc, *caches)])
+    for a, b in zip(results[:3], results[3:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    want, bound = R.attention(results[2][1][1], results[2][6], bt.cpu().numpy(), lens.cpu().numpy(),
+                              np.arange(B + 1), None, 0.1, L)
+    check(results[2][0][1], want, bound, "attention")
+    assert pk.get_device_error()[0] == 0
