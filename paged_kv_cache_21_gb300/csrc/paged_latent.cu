@@ -576,6 +576,10 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             g += nc;
         }
+        // (the commits arrive in both CTAs, and the MMA threads see those of the first: the second's
+        // are waited for here, off the path of the pair's end)
+        if (rank == 1 && lane < 2) mbar_wait_bounded(bar(G::B_END + lane), 0u, kWaitLimit);
+        __syncwarp();
     } else if (warp < G::kWeighWarps) {
         // --------------------------------------------------- weights and output
         const int wq = warp & 3, wg = warp >> 2;
@@ -829,9 +833,6 @@ paged_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     umma::fence_before_sync();
     __syncthreads();
-    // the commits arrive in both CTAs, and the MMA threads have seen those of the first
-    if (rank == 1 && warp == G::kMmaWarp && lane < 2) mbar_wait_bounded(bar(G::B_END + lane), 0u, kWaitLimit);
-    __syncwarp();
     cluster_sync();
     // nothing is under way in either CTA's memory when the pair ends: the copies of a pair that ran
     // to its end were all waited for by the MMA warps, and count on the first CTA's barriers
