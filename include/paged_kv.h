@@ -75,7 +75,7 @@ extern "C" {
 #define KV_BLOCK_SIZE 16
 
 /* Device error flags reported by kv_get_device_error(). */
-#define KV_DEVERR_SLOT_OUT_OF_RANGE 1     /* kv_append: slot >= num_blocks*16 */
+#define KV_DEVERR_SLOT_OUT_OF_RANGE 1     /* the appends: slot >= num_blocks*16 */
 #define KV_DEVERR_BLOCK_OUT_OF_RANGE 2    /* a block-table entry outside [0, num_blocks) */
 #define KV_DEVERR_CONTEXT_TOO_LONG 4      /* context_lens[s] > 16*max_blocks_per_seq, or < 0 */
 #define KV_DEVERR_PIPELINE_TIMEOUT 8      /* a bulk copy never arrived (a bug, never expected) */
@@ -708,8 +708,9 @@ int kv_tree_compact(void* const* k_caches, void* const* v_caches, int num_layers
 #define KV_ROTARY_LINEAR 1   /* f_i / factor */
 #define KV_ROTARY_BASE 2     /* theta * factor^(rotary_dim / (rotary_dim - 2)) for theta */
 #define KV_ROTARY_PARTS 3    /* by parts, over pairs: f_i up to the pair that makes `high` turns
-                                over original_len (rounded down), f_i / factor from the one that
-                                makes `low` turns (rounded up), a linear blend between; the
+                                over original_len (rounded down, pair 0 at least), f_i / factor
+                                from the one that makes `low` turns (rounded up, rotary_dim - 1 at
+                                most, and behind the former), a linear blend between; the
                                 magnitude is 0.1 ln(factor) + 1 */
 #define KV_ROTARY_BANDS 4    /* by bands, over turns: with n_i = original_len f_i / 2 pi turns,
                                 f_i for n_i >= high, f_i / factor for n_i <= low, a blend

@@ -21,21 +21,28 @@
 // What bounds it (L = 512, R = 64).  A chunk's 147 KB take HBM 1.68 us to two SMs (6.7
 // TB/s, 152 SMs), ~3300 clocks.  A chunk's 36 products of N 128 and 16 of N 256 with their
 // commits take ~3010 clocks (measured; one of N 128 takes 53, 45 at least whatever its N,
-// one of N 256 65).  In the loop a chunk takes ~3500: 94 % of HBM's rate.  32 x 8192 tokens,
-// 128 heads: 79 us, of which ~50 are HBM's at its rate, ~6 until the first keys are there
-// (tables, the cut, block ids and a first copy, each behind the one before), ~5 the last
-// chunk's products and its 131 KB of partial results a CTA, ~8 the merge.  Four tokens x 128
-// heads over 32 x 2048: 87 us, tensor cores and the ends of 2.7 tiles a pair.  1024 x 256, 128
-// heads: 187 (HBM 88), the sequences' ends.
+// one of N 256 65).  In the loop a chunk takes ~3500: 94 % of HBM's rate.
+//
+// Where a call's time goes, by stamps of the pairs (means, us; one call by itself, caches cold;
+// back to back 78.4, 88.3 and 187):
+//                                        32 x 8192    32 x 2048 x 4 tokens    1024 x 256
+//   to the first scores (of it the cut)   9.4 (1.6)         10.9 (1.9)         15.6 (4.6)
+//   the loop, over all tiles              39.3 x 1.36       19.0 x 2.42        3.1 x 13.8
+//   a tile's last weights to its products  1.0 x 1.36        1.4 x 2.42        3.5 x 13.8
+//   its result written                     2.5 x 1.36        2.9 x 2.42        3.3 x 13.8
+//   to the next tile's first weights       0.9 x 0.36        0.7 x 1.42        1.0 x 12.8
+//   pairs end apart (mean to last)         4.6               4.7                7.5
+//   to the merge, the merge                2.0, 7.2          2.0, 10.8          2.5, 5.9
+// (128 heads; the pairs' tiles with ranges that the cut has shortened.)
 //
 // How:
 //  * Each byte of the cache is copied twice, as K to one CTA and as V to either, and shared
 //    memory has room for one chunk: a group of K's columns is copied again as soon as its
 //    products are done, by a warp of its own (one warp for all groups and one for V: 92.6
 //    us for the four tokens; so 88.4).  To have the second copy, and the first, find
-//    their bytes in L2, a warp prefetches pages a chunk ahead, line by line (82.8 -> 78.6 us
-//    against two chunks ahead, 84.7 without; by bulk copies to L2, which wait behind the
-//    others in the copy unit: 95).
+//    their bytes in L2, a warp prefetches pages a chunk ahead, line by line (kAheadChunks;
+//    by bulk copies to L2, which wait behind the others in the copy unit: 95 us for 84.7
+//    without).
 //  * Warps: eight weigh (two threads and two halves of O's columns a row), three copy K (the
 //    first also Q), two V, two issue the MMAs of both CTAs (scores; products), one prefetches.
 //  * The warps that copy V clear what must not be multiplied (0 * inf): rows behind the
@@ -75,13 +82,14 @@ namespace {
 constexpr int kPages = 8;                       // pages of a chunk
 constexpr int kRows = 64;                       // rows of a CTA
 constexpr int kTile = 2 * kRows;                // rows of a pair
-// Chunks that are brought to L2 ahead of their copies.  (32 x 8192 tokens, 128 heads: 78.6 us
-// with 1, 80.9 with 2, 84.2 with 3, 84.7 without.)
+// Chunks that are brought to L2 ahead of their copies.  (32 x 8192 tokens, 128 heads: 79.3 us
+// with 1, 82.0 with 2, 84.8 with 3, 84.5 without; ragged 64 contexts 63.4, 64.7, 66.5, 66.3; 32 x 2048 x
+// 4 tokens, where tensor cores bound it, 87.9, 89.1, 90.5, 86.7.)
 constexpr int kAheadChunks = 1;
 constexpr int kMinPages = 16;                   // least range of a pair of CTAs
-// What a (sequence, tile) costs beside its pages: its queries, pipeline and results.  (Ragged 64
-// contexts: 65.6 us with 24, 64.1 with 32, 65.5 with 40; 81 with 16, 104 with 8 before the
-// results were written together.)
+// What a (sequence, tile) costs beside its pages: its queries, pipeline and results.  (With 24, 32,
+// 40: ragged 64 contexts 64.3, 63.4, 64.1 us; 32 x 8192 79.6, 79.3, 80.1; 32 x 2048 x 4 tokens 88.1,
+// 87.9, 88.0.)
 constexpr int kExtraPages = 32;
 template <int LAT>
 struct Geo {

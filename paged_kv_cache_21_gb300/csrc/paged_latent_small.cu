@@ -12,8 +12,8 @@
 // to 58 beside the others) and 16 of M 128, N 64 (49), ~2400 at least.  In the loop a group
 // takes ~3650: 90 % of HBM's rate.  32 x 8192 tokens, 16 heads: 66 us (HBM 45; ~6 until the
 // first keys are there, ~5 for the ends and the merge); 4 x 131072, 64 rows: 125 (91); one
-// context of 128 tokens: 11, a chain of short steps.  paged_latent.cu's kernel copies every
-// byte twice: 78 and 147 us for the first two then, 71 and 139 with this one.
+// context of 128 tokens: 11.9, a chain of short steps.  paged_latent.cu's kernel, which copies
+// every byte twice, takes 72, 127 and 12.4 us for them.
 //
 // How (the rest as in paged_latent.cu):
 //  * Shared memory holds Q (74 KB), a ring of two groups (four at L = 256) and P (8 KB).
@@ -21,8 +21,8 @@
 //    group's rows are at one stride for the scores, and each page, at the same stride, is
 //    one step of the products.  A page is copied anew as soon as its products are done, by a
 //    warp of its own; with two groups only, the time from there to the next scores counts,
-//    so pages are prefetched to L2 shortly before (with a slower merge 69.1 us; 71.2 without,
-//    70.2 two groups ahead, 73 three).
+//    so pages are prefetched to L2 shortly before (32 x 8192, 16 heads: 65.3 us one group ahead,
+//    67.2 two, 69.3 three, 71.1 without).
 //  * An accumulator of M = 64 has row r in lane 32 (r / 16) + r % 16: each warp weighs 16
 //    rows, two threads a row with 32 tokens each.
 //  * What must not be multiplied in V is cleared where it lies after the group's scores are
@@ -43,9 +43,11 @@ namespace {
 constexpr int kPages = 4;                       // pages of a group
 constexpr int kRows = kLatentFew;
 constexpr int kAheadGroups = 1;                 // groups that are brought to L2 ahead of their copies (above)
-constexpr int kMinPages = 8;                    // least range of a CTA
-// What a sequence costs beside its pages.  (32 x 8192 tokens, with a slower merge: 69.0 us with 6, 69.2 with 12,
-// 70.4 with 20; 8 x 4096 at L = 256: 18.0, 16.6 to 17.0, 17.0.)
+// Least range of a CTA.  (With 4, 8, 16: 8 x 4096 at L = 256 16.9, 16.7, 16.4 us; one context of 128
+// tokens 10.9, 12.0, 11.9; 32 x 8192 65.4 with each.)
+constexpr int kMinPages = 8;
+// What a sequence costs beside its pages.  (32 x 8192 tokens, 16 heads: 65.5 us with 6, 65.3 with 12,
+// 66.9 with 20; 8 x 4096 at L = 256: 17.7, 16.7, 16.5.)
 constexpr int kExtraPages = 12;
 
 template <int LAT>

@@ -8,10 +8,12 @@
 // warps, which each work out the angles.  (A thread for each unit with eight angles of its
 // own, in doubles, took 57 us for 8192 tokens of 32 + 8 heads; 24 us of FP64.)
 //
-// HBM bounds the large calls and the launch the small ones.  8192 tokens, 32 q / 8 KV heads,
-// d128: 32.5 us, 6.2 TB/s of its 201 MB; 256 tokens to E4M3: 4.6 us on the device (8.7 a call:
-// the host); one token: 2.1 (8.3).  Latent rows of 512 + 64 and 16 heads, 8192 tokens: 9 us
-// on the device, 17 a call; 32 tokens, 128 heads: 2.2 and 14.
+// On the device (a captured run of calls over sets of buffers that together exceed L2) and a
+// call: 8192 tokens, 32 q / 8 KV heads, d128: 32.4 and 32.7 us, HBM, 6.2 TB/s of its 201 MB;
+// 256 tokens to E4M3: 5.0 and 8.4, the host; one token: 2.1 and 8.0.  Latent rows of 512 + 64
+// and 16 heads, 8192 tokens: 12.5 and 14.7 to 17.8, for 7.9 at HBM's rate: a token, or four of
+// its heads, a warp, each a chain of slot, loads, angles and stores with nothing loaded ahead;
+// 32 tokens, 128 heads: 2.5 and 12.5 to 13.5, the host.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -149,7 +151,7 @@ struct LatentAppendParams {
     float eps, magnitude;
 };
 
-constexpr int kLatentCtas = 8;           // of an SM: little work a warp, so many warps (5: 11.0 us on the device for 9.0)
+constexpr int kLatentCtas = 8;           // of an SM: little work a warp, so many warps (8192 tokens: 12.4 us, with 5 or 6 12.9)
 constexpr int kLatentAhead = 2;
 constexpr int kLatentMax = 1024;         // elements of a latent vector
 

@@ -197,3 +197,18 @@ def test_a_missing_v_of_caches_with_several_heads_is_refused(pk, heads):
 def test_latent_append_refuses_heads_that_its_indexes_do_not_hold(pk, bad):
     """As kv_append_rotary does: 2^29 elements of a token's heads and more."""
     assert lappend(pk, **bad) == pk.KV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("length", [3.0, 10.0, 64.0, 300.0, 1e6, 1e12])
+def test_frequencies_by_parts_of_any_length(pk, length):
+    """Where pairs that make so many turns are not among the pairs: the first of them is pair 0 at
+    least, the second is behind it."""
+    d, theta = 32, 10000.0
+    i = np.arange(d // 2)
+    plain = theta ** (-2.0 * i / d)
+    pair = lambda t: d * math.log(length / (t * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
+    lo, hi = max(math.floor(pair(32)), 0), min(math.ceil(pair(1)), d - 1)
+    slow = np.clip((i - lo) / (hi - lo), 0, 1) if hi > lo else (i > lo) * 1.0
+    want = plain * (1 - slow) + plain / 4 * slow
+    f = pk.rotary_frequencies(d, theta, "parts", 4.0, 1.0, 32.0, length)[0]
+    assert (np.abs(f - want) <= half_ulp(want) * (1 + 2.0 ** -20)).all()
