@@ -33,7 +33,7 @@
 //   to the next tile's first weights       0.9 x 0.36        0.7 x 1.42        1.0 x 12.8
 //   pairs end apart (mean to last)         4.6               4.7                7.5
 //   to the merge, the merge                2.0, 7.2          2.0, 10.8          2.5, 5.9
-// (128 heads; the pairs' tiles with ranges that the cut has shortened.)
+// (128 heads; a pair's range holds 1.36, 2.42 and 13.8 tiles or parts of them in the mean.)
 //
 // How:
 //  * Each byte of the cache is copied twice, as K to one CTA and as V to either, and shared

@@ -246,3 +246,40 @@ def test_a_captured_step_of_appends_and_attention(pk):  # noqa: F811
                               np.arange(B + 1), None, 0.1, L)
     check(results[2][0][1], want, bound, "attention")
     assert pk.get_device_error()[0] == 0
+
+
+def test_the_most_rows_of_a_sequence(pk):  # noqa: F811
+    c = Case([200, 5], [128, 1], 128, 512, 64, "tree", seed=1)
+    c.check(c.run(pk))
+    assert pk.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("B,H,ctx", [(1, 16, 1000003), (1, 128, 700001), (90, 128, 40001), (160, 8, 30007)])
+def test_long_contexts_whole_and_in_many_parts(pk, B, H, ctx):  # noqa: F811
+    """Weights nearly alike over values of one sign, where what sums lose adds up; one sequence in all
+    the device's parts, and more sequences than it has workers, most of them in one.  (64 bits on the
+    GPU, by plain operations; latent_reference.attention's bound.)"""
+    L, R_, W = 256, 32, 288
+    gen = torch.Generator(device="cuda").manual_seed(B + H)
+    pages = -(-ctx // 16)
+    cache = torch.rand((pages + 5, 16, W), generator=gen, device="cuda").to(BF)
+    # (every sequence has the same pages in another order: one copy of them is enough)
+    bt = torch.stack([torch.randperm(pages - 1, generator=gen, device="cuda") for _ in range(B)]).int()
+    bt = torch.cat([bt, torch.full((B, 1), pages - 1, dtype=torch.int32, device="cuda")], dim=1)
+    q = (torch.randn((B, H, W), generator=gen, device="cuda") * 0.1).to(BF)
+    lens = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
+    out = torch.empty((B, H, L), dtype=BF, device="cuda")
+    ws = pk.alloc_latent_workspace(B, 1, H, L, R_)
+    pk.paged_latent_attention(out, q, cache, bt, lens, 0.05, ws)
+    rows = cache[:pages].flatten(0, 1)[:ctx].double()
+    for b in (0, B - 1):
+        x = q[b].double() @ rows.T * 0.05
+        w = torch.softmax(x, dim=1)
+        want = w @ rows[:, :L]
+        off = 0.05 * (q[b].double().abs() @ rows.T).amax(dim=1, keepdim=True)
+        rel = 72 * 2.0 ** -23 * off + (ctx / 16 + 1) * 2.0 ** -23 + 2.0 ** -20
+        bound = 2 * R.HALF_BF16 * want + (R.HALF_BF16 + rel) * want
+        worst = ((out[b].double() - want).abs() / want).max()
+        print("B %d H %d ctx %d: %.2e of %.2e" % (B, H, ctx, worst, float((bound / want).max())))
+        assert ((out[b].double() - want).abs() <= bound * 1.01).all()
+    assert pk.get_device_error()[0] == 0
